@@ -10,6 +10,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "bsa_cache.h"
 #include "bsa_internal.h"
 #include "bsa_regime_table.h"
 
@@ -168,6 +169,21 @@ const PlanImpl* as_impl(const bsa_plan* p) {
 }  // namespace
 
 namespace bsa {
+bsa_status check_device(int* dev_out) { return check_arch(dev_out); }
+long long watchdog_limit_ns() { return env_ll("BSA_WATCHDOG_MS", 1000) * 1000000ll; }
+
+bool encode_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d};
+  cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Forward parameters of one plan (layout L, device views pd, workspace ws)
 // for the given tensors: the TMA views of Q (128-row and q-unit boxes), K and
 // V (contiguous or paged pools), the plan and scratch pointers, the element
@@ -412,9 +428,13 @@ bsa_status bsa_forward_ex(const bsa_plan* plan, const void* Q, const void* K, co
                            BSA_STAGE_ALL, stream);
 }
 
-bsa_status bsa_forward_stage(const bsa_plan* plan, const void* Q, const void* K, const void* V,
-                             const bsa_kv_pages* pages, const int32_t* kv_lens, int flags,
-                             void* O, float* LSE, int d, float scale, int stages, void* stream) {
+namespace {
+
+// bsa_forward_stage; causal_len: the causal offset of batch row b is
+// kv_lens[b] - Nq instead of Nk - Nq.
+bsa_status forward_stage(const bsa_plan* plan, const void* Q, const void* K, const void* V,
+                         const bsa_kv_pages* pages, const int32_t* kv_lens, int flags, void* O,
+                         float* LSE, int d, float scale, int stages, void* stream, bool causal_len) {
   constexpr int kAllBits = BSA_STAGE_ALL | BSA_STAGE_KNORM | BSA_STAGE_ROWBOUND;
   if (stages <= 0 || (stages & ~kAllBits)) return BSA_ERR_INVALID_ARG;
   const PlanImpl* p = as_impl(plan);
@@ -441,6 +461,7 @@ bsa_status bsa_forward_stage(const bsa_plan* plan, const void* Q, const void* K,
                        d, scale, dev, env_ll("BSA_WATCHDOG_MS", 1000) * 1000000ll,
                        env_ll("BSA_GRID", 0), &fp, &grid);
   if (st != BSA_OK) return st;
+  fp.causal_len = causal_len ? 1 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // The key-norm stage resets its own status words, the row-bound stage the
   // pass counters and the forward status (the two may run on different
@@ -456,6 +477,14 @@ bsa_status bsa_forward_stage(const bsa_plan* plan, const void* Q, const void* K,
   }
   if (launch_forward(fp, d, (int)grid, s, stages) != cudaSuccess) return BSA_ERR_CUDA;
   return BSA_OK;
+}
+
+}  // namespace
+
+bsa_status bsa_forward_stage(const bsa_plan* plan, const void* Q, const void* K, const void* V,
+                             const bsa_kv_pages* pages, const int32_t* kv_lens, int flags,
+                             void* O, float* LSE, int d, float scale, int stages, void* stream) {
+  return forward_stage(plan, Q, K, V, pages, kv_lens, flags, O, LSE, d, scale, stages, stream, false);
 }
 
 bsa_status bsa_sync_status(const bsa_plan* plan, void* stream, int32_t* detail) {
@@ -567,3 +596,11 @@ bsa_status bsa_watchdog_selftest(int32_t* status, int limit_us, void* stream) {
 }
 
 }  // extern "C"
+
+namespace bsa {
+bsa_status forward_over_cache(const bsa_plan* plan, const void* Q, const void* K, const void* V,
+                              const int32_t* kv_lens, int flags, void* O, float* LSE, int d, float scale,
+                              cudaStream_t stream) {
+  return forward_stage(plan, Q, K, V, nullptr, kv_lens, flags, O, LSE, d, scale, BSA_STAGE_ALL, stream, true);
+}
+}  // namespace bsa

@@ -1,0 +1,106 @@
+// Internal declarations of the 8-bit K/V cache: device views, the control
+// words and the kernels' launchers.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "bsa.h"
+
+namespace bsa {
+
+constexpr int kCacheListMax = 4096;  // sequences in one resize or fork
+// Control words of a cache; the scratch lists follow at kCacheScratch.
+constexpr int kCacheStatus = 0;
+constexpr int kCacheDetail = 1;
+constexpr int kCacheLive = 2;    // held pages the last compaction found
+constexpr int kCachePairs = 3;   // page copies queued for the copy kernel
+constexpr int kCacheScratch = 16;
+
+// Device view of a cache, by value to every kernel.
+struct CacheDev {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* refs;
+  int32_t* control;
+  int kind, num_pages, Hkv, page, d, sb, max_seqs, max_pages;
+  // Scratch: free pages found / page map / marks; copy pairs; marks by sequence.
+  __host__ __device__ int32_t* list_a() const { return control + kCacheScratch; }
+  __host__ __device__ int32_t* pair_src() const { return control + kCacheScratch + num_pages; }
+  __host__ __device__ int32_t* pair_dst() const { return control + kCacheScratch + 2 * (size_t)num_pages; }
+  __host__ __device__ int32_t* marks() const { return control + kCacheScratch + 3 * (size_t)num_pages; }
+};
+inline size_t cache_control_ints(int num_pages, int max_seqs) {
+  return kCacheScratch + 3 * (size_t)num_pages + (size_t)max_seqs;
+}
+
+#ifdef __CUDACC__
+// First error of its cache since the last report.
+__device__ __forceinline__ void cache_error(int32_t* control, int code, int detail) {
+  if (atomicCAS(control + kCacheStatus, 0, code) == 0) atomicExch(control + kCacheDetail, detail);
+}
+#endif
+
+// Token tensor [n][Hkv][T][d] of bf16 or fp16 elements.
+struct CacheRows {
+  const uint16_t* p;
+  long long sb, sh, st;  // strides in elements
+};
+
+struct CacheAppendParams {
+  CacheDev c;
+  CacheRows k, v;
+  int fp16, n, T, blocks;  // blocks: most scale blocks one row can touch
+  const int32_t* seqs;
+  const int32_t* counts;
+  const int32_t* start;
+};
+
+// Queries per unit of work at most: four row tiles of 16.
+constexpr int kCacheUnitRows = 64;
+constexpr int kCacheTile = 64;       // keys per tile
+constexpr int kCacheMaxGrid = 320;   // most CTAs of the attention kernel (workspace bound)
+
+struct CacheAttnParams {
+  CUtensorMap tmK, tmV;  // pools as [num_pages*Hkv*page][d] bytes, box {d, min(page, 64)}
+  CacheDev c;
+  CacheRows q;
+  uint16_t* o;
+  long long o_sb, o_sh, o_st;
+  float* lse;
+  const int32_t* seqs;
+  const uint8_t* mask;  // [B][Hq][NKB]
+  int32_t* list;        // active tiles of each (b, kv head) [B*Hkv][max_tiles] (with a mask)
+  int32_t* counts;      // how many [B*Hkv]
+  float* part;          // partial O and (m, l): see bsa_cache_attn.cu
+  int32_t* desc;        // rows split over CTAs, for the combine kernel [grid][4]
+  int fp16, B, Hq, g, nq, M, groups, NKB, bk, max_tiles, causal;
+  int rows_cap;         // query rows of a partial's slot
+  float scale_log2;
+  long long watchdog_ns;
+};
+
+cudaError_t launch_cache_resize(const CacheDev& c, const int32_t* seqs, const int32_t* new_lens, int n,
+                                cudaStream_t s);
+cudaError_t launch_cache_fork(const CacheDev& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);
+cudaError_t launch_cache_compact(const CacheDev& c, int sms, cudaStream_t s);
+cudaError_t launch_cache_copy(const CacheDev& dst, const CacheDev& src, const int32_t* dst_pages,
+                              const int32_t* src_pages, int n, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t s);
+cudaError_t launch_cache_attention(const CacheAttnParams& p, int grid, cudaStream_t s);
+// K and V of sequences seqs[0 .. B) as bf16 [B][Hkv][Nk][d] (zero at and past
+// the length) and their lengths [B].
+cudaError_t launch_cache_load(const CacheDev& c, const int32_t* seqs, int B, int Nk, uint16_t* k, uint16_t* v,
+                              int32_t* lens, cudaStream_t s);
+// bsa_forward_stage with the causal offset of each sequence taken from its
+// key length (bsa_api.cu).
+bsa_status forward_over_cache(const bsa_plan* plan, const void* Q, const void* K, const void* V,
+                              const int32_t* kv_lens, int flags, void* O, float* LSE, int d, float scale,
+                              cudaStream_t stream);
+
+}  // namespace bsa

@@ -1,0 +1,872 @@
+// Attention of a few queries per sequence over the 8-bit paged cache.
+//
+// Mathematics.  For the M = g * nq query rows that share a K/V head (g heads
+// of the group, nq queries each):
+//   x[key][row] = S_k(key) * qs(row) * sum_d kcode[key][d] * q16[row][d]
+// with q16 the row divided by a power of two that brings its largest element
+// into [1, 2) (exact in fp16 to 2^-25 of that element) and qs that power times
+// scale * log2(e); p = 2^(x - m) rounded to fp16, and
+//   O[d][row] += S_v * sum over 16 keys of vcode[key][d] * p[key][row]
+// where the 16 keys of one matrix instruction lie in one scale block.  Both
+// products are mma.m16n8k16 with the codes as the 16-row operand (S^T = K Q^T
+// and O^T = V^T P^T): with 1 to 8 rows nothing of the instruction is wasted on
+// the codes' side, codes convert to fp16 exactly, and S^T's accumulators become
+// P^T's operand by one movmatrix per 8 keys.  m is a running reference that is
+// moved only when a score passes it by more than 2^8 (then O and the sums are
+// rescaled), so fp16 weights keep 11 bits.
+//
+// What bounds it: 2 d bytes per key and K/V head at the memory's rate; an SM's
+// share is 23 bytes per cycle, against which a 64-key tile (16 KB at d = 128)
+// costs about 700 warp instructions, a quarter of what the SM issues meanwhile.
+// Hence mma.sync and not tcgen05: the products are 16 to 64 rows wide and far
+// from the tensor pipe's limit, and the codes have to pass through registers
+// to be converted anyway.
+//
+// Work split: the 64-key tiles of all (sequence, K/V head) pairs form one line
+// which the CTAs cut into equal pieces, so that ragged lengths and few long
+// sequences both fill the machine.  A row whose tiles lie in several CTAs
+// leaves partial sums in the workspace; the combine kernel joins them in the
+// order of the CTAs (results do not depend on timing).  Inside a CTA the tiles
+// go round the warps, each with its own sums, joined when the piece of a row
+// ends.  One warp feeds a ring of tiles by TMA (each page's rows of a head are
+// one box, 128-byte swizzled so that both products read without conflicts)
+// and the tiles' scales by 4-byte asynchronous copies.
+#include "bsa_cache.h"
+#include "bsa_cache_codes.cuh"
+#include "bsa_device.cuh"
+
+namespace bsa {
+namespace {
+
+using namespace dev;
+
+constexpr int kWarps = 4;  // consumer warps; one more produces
+constexpr int kAttnThreads = 32 * (kWarps + 1);
+constexpr int kScaleLanes = 8;  // producer lanes that copy scales: 4 groups of 16 keys, K and V
+constexpr float kMoveReference = 8.f;  // log2: weights stay <= 2^8
+
+enum CacheSite : int { kSiteTileFull = 0x50, kSiteTileEmpty = 0x51 };
+
+// NT: 8-row column tiles per warp (1 or 2).
+template <int D, int NT>
+struct AttnCfg {
+  static constexpr int kTileBytes = kCacheTile * D;  // K or V of a tile
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kMergeBytes = kWarps * 8 * NT * D * 4;  // (the tile counts' prefix uses it first)
+  static constexpr int kMlBytes = kWarps * 8 * NT * 8;
+  static constexpr int kBudget = 113 * 1024;  // two CTAs per SM
+  static constexpr int kStages = (kBudget - kMergeBytes - kMlBytes - 16) / (kStageBytes + 48);
+  static constexpr int kOffMerge = kStages * kStageBytes;
+  static constexpr int kOffMl = kOffMerge + kMergeBytes;        // float [warps][8 NT][2]
+  static constexpr int kOffScale = kOffMl + kMlBytes;           // float [stages][8]
+  static constexpr int kOffBar = kOffScale + kStages * 32;      // full, empty [stages]
+  static constexpr int kOffAbort = kOffBar + kStages * 16;
+  static constexpr int kSmem = kOffAbort + 16;
+  static_assert(kSmem <= kBudget && kMergeBytes >= 8 * (kAttnThreads + 1), "shared memory");
+};
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Arrive on `bar` when this thread's copies so far have landed (the arrival is
+// one of those the barrier was initialised for).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+  return r;
+}
+
+// Length of batch row b's sequence (0 for a padded row or one out of range).
+__device__ __forceinline__ int seq_of(const CacheAttnParams& p, int b) {
+  const int s = p.seqs ? __ldg(p.seqs + b) : b;
+  return s >= 0 && s < p.c.max_seqs ? s : -1;
+}
+__device__ __forceinline__ int len_of(const CacheAttnParams& p, int b) {
+  const int s = seq_of(p, b);
+  if (s < 0) return 0;
+  return min(max(__ldg(p.c.lens + s), 0), p.c.max_pages * p.c.page);
+}
+
+// The line of tiles: entry e is a batch row with its Hkv heads (no mask) or one
+// (batch row, head) with its list (mask); each entry's tiles are repeated for
+// its heads and for the groups of kCacheUnitRows query rows.
+__device__ __forceinline__ int entry_tiles(const CacheAttnParams& p, int e) {
+  if (p.mask) return __ldg(p.counts + e);
+  return (len_of(p, e) + kCacheTile - 1) / kCacheTile;
+}
+
+// Walks the pieces of rows in tiles [lo, hi) of the line.
+struct Walk {
+  int e, sub, cnt;   // entry, unit within it, its tiles
+  int t0, t1;        // this piece: tiles [t0, t1) of the unit
+  long long row0;    // first tile of the unit in the line
+  long long at, hi;
+};
+__device__ __forceinline__ void walk_piece(Walk& w) {
+  w.t0 = (int)(w.at - w.row0);
+  const long long left = w.hi - w.at;
+  w.t1 = left < w.cnt - w.t0 ? w.t0 + (int)left : w.cnt;
+}
+__device__ __forceinline__ void walk_start(const CacheAttnParams& p, Walk& w, int mult, int e, long long base,
+                                           long long lo, long long hi) {
+  w.at = lo;
+  w.hi = hi;
+  w.cnt = entry_tiles(p, e);
+  while (lo >= base + (long long)w.cnt * mult) {
+    base += (long long)w.cnt * mult;
+    w.cnt = entry_tiles(p, ++e);
+  }
+  w.e = e;
+  w.sub = (int)((lo - base) / w.cnt);
+  w.row0 = base + (long long)w.sub * w.cnt;
+  walk_piece(w);
+}
+__device__ __forceinline__ bool walk_next(const CacheAttnParams& p, Walk& w, int mult) {
+  w.at += w.t1 - w.t0;
+  if (w.at >= w.hi) return false;
+  w.row0 += w.cnt;
+  if (++w.sub == mult) {
+    w.sub = 0;
+    do w.cnt = entry_tiles(p, ++w.e);
+    while (w.cnt == 0);
+  }
+  walk_piece(w);
+  return true;
+}
+
+// Batch row, K/V head and group of query rows of a unit.
+struct Unit {
+  int b, h, grp;
+};
+__device__ __forceinline__ Unit unit_of(const CacheAttnParams& p, int e, int sub) {
+  Unit u;
+  u.grp = sub % p.groups;
+  const int x = sub / p.groups;
+  if (p.mask) {
+    u.b = e / p.c.Hkv;
+    u.h = e % p.c.Hkv;
+  } else {
+    u.b = e;
+    u.h = x;
+  }
+  return u;
+}
+
+__device__ __forceinline__ void store2(const CacheAttnParams& p, uint16_t* at, float4 f) {
+  uint2 w;
+  if (p.fp16) w = make_uint2(pack_half2(f.x, f.y), pack_half2(f.z, f.w));
+  else w = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+  *reinterpret_cast<uint2*>(at) = w;
+}
+// Query row m of a unit (within its K/V head's M rows): head and query.
+__device__ __forceinline__ uint16_t* o_row(const CacheAttnParams& p, int b, int h, int m) {
+  const int hq = h * p.g + m / p.nq, i = m % p.nq;
+  return p.o + b * p.o_sb + hq * p.o_sh + i * p.o_st;
+}
+__device__ __forceinline__ float* lse_row(const CacheAttnParams& p, int b, int h, int m) {
+  const int hq = h * p.g + m / p.nq, i = m % p.nq;
+  return p.lse + ((size_t)b * p.Hq + hq) * p.nq + i;
+}
+
+// NaN codes among 16 keys' values (v, as loaded for O^T += V^T P^T) where some
+// row does not attend some key: a weight of 0 would not keep them out of that
+// row.  They are taken out of v, and the rows that do attend them (counted by a
+// product of indicators) become NaN.  Nothing to do for a tile without any.
+template <int NT, int DV, int MT>
+__device__ __forceinline__ void take_nans(uint32_t (&v)[4][DV / 4], float (&o)[NT][MT][4], uint32_t kept, int kg) {
+  uint32_t any = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int q = 0; q < DV / 4; ++q) any |= (v[e][q] & 0x7f7f7f7fu) + 0x01010101u;  // 0x80 in a byte: NaN
+  if (!__any_sync(0xffffffffu, (any & 0x80808080u) != 0u)) return;
+  uint32_t kf[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const uint32_t b = kept >> ((kg * NT + nt) * 4);
+    kf[nt][0] = movmatrix((b & 1u ? 0x3c00u : 0u) | (b & 2u ? 0x3c000000u : 0u));
+    kf[nt][1] = movmatrix((b & 4u ? 0x3c00u : 0u) | (b & 8u ? 0x3c000000u : 0u));
+  }
+#pragma unroll
+  for (int q = 0; q < DV / 4; ++q) {
+    uint32_t ind[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t n = (((v[e][q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in a byte: NaN
+      v[e][q] &= ~(n * 0xffu);
+      ind[e] = n * 0x38u;  // 1.0
+    }
+    const uint2 ab0 = codes_to_half4<BSA_CACHE_E4M3>(__byte_perm(ind[0], ind[1], 0x5140));
+    const uint2 cd0 = codes_to_half4<BSA_CACHE_E4M3>(__byte_perm(ind[2], ind[3], 0x5140));
+    const uint2 ab1 = codes_to_half4<BSA_CACHE_E4M3>(__byte_perm(ind[0], ind[1], 0x7362));
+    const uint2 cd1 = codes_to_half4<BSA_CACHE_E4M3>(__byte_perm(ind[2], ind[3], 0x7362));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float y[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
+      mma16816(y, ab0.x, ab0.y, cd0.x, cd0.y, kf[nt][0], kf[nt][1]);
+      mma16816(z, ab1.x, ab1.y, cd1.x, cd1.y, kf[nt][0], kf[nt][1]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (y[e] > 0.f) o[nt][2 * q][e] = __uint_as_float(0x7fffffffu);
+        if (z[e] > 0.f) o[nt][2 * q + 1][e] = __uint_as_float(0x7fffffffu);
+      }
+    }
+  }
+}
+
+template <int D, int KIND, int NT>
+__global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_constant__ CacheAttnParams p) {
+  using C = AttnCfg<D, NT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  long long* s_prefix = reinterpret_cast<long long*>(smem + C::kOffMerge);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = blockIdx.x;
+  const uint32_t base = smem_u32(smem);
+  auto full = [&](int s) { return base + C::kOffBar + 16u * s; };
+  auto empty = [&](int s) { return base + C::kOffBar + 16u * s + 8u; };
+  const Watchdog wd{s_abort, p.c.control + kCacheStatus, p.c.control + kCacheDetail, p.watchdog_ns};
+  // Warps that share a tile: one for each 16 query rows (row tiles), the others
+  // take other tiles.
+  const int rows_unit = min(p.M, kCacheUnitRows);
+  const int R = NT == 1 ? 1 : (rows_unit <= 16 ? 1 : (rows_unit <= 32 ? 2 : 4));
+  if (tid == 0) {
+    *s_abort = 0;
+    if (base & 1023u) record_failure(wd, BSA_ERR_CUDA, 0);  // the swizzle's layout needs it
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1 + kScaleLanes);
+      mbar_init(empty(s), (uint32_t)R);
+    }
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&p.tmK);
+    tma_prefetch_desc(&p.tmV);
+  }
+  // This CTA's piece of the line: sums of the entries' tiles by thread, then a
+  // prefix over the threads.
+  const int E = p.mask ? p.B * p.c.Hkv : p.B;
+  const int mult = p.mask ? p.groups : p.c.Hkv * p.groups;
+  const int per = (E + kAttnThreads - 1) / kAttnThreads;
+  long long sum = 0;
+  for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) sum += entry_tiles(p, e);
+  sum *= mult;
+  s_prefix[tid + 1] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    long long acc = 0;
+    for (int i = 0; i < kAttnThreads; i += 32) {
+      long long x = s_prefix[i + lane + 1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      s_prefix[i + lane + 1] = acc + x;
+      acc += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) s_prefix[0] = 0;
+  }
+  __syncthreads();
+  const long long T = s_prefix[kAttnThreads];
+  // No CTA that works has an empty piece, so the parts of a row are those of
+  // consecutive CTAs.
+  const int G = (int)(T < (long long)gridDim.x ? T : (long long)gridDim.x);
+  const long long lo = cta < G ? cta * T / G : 0, hi = cta < G ? (cta + 1) * T / G : 0;
+  // Empty entries' rows: O = 0, LSE = -inf.
+  for (int e = cta; e < E; e += (int)gridDim.x) {
+    if (entry_tiles(p, e) != 0) continue;
+    const int b = p.mask ? e / p.c.Hkv : e;
+    const int h0 = p.mask ? e % p.c.Hkv : 0, h1 = p.mask ? h0 + 1 : p.c.Hkv;
+    if (tid == 0) {
+      const int s = p.seqs ? __ldg(p.seqs + b) : b;
+      if (s < -1 || s >= p.c.max_seqs) cache_error(p.c.control, BSA_ERR_INVALID_ARG, b);
+    }
+    for (int i = tid; i < (h1 - h0) * p.M * (D / 4); i += kAttnThreads) {
+      const int c4 = i % (D / 4), r = i / (D / 4), m = r % p.M, h = h0 + r / p.M;
+      store2(p, o_row(p, b, h, m) + 4 * c4, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (c4 == 0 && p.lse) *lse_row(p, b, h, m) = -INFINITY;
+    }
+  }
+  if (tid == 0) p.desc[4 * cta] = 0;  // no row of this CTA goes on in the next one (so far)
+  if (lo >= hi || *s_abort) return;   // (the same for every thread: barriers above)
+  // The thread whose entries hold tile lo.
+  int a = 0, z = kAttnThreads;
+  while (z - a > 1) {
+    const int m = (a + z) >> 1;
+    if (s_prefix[m] <= lo) a = m;
+    else z = m;
+  }
+  Walk w;
+  walk_start(p, w, mult, a * per, s_prefix[a], lo, hi);
+  __syncthreads();  // the prefix gives way to the merge buffer
+
+  const int lpage = 31 - __clz(p.c.page), lsb = 31 - __clz(p.c.sb);
+  if (warp == kWarps) {
+    // ------------------------------------------------------------- producer
+    const int cs = min(p.c.page, kCacheTile);  // keys per box
+    const int lcs = 31 - __clz(cs), nc = kCacheTile >> lcs;
+    const uint64_t pol = policy_evict_first();
+    uint32_t it = 0;
+    bool ok = true;
+    do {
+      const Unit u = unit_of(p, w.e, w.sub);
+      const int seq = seq_of(p, u.b), len = len_of(p, u.b);
+      const int32_t* row = p.c.table + (size_t)seq * p.c.max_pages;
+      for (int t = w.t0; t < w.t1 && ok; t += 32) {
+        // A lane per tile: its number, and the pool row of each of its boxes
+        // (-1: no token in it).
+        int tile = 0, pr[4] = {-1, -1, -1, -1};
+        if (t + lane < w.t1) {
+          tile = p.mask ? __ldg(p.list + (size_t)w.e * p.max_tiles + t + lane) : t + lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = tile * kCacheTile + (j << lcs);
+            if (j < nc && key < len) {
+              int ph = __ldg(row + (key >> lpage));
+              if (ph < 0 || ph >= p.c.num_pages) {
+                cache_error(p.c.control, BSA_ERR_PLAN_MISMATCH, seq);
+                ph = 0;  // (some page, so that the row ends like any other)
+              }
+              pr[j] = (ph * p.c.Hkv + u.h) * p.c.page + (key & (p.c.page - 1));
+            }
+          }
+        }
+        const int n = min(32, w.t1 - t);
+        for (int i = 0; i < n; ++i, ++it) {
+          const int s = (int)(it % C::kStages);
+          const uint32_t use = it / C::kStages;
+          if (use > 0) {
+            const bool got = mbar_wait(empty(s), (use - 1) & 1u, wd, kSiteTileEmpty);
+            if (!__all_sync(0xffffffffu, got)) {
+              ok = false;
+              break;
+            }
+          }
+          int box[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) box[j] = __shfl_sync(0xffffffffu, pr[j], i);
+          const int tl = __shfl_sync(0xffffffffu, tile, i);
+          if (lane == 0) {
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bytes += box[j] >= 0 ? 2u * cs * D : 0u;
+            mbar_arrive_expect_tx(full(s), bytes);
+          }
+          __syncwarp();
+          const int j = lane & 3;
+          const int mybox = j == 0 ? box[0] : (j == 1 ? box[1] : (j == 2 ? box[2] : box[3]));
+          if (lane < 8 && mybox >= 0)
+            tma_load_2d(base + s * C::kStageBytes + (lane >> 2) * C::kTileBytes + j * cs * D,
+                        lane < 4 ? &p.tmK : &p.tmV, 0, mybox, full(s), pol);
+          // Scale of keys 16 j .. of the tile: box (16 j) / cs, its pool row
+          // further by the rest; 0 where the keys lie past the length.
+          const int jb = (16 * j) >> lcs;
+          const int sbox = jb == 0 ? box[0] : (jb == 1 ? box[1] : (jb == 2 ? box[2] : box[3]));
+          if (lane >= 8 && lane < 8 + kScaleLanes) {
+            const bool isv = lane >= 12;
+            const bool live = tl * kCacheTile + 16 * j < len;
+            const size_t at = live ? (size_t)((unsigned)(sbox + ((16 * j) & (cs - 1)))) >> lsb : 0;
+            cp_async4(base + C::kOffScale + s * 32 + (lane - 8) * 4, (isv ? p.c.vs : p.c.ks) + at, live ? 4u : 0u);
+            cp_async_arrive(full(s));
+          }
+        }
+        __syncwarp();
+      }
+    } while (ok && walk_next(p, w, mult));
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && lane == 0) {
+      // Let the copies in flight land before the CTA's shared memory goes away.
+      volatile int no_abort = 0;
+      const Watchdog quick{&no_abort, wd.status, wd.detail, 100000000ll};
+      for (uint32_t k = it < (uint32_t)C::kStages ? 0 : it - C::kStages; k < it; ++k)
+        mbar_wait(full((int)(k % C::kStages)), (k / C::kStages) & 1u, quick, kSiteTileFull);
+    }
+    return;
+  }
+
+  // --------------------------------------------------------------- consumers
+  const int g = lane >> 2, t4 = lane & 3;
+  const int KL = kWarps / R, rt = warp % R, kl = warp / R;
+  constexpr int KS = D / 16;    // 16-element steps of q . k
+  constexpr int MT = D / 16;    // 16-row tiles of O^T
+  constexpr int DV = D / 8;     // consecutive elements of O a thread holds
+  float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+  float* ml = reinterpret_cast<float*>(smem + C::kOffMl);
+  const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale);
+  uint32_t it = 0;
+  bool more = true, ok = true;
+  while (more) {
+    const Unit u = unit_of(p, w.e, w.sub);
+    const int len = len_of(p, u.b);
+    const int m0 = u.grp * kCacheUnitRows + rt * 16;  // first query row of this warp
+    // Query fragments: lane (g, t4) holds row 8 nt + g, elements 2 DV' of it.
+    uint32_t qf[NT][KS][2];
+    float qs[NT][2];  // scale of rows 8 nt + 2 t4, + 1
+    int lim[NT][2];   // keys below it are visible to them
+    int hq_of[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int m = m0 + 8 * nt + g;
+      uint32_t raw[KS][2];
+      float amax = 0.f;
+      if (m < p.M) {
+        const uint16_t* qr = p.q.p + u.b * p.q.sb + (u.h * p.g + m / p.nq) * p.q.sh + (m % p.nq) * p.q.st;
+        // Word s of 16-byte chunk (D == 128: 2 t4 + i; D == 64: t4) of a row of
+        // codes are elements 16 chunk + 4 s ..: the same of q.
+#pragma unroll
+        for (int k2 = 0; k2 < KS / 2; ++k2) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(qr + t4 * (D / 4) + k2 * 8));
+          raw[2 * k2][0] = x.x;
+          raw[2 * k2][1] = x.y;
+          raw[2 * k2 + 1][0] = x.z;
+          raw[2 * k2 + 1][1] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) raw[k][0] = raw[k][1] = 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 f = elems_to_float2(raw[k][e], p.fp16);
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^e with amax in [2^e, 2^(e+1)); rows of zeros and of infinities keep 1.
+      int e = (int)(__float_as_uint(amax) >> 23) - 127;
+      if (!(amax > 0.f) || amax == INFINITY) e = 0;
+      e = max(e, -100);
+      const float down = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
+      const float up = __uint_as_float((uint32_t)(127 + min(e, 126)) << 23);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float2 f = elems_to_float2(raw[k][x], p.fp16);
+          qf[nt][k][x] = pack_half2(f.x * down, f.y * down);
+        }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        qs[nt][x] = __shfl_sync(0xffffffffu, up, (2 * t4 + x) * 4) * p.scale_log2;
+        const int mm = m0 + 8 * nt + 2 * t4 + x;
+        hq_of[nt][x] = u.h * p.g + min(mm, p.M - 1) / p.nq;
+        lim[nt][x] = mm < p.M ? (p.causal ? min(len, len - p.nq + mm % p.nq + 1) : len) : 0;
+      }
+    }
+    float o[NT][MT][4];
+    float m_ref[NT][2], l_sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        m_ref[nt][x] = -INFINITY;
+        l_sum[nt][x] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < MT; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[nt][k][x] = 0.f;
+    }
+    const int first_limit = p.causal ? len - p.nq + 1 : len;  // keys below it are visible to every row
+
+    for (int t = w.t0; t < w.t1; ++t, ++it) {
+      if ((int)(it % KL) != kl || !ok) continue;
+      const int s = (int)(it % C::kStages);
+      const int tile = p.mask ? __ldg(p.list + (size_t)w.e * p.max_tiles + t) : t;
+      const int key0 = tile * kCacheTile;
+      // Selection of the tile's two halves of 32 keys by these rows' heads.
+      uint32_t sel = 0xffffffffu;
+      if (p.mask) {
+        sel = 0u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int kb = (key0 + 32 * hf) / p.bk;
+              if (kb < p.NKB && __ldg(p.mask + ((size_t)u.b * p.Hq + hq_of[nt][x]) * p.NKB + kb))
+                sel |= 1u << ((nt * 2 + x) * 2 + hf);
+            }
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(full(s), (it / C::kStages) & 1u, wd, kSiteTileFull))) {
+        ok = false;  // recorded; this row's results are void, the walk goes on so that no barrier is missed
+        continue;
+      }
+      const uint32_t ks = base + s * C::kStageBytes, vs = ks + C::kTileBytes;
+      // ---- S^T = K Q^T: 16 keys a time
+      float x[4][NT][4];
+#pragma unroll
+      for (int kg = 0; kg < 4; ++kg) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[kg][nt][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const int r0 = 16 * kg + g, r1 = r0 + 8;
+          uint4 a, b;
+          if constexpr (D == 128) {
+            a = ld_shared_v4(ks + r0 * 128 + (((2 * t4 + i) ^ (r0 & 7)) << 4));
+            b = ld_shared_v4(ks + r1 * 128 + (((2 * t4 + i) ^ (r1 & 7)) << 4));
+          } else {
+            a = ld_shared_v4(ks + r0 * 64 + ((t4 ^ ((r0 >> 1) & 3)) << 4));
+            b = ld_shared_v4(ks + r1 * 64 + ((t4 ^ ((r1 >> 1) & 3)) << 4));
+          }
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint2 ha = codes_to_half4<KIND>(aw[q]), hb = codes_to_half4<KIND>(bw[q]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(x[kg][nt], ha.x, hb.x, ha.y, hb.y, qf[nt][4 * i + q][0], qf[nt][4 * i + q][1]);
+          }
+        }
+      }
+      // ---- scores (log2), masks, reference
+#pragma unroll
+      for (int kg = 0; kg < 4; ++kg) {
+        const float sk = scales[s * 8 + kg];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[kg][nt][e] *= sk * qs[nt][e & 1];
+      }
+      const bool partial = key0 + kCacheTile > first_limit || p.mask != nullptr;
+      uint32_t kept = 0xffffffffu;  // bit (kg NT + nt) 4 + e: this thread's score is one that is attended
+      if (partial) {
+#pragma unroll
+        for (int kg = 0; kg < 4; ++kg)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + 16 * kg + g + (e >> 1) * 8;
+              const bool keep = key < lim[nt][e & 1] && ((sel >> ((nt * 2 + (e & 1)) * 2 + (kg >> 1))) & 1u);
+              if (!keep) {
+                x[kg][nt][e] = -INFINITY;
+                kept &= ~(1u << ((kg * NT + nt) * 4 + e));
+              }
+            }
+      }
+      bool move = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float v = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
+#pragma unroll
+          for (int kg = 1; kg < 4; ++kg) v = fmax3(v, x[kg][nt][c], x[kg][nt][c + 2]);
+          mx[nt][c] = v;
+          move |= v > m_ref[nt][c] + kMoveReference;
+        }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float f[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float v = mx[nt][c];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            f[c] = 1.f;
+            if (v > m_ref[nt][c]) {
+              f[c] = ex2_approx(m_ref[nt][c] - v);  // 0 from -inf
+              m_ref[nt][c] = v;
+            }
+            l_sum[nt][c] *= f[c];
+          }
+#pragma unroll
+          for (int k = 0; k < MT; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][k][e] *= f[e & 1];
+        }
+      }
+      // ---- weights and P^T fragments
+      uint32_t pf[4][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float r0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0];
+        const float r1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1];
+#pragma unroll
+        for (int kg = 0; kg < 4; ++kg) {
+          const float p0 = ex2_approx(x[kg][nt][0] - r0), p1 = ex2_approx(x[kg][nt][1] - r1);
+          const float p2 = ex2_approx(x[kg][nt][2] - r0), p3 = ex2_approx(x[kg][nt][3] - r1);
+          l_sum[nt][0] += p0 + p2;
+          l_sum[nt][1] += p1 + p3;
+          pf[kg][nt][0] = movmatrix(pack_half2(p0, p1));
+          pf[kg][nt][1] = movmatrix(pack_half2(p2, p3));
+        }
+      }
+      // ---- O^T += S_v V^T P^T: 16 keys a time (one scale block each)
+      const bool tail = key0 + kCacheTile > len;
+#pragma unroll
+      for (int kg = 0; kg < 4; ++kg) {
+        const float sv = scales[s * 8 + 4 + kg];
+        const int ra = 16 * kg + 2 * t4;  // keys 2 t4, + 1, + 8, + 9 of the 16
+        uint32_t v[4][DV / 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = ra + (e & 1) + (e >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 y = ld_shared_v4(vs + r * 128 + ((g ^ (r & 7)) << 4));
+            v[e][0] = y.x;
+            v[e][1] = y.y;
+            v[e][2] = y.z;
+            v[e][3] = y.w;
+          } else {
+            const uint2 y = ld_shared_v2(vs + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+            v[e][0] = y.x;
+            v[e][1] = y.y;
+          }
+          // Rows past the sequence hold anything: weight 0 would not stop a NaN.
+          if (tail && key0 + r >= len) {
+#pragma unroll
+            for (int q = 0; q < DV / 4; ++q) v[e][q] = 0u;
+          }
+        }
+        if (KIND == BSA_CACHE_E4M3 && partial) take_nans<NT, DV, MT>(v, o, kept, kg);
+#pragma unroll
+        for (int q = 0; q < DV / 4; ++q) {
+          // Pairs of keys of one element: {a0 b0 a1 b1}, {a2 b2 a3 b3}.
+          const uint2 ab0 = codes_to_half4<KIND>(__byte_perm(v[0][q], v[1][q], 0x5140));
+          const uint2 cd0 = codes_to_half4<KIND>(__byte_perm(v[2][q], v[3][q], 0x5140));
+          const uint2 ab1 = codes_to_half4<KIND>(__byte_perm(v[0][q], v[1][q], 0x7362));
+          const uint2 cd1 = codes_to_half4<KIND>(__byte_perm(v[2][q], v[3][q], 0x7362));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float y[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(y, ab0.x, ab0.y, cd0.x, cd0.y, pf[kg][nt][0], pf[kg][nt][1]);
+            mma16816(z, ab1.x, ab1.y, cd1.x, cd1.y, pf[kg][nt][0], pf[kg][nt][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[nt][2 * q][e] = fmaf(sv, y[e], o[nt][2 * q][e]);
+              o[nt][2 * q + 1][e] = fmaf(sv, z[e], o[nt][2 * q + 1][e]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(s));
+    }
+
+    // ---- end of the piece: join the warps that took its tiles
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float l = l_sum[nt][c];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int row = 8 * nt + 2 * t4 + c;
+        if (g == 0) {
+          ml[(warp * 8 * NT + row) * 2] = m_ref[nt][c];
+          ml[(warp * 8 * NT + row) * 2 + 1] = l;
+        }
+        float* mr = merge + (size_t)(warp * 8 * NT + row) * D + g * DV;
+#pragma unroll
+        for (int k = 0; k < MT; k += 2)
+          *reinterpret_cast<float4*>(mr + 2 * k) =
+              make_float4(o[nt][k][c], o[nt][k][c + 2], o[nt][k + 1][c], o[nt][k + 1][c + 2]);
+      }
+    }
+    named_bar_sync(1, 32 * kWarps);
+    {
+      const bool whole = w.t0 == 0 && w.t1 == w.cnt;
+      const bool starts = w.t0 == 0;
+      const int rows = min(p.M - u.grp * kCacheUnitRows, kCacheUnitRows);
+      float* part = p.part + (size_t)(2 * cta + (starts ? 1 : 0)) * p.rows_cap * (D + 2);
+      // A thread per (row, 4 elements).
+      for (int i = tid; i < rows * (D / 4); i += 32 * kWarps) {
+        const int r = i / (D / 4), c4 = i % (D / 4);
+        const int rtile = r / (8 * NT), rr = r % (8 * NT);
+        float mw[kWarps], M = -INFINITY;
+        for (int k = 0; k < KL; ++k) {
+          mw[k] = ml[((k * R + rtile) * 8 * NT + rr) * 2];
+          M = fmaxf(M, mw[k]);
+        }
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < KL; ++k) {
+          const int at = (k * R + rtile) * 8 * NT + rr;
+          const float f = M == -INFINITY ? 1.f : ex2_approx(mw[k] - M);
+          const float4 y = *reinterpret_cast<const float4*>(merge + (size_t)at * D + 4 * c4);
+          L += f * ml[at * 2 + 1];
+          acc.x = fmaf(f, y.x, acc.x);
+          acc.y = fmaf(f, y.y, acc.y);
+          acc.z = fmaf(f, y.z, acc.z);
+          acc.w = fmaf(f, y.w, acc.w);
+        }
+        if (whole) {
+          const int m = u.grp * kCacheUnitRows + r;
+          const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+          store2(p, o_row(p, u.b, u.h, m) + 4 * c4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+          if (c4 == 0 && p.lse)
+            *lse_row(p, u.b, u.h, m) = L > 0.f || L != L ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          float* pr = part + (size_t)r * (D + 2);
+          *reinterpret_cast<float2*>(pr + 4 * c4) = make_float2(acc.x, acc.y);
+          *reinterpret_cast<float2*>(pr + 4 * c4 + 2) = make_float2(acc.z, acc.w);
+          if (c4 == 0) *reinterpret_cast<float2*>(pr + D) = make_float2(M, L);
+        }
+      }
+      if (tid == 0 && starts && !whole) {
+        // CTAs up to the one that holds the unit's last tile.
+        const long long last = w.row0 + w.cnt - 1;
+        const int c1 = (int)(((last + 1) * G - 1) / T);
+        p.desc[4 * cta + 1] = u.b;
+        p.desc[4 * cta + 2] = u.h;
+        p.desc[4 * cta + 3] = u.grp;
+        p.desc[4 * cta] = c1 - cta + 1;
+      }
+    }
+    named_bar_sync(1, 32 * kWarps);
+    more = walk_next(p, w, mult);
+  }
+}
+
+// Joins the parts of a row that several CTAs worked on, in the CTAs' order.
+// One CTA per (first CTA of the row, query row); its warps take every fourth
+// part each.
+template <int D>
+__global__ void __launch_bounds__(128) combine_kernel(const CacheAttnParams p) {
+  __shared__ float s_ml[4][2];
+  __shared__ float s_o[4][D];
+  const int c0 = blockIdx.x, r = blockIdx.y;
+  const int4 ds = *reinterpret_cast<const int4*>(p.desc + 4 * c0);
+  const int n = ds.x;
+  if (n <= 0) return;
+  const int m = ds.w * kCacheUnitRows + r;
+  if (m >= p.M) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto slot = [&](int k) { return p.part + ((size_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * p.rows_cap + r) * (D + 2); };
+  float M = -INFINITY;
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, slot(k)[D]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f;
+  constexpr int E = D / 32;
+  float acc[E] = {};
+#pragma unroll 4
+  for (int k = warp; k < n; k += 4) {
+    const float* s = slot(k);
+    const float2 ml = *reinterpret_cast<const float2*>(s + D);
+    const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
+    L = fmaf(f, ml.y, L);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const float2 y = *reinterpret_cast<const float2*>(s + lane * E + 2 * e);
+      acc[2 * e] = fmaf(f, y.x, acc[2 * e]);
+      acc[2 * e + 1] = fmaf(f, y.y, acc[2 * e + 1]);
+    }
+  }
+  if (lane == 0) s_ml[warp][1] = L;
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+  __syncthreads();
+  L = s_ml[0][1] + s_ml[1][1] + s_ml[2][1] + s_ml[3][1];
+  const bool some = L > 0.f || L != L;
+  if (tid < D / 4) {
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = 4 * tid + e;
+      v[e] = s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d];
+      v[e] = some ? v[e] / L : 0.f;
+    }
+    store2(p, o_row(p, ds.y, ds.z, m) + 4 * tid, make_float4(v[0], v[1], v[2], v[3]));
+    if (tid == 0 && p.lse) *lse_row(p, ds.y, ds.z, m) = some ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+// Tiles of 64 keys that some head of the group selects, below the length:
+// one CTA per (batch row, K/V head).
+__global__ void __launch_bounds__(256) tiles_kernel(const CacheAttnParams p) {
+  __shared__ int warp_s[8];
+  const int e = blockIdx.x, b = e / p.c.Hkv, h = e % p.c.Hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int len = len_of(p, b);
+  const int tiles = min((len + kCacheTile - 1) / kCacheTile, p.max_tiles);
+  const uint8_t* mrow = p.mask + ((size_t)b * p.Hq + (size_t)h * p.g) * p.NKB;
+  int32_t* out = p.list + (size_t)e * p.max_tiles;
+  int done = 0;
+  for (int base = 0; base < tiles; base += 256) {
+    const int t = base + tid;
+    bool on = false;
+    if (t < tiles) {
+      const int k0 = t * kCacheTile / p.bk, k1 = min((t * kCacheTile + kCacheTile - 1) / p.bk, p.NKB - 1);
+      for (int i = 0; i < p.g && !on; ++i)
+        for (int k = k0; k <= k1; ++k) on |= __ldg(mrow + (size_t)i * p.NKB + k) != 0;
+    }
+    const unsigned bal = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) warp_s[warp] = __popc(bal);
+    __syncthreads();
+    int before = done;
+    for (int k = 0; k < 8; ++k) {
+      if (k < warp) before += warp_s[k];
+      done += warp_s[k];
+    }
+    if (on) out[before + __popc(bal & ((1u << lane) - 1u))] = t;
+    __syncthreads();
+  }
+  if (tid == 0) p.counts[e] = done;
+}
+
+template <int D, int KIND, int NT>
+cudaError_t launch_t(const CacheAttnParams& p, int grid, cudaStream_t s) {
+  const int smem = AttnCfg<D, NT>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attn_kernel<D, KIND, NT><<<grid, kAttnThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+template <int D, int KIND>
+cudaError_t launch_k(const CacheAttnParams& p, int grid, cudaStream_t s) {
+  return p.M <= 8 ? launch_t<D, KIND, 1>(p, grid, s) : launch_t<D, KIND, 2>(p, grid, s);
+}
+template <int D>
+cudaError_t launch_d(const CacheAttnParams& p, int grid, cudaStream_t s) {
+  cudaError_t e = p.c.kind == BSA_CACHE_INT8 ? launch_k<D, BSA_CACHE_INT8>(p, grid, s)
+                                             : launch_k<D, BSA_CACHE_E4M3>(p, grid, s);
+  if (e != cudaSuccess) return e;
+  combine_kernel<D><<<dim3(grid, p.rows_cap), 128, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attention(const CacheAttnParams& p, int grid, cudaStream_t s) {
+  if (p.mask) {
+    tiles_kernel<<<p.B * p.c.Hkv, 256, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return p.c.d == 64 ? launch_d<64>(p, grid, s) : launch_d<128>(p, grid, s);
+}
+
+}  // namespace bsa

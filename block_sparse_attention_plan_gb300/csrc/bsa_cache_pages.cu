@@ -1,0 +1,429 @@
+// Page operations of the 8-bit K/V cache: resize (with copy on write), fork,
+// compact and copy.  The whole state is the page table, the lengths and a
+// reference count per page; "free" means a count of 0 and pages are taken
+// lowest first, so every result is a function of the state and the arguments.
+//
+// The bookkeeping is a few thousand integers: one CTA of 1024 threads does it
+// with block scans (no grid synchronisation, no host), and a second, wide
+// kernel moves the page contents it queued.  The copies are what costs: a page
+// of 64 tokens and 8 heads is 131 KB.
+#include "bsa_cache.h"
+
+namespace bsa {
+namespace {
+
+constexpr int kThreads = 1024;
+
+// Exclusive block scan of one int per thread; `total` gets the sum.  `warp_s`
+// is shared scratch of 33 ints.
+__device__ __forceinline__ int block_scan(int x, int* warp_s, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) warp_s[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warp_s[lane], s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_s[lane] = s - w;
+    if (lane == 31) warp_s[32] = s;
+  }
+  __syncthreads();
+  total = warp_s[32];
+  const int r = warp_s[warp] + inc - x;
+  __syncthreads();  // warp_s may be reused
+  return r;
+}
+
+__device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
+
+// One CTA.  s_need: pages item i takes (-1: skipped); s_page: its partly
+// filled last page where that is shared (else -1), then the offset of its
+// pages in the list of free ones.
+__global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, const int32_t* seqs,
+                                                          const int32_t* new_lens, int n) {
+  __shared__ int s_need[kCacheListMax];
+  __shared__ int s_page[kCacheListMax];
+  __shared__ int warp_s[33];
+  __shared__ int s_pairs;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cap = c.max_pages * c.page;
+  int32_t* marks = c.marks();
+  auto seq_of = [&](int i) { return seqs ? __ldg(seqs + i) : i; };
+  auto new_of = [&](int i) { return new_lens ? __ldg(new_lens + i) : 0; };
+  if (tid == 0) s_pairs = 0;
+  // A sequence may appear once: the first of its items marks it.
+  for (int i = tid; i < n; i += kThreads) {
+    const int s = seq_of(i);
+    if (s >= 0 && s < c.max_seqs) marks[s] = 0x7fffffff;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const int s = seq_of(i);
+    if (s >= 0 && s < c.max_seqs) atomicMin(marks + s, i);
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const int s = seq_of(i), want = new_of(i);
+    bool ok = s >= 0 && s < c.max_seqs && __ldcg(marks + s) == i && want >= 0 && want <= cap;
+    if (ok) {
+      const int have = __ldcg(c.lens + s);
+      ok = have >= 0 && have <= cap;
+    }
+    if (!ok && s != -1) cache_error(c.control, BSA_ERR_INVALID_ARG, i);
+    s_need[i] = ok ? 0 : -1;
+  }
+  __syncthreads();
+  // Releases: a warp per item, a lane per page.
+  for (int i = warp; i < n; i += kThreads / 32) {
+    if (s_need[i] < 0) continue;
+    const int s = seq_of(i);
+    const int hp = pages_of(__ldcg(c.lens + s), c.page), wp = pages_of(new_of(i), c.page);
+    for (int j = wp + lane; j < hp; j += 32) {
+      const int p = __ldcg(c.table + (size_t)s * c.max_pages + j);
+      if (p >= 0 && p < c.num_pages) atomicSub(c.refs + p, 1);
+      else cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s);
+    }
+  }
+  __syncthreads();
+  // Growth into a partly filled last page that others hold too.
+  for (int i = tid; i < n; i += kThreads) {
+    int shared_page = -1;
+    if (s_need[i] >= 0) {
+      const int s = seq_of(i), have = __ldcg(c.lens + s);
+      if (new_of(i) > have && have % c.page) {
+        const int p = __ldcg(c.table + (size_t)s * c.max_pages + have / c.page);
+        if (p < 0 || p >= c.num_pages) cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s);
+        else if (__ldcg(c.refs + p) > 1) shared_page = p;
+      }
+    }
+    s_page[i] = shared_page;
+  }
+  __syncthreads();
+  int mine[kCacheListMax / kThreads], sum = 0;
+#pragma unroll
+  for (int u = 0; u < kCacheListMax / kThreads; ++u) {  // items tid * 4 + u, in order
+    const int i = tid * (kCacheListMax / kThreads) + u;
+    mine[u] = 0;
+    if (i < n && s_need[i] >= 0) {
+      const int s = seq_of(i), have = __ldcg(c.lens + s);
+      mine[u] = max(0, pages_of(new_of(i), c.page) - pages_of(have, c.page));
+      const int p = s_page[i];
+      if (p >= 0) {
+        int rank = 0;  // earlier items of this call that grow into the same page
+        for (int j = 0; j < i; ++j) rank += s_page[j] == p;
+        if (__ldcg(c.refs + p) - rank > 1) mine[u] |= 1 << 30;  // a page of its own
+      }
+    }
+    sum += (mine[u] & 0x3fffffff) + (mine[u] >> 30);
+  }
+  int total;
+  int off = block_scan(sum, warp_s, total);  // (its barriers: every rank is taken)
+#pragma unroll
+  for (int u = 0; u < kCacheListMax / kThreads; ++u) {
+    const int i = tid * (kCacheListMax / kThreads) + u;
+    if (i < n && s_need[i] >= 0) {
+      s_need[i] = mine[u];
+      s_page[i] = off;
+      off += (mine[u] & 0x3fffffff) + (mine[u] >> 30);
+    }
+  }
+  // The lowest `total` free pages, in order: 16 pages per thread and step.
+  int found = 0;
+  for (int base = 0; base < c.num_pages && found < total; base += kThreads * 16) {
+    unsigned free_bits = 0;
+    const int p0 = base + tid * 16;
+    if (p0 + 16 <= c.num_pages && (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0) {
+      int4 r[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r[q] = __ldcg(reinterpret_cast<const int4*>(c.refs + p0) + q);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        free_bits |= ((r[q].x <= 0) | (r[q].y <= 0) << 1 | (r[q].z <= 0) << 2 | (r[q].w <= 0) << 3) << (4 * q);
+    } else {
+      for (int q = 0; q < 16; ++q)
+        if (p0 + q < c.num_pages && __ldcg(c.refs + p0 + q) <= 0) free_bits |= 1u << q;
+    }
+    int here;
+    int at = found + block_scan(__popc(free_bits), warp_s, here);
+    while (free_bits && at < total) {
+      const int q = __ffs(free_bits) - 1;
+      free_bits &= free_bits - 1;
+      c.list_a()[at++] = p0 + q;
+    }
+    found += here;
+  }
+  __syncthreads();
+  if (found < total) {  // nothing changes: take the releases back
+    for (int i = warp; i < n; i += kThreads / 32) {
+      if (s_need[i] < 0) continue;
+      const int s = seq_of(i);
+      const int hp = pages_of(__ldcg(c.lens + s), c.page), wp = pages_of(new_of(i), c.page);
+      for (int j = wp + lane; j < hp; j += 32) {
+        const int p = __ldcg(c.table + (size_t)s * c.max_pages + j);
+        if (p >= 0 && p < c.num_pages) atomicAdd(c.refs + p, 1);
+      }
+    }
+    if (tid == 0) {
+      cache_error(c.control, BSA_ERR_WORKSPACE, total - found);
+      c.control[kCachePairs] = 0;
+    }
+    return;
+  }
+  for (int i = warp; i < n; i += kThreads / 32) {
+    const int need = s_need[i];
+    if (need < 0) continue;
+    const int s = seq_of(i), have = __ldcg(c.lens + s), want = new_of(i);
+    const int hp = pages_of(have, c.page), wp = pages_of(want, c.page);
+    int32_t* row = c.table + (size_t)s * c.max_pages;
+    const int32_t* list = c.list_a() + s_page[i];
+    const int own = need >> 30;
+    if (own && lane == 0) {
+      const int old = __ldcg(row + hp - 1), fresh = __ldcg(list);
+      const int at = atomicAdd(&s_pairs, 1);
+      c.pair_src()[at] = old;
+      c.pair_dst()[at] = fresh;
+      atomicSub(c.refs + old, 1);
+      c.refs[fresh] = 1;
+      row[hp - 1] = fresh;
+    }
+    for (int j = hp + lane; j < wp; j += 32) {
+      const int p = __ldcg(list + own + j - hp);
+      c.refs[p] = 1;
+      row[j] = p;
+    }
+    for (int j = wp + lane; j < hp; j += 32) row[j] = -1;
+    __syncwarp();
+    if (lane == 0) c.lens[s] = want;
+  }
+  __syncthreads();
+  if (tid == 0) c.control[kCachePairs] = s_pairs;
+}
+
+// One CTA per pair; each checks its own pair against the whole list.  A length
+// that a pair reads is written by no other one: a source is no destination.
+__global__ void __launch_bounds__(256) fork_kernel(const CacheDev c, const int32_t* src, const int32_t* dst, int n) {
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const int a = __ldg(src + i), b = __ldg(dst + i);
+  if (a == -1 || b == -1) return;
+  bool ok = a >= 0 && a < c.max_seqs && b >= 0 && b < c.max_seqs;
+  for (int j = tid; ok && j < n; j += 256) {
+    const int sj = __ldg(src + j), dj = __ldg(dst + j);
+    if (sj == -1 || dj == -1) continue;
+    if ((dj == b && j < i) || sj == b) ok = false;
+  }
+  int len = 0;
+  if (ok) {
+    len = c.lens[a];
+    ok = len >= 0 && len <= c.max_pages * c.page && c.lens[b] == 0;
+  }
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0) cache_error(c.control, BSA_ERR_INVALID_ARG, i);
+    return;
+  }
+  const int held = pages_of(len, c.page);
+  const int32_t* from = c.table + (size_t)a * c.max_pages;
+  int32_t* to = c.table + (size_t)b * c.max_pages;
+  for (int j = tid; j < held; j += 256) {
+    const int p = from[j];
+    to[j] = p;
+    if (p >= 0 && p < c.num_pages) atomicAdd(c.refs + p, 1);
+    else cache_error(c.control, BSA_ERR_PLAN_MISMATCH, a);
+  }
+  if (tid == 0) c.lens[b] = len;  // (every thread has read lens[b]: the barrier above)
+}
+
+// One CTA.  The i-th held page at or past L goes to the i-th free page below
+// L; list_a gets the map of the moved pages (indexed by page), the pairs what
+// the copy kernel moves.
+__global__ void __launch_bounds__(kThreads) compact_kernel(const CacheDev c) {
+  __shared__ int warp_s[33];
+  const int tid = threadIdx.x;
+  int live = 0;
+  for (int p = tid; p < c.num_pages; p += kThreads) live += c.refs[p] > 0;
+  int L;
+  block_scan(live, warp_s, L);
+  int holes = 0, moved = 0;
+  for (int base = 0; base < c.num_pages; base += kThreads * 4) {
+    const int p0 = base + tid * 4;
+    int r[4];
+    unsigned hole = 0, mover = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int p = p0 + q;
+      r[q] = p < c.num_pages ? c.refs[p] : 0;
+      if (p < c.num_pages && p < L && r[q] <= 0) hole |= 1u << q;
+      if (p >= L && r[q] > 0) mover |= 1u << q;
+    }
+    // Holes lie below L and movers at or past it: one scan of both counts.
+    int both;
+    int at = block_scan(__popc(hole) | __popc(mover) << 16, warp_s, both);
+    int ha = holes + (at & 0xffff), ma = moved + (at >> 16);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (hole >> q & 1) c.pair_dst()[ha++] = p0 + q;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (!(mover >> q & 1)) continue;
+      const int to = __ldcg(c.pair_dst() + ma);
+      c.pair_src()[ma++] = p0 + q;
+      c.list_a()[p0 + q] = to;
+      c.refs[to] = r[q];
+      c.refs[p0 + q] = 0;
+    }
+    holes += both & 0xffff;
+    moved += both >> 16;
+  }
+  if (tid == 0) {
+    c.control[kCacheLive] = L;
+    c.control[kCachePairs] = moved;
+  }
+}
+
+// The pairs a caller asks for: those that are in range, whose destination no
+// earlier pair has and (within one cache) no pair reads.
+__global__ void __launch_bounds__(kThreads) check_pairs_kernel(const CacheDev dst, const CacheDev src, int same,
+                                                               const int32_t* dp, const int32_t* sp, int n) {
+  __shared__ int s_pairs;
+  const int tid = threadIdx.x;
+  int32_t* mark = dst.list_a();
+  if (tid == 0) s_pairs = 0;
+  for (int i = tid; i < n; i += kThreads) {
+    const int d = dp[i], s = sp[i];
+    if (d >= 0 && d < dst.num_pages) mark[d] = 0x7fffffff;
+    if (same && s >= 0 && s < dst.num_pages) mark[s] = 0x7fffffff;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const int d = dp[i];
+    if (d >= 0 && d < dst.num_pages) atomicMin(mark + d, i);
+  }
+  __syncthreads();
+  if (same) {  // a source: negative from here on
+    for (int i = tid; i < n; i += kThreads) {
+      const int s = sp[i];
+      if (s >= 0 && s < dst.num_pages) atomicOr(mark + s, (int)0x80000000);
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const int d = dp[i], s = sp[i];
+    const bool ok = d >= 0 && d < dst.num_pages && s >= 0 && s < src.num_pages && __ldcg(mark + d) == i;
+    if (!ok) {
+      cache_error(dst.control, BSA_ERR_INVALID_ARG, i);
+      continue;
+    }
+    const int at = atomicAdd(&s_pairs, 1);
+    dst.pair_src()[at] = s;
+    dst.pair_dst()[at] = d;
+  }
+  __syncthreads();
+  if (tid == 0) dst.control[kCachePairs] = s_pairs;
+}
+
+// Moves the contents of the queued pairs (and, after a compaction, rewrites the
+// table).  Work items of 16 KB of codes: 256 threads x 4 independent 16-byte
+// copies, so that eight CTAs keep 128 KB in flight per SM; a pair's scales are
+// one more item.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyBytes = kCopyThreads * 16 * 4;
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CacheDev dst, const CacheDev src, int remap) {
+  const int tid = threadIdx.x;
+  const int pairs = __ldcg(dst.control + kCachePairs);
+  const long long bytes = (long long)dst.Hkv * dst.page * dst.d;  // of a page of K or V: a multiple of 1 KB
+  const int chunks = (int)((bytes + kCopyBytes - 1) / kCopyBytes);
+  const int per = 2 * chunks + 1;
+  const int scales = dst.Hkv * (dst.page / dst.sb);
+  const long long items = (long long)pairs * per;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int pr = (int)(it / per), w = (int)(it % per);
+    const int a = __ldcg(dst.pair_src() + pr), b = __ldcg(dst.pair_dst() + pr);
+    if (w < 2 * chunks) {
+      const uint8_t* from = (w < chunks ? src.k : src.v) + (size_t)a * bytes;
+      uint8_t* to = (w < chunks ? dst.k : dst.v) + (size_t)b * bytes;
+      const long long o = (long long)(w < chunks ? w : w - chunks) * kCopyBytes + tid * 16;
+      uint4 x[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (o + q * (kCopyThreads * 16) < bytes) x[q] = __ldcs(reinterpret_cast<const uint4*>(from + o + q * (kCopyThreads * 16)));
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (o + q * (kCopyThreads * 16) < bytes) *reinterpret_cast<uint4*>(to + o + q * (kCopyThreads * 16)) = x[q];
+    } else {
+      for (int i = tid; i < scales; i += kCopyThreads) {
+        dst.ks[(size_t)b * scales + i] = src.ks[(size_t)a * scales + i];
+        dst.vs[(size_t)b * scales + i] = src.vs[(size_t)a * scales + i];
+      }
+    }
+  }
+  if (remap && pairs > 0) {
+    const int L = __ldcg(dst.control + kCacheLive);
+    const long long entries = (long long)dst.max_seqs * dst.max_pages;
+    for (long long e = (long long)blockIdx.x * kCopyThreads + tid; e < entries; e += (long long)gridDim.x * kCopyThreads) {
+      const int p = dst.table[e];
+      if (p >= L && p < dst.num_pages) dst.table[e] = __ldcg(dst.list_a() + p);
+    }
+  }
+}
+
+// CTAs of the copy kernel for at most `pairs` pairs: eight per SM at most.
+int copy_grid(const CacheDev& c, long long pairs, int sms) {
+  const long long per = 2 * (((long long)c.Hkv * c.page * c.d + kCopyBytes - 1) / kCopyBytes) + 1;
+  const long long want = pairs * per;
+  const long long most = 8ll * (sms > 0 ? sms : 1);
+  return (int)(want < 1 ? 1 : (want < most ? want : most));
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 1;
+  return sms;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_resize(const CacheDev& c, const int32_t* seqs, const int32_t* new_lens, int n,
+                                cudaStream_t s) {
+  resize_kernel<<<1, kThreads, 0, s>>>(c, seqs, new_lens, n);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !new_lens) return e;  // freeing copies nothing
+  copy_kernel<<<copy_grid(c, n, sm_count()), kCopyThreads, 0, s>>>(c, c, 0);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_fork(const CacheDev& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
+  fork_kernel<<<n, 256, 0, s>>>(c, src, dst, n);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_compact(const CacheDev& c, int sms, cudaStream_t s) {
+  compact_kernel<<<1, kThreads, 0, s>>>(c);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  copy_kernel<<<copy_grid(c, c.num_pages / 2 + 1, sms), kCopyThreads, 0, s>>>(c, c, 1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_copy(const CacheDev& dst, const CacheDev& src, const int32_t* dst_pages,
+                              const int32_t* src_pages, int n, cudaStream_t s) {
+  const int same = dst.k == src.k ? 1 : 0;
+  check_pairs_kernel<<<1, kThreads, 0, s>>>(dst, src, same, dst_pages, src_pages, n);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  copy_kernel<<<copy_grid(dst, n, sm_count()), kCopyThreads, 0, s>>>(dst, src, 0);
+  return cudaGetLastError();
+}
+
+}  // namespace bsa

@@ -505,9 +505,10 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint8_t* smem, 
     if (kElem && p.elem_mask) {
       const int qmin = qpos - lane;  // the warp's 32 rows lie in one q-unit (qu >= 32)
       const int kvl = p.kv_lens ? __ldg(p.kv_lens + m.bh / p.H) : 0x7fffffff;
-      lim_row = min(p.causal ? qpos + p.causal_off : 0x7fffffff, kvl - 1);
-      lim_warp = min(p.causal ? qmin + p.causal_off : 0x7fffffff, kvl - 1);
-      lim_warp_hi = min(p.causal ? qmin + 31 + p.causal_off : 0x7fffffff, kvl - 1);
+      const int coff = p.causal_len ? kvl - p.Nq : p.causal_off;
+      lim_row = min(p.causal ? qpos + coff : 0x7fffffff, kvl - 1);
+      lim_warp = min(p.causal ? qmin + coff : 0x7fffffff, kvl - 1);
+      lim_warp_hi = min(p.causal ? qmin + 31 + coff : 0x7fffffff, kvl - 1);
     }
     float l_run = 0.f;                // the row sum of p (this thread's keys)
     bool has_keys = false;            // (bounded pass) some key of this thread's columns is kept

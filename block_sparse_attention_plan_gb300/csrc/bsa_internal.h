@@ -166,6 +166,7 @@ struct FwdParams {
   const int32_t* kv_lens;        // [B] or nullptr
   int causal;                    // key j visible to query i iff j <= i + causal_off
   int causal_off;                // Nk - Nq
+  int causal_len;                // the offset is kv_lens[b] - Nq instead
   int elem_mask;                 // causal || kv_lens
   int32_t* work_counter;         // set by launch_forward: the pass's work counter
   const int32_t* work_count;     // number of work items (nullptr: rows)
@@ -196,6 +197,11 @@ bsa_status make_fwd_params(const bsa_plan_layout& L, const PlanDev& pd, uint8_t*
                            const int32_t* kv_lens, int flags, void* O, float* LSE, int d,
                            float scale, int dev, long long watchdog_ns, long long grid_override,
                            FwdParams* out, int* grid_out);
+// Device check of every entry point, and the watchdog limit (bsa_api.cu).
+bsa_status check_device(int* dev_out);
+long long watchdog_limit_ns();
+// Tensor map of `rows` rows of d bytes, box {d, box_rows}, d-byte swizzle (d 64 or 128).
+bool encode_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int box_rows);
 cudaError_t launch_watchdog_selftest(int32_t* status, long long limit_ns, cudaStream_t stream);
 
 }  // namespace bsa

@@ -30,6 +30,10 @@
  * bsa_forward_stage (the forward's passes one by one), bsa_attention_host
  * (from host buffers with overlapped copies), bsa_attention_static (no
  * allocation at all).
+ * Serving: a paged K/V cache held in 8 bits (bsa_cache): bsa_cache_append
+ * (quantise and store tokens), bsa_cache_attention (single tokens and short
+ * drafts), bsa_cache_forward (a plan's forward over it: chunked prefill) and
+ * its pages (bsa_cache_resize, _fork, _compact, _copy_pages).
  *
  * Conventions
  *   - Every pointer argument named "device" is a CUDA device pointer owned by
@@ -476,6 +480,199 @@ bsa_status bsa_attention_host(const uint8_t* mask, int B, int H, int NQB, int NK
                               int gqa_group, const void* Q, const void* K, const void* V, void* O,
                               float* LSE, int d, float scale, int chunks, void* buffer,
                               size_t buffer_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------- 8-bit cache
+ * bsa_cache -- a paged K/V cache in 8 bits, with one fp32 scale for each block
+ * of scale_block tokens of a page and K/V head (value = code * scale).  Pages
+ * are laid out as for bsa_kv_pages: token j of a sequence lives in page
+ * block_table[seq * max_pages + j / page_size], row j % page_size.  The struct
+ * is read on the host; every pointer in it is a device buffer owned by the
+ * caller:
+ *   k, v         1-byte codes [num_pages][Hkv][page_size][d], 16-byte aligned
+ *   k_scale, v_scale  fp32 [num_pages][Hkv][page_size / scale_block]
+ *   block_table  int32 [max_seqs][max_pages], -1 = no page
+ *   seq_lens     int32 [max_seqs], tokens held by each sequence
+ *   page_refs    int32 [num_pages], sequences that hold each page (0 = free)
+ *   control      int32, bsa_cache_control_bytes(num_pages, max_seqs) bytes,
+ *                first 64 bytes zero before the first call: status words and
+ *                scratch of the page operations
+ * d in {64, 128}; page_size and scale_block powers of two, 16 <= scale_block
+ * <= page_size <= 256.  Calls on one cache must not overlap in time, except
+ * that calls which only read it (bsa_cache_attention, bsa_cache_forward) may
+ * overlap each other.  A sequence index of -1 in a list of sequences is a
+ * padded batch row: nothing is stored for it, and its attention is that of an
+ * empty sequence (O = 0, LSE = -inf).
+ *
+ * What the kernels find wrong in device data is recorded in the control words,
+ * the first of its kind kept, and reported by bsa_cache_status: a sequence
+ * index or length out of range, a sequence named twice, a fork onto a sequence
+ * that holds tokens (BSA_ERR_INVALID_ARG, detail = index in the list); a held
+ * token whose table entry is no page (BSA_ERR_PLAN_MISMATCH, detail = the
+ * sequence); too few free pages (BSA_ERR_WORKSPACE, detail = pages missing).
+ * Such an item is skipped (for BSA_ERR_WORKSPACE the whole call is); memory
+ * outside the cache is never touched.
+ */
+#define BSA_CACHE_E4M3 0 /* 8-bit floating point: 4 exponent bits, 3 mantissa bits, largest 448 */
+#define BSA_CACHE_INT8 1 /* -127 .. 127 */
+#define BSA_BF16 0       /* element types of tokens, queries and outputs */
+#define BSA_FP16 1
+
+typedef struct bsa_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* page_refs;
+  int32_t* control;
+  int32_t kind; /* BSA_CACHE_* */
+  int32_t num_pages, Hkv, page_size, d, scale_block, max_seqs, max_pages;
+} bsa_cache;
+
+/* A 4-dimensional tensor [batch][heads][tokens][d] of 2-byte elements, the d
+ * elements of a row contiguous; strides in elements, multiples of 8 (>= 0),
+ * data 16-byte aligned. */
+typedef struct bsa_rows {
+  void* data;
+  int64_t stride_b, stride_h, stride_t;
+} bsa_rows;
+
+/* Bytes of bsa_cache.control (0 for sizes < 1). */
+size_t bsa_cache_control_bytes(int num_pages, int max_seqs);
+
+/* Make a cache empty: no sequence holds a page, every page is free, the status
+ * words are clear.  The pools are not written. */
+bsa_status bsa_cache_init(const bsa_cache* cache, void* stream);
+
+/*
+ * bsa_cache_status -- synchronise `stream` (which the cache's calls have been
+ * enqueued on or before), report what its kernels recorded since the last
+ * report, and clear it.  *detail (may be NULL) receives the detail word.
+ */
+bsa_status bsa_cache_status(const bsa_cache* cache, void* stream, int32_t* detail);
+
+/*
+ * bsa_cache_resize -- set the lengths of n sequences, giving back the pages
+ * that shorter ones no longer need and taking pages for longer ones.
+ * seqs: device int32 [n], or NULL for sequences 0 .. n-1; each at most once.
+ * new_lens: device int32 [n], or NULL to free the sequences (length 0).
+ * Releases come first; then pages are taken in the order of the list, the
+ * lowest free page first (so a result depends on the cache's state and the
+ * arguments alone).  A sequence that grows into a partly filled last page
+ * which other sequences hold too gets a page of its own there, with the
+ * contents copied (of several such sequences in one call, those later in the
+ * list come last, and the one that is left alone with the page keeps it).
+ * New tokens' contents are what bsa_cache_append then stores.  If the free
+ * pages do not suffice nothing is changed.  n <= 4096.
+ * One kernel (two unless new_lens is NULL), no synchronisation.
+ */
+bsa_status bsa_cache_resize(const bsa_cache* cache, const int32_t* seqs, const int32_t* new_lens,
+                            int n, void* stream);
+
+/*
+ * bsa_cache_fork -- for each i < n, sequence dst[i] (empty, named once, and no
+ * src) takes the tokens of sequence src[i] by sharing its pages.  Nothing is
+ * copied: bsa_cache_resize separates the sequences where they grow.
+ * src, dst: device int32 [n]; -1 in either skips the pair.  n <= 4096.
+ */
+bsa_status bsa_cache_fork(const bsa_cache* cache, const int32_t* src, const int32_t* dst, int n,
+                          void* stream);
+
+/*
+ * bsa_cache_compact -- move pages so that the held ones are pages 0 .. L-1
+ * (L = how many are held): the i-th held page at or past L, ascending, goes to
+ * the i-th free page below L; tables and counts follow.  Pages past L are then
+ * free, and the pool may be cut there.  Two kernels, no synchronisation.
+ */
+bsa_status bsa_cache_compact(const bsa_cache* cache, void* stream);
+
+/*
+ * bsa_cache_copy_pages -- copy codes and scales of pages src_pages[i] of `src`
+ * to pages dst_pages[i] of `dst` (the same cache, or another of the same kind,
+ * heads, page size, d and scale block).  Tables and counts are not touched.
+ * Device int32 [n], n <= dst->num_pages.  A pair with an index out of range, a
+ * destination named earlier in the list, or (within one cache) one that is
+ * also a source, is skipped and recorded in dst's status
+ * (BSA_ERR_INVALID_ARG).  Two kernels, no synchronisation.
+ */
+bsa_status bsa_cache_copy_pages(const bsa_cache* dst, const bsa_cache* src, const int32_t* dst_pages,
+                                const int32_t* src_pages, int n, void* stream);
+
+/*
+ * bsa_cache_append -- quantise tokens and store them in the cache, in pages
+ * the sequences hold already (bsa_cache_resize first).
+ * k, v: [n][Hkv][T][d] of `dtype` (BSA_BF16 / BSA_FP16).
+ * seqs: device int32 [n] or NULL (sequences 0 .. n-1); each at most once.
+ * counts: device int32 [n] or NULL (all T): how many of the T tokens of each
+ *   row are stored (the first ones; 0 .. T).
+ * start: device int32 [n] or NULL: position of the first one; NULL = the
+ *   sequence's length - count, i.e. they are its last tokens.
+ * Tokens outside [0, length) are not stored and recorded (BSA_ERR_INVALID_ARG).
+ * Scale of a block: the smallest power of two, at least 2^-100, that takes the
+ * largest finite |x| of the stored tokens into the codes' range; if the
+ * sequence has other tokens in the block, the larger of that and the block's
+ * scale, and if that grows their codes are re-rounded to it.  Codes are
+ * rounded to nearest, ties to even; infinities saturate; NaN is stored as NaN
+ * (E4M3) or 0 (INT8).  Rows of pages that hold no token of the sequence are
+ * left as they were.  One kernel.
+ */
+bsa_status bsa_cache_append(const bsa_cache* cache, const bsa_rows* k, const bsa_rows* v, int dtype,
+                            const int32_t* seqs, const int32_t* counts, const int32_t* start, int n,
+                            int T, void* stream);
+
+/* Causal: query i of nq sees key j only when j <= length - nq + i (the queries
+ * are the sequence's last nq tokens). */
+#define BSA_CACHE_CAUSAL 0x1
+
+/*
+ * bsa_cache_attention -- attention of nq queries per sequence (one when
+ * decoding, a few for drafts; any number is taken) over the cached tokens:
+ *   O = sum_j p_j V_j / sum_j p_j, p_j = exp(scale <q, K_j> - m), over the keys
+ * j below the sequence's length that the mask selects; O = 0 and LSE = -inf
+ * where none is left.
+ * q: [B][Hq][nq][d], o: the same shape (written), both of `dtype`; LSE: device
+ *   fp32 [B][Hq][nq] contiguous (written), or NULL.  Hq a multiple of Hkv.
+ * seqs: device int32 [B] or NULL (sequences 0 .. B-1); the same sequence may
+ *   be named several times.
+ * mask: NULL, or device u8 [B][Hq][NKB]: non-zero selects key block j / bk for
+ *   a query head (keys past the last block are not selected); bk in {32, 64,
+ *   128, 256}.  Tiles of 64 keys that no head of a group selects are not read.
+ * flags: 0 or BSA_CACHE_CAUSAL.  scale <= 0 selects 1/sqrt(d).
+ * workspace: device, 16-byte aligned, bsa_cache_attention_workspace_bytes
+ *   bytes; scratch of this call (calls that overlap in time need their own).
+ * Q is used as given, codes and scales exactly; weights are rounded to fp16
+ * relative to (at most 2^8 times) the row's largest, sums are fp32.
+ * Two kernels, three with a mask.
+ */
+size_t bsa_cache_attention_workspace_bytes(const bsa_cache* cache, int B, int Hq, int nq, int NKB,
+                                           int bk);
+bsa_status bsa_cache_attention(const bsa_cache* cache, const bsa_rows* q, const bsa_rows* o, float* LSE,
+                               int dtype, const int32_t* seqs, const uint8_t* mask, int NKB, int bk,
+                               int B, int Hq, int nq, int flags, float scale, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * bsa_cache_forward -- bsa_forward_ex over a cache: the plan's B sequences are
+ * cache sequences seqs[b] (NULL: 0 .. B-1), key positions are their tokens,
+ * keys at or past a sequence's length are dropped, and with BSA_FWD_CAUSAL
+ * query i of the plan's Nq sees key j only when j <= length - Nq + i (each
+ * sequence's queries are its last Nq tokens).  The plan's Nk may be larger or
+ * smaller than the lengths (tokens past Nk are not attended).  d and Hkv are
+ * the cache's; 128-row q-tiles only.
+ * Q, O: device bf16 [B][Hq][Nq][d]; LSE fp32 [B][Hq][Nq]; flags as
+ *   bsa_forward_ex; workspace: device, 256-byte aligned,
+ *   bsa_cache_forward_workspace_bytes bytes (the keys and values in bf16).
+ * Scales other than powers of two round the values to bf16.
+ * Other errors as bsa_forward_ex; BSA_ERR_PLAN_MISMATCH for a plan of other
+ * heads.  Kernel errors are reported by bsa_sync_status (the plan's) and
+ * bsa_cache_status (the table's).
+ */
+size_t bsa_cache_forward_workspace_bytes(const bsa_plan* plan, const bsa_cache* cache);
+bsa_status bsa_cache_forward(const bsa_plan* plan, const bsa_cache* cache, const int32_t* seqs,
+                             const void* Q, int flags, void* O, float* LSE, float scale,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* bsa_status_string(int status);
