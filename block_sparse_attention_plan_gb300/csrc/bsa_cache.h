@@ -61,8 +61,8 @@ struct CacheAppendParams {
   const int32_t* start;
 };
 
-// Queries per unit of work at most: four row tiles of 16.
-constexpr int kCacheUnitRows = 64;
+// Queries per unit of work at most: three row tiles of 16.
+constexpr int kCacheUnitRows = 48;
 constexpr int kCacheTile = 64;       // keys per tile
 constexpr int kCacheMaxGrid = 320;   // most CTAs of the attention kernel (workspace bound)
 

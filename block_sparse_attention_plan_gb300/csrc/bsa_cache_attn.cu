@@ -18,7 +18,7 @@
 // What bounds it: 2 d bytes per key and K/V head at the memory's rate; an SM's
 // share is 23 bytes per cycle, against which a 64-key tile (16 KB at d = 128)
 // costs about 700 warp instructions, a quarter of what the SM issues meanwhile.
-// Hence mma.sync and not tcgen05: the products are 16 to 64 rows wide and far
+// Hence mma.sync and not tcgen05: the products are at most 48 rows wide and far
 // from the tensor pipe's limit, and the codes have to pass through registers
 // to be converted anyway.
 //
@@ -40,8 +40,12 @@ namespace {
 
 using namespace dev;
 
-constexpr int kWarps = 4;  // consumer warps; one more produces
+// Three consumer warps and a producer: eight warps on an SM with two CTAs, so
+// that each may hold 255 registers (with five warps per CTA it is 168, and two
+// column tiles spill).
+constexpr int kWarps = 3;
 constexpr int kAttnThreads = 32 * (kWarps + 1);
+static_assert(kCacheUnitRows == 16 * kWarps, "a warp for each 16 query rows of a full unit");
 constexpr int kScaleLanes = 8;  // producer lanes that copy scales: 4 groups of 16 keys, K and V
 constexpr float kMoveReference = 8.f;  // log2: weights stay <= 2^8
 
@@ -52,17 +56,20 @@ template <int D, int NT>
 struct AttnCfg {
   static constexpr int kTileBytes = kCacheTile * D;  // K or V of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kMergeBytes = kWarps * 8 * NT * D * 4;  // (the tile counts' prefix uses it first)
-  static constexpr int kMlBytes = kWarps * 8 * NT * 8;
+  static constexpr int kMergeBytes = kWarps * 8 * D * 4;  // 8 rows a warp at a time (the tile counts' prefix uses it first)
+  static constexpr int kMlBytes = kWarps * 8 * 8;
   static constexpr int kBudget = 113 * 1024;  // two CTAs per SM
-  static constexpr int kStages = (kBudget - kMergeBytes - kMlBytes - 16) / (kStageBytes + 48);
+  // A multiple of the consumer warps: a stage is used by the same warps every
+  // time.  (A warp that met a stage another one had used before could be a
+  // whole phase ahead of its barrier, where the parity of a wait is ambiguous.)
+  static constexpr int kStages = (kBudget - kMergeBytes - kMlBytes - 16) / (kStageBytes + 48) / kWarps * kWarps;
   static constexpr int kOffMerge = kStages * kStageBytes;
-  static constexpr int kOffMl = kOffMerge + kMergeBytes;        // float [warps][8 NT][2]
+  static constexpr int kOffMl = kOffMerge + kMergeBytes;        // float [warps][8][2]
   static constexpr int kOffScale = kOffMl + kMlBytes;           // float [stages][8]
   static constexpr int kOffBar = kOffScale + kStages * 32;      // full, empty [stages]
   static constexpr int kOffAbort = kOffBar + kStages * 16;
   static constexpr int kSmem = kOffAbort + 16;
-  static_assert(kSmem <= kBudget && kMergeBytes >= 8 * (kAttnThreads + 1), "shared memory");
+  static_assert(kStages % kWarps == 0 && kStages > 0 && kSmem <= kBudget && kMergeBytes >= 8 * (kAttnThreads + 1), "shared memory");
 };
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   // Warps that share a tile: one for each 16 query rows (row tiles), the others
   // take other tiles.
   const int rows_unit = min(p.M, kCacheUnitRows);
-  const int R = NT == 1 ? 1 : (rows_unit <= 16 ? 1 : (rows_unit <= 32 ? 2 : 4));
+  const int R = rows_unit <= 8 * NT ? 1 : kWarps;
   if (tid == 0) {
     *s_abort = 0;
     if (base & 1023u) record_failure(wd, BSA_ERR_CUDA, 0);  // the swizzle's layout needs it
@@ -674,49 +681,46 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(empty(s));
     }
 
-    // ---- end of the piece: join the warps that took its tiles
+    // ---- end of the piece: join the warps that took its tiles, 8 rows of each
+    // warp at a time
+    const bool starts = w.t0 == 0, whole = starts && w.t1 == w.cnt;
+    const int rows = min(p.M - u.grp * kCacheUnitRows, kCacheUnitRows);
+    float* part = p.part + (size_t)(2 * cta + (starts ? 1 : 0)) * p.rows_cap * (D + 2);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      if (nt > 0) named_bar_sync(1, 32 * kWarps);  // the rows before have been read
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float l = l_sum[nt][c];
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        const int row = 8 * nt + 2 * t4 + c;
+        const int row = warp * 8 + 2 * t4 + c;
         if (g == 0) {
-          ml[(warp * 8 * NT + row) * 2] = m_ref[nt][c];
-          ml[(warp * 8 * NT + row) * 2 + 1] = l;
+          ml[row * 2] = m_ref[nt][c];
+          ml[row * 2 + 1] = l;
         }
-        float* mr = merge + (size_t)(warp * 8 * NT + row) * D + g * DV;
+        float* mr = merge + (size_t)row * D + g * DV;
 #pragma unroll
         for (int k = 0; k < MT; k += 2)
           *reinterpret_cast<float4*>(mr + 2 * k) =
               make_float4(o[nt][k][c], o[nt][k][c + 2], o[nt][k + 1][c], o[nt][k + 1][c + 2]);
       }
-    }
-    named_bar_sync(1, 32 * kWarps);
-    {
-      const bool whole = w.t0 == 0 && w.t1 == w.cnt;
-      const bool starts = w.t0 == 0;
-      const int rows = min(p.M - u.grp * kCacheUnitRows, kCacheUnitRows);
-      float* part = p.part + (size_t)(2 * cta + (starts ? 1 : 0)) * p.rows_cap * (D + 2);
+      named_bar_sync(1, 32 * kWarps);
       // A thread per (row, 4 elements).
-      for (int i = tid; i < rows * (D / 4); i += 32 * kWarps) {
-        const int r = i / (D / 4), c4 = i % (D / 4);
-        const int rtile = r / (8 * NT), rr = r % (8 * NT);
-        float mw[kWarps], M = -INFINITY;
-        for (int k = 0; k < KL; ++k) {
-          mw[k] = ml[((k * R + rtile) * 8 * NT + rr) * 2];
-          M = fmaxf(M, mw[k]);
-        }
+      for (int i = tid; i < R * 8 * (D / 4); i += 32 * kWarps) {
+        const int c4 = i % (D / 4), rr = i / (D / 4) % 8, rtile = i / (D / 4) / 8;
+        const int r = rtile * 16 + 8 * nt + rr;  // row of the unit
+        if (r >= rows) continue;
+        float M = -INFINITY;
+        for (int k = 0; k < KL; ++k) M = fmaxf(M, ml[((k * R + rtile) * 8 + rr) * 2]);
         float L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < KL; ++k) {
-          const int at = (k * R + rtile) * 8 * NT + rr;
-          const float f = M == -INFINITY ? 1.f : ex2_approx(mw[k] - M);
+          const int at = (k * R + rtile) * 8 + rr;
+          const float f = M == -INFINITY ? 1.f : ex2_approx(ml[at * 2] - M);
           const float4 y = *reinterpret_cast<const float4*>(merge + (size_t)at * D + 4 * c4);
-          L += f * ml[at * 2 + 1];
+          L = fmaf(f, ml[at * 2 + 1], L);
           acc.x = fmaf(f, y.x, acc.x);
           acc.y = fmaf(f, y.y, acc.y);
           acc.z = fmaf(f, y.z, acc.z);
@@ -724,10 +728,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         }
         if (whole) {
           const int m = u.grp * kCacheUnitRows + r;
-          const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+          const bool some = L > 0.f || L != L;
+          const float inv = some ? 1.f / L : 0.f;
           store2(p, o_row(p, u.b, u.h, m) + 4 * c4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
           if (c4 == 0 && p.lse)
-            *lse_row(p, u.b, u.h, m) = L > 0.f || L != L ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+            *lse_row(p, u.b, u.h, m) = some ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
         } else {
           float* pr = part + (size_t)r * (D + 2);
           *reinterpret_cast<float2*>(pr + 4 * c4) = make_float2(acc.x, acc.y);
@@ -735,15 +740,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
           if (c4 == 0) *reinterpret_cast<float2*>(pr + D) = make_float2(M, L);
         }
       }
-      if (tid == 0 && starts && !whole) {
-        // CTAs up to the one that holds the unit's last tile.
-        const long long last = w.row0 + w.cnt - 1;
-        const int c1 = (int)(((last + 1) * G - 1) / T);
-        p.desc[4 * cta + 1] = u.b;
-        p.desc[4 * cta + 2] = u.h;
-        p.desc[4 * cta + 3] = u.grp;
-        p.desc[4 * cta] = c1 - cta + 1;
-      }
+    }
+    if (tid == 0 && starts && !whole) {
+      // CTAs up to the one that holds the unit's last tile.
+      const long long last = w.row0 + w.cnt - 1;
+      const int c1 = (int)(((last + 1) * G - 1) / T);
+      p.desc[4 * cta + 1] = u.b;
+      p.desc[4 * cta + 2] = u.h;
+      p.desc[4 * cta + 3] = u.grp;
+      p.desc[4 * cta] = c1 - cta + 1;
     }
     named_bar_sync(1, 32 * kWarps);
     more = walk_next(p, w, mult);

@@ -172,9 +172,10 @@ class CacheModel:
         out = []
         for codes, scales in zip(self.codes, self.scales):
             x = np.zeros((codes.shape[1], n, self.d))
-            for t in range(n):
-                p, r = int(self.table[seq, t // self.page]), t % self.page
-                x[:, t] = decode(codes[p, :, r], self.kind) * scales[p, :, r // self.sb].astype(np.float64)[:, None]
+            for j in range(self._pages(n)):
+                p, a = int(self.table[seq, j]), j * self.page
+                w = decode(codes[p], self.kind) * scales[p].astype(np.float64).repeat(self.sb, 1)[..., None]
+                x[:, a:a + self.page] = w[:, :n - a]
             out.append(x)
         return out
 

@@ -341,14 +341,18 @@ def test_block_masks(bsa, bk, nq):
     check_attention(bsa, m, c, q, causal=nq > 1, mask=mask, bk=bk, what=f"bk {bk}")
 
 
-@pytest.mark.parametrize("B,length,heads", [(1, 20000, 1), (2, 9000, 4), (300, 70, 2)])
-def test_rows_cut_over_many_ctas(bsa, B, length, heads):
+@pytest.mark.parametrize("B,length,heads,g,nq,d,kind", [
+    (1, 20000, 1, 2, 1, 64, "int8"), (2, 9000, 4, 2, 1, 64, "int8"), (300, 70, 2, 2, 1, 64, "int8"),
+    # tens of tiles per CTA, so that every stage of the ring is used many times
+    (6, 24000, 4, 4, 1, 128, "e4m3"), (3, 30000, 4, 12, 1, 128, "int8"), (4, 26000, 4, 4, 6, 64, "e4m3"),
+    (2, 24000, 4, 4, 13, 128, "e4m3")])
+def test_rows_cut_over_many_ctas(bsa, B, length, heads, g, nq, d, kind):
     lens = [length - (i * 13) % min(length, 61) for i in range(B)]
-    m, c = filled(bsa, lens, heads, 64, 64, 64, "int8", -(-length // 64), seed=B)
-    q = rand(torch.Generator().manual_seed(3), B, heads * 2, 1, 64)
-    o, lse = check_attention(bsa, m, c, q, what=f"B {B} length {length}")
-    for _ in range(3):  # nothing depends on which CTA is first
-        o2, lse2 = bsa.cache_attention(c, q.cuda())
+    m, c = filled(bsa, lens, heads, 64, 64, d, kind, -(-length // 64), seed=B)
+    q = rand(torch.Generator().manual_seed(3), B, heads * g, nq, d)
+    o, lse = check_attention(bsa, m, c, q, causal=nq > 1, what=f"B {B} length {length}")
+    for _ in range(10):  # nothing depends on which CTA is first
+        o2, lse2 = bsa.cache_attention(c, q.cuda(), causal=nq > 1)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
