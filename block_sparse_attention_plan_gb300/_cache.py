@@ -43,7 +43,7 @@ def _library() -> ctypes.CDLL:
     P, I, F, VP, N = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
     C, R = ctypes.POINTER(CacheC), ctypes.POINTER(RowsC)
     lib.bsa_cache_control_bytes.restype = N
-    lib.bsa_cache_control_bytes.argtypes = [I, I]
+    lib.bsa_cache_control_bytes.argtypes = [I]
     lib.bsa_cache_attention_workspace_bytes.restype = N
     lib.bsa_cache_attention_workspace_bytes.argtypes = [C, I, I, I, I, I]
     lib.bsa_cache_forward_workspace_bytes.restype = N
@@ -89,8 +89,8 @@ class Cache:
             raise ValueError("k_scale does not divide a page into blocks")
         if block_table.dim() != 2 or tuple(lens.shape) != (block_table.shape[0],) or tuple(refs.shape) != (pages,):
             raise ValueError("block_table must be [max_seqs, max_pages], lens [max_seqs], refs [num_pages]")
-        self.device = k.device
-        need = int(_library().bsa_cache_control_bytes(pages, block_table.shape[0])) // 4
+        self.device, self._index = k.device, k.device.index
+        need = int(_library().bsa_cache_control_bytes(pages)) // 4
         if control is None:
             control = torch.zeros(need, dtype=torch.int32, device=k.device)
         for name, t, dtype in (("k", k, k.dtype), ("v", v, k.dtype), ("k_scale", k_scale, torch.float32),
@@ -133,30 +133,30 @@ def cache_create(num_pages: int, heads: int, page_size: int, d: int, max_seqs: i
     scale = lambda: z(num_pages, heads, page_size // sb, dtype=torch.float32)
     c = Cache(pool(), pool(), scale(), scale(), z(max_seqs, max_pages, dtype=torch.int32),
               z(max_seqs, dtype=torch.int32), z(num_pages, dtype=torch.int32))
-    with _On(c.device):
-        _check(_library().bsa_cache_init(c._ref, _stream(c, None)), "bsa_cache_init")
+    _call(c, "bsa_cache_init", c._ref, _stream(c, None))
     return c
 
 
-class _On:
-    """Makes a device current where it is not."""
-    __slots__ = ("to", "was")
-
-    def __init__(self, device: torch.device):
-        self.to = device.index
-
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.was != self.to:
-            torch.cuda.set_device(self.to)
-
-    def __exit__(self, *a):
-        if self.was != self.to:
-            torch.cuda.set_device(self.was)
+# The raw handle of a device's current stream (the object that
+# torch.cuda.current_stream builds around it costs 2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _stream(c: Cache, stream) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(c.device)).cuda_stream
+    return _raw_stream(c._index) if stream is None else stream.cuda_stream
+
+
+def _call(c: Cache, name: str, *args) -> None:
+    """One entry point, on the cache's device."""
+    f = getattr(_bound, name)
+    if torch.cuda.current_device() == c._index:
+        status = f(*args)
+    else:
+        with torch.cuda.device(c._index):
+            status = f(*args)
+    if status:
+        _check(status, name)
 
 
 def _list(c: Cache, t: Optional[torch.Tensor], name: str, n: Optional[int] = None) -> Optional[int]:
@@ -169,12 +169,14 @@ def _list(c: Cache, t: Optional[torch.Tensor], name: str, n: Optional[int] = Non
     return t.data_ptr()
 
 
-def _rows(c: Cache, t: torch.Tensor, name: str) -> RowsC:
+def _rows(c: Cache, t: torch.Tensor, name: str):
+    """bsa_rows of a tensor [batch, heads, tokens, d], by reference."""
     if t.dtype not in _ELEMENTS or t.device != c.device or t.dim() != 4 or t.stride(3) != 1:
         raise ValueError(f"{name} must be a 4-dimensional CUDA bfloat16 or float16 tensor with contiguous rows")
-    # A dimension of one element has no stride of its own.
-    s, n = t.stride(), t.shape
-    return RowsC(t.data_ptr(), *(s[i] if n[i] > 1 else 0 for i in range(3)))
+    b, h, r, _ = t.stride()
+    if (b | h | r) & 7:  # a dimension of one element has no stride of its own
+        b, h, r = (x if n > 1 else 0 for x, n in zip((b, h, r), t.shape))
+    return ctypes.byref(RowsC(t.data_ptr(), b, h, r))
 
 
 def cache_append(c: Cache, k: torch.Tensor, v: torch.Tensor, seqs: Optional[torch.Tensor] = None,
@@ -189,11 +191,9 @@ def cache_append(c: Cache, k: torch.Tensor, v: torch.Tensor, seqs: Optional[torc
         raise ValueError("k and v differ in shape or type")
     if h != c.heads or d != c.d:
         raise ValueError("k and v must be [n, Hkv, T, d] of the cache's Hkv and d")
-    kr, vr = _rows(c, k, "k"), _rows(c, v, "v")
-    with _On(c.device):
-        _check(_library().bsa_cache_append(
-            c._ref, ctypes.byref(kr), ctypes.byref(vr), _ELEMENTS[k.dtype], _list(c, seqs, "seqs", n),
-            _list(c, counts, "counts", n), _list(c, start, "start", n), n, T, _stream(c, stream)), "bsa_cache_append")
+    _call(c, "bsa_cache_append", c._ref, _rows(c, k, "k"), _rows(c, v, "v"), _ELEMENTS[k.dtype],
+          _list(c, seqs, "seqs", n), _list(c, counts, "counts", n), _list(c, start, "start", n), n, T,
+          _stream(c, stream))
 
 
 def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = None,
@@ -212,42 +212,38 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
     NKB, mptr = 0, None
     if mask is not None:
         if (mask.dtype != torch.uint8 or mask.device != c.device or mask.dim() != 3
-                or tuple(mask.shape[:2]) != (B, Hq) or not mask.is_contiguous()):
+                or mask.shape[:2] != q.shape[:2] or not mask.is_contiguous()):
             raise ValueError("mask must be a contiguous CUDA uint8 tensor [B, Hq, NKB]")
         NKB, mptr = mask.shape[2], mask.data_ptr()
     if out is None:
-        out = torch.empty(B, Hq, nq, d, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and type")
     if lse is None:
-        lse = torch.empty(B, Hq, nq, dtype=torch.float32, device=q.device)
-    elif (lse.dtype != torch.float32 or lse.device != c.device or tuple(lse.shape) != (B, Hq, nq)
+        lse = torch.empty((B, Hq, nq), dtype=torch.float32, device=c.device)
+    elif (lse.dtype != torch.float32 or lse.device != c.device or lse.shape != q.shape[:3]
           or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous CUDA float32 tensor [B, Hq, nq]")
-    orows = _rows(c, out, "out")
-    lib = _library()
     key = (B, Hq, nq, NKB, bk)
     need = c._workspace_bytes.get(key)
     if need is None:
-        need = int(lib.bsa_cache_attention_workspace_bytes(c._ref, *key))
+        need = int(_bound.bsa_cache_attention_workspace_bytes(c._ref, *key))
         if len(c._workspace_bytes) > 256:
             c._workspace_bytes.clear()
         c._workspace_bytes[key] = need
     ws = torch.empty(max(need, 16), dtype=torch.uint8, device=c.device)
-    with _On(c.device):
-        s = _stream(c, stream)
-        _check(lib.bsa_cache_attention(
-            c._ref, ctypes.byref(qr), ctypes.byref(orows), lse.data_ptr(), _ELEMENTS[q.dtype],
-            _list(c, seqs, "seqs", B), mptr, NKB, bk, B, Hq, nq, CACHE_CAUSAL if causal else 0,
-            0.0 if scale is None else float(scale), ws.data_ptr(), need, s), "bsa_cache_attention")
-    _used_on(ws, stream)
+    _call(c, "bsa_cache_attention", c._ref, qr, _rows(c, out, "out"), lse.data_ptr(), _ELEMENTS[q.dtype],
+          _list(c, seqs, "seqs", B), mptr, NKB, bk, B, Hq, nq, CACHE_CAUSAL if causal else 0,
+          0.0 if scale is None else scale, ws.data_ptr(), need, _stream(c, stream))
+    if stream is not None:
+        _used_on(ws, stream)
     return out, lse
 
 
-def _used_on(ws: torch.Tensor, stream) -> None:
+def _used_on(ws: torch.Tensor, stream: torch.cuda.Stream) -> None:
     """A workspace that a call on another stream still uses goes back to the
     allocator only after it."""
-    if stream is not None and stream != torch.cuda.current_stream(ws.device):
+    if stream != torch.cuda.current_stream(ws.device):
         ws.record_stream(stream)
 
 
@@ -270,20 +266,16 @@ def cache_forward(p: Plan, c: Cache, q: torch.Tensor, seqs: Optional[torch.Tenso
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    lib = _library()
-    need = int(lib.bsa_cache_forward_workspace_bytes(p.handle, c._ref))
+    need = int(_bound.bsa_cache_forward_workspace_bytes(p.handle, c._ref))
     ws = workspace
     if ws is None:
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=c.device)
     elif ws.dtype != torch.uint8 or ws.device != c.device or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
-    with _On(c.device):
-        _check(lib.bsa_cache_forward(
-            p.handle, c._ref, _list(c, seqs, "seqs", L.B), q.data_ptr(),
-            (_lib.FWD_CAUSAL if causal else 0) | (_lib.FWD_SPLIT_P if split else 0), out.data_ptr(), lse.data_ptr(),
-            0.0 if scale is None else float(scale), ws.data_ptr(), ws.numel(), _stream(c, stream)),
-            "bsa_cache_forward")
-    if workspace is None:
+    _call(c, "bsa_cache_forward", p.handle, c._ref, _list(c, seqs, "seqs", L.B), q.data_ptr(),
+          (_lib.FWD_CAUSAL if causal else 0) | (_lib.FWD_SPLIT_P if split else 0), out.data_ptr(), lse.data_ptr(),
+          0.0 if scale is None else scale, ws.data_ptr(), ws.numel(), _stream(c, stream))
+    if workspace is None and stream is not None:
         _used_on(ws, stream)
     return out, lse
 
@@ -292,31 +284,24 @@ def cache_resize(c: Cache, new_lens: torch.Tensor, seqs: Optional[torch.Tensor] 
                  stream: Optional[torch.cuda.Stream] = None) -> None:
     """Set sequences' lengths, taking and giving back pages (bsa_cache_resize)."""
     n = new_lens.shape[0]
-    with _On(c.device):
-        _check(_library().bsa_cache_resize(c._ref, _list(c, seqs, "seqs", n), _list(c, new_lens, "new_lens"), n,
-                                           _stream(c, stream)), "bsa_cache_resize")
+    _call(c, "bsa_cache_resize", c._ref, _list(c, seqs, "seqs", n), _list(c, new_lens, "new_lens"), n, _stream(c, stream))
 
 
 def cache_free(c: Cache, seqs: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Free sequences, all of them by default (bsa_cache_resize to length 0)."""
     n = c.max_seqs if seqs is None else seqs.shape[0]
-    with _On(c.device):
-        _check(_library().bsa_cache_resize(c._ref, _list(c, seqs, "seqs"), None, n, _stream(c, stream)),
-               "bsa_cache_resize")
+    _call(c, "bsa_cache_resize", c._ref, _list(c, seqs, "seqs"), None, n, _stream(c, stream))
 
 
 def cache_fork(c: Cache, src: torch.Tensor, dst: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Let empty sequences dst[i] share the tokens of src[i] (bsa_cache_fork)."""
     n = src.shape[0]
-    with _On(c.device):
-        _check(_library().bsa_cache_fork(c._ref, _list(c, src, "src"), _list(c, dst, "dst", n), n,
-                                         _stream(c, stream)), "bsa_cache_fork")
+    _call(c, "bsa_cache_fork", c._ref, _list(c, src, "src"), _list(c, dst, "dst", n), n, _stream(c, stream))
 
 
 def cache_compact(c: Cache, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Move the held pages to the front of the pools (bsa_cache_compact)."""
-    with _On(c.device):
-        _check(_library().bsa_cache_compact(c._ref, _stream(c, stream)), "bsa_cache_compact")
+    _call(c, "bsa_cache_compact", c._ref, _stream(c, stream))
 
 
 def cache_copy_pages(dst: Cache, src: Cache, dst_pages: torch.Tensor, src_pages: torch.Tensor,
@@ -326,16 +311,14 @@ def cache_copy_pages(dst: Cache, src: Cache, dst_pages: torch.Tensor, src_pages:
     if dst.device != src.device:
         raise ValueError("dst and src must be on one device")
     n = dst_pages.shape[0]
-    with _On(dst.device):
-        _check(_library().bsa_cache_copy_pages(dst._ref, src._ref, _list(dst, dst_pages, "dst_pages"),
-                                               _list(dst, src_pages, "src_pages", n), n, _stream(dst, stream)),
-               "bsa_cache_copy_pages")
+    _call(dst, "bsa_cache_copy_pages", dst._ref, src._ref, _list(dst, dst_pages, "dst_pages"),
+          _list(dst, src_pages, "src_pages", n), n, _stream(dst, stream))
 
 
 def cache_status(c: Cache, stream: Optional[torch.cuda.Stream] = None) -> Tuple[int, int]:
     """(status, detail) the cache's kernels recorded since the last report;
     synchronises, and clears it (bsa_cache_status)."""
     det = ctypes.c_int32(0)
-    with _On(c.device):
-        st = _library().bsa_cache_status(c._ref, _stream(c, stream), ctypes.byref(det))
+    with torch.cuda.device(c._index):
+        st = _bound.bsa_cache_status(c._ref, _stream(c, stream), ctypes.byref(det))
     return st, det.value

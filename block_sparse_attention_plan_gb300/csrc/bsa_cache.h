@@ -29,17 +29,38 @@ struct CacheDev {
   int32_t* refs;
   int32_t* control;
   int kind, num_pages, Hkv, page, d, sb, max_seqs, max_pages;
-  // Scratch: free pages found / page map / marks; copy pairs; marks by sequence.
+  // Scratch: free pages found / page map / marks; copy pairs.
   __host__ __device__ int32_t* list_a() const { return control + kCacheScratch; }
   __host__ __device__ int32_t* pair_src() const { return control + kCacheScratch + num_pages; }
   __host__ __device__ int32_t* pair_dst() const { return control + kCacheScratch + 2 * (size_t)num_pages; }
-  __host__ __device__ int32_t* marks() const { return control + kCacheScratch + 3 * (size_t)num_pages; }
 };
-inline size_t cache_control_ints(int num_pages, int max_seqs) {
-  return kCacheScratch + 3 * (size_t)num_pages + (size_t)max_seqs;
+inline size_t cache_control_ints(int num_pages) { return kCacheScratch + 3 * (size_t)num_pages; }
+
+// Launch that may become resident before the kernel ahead of it in the stream
+// has ended.  Every kernel launched so begins with wait_for_previous(), which
+// returns when that one has ended and its writes are visible; it lets its own
+// successor queue up right away.  Hides most of the 2 us between dependent
+// kernels, which is what calls on a few sequences consist of.
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t s,
+                         const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 #ifdef __CUDACC__
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // First error of its cache since the last report.
 __device__ __forceinline__ void cache_error(int32_t* control, int code, int detail) {
   if (atomicCAS(control + kCacheStatus, 0, code) == 0) atomicExch(control + kCacheDetail, detail);
@@ -91,7 +112,7 @@ cudaError_t launch_cache_fork(const CacheDev& c, const int32_t* src, const int32
 cudaError_t launch_cache_compact(const CacheDev& c, int sms, cudaStream_t s);
 cudaError_t launch_cache_copy(const CacheDev& dst, const CacheDev& src, const int32_t* dst_pages,
                               const int32_t* src_pages, int n, cudaStream_t s);
-cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheAppendParams& p, int sms, cudaStream_t s);
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int grid, cudaStream_t s);
 // K and V of sequences seqs[0 .. B) as bf16 [B][Hkv][Nk][d] (zero at and past
 // the length) and their lengths [B].

@@ -100,9 +100,7 @@ bsa_status attn_layout(const CacheDev& c, int B, int Hq, int nq, int NKB, int bk
 
 extern "C" {
 
-size_t bsa_cache_control_bytes(int num_pages, int max_seqs) {
-  return num_pages < 1 || max_seqs < 1 ? 0 : 4 * cache_control_ints(num_pages, max_seqs);
-}
+size_t bsa_cache_control_bytes(int num_pages) { return num_pages < 1 ? 0 : 4 * cache_control_ints(num_pages); }
 
 bsa_status bsa_cache_init(const bsa_cache* cache, void* stream) {
   CacheDev c;
@@ -187,7 +185,8 @@ bsa_status bsa_cache_append(const bsa_cache* cache, const bsa_rows* k, const bsa
   if (!list_ok(seqs) || !list_ok(counts) || !list_ok(start) || (!seqs && n > p.c.max_seqs)) return BSA_ERR_INVALID_ARG;
   if (dtype != BSA_BF16 && dtype != BSA_FP16) return BSA_ERR_UNSUPPORTED;
   if ((long long)T > (long long)p.c.max_pages * p.c.page) return BSA_ERR_INVALID_ARG;
-  if ((st = check_device(nullptr)) != BSA_OK) return st;
+  int dev = 0, sms = 0;
+  if ((st = check_device(&dev)) != BSA_OK || (st = sms_of(dev, &sms)) != BSA_OK) return st;
   p.k = rows_of(k);
   p.v = rows_of(v);
   p.fp16 = dtype == BSA_FP16;
@@ -197,7 +196,7 @@ bsa_status bsa_cache_append(const bsa_cache* cache, const bsa_rows* k, const bsa
   p.seqs = seqs;
   p.counts = counts;
   p.start = start;
-  return launch_cache_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  return launch_cache_append(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
 size_t bsa_cache_attention_workspace_bytes(const bsa_cache* cache, int B, int Hq, int nq, int NKB, int bk) {

@@ -26,7 +26,11 @@
 // which the CTAs cut into equal pieces, so that ragged lengths and few long
 // sequences both fill the machine.  A row whose tiles lie in several CTAs
 // leaves partial sums in the workspace; the combine kernel joins them in the
-// order of the CTAs (results do not depend on timing).  Inside a CTA the tiles
+// order of the CTAs (results do not depend on timing).  It is launched ahead of
+// this kernel's end and waits for it.  (Joining by the CTA that is last, behind
+// a flag per part, saves the launch but puts fences and reads of L2 that is
+// busy with the others' tiles at the end of every CTA: 193 us against 183 us
+// for 32 sequences of up to 32768 tokens.)  Inside a CTA the tiles
 // go round the warps, each with its own sums, joined when the piece of a row
 // ends.  One warp feeds a ring of tiles by TMA (each page's rows of a head are
 // one box, 128-byte swizzled so that both products read without conflicts)
@@ -269,6 +273,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     tma_prefetch_desc(&p.tmK);
     tma_prefetch_desc(&p.tmV);
   }
+  next_may_launch();  // the combine kernel may queue up
+  wait_for_previous();
   // This CTA's piece of the line: sums of the entries' tiles by thread, then a
   // prefix over the threads.
   const int E = p.mask ? p.B * p.c.Hkv : p.B;
@@ -295,9 +301,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   }
   __syncthreads();
   const long long T = s_prefix[kAttnThreads];
-  // No CTA that works has an empty piece, so the parts of a row are those of
-  // consecutive CTAs.
-  const int G = (int)(T < (long long)gridDim.x ? T : (long long)gridDim.x);
+  // A tile at least for each set of warps that shares one, so that short lines
+  // leave few parts to join.  No CTA that works has an empty piece: the parts of
+  // a row are those of consecutive CTAs.
+  const int KL = kWarps / R;
+  const long long most = (T + KL - 1) / KL;
+  const int G = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x);
   const long long lo = cta < G ? cta * T / G : 0, hi = cta < G ? (cta + 1) * T / G : 0;
   // Empty entries' rows: O = 0, LSE = -inf.
   for (int e = cta; e < E; e += (int)gridDim.x) {
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
 
   // --------------------------------------------------------------- consumers
   const int g = lane >> 2, t4 = lane & 3;
-  const int KL = kWarps / R, rt = warp % R, kl = warp / R;
+  const int rt = warp % R, kl = warp / R;
   constexpr int KS = D / 16;    // 16-element steps of q . k
   constexpr int MT = D / 16;    // 16-row tiles of O^T
   constexpr int DV = D / 8;     // consecutive elements of O a thread holds
@@ -745,10 +754,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       // CTAs up to the one that holds the unit's last tile.
       const long long last = w.row0 + w.cnt - 1;
       const int c1 = (int)(((last + 1) * G - 1) / T);
-      p.desc[4 * cta + 1] = u.b;
-      p.desc[4 * cta + 2] = u.h;
-      p.desc[4 * cta + 3] = u.grp;
-      p.desc[4 * cta] = c1 - cta + 1;
+      *reinterpret_cast<int4*>(p.desc + 4 * cta) = make_int4(c1 - cta + 1, u.b, u.h, u.grp);
     }
     named_bar_sync(1, 32 * kWarps);
     more = walk_next(p, w, mult);
@@ -756,63 +762,72 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
 }
 
 // Joins the parts of a row that several CTAs worked on, in the CTAs' order.
-// One CTA per (first CTA of the row, query row); its warps take every fourth
-// part each.
+// One CTA per (first CTA of the row, query row and every kCombineRows-th after
+// it); its warps take every fourth part each.
+constexpr int kCombineRows = 4;
+
 template <int D>
-__global__ void __launch_bounds__(128) combine_kernel(const CacheAttnParams p) {
-  __shared__ float s_ml[4][2];
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CacheAttnParams p) {
+  __shared__ float s_l[4];
   __shared__ float s_o[4][D];
-  const int c0 = blockIdx.x, r = blockIdx.y;
+  next_may_launch();
+  wait_for_previous();
+  const int c0 = blockIdx.x;
   const int4 ds = *reinterpret_cast<const int4*>(p.desc + 4 * c0);
   const int n = ds.x;
   if (n <= 0) return;
-  const int m = ds.w * kCacheUnitRows + r;
-  if (m >= p.M) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto slot = [&](int k) { return p.part + ((size_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * p.rows_cap + r) * (D + 2); };
-  float M = -INFINITY;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, slot(k)[D]);
+  const int rows = min(p.M - ds.w * kCacheUnitRows, kCacheUnitRows);
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    auto slot = [&](int k) { return p.part + ((size_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * p.rows_cap + r) * (D + 2); };
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, slot(k)[D]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f;
-  constexpr int E = D / 32;
-  float acc[E] = {};
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    constexpr int E = D / 32;
+    float acc[E] = {};
 #pragma unroll 4
-  for (int k = warp; k < n; k += 4) {
-    const float* s = slot(k);
-    const float2 ml = *reinterpret_cast<const float2*>(s + D);
-    const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
-    L = fmaf(f, ml.y, L);
+    for (int k = warp; k < n; k += 4) {
+      const float* s = slot(k);
+      const float2 ml = *reinterpret_cast<const float2*>(s + D);
+      const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
+      L = fmaf(f, ml.y, L);
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      const float2 y = *reinterpret_cast<const float2*>(s + lane * E + 2 * e);
-      acc[2 * e] = fmaf(f, y.x, acc[2 * e]);
-      acc[2 * e + 1] = fmaf(f, y.y, acc[2 * e + 1]);
+      for (int e = 0; e < E / 2; ++e) {
+        const float2 y = *reinterpret_cast<const float2*>(s + lane * E + 2 * e);
+        acc[2 * e] = fmaf(f, y.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(f, y.y, acc[2 * e + 1]);
+      }
     }
-  }
-  if (lane == 0) s_ml[warp][1] = L;
+    __syncthreads();  // the row before has been read
+    if (lane == 0) s_l[warp] = L;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
-  __syncthreads();
-  L = s_ml[0][1] + s_ml[1][1] + s_ml[2][1] + s_ml[3][1];
-  const bool some = L > 0.f || L != L;
-  if (tid < D / 4) {
-    float v[4];
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+    const bool some = L > 0.f || L != L;
+    const int m = ds.w * kCacheUnitRows + r;
+    if (tid < D / 4) {
+      float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int d = 4 * tid + e;
-      v[e] = s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d];
-      v[e] = some ? v[e] / L : 0.f;
+      for (int e = 0; e < 4; ++e) {
+        const int d = 4 * tid + e;
+        v[e] = s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d];
+        v[e] = some ? v[e] / L : 0.f;
+      }
+      store2(p, o_row(p, ds.y, ds.z, m) + 4 * tid, make_float4(v[0], v[1], v[2], v[3]));
+      if (tid == 0 && p.lse) *lse_row(p, ds.y, ds.z, m) = some ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
     }
-    store2(p, o_row(p, ds.y, ds.z, m) + 4 * tid, make_float4(v[0], v[1], v[2], v[3]));
-    if (tid == 0 && p.lse) *lse_row(p, ds.y, ds.z, m) = some ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
 // Tiles of 64 keys that some head of the group selects, below the length:
 // one CTA per (batch row, K/V head).
-__global__ void __launch_bounds__(256) tiles_kernel(const CacheAttnParams p) {
+__global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ CacheAttnParams p) {
   __shared__ int warp_s[8];
+  next_may_launch();
+  wait_for_previous();
   const int e = blockIdx.x, b = e / p.c.Hkv, h = e % p.c.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int len = len_of(p, b);
@@ -847,8 +862,7 @@ cudaError_t launch_t(const CacheAttnParams& p, int grid, cudaStream_t s) {
   const int smem = AttnCfg<D, NT>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_kernel<D, KIND, NT><<<grid, kAttnThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(attn_kernel<D, KIND, NT>, dim3(grid), dim3(kAttnThreads), smem, s, p);
 }
 template <int D, int KIND>
 cudaError_t launch_k(const CacheAttnParams& p, int grid, cudaStream_t s) {
@@ -859,16 +873,15 @@ cudaError_t launch_d(const CacheAttnParams& p, int grid, cudaStream_t s) {
   cudaError_t e = p.c.kind == BSA_CACHE_INT8 ? launch_k<D, BSA_CACHE_INT8>(p, grid, s)
                                              : launch_k<D, BSA_CACHE_E4M3>(p, grid, s);
   if (e != cudaSuccess) return e;
-  combine_kernel<D><<<dim3(grid, p.rows_cap), 128, 0, s>>>(p);
-  return cudaGetLastError();
+  const int rows = p.rows_cap < kCombineRows ? p.rows_cap : kCombineRows;
+  return launch_after(combine_kernel<D>, dim3(grid, rows), dim3(128), 0, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int grid, cudaStream_t s) {
   if (p.mask) {
-    tiles_kernel<<<p.B * p.c.Hkv, 256, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(tiles_kernel, dim3(p.B * p.c.Hkv), dim3(256), 0, s, p);
     if (e != cudaSuccess) return e;
   }
   return p.c.d == 64 ? launch_d<64>(p, grid, s) : launch_d<128>(p, grid, s);

@@ -20,6 +20,8 @@ constexpr int kThreads = 256;
 template <int KIND>
 __global__ void __launch_bounds__(kThreads) load_kernel(const CacheDev c, const int32_t* seqs, int B, int Nk,
                                                         uint16_t* k_out, uint16_t* v_out, int32_t* lens_out) {
+  next_may_launch();
+  wait_for_previous();
   // Work item: 16 codes of a token.
   const int cols = c.d / 16;
   const long long per = (long long)Nk * cols;              // of one (batch row, head)
@@ -69,9 +71,8 @@ cudaError_t launch_cache_load(const CacheDev& c, const int32_t* seqs, int B, int
   long long gx = (items + 4 * kThreads - 1) / (4 * kThreads);
   if (gx < 1) gx = 1;
   const dim3 grid((unsigned)gx, (unsigned)(B * c.Hkv), 2);
-  if (c.kind == BSA_CACHE_INT8) load_kernel<BSA_CACHE_INT8><<<grid, kThreads, 0, s>>>(c, seqs, B, Nk, k, v, lens);
-  else load_kernel<BSA_CACHE_E4M3><<<grid, kThreads, 0, s>>>(c, seqs, B, Nk, k, v, lens);
-  return cudaGetLastError();
+  return launch_after(c.kind == BSA_CACHE_INT8 ? load_kernel<BSA_CACHE_INT8> : load_kernel<BSA_CACHE_E4M3>, grid,
+                      dim3(kThreads), 0, s, c, seqs, B, Nk, k, v, lens);
 }
 
 }  // namespace bsa

@@ -45,95 +45,136 @@ __device__ __forceinline__ int block_scan(int x, int* warp_s, int& total) {
 
 __device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
 
-// One CTA.  s_need: pages item i takes (-1: skipped); s_page: its partly
-// filled last page where that is shared (else -1), then the offset of its
-// pages in the list of free ones.
+// One CTA.  Everything the decisions need is read once, into shared memory, so
+// that a step of a serving loop (a token more for each sequence, no page more)
+// is a chain of four reads: list, length, last page, its count.
+//   s_seq: the sequence (-1: skipped)  s_have, s_want: lengths
+//   s_page: its partly filled last page where that is shared (else -1); then
+//           whether it takes a page in its place; then where its pages start in
+//           the list of free ones
+constexpr int kItems = kCacheListMax / kThreads;  // consecutive items per thread
+
 __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, const int32_t* seqs,
                                                           const int32_t* new_lens, int n) {
-  __shared__ int s_need[kCacheListMax];
-  __shared__ int s_page[kCacheListMax];
+  next_may_launch();
+  wait_for_previous();
+  extern __shared__ int resize_s[];
+  int* s_seq = resize_s;
+  int* s_have = resize_s + n;
+  int* s_want = resize_s + 2 * n;
+  int* s_page = resize_s + 3 * n;
   __shared__ int warp_s[33];
   __shared__ int s_pairs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = c.max_pages * c.page;
-  int32_t* marks = c.marks();
-  auto seq_of = [&](int i) { return seqs ? __ldg(seqs + i) : i; };
-  auto new_of = [&](int i) { return new_lens ? __ldg(new_lens + i) : 0; };
   if (tid == 0) s_pairs = 0;
-  // A sequence may appear once: the first of its items marks it.
   for (int i = tid; i < n; i += kThreads) {
-    const int s = seq_of(i);
-    if (s >= 0 && s < c.max_seqs) marks[s] = 0x7fffffff;
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
-    const int s = seq_of(i);
-    if (s >= 0 && s < c.max_seqs) atomicMin(marks + s, i);
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
-    const int s = seq_of(i), want = new_of(i);
-    bool ok = s >= 0 && s < c.max_seqs && __ldcg(marks + s) == i && want >= 0 && want <= cap;
-    if (ok) {
-      const int have = __ldcg(c.lens + s);
-      ok = have >= 0 && have <= cap;
-    }
+    const int s = seqs ? __ldg(seqs + i) : i, want = __ldg(new_lens + i);
+    const bool known = s >= 0 && s < c.max_seqs;
+    const int have = known ? __ldcg(c.lens + s) : -1;
+    const bool ok = known && want >= 0 && want <= cap && have >= 0 && have <= cap;
     if (!ok && s != -1) cache_error(c.control, BSA_ERR_INVALID_ARG, i);
-    s_need[i] = ok ? 0 : -1;
+    s_seq[i] = s;
+    s_have[i] = ok ? have : -1;
+    s_want[i] = want;
   }
   __syncthreads();
-  // Releases: a warp per item, a lane per page.
-  for (int i = warp; i < n; i += kThreads / 32) {
-    if (s_need[i] < 0) continue;
-    const int s = seq_of(i);
-    const int hp = pages_of(__ldcg(c.lens + s), c.page), wp = pages_of(new_of(i), c.page);
-    for (int j = wp + lane; j < hp; j += 32) {
-      const int p = __ldcg(c.table + (size_t)s * c.max_pages + j);
-      if (p >= 0 && p < c.num_pages) atomicSub(c.refs + p, 1);
-      else cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s);
+  // A sequence may appear once, its first item counts.
+  if (seqs) {
+    bool twice[kItems];
+    for (int u = 0, i = tid; i < n; i += kThreads, ++u) {
+      twice[u] = false;
+      const int s = s_seq[i];
+      for (int j = 0; j < i; ++j) twice[u] |= s_seq[j] == s;
+      if (s < 0) twice[u] = false;
     }
+    __syncthreads();
+    for (int u = 0, i = tid; i < n; i += kThreads, ++u)
+      if (twice[u]) {
+        cache_error(c.control, BSA_ERR_INVALID_ARG, i);
+        s_have[i] = -1;
+      }
   }
-  __syncthreads();
+  for (int i = tid; i < n; i += kThreads)
+    if (s_have[i] < 0) s_seq[i] = -1;  // (a skipped item's own entry only: no other thread reads it before the barrier)
+  bool shrinks = false;
+  for (int i = tid; i < n; i += kThreads)
+    shrinks |= s_seq[i] >= 0 && pages_of(s_want[i], c.page) < pages_of(s_have[i], c.page);
+  // Releases (`sign` -1; +1 takes them back): eight lanes per item, four pages
+  // per lane and step.
+  auto release = [&](int sign) {
+    const int sub = tid & 7;
+    for (int i = tid >> 3; i < n; i += kThreads / 8) {
+      const int s = s_seq[i];
+      if (s < 0) continue;
+      const int hp = pages_of(s_have[i], c.page), wp = pages_of(s_want[i], c.page);
+      const int32_t* row = c.table + (size_t)s * c.max_pages;
+      for (int j = wp + sub; j < hp; j += 32) {
+        int pg[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) pg[q] = j + 8 * q < hp ? __ldcg(row + j + 8 * q) : -1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (j + 8 * q >= hp) continue;
+          if (pg[q] >= 0 && pg[q] < c.num_pages) atomicAdd(c.refs + pg[q], sign);
+          else cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s);
+        }
+      }
+    }
+  };
+  shrinks = __syncthreads_or(shrinks);
+  if (shrinks) {
+    release(-1);
+    __syncthreads();
+  }
   // Growth into a partly filled last page that others hold too.
+  bool cow = false;
   for (int i = tid; i < n; i += kThreads) {
     int shared_page = -1;
-    if (s_need[i] >= 0) {
-      const int s = seq_of(i), have = __ldcg(c.lens + s);
-      if (new_of(i) > have && have % c.page) {
-        const int p = __ldcg(c.table + (size_t)s * c.max_pages + have / c.page);
-        if (p < 0 || p >= c.num_pages) cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s);
-        else if (__ldcg(c.refs + p) > 1) shared_page = p;
-      }
+    const int s = s_seq[i], have = s_have[i];
+    if (s >= 0 && s_want[i] > have && have % c.page) {
+      const int p = __ldcg(c.table + (size_t)s * c.max_pages + have / c.page);
+      if (p < 0 || p >= c.num_pages) cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s);
+      else if (__ldcg(c.refs + p) > 1) shared_page = p;
     }
     s_page[i] = shared_page;
+    cow |= shared_page >= 0;
   }
-  __syncthreads();
-  int mine[kCacheListMax / kThreads], sum = 0;
-#pragma unroll
-  for (int u = 0; u < kCacheListMax / kThreads; ++u) {  // items tid * 4 + u, in order
-    const int i = tid * (kCacheListMax / kThreads) + u;
-    mine[u] = 0;
-    if (i < n && s_need[i] >= 0) {
-      const int s = seq_of(i), have = __ldcg(c.lens + s);
-      mine[u] = max(0, pages_of(new_of(i), c.page) - pages_of(have, c.page));
+  cow = __syncthreads_or(cow);
+  if (cow) {
+    bool own[kItems];
+    for (int u = 0, i = tid; i < n; i += kThreads, ++u) {
       const int p = s_page[i];
-      if (p >= 0) {
-        int rank = 0;  // earlier items of this call that grow into the same page
-        for (int j = 0; j < i; ++j) rank += s_page[j] == p;
-        if (__ldcg(c.refs + p) - rank > 1) mine[u] |= 1 << 30;  // a page of its own
-      }
+      own[u] = false;
+      if (p < 0) continue;
+      int rank = 0;  // earlier items of this call that grow into the same page
+      for (int j = 0; j < i; ++j) rank += s_page[j] == p;
+      own[u] = __ldcg(c.refs + p) - rank > 1;
     }
-    sum += (mine[u] & 0x3fffffff) + (mine[u] >> 30);
+    __syncthreads();
+    for (int u = 0, i = tid; i < n; i += kThreads, ++u) s_page[i] = own[u] ? 1 : -1;
+    __syncthreads();
+  }
+  // s_page is now 1 for an item that replaces its last page.
+  int mine[kItems], sum = 0;
+#pragma unroll
+  for (int u = 0; u < kItems; ++u) {
+    const int i = tid * kItems + u;
+    mine[u] = 0;
+    if (i < n && s_seq[i] >= 0)
+      mine[u] = max(0, pages_of(s_want[i], c.page) - pages_of(s_have[i], c.page)) + (s_page[i] > 0 ? 1 : 0);
+    sum += mine[u];
   }
   int total;
-  int off = block_scan(sum, warp_s, total);  // (its barriers: every rank is taken)
+  int off = block_scan(sum, warp_s, total);
+  // From here on s_page: where an item's pages start in the list, and in the
+  // sign bit whether the first of them replaces the shared page.
 #pragma unroll
-  for (int u = 0; u < kCacheListMax / kThreads; ++u) {
-    const int i = tid * (kCacheListMax / kThreads) + u;
-    if (i < n && s_need[i] >= 0) {
-      s_need[i] = mine[u];
-      s_page[i] = off;
-      off += (mine[u] & 0x3fffffff) + (mine[u] >> 30);
+  for (int u = 0; u < kItems; ++u) {
+    const int i = tid * kItems + u;
+    if (i < n) {
+      s_page[i] = off | (s_page[i] > 0 ? (int)0x80000000 : 0);
+      off += mine[u];
     }
   }
   // The lowest `total` free pages, in order: 16 pages per thread and step.
@@ -163,15 +204,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
   }
   __syncthreads();
   if (found < total) {  // nothing changes: take the releases back
-    for (int i = warp; i < n; i += kThreads / 32) {
-      if (s_need[i] < 0) continue;
-      const int s = seq_of(i);
-      const int hp = pages_of(__ldcg(c.lens + s), c.page), wp = pages_of(new_of(i), c.page);
-      for (int j = wp + lane; j < hp; j += 32) {
-        const int p = __ldcg(c.table + (size_t)s * c.max_pages + j);
-        if (p >= 0 && p < c.num_pages) atomicAdd(c.refs + p, 1);
-      }
-    }
+    if (shrinks) release(1);
     if (tid == 0) {
       cache_error(c.control, BSA_ERR_WORKSPACE, total - found);
       c.control[kCachePairs] = 0;
@@ -179,14 +212,13 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
     return;
   }
   for (int i = warp; i < n; i += kThreads / 32) {
-    const int need = s_need[i];
-    if (need < 0) continue;
-    const int s = seq_of(i), have = __ldcg(c.lens + s), want = new_of(i);
-    const int hp = pages_of(have, c.page), wp = pages_of(want, c.page);
+    const int s = s_seq[i];
+    if (s < 0) continue;
+    const int want = s_want[i], hp = pages_of(s_have[i], c.page), wp = pages_of(want, c.page);
     int32_t* row = c.table + (size_t)s * c.max_pages;
-    const int32_t* list = c.list_a() + s_page[i];
-    const int own = need >> 30;
-    if (own && lane == 0) {
+    const int32_t* list = c.list_a() + (s_page[i] & 0x7fffffff);
+    const int replaced = s_page[i] < 0 ? 1 : 0;
+    if (replaced && lane == 0) {
       const int old = __ldcg(row + hp - 1), fresh = __ldcg(list);
       const int at = atomicAdd(&s_pairs, 1);
       c.pair_src()[at] = old;
@@ -196,21 +228,50 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
       row[hp - 1] = fresh;
     }
     for (int j = hp + lane; j < wp; j += 32) {
-      const int p = __ldcg(list + own + j - hp);
+      const int p = __ldcg(list + replaced + j - hp);
       c.refs[p] = 1;
       row[j] = p;
     }
     for (int j = wp + lane; j < hp; j += 32) row[j] = -1;
-    __syncwarp();
     if (lane == 0) c.lens[s] = want;
   }
   __syncthreads();
   if (tid == 0) c.control[kCachePairs] = s_pairs;
 }
 
+// Freeing sequences needs no order: one CTA per item, which is skipped if an
+// earlier item names its sequence.
+__global__ void __launch_bounds__(256) free_kernel(const CacheDev c, const int32_t* seqs, int n) {
+  next_may_launch();
+  wait_for_previous();
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const int s = seqs ? __ldg(seqs + i) : i;
+  if (s == -1) return;
+  bool ok = s >= 0 && s < c.max_seqs;
+  if (seqs && ok)
+    for (int j = tid; j < i; j += 256) ok = ok && __ldg(seqs + j) != s;
+  const int len = s >= 0 && s < c.max_seqs ? c.lens[s] : 0;
+  ok = ok && len >= 0 && len <= c.max_pages * c.page;
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0) cache_error(c.control, BSA_ERR_INVALID_ARG, i);
+    return;
+  }
+  const int held = pages_of(len, c.page);
+  int32_t* row = c.table + (size_t)s * c.max_pages;
+  for (int j = tid; j < held; j += 256) {
+    const int p = row[j];
+    if (p >= 0 && p < c.num_pages) atomicSub(c.refs + p, 1);
+    else cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s);
+    row[j] = -1;
+  }
+  if (tid == 0) c.lens[s] = 0;  // (every thread has read it)
+}
+
 // One CTA per pair; each checks its own pair against the whole list.  A length
 // that a pair reads is written by no other one: a source is no destination.
 __global__ void __launch_bounds__(256) fork_kernel(const CacheDev c, const int32_t* src, const int32_t* dst, int n) {
+  next_may_launch();
+  wait_for_previous();
   const int i = blockIdx.x, tid = threadIdx.x;
   const int a = __ldg(src + i), b = __ldg(dst + i);
   if (a == -1 || b == -1) return;
@@ -245,6 +306,8 @@ __global__ void __launch_bounds__(256) fork_kernel(const CacheDev c, const int32
 // L; list_a gets the map of the moved pages (indexed by page), the pairs what
 // the copy kernel moves.
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CacheDev c) {
+  next_may_launch();
+  wait_for_previous();
   __shared__ int warp_s[33];
   const int tid = threadIdx.x;
   int live = 0;
@@ -293,6 +356,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CacheDev c) {
 // earlier pair has and (within one cache) no pair reads.
 __global__ void __launch_bounds__(kThreads) check_pairs_kernel(const CacheDev dst, const CacheDev src, int same,
                                                                const int32_t* dp, const int32_t* sp, int n) {
+  next_may_launch();
+  wait_for_previous();
   __shared__ int s_pairs;
   const int tid = threadIdx.x;
   int32_t* mark = dst.list_a();
@@ -338,6 +403,8 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyBytes = kCopyThreads * 16 * 4;
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CacheDev dst, const CacheDev src, int remap) {
+  next_may_launch();
+  wait_for_previous();
   const int tid = threadIdx.x;
   const int pairs = __ldcg(dst.control + kCachePairs);
   const long long bytes = (long long)dst.Hkv * dst.page * dst.d;  // of a page of K or V: a multiple of 1 KB
@@ -396,34 +463,36 @@ int sm_count() {
 
 cudaError_t launch_cache_resize(const CacheDev& c, const int32_t* seqs, const int32_t* new_lens, int n,
                                 cudaStream_t s) {
-  resize_kernel<<<1, kThreads, 0, s>>>(c, seqs, new_lens, n);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !new_lens) return e;  // freeing copies nothing
-  copy_kernel<<<copy_grid(c, n, sm_count()), kCopyThreads, 0, s>>>(c, c, 0);
-  return cudaGetLastError();
+  if (!new_lens) {
+    return launch_after(free_kernel, dim3(n), dim3(256), 0, s, c, seqs, n);
+  }
+  const int smem = 4 * n * (int)sizeof(int);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024 - 256)
+    e = cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_after(resize_kernel, dim3(1), dim3(kThreads), smem, s, c, seqs, new_lens, n);
+  if (e != cudaSuccess) return e;
+  return launch_after(copy_kernel, dim3(copy_grid(c, n, sm_count())), dim3(kCopyThreads), 0, s, c, c, 0);
 }
 
 cudaError_t launch_cache_fork(const CacheDev& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
-  fork_kernel<<<n, 256, 0, s>>>(c, src, dst, n);
-  return cudaGetLastError();
+  return launch_after(fork_kernel, dim3(n), dim3(256), 0, s, c, src, dst, n);
 }
 
 cudaError_t launch_cache_compact(const CacheDev& c, int sms, cudaStream_t s) {
-  compact_kernel<<<1, kThreads, 0, s>>>(c);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(compact_kernel, dim3(1), dim3(kThreads), 0, s, c);
   if (e != cudaSuccess) return e;
-  copy_kernel<<<copy_grid(c, c.num_pages / 2 + 1, sms), kCopyThreads, 0, s>>>(c, c, 1);
-  return cudaGetLastError();
+  return launch_after(copy_kernel, dim3(copy_grid(c, c.num_pages / 2 + 1, sms)), dim3(kCopyThreads), 0, s, c, c, 1);
 }
 
 cudaError_t launch_cache_copy(const CacheDev& dst, const CacheDev& src, const int32_t* dst_pages,
                               const int32_t* src_pages, int n, cudaStream_t s) {
   const int same = dst.k == src.k ? 1 : 0;
-  check_pairs_kernel<<<1, kThreads, 0, s>>>(dst, src, same, dst_pages, src_pages, n);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_after(check_pairs_kernel, dim3(1), dim3(kThreads), 0, s, dst, src, same, dst_pages, src_pages, n);
   if (e != cudaSuccess) return e;
-  copy_kernel<<<copy_grid(dst, n, sm_count()), kCopyThreads, 0, s>>>(dst, src, 0);
-  return cudaGetLastError();
+  return launch_after(copy_kernel, dim3(copy_grid(dst, n, sm_count())), dim3(kCopyThreads), 0, s, dst, src, 0);
 }
 
 }  // namespace bsa

@@ -494,7 +494,7 @@ bsa_status bsa_attention_host(const uint8_t* mask, int B, int H, int NQB, int NK
  *   block_table  int32 [max_seqs][max_pages], -1 = no page
  *   seq_lens     int32 [max_seqs], tokens held by each sequence
  *   page_refs    int32 [num_pages], sequences that hold each page (0 = free)
- *   control      int32, bsa_cache_control_bytes(num_pages, max_seqs) bytes,
+ *   control      int32, bsa_cache_control_bytes(num_pages) bytes,
  *                first 64 bytes zero before the first call: status words and
  *                scratch of the page operations
  * d in {64, 128}; page_size and scale_block powers of two, 16 <= scale_block
@@ -539,8 +539,8 @@ typedef struct bsa_rows {
   int64_t stride_b, stride_h, stride_t;
 } bsa_rows;
 
-/* Bytes of bsa_cache.control (0 for sizes < 1). */
-size_t bsa_cache_control_bytes(int num_pages, int max_seqs);
+/* Bytes of bsa_cache.control (0 for num_pages < 1). */
+size_t bsa_cache_control_bytes(int num_pages);
 
 /* Make a cache empty: no sequence holds a page, every page is free, the status
  * words are clear.  The pools are not written. */
@@ -566,7 +566,7 @@ bsa_status bsa_cache_status(const bsa_cache* cache, void* stream, int32_t* detai
  * list come last, and the one that is left alone with the page keeps it).
  * New tokens' contents are what bsa_cache_append then stores.  If the free
  * pages do not suffice nothing is changed.  n <= 4096.
- * One kernel (two unless new_lens is NULL), no synchronisation.
+ * Two kernels (one if new_lens is NULL), no synchronisation.
  */
 bsa_status bsa_cache_resize(const bsa_cache* cache, const int32_t* seqs, const int32_t* new_lens,
                             int n, void* stream);

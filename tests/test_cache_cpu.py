@@ -31,9 +31,9 @@ def cache(buf, **kw):
 
 
 def test_control_bytes(lib):
-    assert lib.bsa_cache_control_bytes(8, 4) == 4 * (16 + 3 * 8 + 4)
-    assert lib.bsa_cache_control_bytes(0, 4) == 0 and lib.bsa_cache_control_bytes(8, 0) == 0
-    assert lib.bsa_cache_control_bytes(1 << 30, 4) > 1 << 33
+    assert lib.bsa_cache_control_bytes(8) == 4 * (16 + 3 * 8)
+    assert lib.bsa_cache_control_bytes(0) == 0
+    assert lib.bsa_cache_control_bytes(1 << 30) > 1 << 33
 
 
 @pytest.mark.parametrize("kw,status", [
