@@ -82,8 +82,8 @@ struct CacheAppendParams {
   const int32_t* start;
 };
 
-// Queries per unit of work at most: three row tiles of 16.
-constexpr int kCacheUnitRows = 48;
+// Queries per unit of work at most: three row tiles of 24.
+constexpr int kCacheUnitRows = 72;
 constexpr int kCacheTile = 64;       // keys per tile
 constexpr int kCacheMaxGrid = 320;   // most CTAs of the attention kernel (workspace bound)
 

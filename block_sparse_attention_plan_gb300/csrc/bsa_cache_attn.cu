@@ -18,7 +18,7 @@
 // What bounds it: 2 d bytes per key and K/V head at the memory's rate; an SM's
 // share is 23 bytes per cycle, against which a 64-key tile (16 KB at d = 128)
 // costs about 700 warp instructions, a quarter of what the SM issues meanwhile.
-// Hence mma.sync and not tcgen05: the products are at most 48 rows wide and far
+// Hence mma.sync and not tcgen05: the products are at most 72 rows wide and far
 // from the tensor pipe's limit, and the codes have to pass through registers
 // to be converted anyway.
 //
@@ -49,13 +49,14 @@ using namespace dev;
 // column tiles spill).
 constexpr int kWarps = 3;
 constexpr int kAttnThreads = 32 * (kWarps + 1);
-static_assert(kCacheUnitRows == 16 * kWarps, "a warp for each 16 query rows of a full unit");
+constexpr int kMaxNT = 3;  // 8-row column tiles per warp at most
+static_assert(kCacheUnitRows == 8 * kMaxNT * kWarps, "a warp for each 24 query rows of a full unit");
 constexpr int kScaleLanes = 8;  // producer lanes that copy scales: 4 groups of 16 keys, K and V
 constexpr float kMoveReference = 8.f;  // log2: weights stay <= 2^8
 
 enum CacheSite : int { kSiteTileFull = 0x50, kSiteTileEmpty = 0x51 };
 
-// NT: 8-row column tiles per warp (1 or 2).
+// NT: 8-row column tiles per warp.
 template <int D, int NT>
 struct AttnCfg {
   static constexpr int kTileBytes = kCacheTile * D;  // K or V of a tile
@@ -257,10 +258,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   auto full = [&](int s) { return base + C::kOffBar + 16u * s; };
   auto empty = [&](int s) { return base + C::kOffBar + 16u * s + 8u; };
   const Watchdog wd{s_abort, p.c.control + kCacheStatus, p.c.control + kCacheDetail, p.watchdog_ns};
-  // Warps that share a tile: one for each 16 query rows (row tiles), the others
-  // take other tiles.
+  // Warps that share a tile: each has 8 NT query rows of it (row tiles); with one
+  // row tile every warp takes tiles of its own.
   const int rows_unit = min(p.M, kCacheUnitRows);
   const int R = rows_unit <= 8 * NT ? 1 : kWarps;
+  constexpr int KG = NT * D <= 128 ? 4 : (NT * D < 384 ? 2 : 1);  // groups of 16 keys whose scores are held at once
   if (tid == 0) {
     *s_abort = 0;
     if (base & 1023u) record_failure(wd, BSA_ERR_CUDA, 0);  // the swizzle's layout needs it
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   while (more) {
     const Unit u = unit_of(p, w.e, w.sub);
     const int len = len_of(p, u.b);
-    const int m0 = u.grp * kCacheUnitRows + rt * 16;  // first query row of this warp
+    const int m0 = u.grp * kCacheUnitRows + rt * 8 * NT;  // first query row of this warp
     // Query fragments: lane (g, t4) holds row 8 nt + g, elements 2 DV' of it.
     uint32_t qf[NT][KS][2];
     float qs[NT][2];  // scale of rows 8 nt + 2 t4, + 1
@@ -507,10 +509,35 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     }
     const int first_limit = p.causal ? len - p.nq + 1 : len;  // keys below it are visible to every row
 
+    // With a mask: the number of this warp's next tile and its rows' bytes of
+    // the mask are read a tile ahead.
+    const int lead = (kl - (int)(it % KL) + KL) % KL;  // tiles of the piece before this warp's first
+    int tile_next = 0;
+    uint8_t sel_next[NT][2][2];
+    auto tile_at = [&](int t) { return t < w.t1 ? __ldg(p.list + (size_t)w.e * p.max_tiles + t) : 0; };
+    auto read_mask = [&](int tile) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int kb = (tile * kCacheTile + 32 * hf) / p.bk;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            sel_next[nt][c][hf] =
+                hf > 0 && p.bk > 32 ? sel_next[nt][c][0]
+                                    : (kb < p.NKB ? __ldg(p.mask + ((size_t)u.b * p.Hq + hq_of[nt][c]) * p.NKB + kb) : 0);
+      }
+    };
+    int tile_after = 0;
+    if (p.mask) {
+      tile_next = tile_at(w.t0 + lead);
+      tile_after = tile_at(w.t0 + lead + KL);
+      read_mask(tile_next);
+    }
     for (int t = w.t0; t < w.t1; ++t, ++it) {
       if ((int)(it % KL) != kl || !ok) continue;
       const int s = (int)(it % C::kStages);
-      const int tile = p.mask ? __ldg(p.list + (size_t)w.e * p.max_tiles + t) : t;
+      const int tile = p.mask ? tile_next : t;
       const int key0 = tile * kCacheTile;
       // Selection of the tile's two halves of 32 keys by these rows' heads.
       uint32_t sel = 0xffffffffu;
@@ -519,30 +546,31 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const int kb = (key0 + 32 * hf) / p.bk;
-              if (kb < p.NKB && __ldg(p.mask + ((size_t)u.b * p.Hq + hq_of[nt][x]) * p.NKB + kb))
-                sel |= 1u << ((nt * 2 + x) * 2 + hf);
-            }
+            for (int hf = 0; hf < 2; ++hf) sel |= sel_next[nt][c][hf] ? 1u << ((nt * 2 + c) * 2 + hf) : 0u;
+        tile_next = tile_after;
+        tile_after = tile_at(t + 2 * KL);
+        read_mask(tile_next);
       }
       if (!__all_sync(0xffffffffu, mbar_wait(full(s), (it / C::kStages) & 1u, wd, kSiteTileFull))) {
         ok = false;  // recorded; this row's results are void, the walk goes on so that no barrier is missed
         continue;
       }
       const uint32_t ks = base + s * C::kStageBytes, vs = ks + C::kTileBytes;
+#pragma unroll 1
+      for (int kb16 = 0; kb16 < kCacheTile; kb16 += 16 * KG) {
       // ---- S^T = K Q^T: 16 keys a time
-      float x[4][NT][4];
+      float x[KG][NT][4];
 #pragma unroll
-      for (int kg = 0; kg < 4; ++kg) {
+      for (int kg = 0; kg < KG; ++kg) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[kg][nt][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          const int r0 = 16 * kg + g, r1 = r0 + 8;
+          const int r0 = kb16 + 16 * kg + g, r1 = r0 + 8;
           uint4 a, b;
           if constexpr (D == 128) {
             a = ld_shared_v4(ks + r0 * 128 + (((2 * t4 + i) ^ (r0 & 7)) << 4));
@@ -563,8 +591,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       }
       // ---- scores (log2), masks, reference
 #pragma unroll
-      for (int kg = 0; kg < 4; ++kg) {
-        const float sk = scales[s * 8 + kg];
+      for (int kg = 0; kg < KG; ++kg) {
+        const float sk = scales[s * 8 + kb16 / 16 + kg];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -574,13 +602,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       uint32_t kept = 0xffffffffu;  // bit (kg NT + nt) 4 + e: this thread's score is one that is attended
       if (partial) {
 #pragma unroll
-        for (int kg = 0; kg < 4; ++kg)
+        for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int key = key0 + 16 * kg + g + (e >> 1) * 8;
-              const bool keep = key < lim[nt][e & 1] && ((sel >> ((nt * 2 + (e & 1)) * 2 + (kg >> 1))) & 1u);
+              const int key = key0 + kb16 + 16 * kg + g + (e >> 1) * 8;
+              const bool keep = key < lim[nt][e & 1] && ((sel >> ((nt * 2 + (e & 1)) * 2 + ((kb16 + 16 * kg) >> 5))) & 1u);
               if (!keep) {
                 x[kg][nt][e] = -INFINITY;
                 kept &= ~(1u << ((kg * NT + nt) * 4 + e));
@@ -595,7 +623,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         for (int c = 0; c < 2; ++c) {
           float v = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
 #pragma unroll
-          for (int kg = 1; kg < 4; ++kg) v = fmax3(v, x[kg][nt][c], x[kg][nt][c + 2]);
+          for (int kg = 1; kg < KG; ++kg) v = fmax3(v, x[kg][nt][c], x[kg][nt][c + 2]);
           mx[nt][c] = v;
           move |= v > m_ref[nt][c] + kMoveReference;
         }
@@ -623,13 +651,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         }
       }
       // ---- weights and P^T fragments
-      uint32_t pf[4][NT][2];
+      uint32_t pf[KG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float r0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0];
         const float r1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1];
 #pragma unroll
-        for (int kg = 0; kg < 4; ++kg) {
+        for (int kg = 0; kg < KG; ++kg) {
           const float p0 = ex2_approx(x[kg][nt][0] - r0), p1 = ex2_approx(x[kg][nt][1] - r1);
           const float p2 = ex2_approx(x[kg][nt][2] - r0), p3 = ex2_approx(x[kg][nt][3] - r1);
           l_sum[nt][0] += p0 + p2;
@@ -641,9 +669,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       // ---- O^T += S_v V^T P^T: 16 keys a time (one scale block each)
       const bool tail = key0 + kCacheTile > len;
 #pragma unroll
-      for (int kg = 0; kg < 4; ++kg) {
-        const float sv = scales[s * 8 + 4 + kg];
-        const int ra = 16 * kg + 2 * t4;  // keys 2 t4, + 1, + 8, + 9 of the 16
+      for (int kg = 0; kg < KG; ++kg) {
+        const float sv = scales[s * 8 + 4 + kb16 / 16 + kg];
+        const int ra = kb16 + 16 * kg + 2 * t4;  // keys 2 t4, + 1, + 8, + 9 of the 16
         uint32_t v[4][DV / 4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -686,6 +714,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
           }
         }
       }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(s));
     }
@@ -719,7 +748,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       // A thread per (row, 4 elements).
       for (int i = tid; i < R * 8 * (D / 4); i += 32 * kWarps) {
         const int c4 = i % (D / 4), rr = i / (D / 4) % 8, rtile = i / (D / 4) / 8;
-        const int r = rtile * 16 + 8 * nt + rr;  // row of the unit
+        const int r = rtile * 8 * NT + 8 * nt + rr;  // row of the unit
         if (r >= rows) continue;
         float M = -INFINITY;
         for (int k = 0; k < KL; ++k) M = fmaxf(M, ml[((k * R + rtile) * 8 + rr) * 2]);
@@ -764,7 +793,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
 // Joins the parts of a row that several CTAs worked on, in the CTAs' order.
 // One CTA per (first CTA of the row, query row and every kCombineRows-th after
 // it); its warps take every fourth part each.
-constexpr int kCombineRows = 4;
+constexpr int kCombineRows = 12;
 
 template <int D>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CacheAttnParams p) {
@@ -824,8 +853,11 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Ca
 
 // Tiles of 64 keys that some head of the group selects, below the length:
 // one CTA per (batch row, K/V head).
-__global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ CacheAttnParams p) {
-  __shared__ int warp_s[8];
+constexpr int kTilesThreads = 1024;
+static_assert(kTilesThreads / 32 == 32, "a lane per warp");
+
+__global__ void __launch_bounds__(kTilesThreads) tiles_kernel(const __grid_constant__ CacheAttnParams p) {
+  __shared__ int warp_s[kTilesThreads / 32];
   next_may_launch();
   wait_for_previous();
   const int e = blockIdx.x, b = e / p.c.Hkv, h = e % p.c.Hkv;
@@ -835,23 +867,27 @@ __global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ Cach
   const uint8_t* mrow = p.mask + ((size_t)b * p.Hq + (size_t)h * p.g) * p.NKB;
   int32_t* out = p.list + (size_t)e * p.max_tiles;
   int done = 0;
-  for (int base = 0; base < tiles; base += 256) {
+  for (int base = 0; base < tiles; base += kTilesThreads) {
     const int t = base + tid;
-    bool on = false;
+    unsigned on = 0u;
     if (t < tiles) {
-      const int k0 = t * kCacheTile / p.bk, k1 = min((t * kCacheTile + kCacheTile - 1) / p.bk, p.NKB - 1);
-      for (int i = 0; i < p.g && !on; ++i)
-        for (int k = k0; k <= k1; ++k) on |= __ldg(mrow + (size_t)i * p.NKB + k) != 0;
+      const int k0 = t * kCacheTile / p.bk, k1 = p.bk == 32 ? min(k0 + 1, p.NKB - 1) : k0;
+#pragma unroll 8
+      for (int i = 0; i < p.g; ++i) on |= __ldg(mrow + (size_t)i * p.NKB + k0) | __ldg(mrow + (size_t)i * p.NKB + k1);
     }
-    const unsigned bal = __ballot_sync(0xffffffffu, on);
+    const unsigned bal = __ballot_sync(0xffffffffu, on != 0u);
     if (lane == 0) warp_s[warp] = __popc(bal);
     __syncthreads();
-    int before = done;
-    for (int k = 0; k < 8; ++k) {
-      if (k < warp) before += warp_s[k];
-      done += warp_s[k];
+    // A lane per warp: the tiles of the warps below this one, and of all.
+    const int cnt = warp_s[lane];
+    int below = lane < warp ? cnt : 0, all = cnt;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      below += __shfl_xor_sync(0xffffffffu, below, o);
+      all += __shfl_xor_sync(0xffffffffu, all, o);
     }
-    if (on) out[before + __popc(bal & ((1u << lane) - 1u))] = t;
+    if (on) out[done + below + __popc(bal & ((1u << lane) - 1u))] = t;
+    done += all;
     __syncthreads();
   }
   if (tid == 0) p.counts[e] = done;
@@ -866,7 +902,12 @@ cudaError_t launch_t(const CacheAttnParams& p, int grid, cudaStream_t s) {
 }
 template <int D, int KIND>
 cudaError_t launch_k(const CacheAttnParams& p, int grid, cudaStream_t s) {
-  return p.M <= 8 ? launch_t<D, KIND, 1>(p, grid, s) : launch_t<D, KIND, 2>(p, grid, s);
+  // Up to 24 rows: each warp has all of them and tiles of its own, so that a code
+  // is converted once.  Beyond, the three warps share each tile (and convert it
+  // three times, which is still less than a second pass over the cache).
+  const int rows = p.M < kCacheUnitRows ? p.M : kCacheUnitRows;
+  const int nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 24 ? 3 : (rows <= 48 ? 2 : 3)));
+  return nt == 1 ? launch_t<D, KIND, 1>(p, grid, s) : (nt == 2 ? launch_t<D, KIND, 2>(p, grid, s) : launch_t<D, KIND, 3>(p, grid, s));
 }
 template <int D>
 cudaError_t launch_d(const CacheAttnParams& p, int grid, cudaStream_t s) {
@@ -881,7 +922,7 @@ cudaError_t launch_d(const CacheAttnParams& p, int grid, cudaStream_t s) {
 
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int grid, cudaStream_t s) {
   if (p.mask) {
-    const cudaError_t e = launch_after(tiles_kernel, dim3(p.B * p.c.Hkv), dim3(256), 0, s, p);
+    const cudaError_t e = launch_after(tiles_kernel, dim3(p.B * p.c.Hkv), dim3(kTilesThreads), 0, s, p);
     if (e != cudaSuccess) return e;
   }
   return p.c.d == 64 ? launch_d<64>(p, grid, s) : launch_d<128>(p, grid, s);
