@@ -172,16 +172,16 @@ namespace bsa {
 bsa_status check_device(int* dev_out) { return check_arch(dev_out); }
 long long watchdog_limit_ns() { return env_ll("BSA_WATCHDOG_MS", 1000) * 1000000ll; }
 
-bool encode_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int box_rows) {
+bool encode_lines_map(CUtensorMap* m, const void* base, uint64_t lines, int box_lines) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)d};
-  cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)box_rows};
+  cuuint64_t dims[2] = {128u, (cuuint64_t)lines};
+  cuuint64_t strides[1] = {128u};
+  cuuint32_t box[2] = {128u, (cuuint32_t)box_lines};
   cuuint32_t estr[2] = {1u, 1u};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Forward parameters of one plan (layout L, device views pd, workspace ws)

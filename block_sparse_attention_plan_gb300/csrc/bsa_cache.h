@@ -82,13 +82,14 @@ struct CacheAppendParams {
   const int32_t* start;
 };
 
-// Queries per unit of work at most: three row tiles of 24.
-constexpr int kCacheUnitRows = 72;
-constexpr int kCacheTile = 64;       // keys per tile
+// Queries per unit of work at most: four row tiles of 24.
+constexpr int kCacheUnitRows = 96;
+// Keys per tile: 4 KB of K and of V.
+constexpr int cache_tile_keys(int d) { return 4096 / d; }
 constexpr int kCacheMaxGrid = 320;   // most CTAs of the attention kernel (workspace bound)
 
 struct CacheAttnParams {
-  CUtensorMap tmK, tmV;  // pools as [num_pages*Hkv*page][d] bytes, box {d, min(page, 64)}
+  CUtensorMap tmK, tmV;  // pools as lines of 128 bytes (128 / d tokens), box: min(page, tile) tokens
   CacheDev c;
   CacheRows q;
   uint16_t* o;
@@ -100,7 +101,7 @@ struct CacheAttnParams {
   int32_t* counts;      // how many [B*Hkv]
   float* part;          // partial O and (m, l): see bsa_cache_attn.cu
   int32_t* desc;        // rows split over CTAs, for the combine kernel [grid][4]
-  int fp16, B, Hq, g, nq, M, groups, NKB, bk, max_tiles, causal;
+  int fp16, B, Hq, g, nq, M, groups, NKB, bk, tile, max_tiles, causal;
   int rows_cap;         // query rows of a partial's slot
   float scale_log2;
   long long watchdog_ns;

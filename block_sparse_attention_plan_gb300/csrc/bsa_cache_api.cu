@@ -72,11 +72,12 @@ struct AttnLayout {
 bsa_status attn_layout(const CacheDev& c, int B, int Hq, int nq, int NKB, int bk, bool masked, AttnLayout* out) {
   if (B < 1 || Hq < 1 || nq < 1 || Hq % c.Hkv) return BSA_ERR_INVALID_ARG;
   const long long M = (long long)(Hq / c.Hkv) * nq;
-  long long tiles = ((long long)c.max_pages * c.page + kCacheTile - 1) / kCacheTile;
+  const int tile = cache_tile_keys(c.d);
+  long long tiles = ((long long)c.max_pages * c.page + tile - 1) / tile;
   if (masked) {
     if (bk != 32 && bk != 64 && bk != 128 && bk != 256) return BSA_ERR_UNSUPPORTED;
     if (NKB < 1) return BSA_ERR_INVALID_ARG;
-    const long long mt = ((long long)NKB * bk + kCacheTile - 1) / kCacheTile;
+    const long long mt = ((long long)NKB * bk + tile - 1) / tile;
     if (mt < tiles) tiles = mt;
   }
   const long long groups = (M + kCacheUnitRows - 1) / kCacheUnitRows;
@@ -224,9 +225,11 @@ bsa_status bsa_cache_attention(const bsa_cache* cache, const bsa_rows* q, const 
   if (workspace_bytes < l.bytes) return BSA_ERR_WORKSPACE;
   int dev = 0, sms = 0;
   if ((st = check_device(&dev)) != BSA_OK || (st = sms_of(dev, &sms)) != BSA_OK) return st;
-  const uint64_t pool_rows = (uint64_t)p.c.num_pages * p.c.Hkv * p.c.page;
-  const int box = p.c.page < kCacheTile ? p.c.page : kCacheTile;
-  if (!encode_bytes_map(&p.tmK, p.c.k, pool_rows, p.c.d, box) || !encode_bytes_map(&p.tmV, p.c.v, pool_rows, p.c.d, box))
+  const int tokens = 128 / p.c.d;  // of a line
+  const uint64_t lines = (uint64_t)p.c.num_pages * p.c.Hkv * p.c.page / tokens;
+  p.tile = cache_tile_keys(p.c.d);
+  const int box = (p.c.page < p.tile ? p.c.page : p.tile) / tokens;
+  if (!encode_lines_map(&p.tmK, p.c.k, lines, box) || !encode_lines_map(&p.tmV, p.c.v, lines, box))
     return BSA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = rows_of(q);

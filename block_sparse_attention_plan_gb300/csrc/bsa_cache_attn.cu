@@ -16,13 +16,13 @@
 // rescaled), so fp16 weights keep 11 bits.
 //
 // What bounds it: 2 d bytes per key and K/V head at the memory's rate; an SM's
-// share is 23 bytes per cycle, against which a 64-key tile (16 KB at d = 128)
-// costs about 700 warp instructions, a quarter of what the SM issues meanwhile.
-// Hence mma.sync and not tcgen05: the products are at most 72 rows wide and far
+// share is 23 bytes per cycle, against which a tile of 8 KB costs 250 to 800 warp
+// instructions (8 to 24 rows) of the 1400 that the SM can issue meanwhile.
+// Hence mma.sync and not tcgen05: the products are at most 96 rows wide and far
 // from the tensor pipe's limit, and the codes have to pass through registers
 // to be converted anyway.
 //
-// Work split: the 64-key tiles of all (sequence, K/V head) pairs form one line
+// Work split: the tiles (8 KB: 32 keys at d = 128, 64 at d = 64) of all (sequence, K/V head) pairs form one line
 // which the CTAs cut into equal pieces, so that ragged lengths and few long
 // sequences both fill the machine.  A row whose tiles lie in several CTAs
 // leaves partial sums in the workspace; the combine kernel joins them in the
@@ -32,9 +32,12 @@
 // busy with the others' tiles at the end of every CTA: 193 us against 183 us
 // for 32 sequences of up to 32768 tokens.)  Inside a CTA the tiles
 // go round the warps, each with its own sums, joined when the piece of a row
-// ends.  One warp feeds a ring of tiles by TMA (each page's rows of a head are
-// one box, 128-byte swizzled so that both products read without conflicts)
-// and the tiles' scales by 4-byte asynchronous copies.
+// ends.  Each warp feeds itself: a ring of tiles of its own, filled by TMA (a
+// page's rows of a head are one box; the copy engine takes a line of the box at
+// a time whatever its length, so at d = 64 a line is two tokens; 128-byte
+// swizzled so that the products read with few conflicts), the next tile requested as soon as one is used up.
+// (A warp that feeds all others issues a tile every 700 cycles, too slow for
+// tiles of 8 KB, and tiles of 16 KB leave room for six warps' rings at most.)
 #include "bsa_cache.h"
 #include "bsa_cache_codes.cuh"
 #include "bsa_device.cuh"
@@ -44,53 +47,43 @@ namespace {
 
 using namespace dev;
 
-// Three consumer warps and a producer: eight warps on an SM with two CTAs, so
-// that each may hold 255 registers (with five warps per CTA it is 168, and two
-// column tiles spill).
-constexpr int kWarps = 3;
-constexpr int kAttnThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 4;
+constexpr int kAttnThreads = 32 * kWarps;
 constexpr int kMaxNT = 3;  // 8-row column tiles per warp at most
-static_assert(kCacheUnitRows == 8 * kMaxNT * kWarps, "a warp for each 24 query rows of a full unit");
-constexpr int kScaleLanes = 8;  // producer lanes that copy scales: 4 groups of 16 keys, K and V
+static_assert(kCacheUnitRows == 8 * kMaxNT * kWarps, "24 query rows for each warp of a full unit");
 constexpr float kMoveReference = 8.f;  // log2: weights stay <= 2^8
 
-enum CacheSite : int { kSiteTileFull = 0x50, kSiteTileEmpty = 0x51 };
+enum CacheSite : int { kSiteTileFull = 0x50 };
 
-// NT: 8-row column tiles per warp.
-template <int D, int NT>
+template <int D>
 struct AttnCfg {
-  static constexpr int kTileBytes = kCacheTile * D;  // K or V of a tile
+  static constexpr int TK = cache_tile_keys(D);      // keys of a tile
+  static constexpr int kGroups = TK / 16;            // keys of one matrix instruction, one scale each for K and V
+  static constexpr int kTileBytes = TK * D;          // K or V of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = 3;                  // per warp
   static constexpr int kMergeBytes = kWarps * 8 * D * 4;  // 8 rows a warp at a time (the tile counts' prefix uses it first)
-  static constexpr int kMlBytes = kWarps * 8 * 8;
-  static constexpr int kBudget = 113 * 1024;  // two CTAs per SM
-  // A multiple of the consumer warps: a stage is used by the same warps every
-  // time.  (A warp that met a stage another one had used before could be a
-  // whole phase ahead of its barrier, where the parity of a wait is ambiguous.)
-  static constexpr int kStages = (kBudget - kMergeBytes - kMlBytes - 16) / (kStageBytes + 48) / kWarps * kWarps;
-  static constexpr int kOffMerge = kStages * kStageBytes;
-  static constexpr int kOffMl = kOffMerge + kMergeBytes;        // float [warps][8][2]
-  static constexpr int kOffScale = kOffMl + kMlBytes;           // float [stages][8]
-  static constexpr int kOffBar = kOffScale + kStages * 32;      // full, empty [stages]
-  static constexpr int kOffAbort = kOffBar + kStages * 16;
+  static constexpr int kOffMerge = kWarps * kStages * kStageBytes;
+  static constexpr int kOffMl = kOffMerge + kMergeBytes;      // float [warps][8][2]
+  static constexpr int kOffBar = kOffMl + kWarps * 8 * 8;     // full [warps][stages]
+  static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
   static constexpr int kSmem = kOffAbort + 16;
-  static_assert(kStages % kWarps == 0 && kStages > 0 && kSmem <= kBudget && kMergeBytes >= 8 * (kAttnThreads + 1), "shared memory");
+  static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
+  static_assert(kMergeBytes >= 8 * (kAttnThreads + 1), "prefix");
 };
-
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// Arrive on `bar` when this thread's copies so far have landed (the arrival is
-// one of those the barrier was initialised for).
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with an accumulator that starts at zero.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
@@ -101,6 +94,11 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   uint2 r;
@@ -124,7 +122,7 @@ __device__ __forceinline__ int len_of(const CacheAttnParams& p, int b) {
 // its heads and for the groups of kCacheUnitRows query rows.
 __device__ __forceinline__ int entry_tiles(const CacheAttnParams& p, int e) {
   if (p.mask) return __ldg(p.counts + e);
-  return (len_of(p, e) + kCacheTile - 1) / kCacheTile;
+  return (len_of(p, e) + p.tile - 1) / p.tile;
 }
 
 // Walks the pieces of rows in tiles [lo, hi) of the line.
@@ -234,9 +232,9 @@ __device__ __forceinline__ void take_nans(uint32_t (&v)[4][DV / 4], float (&o)[N
     const uint2 cd1 = codes_to_half4<BSA_CACHE_E4M3>(__byte_perm(ind[2], ind[3], 0x7362));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float y[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
-      mma16816(y, ab0.x, ab0.y, cd0.x, cd0.y, kf[nt][0], kf[nt][1]);
-      mma16816(z, ab1.x, ab1.y, cd1.x, cd1.y, kf[nt][0], kf[nt][1]);
+      float y[4], z[4];
+      mma16816_first(y, ab0.x, ab0.y, cd0.x, cd0.y, kf[nt][0], kf[nt][1]);
+      mma16816_first(z, ab1.x, ab1.y, cd1.x, cd1.y, kf[nt][0], kf[nt][1]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (y[e] > 0.f) o[nt][2 * q][e] = __uint_as_float(0x7fffffffu);
@@ -246,30 +244,41 @@ __device__ __forceinline__ void take_nans(uint32_t (&v)[4][DV / 4], float (&o)[N
   }
 }
 
+// A warp's requests for tiles: where it is in the line, and for the next (up to)
+// 32 tiles of the piece a lane each with the tile's number and the pool row of
+// each of its boxes (-1: no token in it).
+struct Feed {
+  Walk w;
+  int pos, n, i;    // first tile of the batch (within the unit), its size, the next one to request
+  int tile, pr[4];  // this lane's tile
+  int len;          // of the piece's sequence
+  bool more;
+};
+
 template <int D, int KIND, int NT>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_constant__ CacheAttnParams p) {
-  using C = AttnCfg<D, NT>;
+  using C = AttnCfg<D>;
+  constexpr int TK = C::TK;
+  constexpr int KG = NT * D >= 384 ? 1 : 2;  // groups of 16 keys whose scores are held at once
   extern __shared__ __align__(1024) uint8_t smem[];
   long long* s_prefix = reinterpret_cast<long long*>(smem + C::kOffMerge);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x;
   const uint32_t base = smem_u32(smem);
-  auto full = [&](int s) { return base + C::kOffBar + 16u * s; };
-  auto empty = [&](int s) { return base + C::kOffBar + 16u * s + 8u; };
+  const uint32_t bars = base + C::kOffBar + warp * C::kStages * 8;  // this warp's
+  const uint32_t ring = base + warp * C::kStages * C::kStageBytes;
   const Watchdog wd{s_abort, p.c.control + kCacheStatus, p.c.control + kCacheDetail, p.watchdog_ns};
-  // Warps that share a tile: each has 8 NT query rows of it (row tiles); with one
-  // row tile every warp takes tiles of its own.
+  // Row tiles of 8 NT query rows: a warp each.  Warps of the same row tile take
+  // tiles in turn (KL of them); those of other row tiles read the same tiles
+  // again, from L2.
   const int rows_unit = min(p.M, kCacheUnitRows);
-  const int R = rows_unit <= 8 * NT ? 1 : kWarps;
-  constexpr int KG = NT * D <= 128 ? 4 : (NT * D < 384 ? 2 : 1);  // groups of 16 keys whose scores are held at once
+  const int R = rows_unit <= 8 * NT ? 1 : (rows_unit <= 16 * NT ? 2 : 4);
+  const int KL = kWarps / R, rt = warp % R, kl = warp / R;
   if (tid == 0) {
     *s_abort = 0;
     if (base & 1023u) record_failure(wd, BSA_ERR_CUDA, 0);  // the swizzle's layout needs it
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full(s), 1 + kScaleLanes);
-      mbar_init(empty(s), (uint32_t)R);
-    }
+    for (int s = 0; s < kWarps * C::kStages; ++s) mbar_init(base + C::kOffBar + 8 * s, 1);
     fence_barrier_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&p.tmK);
@@ -306,7 +315,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   // A tile at least for each set of warps that shares one, so that short lines
   // leave few parts to join.  No CTA that works has an empty piece: the parts of
   // a row are those of consecutive CTAs.
-  const int KL = kWarps / R;
   const long long most = (T + KL - 1) / KL;
   const int G = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x);
   const long long lo = cta < G ? cta * T / G : 0, hi = cta < G ? (cta + 1) * T / G : 0;
@@ -338,106 +346,111 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   walk_start(p, w, mult, a * per, s_prefix[a], lo, hi);
   __syncthreads();  // the prefix gives way to the merge buffer
 
+  // ---------------------------------------------------------------- requests
   const int lpage = 31 - __clz(p.c.page), lsb = 31 - __clz(p.c.sb);
-  if (warp == kWarps) {
-    // ------------------------------------------------------------- producer
-    const int cs = min(p.c.page, kCacheTile);  // keys per box
-    const int lcs = 31 - __clz(cs), nc = kCacheTile >> lcs;
-    const uint64_t pol = policy_evict_first();
-    uint32_t it = 0;
-    bool ok = true;
-    do {
-      const Unit u = unit_of(p, w.e, w.sub);
-      const int seq = seq_of(p, u.b), len = len_of(p, u.b);
-      const int32_t* row = p.c.table + (size_t)seq * p.c.max_pages;
-      for (int t = w.t0; t < w.t1 && ok; t += 32) {
-        // A lane per tile: its number, and the pool row of each of its boxes
-        // (-1: no token in it).
-        int tile = 0, pr[4] = {-1, -1, -1, -1};
-        if (t + lane < w.t1) {
-          tile = p.mask ? __ldg(p.list + (size_t)w.e * p.max_tiles + t + lane) : t + lane;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int key = tile * kCacheTile + (j << lcs);
-            if (j < nc && key < len) {
-              int ph = __ldg(row + (key >> lpage));
-              if (ph < 0 || ph >= p.c.num_pages) {
-                cache_error(p.c.control, BSA_ERR_PLAN_MISMATCH, seq);
-                ph = 0;  // (some page, so that the row ends like any other)
-              }
-              pr[j] = (ph * p.c.Hkv + u.h) * p.c.page + (key & (p.c.page - 1));
-            }
-          }
-        }
-        const int n = min(32, w.t1 - t);
-        for (int i = 0; i < n; ++i, ++it) {
-          const int s = (int)(it % C::kStages);
-          const uint32_t use = it / C::kStages;
-          if (use > 0) {
-            const bool got = mbar_wait(empty(s), (use - 1) & 1u, wd, kSiteTileEmpty);
-            if (!__all_sync(0xffffffffu, got)) {
-              ok = false;
-              break;
-            }
-          }
-          int box[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) box[j] = __shfl_sync(0xffffffffu, pr[j], i);
-          const int tl = __shfl_sync(0xffffffffu, tile, i);
-          if (lane == 0) {
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) bytes += box[j] >= 0 ? 2u * cs * D : 0u;
-            mbar_arrive_expect_tx(full(s), bytes);
-          }
-          __syncwarp();
-          const int j = lane & 3;
-          const int mybox = j == 0 ? box[0] : (j == 1 ? box[1] : (j == 2 ? box[2] : box[3]));
-          if (lane < 8 && mybox >= 0)
-            tma_load_2d(base + s * C::kStageBytes + (lane >> 2) * C::kTileBytes + j * cs * D,
-                        lane < 4 ? &p.tmK : &p.tmV, 0, mybox, full(s), pol);
-          // Scale of keys 16 j .. of the tile: box (16 j) / cs, its pool row
-          // further by the rest; 0 where the keys lie past the length.
-          const int jb = (16 * j) >> lcs;
-          const int sbox = jb == 0 ? box[0] : (jb == 1 ? box[1] : (jb == 2 ? box[2] : box[3]));
-          if (lane >= 8 && lane < 8 + kScaleLanes) {
-            const bool isv = lane >= 12;
-            const bool live = tl * kCacheTile + 16 * j < len;
-            const size_t at = live ? (size_t)((unsigned)(sbox + ((16 * j) & (cs - 1)))) >> lsb : 0;
-            cp_async4(base + C::kOffScale + s * 32 + (lane - 8) * 4, (isv ? p.c.vs : p.c.ks) + at, live ? 4u : 0u);
-            cp_async_arrive(full(s));
-          }
-        }
-        __syncwarp();
+  const int cs = min(p.c.page, TK);  // keys per box
+  const int lcs = 31 - __clz(cs), nc = TK >> lcs;
+  // Read once, unless other row tiles or groups of rows come back for it.
+  const uint64_t pol = R == 1 && p.groups == 1 ? policy_evict_first() : policy_evict_normal();
+  // First tile of a piece that is this warp's: tile t of the CTA's line is taken
+  // by the warps with kl = t mod KL.
+  auto first_of = [&](const Walk& x) { return x.t0 + (int)((kl + KL - (int)((x.at - lo) % KL)) % KL); };
+  Feed f;
+  f.w = w;
+  f.pos = first_of(w);
+  f.n = f.i = 0;
+  f.more = true;
+  f.len = 0;
+  f.tile = 0;
+  // The batch at f.pos (of the next piece that has a tile for this warp).
+  auto refill = [&]() {
+    f.pos += f.n * KL;
+    while (f.pos >= f.w.t1) {
+      if (!walk_next(p, f.w, mult)) {
+        f.more = false;
+        return;
       }
-    } while (ok && walk_next(p, w, mult));
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok && lane == 0) {
-      // Let the copies in flight land before the CTA's shared memory goes away.
-      volatile int no_abort = 0;
-      const Watchdog quick{&no_abort, wd.status, wd.detail, 100000000ll};
-      for (uint32_t k = it < (uint32_t)C::kStages ? 0 : it - C::kStages; k < it; ++k)
-        mbar_wait(full((int)(k % C::kStages)), (k / C::kStages) & 1u, quick, kSiteTileFull);
+      f.pos = first_of(f.w);
     }
-    return;
-  }
+    const Unit u = unit_of(p, f.w.e, f.w.sub);
+    const int seq = seq_of(p, u.b);
+    f.len = len_of(p, u.b);
+    f.n = min(32, (f.w.t1 - f.pos + KL - 1) / KL);
+    f.i = 0;
+    const int32_t* row = p.c.table + (size_t)seq * p.c.max_pages;
+    f.tile = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.pr[j] = -1;
+    if (lane < f.n) {
+      const int t = f.pos + lane * KL;
+      f.tile = p.mask ? __ldg(p.list + (size_t)f.w.e * p.max_tiles + t) : t;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = f.tile * TK + (j << lcs);
+        if (j < nc && key < f.len) {
+          int ph = __ldg(row + (key >> lpage));
+          if (ph < 0 || ph >= p.c.num_pages) {
+            cache_error(p.c.control, BSA_ERR_PLAN_MISMATCH, seq);
+            ph = 0;  // (some page, so that the row ends like any other)
+          }
+          f.pr[j] = (ph * p.c.Hkv + u.h) * p.c.page + (key & (p.c.page - 1));
+        }
+      }
+    }
+  };
+  // Request the warp's next tile into stage s.  Returns its number (-1: there is
+  // none); `scale` gets this lane's scale of it: lanes 0 .. kGroups - 1 K's of 16
+  // keys each, the next kGroups V's (0 where the keys lie past the length).
+  auto request = [&](int s, float& scale) -> int {
+    scale = 0.f;
+    if (f.more && f.i == f.n) refill();
+    if (!f.more) return -1;
+    int box[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) box[j] = __shfl_sync(0xffffffffu, f.pr[j], f.i);
+    const int tile = __shfl_sync(0xffffffffu, f.tile, f.i);
+    ++f.i;
+    if (lane == 0) {
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bytes += box[j] >= 0 ? 2u * cs * D : 0u;
+      mbar_arrive_expect_tx(bars + 8 * s, bytes);
+    }
+    __syncwarp();
+    const int j = lane & 3;
+    const int mybox = j == 0 ? box[0] : (j == 1 ? box[1] : (j == 2 ? box[2] : box[3]));
+    if (lane < 8 && mybox >= 0)
+      tma_load_2d(ring + s * C::kStageBytes + (lane >> 2) * C::kTileBytes + j * cs * D, lane < 4 ? &p.tmK : &p.tmV, 0,
+                  mybox / (128 / D), bars + 8 * s, pol);
+    if (lane < 2 * C::kGroups) {
+      const int gr = lane % C::kGroups, jb = (16 * gr) >> lcs;
+      const int sbox = jb == 0 ? box[0] : (jb == 1 ? box[1] : (jb == 2 ? box[2] : box[3]));
+      if (tile * TK + 16 * gr < f.len)
+        scale = __ldg((lane < C::kGroups ? p.c.ks : p.c.vs) + ((size_t)(unsigned)(sbox + ((16 * gr) & (cs - 1))) >> lsb));
+    }
+    return tile;
+  };
+  // Tiles and scales of the stages, the one to be used next first.
+  int tq[C::kStages];
+  float sq[C::kStages];
+#pragma unroll
+  for (int s = 0; s < C::kStages; ++s) tq[s] = request(s, sq[s]);
+  int stage = 0;
+  uint32_t phase = 0;
 
-  // --------------------------------------------------------------- consumers
+  // ------------------------------------------------------------- computation
   const int g = lane >> 2, t4 = lane & 3;
-  const int rt = warp % R, kl = warp / R;
   constexpr int KS = D / 16;    // 16-element steps of q . k
   constexpr int MT = D / 16;    // 16-row tiles of O^T
   constexpr int DV = D / 8;     // consecutive elements of O a thread holds
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* ml = reinterpret_cast<float*>(smem + C::kOffMl);
-  const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale);
-  uint32_t it = 0;
   bool more = true, ok = true;
   while (more) {
     const Unit u = unit_of(p, w.e, w.sub);
     const int len = len_of(p, u.b);
     const int m0 = u.grp * kCacheUnitRows + rt * 8 * NT;  // first query row of this warp
-    // Query fragments: lane (g, t4) holds row 8 nt + g, elements 2 DV' of it.
+    // Query fragments: lane (g, t4) holds row 8 nt + g, elements 4 a word of codes.
     uint32_t qf[NT][KS][2];
     float qs[NT][2];  // scale of rows 8 nt + 2 t4, + 1
     int lim[NT][2];   // keys below it are visible to them
@@ -509,37 +522,26 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     }
     const int first_limit = p.causal ? len - p.nq + 1 : len;  // keys below it are visible to every row
 
-    // With a mask: the number of this warp's next tile and its rows' bytes of
-    // the mask are read a tile ahead.
-    const int lead = (kl - (int)(it % KL) + KL) % KL;  // tiles of the piece before this warp's first
-    int tile_next = 0;
+    // With a mask: this warp's rows' bytes of it are read a tile ahead.
     uint8_t sel_next[NT][2][2];
-    auto tile_at = [&](int t) { return t < w.t1 ? __ldg(p.list + (size_t)w.e * p.max_tiles + t) : 0; };
     auto read_mask = [&](int tile) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int kb = (tile * kCacheTile + 32 * hf) / p.bk;
+        const int kb = (tile * TK + 32 * hf) / p.bk;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c)
             sel_next[nt][c][hf] =
-                hf > 0 && p.bk > 32 ? sel_next[nt][c][0]
+                hf > 0 && (p.bk > 32 || TK <= 32) ? sel_next[nt][c][0]
                                     : (kb < p.NKB ? __ldg(p.mask + ((size_t)u.b * p.Hq + hq_of[nt][c]) * p.NKB + kb) : 0);
       }
     };
-    int tile_after = 0;
-    if (p.mask) {
-      tile_next = tile_at(w.t0 + lead);
-      tile_after = tile_at(w.t0 + lead + KL);
-      read_mask(tile_next);
-    }
-    for (int t = w.t0; t < w.t1; ++t, ++it) {
-      if ((int)(it % KL) != kl || !ok) continue;
-      const int s = (int)(it % C::kStages);
-      const int tile = p.mask ? tile_next : t;
-      const int key0 = tile * kCacheTile;
-      // Selection of the tile's two halves of 32 keys by these rows' heads.
+    int t = first_of(w);
+    if (p.mask && t < w.t1) read_mask(tq[0]);
+    for (; t < w.t1 && ok; t += KL) {
+      const int key0 = tq[0] * TK;
+      // Selection of the tile's halves of 32 keys by these rows' heads.
       uint32_t sel = 0xffffffffu;
       if (p.mask) {
         sel = 0u;
@@ -549,174 +551,201 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) sel |= sel_next[nt][c][hf] ? 1u << ((nt * 2 + c) * 2 + hf) : 0u;
-        tile_next = tile_after;
-        tile_after = tile_at(t + 2 * KL);
-        read_mask(tile_next);
+        if (t + KL < w.t1) read_mask(tq[1]);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(full(s), (it / C::kStages) & 1u, wd, kSiteTileFull))) {
-        ok = false;  // recorded; this row's results are void, the walk goes on so that no barrier is missed
-        continue;
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, phase, wd, kSiteTileFull))) {
+        ok = false;  // recorded; these rows' results are void, the walk goes on so that no barrier is missed
+        break;
       }
-      const uint32_t ks = base + s * C::kStageBytes, vs = ks + C::kTileBytes;
+      const uint32_t ks = ring + stage * C::kStageBytes, vs = ks + C::kTileBytes;
+      const bool partial = key0 + TK > first_limit || p.mask != nullptr;
+      const bool tail = key0 + TK > len;
 #pragma unroll 1
-      for (int kb16 = 0; kb16 < kCacheTile; kb16 += 16 * KG) {
-      // ---- S^T = K Q^T: 16 keys a time
-      float x[KG][NT][4];
-#pragma unroll
-      for (int kg = 0; kg < KG; ++kg) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[kg][nt][e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const int r0 = kb16 + 16 * kg + g, r1 = r0 + 8;
-          uint4 a, b;
-          if constexpr (D == 128) {
-            a = ld_shared_v4(ks + r0 * 128 + (((2 * t4 + i) ^ (r0 & 7)) << 4));
-            b = ld_shared_v4(ks + r1 * 128 + (((2 * t4 + i) ^ (r1 & 7)) << 4));
-          } else {
-            a = ld_shared_v4(ks + r0 * 64 + ((t4 ^ ((r0 >> 1) & 3)) << 4));
-            b = ld_shared_v4(ks + r1 * 64 + ((t4 ^ ((r1 >> 1) & 3)) << 4));
-          }
-          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint2 ha = codes_to_half4<KIND>(aw[q]), hb = codes_to_half4<KIND>(bw[q]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(x[kg][nt], ha.x, hb.x, ha.y, hb.y, qf[nt][4 * i + q][0], qf[nt][4 * i + q][1]);
-          }
-        }
-      }
-      // ---- scores (log2), masks, reference
-#pragma unroll
-      for (int kg = 0; kg < KG; ++kg) {
-        const float sk = scales[s * 8 + kb16 / 16 + kg];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[kg][nt][e] *= sk * qs[nt][e & 1];
-      }
-      const bool partial = key0 + kCacheTile > first_limit || p.mask != nullptr;
-      uint32_t kept = 0xffffffffu;  // bit (kg NT + nt) 4 + e: this thread's score is one that is attended
-      if (partial) {
-#pragma unroll
-        for (int kg = 0; kg < KG; ++kg)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = key0 + kb16 + 16 * kg + g + (e >> 1) * 8;
-              const bool keep = key < lim[nt][e & 1] && ((sel >> ((nt * 2 + (e & 1)) * 2 + ((kb16 + 16 * kg) >> 5))) & 1u);
-              if (!keep) {
-                x[kg][nt][e] = -INFINITY;
-                kept &= ~(1u << ((kg * NT + nt) * 4 + e));
-              }
-            }
-      }
-      bool move = false;
-      float mx[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float v = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
-#pragma unroll
-          for (int kg = 1; kg < KG; ++kg) v = fmax3(v, x[kg][nt][c], x[kg][nt][c + 2]);
-          mx[nt][c] = v;
-          move |= v > m_ref[nt][c] + kMoveReference;
-        }
-      if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float f[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float v = mx[nt][c];
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            f[c] = 1.f;
-            if (v > m_ref[nt][c]) {
-              f[c] = ex2_approx(m_ref[nt][c] - v);  // 0 from -inf
-              m_ref[nt][c] = v;
-            }
-            l_sum[nt][c] *= f[c];
-          }
-#pragma unroll
-          for (int k = 0; k < MT; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][k][e] *= f[e & 1];
-        }
-      }
-      // ---- weights and P^T fragments
-      uint32_t pf[KG][NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float r0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0];
-        const float r1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1];
+      for (int kb16 = 0; kb16 < TK; kb16 += 16 * KG) {
+        // ---- S^T = K Q^T: 16 keys a time
+        float x[KG][NT][4];
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg) {
-          const float p0 = ex2_approx(x[kg][nt][0] - r0), p1 = ex2_approx(x[kg][nt][1] - r1);
-          const float p2 = ex2_approx(x[kg][nt][2] - r0), p3 = ex2_approx(x[kg][nt][3] - r1);
-          l_sum[nt][0] += p0 + p2;
-          l_sum[nt][1] += p1 + p3;
-          pf[kg][nt][0] = movmatrix(pack_half2(p0, p1));
-          pf[kg][nt][1] = movmatrix(pack_half2(p2, p3));
-        }
-      }
-      // ---- O^T += S_v V^T P^T: 16 keys a time (one scale block each)
-      const bool tail = key0 + kCacheTile > len;
 #pragma unroll
-      for (int kg = 0; kg < KG; ++kg) {
-        const float sv = scales[s * 8 + 4 + kb16 / 16 + kg];
-        const int ra = kb16 + 16 * kg + 2 * t4;  // keys 2 t4, + 1, + 8, + 9 of the 16
-        uint32_t v[4][DV / 4];
+          for (int i = 0; i < D / 64; ++i) {
+            const int r0 = kb16 + 16 * kg + g, r1 = r0 + 8;
+            uint4 a, b;
+            if constexpr (D == 128) {
+              a = ld_shared_v4(ks + r0 * 128 + (((2 * t4 + i) ^ (r0 & 7)) << 4));
+              b = ld_shared_v4(ks + r1 * 128 + (((2 * t4 + i) ^ (r1 & 7)) << 4));
+            } else {
+              a = ld_shared_v4(ks + (r0 >> 1) * 128 + (((r0 & 1) * 4 + t4) ^ ((r0 >> 1) & 7)) * 16);
+              b = ld_shared_v4(ks + (r1 >> 1) * 128 + (((r1 & 1) * 4 + t4) ^ ((r1 >> 1) & 7)) * 16);
+            }
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = ra + (e & 1) + (e >> 1) * 8;
-          if constexpr (D == 128) {
-            const uint4 y = ld_shared_v4(vs + r * 128 + ((g ^ (r & 7)) << 4));
-            v[e][0] = y.x;
-            v[e][1] = y.y;
-            v[e][2] = y.z;
-            v[e][3] = y.w;
-          } else {
-            const uint2 y = ld_shared_v2(vs + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
-            v[e][0] = y.x;
-            v[e][1] = y.y;
-          }
-          // Rows past the sequence hold anything: weight 0 would not stop a NaN.
-          if (tail && key0 + r >= len) {
+            for (int q = 0; q < 4; ++q) {
+              const uint2 ha = codes_to_half4<KIND>(aw[q]), hb = codes_to_half4<KIND>(bw[q]);
 #pragma unroll
-            for (int q = 0; q < DV / 4; ++q) v[e][q] = 0u;
-          }
-        }
-        if (KIND == BSA_CACHE_E4M3 && partial) take_nans<NT, DV, MT>(v, o, kept, kg);
-#pragma unroll
-        for (int q = 0; q < DV / 4; ++q) {
-          // Pairs of keys of one element: {a0 b0 a1 b1}, {a2 b2 a3 b3}.
-          const uint2 ab0 = codes_to_half4<KIND>(__byte_perm(v[0][q], v[1][q], 0x5140));
-          const uint2 cd0 = codes_to_half4<KIND>(__byte_perm(v[2][q], v[3][q], 0x5140));
-          const uint2 ab1 = codes_to_half4<KIND>(__byte_perm(v[0][q], v[1][q], 0x7362));
-          const uint2 cd1 = codes_to_half4<KIND>(__byte_perm(v[2][q], v[3][q], 0x7362));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float y[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(y, ab0.x, ab0.y, cd0.x, cd0.y, pf[kg][nt][0], pf[kg][nt][1]);
-            mma16816(z, ab1.x, ab1.y, cd1.x, cd1.y, pf[kg][nt][0], pf[kg][nt][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[nt][2 * q][e] = fmaf(sv, y[e], o[nt][2 * q][e]);
-              o[nt][2 * q + 1][e] = fmaf(sv, z[e], o[nt][2 * q + 1][e]);
+              for (int nt = 0; nt < NT; ++nt) {
+                if (i == 0 && q == 0)
+                  mma16816_first(x[kg][nt], ha.x, hb.x, ha.y, hb.y, qf[nt][0][0], qf[nt][0][1]);
+                else
+                  mma16816(x[kg][nt], ha.x, hb.x, ha.y, hb.y, qf[nt][4 * i + q][0], qf[nt][4 * i + q][1]);
+              }
             }
           }
         }
+        // ---- scores (log2), masks, reference
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg) {
+          const float sk = __shfl_sync(0xffffffffu, sq[0], kb16 / 16 + kg);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint64_t f = fmul2(f2_make(sk, sk), f2_make(qs[nt][0], qs[nt][1]));
+            f2_split(fmul2(f2_make(x[kg][nt][0], x[kg][nt][1]), f), x[kg][nt][0], x[kg][nt][1]);
+            f2_split(fmul2(f2_make(x[kg][nt][2], x[kg][nt][3]), f), x[kg][nt][2], x[kg][nt][3]);
+          }
+        }
+        uint32_t kept = 0xffffffffu;  // bit (kg NT + nt) 4 + e: this thread's score is one that is attended
+        if (partial) {
+#pragma unroll
+          for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = kb16 + 16 * kg + g + (e >> 1) * 8;
+                const bool keep = key0 + key < lim[nt][e & 1] && ((sel >> ((nt * 2 + (e & 1)) * 2 + ((kb16 + 16 * kg) >> 5))) & 1u);
+                if (!keep) {
+                  x[kg][nt][e] = -INFINITY;
+                  kept &= ~(1u << ((kg * NT + nt) * 4 + e));
+                }
+              }
+        }
+        bool move = false;
+        float mx[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float v = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
+#pragma unroll
+            for (int kg = 1; kg < KG; ++kg) v = fmax3(v, x[kg][nt][c], x[kg][nt][c + 2]);
+            mx[nt][c] = v;
+            move |= v > m_ref[nt][c] + kMoveReference;
+          }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float v = mx[nt][c];
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+              f[c] = 1.f;
+              if (v > m_ref[nt][c]) {
+                f[c] = ex2_approx(m_ref[nt][c] - v);  // 0 from -inf
+                m_ref[nt][c] = v;
+              }
+              l_sum[nt][c] *= f[c];
+            }
+#pragma unroll
+            for (int k = 0; k < MT; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][k][e] *= f[e & 1];
+          }
+        }
+        // ---- weights and P^T fragments
+        uint32_t pf[KG][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint64_t ref = f2_make(m_ref[nt][0] == -INFINITY ? 0.f : -m_ref[nt][0],
+                                       m_ref[nt][1] == -INFINITY ? 0.f : -m_ref[nt][1]);
+          uint64_t l2 = f2_make(l_sum[nt][0], l_sum[nt][1]);
+#pragma unroll
+          for (int kg = 0; kg < KG; ++kg) {
+            float y0, y1, y2, y3;
+            f2_split(fadd2(f2_make(x[kg][nt][0], x[kg][nt][1]), ref), y0, y1);
+            f2_split(fadd2(f2_make(x[kg][nt][2], x[kg][nt][3]), ref), y2, y3);
+            const float p0 = ex2_approx(y0), p1 = ex2_approx(y1), p2 = ex2_approx(y2), p3 = ex2_approx(y3);
+            l2 = fadd2(l2, fadd2(f2_make(p0, p1), f2_make(p2, p3)));
+            pf[kg][nt][0] = movmatrix(pack_half2(p0, p1));
+            pf[kg][nt][1] = movmatrix(pack_half2(p2, p3));
+          }
+          f2_split(l2, l_sum[nt][0], l_sum[nt][1]);
+        }
+        // ---- O^T += S_v V^T P^T: the 16 keys of a group lie in one scale block;
+        // groups that follow each other with the same scale share the addition
+        float sv[KG];
+        uint32_t v[KG][4][DV / 4];
+        bool same = true;
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg) {
+          sv[kg] = __shfl_sync(0xffffffffu, sq[0], C::kGroups + kb16 / 16 + kg);
+          same = same && sv[kg] == sv[0];
+          const int ra = kb16 + 16 * kg + 2 * t4;  // keys 2 t4, + 1, + 8, + 9 of the 16
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = ra + (e & 1) + (e >> 1) * 8;
+            if constexpr (D == 128) {
+              const uint4 y = ld_shared_v4(vs + r * 128 + ((g ^ (r & 7)) << 4));
+              v[kg][e][0] = y.x;
+              v[kg][e][1] = y.y;
+              v[kg][e][2] = y.z;
+              v[kg][e][3] = y.w;
+            } else {
+              const uint2 y = ld_shared_v2(vs + (r >> 1) * 128 + (((r & 1) * 4 + (g >> 1)) ^ ((r >> 1) & 7)) * 16 + (g & 1) * 8);
+              v[kg][e][0] = y.x;
+              v[kg][e][1] = y.y;
+            }
+            // Rows past the sequence hold anything: weight 0 would not stop a NaN.
+            if (tail && key0 + r >= len) {
+#pragma unroll
+              for (int q = 0; q < DV / 4; ++q) v[kg][e][q] = 0u;
+            }
+          }
+          if (KIND == BSA_CACHE_E4M3 && partial) take_nans<NT, DV, MT>(v[kg], o, kept, kg);
+        }
+        auto accumulate = [&](float (&acc)[4], float f, const float (&y)[4]) {
+          const uint64_t ff = f2_make(f, f);
+          f2_split(ffma2(ff, f2_make(y[0], y[1]), f2_make(acc[0], acc[1])), acc[0], acc[1]);
+          f2_split(ffma2(ff, f2_make(y[2], y[3]), f2_make(acc[2], acc[3])), acc[2], acc[3]);
+        };
+        // Pairs of keys of one element: {a0 b0 a1 b1}, {a2 b2 a3 b3}.
+#pragma unroll
+        for (int q = 0; q < DV / 4; ++q) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float y[NT][4];
+#pragma unroll
+            for (int kg = 0; kg < KG; ++kg) {
+              const uint32_t pick = hh ? 0x7362 : 0x5140;
+              const uint2 ab = codes_to_half4<KIND>(__byte_perm(v[kg][0][q], v[kg][1][q], pick));
+              const uint2 cd = codes_to_half4<KIND>(__byte_perm(v[kg][2][q], v[kg][3][q], pick));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (kg > 0 && same) {
+                  mma16816(y[nt], ab.x, ab.y, cd.x, cd.y, pf[kg][nt][0], pf[kg][nt][1]);
+                } else {
+                  if (kg > 0) accumulate(o[nt][2 * q + hh], sv[kg - 1], y[nt]);
+                  mma16816_first(y[nt], ab.x, ab.y, cd.x, cd.y, pf[kg][nt][0], pf[kg][nt][1]);
+                }
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) accumulate(o[nt][2 * q + hh], sv[KG - 1], y[nt]);
+          }
+        }
       }
+      __syncwarp();  // every lane has read the stage
+#pragma unroll
+      for (int s = 0; s + 1 < C::kStages; ++s) {
+        tq[s] = tq[s + 1];
+        sq[s] = sq[s + 1];
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
+      tq[C::kStages - 1] = request(stage, sq[C::kStages - 1]);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
 
     // ---- end of the piece: join the warps that took its tiles, 8 rows of each
@@ -788,6 +817,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     named_bar_sync(1, 32 * kWarps);
     more = walk_next(p, w, mult);
   }
+  if (!ok) {
+    // Let the tiles in flight land before the CTA's shared memory goes away.
+    volatile int no_abort = 0;
+    const Watchdog quick{&no_abort, wd.status, wd.detail, 100000000ll};
+#pragma unroll 1
+    for (int k = 0; k < C::kStages; ++k) {
+      if (tq[0] >= 0) mbar_wait(bars + 8 * stage, phase, quick, kSiteTileFull);
+      tq[0] = k + 1 < C::kStages ? (k == 0 ? tq[1] : tq[2]) : -1;
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  }
 }
 
 // Joins the parts of a row that several CTAs worked on, in the CTAs' order.
@@ -851,7 +894,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Ca
   }
 }
 
-// Tiles of 64 keys that some head of the group selects, below the length:
+// Tiles that some head of the group selects, below the length:
 // one CTA per (batch row, K/V head).
 constexpr int kTilesThreads = 1024;
 static_assert(kTilesThreads / 32 == 32, "a lane per warp");
@@ -863,7 +906,7 @@ __global__ void __launch_bounds__(kTilesThreads) tiles_kernel(const __grid_const
   const int e = blockIdx.x, b = e / p.c.Hkv, h = e % p.c.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int len = len_of(p, b);
-  const int tiles = min((len + kCacheTile - 1) / kCacheTile, p.max_tiles);
+  const int tiles = min((len + p.tile - 1) / p.tile, p.max_tiles);
   const uint8_t* mrow = p.mask + ((size_t)b * p.Hq + (size_t)h * p.g) * p.NKB;
   int32_t* out = p.list + (size_t)e * p.max_tiles;
   int done = 0;
@@ -871,7 +914,7 @@ __global__ void __launch_bounds__(kTilesThreads) tiles_kernel(const __grid_const
     const int t = base + tid;
     unsigned on = 0u;
     if (t < tiles) {
-      const int k0 = t * kCacheTile / p.bk, k1 = p.bk == 32 ? min(k0 + 1, p.NKB - 1) : k0;
+      const int k0 = t * p.tile / p.bk, k1 = p.bk < p.tile ? min(k0 + 1, p.NKB - 1) : k0;
 #pragma unroll 8
       for (int i = 0; i < p.g; ++i) on |= __ldg(mrow + (size_t)i * p.NKB + k0) | __ldg(mrow + (size_t)i * p.NKB + k1);
     }
@@ -895,19 +938,19 @@ __global__ void __launch_bounds__(kTilesThreads) tiles_kernel(const __grid_const
 
 template <int D, int KIND, int NT>
 cudaError_t launch_t(const CacheAttnParams& p, int grid, cudaStream_t s) {
-  const int smem = AttnCfg<D, NT>::kSmem;
+  const int smem = AttnCfg<D>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_after(attn_kernel<D, KIND, NT>, dim3(grid), dim3(kAttnThreads), smem, s, p);
 }
 template <int D, int KIND>
 cudaError_t launch_k(const CacheAttnParams& p, int grid, cudaStream_t s) {
-  // Up to 24 rows: each warp has all of them and tiles of its own, so that a code
-  // is converted once.  Beyond, the three warps share each tile (and convert it
-  // three times, which is still less than a second pass over the cache).
+  // As few row tiles as hold the rows (1, 2 or 4 of at most 24), for each
+  // converts the codes again, and as few columns in them.
   const int rows = p.M < kCacheUnitRows ? p.M : kCacheUnitRows;
-  const int nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 24 ? 3 : (rows <= 48 ? 2 : 3)));
-  return nt == 1 ? launch_t<D, KIND, 1>(p, grid, s) : (nt == 2 ? launch_t<D, KIND, 2>(p, grid, s) : launch_t<D, KIND, 3>(p, grid, s));
+  const int per = rows <= 24 ? rows : (rows <= 48 ? (rows + 1) / 2 : (rows + 3) / 4);
+  if (per <= 8) return launch_t<D, KIND, 1>(p, grid, s);
+  return per <= 16 ? launch_t<D, KIND, 2>(p, grid, s) : launch_t<D, KIND, 3>(p, grid, s);
 }
 template <int D>
 cudaError_t launch_d(const CacheAttnParams& p, int grid, cudaStream_t s) {

@@ -200,8 +200,8 @@ bsa_status make_fwd_params(const bsa_plan_layout& L, const PlanDev& pd, uint8_t*
 // Device check of every entry point, and the watchdog limit (bsa_api.cu).
 bsa_status check_device(int* dev_out);
 long long watchdog_limit_ns();
-// Tensor map of `rows` rows of d bytes, box {d, box_rows}, d-byte swizzle (d 64 or 128).
-bool encode_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int box_rows);
+// Tensor map of `lines` lines of 128 bytes, box {128, box_lines}, 128-byte swizzle.
+bool encode_lines_map(CUtensorMap* m, const void* base, uint64_t lines, int box_lines);
 cudaError_t launch_watchdog_selftest(int32_t* status, long long limit_ns, cudaStream_t stream);
 
 }  // namespace bsa

@@ -638,7 +638,8 @@ bsa_status bsa_cache_append(const bsa_cache* cache, const bsa_rows* k, const bsa
  *   be named several times.
  * mask: NULL, or device u8 [B][Hq][NKB]: non-zero selects key block j / bk for
  *   a query head (keys past the last block are not selected); bk in {32, 64,
- *   128, 256}.  Tiles of 64 keys that no head of a group selects are not read.
+ *   128, 256}.  Tiles of 32 (d = 128) or 64 keys that no head of a group
+ *   selects are not read.
  * flags: 0 or BSA_CACHE_CAUSAL.  scale <= 0 selects 1/sqrt(d).
  * workspace: device, 16-byte aligned, bsa_cache_attention_workspace_bytes
  *   bytes; scratch of this call (calls that overlap in time need their own).
