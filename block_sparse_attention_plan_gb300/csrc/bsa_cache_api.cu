@@ -82,7 +82,7 @@ bsa_status attn_layout(const CacheDev& c, int B, int Hq, int nq, int NKB, int bk
   }
   const long long groups = (M + kCacheUnitRows - 1) / kCacheUnitRows;
   if (M >= (1ll << 30) || (long long)B * Hq * nq >= (1ll << 31) ||
-      (long long)B * c.Hkv * groups * tiles >= (1ll << 40) || (long long)B * c.Hkv > (1ll << 24))
+      (double)B * c.Hkv * groups * tiles >= 2147483648.0 || (long long)B * c.Hkv > (1ll << 24))
     return BSA_ERR_UNSUPPORTED;
   AttnLayout l;
   l.rows_cap = (int)(M < kCacheUnitRows ? M : kCacheUnitRows);

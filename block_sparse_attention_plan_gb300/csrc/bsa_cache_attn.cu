@@ -38,6 +38,8 @@
 // swizzled so that the products read with few conflicts), the next tile requested as soon as one is used up.
 // (A warp that feeds all others issues a tile every 700 cycles, too slow for
 // tiles of 8 KB, and tiles of 16 KB leave room for six warps' rings at most.)
+#include <type_traits>
+
 #include "bsa_cache.h"
 #include "bsa_cache_codes.cuh"
 #include "bsa_device.cuh"
@@ -69,7 +71,7 @@ struct AttnCfg {
   static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
   static constexpr int kSmem = kOffAbort + 16;
   static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
-  static_assert(kMergeBytes >= 8 * (kAttnThreads + 1), "prefix");
+  static_assert(kMergeBytes >= 4 * (kAttnThreads + kWarps), "prefix");
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -125,30 +127,29 @@ __device__ __forceinline__ int entry_tiles(const CacheAttnParams& p, int e) {
   return (len_of(p, e) + p.tile - 1) / p.tile;
 }
 
-// Walks the pieces of rows in tiles [lo, hi) of the line.
+// Walks the pieces of rows in tiles [lo, hi) of the line (fewer than 2^31 tiles:
+// checked on the host).
 struct Walk {
   int e, sub, cnt;   // entry, unit within it, its tiles
   int t0, t1;        // this piece: tiles [t0, t1) of the unit
-  long long row0;    // first tile of the unit in the line
-  long long at, hi;
+  int row0;          // first tile of the unit in the line
+  int at, hi;
 };
 __device__ __forceinline__ void walk_piece(Walk& w) {
-  w.t0 = (int)(w.at - w.row0);
-  const long long left = w.hi - w.at;
-  w.t1 = left < w.cnt - w.t0 ? w.t0 + (int)left : w.cnt;
+  w.t0 = w.at - w.row0;
+  w.t1 = min(w.cnt, w.t0 + w.hi - w.at);
 }
-__device__ __forceinline__ void walk_start(const CacheAttnParams& p, Walk& w, int mult, int e, long long base,
-                                           long long lo, long long hi) {
+__device__ __forceinline__ void walk_start(const CacheAttnParams& p, Walk& w, int mult, int e, int base, int lo, int hi) {
   w.at = lo;
   w.hi = hi;
   w.cnt = entry_tiles(p, e);
-  while (lo >= base + (long long)w.cnt * mult) {
-    base += (long long)w.cnt * mult;
+  while (lo >= base + w.cnt * mult) {
+    base += w.cnt * mult;
     w.cnt = entry_tiles(p, ++e);
   }
   w.e = e;
-  w.sub = (int)((lo - base) / w.cnt);
-  w.row0 = base + (long long)w.sub * w.cnt;
+  w.sub = (lo - base) / w.cnt;
+  w.row0 = base + w.sub * w.cnt;
   walk_piece(w);
 }
 __device__ __forceinline__ bool walk_next(const CacheAttnParams& p, Walk& w, int mult) {
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   constexpr int TK = C::TK;
   constexpr int KG = NT * D >= 384 ? 1 : 2;  // groups of 16 keys whose scores are held at once
   extern __shared__ __align__(1024) uint8_t smem[];
-  long long* s_prefix = reinterpret_cast<long long*>(smem + C::kOffMerge);
+  int* s_prefix = reinterpret_cast<int*>(smem + C::kOffMerge);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x;
@@ -291,33 +292,32 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   const int E = p.mask ? p.B * p.c.Hkv : p.B;
   const int mult = p.mask ? p.groups : p.c.Hkv * p.groups;
   const int per = (E + kAttnThreads - 1) / kAttnThreads;
-  long long sum = 0;
+  int sum = 0;
   for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) sum += entry_tiles(p, e);
   sum *= mult;
-  s_prefix[tid + 1] = sum;
-  __syncthreads();
-  if (warp == 0) {
-    long long acc = 0;
-    for (int i = 0; i < kAttnThreads; i += 32) {
-      long long x = s_prefix[i + lane + 1];
+  int x = sum;  // inclusive prefix over the warp, then over the warps
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      s_prefix[i + lane + 1] = acc + x;
-      acc += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) s_prefix[0] = 0;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
+  if (lane == 31) s_prefix[kAttnThreads + warp] = x;
   __syncthreads();
-  const long long T = s_prefix[kAttnThreads];
+  int T = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i == warp) x += T;
+    T += s_prefix[kAttnThreads + i];
+  }
+  s_prefix[tid] = x - sum;  // tiles before this thread's entries
+  __syncthreads();
   // A tile at least for each set of warps that shares one, so that short lines
   // leave few parts to join.  No CTA that works has an empty piece: the parts of
-  // a row are those of consecutive CTAs.
-  const long long most = (T + KL - 1) / KL;
-  const int G = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x);
-  const long long lo = cta < G ? cta * T / G : 0, hi = cta < G ? (cta + 1) * T / G : 0;
+  // a row are those of consecutive CTAs.  The first `more_of` CTAs have a tile more.
+  const int G = min((T + KL - 1) / KL, (int)gridDim.x);
+  const int share = G > 0 ? T / G : 0, more_of = T - share * G;
+  const int lo = cta < G ? cta * share + min(cta, more_of) : 0;
+  const int hi = cta < G ? lo + share + (cta < more_of ? 1 : 0) : 0;
   // Empty entries' rows: O = 0, LSE = -inf.
   for (int e = cta; e < E; e += (int)gridDim.x) {
     if (entry_tiles(p, e) != 0) continue;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   }
   if (tid == 0) p.desc[4 * cta] = 0;  // no row of this CTA goes on in the next one (so far)
   if (lo >= hi || *s_abort) return;   // (the same for every thread: barriers above)
-  // The thread whose entries hold tile lo.
+  // The thread whose entries hold tile lo (the last that does not start past it).
   int a = 0, z = kAttnThreads;
   while (z - a > 1) {
     const int m = (a + z) >> 1;
@@ -346,6 +346,38 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   walk_start(p, w, mult, a * per, s_prefix[a], lo, hi);
   __syncthreads();  // the prefix gives way to the merge buffer
 
+  // ------------------------------------------------------------- computation
+  const int g = lane >> 2, t4 = lane & 3;
+  constexpr int KS = D / 16;    // 16-element steps of q . k
+  constexpr int MT = D / 16;    // 16-row tiles of O^T
+  constexpr int DV = D / 8;     // consecutive elements of O a thread holds
+  // This warp's query rows as they are: read ahead of the first tiles, which the
+  // memory is then busy with.
+  uint32_t q_raw[NT][KS][2];
+  auto load_q = [&](const Unit& u) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int m = u.grp * kCacheUnitRows + rt * 8 * NT + 8 * nt + g;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) q_raw[nt][k][0] = q_raw[nt][k][1] = 0u;
+      if (m < p.M) {
+        const uint16_t* qr = p.q.p + u.b * p.q.sb + (u.h * p.g + m / p.nq) * p.q.sh + (m % p.nq) * p.q.st;
+        // Word s of 16-byte chunk (D == 128: 2 t4 + i; D == 64: t4) of a row of
+        // codes are elements 16 chunk + 4 s ..: the same of q.
+#pragma unroll
+        for (int k2 = 0; k2 < KS / 2; ++k2) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(qr + t4 * (D / 4) + k2 * 8));
+          q_raw[nt][2 * k2][0] = x.x;
+          q_raw[nt][2 * k2][1] = x.y;
+          q_raw[nt][2 * k2 + 1][0] = x.z;
+          q_raw[nt][2 * k2 + 1][1] = x.w;
+        }
+      }
+    }
+  };
+  load_q(unit_of(p, w.e, w.sub));
+  bool later = false;
+
   // ---------------------------------------------------------------- requests
   const int lpage = 31 - __clz(p.c.page), lsb = 31 - __clz(p.c.sb);
   const int cs = min(p.c.page, TK);  // keys per box
@@ -354,7 +386,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   const uint64_t pol = R == 1 && p.groups == 1 ? policy_evict_first() : policy_evict_normal();
   // First tile of a piece that is this warp's: tile t of the CTA's line is taken
   // by the warps with kl = t mod KL.
-  auto first_of = [&](const Walk& x) { return x.t0 + (int)((kl + KL - (int)((x.at - lo) % KL)) % KL); };
+  auto first_of = [&](const Walk& x) { return x.t0 + ((kl - (x.at - lo)) & (KL - 1)); };  // (KL is 1, 2 or 4)
   Feed f;
   f.w = w;
   f.pos = first_of(w);
@@ -438,17 +470,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   int stage = 0;
   uint32_t phase = 0;
 
-  // ------------------------------------------------------------- computation
-  const int g = lane >> 2, t4 = lane & 3;
-  constexpr int KS = D / 16;    // 16-element steps of q . k
-  constexpr int MT = D / 16;    // 16-row tiles of O^T
-  constexpr int DV = D / 8;     // consecutive elements of O a thread holds
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* ml = reinterpret_cast<float*>(smem + C::kOffMl);
   bool more = true, ok = true;
   while (more) {
     const Unit u = unit_of(p, w.e, w.sub);
     const int len = len_of(p, u.b);
+    if (later) load_q(u);
+    later = true;
     const int m0 = u.grp * kCacheUnitRows + rt * 8 * NT;  // first query row of this warp
     // Query fragments: lane (g, t4) holds row 8 nt + g, elements 4 a word of codes.
     uint32_t qf[NT][KS][2];
@@ -457,25 +486,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     int hq_of[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int m = m0 + 8 * nt + g;
-      uint32_t raw[KS][2];
+      auto& raw = q_raw[nt];
       float amax = 0.f;
-      if (m < p.M) {
-        const uint16_t* qr = p.q.p + u.b * p.q.sb + (u.h * p.g + m / p.nq) * p.q.sh + (m % p.nq) * p.q.st;
-        // Word s of 16-byte chunk (D == 128: 2 t4 + i; D == 64: t4) of a row of
-        // codes are elements 16 chunk + 4 s ..: the same of q.
-#pragma unroll
-        for (int k2 = 0; k2 < KS / 2; ++k2) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(qr + t4 * (D / 4) + k2 * 8));
-          raw[2 * k2][0] = x.x;
-          raw[2 * k2][1] = x.y;
-          raw[2 * k2 + 1][0] = x.z;
-          raw[2 * k2 + 1][1] = x.w;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) raw[k][0] = raw[k][1] = 0u;
-      }
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -710,30 +722,36 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
           f2_split(ffma2(ff, f2_make(y[2], y[3]), f2_make(acc[2], acc[3])), acc[2], acc[3]);
         };
         // Pairs of keys of one element: {a0 b0 a1 b1}, {a2 b2 a3 b3}.
+        auto products = [&](auto one_scale) {
 #pragma unroll
-        for (int q = 0; q < DV / 4; ++q) {
+          for (int q = 0; q < DV / 4; ++q) {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float y[NT][4];
+            for (int hh = 0; hh < 2; ++hh) {
+              float y[NT][4];
 #pragma unroll
-            for (int kg = 0; kg < KG; ++kg) {
-              const uint32_t pick = hh ? 0x7362 : 0x5140;
-              const uint2 ab = codes_to_half4<KIND>(__byte_perm(v[kg][0][q], v[kg][1][q], pick));
-              const uint2 cd = codes_to_half4<KIND>(__byte_perm(v[kg][2][q], v[kg][3][q], pick));
+              for (int kg = 0; kg < KG; ++kg) {
+                const uint32_t pick = hh ? 0x7362 : 0x5140;
+                const uint2 ab = codes_to_half4<KIND>(__byte_perm(v[kg][0][q], v[kg][1][q], pick));
+                const uint2 cd = codes_to_half4<KIND>(__byte_perm(v[kg][2][q], v[kg][3][q], pick));
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                if (kg > 0 && same) {
-                  mma16816(y[nt], ab.x, ab.y, cd.x, cd.y, pf[kg][nt][0], pf[kg][nt][1]);
-                } else {
-                  if (kg > 0) accumulate(o[nt][2 * q + hh], sv[kg - 1], y[nt]);
-                  mma16816_first(y[nt], ab.x, ab.y, cd.x, cd.y, pf[kg][nt][0], pf[kg][nt][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (kg > 0 && decltype(one_scale)::value) {
+                    mma16816(y[nt], ab.x, ab.y, cd.x, cd.y, pf[kg][nt][0], pf[kg][nt][1]);
+                  } else {
+                    mma16816_first(y[nt], ab.x, ab.y, cd.x, cd.y, pf[kg][nt][0], pf[kg][nt][1]);
+                    if (!decltype(one_scale)::value) accumulate(o[nt][2 * q + hh], sv[kg], y[nt]);
+                  }
                 }
               }
-            }
+              if (decltype(one_scale)::value) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) accumulate(o[nt][2 * q + hh], sv[KG - 1], y[nt]);
+                for (int nt = 0; nt < NT; ++nt) accumulate(o[nt][2 * q + hh], sv[0], y[nt]);
+              }
+            }
           }
-        }
+        };
+        if (KG == 1 || same) products(std::true_type{});
+        else products(std::false_type{});
       }
       __syncwarp();  // every lane has read the stage
 #pragma unroll
@@ -810,8 +828,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     }
     if (tid == 0 && starts && !whole) {
       // CTAs up to the one that holds the unit's last tile.
-      const long long last = w.row0 + w.cnt - 1;
-      const int c1 = (int)(((last + 1) * G - 1) / T);
+      const int last = w.row0 + w.cnt - 1, longer = more_of * (share + 1);
+      const int c1 = last < longer ? last / (share + 1) : more_of + (last - longer) / share;
       *reinterpret_cast<int4*>(p.desc + 4 * cta) = make_int4(c1 - cta + 1, u.b, u.h, u.grp);
     }
     named_bar_sync(1, 32 * kWarps);
