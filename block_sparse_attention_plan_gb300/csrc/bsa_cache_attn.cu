@@ -253,6 +253,7 @@ struct Feed {
   int pos, n, i;    // first tile of the batch (within the unit), its size, the next one to request
   int tile, pr[4];  // this lane's tile
   int len;          // of the piece's sequence
+  const uint8_t* mask;  // of query row `lane` of the warp (with a mask)
   bool more;
 };
 
@@ -260,7 +261,7 @@ template <int D, int KIND, int NT>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = AttnCfg<D>;
   constexpr int TK = C::TK;
-  constexpr int KG = NT * D >= 384 ? 1 : 2;  // groups of 16 keys whose scores are held at once
+  constexpr int KG = NT * D <= 64 ? 4 : (NT * D < 384 ? 2 : 1);  // groups of 16 keys whose scores are held at once
   extern __shared__ __align__(1024) uint8_t smem[];
   int* s_prefix = reinterpret_cast<int*>(smem + C::kOffMerge);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
@@ -410,6 +411,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     f.n = min(32, (f.w.t1 - f.pos + KL - 1) / KL);
     f.i = 0;
     const int32_t* row = p.c.table + (size_t)seq * p.c.max_pages;
+    if (p.mask) {
+      const int m = min(u.grp * kCacheUnitRows + rt * 8 * NT + lane, p.M - 1);
+      f.mask = p.mask + ((size_t)u.b * p.Hq + u.h * p.g + m / p.nq) * p.NKB;
+    }
     f.tile = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) f.pr[j] = -1;
@@ -432,9 +437,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   };
   // Request the warp's next tile into stage s.  Returns its number (-1: there is
   // none); `scale` gets this lane's scale of it: lanes 0 .. kGroups - 1 K's of 16
-  // keys each, the next kGroups V's (0 where the keys lie past the length).
-  auto request = [&](int s, float& scale) -> int {
+  // keys each, the next kGroups V's (0 where the keys lie past the length);
+  // `sel` the mask's bytes of query row `lane` for the tile's halves of 32 keys.
+  auto request = [&](int s, float& scale, uchar2& sel) -> int {
     scale = 0.f;
+    sel = make_uchar2(0, 0);
     if (f.more && f.i == f.n) refill();
     if (!f.more) return -1;
     int box[4];
@@ -460,13 +467,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       if (tile * TK + 16 * gr < f.len)
         scale = __ldg((lane < C::kGroups ? p.c.ks : p.c.vs) + ((size_t)(unsigned)(sbox + ((16 * gr) & (cs - 1))) >> lsb));
     }
+    if (p.mask && lane < 8 * NT) {
+      const int k0 = tile * TK / p.bk;
+      if (k0 < p.NKB) sel.x = __ldg(f.mask + k0);
+      if (TK > 32) {
+        const int k1 = (tile * TK + 32) / p.bk;
+        if (k1 < p.NKB) sel.y = __ldg(f.mask + k1);
+      }
+    }
     return tile;
   };
   // Tiles and scales of the stages, the one to be used next first.
   int tq[C::kStages];
   float sq[C::kStages];
+  uchar2 mq[C::kStages];
 #pragma unroll
-  for (int s = 0; s < C::kStages; ++s) tq[s] = request(s, sq[s]);
+  for (int s = 0; s < C::kStages; ++s) tq[s] = request(s, sq[s], mq[s]);
   int stage = 0;
   uint32_t phase = 0;
 
@@ -482,8 +498,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     // Query fragments: lane (g, t4) holds row 8 nt + g, elements 4 a word of codes.
     uint32_t qf[NT][KS][2];
     float qs[NT][2];  // scale of rows 8 nt + 2 t4, + 1
-    int lim[NT][2];   // keys below it are visible to them
-    int hq_of[NT][2];
+    int lim;          // keys below it are visible to row `lane` of the warp
+    {
+      const int m = m0 + lane;
+      lim = m < p.M ? (p.causal ? min(len, len - p.nq + m % p.nq + 1) : len) : 0;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       auto& raw = q_raw[nt];
@@ -513,9 +532,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         qs[nt][x] = __shfl_sync(0xffffffffu, up, (2 * t4 + x) * 4) * p.scale_log2;
-        const int mm = m0 + 8 * nt + 2 * t4 + x;
-        hq_of[nt][x] = u.h * p.g + min(mm, p.M - 1) / p.nq;
-        lim[nt][x] = mm < p.M ? (p.causal ? min(len, len - p.nq + mm % p.nq + 1) : len) : 0;
       }
     }
     float o[NT][MT][4];
@@ -534,44 +550,21 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     }
     const int first_limit = p.causal ? len - p.nq + 1 : len;  // keys below it are visible to every row
 
-    // With a mask: this warp's rows' bytes of it are read a tile ahead.
-    uint8_t sel_next[NT][2][2];
-    auto read_mask = [&](int tile) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int kb = (tile * TK + 32 * hf) / p.bk;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            sel_next[nt][c][hf] =
-                hf > 0 && (p.bk > 32 || TK <= 32) ? sel_next[nt][c][0]
-                                    : (kb < p.NKB ? __ldg(p.mask + ((size_t)u.b * p.Hq + hq_of[nt][c]) * p.NKB + kb) : 0);
-      }
-    };
     int t = first_of(w);
-    if (p.mask && t < w.t1) read_mask(tq[0]);
     for (; t < w.t1 && ok; t += KL) {
       const int key0 = tq[0] * TK;
-      // Selection of the tile's halves of 32 keys by these rows' heads.
-      uint32_t sel = 0xffffffffu;
-      if (p.mask) {
-        sel = 0u;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) sel |= sel_next[nt][c][hf] ? 1u << ((nt * 2 + c) * 2 + hf) : 0u;
-        if (t + KL < w.t1) read_mask(tq[1]);
-      }
       if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, phase, wd, kSiteTileFull))) {
         ok = false;  // recorded; these rows' results are void, the walk goes on so that no barrier is missed
         break;
       }
       const uint32_t ks = ring + stage * C::kStageBytes, vs = ks + C::kTileBytes;
-      const bool partial = key0 + TK > first_limit || p.mask != nullptr;
       const bool tail = key0 + TK > len;
+      // The tile's computation, for tiles that every row attends wholly and for
+      // the others: the code of the masks, in the loop that most tiles take,
+      // would cost those a tenth (registers, and the loop outgrows the
+      // instruction cache).
+      auto compute = [&](auto masked_c) {
+      constexpr bool kMasked = decltype(masked_c)::value;
 #pragma unroll 1
       for (int kb16 = 0; kb16 < TK; kb16 += 16 * KG) {
         // ---- S^T = K Q^T: 16 keys a time
@@ -615,20 +608,30 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
           }
         }
         uint32_t kept = 0xffffffffu;  // bit (kg NT + nt) 4 + e: this thread's score is one that is attended
-        if (partial) {
+        if constexpr (kMasked) {
+          // Rows whose heads select the tile's halves of 32 keys.
+          uint32_t sel[2] = {0xffffffffu, 0xffffffffu};
+          if (p.mask) {
+            sel[0] = __ballot_sync(0xffffffffu, mq[0].x != 0);
+            sel[1] = __ballot_sync(0xffffffffu, mq[0].y != 0);
+          }
 #pragma unroll
-          for (int kg = 0; kg < KG; ++kg)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int c = 0; c < 2; ++c) {
+              const int row = 8 * nt + 2 * t4 + c;
+              const int end = __shfl_sync(0xffffffffu, lim, row) - key0 - kb16;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int key = kb16 + 16 * kg + g + (e >> 1) * 8;
-                const bool keep = key0 + key < lim[nt][e & 1] && ((sel >> ((nt * 2 + (e & 1)) * 2 + ((kb16 + 16 * kg) >> 5))) & 1u);
-                if (!keep) {
-                  x[kg][nt][e] = -INFINITY;
-                  kept &= ~(1u << ((kg * NT + nt) * 4 + e));
+              for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+                for (int hi8 = 0; hi8 < 2; ++hi8) {
+                  const bool keep = 16 * kg + g + 8 * hi8 < end && (sel[(kb16 + 16 * kg) >> 5] >> row & 1u);
+                  if (!keep) {
+                    x[kg][nt][2 * hi8 + c] = -INFINITY;
+                    kept &= ~(1u << ((kg * NT + nt) * 4 + 2 * hi8 + c));
+                  }
                 }
-              }
+            }
         }
         bool move = false;
         float mx[NT][2];
@@ -709,12 +712,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
               v[kg][e][1] = y.y;
             }
             // Rows past the sequence hold anything: weight 0 would not stop a NaN.
-            if (tail && key0 + r >= len) {
+            if (kMasked && tail && key0 + r >= len) {
 #pragma unroll
               for (int q = 0; q < DV / 4; ++q) v[kg][e][q] = 0u;
             }
           }
-          if (KIND == BSA_CACHE_E4M3 && partial) take_nans<NT, DV, MT>(v[kg], o, kept, kg);
+          if constexpr (KIND == BSA_CACHE_E4M3 && kMasked) take_nans<NT, DV, MT>(v[kg], o, kept, kg);
         }
         auto accumulate = [&](float (&acc)[4], float f, const float (&y)[4]) {
           const uint64_t ff = f2_make(f, f);
@@ -753,13 +756,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         if (KG == 1 || same) products(std::true_type{});
         else products(std::false_type{});
       }
+      };
+      if (key0 + TK > first_limit || p.mask != nullptr) compute(std::true_type{});
+      else compute(std::false_type{});
       __syncwarp();  // every lane has read the stage
 #pragma unroll
       for (int s = 0; s + 1 < C::kStages; ++s) {
         tq[s] = tq[s + 1];
         sq[s] = sq[s + 1];
+        mq[s] = mq[s + 1];
       }
-      tq[C::kStages - 1] = request(stage, sq[C::kStages - 1]);
+      tq[C::kStages - 1] = request(stage, sq[C::kStages - 1], mq[C::kStages - 1]);
       if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1u;
