@@ -598,9 +598,24 @@ bsa_status bsa_watchdog_selftest(int32_t* status, int limit_us, void* stream) {
 }  // extern "C"
 
 namespace bsa {
-bsa_status forward_over_cache(const bsa_plan* plan, const void* Q, const void* K, const void* V,
-                              const int32_t* kv_lens, int flags, void* O, float* LSE, int d, float scale,
-                              cudaStream_t stream) {
-  return forward_stage(plan, Q, K, V, nullptr, kv_lens, flags, O, LSE, d, scale, BSA_STAGE_ALL, stream, true);
+bsa_status key_norm_views(const bsa_plan* plan, CacheLoadParams* p) {
+  const PlanImpl* q = as_impl(plan);
+  if (!q) return BSA_ERR_PLAN_MISMATCH;
+  const FwdScratch fs = fwd_scratch(q->L);
+  p->kmax = reinterpret_cast<float*>(q->ws + fs.off_kmax);
+  p->vmax = reinterpret_cast<float*>(q->ws + fs.off_vmax);
+  p->fb_flag = reinterpret_cast<int32_t*>(q->ws + fs.off_fb_flag);
+  p->knorm_status = q->dev.control + kCtlKnormStatus;
+  p->rows = q->L.rows;
+  p->ku = q->L.ku;
+  p->NKU = q->L.NKU;
+  p->device = q->device;
+  return BSA_OK;
+}
+
+bsa_status forward_after_load(const bsa_plan* plan, const void* Q, const CacheLoadParams& p, int flags, void* O,
+                              float* LSE, float scale, cudaStream_t stream) {
+  return forward_stage(plan, Q, p.k, p.v, nullptr, p.lens, flags, O, LSE, p.c.d, scale,
+                       BSA_STAGE_ROWBOUND | BSA_STAGE_BOUNDED | BSA_STAGE_EXACT, stream, true);
 }
 }  // namespace bsa

@@ -107,6 +107,24 @@ struct CacheAttnParams {
   long long watchdog_ns;
 };
 
+// K and V of sequences seqs[0 .. B) as bf16 [B][Hkv][Nk][d] (zero at and past
+// the length), their lengths [B], and what the forward's key-norm pass gives:
+// the largest key norm and value of every unit of ku keys, rows' flags cleared.
+struct CacheLoadParams {
+  CacheDev c;
+  const int32_t* seqs;
+  int B, Nk;
+  uint16_t* k;
+  uint16_t* v;
+  int32_t* lens;
+  float* kmax;  // [B*Hkv][NKU]
+  float* vmax;
+  int32_t* fb_flag;  // [rows]
+  int32_t* knorm_status;  // status and detail of the key-norm pass
+  int rows, ku, NKU;
+  int device;  // the plan's
+};
+
 cudaError_t launch_cache_resize(const CacheDev& c, const int32_t* seqs, const int32_t* new_lens, int n,
                                 cudaStream_t s);
 cudaError_t launch_cache_fork(const CacheDev& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);
@@ -115,14 +133,12 @@ cudaError_t launch_cache_copy(const CacheDev& dst, const CacheDev& src, const in
                               const int32_t* src_pages, int n, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheAppendParams& p, int sms, cudaStream_t s);
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int grid, cudaStream_t s);
-// K and V of sequences seqs[0 .. B) as bf16 [B][Hkv][Nk][d] (zero at and past
-// the length) and their lengths [B].
-cudaError_t launch_cache_load(const CacheDev& c, const int32_t* seqs, int B, int Nk, uint16_t* k, uint16_t* v,
-                              int32_t* lens, cudaStream_t s);
-// bsa_forward_stage with the causal offset of each sequence taken from its
-// key length (bsa_api.cu).
-bsa_status forward_over_cache(const bsa_plan* plan, const void* Q, const void* K, const void* V,
-                              const int32_t* kv_lens, int flags, void* O, float* LSE, int d, float scale,
-                              cudaStream_t stream);
+cudaError_t launch_cache_load(const CacheLoadParams& p, cudaStream_t s);
+// The arrays of a plan's forward that its key-norm pass writes, and that forward
+// without the pass, the causal offset of each sequence taken from its key length
+// (bsa_api.cu).
+bsa_status key_norm_views(const bsa_plan* plan, CacheLoadParams* p);
+bsa_status forward_after_load(const bsa_plan* plan, const void* Q, const CacheLoadParams& p, int flags, void* O,
+                              float* LSE, float scale, cudaStream_t stream);
 
 }  // namespace bsa

@@ -274,7 +274,9 @@ size_t bsa_cache_forward_workspace_bytes(const bsa_plan* plan, const bsa_cache* 
 bsa_status bsa_cache_forward(const bsa_plan* plan, const bsa_cache* cache, const int32_t* seqs, const void* Q,
                              int flags, void* O, float* LSE, float scale, void* workspace, size_t workspace_bytes,
                              void* stream) {
-  CacheDev c;
+  CacheLoadParams p;
+  std::memset(&p, 0, sizeof(p));
+  CacheDev& c = p.c;
   bsa_status st = check_cache(cache, &c);
   if (st != BSA_OK) return st;
   bsa_plan_layout L;
@@ -290,15 +292,21 @@ bsa_status bsa_cache_forward(const bsa_plan* plan, const bsa_cache* cache, const
   const long long Nk = (long long)L.NKB * L.bk;
   if ((long long)L.B * L.Hkv * Nk >= (1ll << 31) || (long long)L.B * L.Hkv > 65535) return BSA_ERR_UNSUPPORTED;
   if (workspace_bytes < bsa_cache_forward_workspace_bytes(plan, cache)) return BSA_ERR_WORKSPACE;
-  if ((st = check_device(nullptr)) != BSA_OK) return st;
+  int dev = 0;
+  if ((st = check_device(&dev)) != BSA_OK) return st;
+  if ((st = key_norm_views(plan, &p)) != BSA_OK) return st;
+  if (p.device != dev) return BSA_ERR_PLAN_MISMATCH;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const uint64_t kv = align256(2ull * L.B * c.Hkv * (uint64_t)Nk * c.d);
-  uint16_t* k = reinterpret_cast<uint16_t*>(ws);
-  uint16_t* v = reinterpret_cast<uint16_t*>(ws + kv);
-  int32_t* lens = reinterpret_cast<int32_t*>(ws + 2 * kv);
+  p.seqs = seqs;
+  p.B = L.B;
+  p.Nk = (int)Nk;
+  p.k = reinterpret_cast<uint16_t*>(ws);
+  p.v = reinterpret_cast<uint16_t*>(ws + kv);
+  p.lens = reinterpret_cast<int32_t*>(ws + 2 * kv);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (launch_cache_load(c, seqs, L.B, (int)Nk, k, v, lens, s) != cudaSuccess) return BSA_ERR_CUDA;
-  return forward_over_cache(plan, Q, k, v, lens, flags, O, LSE, c.d, scale, s);
+  if (launch_cache_load(p, s) != cudaSuccess) return BSA_ERR_CUDA;
+  return forward_after_load(plan, Q, p, flags, O, LSE, scale, s);
 }
 
 }  // extern "C"
