@@ -6,8 +6,11 @@
 // maximum and the rounding.  A CTA takes units of one (row, block): what leads
 // to the page (sequence -> length -> table entry) is read once for all of
 // them, and a unit's elements are loaded while the one before is rounded.
-// Bound by the 2 bytes read and the byte written per element for a long
-// append, by that chain of reads for a token per sequence.
+// A long append would be bound by the 2 bytes read and the byte written per
+// element but for the instructions, which are counted here (about five per
+// element: maxima of pairs as integers, the scale's reciprocal from its bits,
+// what depends on the thread alone kept out of the units' loop); a token per
+// sequence is bound by that chain of reads.
 //
 // With power-of-two scales x / scale is exact, codes move to a larger scale
 // without a second rounding (subnormal codes excepted), and both code types
@@ -22,25 +25,22 @@ using namespace dev;
 
 constexpr int kVec = 4;  // 16-byte chunks (8 elements) per thread and unit
 
-// Larger of the magnitudes of two pairs of elements (a NaN never wins).
-template <bool FP16>
+// Larger of each two elements' magnitudes, as integers: of elements of one sign
+// these compare like the numbers, with infinity and then NaN above all others.
 __device__ __forceinline__ uint32_t max_magnitude2(uint32_t m, uint32_t x) {
   uint32_t r;
-  if constexpr (FP16) asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
-  else asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
   return r;
 }
 
-// Codes of 8 elements, x / scale rounded.  `inv`: 1 / scale where scale is a
-// power of two (then the product is exact), else 0.  `finite`: no infinity and
-// no NaN among them.
+// Codes of 8 elements, rounded from x * inv (scale = 1 / inv a power of two: the
+// product is exact).  `finite`: no infinity and no NaN among them.
 template <int KIND, bool FP16>
-__device__ __forceinline__ uint2 encode8(const uint4& x, float scale, float inv, bool finite) {
+__device__ __forceinline__ uint2 encode8(const uint4& x, float inv, bool finite) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t q[4];
-  if (KIND == BSA_CACHE_INT8 && inv != 0.f && finite) {
-    // x / scale + 1.5 * 2^23: the sum's last byte is the integer, rounded to
-    // nearest even (|x / scale| <= 127 by the scale's choice).
+  if (KIND == BSA_CACHE_INT8 && finite) {
+    // x * inv + 1.5 * 2^23: the sum's last byte is the integer, rounded to
+    // nearest even (|x * inv| <= 127 by the scale's choice).
     uint32_t b[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -51,12 +51,55 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float scale, float inv,
     return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
                       __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
   }
+  uint32_t q[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 f = elems_to_float2(w[e], FP16);
-    q[e] = inv != 0.f ? encode2<KIND>(f.x * inv, f.y * inv) : encode2<KIND>(f.x / scale, f.y / scale);
+    q[e] = encode2<KIND>(f.x * inv, f.y * inv);
   }
   return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
+
+// The same for a scale that is no power of two (a cache filled by others).
+template <int KIND, bool FP16>
+__device__ __noinline__ uint2 encode8_div(uint4 x, float scale) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = elems_to_float2(w[e], FP16);
+    q[e] = encode2<KIND>(f.x / scale, f.y / scale);
+  }
+  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
+
+// 8 codes moved from scale `was` to `scale`.
+template <int KIND>
+__device__ __noinline__ uint2 recode8(uint2 old, float ratio) {
+  uint32_t q[4];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint2 hh = codes_to_half4<KIND>(e ? old.y : old.x);
+    const float2 f0 = half2_to_float2(hh.x), f1 = half2_to_float2(hh.y);
+    q[2 * e] = encode2<KIND>(f0.x * ratio, f0.y * ratio);
+    q[2 * e + 1] = encode2<KIND>(f1.x * ratio, f1.y * ratio);
+  }
+  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
+
+// Largest finite magnitude of a thread's elements where some are not finite.
+template <bool FP16>
+__device__ __noinline__ float finite_max(uint4 x0, uint4 x1, uint4 x2, uint4 x3) {
+  const uint32_t w[16] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w,
+                          x2.x, x2.y, x2.z, x2.w, x3.x, x3.y, x3.z, x3.w};
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float2 f = elems_to_float2(w[e], FP16);
+    if (fabsf(f.x) < INFINITY) m = fmaxf(m, fabsf(f.x));
+    if (fabsf(f.y) < INFINITY) m = fmaxf(m, fabsf(f.y));
+  }
+  return m;
 }
 
 // Grid: (rows x blocks, parts); a CTA takes the units [part U / parts,
@@ -90,21 +133,31 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
   int u = (int)((long long)blockIdx.y * U / gridDim.y) + unit_in;
   const int steps = (u1 - (u - unit_in) + upi - 1) / upi;
 
-  // This thread's chunks: row of the block and column, the same in every unit.
-  const int cols = c.d / 8;
-  int r[kVec];
-  const int col = ut % cols;  // (tpu is a multiple of d / 8 or d / 8 a multiple of it: see below)
+  // This thread's chunks, the same in every unit: chunk j is row (j tpu + ut) /
+  // (d / 8) of the block (tpu is a multiple of d / 8, so all have one column).
+  const int cols = c.d / 8, row0 = ut / cols, rows_j = tpu / cols;
+  unsigned fresh = 0, old = 0;  // bit j: a new token, another token of the sequence
+  const int held = min(b0 + c.sb, len);
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) r[j] = (j * tpu + ut) / cols;
+  for (int j = 0; j < kVec; ++j) {
+    const int t = b0 + row0 + j * rows_j;
+    if (t >= lo && t < hi) fresh |= 1u << j;
+    else if (t < held) old |= 1u << j;
+  }
+  const long long first_row = (long long)(b0 - pos + row0);
+  const int col = (ut - row0 * cols) * 8;
+  const uint16_t* kp = p.k.p + (long long)row * p.k.sb + first_row * p.k.st + col;
+  const uint16_t* vp = p.v.p + (long long)row * p.v.sb + first_row * p.v.st + col;
+  const long long kstep = rows_j * p.k.st, vstep = rows_j * p.v.st;
   auto load = [&](int unit, uint4 (&x)[kVec]) {
-    const CacheRows& src = unit < c.Hkv ? p.k : p.v;
-    const uint16_t* base = src.p + (long long)row * src.sb + (long long)(unit < c.Hkv ? unit : unit - c.Hkv) * src.sh +
-                           (long long)(b0 - pos) * src.st + col * 8;
+    const bool isv = unit >= c.Hkv;
+    const uint16_t* at = isv ? vp + (unit - c.Hkv) * p.v.sh : kp + unit * p.k.sh;
+    const long long step = isv ? vstep : kstep;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       x[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (unit < u1 && b0 + r[j] >= lo && b0 + r[j] < hi)
-        x[j] = __ldcs(reinterpret_cast<const uint4*>(base + (long long)r[j] * src.st));
+      if (unit < u1 && (fresh >> j & 1u)) x[j] = __ldcs(reinterpret_cast<const uint4*>(at));
+      at += step;
     }
   };
   uint4 x[kVec];
@@ -115,38 +168,28 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
     return;
   }
   // Other tokens of the sequence in this block: below lo, or from hi on.
-  const int held = min(b0 + c.sb, len);
   const bool others = lo > b0 || hi < held;
+  const int per_page = c.page / c.sb, sub = (b0 & (c.page - 1)) / c.sb;
+  const size_t page_bytes = (size_t)c.page * c.d, block0 = (size_t)(b0 & (c.page - 1)) * c.d + ut * 8;
+  const size_t heads0 = (size_t)phys * c.Hkv;
 
   for (int step = 0; step < steps; ++step, u += upi) {
-    const bool active = u < u1;
-    const bool isv = u >= c.Hkv;
-    const size_t head = (size_t)phys * c.Hkv + (isv ? u - c.Hkv : u);
-    float* scale_p = (isv ? c.vs : c.ks) + head * (c.page / c.sb) + (b0 & (c.page - 1)) / c.sb;
+    const bool active = u < u1, isv = u >= c.Hkv;
+    const size_t head = heads0 + (isv ? u - c.Hkv : u);
+    float* scale_p = (isv ? c.vs : c.ks) + head * per_page + sub;
     const float was = active && others ? *scale_p : 0.f;
     uint4 next[kVec];
     load(u + upi, next);
     uint32_t m2 = 0u;
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
-      m2 = max_magnitude2<FP16>(max_magnitude2<FP16>(max_magnitude2<FP16>(max_magnitude2<FP16>(m2, x[j].x), x[j].y), x[j].z), x[j].w);
-    const float2 mm = elems_to_float2(m2, FP16);
-    float amax = fmaxf(mm.x, mm.y);
-    if (amax == INFINITY) {  // rare: the finite elements alone decide
-      amax = 0.f;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = elems_to_float2(w[e], FP16);
-          if (fabsf(f.x) < INFINITY) amax = fmaxf(amax, fabsf(f.x));
-          if (fabsf(f.y) < INFINITY) amax = fmaxf(amax, fabsf(f.y));
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      m2 = max_magnitude2(max_magnitude2(max_magnitude2(max_magnitude2(m2, x[j].x), x[j].y), x[j].z), x[j].w);
+    constexpr uint32_t inf = FP16 ? 0x7c00u : 0x7f80u;
+    m2 = max(m2 & 0xffffu, m2 >> 16);
+    const bool finite = m2 < inf;
+    float mine = elems_to_float2(m2, FP16).x;
+    if (!finite) mine = finite_max<FP16>(x[0], x[1], x[2], x[3]);  // rare
+    float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));  // (not negative)
     if (tpu > 32) {
       // (the other half of s_max may still be read by a warp one step behind)
       if (lane == 0) s_max[step & 1][warp] = amax;
@@ -159,37 +202,26 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
     if (active) {
       float scale = scale_for<KIND>(amax);
       if (others) scale = fmaxf(scale, was);
-      const float inv = (__float_as_uint(scale) & 0x7fffffu) == 0 ? 1.f / scale : 0.f;
       const bool grown = others && scale != was;
       if (ut == 0 && (!others || grown)) *scale_p = scale;
-      uint8_t* codes = (isv ? c.v : c.k) + (head * c.page + (b0 & (c.page - 1))) * (size_t)c.d + col * 8;
+      uint8_t* at = (isv ? c.v : c.k) + head * page_bytes + block0;
+      if ((__float_as_uint(scale) & 0x7fffffu) == 0) {
+        const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 2^-e of 2^e
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        uint2* at = reinterpret_cast<uint2*>(codes + (size_t)r[j] * c.d);
-        if (b0 + r[j] >= lo && b0 + r[j] < hi) {
-          // Infinities and NaN have all exponent bits set.
-          bool finite = true;
-          if (KIND == BSA_CACHE_INT8) {
-            const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-            constexpr uint32_t ex = FP16 ? 0x7c00u : 0x7f80u;
+        for (int j = 0; j < kVec; ++j)
+          if (fresh >> j & 1u) *reinterpret_cast<uint2*>(at + j * tpu * 8) = encode8<KIND, FP16>(x[j], inv, finite);
+      } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) finite = finite && (w[e] & ex) != ex && (w[e] & ex << 16) != ex << 16;
+        for (int j = 0; j < kVec; ++j)
+          if (fresh >> j & 1u) *reinterpret_cast<uint2*>(at + j * tpu * 8) = encode8_div<KIND, FP16>(x[j], scale);
+      }
+      if (grown && old) {  // the codes of the other tokens move to the larger scale
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          if (old >> j & 1u) {
+            uint2* o = reinterpret_cast<uint2*>(at + j * tpu * 8);
+            *o = recode8<KIND>(*o, was / scale);
           }
-          *at = encode8<KIND, FP16>(x[j], scale, inv, finite);
-        } else if (grown && b0 + r[j] < held) {
-          // Another token of the sequence: its codes move to the larger scale.
-          const uint2 old = *at;
-          const float ratio = was / scale;
-          uint32_t q[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint2 hh = codes_to_half4<KIND>(e ? old.y : old.x);
-            const float2 f0 = half2_to_float2(hh.x), f1 = half2_to_float2(hh.y);
-            q[2 * e] = encode2<KIND>(f0.x * ratio, f0.y * ratio);
-            q[2 * e + 1] = encode2<KIND>(f1.x * ratio, f1.y * ratio);
-          }
-          *at = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-        }
       }
     }
 #pragma unroll
@@ -205,10 +237,11 @@ cudaError_t launch_cache_append(const CacheAppendParams& p, int sms, cudaStream_
   const int threads = tpu < 256 ? 256 : tpu;
   const long long gx = (long long)p.n * p.blocks;
   if (gx > 0x7fffffffll) return cudaErrorInvalidValue;
-  // Units of a (row, block) are spread over CTAs until there are about eight
-  // CTAs' worth of threads for each SM.
+  // Units of a (row, block) are spread over CTAs until there are about four CTAs
+  // of 256 threads for each SM, which is what fits: more only repeat the way to
+  // the page (eight: 23.7 us, four: 21.9 us for 6 x 4001 tokens of 16 heads).
   const int most = (2 * p.c.Hkv + threads / tpu - 1) / (threads / tpu);
-  const long long want = (8ll * sms * 256 / threads + gx - 1) / gx;
+  const long long want = (4ll * sms * 256 / threads + gx - 1) / gx;
   const int parts = (int)(want < 1 ? 1 : (want < most ? want : most));
   const dim3 grid((unsigned)gx, (unsigned)parts);
   if (p.c.kind == BSA_CACHE_INT8)

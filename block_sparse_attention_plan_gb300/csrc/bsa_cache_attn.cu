@@ -261,7 +261,7 @@ template <int D, int KIND, int NT>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = AttnCfg<D>;
   constexpr int TK = C::TK;
-  constexpr int KG = NT * D <= 64 ? 4 : (NT * D < 384 ? 2 : 1);  // groups of 16 keys whose scores are held at once
+  constexpr int KG = NT * D <= 64 ? 4 : (NT < 3 ? 2 : 1);  // groups of 16 keys whose scores are held at once
   extern __shared__ __align__(1024) uint8_t smem[];
   int* s_prefix = reinterpret_cast<int*>(smem + C::kOffMerge);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
