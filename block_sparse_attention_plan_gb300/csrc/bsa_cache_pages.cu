@@ -45,6 +45,23 @@ __device__ __forceinline__ int block_scan(int x, int* warp_s, int& total) {
 
 __device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
 
+// Bit q of the result: page p0 + q is held (16 pages, a multiple of 16 first).
+__device__ __forceinline__ unsigned held_pages(const CacheDev& c, int p0) {
+  unsigned bits = 0;
+  if (p0 + 16 <= c.num_pages && (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0) {
+    int4 r[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) r[q] = __ldcg(reinterpret_cast<const int4*>(c.refs + p0) + q);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      bits |= ((r[q].x > 0) | (r[q].y > 0) << 1 | (r[q].z > 0) << 2 | (r[q].w > 0) << 3) << (4 * q);
+  } else {
+    for (int q = 0; q < 16; ++q)
+      if (p0 + q < c.num_pages && __ldcg(c.refs + p0 + q) > 0) bits |= 1u << q;
+  }
+  return bits;
+}
+
 // One CTA.  Everything the decisions need is read once, into shared memory, so
 // that a step of a serving loop (a token more for each sequence, no page more)
 // is a chain of four reads: list, length, last page, its count.
@@ -180,19 +197,9 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
   // The lowest `total` free pages, in order: 16 pages per thread and step.
   int found = 0;
   for (int base = 0; base < c.num_pages && found < total; base += kThreads * 16) {
-    unsigned free_bits = 0;
     const int p0 = base + tid * 16;
-    if (p0 + 16 <= c.num_pages && (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0) {
-      int4 r[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) r[q] = __ldcg(reinterpret_cast<const int4*>(c.refs + p0) + q);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        free_bits |= ((r[q].x <= 0) | (r[q].y <= 0) << 1 | (r[q].z <= 0) << 2 | (r[q].w <= 0) << 3) << (4 * q);
-    } else {
-      for (int q = 0; q < 16; ++q)
-        if (p0 + q < c.num_pages && __ldcg(c.refs + p0 + q) <= 0) free_bits |= 1u << q;
-    }
+    const unsigned exist = p0 + 16 <= c.num_pages ? 0xffffu : (p0 >= c.num_pages ? 0u : (1u << (c.num_pages - p0)) - 1u);
+    unsigned free_bits = ~held_pages(c, p0) & exist;
     int here;
     int at = found + block_scan(__popc(free_bits), warp_s, here);
     while (free_bits && at < total) {
@@ -304,47 +311,48 @@ __global__ void __launch_bounds__(256) fork_kernel(const CacheDev c, const int32
 
 // One CTA.  The i-th held page at or past L goes to the i-th free page below
 // L; list_a gets the map of the moved pages (indexed by page), the pairs what
-// the copy kernel moves.
+// the copy kernel moves.  16 pages per thread and step; a pool of up to 16384
+// pages is read once, held in registers between the count and the lists.
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CacheDev c) {
   next_may_launch();
   wait_for_previous();
   __shared__ int warp_s[33];
   const int tid = threadIdx.x;
-  int live = 0;
-  for (int p = tid; p < c.num_pages; p += kThreads) live += c.refs[p] > 0;
+  constexpr int kStep = kThreads * 16;
+  const unsigned first = held_pages(c, tid * 16);
+  int live = __popc(first);
+  for (int base = kStep; base < c.num_pages; base += kStep) live += __popc(held_pages(c, base + tid * 16));
   int L;
   block_scan(live, warp_s, L);
   int holes = 0, moved = 0;
-  for (int base = 0; base < c.num_pages; base += kThreads * 4) {
-    const int p0 = base + tid * 4;
-    int r[4];
-    unsigned hole = 0, mover = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int p = p0 + q;
-      r[q] = p < c.num_pages ? c.refs[p] : 0;
-      if (p < c.num_pages && p < L && r[q] <= 0) hole |= 1u << q;
-      if (p >= L && r[q] > 0) mover |= 1u << q;
-    }
+  for (int base = 0; base < c.num_pages; base += kStep) {
+    const int p0 = base + tid * 16;
+    const unsigned held = base == 0 ? first : held_pages(c, p0);
+    // Pages of these 16 below L, and that exist.
+    const unsigned below = p0 + 16 <= L ? 0xffffu : (p0 >= L ? 0u : (1u << (L - p0)) - 1u);
+    unsigned hole = ~held & below, mover = held & ~below;
     // Holes lie below L and movers at or past it: one scan of both counts.
     int both;
-    int at = block_scan(__popc(hole) | __popc(mover) << 16, warp_s, both);
+    const int at = block_scan(__popc(hole) | __popc(mover) << 16, warp_s, both);
     int ha = holes + (at & 0xffff), ma = moved + (at >> 16);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (hole >> q & 1) c.pair_dst()[ha++] = p0 + q;
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (!(mover >> q & 1)) continue;
-      const int to = __ldcg(c.pair_dst() + ma);
-      c.pair_src()[ma++] = p0 + q;
-      c.list_a()[p0 + q] = to;
-      c.refs[to] = r[q];
-      c.refs[p0 + q] = 0;
+    while (hole) {
+      c.pair_dst()[ha++] = p0 + __ffs(hole) - 1;
+      hole &= hole - 1;
+    }
+    while (mover) {
+      c.pair_src()[ma++] = p0 + __ffs(mover) - 1;
+      mover &= mover - 1;
     }
     holes += both & 0xffff;
     moved += both >> 16;
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int i = tid; i < moved; i += kThreads) {
+    const int p = __ldcg(c.pair_src() + i), to = __ldcg(c.pair_dst() + i);
+    c.list_a()[p] = to;
+    c.refs[to] = __ldcg(c.refs + p);
+    c.refs[p] = 0;
   }
   if (tid == 0) {
     c.control[kCacheLive] = L;
