@@ -33,6 +33,7 @@ class RowsC(ctypes.Structure):
 
 
 _bound = None
+_calls = {}  # entry points by name, without the prefix
 
 
 def _library() -> ctypes.CDLL:
@@ -57,6 +58,7 @@ def _library() -> ctypes.CDLL:
         f = getattr(lib, "bsa_cache_" + name)
         f.restype = I
         f.argtypes = args
+        _calls[name] = f
     _bound = lib
     return lib
 
@@ -133,7 +135,7 @@ def cache_create(num_pages: int, heads: int, page_size: int, d: int, max_seqs: i
     scale = lambda: z(num_pages, heads, page_size // sb, dtype=torch.float32)
     c = Cache(pool(), pool(), scale(), scale(), z(max_seqs, max_pages, dtype=torch.int32),
               z(max_seqs, dtype=torch.int32), z(num_pages, dtype=torch.int32))
-    _call(c, "bsa_cache_init", c._ref, _stream(c, None))
+    _call(c, "init", c._ref, _stream(c, None))
     return c
 
 
@@ -147,16 +149,19 @@ def _stream(c: Cache, stream) -> int:
     return _raw_stream(c._index) if stream is None else stream.cuda_stream
 
 
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(c: Cache, name: str, *args) -> None:
     """One entry point, on the cache's device."""
-    f = getattr(_bound, name)
-    if torch.cuda.current_device() == c._index:
+    f = _calls[name]
+    if _device() == c._index:
         status = f(*args)
     else:
         with torch.cuda.device(c._index):
             status = f(*args)
     if status:
-        _check(status, name)
+        _check(status, "bsa_cache_" + name)
 
 
 def _list(c: Cache, t: Optional[torch.Tensor], name: str, n: Optional[int] = None) -> Optional[int]:
@@ -191,7 +196,7 @@ def cache_append(c: Cache, k: torch.Tensor, v: torch.Tensor, seqs: Optional[torc
         raise ValueError("k and v differ in shape or type")
     if h != c.heads or d != c.d:
         raise ValueError("k and v must be [n, Hkv, T, d] of the cache's Hkv and d")
-    _call(c, "bsa_cache_append", c._ref, _rows(c, k, "k"), _rows(c, v, "v"), _ELEMENTS[k.dtype],
+    _call(c, "append", c._ref, _rows(c, k, "k"), _rows(c, v, "v"), _ELEMENTS[k.dtype],
           _list(c, seqs, "seqs", n), _list(c, counts, "counts", n), _list(c, start, "start", n), n, T,
           _stream(c, stream))
 
@@ -232,7 +237,7 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
             c._workspace_bytes.clear()
         c._workspace_bytes[key] = need
     ws = torch.empty(max(need, 16), dtype=torch.uint8, device=c.device)
-    _call(c, "bsa_cache_attention", c._ref, qr, _rows(c, out, "out"), lse.data_ptr(), _ELEMENTS[q.dtype],
+    _call(c, "attention", c._ref, qr, _rows(c, out, "out"), lse.data_ptr(), _ELEMENTS[q.dtype],
           _list(c, seqs, "seqs", B), mptr, NKB, bk, B, Hq, nq, CACHE_CAUSAL if causal else 0,
           0.0 if scale is None else scale, ws.data_ptr(), need, _stream(c, stream))
     if stream is not None:
@@ -272,7 +277,7 @@ def cache_forward(p: Plan, c: Cache, q: torch.Tensor, seqs: Optional[torch.Tenso
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=c.device)
     elif ws.dtype != torch.uint8 or ws.device != c.device or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
-    _call(c, "bsa_cache_forward", p.handle, c._ref, _list(c, seqs, "seqs", L.B), q.data_ptr(),
+    _call(c, "forward", p.handle, c._ref, _list(c, seqs, "seqs", L.B), q.data_ptr(),
           (_lib.FWD_CAUSAL if causal else 0) | (_lib.FWD_SPLIT_P if split else 0), out.data_ptr(), lse.data_ptr(),
           0.0 if scale is None else scale, ws.data_ptr(), ws.numel(), _stream(c, stream))
     if workspace is None and stream is not None:
@@ -284,24 +289,24 @@ def cache_resize(c: Cache, new_lens: torch.Tensor, seqs: Optional[torch.Tensor] 
                  stream: Optional[torch.cuda.Stream] = None) -> None:
     """Set sequences' lengths, taking and giving back pages (bsa_cache_resize)."""
     n = new_lens.shape[0]
-    _call(c, "bsa_cache_resize", c._ref, _list(c, seqs, "seqs", n), _list(c, new_lens, "new_lens"), n, _stream(c, stream))
+    _call(c, "resize", c._ref, _list(c, seqs, "seqs", n), _list(c, new_lens, "new_lens"), n, _stream(c, stream))
 
 
 def cache_free(c: Cache, seqs: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Free sequences, all of them by default (bsa_cache_resize to length 0)."""
     n = c.max_seqs if seqs is None else seqs.shape[0]
-    _call(c, "bsa_cache_resize", c._ref, _list(c, seqs, "seqs"), None, n, _stream(c, stream))
+    _call(c, "resize", c._ref, _list(c, seqs, "seqs"), None, n, _stream(c, stream))
 
 
 def cache_fork(c: Cache, src: torch.Tensor, dst: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Let empty sequences dst[i] share the tokens of src[i] (bsa_cache_fork)."""
     n = src.shape[0]
-    _call(c, "bsa_cache_fork", c._ref, _list(c, src, "src"), _list(c, dst, "dst", n), n, _stream(c, stream))
+    _call(c, "fork", c._ref, _list(c, src, "src"), _list(c, dst, "dst", n), n, _stream(c, stream))
 
 
 def cache_compact(c: Cache, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Move the held pages to the front of the pools (bsa_cache_compact)."""
-    _call(c, "bsa_cache_compact", c._ref, _stream(c, stream))
+    _call(c, "compact", c._ref, _stream(c, stream))
 
 
 def cache_copy_pages(dst: Cache, src: Cache, dst_pages: torch.Tensor, src_pages: torch.Tensor,
@@ -311,7 +316,7 @@ def cache_copy_pages(dst: Cache, src: Cache, dst_pages: torch.Tensor, src_pages:
     if dst.device != src.device:
         raise ValueError("dst and src must be on one device")
     n = dst_pages.shape[0]
-    _call(dst, "bsa_cache_copy_pages", dst._ref, src._ref, _list(dst, dst_pages, "dst_pages"),
+    _call(dst, "copy_pages", dst._ref, src._ref, _list(dst, dst_pages, "dst_pages"),
           _list(dst, src_pages, "src_pages", n), n, _stream(dst, stream))
 
 

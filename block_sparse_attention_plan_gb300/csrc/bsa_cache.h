@@ -84,6 +84,10 @@ struct CacheAppendParams {
 
 // Queries per unit of work at most: four row tiles of 24.
 constexpr int kCacheUnitRows = 96;
+// What a unit's beginning (queries, joining the warps) costs a CTA, in tiles.  Measured for 0, 4, 8, 12,
+// 16, 24: 32 sequences of up to 32768 tokens 176, 170, 170, 170, 170, 172 us; 5 draft tokens of 16
+// sequences, INT8, d 64: 70, 67, 63, 62, 63, 65 us; 64 sequences of up to 700 tokens 34, 26, 25, 25, 24, 25 us.
+constexpr int kCacheUnitHead = 12;
 // Keys per tile: 4 KB of K and of V.
 constexpr int cache_tile_keys(int d) { return 4096 / d; }
 constexpr int kCacheMaxGrid = 320;   // most CTAs of the attention kernel (workspace bound)
@@ -103,6 +107,7 @@ struct CacheAttnParams {
   int32_t* desc;        // rows split over CTAs, for the combine kernel [grid][4]
   int fp16, B, Hq, g, nq, M, groups, NKB, bk, tile, max_tiles, causal;
   int rows_cap;         // query rows of a partial's slot
+  int head;             // places of the line that a unit's beginning counts for
   float scale_log2;
   long long watchdog_ns;
 };

@@ -82,7 +82,7 @@ bsa_status attn_layout(const CacheDev& c, int B, int Hq, int nq, int NKB, int bk
   }
   const long long groups = (M + kCacheUnitRows - 1) / kCacheUnitRows;
   if (M >= (1ll << 30) || (long long)B * Hq * nq >= (1ll << 31) ||
-      (double)B * c.Hkv * groups * tiles >= 2147483648.0 || (long long)B * c.Hkv > (1ll << 24))
+      (double)B * c.Hkv * groups * (tiles + kCacheUnitHead) >= 2147483648.0 || (long long)B * c.Hkv > (1ll << 24))
     return BSA_ERR_UNSUPPORTED;
   AttnLayout l;
   l.rows_cap = (int)(M < kCacheUnitRows ? M : kCacheUnitRows);
@@ -256,6 +256,7 @@ bsa_status bsa_cache_attention(const bsa_cache* cache, const bsa_rows* q, const 
   p.max_tiles = l.max_tiles;
   p.causal = flags & BSA_CACHE_CAUSAL ? 1 : 0;
   p.rows_cap = l.rows_cap;
+  p.head = kCacheUnitHead;
   const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)p.c.d);
   p.scale_log2 = (float)(sc * 1.4426950408889634);
   p.watchdog_ns = watchdog_limit_ns();

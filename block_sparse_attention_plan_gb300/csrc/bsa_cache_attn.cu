@@ -127,42 +127,49 @@ __device__ __forceinline__ int entry_tiles(const CacheAttnParams& p, int e) {
   return (len_of(p, e) + p.tile - 1) / p.tile;
 }
 
-// Walks the pieces of rows in tiles [lo, hi) of the line (fewer than 2^31 tiles:
-// checked on the host).
+// Walks the pieces of units in places [lo, hi) of the line (fewer than 2^31
+// places: checked on the host).  A unit has `head` places that hold no tile ahead
+// of those of its tiles: what beginning it costs a CTA, so that CTAs with few
+// beginnings get more tiles.
 struct Walk {
   int e, sub, cnt;   // entry, unit within it, its tiles
   int t0, t1;        // this piece: tiles [t0, t1) of the unit
-  int row0;          // first tile of the unit in the line
-  int at, hi;
+  int row0;          // place of the unit's first tile
+  int lo, hi;
 };
 __device__ __forceinline__ void walk_piece(Walk& w) {
-  w.t0 = w.at - w.row0;
-  w.t1 = min(w.cnt, w.t0 + w.hi - w.at);
+  w.t0 = max(w.lo - w.row0, 0);
+  w.t1 = min(w.cnt, w.hi - w.row0);
 }
-__device__ __forceinline__ void walk_start(const CacheAttnParams& p, Walk& w, int mult, int e, int base, int lo, int hi) {
-  w.at = lo;
-  w.hi = hi;
-  w.cnt = entry_tiles(p, e);
-  while (lo >= base + w.cnt * mult) {
-    base += w.cnt * mult;
-    w.cnt = entry_tiles(p, ++e);
-  }
-  w.e = e;
-  w.sub = (lo - base) / w.cnt;
-  w.row0 = base + w.sub * w.cnt;
-  walk_piece(w);
-}
-__device__ __forceinline__ bool walk_next(const CacheAttnParams& p, Walk& w, int mult) {
-  w.at += w.t1 - w.t0;
-  if (w.at >= w.hi) return false;
+// To the next unit with tiles in the piece; false when the piece ends.
+__device__ __forceinline__ bool walk_next(const CacheAttnParams& p, Walk& w, int mult, int head) {
   w.row0 += w.cnt;
+  if (w.row0 + head >= w.hi) return false;
   if (++w.sub == mult) {
     w.sub = 0;
     do w.cnt = entry_tiles(p, ++w.e);
     while (w.cnt == 0);
   }
+  w.row0 += head;
   walk_piece(w);
   return true;
+}
+// To the first unit of the piece.  `base`: place where entry e begins; it, or one
+// behind it, holds place lo.
+__device__ __forceinline__ bool walk_start(const CacheAttnParams& p, Walk& w, int mult, int head, int e, int base, int lo,
+                                           int hi) {
+  w.lo = lo;
+  w.hi = hi;
+  w.cnt = entry_tiles(p, e);
+  while (w.cnt == 0 || lo >= base + (w.cnt + head) * mult) {
+    if (w.cnt > 0) base += (w.cnt + head) * mult;
+    w.cnt = entry_tiles(p, ++e);
+  }
+  w.e = e;
+  w.sub = (lo - base) / (w.cnt + head);
+  w.row0 = base + w.sub * (w.cnt + head) + head;
+  walk_piece(w);
+  return w.t1 > w.t0 || walk_next(p, w, mult, head);  // (the piece may end in the head)
 }
 
 // Batch row, K/V head and group of query rows of a unit.
@@ -294,8 +301,16 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   const int mult = p.mask ? p.groups : p.c.Hkv * p.groups;
   const int per = (E + kAttnThreads - 1) / kAttnThreads;
   int sum = 0;
-  for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) sum += entry_tiles(p, e);
+  int units = 0;
+  for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) {
+    const int cnt = entry_tiles(p, e);
+    sum += cnt;
+    units += cnt > 0 ? 1 : 0;
+  }
   sum *= mult;
+  units *= mult;
+  const int head = p.head;
+  sum += head * units;
   int x = sum;  // inclusive prefix over the warp, then over the warps
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -312,9 +327,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   }
   s_prefix[tid] = x - sum;  // tiles before this thread's entries
   __syncthreads();
-  // A tile at least for each set of warps that shares one, so that short lines
-  // leave few parts to join.  No CTA that works has an empty piece: the parts of
-  // a row are those of consecutive CTAs.  The first `more_of` CTAs have a tile more.
+  // A few places at least for each CTA, so that short lines leave few parts to
+  // join; the first `more_of` CTAs have one more.  The CTAs that hold tiles of a
+  // unit are consecutive ones.
   const int G = min((T + KL - 1) / KL, (int)gridDim.x);
   const int share = G > 0 ? T / G : 0, more_of = T - share * G;
   const int lo = cta < G ? cta * share + min(cta, more_of) : 0;
@@ -344,8 +359,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     else z = m;
   }
   Walk w;
-  walk_start(p, w, mult, a * per, s_prefix[a], lo, hi);
+  bool more = walk_start(p, w, mult, head, a * per, s_prefix[a], lo, hi);
   __syncthreads();  // the prefix gives way to the merge buffer
+  if (!more) return;
 
   // ------------------------------------------------------------- computation
   const int g = lane >> 2, t4 = lane & 3;
@@ -377,7 +393,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     }
   };
   load_q(unit_of(p, w.e, w.sub));
-  bool later = false;
 
   // ---------------------------------------------------------------- requests
   const int lpage = 31 - __clz(p.c.page), lsb = 31 - __clz(p.c.sb);
@@ -385,9 +400,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   const int lcs = 31 - __clz(cs), nc = TK >> lcs;
   // Read once, unless other row tiles or groups of rows come back for it.
   const uint64_t pol = R == 1 && p.groups == 1 ? policy_evict_first() : policy_evict_normal();
-  // First tile of a piece that is this warp's: tile t of the CTA's line is taken
-  // by the warps with kl = t mod KL.
-  auto first_of = [&](const Walk& x) { return x.t0 + ((kl - (x.at - lo)) & (KL - 1)); };  // (KL is 1, 2 or 4)
+  // First tile of a piece that is this warp's: the tile at place t of the line is
+  // taken by the warps with kl = t mod KL.
+  auto first_of = [&](const Walk& x) { return x.t0 + ((kl - (x.row0 + x.t0)) & (KL - 1)); };  // (KL is 1, 2 or 4)
   Feed f;
   f.w = w;
   f.pos = first_of(w);
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
   auto refill = [&]() {
     f.pos += f.n * KL;
     while (f.pos >= f.w.t1) {
-      if (!walk_next(p, f.w, mult)) {
+      if (!walk_next(p, f.w, mult, head)) {
         f.more = false;
         return;
       }
@@ -488,12 +503,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
 
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* ml = reinterpret_cast<float*>(smem + C::kOffMl);
-  bool more = true, ok = true;
+  bool ok = true;
   while (more) {
     const Unit u = unit_of(p, w.e, w.sub);
     const int len = len_of(p, u.b);
-    if (later) load_q(u);
-    later = true;
     const int m0 = u.grp * kCacheUnitRows + rt * 8 * NT;  // first query row of this warp
     // Query fragments: lane (g, t4) holds row 8 nt + g, elements 4 a word of codes.
     uint32_t qf[NT][KS][2];
@@ -776,6 +789,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     // ---- end of the piece: join the warps that took its tiles, 8 rows of each
     // warp at a time
     const bool starts = w.t0 == 0, whole = starts && w.t1 == w.cnt;
+    Walk after = w;
+    more = walk_next(p, after, mult, head);
+    if (more) load_q(unit_of(p, after.e, after.sub));  // the next piece's queries, ahead of the barriers
     const int rows = min(p.M - u.grp * kCacheUnitRows, kCacheUnitRows);
     float* part = p.part + (size_t)(2 * cta + (starts ? 1 : 0)) * p.rows_cap * (D + 2);
 #pragma unroll
@@ -840,7 +856,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       *reinterpret_cast<int4*>(p.desc + 4 * cta) = make_int4(c1 - cta + 1, u.b, u.h, u.grp);
     }
     named_bar_sync(1, 32 * kWarps);
-    more = walk_next(p, w, mult);
+    w = after;
   }
   if (!ok) {
     // Let the tiles in flight land before the CTA's shared memory goes away.
