@@ -220,6 +220,12 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
                 or mask.shape[:2] != q.shape[:2] or not mask.is_contiguous()):
             raise ValueError("mask must be a contiguous CUDA uint8 tensor [B, Hq, NKB]")
         NKB, mptr = mask.shape[2], mask.data_ptr()
+        if NKB == 0:
+            raise ValueError("mask has no key blocks")
+    if stream is not None and (out is None or lse is None):
+        with torch.cuda.stream(stream):  # memory that this stream may write
+            out = torch.empty_like(q) if out is None else out
+            lse = torch.empty((B, Hq, nq), dtype=torch.float32, device=c.device) if lse is None else lse
     if out is None:
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
@@ -236,20 +242,20 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
         if len(c._workspace_bytes) > 256:
             c._workspace_bytes.clear()
         c._workspace_bytes[key] = need
-    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=c.device)
+    ws = _scratch(c, need, stream)
     _call(c, "attention", c._ref, qr, _rows(c, out, "out"), lse.data_ptr(), _ELEMENTS[q.dtype],
           _list(c, seqs, "seqs", B), mptr, NKB, bk, B, Hq, nq, CACHE_CAUSAL if causal else 0,
           0.0 if scale is None else scale, ws.data_ptr(), need, _stream(c, stream))
-    if stream is not None:
-        _used_on(ws, stream)
     return out, lse
 
 
-def _used_on(ws: torch.Tensor, stream: torch.cuda.Stream) -> None:
-    """A workspace that a call on another stream still uses goes back to the
-    allocator only after it."""
-    if stream != torch.cuda.current_stream(ws.device):
-        ws.record_stream(stream)
+def _scratch(c: Cache, need: int, stream) -> torch.Tensor:
+    """Memory for one call, of the stream's own: what it held before, and what
+    will hold it next, are in order with the call."""
+    if stream is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=c.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=c.device)
 
 
 def cache_forward(p: Plan, c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = None, causal: bool = False,
@@ -267,6 +273,10 @@ def cache_forward(p: Plan, c: Cache, q: torch.Tensor, seqs: Optional[torch.Tenso
     for name, t, dtype, shape in (("out", out, torch.bfloat16, q.shape), ("lse", lse, torch.float32, q.shape[:3])):
         if t is not None and (t.dtype != dtype or t.device != c.device or t.shape != shape or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {list(shape)}")
+    if stream is not None and (out is None or lse is None):
+        with torch.cuda.stream(stream):  # memory that this stream may write
+            out = torch.empty_like(q) if out is None else out
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if lse is None else lse
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
@@ -274,14 +284,12 @@ def cache_forward(p: Plan, c: Cache, q: torch.Tensor, seqs: Optional[torch.Tenso
     need = int(_bound.bsa_cache_forward_workspace_bytes(p.handle, c._ref))
     ws = workspace
     if ws is None:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=c.device)
+        ws = _scratch(c, need, stream)
     elif ws.dtype != torch.uint8 or ws.device != c.device or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     _call(c, "forward", p.handle, c._ref, _list(c, seqs, "seqs", L.B), q.data_ptr(),
           (_lib.FWD_CAUSAL if causal else 0) | (_lib.FWD_SPLIT_P if split else 0), out.data_ptr(), lse.data_ptr(),
           0.0 if scale is None else scale, ws.data_ptr(), ws.numel(), _stream(c, stream))
-    if workspace is None and stream is not None:
-        _used_on(ws, stream)
     return out, lse
 
 

@@ -136,7 +136,7 @@ bsa_status bsa_cache_resize(const bsa_cache* cache, const int32_t* seqs, const i
   bsa_status st = check_cache(cache, &c);
   if (st != BSA_OK) return st;
   if (n < 1 || !list_ok(seqs) || !list_ok(new_lens) || (!seqs && n > c.max_seqs)) return BSA_ERR_INVALID_ARG;
-  if (n > kCacheListMax) return BSA_ERR_UNSUPPORTED;
+  if (n > kCacheListMax && (seqs || new_lens)) return BSA_ERR_UNSUPPORTED;
   if ((st = check_device(nullptr)) != BSA_OK) return st;
   return launch_cache_resize(c, seqs, new_lens, n, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK
                                                                                                      : BSA_ERR_CUDA;

@@ -120,6 +120,14 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
   const int len = known ? __ldg(c.lens + seq) : 0;
   const int pos = p.start ? given : len - count;
   const bool first = blk == 0 && blockIdx.y == 0 && tid == 0;
+  if (p.seqs) {  // a sequence named before: two rows would write one block
+    bool twice = false;
+    for (int j = tid; j < row; j += blockDim.x) twice |= __ldg(p.seqs + j) == seq;
+    if (__syncthreads_or(twice && seq != -1)) {
+      if (first) cache_error(c.control, BSA_ERR_INVALID_ARG, row);
+      return;
+    }
+  }
   // Counts out of [0, T], tokens out of [0, len) or a sequence out of range.
   bool good = known && count >= 0 && count <= p.T && len <= c.max_pages * c.page;
   if (good && count > 0) good = pos >= 0 && pos <= len - count;

@@ -565,7 +565,8 @@ bsa_status bsa_cache_status(const bsa_cache* cache, void* stream, int32_t* detai
  * contents copied (of several such sequences in one call, those later in the
  * list come last, and the one that is left alone with the page keeps it).
  * New tokens' contents are what bsa_cache_append then stores.  If the free
- * pages do not suffice nothing is changed.  n <= 4096.
+ * pages do not suffice nothing is changed.  n <= 4096 (any n if both lists are
+ * NULL).
  * Two kernels (one if new_lens is NULL), no synchronisation.
  */
 bsa_status bsa_cache_resize(const bsa_cache* cache, const int32_t* seqs, const int32_t* new_lens,
@@ -604,7 +605,9 @@ bsa_status bsa_cache_copy_pages(const bsa_cache* dst, const bsa_cache* src, cons
  * bsa_cache_append -- quantise tokens and store them in the cache, in pages
  * the sequences hold already (bsa_cache_resize first).
  * k, v: [n][Hkv][T][d] of `dtype` (BSA_BF16 / BSA_FP16).
- * seqs: device int32 [n] or NULL (sequences 0 .. n-1); each at most once.
+ * seqs: device int32 [n] or NULL (sequences 0 .. n-1); each at most once (a
+ *   later row that names it again is skipped and recorded,
+ *   BSA_ERR_INVALID_ARG).
  * counts: device int32 [n] or NULL (all T): how many of the T tokens of each
  *   row are stored (the first ones; 0 .. T).
  * start: device int32 [n] or NULL: position of the first one; NULL = the

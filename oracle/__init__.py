@@ -22,7 +22,12 @@ Modules:
   plus the GQA per-group union table ("CompactAttention", summary: Q-block
   union + intra-group union build a per-group KV block table).
 
+* ``oracle.cache`` -- the paged K/V cache in 8 bits as a model of its state:
+  page bookkeeping, appending (block scales, rounding), attention over the
+  stored values.
+
 Pins (what each part is checked against, other than itself) are listed in each
-module's docstring.  Parity status: attention -- pinned; plan -- pinned.
+module's docstring or its test file.  Parity status: attention -- pinned;
+plan -- pinned; cache -- pinned.
 """
-from . import attention, plan  # noqa: F401
+from . import attention, cache, plan  # noqa: F401

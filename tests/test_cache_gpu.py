@@ -214,6 +214,12 @@ def test_append_of_special_values_strides_and_positions(bsa, kind):
         bsa.cache_append(c, one, one, **kw)
         assert bsa.cache_status(c) == (st, 0), kw
         assert_state(c, m)
+    # A sequence named twice: the first row counts.
+    two = rand(g, 3, 2, 1, 64)
+    bsa.cache_append(c, two.cuda(), two.cuda(), seqs=i32(3, 1, 3))
+    m.append(two[:2].double().numpy(), two[:2].double().numpy(), seqs=[3, 1])
+    assert bsa.cache_status(c) == (-1, 2)
+    assert_state(c, m)
     c.block_table[0, 2] = 12
     bsa.cache_append(c, one, one)
     assert bsa.cache_status(c) == (-7, 0)
@@ -561,6 +567,38 @@ def test_two_streams_read_one_cache(bsa):
         assert torch.equal(y[0], b[0]) and torch.equal(y[1], b[1])
 
 
+def test_calls_on_another_stream_use_memory_of_their_own(bsa):
+    """Results and scratch of calls on a given stream are that stream's memory:
+    work that is still queued on the current stream cannot run into them."""
+    m, c = filled(bsa, [2500, 700], 2, 64, 64, 64, "int8", 40, seed=4)
+    gen = torch.Generator().manual_seed(4)
+    q = rand(gen, 2, 8, 1, 64).cuda()
+    want = bsa.cache_attention(c, q)
+    p = bsa.plan(torch.ones(2, 8, 1, 20, dtype=torch.uint8, device="cuda"), 128, 128, 4)
+    q2 = rand(gen, 2, 8, 128, 64).cuda()
+    want2 = bsa.cache_forward(p, c, q2)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        busy = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+        for _ in range(20):
+            busy.fill_(255)          # queued on the current stream ...
+        del busy                     # ... whose memory is free to be handed out there
+        got, got2 = bsa.cache_attention(c, q, stream=side), bsa.cache_forward(p, c, q2, stream=side)
+        torch.cuda.synchronize()
+        for x, y in zip(got + got2, want + want2):
+            assert torch.equal(x, y)
+
+
+def test_free_of_every_sequence(bsa):
+    c = bsa.cache_create(64, 1, 16, 64, 5000, 2)
+    bsa.cache_resize(c, torch.full((60,), 16, dtype=torch.int32, device="cuda"))
+    assert int((c.refs > 0).sum()) == 60
+    bsa.cache_free(c)
+    assert bsa.cache_status(c) == (0, 0)
+    assert not c.refs.any() and not c.lens.any() and (c.block_table == -1).all()
+
+
 def test_argument_errors(bsa):
     m, c = filled(bsa, [10], 2, 32, 32, 64, "e4m3", 1, seed=3)
     q = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
@@ -586,6 +624,8 @@ def test_argument_errors(bsa):
     with pytest.raises(bsa.BsaError):                          # rows that start off a 16-byte boundary
         x = torch.zeros(1, 2, 1, 72, dtype=torch.bfloat16, device="cuda")[..., 4:68]
         bsa.cache_append(c, x, x)
+    with pytest.raises(ValueError):
+        bsa.cache_attention(c, q, mask=torch.ones(1, 4, 0, dtype=torch.uint8, device="cuda"), bk=64)
     for bad in (dict(page_size=24), dict(page_size=8), dict(page_size=512), dict(d=96), dict(scale_block=8)):
         with pytest.raises((bsa.BsaError, ValueError)):
             bsa.cache_create(**{**dict(num_pages=4, heads=1, page_size=32, d=64, max_seqs=1, max_pages=1), **bad})
