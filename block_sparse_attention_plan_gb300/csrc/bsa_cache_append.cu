@@ -15,6 +15,8 @@
 // With power-of-two scales x / scale is exact, codes move to a larger scale
 // without a second rounding (subnormal codes excepted), and both code types
 // times their scale are exact in bf16 and fp16 products.
+#include <type_traits>
+
 #include "bsa_cache.h"
 #include "bsa_cache_codes.cuh"
 
@@ -104,7 +106,9 @@ __device__ __noinline__ float finite_max(uint4 x0, uint4 x1, uint4 x2, uint4 x3)
 
 // Grid: (rows x blocks, parts); a CTA takes the units [part U / parts,
 // (part + 1) U / parts) of its (row, block), U = 2 Hkv, blockDim / tpu at once.
-template <int KIND, bool FP16>
+// LIST: the sequences are given in a list, in which none may appear twice (an
+// instantiation of its own: the search costs the others a microsecond).
+template <int KIND, bool FP16, bool LIST>
 __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ CacheAppendParams p, int tpu) {
   __shared__ float s_max[2][32];
   next_may_launch();
@@ -113,21 +117,21 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int unit_in = tid / tpu, ut = tid - unit_in * tpu;
   const int row = blockIdx.x / p.blocks, blk = blockIdx.x - row * p.blocks;
-  const int seq = p.seqs ? __ldg(p.seqs + row) : row;
+  const int seq = LIST ? __ldg(p.seqs + row) : row;
+  if constexpr (LIST) {
+    bool twice = false;  // named by an earlier row: both would write one block
+    for (int j = tid; j < row; j += blockDim.x) twice |= __ldg(p.seqs + j) == seq;
+    if (__syncthreads_or(twice && seq != -1)) {
+      if (blk == 0 && blockIdx.y == 0 && tid == 0) cache_error(c.control, BSA_ERR_INVALID_ARG, row);
+      return;
+    }
+  }
   const int count = p.counts ? __ldg(p.counts + row) : p.T;
   const int given = p.start ? __ldg(p.start + row) : 0;
   const bool known = seq >= 0 && seq < c.max_seqs;
   const int len = known ? __ldg(c.lens + seq) : 0;
   const int pos = p.start ? given : len - count;
   const bool first = blk == 0 && blockIdx.y == 0 && tid == 0;
-  if (p.seqs) {  // a sequence named before: two rows would write one block
-    bool twice = false;
-    for (int j = tid; j < row; j += blockDim.x) twice |= __ldg(p.seqs + j) == seq;
-    if (__syncthreads_or(twice && seq != -1)) {
-      if (first) cache_error(c.control, BSA_ERR_INVALID_ARG, row);
-      return;
-    }
-  }
   // Counts out of [0, T], tokens out of [0, len) or a sequence out of range.
   bool good = known && count >= 0 && count <= p.T && len <= c.max_pages * c.page;
   if (good && count > 0) good = pos >= 0 && pos <= len - count;
@@ -152,15 +156,16 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
     if (t >= lo && t < hi) fresh |= 1u << j;
     else if (t < held) old |= 1u << j;
   }
-  const long long first_row = (long long)(b0 - pos + row0);
+  const int first_row = b0 - pos + row0;  // (of the tensor; below 0 where the tokens begin in the block)
   const int col = (ut - row0 * cols) * 8;
-  const uint16_t* kp = p.k.p + (long long)row * p.k.sb + first_row * p.k.st + col;
-  const uint16_t* vp = p.v.p + (long long)row * p.v.sb + first_row * p.v.st + col;
-  const long long kstep = rows_j * p.k.st, vstep = rows_j * p.v.st;
+  // (addresses are built anew for each unit: kept, they cost the registers that
+  // let four CTAs share an SM without spills)
   auto load = [&](int unit, uint4 (&x)[kVec]) {
     const bool isv = unit >= c.Hkv;
-    const uint16_t* at = isv ? vp + (unit - c.Hkv) * p.v.sh : kp + unit * p.k.sh;
-    const long long step = isv ? vstep : kstep;
+    const CacheRows& src = isv ? p.v : p.k;
+    const uint16_t* at = src.p + (long long)row * src.sb + (long long)(isv ? unit - c.Hkv : unit) * src.sh +
+                         (long long)first_row * src.st + col;
+    const long long step = (long long)rows_j * src.st;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       x[j] = make_uint4(0u, 0u, 0u, 0u);
@@ -177,14 +182,12 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
   }
   // Other tokens of the sequence in this block: below lo, or from hi on.
   const bool others = lo > b0 || hi < held;
-  const int per_page = c.page / c.sb, sub = (b0 & (c.page - 1)) / c.sb;
-  const size_t page_bytes = (size_t)c.page * c.d, block0 = (size_t)(b0 & (c.page - 1)) * c.d + ut * 8;
-  const size_t heads0 = (size_t)phys * c.Hkv;
+  const int lsb = 31 - __clz(c.sb), in_page = b0 & (c.page - 1);
 
   for (int step = 0; step < steps; ++step, u += upi) {
     const bool active = u < u1, isv = u >= c.Hkv;
-    const size_t head = heads0 + (isv ? u - c.Hkv : u);
-    float* scale_p = (isv ? c.vs : c.ks) + head * per_page + sub;
+    const size_t first = ((size_t)phys * c.Hkv + (isv ? u - c.Hkv : u)) * c.page + in_page;  // row of the pool
+    float* scale_p = (isv ? c.vs : c.ks) + (first >> lsb);
     const float was = active && others ? *scale_p : 0.f;
     uint4 next[kVec];
     load(u + upi, next);
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
       if (others) scale = fmaxf(scale, was);
       const bool grown = others && scale != was;
       if (ut == 0 && (!others || grown)) *scale_p = scale;
-      uint8_t* at = (isv ? c.v : c.k) + head * page_bytes + block0;
+      uint8_t* at = (isv ? c.v : c.k) + first * c.d + ut * 8;
       if ((__float_as_uint(scale) & 0x7fffffu) == 0) {
         const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 2^-e of 2^e
 #pragma unroll
@@ -252,11 +255,18 @@ cudaError_t launch_cache_append(const CacheAppendParams& p, int sms, cudaStream_
   const long long want = (4ll * sms * 256 / threads + gx - 1) / gx;
   const int parts = (int)(want < 1 ? 1 : (want < most ? want : most));
   const dim3 grid((unsigned)gx, (unsigned)parts);
-  if (p.c.kind == BSA_CACHE_INT8)
-    return launch_after(p.fp16 ? append_kernel<BSA_CACHE_INT8, true> : append_kernel<BSA_CACHE_INT8, false>, grid,
-                        dim3(threads), 0, s, p, tpu);
-  return launch_after(p.fp16 ? append_kernel<BSA_CACHE_E4M3, true> : append_kernel<BSA_CACHE_E4M3, false>, grid,
-                      dim3(threads), 0, s, p, tpu);
+  auto kernel = [&](auto kind, auto fp16) {
+    constexpr int K = decltype(kind)::value;
+    constexpr bool F = decltype(fp16)::value;
+    return p.seqs ? append_kernel<K, F, true> : append_kernel<K, F, false>;
+  };
+  using std::integral_constant;
+  auto of_kind = [&](auto kind) {
+    return p.fp16 ? kernel(kind, std::true_type{}) : kernel(kind, std::false_type{});
+  };
+  return launch_after(p.c.kind == BSA_CACHE_INT8 ? of_kind(integral_constant<int, BSA_CACHE_INT8>{})
+                                                 : of_kind(integral_constant<int, BSA_CACHE_E4M3>{}),
+                      grid, dim3(threads), 0, s, p, tpu);
 }
 
 }  // namespace bsa
