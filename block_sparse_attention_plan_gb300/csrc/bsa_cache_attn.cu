@@ -700,15 +700,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
           }
           f2_split(l2, l_sum[nt][0], l_sum[nt][1]);
         }
-        // ---- O^T += S_v V^T P^T: the 16 keys of a group lie in one scale block;
-        // groups that follow each other with the same scale share the addition
+        // ---- O^T += S_v V^T P^T: the 16 keys of a group lie in one scale block
+        // (One addition for groups that have the same scale would save a tenth of
+        // the instructions, but the second path's code costs more than that.)
         float sv[KG];
         uint32_t v[KG][4][DV / 4];
-        bool same = true;
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg) {
           sv[kg] = __shfl_sync(0xffffffffu, sq[0], C::kGroups + kb16 / 16 + kg);
-          same = same && sv[kg] == sv[0];
           const int ra = kb16 + 16 * kg + 2 * t4;  // keys 2 t4, + 1, + 8, + 9 of the 16
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -732,42 +731,33 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
           }
           if constexpr (KIND == BSA_CACHE_E4M3 && kMasked) take_nans<NT, DV, MT>(v[kg], o, kept, kg);
         }
-        auto accumulate = [&](float (&acc)[4], float f, const float (&y)[4]) {
-          const uint64_t ff = f2_make(f, f);
-          f2_split(ffma2(ff, f2_make(y[0], y[1]), f2_make(acc[0], acc[1])), acc[0], acc[1]);
-          f2_split(ffma2(ff, f2_make(y[2], y[3]), f2_make(acc[2], acc[3])), acc[2], acc[3]);
-        };
         // Pairs of keys of one element: {a0 b0 a1 b1}, {a2 b2 a3 b3}.
-        auto products = [&](auto one_scale) {
 #pragma unroll
-          for (int q = 0; q < DV / 4; ++q) {
+        for (int q = 0; q < DV / 4; ++q) {
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              float y[NT][4];
+          for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
-              for (int kg = 0; kg < KG; ++kg) {
-                const uint32_t pick = hh ? 0x7362 : 0x5140;
-                const uint2 ab = codes_to_half4<KIND>(__byte_perm(v[kg][0][q], v[kg][1][q], pick));
-                const uint2 cd = codes_to_half4<KIND>(__byte_perm(v[kg][2][q], v[kg][3][q], pick));
+            for (int kg = 0; kg < KG; ++kg) {
+              const uint32_t pick = hh ? 0x7362 : 0x5140;
+              const uint2 ab = codes_to_half4<KIND>(__byte_perm(v[kg][0][q], v[kg][1][q], pick));
+              const uint2 cd = codes_to_half4<KIND>(__byte_perm(v[kg][2][q], v[kg][3][q], pick));
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  if (kg > 0 && decltype(one_scale)::value) {
-                    mma16816(y[nt], ab.x, ab.y, cd.x, cd.y, pf[kg][nt][0], pf[kg][nt][1]);
-                  } else {
-                    mma16816_first(y[nt], ab.x, ab.y, cd.x, cd.y, pf[kg][nt][0], pf[kg][nt][1]);
-                    if (!decltype(one_scale)::value) accumulate(o[nt][2 * q + hh], sv[kg], y[nt]);
-                  }
+              for (int nt = 0; nt < NT; ++nt) {
+                float y[4];
+                mma16816_first(y, ab.x, ab.y, cd.x, cd.y, pf[kg][nt][0], pf[kg][nt][1]);
+                float (&acc)[4] = o[nt][2 * q + hh];
+                if constexpr (NT * D < 384) {
+                  const uint64_t f = f2_make(sv[kg], sv[kg]);
+                  f2_split(ffma2(f, f2_make(y[0], y[1]), f2_make(acc[0], acc[1])), acc[0], acc[1]);
+                  f2_split(ffma2(f, f2_make(y[2], y[3]), f2_make(acc[2], acc[3])), acc[2], acc[3]);
+                } else {  // (pairs cost the fullest variant registers: 102 against 96 us for 20 rows)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[e] = fmaf(sv[kg], y[e], acc[e]);
                 }
-              }
-              if (decltype(one_scale)::value) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) accumulate(o[nt][2 * q + hh], sv[0], y[nt]);
               }
             }
           }
-        };
-        if (KG == 1 || same) products(std::true_type{});
-        else products(std::false_type{});
+        }
       }
       };
       if (key0 + TK > first_limit || p.mask != nullptr) compute(std::true_type{});
