@@ -362,6 +362,53 @@ def test_rows_cut_over_many_ctas(bsa, B, length, heads, g, nq, d, kind):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_masks_of_many_rows(bsa):
+    # More (row, head) lists than threads that add them up; empty rows among them.
+    B = 210
+    lens = [(i * 37) % 91 for i in range(B)]
+    m, c = filled(bsa, lens, 2, 32, 32, 128, "e4m3", 3, seed=21)
+    gen = torch.Generator().manual_seed(21)
+    mask = (torch.rand(B, 4, 3, generator=gen) < 0.5).to(torch.uint8)
+    check_attention(bsa, m, c, rand(gen, B, 4, 1, 128), mask=mask, bk=32, what="many rows")
+
+
+def test_pools_past_32_bit_offsets(bsa):
+    """Pages that lie beyond 4 GB in the pools hold and give what the same pages
+    of a small cache do."""
+    heads, page, d, far = 8, 64, 128, 69000       # 64 KB a page: byte offsets past 2^32
+    lens = [700, 130, 64]
+    m, c = filled(bsa, lens, heads, page, 32, d, "e4m3", 12, seed=31)
+    pages = m.refs.shape[0]
+    n = far + pages + 40
+    e = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device="cuda")
+    big = bsa.Cache(*(e(n, heads, page, d, dtype=torch.uint8).view(torch.float8_e4m3fn) for _ in range(2)),
+                    *(e(n, heads, page // 32, dtype=torch.float32) for _ in range(2)),
+                    torch.where(c.block_table >= 0, c.block_table + far, c.block_table), c.lens.clone(),
+                    torch.zeros(n, dtype=torch.int32, device="cuda"))
+    big.refs[far:far + pages] = c.refs
+    src = torch.arange(pages, dtype=torch.int32, device="cuda")
+    bsa.cache_copy_pages(big, c, src + far, src)
+    gen = torch.Generator().manual_seed(31)
+    new = rand(gen, 3, heads, 1, d).cuda() * 40      # scales grow: old codes are read and rewritten
+    q = rand(gen, 3, 2 * heads, 1, d).cuda()
+    for x in (c, big):
+        bsa.cache_append(x, new, new)
+    same = lambda a, b: torch.equal(a[far:far + pages].contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    assert same(big.k, c.k) and same(big.v, c.v) and same(big.k_scale, c.k_scale) and same(big.v_scale, c.v_scale)
+    a, b = bsa.cache_attention(c, q), bsa.cache_attention(big, q)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    p = bsa.plan(torch.ones(3, 2 * heads, 1, 6, dtype=torch.uint8, device="cuda"), 128, 128, 2)
+    q2 = rand(gen, 3, 2 * heads, 128, d).cuda()
+    a, b = bsa.cache_forward(p, c, q2, causal=True), bsa.cache_forward(p, big, q2, causal=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    bsa.cache_compact(big)                            # back to the front
+    assert int((big.refs[:int((c.refs > 0).sum())] > 0).all())
+    b = bsa.cache_attention(big, q)
+    a = bsa.cache_attention(c, q)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert bsa.cache_status(big) == (0, 0) and bsa.cache_status(c) == (0, 0)
+
+
 def test_large_and_uneven_scores(bsa):
     # The largest score comes late, scores spread over thousands, scales differ
     # by 2^40 between blocks, q far from 1.
