@@ -3,6 +3,7 @@ Argument marshalling only: every step runs in the library's CUDA kernels."""
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -242,11 +243,28 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
         if len(c._workspace_bytes) > 256:
             c._workspace_bytes.clear()
         c._workspace_bytes[key] = need
-    ws = _scratch(c, need, stream)
-    _call(c, "attention", c._ref, qr, _rows(c, out, "out"), lse.data_ptr(), _ELEMENTS[q.dtype],
-          _list(c, seqs, "seqs", B), mptr, NKB, bk, B, Hq, nq, CACHE_CAUSAL if causal else 0,
-          0.0 if scale is None else scale, ws.data_ptr(), need, _stream(c, stream))
+    handle = _stream(c, stream)
+    args = (c._ref, qr, _rows(c, out, "out"), lse.data_ptr(), _ELEMENTS[q.dtype], _list(c, seqs, "seqs", B), mptr, NKB,
+            bk, B, Hq, nq, CACHE_CAUSAL if causal else 0, 0.0 if scale is None else scale)
+    if handle == 0 and need <= _KEPT_BYTES:
+        with _kept_lock:  # the call's kernels are enqueued one after another
+            ws = _kept.get(c._index)
+            if ws is None:
+                ws = _kept[c._index] = torch.empty(_KEPT_BYTES, dtype=torch.uint8, device=c.device)
+            _call(c, "attention", *args, ws.data_ptr(), need, handle)
+    else:
+        ws = _scratch(c, need, stream)
+        _call(c, "attention", *args, ws.data_ptr(), need, handle)
     return out, lse
+
+
+# Scratch of calls on a device's default stream: they are in order with each
+# other, and never captured into a graph, so one piece serves them all (an
+# allocation per call costs a third of a small call's time).  Other streams'
+# calls, and larger ones, take theirs from the allocator.
+_KEPT_BYTES = 16 << 20
+_kept = {}
+_kept_lock = threading.Lock()
 
 
 def _scratch(c: Cache, need: int, stream) -> torch.Tensor:

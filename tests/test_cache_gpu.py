@@ -637,6 +637,30 @@ def test_calls_on_another_stream_use_memory_of_their_own(bsa):
             assert torch.equal(x, y)
 
 
+def test_two_threads_on_the_default_stream(bsa):
+    """Calls of two host threads on one stream share their scratch in turn."""
+    import threading
+    m, c = filled(bsa, [3000, 1500, 40], 2, 64, 64, 64, "e4m3", 47, seed=14)
+    gen = torch.Generator().manual_seed(14)
+    qs = [rand(gen, 3, 8, n, 64).cuda() for n in (1, 3)]
+    want = [bsa.cache_attention(c, q) for q in qs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        for _ in range(200):
+            got = bsa.cache_attention(c, qs[i])
+            if not (torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1])):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_free_of_every_sequence(bsa):
     c = bsa.cache_create(64, 1, 16, 64, 5000, 2)
     bsa.cache_resize(c, torch.full((60,), 16, dtype=torch.int32, device="cuda"))
