@@ -105,7 +105,16 @@ bsa_status check_arch(int* dev_out) {
     cache[dev] = (maj == 10 && min == 3) ? 1 : 2;
   }
   if (dev_out) *dev_out = dev;
-  return cache[dev] == 1 ? BSA_OK : BSA_ERR_ARCH;
+  if (cache[dev] != 1) return BSA_ERR_ARCH;
+  // A host thread's first call: make the device's context current, which the
+  // runtime does by itself only for calls that need it, and the driver's tensor
+  // map encoder, called before any of those, asks for.
+  static thread_local int current = -1;
+  if (current != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return BSA_ERR_CUDA;
+    current = dev;
+  }
+  return BSA_OK;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
