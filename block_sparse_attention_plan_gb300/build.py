@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libbsa.so")
 SOURCES = ["bsa_api.cu", "bsa_plan.cu", "bsa_prep.cu", "bsa_forward.cu", "bsa_forward_q64.cu", "bsa_noalloc.cu",
            "bsa_pipeline.cu", "bsa_cache_api.cu", "bsa_cache_pages.cu", "bsa_cache_append.cu", "bsa_cache_attn.cu",
            "bsa_cache_load.cu"]
-HEADERS = ["bsa_internal.h", "bsa_device.cuh", "bsa_fwd_common.cuh", "bsa_regime_table.h", "bsa_cache.h",
+HEADERS = ["bsa_internal.h", "bsa_device.cuh", "bsa_fwd_common.cuh", "bsa_regime_table.h", "bsa_cache.h", "bsa_launch.h",
            "bsa_cache_codes.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -439,11 +439,12 @@ bsa_status bsa_forward_ex(const bsa_plan* plan, const void* Q, const void* K, co
 
 namespace {
 
-// bsa_forward_stage; causal_len: the causal offset of batch row b is
-// kv_lens[b] - Nq instead of Nk - Nq.
+// bsa_forward_stage; after_load: behind the pass that loaded K and V from a
+// cache, which has reset the control words, and with the causal offset of batch
+// row b kv_lens[b] - Nq instead of Nk - Nq.
 bsa_status forward_stage(const bsa_plan* plan, const void* Q, const void* K, const void* V,
                          const bsa_kv_pages* pages, const int32_t* kv_lens, int flags, void* O,
-                         float* LSE, int d, float scale, int stages, void* stream, bool causal_len) {
+                         float* LSE, int d, float scale, int stages, void* stream, bool after_load) {
   constexpr int kAllBits = BSA_STAGE_ALL | BSA_STAGE_KNORM | BSA_STAGE_ROWBOUND;
   if (stages <= 0 || (stages & ~kAllBits)) return BSA_ERR_INVALID_ARG;
   const PlanImpl* p = as_impl(plan);
@@ -470,13 +471,13 @@ bsa_status forward_stage(const bsa_plan* plan, const void* Q, const void* K, con
                        d, scale, dev, env_ll("BSA_WATCHDOG_MS", 1000) * 1000000ll,
                        env_ll("BSA_GRID", 0), &fp, &grid);
   if (st != BSA_OK) return st;
-  fp.causal_len = causal_len ? 1 : 0;
+  fp.causal_len = after_load ? 1 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // The key-norm stage resets its own status words, the row-bound stage the
   // pass counters and the forward status (the two may run on different
   // streams, the first beside the plan kernels).
-  const bool knorm = stages & (BSA_STAGE_PREPARE | BSA_STAGE_KNORM);
-  const bool rowbound = stages & (BSA_STAGE_PREPARE | BSA_STAGE_ROWBOUND);
+  const bool knorm = !after_load && (stages & (BSA_STAGE_PREPARE | BSA_STAGE_KNORM));
+  const bool rowbound = !after_load && (stages & (BSA_STAGE_PREPARE | BSA_STAGE_ROWBOUND));
   if (knorm && rowbound) {  // one reset of both sets of words
     if (cudaMemsetAsync(pd.control, 0, 4 * (kCtlKnormDetail + 1), s) != cudaSuccess) return BSA_ERR_CUDA;
   } else if (knorm) {
@@ -614,7 +615,8 @@ bsa_status key_norm_views(const bsa_plan* plan, CacheLoadParams* p) {
   p->kmax = reinterpret_cast<float*>(q->ws + fs.off_kmax);
   p->vmax = reinterpret_cast<float*>(q->ws + fs.off_vmax);
   p->fb_flag = reinterpret_cast<int32_t*>(q->ws + fs.off_fb_flag);
-  p->knorm_status = q->dev.control + kCtlKnormStatus;
+  p->control = q->dev.control;
+  p->control_words = kCtlKnormDetail + 1;
   p->rows = q->L.rows;
   p->ku = q->L.ku;
   p->NKU = q->L.NKU;

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "bsa.h"
+#include "bsa_launch.h"
 
 namespace bsa {
 
@@ -36,31 +37,7 @@ struct CacheDev {
 };
 inline size_t cache_control_ints(int num_pages) { return kCacheScratch + 3 * (size_t)num_pages; }
 
-// Launch that may become resident before the kernel ahead of it in the stream
-// has ended.  Every kernel launched so begins with wait_for_previous(), which
-// returns when that one has ended and its writes are visible; it lets its own
-// successor queue up right away.  Hides most of the 2 us between dependent
-// kernels, which is what calls on a few sequences consist of.
-template <class... Params, class... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t s,
-                         const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 #ifdef __CUDACC__
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void next_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // First error of its cache since the last report.
 __device__ __forceinline__ void cache_error(int32_t* control, int code, int detail) {
   if (atomicCAS(control + kCacheStatus, 0, code) == 0) atomicExch(control + kCacheDetail, detail);
@@ -125,7 +102,8 @@ struct CacheLoadParams {
   float* kmax;  // [B*Hkv][NKU]
   float* vmax;
   int32_t* fb_flag;  // [rows]
-  int32_t* knorm_status;  // status and detail of the key-norm pass
+  int32_t* control;  // the forward's control words
+  int control_words;
   int rows, ku, NKU;
   int device;  // the plan's
 };

@@ -42,11 +42,11 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
     p.lens[b] = len;
     if (!known && seq != -1) cache_error(c.control, BSA_ERR_INVALID_ARG, b);
   }
-  // What the forward's key-norm pass resets.
+  // What a forward resets ahead of its passes.
   const long long at = ((long long)(blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + tid;
   const long long all = (long long)gridDim.x * gridDim.y * gridDim.z * kThreads;
   for (long long i = at; i < p.rows; i += all) p.fb_flag[i] = 0;
-  if (at < 2) p.knorm_status[at] = 0;
+  if (at < p.control_words) p.control[at] = 0;
   const uint8_t* codes = isv ? c.v : c.k;
   const float* scales = isv ? c.vs : c.ks;
   uint16_t* out = (isv ? p.v : p.k) + (size_t)bh * p.Nk * D;

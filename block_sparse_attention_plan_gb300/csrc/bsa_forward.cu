@@ -68,6 +68,7 @@
 #include <cuda_bf16.h>
 
 #include "bsa_fwd_common.cuh"
+#include "bsa_launch.h"
 
 namespace bsa {
 namespace {
@@ -758,6 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_fwd_kernel(const __grid_const
   volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const Watchdog wd{abort_flag, p.control + kCtlStatus, p.control + kCtlDetail, p.watchdog_ns};
+  next_may_launch();
+  wait_for_previous();
   // A pass over a queue (the exact pass) with nothing queued: leave before
   // any setup.  The count was written by the previous kernel in the stream.
   if (p.work_count != nullptr && *reinterpret_cast<const volatile int32_t*>(p.work_count) <= 0) return;
@@ -848,8 +851,7 @@ cudaError_t launch_dm(const FwdParams& p, int grid, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(bsa_fwd_kernel<D, kExact, kMode, kMulti>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  bsa_fwd_kernel<D, kExact, kMode, kMulti><<<grid, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(bsa_fwd_kernel<D, kExact, kMode, kMulti>, dim3(grid), dim3(kThreads), smem, stream, p);
 }
 template <int D, bool kExact, int kMode>
 cudaError_t launch_dk(const FwdParams& p, int grid, cudaStream_t stream) {

@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "bsa_fwd_common.cuh"
+#include "bsa_launch.h"
 
 namespace bsa {
 namespace {
@@ -192,7 +193,9 @@ __global__ void __launch_bounds__(kKmaxThreads) kmax_kernel(const FwdParams p) {
 // rows as they would plan entries.  A page outside the table is an error only
 // when the unit holds keys within the sequence's key length (beyond it the
 // keys are masked, so page 0 serves).
-__global__ void __launch_bounds__(256) rowbound_kernel(const FwdParams p) {
+__global__ void __launch_bounds__(256) rowbound_kernel(const __grid_constant__ FwdParams p) {
+  next_may_launch();
+  wait_for_previous();
   const int row = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (row >= p.rows) return;
   const int s0 = __ldg(p.row_ptr + row), s1 = __ldg(p.row_ptr + row + 1);
@@ -202,14 +205,24 @@ __global__ void __launch_bounds__(256) rowbound_kernel(const FwdParams p) {
     const float* kh = p.kmax + (size_t)(b * p.Hkv + hkv) * p.NKU;
     const float* vh = p.vmax + (size_t)(b * p.Hkv + hkv) * p.NKU;
     const int kvl = (p.prow && p.kv_lens) ? __ldg(p.kv_lens + b) : 0x7fffffff;
-    for (long long i = (long long)s0 * p.rk + lane; i < (long long)s1 * p.rk; i += 32) {
-      const int y = __ldg(p.slot_ku + i);
-      const bool valid = y >= 0 && y < p.NKU;
-      if (valid) {
-        km = fmaxf(km, __ldg(kh + y));
-        vm = fmaxf(vm, __ldg(vh + y));
+    const long long end = (long long)s1 * p.rk;
+    for (long long i0 = (long long)s0 * p.rk + lane; i0 < end; i0 += 128) {
+      int y4[4];  // four positions' reads at once: the pass is their latency
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y4[q] = i0 + 32 * q < end ? __ldg(p.slot_ku + i0 + 32 * q) : -1;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bool valid = y4[q] >= 0 && y4[q] < p.NKU;
+        km = fmaxf(km, valid ? __ldg(kh + y4[q]) : 0.f);
+        vm = fmaxf(vm, valid ? __ldg(vh + y4[q]) : 0.f);
       }
-      if (p.prow) {
+      if (!p.prow) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const long long i = i0 + 32 * q;
+        if (i >= end) break;
+        const int y = y4[q];
+        const bool valid = y >= 0 && y < p.NKU;
         int prow = -1;  // padding, or an entry out of range (reported here)
         if (valid) {
           const int key = y * p.ku;
@@ -261,8 +274,7 @@ cudaError_t launch_prep(const FwdParams& p, int d, int stages, cudaStream_t stre
     if (e != cudaSuccess) return e;
   }
   if (stages & (BSA_STAGE_PREPARE | BSA_STAGE_ROWBOUND)) {
-    rowbound_kernel<<<(unsigned)((p.rows + 7) / 8), 256, 0, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_after(rowbound_kernel, dim3((unsigned)((p.rows + 7) / 8)), dim3(256), 0, stream, p);
   }
   return e;
 }
