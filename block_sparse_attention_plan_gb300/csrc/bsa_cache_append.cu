@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
   if (good && count > 0) good = pos >= 0 && pos <= len - count;
   if (first && !good && seq != -1) cache_error(c.control, BSA_ERR_INVALID_ARG, row);
   if (!good || count == 0) return;
-  const int b0 = (pos / c.sb + blk) * c.sb;  // first position of the block
+  const int b0 = ((pos >> (31 - __clz(c.sb))) + blk) * c.sb;  // first position of the block
   const int lo = max(b0, pos), hi = min(b0 + c.sb, pos + count);
   if (lo >= hi) return;
   const int U = 2 * c.Hkv, upi = blockDim.x / tpu;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
   };
   uint4 x[kVec];
   load(u, x);  // (does not need the page)
-  const int phys = __ldg(c.table + (size_t)seq * c.max_pages + b0 / c.page);
+  const int phys = __ldg(c.table + (size_t)seq * c.max_pages + (b0 >> (31 - __clz(c.page))));
   if (phys < 0 || phys >= c.num_pages) {
     if (blockIdx.y == 0 && tid == 0) cache_error(c.control, BSA_ERR_PLAN_MISMATCH, seq);
     return;

@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
 
   // ---------------------------------------------------------------- requests
   const int lpage = 31 - __clz(p.c.page), lsb = 31 - __clz(p.c.sb);
+  const int lbk = p.mask ? 31 - __clz(p.bk) : 0;
   const int cs = min(p.c.page, TK);  // keys per box
   const int lcs = 31 - __clz(cs), nc = TK >> lcs;
   // Read once, unless other row tiles or groups of rows come back for it.
@@ -483,10 +484,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         scale = __ldg((lane < C::kGroups ? p.c.ks : p.c.vs) + ((size_t)(unsigned)(sbox + ((16 * gr) & (cs - 1))) >> lsb));
     }
     if (p.mask && lane < 8 * NT) {
-      const int k0 = tile * TK / p.bk;
+      const int k0 = tile * TK >> lbk;
       if (k0 < p.NKB) sel.x = __ldg(f.mask + k0);
       if (TK > 32) {
-        const int k1 = (tile * TK + 32) / p.bk;
+        const int k1 = (tile * TK + 32) >> lbk;
         if (k1 < p.NKB) sel.y = __ldg(f.mask + k1);
       }
     }
@@ -940,12 +941,13 @@ __global__ void __launch_bounds__(kTilesThreads) tiles_kernel(const __grid_const
   const int tiles = min((len + p.tile - 1) / p.tile, p.max_tiles);
   const uint8_t* mrow = p.mask + ((size_t)b * p.Hq + (size_t)h * p.g) * p.NKB;
   int32_t* out = p.list + (size_t)e * p.max_tiles;
+  const int lbk = 31 - __clz(p.bk);
   int done = 0;
   for (int base = 0; base < tiles; base += kTilesThreads) {
     const int t = base + tid;
     unsigned on = 0u;
     if (t < tiles) {
-      const int k0 = t * p.tile / p.bk, k1 = p.bk < p.tile ? min(k0 + 1, p.NKB - 1) : k0;
+      const int k0 = t * p.tile >> lbk, k1 = p.bk < p.tile ? min(k0 + 1, p.NKB - 1) : k0;
 #pragma unroll 8
       for (int i = 0; i < p.g; ++i) on |= __ldg(mrow + (size_t)i * p.NKB + k0) | __ldg(mrow + (size_t)i * p.NKB + k1);
     }

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
   const float* scales = isv ? c.vs : c.ks;
   uint16_t* out = (isv ? p.v : p.k) + (size_t)bh * p.Nk * D;
   const int t0 = blockIdx.x * kTokens;
+  const int lpage = 31 - __clz(c.page), lsb = 31 - __clz(c.sb);
   if (tid < kBlocks) s_max[tid] = 0.f;
   const int col = tid % kCols;
   uint4 x[kItems];
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
     const int key = t0 + (j * kThreads + tid) / kCols;
-    ph[j] = key < len ? __ldg(c.table + (size_t)seq * c.max_pages + key / c.page) : 0;
+    ph[j] = key < len ? __ldg(c.table + (size_t)seq * c.max_pages + (key >> lpage)) : 0;
     if (ph[j] < 0 || ph[j] >= c.num_pages) {
       cache_error(c.control, BSA_ERR_PLAN_MISMATCH, seq);
       ph[j] = -1;
@@ -71,9 +72,9 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
     x[j] = make_uint4(0u, 0u, 0u, 0u);  // (codes 0)
     sc[j] = 0.f;
     if (key < len && ph[j] >= 0) {
-      const size_t row = ((size_t)ph[j] * c.Hkv + h) * c.page + (key & (c.page - 1));
-      x[j] = __ldcs(reinterpret_cast<const uint4*>(codes + row * D + col * 16));
-      sc[j] = __ldg(scales + row / c.sb);
+      const unsigned row = ((unsigned)(ph[j] * c.Hkv + h) << lpage) + (key & (c.page - 1));  // (below 2^31)
+      x[j] = __ldcs(reinterpret_cast<const uint4*>(codes + (size_t)row * D + col * 16));
+      sc[j] = __ldg(scales + (row >> lsb));
     }
   }
   __syncthreads();
