@@ -369,10 +369,7 @@ bsa_status create_plan(const uint8_t* mask, const int32_t* seg, const int32_t* s
   d.remap = ((flags & BSA_PLAN_REMAP) && L.rq > 1 && gqa_group == 1 && L.NQT <= kMaxRemapTiles) ? 1 : 0;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Pass counters and forward status only: a key-norm stage of this plan's
-  // forward may already be running on another stream.
-  if (cudaMemsetAsync(d.control, 0, 4 * (kCtlFallbackWork + 1), s) != cudaSuccess ||
-      launch_plan(d, s) != cudaSuccess) {
+  if (launch_plan(d, s) != cudaSuccess) {
     delete impl;
     return BSA_ERR_CUDA;
   }

@@ -26,6 +26,7 @@
 #include <cstdint>
 
 #include "bsa_internal.h"
+#include "bsa_launch.h"
 
 namespace bsa {
 namespace {
@@ -172,6 +173,11 @@ __device__ uint32_t segment_word(const PlanDev& p, int s0, int s1, int qb, int w
 }
 
 __global__ void __launch_bounds__(kThreads) plan_count_kernel(const PlanDev p) {
+  next_may_launch();
+  wait_for_previous();
+  // Pass counters and forward status only: a key-norm stage of this plan's
+  // forward may already be running on another stream.
+  if (blockIdx.x == 0 && threadIdx.x <= kCtlFallbackWork) p.control[threadIdx.x] = 0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row_ctas = (p.rows + kWarps - 1) / kWarps;
   if ((int)blockIdx.x < row_ctas) {
@@ -283,6 +289,8 @@ __device__ long long block_sum(long long v, long long* red) {
 // fewest wins, ties to the smaller stride.  Writes the stride and the plane's
 // per-row slot counts for it.  Launched only with BSA_PLAN_REMAP.
 __global__ void __launch_bounds__(kThreads) plan_choose_kernel(const PlanDev p) {
+  next_may_launch();
+  wait_for_previous();
   extern __shared__ int tile_cnt[];  // [NQT] set bits of each tile's union
   __shared__ long long red[kWarps];
   const int bh = blockIdx.x;
@@ -404,6 +412,8 @@ __device__ long long block_scan_array(const TIn* in, int32_t* out, int n, long l
 }
 
 __global__ void __launch_bounds__(kScanThreads) plan_scan_kernel(const PlanDev p) {
+  next_may_launch();
+  wait_for_previous();
   __shared__ long long wsum[32];
   extern __shared__ int work_s[];  // [groups] total slots per K/V-head group
   long long A = 0;  // selected logical blocks: summed in the row-pointer scan's load pass
@@ -547,6 +557,8 @@ __device__ void order_group(const PlanDev& p, int gi, int* start_s) {
 }
 
 __global__ void __launch_bounds__(kThreads) plan_fill_kernel(const PlanDev p) {
+  next_may_launch();
+  wait_for_previous();
   extern __shared__ int start_s[];  // [nkeys]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row_ctas = (p.rows + kWarps - 1) / kWarps;
@@ -576,23 +588,20 @@ cudaError_t launch_plan(const PlanDev& p, cudaStream_t stream) {
   e = cudaFuncSetAttribute(plan_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kMaxGroups * (int)sizeof(int));
   if (e != cudaSuccess) return e;
-  plan_count_kernel<<<row_ctas + union_ctas, kThreads, 0, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_after(plan_count_kernel, dim3(row_ctas + union_ctas), dim3(kThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
   if (p.remap) {
     const size_t tiles_smem = (size_t)p.NQT * sizeof(int);
     e = cudaFuncSetAttribute(plan_choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMaxRemapTiles * (int)sizeof(int));
     if (e != cudaSuccess) return e;
-    plan_choose_kernel<<<p.B * p.H, kThreads, tiles_smem, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_after(plan_choose_kernel, dim3(p.B * p.H), dim3(kThreads), (int)tiles_smem, stream, p);
     if (e != cudaSuccess) return e;
   }
-  plan_scan_kernel<<<1, kScanThreads, groups_smem, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_after(plan_scan_kernel, dim3(1), dim3(kScanThreads), (int)groups_smem, stream, p);
   if (e != cudaSuccess) return e;
-  plan_fill_kernel<<<row_ctas + union_ctas + p.groups, kThreads, keys_smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(plan_fill_kernel, dim3(row_ctas + union_ctas + p.groups), dim3(kThreads), (int)keys_smem,
+                      stream, p);
 }
 
 }  // namespace bsa

@@ -57,6 +57,8 @@ template <int D>
 __global__ void __launch_bounds__(kKmaxThreads) kmax_kernel(const FwdParams p) {
   extern __shared__ __align__(1024) uint8_t kmax_smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  next_may_launch();
+  wait_for_previous();
   for (int i = blockIdx.x * kKmaxThreads + tid; i < p.rows; i += gridDim.x * kKmaxThreads)
     p.fb_flag[i] = 0;
   const uint32_t base = smem_u32(kmax_smem);
@@ -264,13 +266,13 @@ cudaError_t launch_prep(const FwdParams& p, int d, int stages, cudaStream_t stre
     if (kgrid < 1) kgrid = 1;
     if (d == 64) {
       e = cudaFuncSetAttribute(kmax_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKmaxSmem);
-      if (e == cudaSuccess) kmax_kernel<64><<<(unsigned)kgrid, kKmaxThreads, kKmaxSmem, stream>>>(p);
+      if (e == cudaSuccess)
+        e = launch_after(kmax_kernel<64>, dim3((unsigned)kgrid), dim3(kKmaxThreads), kKmaxSmem, stream, p);
     } else {
       e = cudaFuncSetAttribute(kmax_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKmaxSmem);
-      if (e == cudaSuccess) kmax_kernel<128><<<(unsigned)kgrid, kKmaxThreads, kKmaxSmem, stream>>>(p);
+      if (e == cudaSuccess)
+        e = launch_after(kmax_kernel<128>, dim3((unsigned)kgrid), dim3(kKmaxThreads), kKmaxSmem, stream, p);
     }
-    if (e != cudaSuccess) return e;
-    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (stages & (BSA_STAGE_PREPARE | BSA_STAGE_ROWBOUND)) {
