@@ -268,7 +268,10 @@ template <int D, int KIND, int NT>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = AttnCfg<D>;
   constexpr int TK = C::TK;
-  constexpr int KG = NT * D <= 64 ? 4 : (NT < 3 ? 2 : 1);  // groups of 16 keys whose scores are held at once
+  // Groups of 16 keys whose scores are held at once, as registers allow (d = 128
+  // with 16 rows: 67.3 us with one, 68.6 with two and its spills; d = 64: 46.6
+  // and 43.9).
+  constexpr int KG = NT * D <= 64 ? 4 : (NT * D <= 128 ? 2 : 1);
   extern __shared__ __align__(1024) uint8_t smem[];
   int* s_prefix = reinterpret_cast<int*>(smem + C::kOffMerge);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
