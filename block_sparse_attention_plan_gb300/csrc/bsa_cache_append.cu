@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
     if (blockIdx.y == 0 && tid == 0) cache_error(c.control, BSA_ERR_PLAN_MISMATCH, seq);
     return;
   }
+  const int refs = __ldg(c.refs + phys);  // (arrives while the first units' maxima are taken)
   // Other tokens of the sequence in this block: below lo, or from hi on.
   const bool others = lo > b0 || hi < held;
   const int lsb = 31 - __clz(c.sb), in_page = b0 & (c.page - 1);
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
     } else {
       __syncwarp();  // every thread of the unit has read its scale before one writes it
     }
-    if (active) {
+    if (active && refs <= 1) {
       float scale = scale_for<KIND>(amax);
       if (others) scale = fmaxf(scale, was);
       const bool grown = others && scale != was;
@@ -238,6 +239,8 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
 #pragma unroll
     for (int j = 0; j < kVec; ++j) x[j] = next[j];
   }
+  // A page that other sequences hold is theirs too.
+  if (refs > 1 && blockIdx.y == 0 && tid == 0) cache_error(c.control, BSA_ERR_INVALID_ARG, row);
 }
 
 }  // namespace

@@ -507,7 +507,7 @@ bsa_status bsa_attention_host(const uint8_t* mask, int B, int H, int NQB, int NK
  * What the kernels find wrong in device data is recorded in the control words,
  * the first of its kind kept, and reported by bsa_cache_status: a sequence
  * index or length out of range, a sequence named twice, a fork onto a sequence
- * that holds tokens (BSA_ERR_INVALID_ARG, detail = index in the list); a held
+ * that holds tokens, tokens for a shared page (BSA_ERR_INVALID_ARG, detail = index in the list); a held
  * token whose table entry is no page (BSA_ERR_PLAN_MISMATCH, detail = the
  * sequence); too few free pages (BSA_ERR_WORKSPACE, detail = pages missing).
  * Such an item is skipped (for BSA_ERR_WORKSPACE the whole call is); memory
@@ -612,7 +612,9 @@ bsa_status bsa_cache_copy_pages(const bsa_cache* dst, const bsa_cache* src, cons
  *   row are stored (the first ones; 0 .. T).
  * start: device int32 [n] or NULL: position of the first one; NULL = the
  *   sequence's length - count, i.e. they are its last tokens.
- * Tokens outside [0, length) are not stored and recorded (BSA_ERR_INVALID_ARG).
+ * Tokens outside [0, length), or in a page that other sequences hold too
+ * (page_refs above 1; growing a sequence gives it a last page of its own), are
+ * not stored and recorded (BSA_ERR_INVALID_ARG, detail = the row).
  * Scale of a block: the smallest power of two, at least 2^-100, that takes the
  * largest finite |x| of the stored tokens into the codes' range; if the
  * sequence has other tokens in the block, the larger of that and the block's

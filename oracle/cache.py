@@ -150,6 +150,9 @@ class CacheModel:
                 b = min(at + c, (a // self.sb + 1) * self.sb)
                 b0 = a // self.sb * self.sb
                 page, r0 = int(self.table[s, a // self.page]), b0 % self.page
+                if self.refs[page] > 1:  # other sequences' too: left as it is
+                    a = b
+                    continue
                 others = [t - b0 for t in range(b0, min(b0 + self.sb, int(self.lens[s]))) if not a <= t < b]
                 for w, x in enumerate((k, v)):
                     for h in range(heads):

@@ -664,6 +664,36 @@ def test_two_threads_on_the_default_stream(bsa):
     assert not bad, bad[:3]
 
 
+def test_append_leaves_shared_pages_alone(bsa):
+    gen = torch.Generator().manual_seed(71)
+    m = OC.CacheModel(12, 2, 16, 64, 4, 4, seed=7)
+    assert m.resize([20], [0]) == 0
+    c = upload(bsa, m)
+
+    def append(T, seqs, start=None):
+        k, v = (rand(gen, len(seqs), 2, T, 64) for _ in range(2))
+        m.append(k.double().numpy(), v.double().numpy(), seqs, None, start)
+        bsa.cache_append(c, k.cuda(), v.cuda(), seqs=i32(*seqs), start=None if start is None else i32(*start))
+        assert_state(c, m)
+
+    append(20, [0])
+    assert bsa.cache_status(c) == (0, 0)
+    bsa.cache_fork(c, i32(0), i32(2))
+    m.fork([0], [2])
+    # Both hold pages of tokens 0 .. 19: nothing of either row is stored.
+    append(3, [0, 2])
+    assert bsa.cache_status(c)[0] == -1
+    # Grown by 14, sequence 2 has tokens 16 .. 33 to itself, and 0 (alone with
+    # its last page again) 16 .. 19; tokens 0 .. 15 stay as they are.
+    bsa.cache_resize(c, i32(34), i32(2))
+    assert m.resize([34], [2]) == 0
+    append(14, [2])
+    append(4, [0])
+    assert bsa.cache_status(c) == (0, 0)
+    append(20, [2], [8])  # 8 .. 15 lie in the shared page, 16 .. 27 do not
+    assert bsa.cache_status(c) == (-1, 0)
+
+
 def test_free_of_every_sequence(bsa):
     c = bsa.cache_create(64, 1, 16, 64, 5000, 2)
     bsa.cache_resize(c, torch.full((60,), 16, dtype=torch.int32, device="cuda"))

@@ -70,3 +70,18 @@ def test_page_bookkeeping_invariants():
         assert np.array_equal(np.bincount(np.array(held, dtype=int), minlength=40), m.refs)
         for s in range(8):  # no page past the length; a partly filled last page of a grown sequence is its own
             assert (m.table[s, m._pages(m.lens[s]):] == -1).all()
+
+
+def test_append_leaves_shared_pages_alone():
+    m = OC.CacheModel(8, 1, 16, 8, 4, 3, seed=1)
+    assert m.resize([20], [0]) == 0
+    x = np.random.default_rng(2).standard_normal((1, 1, 20, 8))
+    m.append(x, x, [0])
+    m.fork([0], [1])
+    before = [a.copy() for a in m.codes + m.scales]
+    m.append(x[:, :, :5], x[:, :, :5], [1])
+    assert all(np.array_equal(a, b) for a, b in zip(before, m.codes + m.scales))
+    assert m.resize([22], [1]) == 0
+    m.append(x[:, :, :6], x[:, :, :6], [1])  # tokens 16 .. 21, in a page of its own
+    k0, k1 = m.values(0)[0], m.values(1)[0]
+    assert np.array_equal(k0[:, :16], k1[:, :16]) and not np.array_equal(k0[:, 16:20], k1[:, 16:20])
