@@ -9,8 +9,10 @@
 // A long append would be bound by the 2 bytes read and the byte written per
 // element but for the instructions, which are counted here (about five per
 // element: maxima of pairs as integers, the scale's reciprocal from its bits,
-// what depends on the thread alone kept out of the units' loop); a token per
-// sequence is bound by that chain of reads.
+// what depends on the thread alone kept out of the units' loop): 113 MB for 6
+// sequences of up to 4001 tokens, 16 heads of 64, in 22.2 us, 5.1 TB/s.  A token
+// per sequence is bound by that chain of reads: 7.3 us for 64 sequences, 8 heads
+// of 128.
 //
 // With power-of-two scales x / scale is exact, codes move to a larger scale
 // without a second rounding (subnormal codes excepted), and both code types
