@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
   const int count = p.counts ? __ldg(p.counts + row) : p.T;
   const int given = p.start ? __ldg(p.start + row) : 0;
   const bool known = seq >= 0 && seq < c.max_seqs;
-  const int len = known ? __ldg(c.lens + seq) : 0;
+  const int len = known ? load_written(c.lens + seq) : 0;
   const int pos = p.start ? given : len - count;
   const bool first = blk == 0 && blockIdx.y == 0 && tid == 0;
   // Counts out of [0, T], tokens out of [0, len) or a sequence out of range.
@@ -177,12 +177,12 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
   };
   uint4 x[kVec];
   load(u, x);  // (does not need the page)
-  const int phys = __ldg(c.table + (size_t)seq * c.max_pages + (b0 >> (31 - __clz(c.page))));
+  const int phys = load_written(c.table + (size_t)seq * c.max_pages + (b0 >> (31 - __clz(c.page))));
   if (phys < 0 || phys >= c.num_pages) {
     if (blockIdx.y == 0 && tid == 0) cache_error(c.control, BSA_ERR_PLAN_MISMATCH, seq);
     return;
   }
-  const int refs = __ldg(c.refs + phys);  // (arrives while the first units' maxima are taken)
+  const int refs = load_written(c.refs + phys);  // (arrives while the first units' maxima are taken)
   // Other tokens of the sequence in this block: below lo, or from hi on.
   const bool others = lo > b0 || hi < held;
   const int lsb = 31 - __clz(c.sb), in_page = b0 & (c.page - 1);

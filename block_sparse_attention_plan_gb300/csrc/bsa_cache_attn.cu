@@ -119,14 +119,14 @@ __device__ __forceinline__ int seq_of(const CacheAttnParams& p, int b) {
 __device__ __forceinline__ int len_of(const CacheAttnParams& p, int b) {
   const int s = seq_of(p, b);
   if (s < 0) return 0;
-  return min(max(__ldg(p.c.lens + s), 0), p.c.max_pages * p.c.page);
+  return min(max(load_written(p.c.lens + s), 0), p.c.max_pages * p.c.page);
 }
 
 // The line of tiles: entry e is a batch row with its Hkv heads (no mask) or one
 // (batch row, head) with its list (mask); each entry's tiles are repeated for
 // its heads and for the groups of kCacheUnitRows query rows.
 __device__ __forceinline__ int entry_tiles(const CacheAttnParams& p, int e) {
-  if (p.mask) return __ldg(p.counts + e);
+  if (p.mask) return load_written(p.counts + e);
   return (len_of(p, e) + p.tile - 1) / p.tile;
 }
 
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         // codes are elements 16 chunk + 4 s ..: the same of q.
 #pragma unroll
         for (int k2 = 0; k2 < KS / 2; ++k2) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(qr + t4 * (D / 4) + k2 * 8));
+          const uint4 x = load_written(reinterpret_cast<const uint4*>(qr + t4 * (D / 4) + k2 * 8));
           q_raw[nt][2 * k2][0] = x.x;
           q_raw[nt][2 * k2][1] = x.y;
           q_raw[nt][2 * k2 + 1][0] = x.z;
@@ -442,12 +442,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     for (int j = 0; j < 4; ++j) f.pr[j] = -1;
     if (lane < f.n) {
       const int t = f.pos + lane * KL;
-      f.tile = p.mask ? __ldg(p.list + (size_t)f.w.e * p.max_tiles + t) : t;
+      f.tile = p.mask ? load_written(p.list + (size_t)f.w.e * p.max_tiles + t) : t;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int key = f.tile * TK + (j << lcs);
         if (j < nc && key < f.len) {
-          int ph = __ldg(row + (key >> lpage));
+          int ph = load_written(row + (key >> lpage));
           if (ph < 0 || ph >= p.c.num_pages) {
             cache_error(p.c.control, BSA_ERR_PLAN_MISMATCH, seq);
             ph = 0;  // (some page, so that the row ends like any other)
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       const int gr = lane % C::kGroups, jb = (16 * gr) >> lcs;
       const int sbox = jb == 0 ? box[0] : (jb == 1 ? box[1] : (jb == 2 ? box[2] : box[3]));
       if (tile * TK + 16 * gr < f.len)
-        scale = __ldg((lane < C::kGroups ? p.c.ks : p.c.vs) + ((size_t)(unsigned)(sbox + ((16 * gr) & (cs - 1))) >> lsb));
+        scale = load_written((lane < C::kGroups ? p.c.ks : p.c.vs) + ((size_t)(unsigned)(sbox + ((16 * gr) & (cs - 1))) >> lsb));
     }
     if (p.mask && lane < 8 * NT) {
       const int k0 = tile * TK >> lbk;

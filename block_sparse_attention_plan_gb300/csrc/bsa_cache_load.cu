@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
   const int bh = blockIdx.y, b = bh / c.Hkv, h = bh % c.Hkv;
   const int seq = p.seqs ? __ldg(p.seqs + b) : b;
   const bool known = seq >= 0 && seq < c.max_seqs;
-  int len = known ? __ldg(c.lens + seq) : 0;
+  int len = known ? load_written(c.lens + seq) : 0;
   len = min(max(len, 0), min(p.Nk, c.max_pages * c.page));
   const bool isv = blockIdx.z != 0;
   if (blockIdx.x == 0 && h == 0 && tid == 0 && !isv) {
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
     const int key = t0 + (j * kThreads + tid) / kCols;
-    ph[j] = key < len ? __ldg(c.table + (size_t)seq * c.max_pages + (key >> lpage)) : 0;
+    ph[j] = key < len ? load_written(c.table + (size_t)seq * c.max_pages + (key >> lpage)) : 0;
     if (ph[j] < 0 || ph[j] >= c.num_pages) {
       cache_error(c.control, BSA_ERR_PLAN_MISMATCH, seq);
       ph[j] = -1;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
     if (key < len && ph[j] >= 0) {
       const unsigned row = ((unsigned)(ph[j] * c.Hkv + h) << lpage) + (key & (c.page - 1));  // (below 2^31)
       x[j] = __ldcs(reinterpret_cast<const uint4*>(codes + (size_t)row * D + col * 16));
-      sc[j] = __ldg(scales + (row >> lsb));
+      sc[j] = load_written(scales + (row >> lsb));
     }
   }
   __syncthreads();

@@ -505,7 +505,7 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint8_t* smem, 
     ++q_it;
     if (kElem && p.elem_mask) {
       const int qmin = qpos - lane;  // the warp's 32 rows lie in one q-unit (qu >= 32)
-      const int kvl = p.kv_lens ? __ldg(p.kv_lens + m.bh / p.H) : 0x7fffffff;
+      const int kvl = p.kv_lens ? load_written(p.kv_lens + m.bh / p.H) : 0x7fffffff;
       const int coff = p.causal_len ? kvl - p.Nq : p.causal_off;
       lim_row = min(p.causal ? qpos + coff : 0x7fffffff, kvl - 1);
       lim_warp = min(p.causal ? qmin + coff : 0x7fffffff, kvl - 1);
@@ -521,12 +521,12 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint8_t* smem, 
     for (int j = 0; j < m.n; ++j) {
       const int b = (int)(sg & 1u);
       const uint32_t u = sg >> 1;
-      if (submask) bits = (__ldg(p.slot_mask + m.s0 + j) >> (qi * p.rk)) & my_bits_mask;
+      if (submask) bits = (load_written(p.slot_mask + m.s0 + j) >> (qi * p.rk)) & my_bits_mask;
       if (kElem && p.elem_mask) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int col0 = 64 * h + 32 * c;  // ku = 32 << ku_shift
-          const int y = __ldg(p.slot_ku + (size_t)(m.s0 + j) * p.rk + (col0 >> (5 + ku_shift)));
+          const int y = load_written(p.slot_ku + (size_t)(m.s0 + j) * p.rk + (col0 >> (5 + ku_shift)));
           cbase[c] = (y < 0) ? -1 : (y << (5 + ku_shift)) + (col0 & (p.ku - 1));
         }
       }

@@ -16,6 +16,7 @@
 
 #include "bsa_device.cuh"
 #include "bsa_internal.h"
+#include "bsa_launch.h"
 
 namespace bsa {
 namespace {
@@ -69,20 +70,20 @@ __device__ __forceinline__ void record_status(int32_t* ctl, int code, int site) 
 // treated as empty and BSA_ERR_PLAN_MISMATCH is recorded).
 __device__ __forceinline__ Item load_item(const FwdParams& p, int it, bool report) {
   Item m{0, 0, 0, 0, 1, 0, false, 0, it, 0.f, false};
-  const int row = __ldg(p.order + it);
+  const int row = load_written(p.order + it);
   if (row < 0 || row >= p.rows) {
     if (report) record_status(p.control, -7, kSitePlanRange);
     return m;
   }
   m.valid = true;
   m.row = row;
-  const int s0 = __ldg(p.row_ptr + row), s1 = __ldg(p.row_ptr + row + 1);
+  const int s0 = load_written(p.row_ptr + row), s1 = load_written(p.row_ptr + row + 1);
   m.bh = row / p.NQT;
   const int qt = row % p.NQT;
   m.qs = 1;
   m.qx = qt * p.rq;
   if (p.sigma != nullptr) {  // a plan built with regrouping
-    int sig = __ldg(p.sigma + m.bh);
+    int sig = load_written(p.sigma + m.bh);
     if (!(sig == 1 || sig == 2 || sig == 4 || sig == 8 || sig == 16) || p.NQT % sig) {
       if (report) record_status(p.control, -7, kSitePlanRange + 5);
       sig = 1;
@@ -184,7 +185,7 @@ constexpr unsigned kFullMask = 0xffffffffu;
 template <bool kGeneral>
 __device__ __forceinline__ int fetch_key(const FwdParams& p, const Item& m, int j, int lane) {
   const int32_t* ent = ((kGeneral && p.prow) ? p.prow : p.slot_ku) + (size_t)(m.s0 + j) * p.rk;
-  return lane < p.rk ? __ldg(ent + lane) : -1;
+  return lane < p.rk ? load_written(ent + lane) : -1;
 }
 
 // One ring of tile stages with a single producer and a single consumer.
@@ -286,8 +287,8 @@ __device__ __noinline__ void producer_body(const FwdParams& p, uint8_t* smem, co
       if (it >= 0) {
         m = load_item(p, it, lane == 0);  // the same loads on every lane
         if (m.n > 0) {
-          m.kb = __ldg(p.rowk + m.row);
-          m.split = p.split_all || __ldg(p.rowv + m.row) > kSplitV;
+          m.kb = load_written(p.rowk + m.row);
+          m.split = p.split_all || load_written(p.rowv + m.row) > kSplitV;
           if (C::kQueueSplit && m.split) {
             // This pass does not apply split weights: the row is left to
             // the exact pass (queued once) and handed on as skipped.

@@ -93,10 +93,10 @@ __global__ void __launch_bounds__(kKmaxThreads) kmax_kernel(const FwdParams p) {
         const int head = (int)(unit / p.NKU), y = (int)(unit % p.NKU);  // head = b * Hkv + hkv
         const int b = head / p.Hkv;
         const int key = y * p.ku;
-        skip = (p.kv_lens != nullptr && key >= __ldg(p.kv_lens + b)) ? 1 : 0;
+        skip = (p.kv_lens != nullptr && key >= load_written(p.kv_lens + b)) ? 1 : 0;
         if (p.block_table != nullptr && !skip) {
           const int lp = key / p.page_size;
-          const int phys = (lp < p.max_pages) ? __ldg(p.block_table + (size_t)b * p.max_pages + lp) : -1;
+          const int phys = (lp < p.max_pages) ? load_written(p.block_table + (size_t)b * p.max_pages + lp) : -1;
           if (phys < 0 || phys >= p.num_pages) skip = 1;
         }
       }
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kKmaxThreads) kmax_kernel(const FwdParams p) {
       long long row0 = unit * p.ku;  // contiguous: units in row order
       if (p.block_table != nullptr) {
         const int b = head / p.Hkv, hkv = head % p.Hkv, key = y * p.ku, lp = key / p.page_size;
-        const int phys = __ldg(p.block_table + (size_t)b * p.max_pages + lp);
+        const int phys = load_written(p.block_table + (size_t)b * p.max_pages + lp);
         row0 = ((long long)phys * p.Hkv + hkv) * p.page_size + (key - lp * p.page_size);
       }
       bulk_load(base + s * kKmaxGroupBytes + k * ubytes, src + (size_t)row0 * D, ubytes, bars + 8u * s);
@@ -200,23 +200,23 @@ __global__ void __launch_bounds__(256) rowbound_kernel(const __grid_constant__ F
   wait_for_previous();
   const int row = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (row >= p.rows) return;
-  const int s0 = __ldg(p.row_ptr + row), s1 = __ldg(p.row_ptr + row + 1);
+  const int s0 = load_written(p.row_ptr + row), s1 = load_written(p.row_ptr + row + 1);
   float km = 0.f, vm = 0.f;
   if (s0 >= 0 && s1 >= s0 && (long long)s1 <= p.slot_capacity) {  // else the forward reports it
     const int bh = row / p.NQT, b = bh / p.H, h = bh % p.H, hkv = h / p.g;
     const float* kh = p.kmax + (size_t)(b * p.Hkv + hkv) * p.NKU;
     const float* vh = p.vmax + (size_t)(b * p.Hkv + hkv) * p.NKU;
-    const int kvl = (p.prow && p.kv_lens) ? __ldg(p.kv_lens + b) : 0x7fffffff;
+    const int kvl = (p.prow && p.kv_lens) ? load_written(p.kv_lens + b) : 0x7fffffff;
     const long long end = (long long)s1 * p.rk;
     for (long long i0 = (long long)s0 * p.rk + lane; i0 < end; i0 += 128) {
       int y4[4];  // four positions' reads at once: the pass is their latency
 #pragma unroll
-      for (int q = 0; q < 4; ++q) y4[q] = i0 + 32 * q < end ? __ldg(p.slot_ku + i0 + 32 * q) : -1;
+      for (int q = 0; q < 4; ++q) y4[q] = i0 + 32 * q < end ? load_written(p.slot_ku + i0 + 32 * q) : -1;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const bool valid = y4[q] >= 0 && y4[q] < p.NKU;
-        km = fmaxf(km, valid ? __ldg(kh + y4[q]) : 0.f);
-        vm = fmaxf(vm, valid ? __ldg(vh + y4[q]) : 0.f);
+        km = fmaxf(km, valid ? load_written(kh + y4[q]) : 0.f);
+        vm = fmaxf(vm, valid ? load_written(vh + y4[q]) : 0.f);
       }
       if (!p.prow) continue;
 #pragma unroll
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(256) rowbound_kernel(const __grid_constant__ F
         if (valid) {
           const int key = y * p.ku;
           const int lp = key / p.page_size;
-          int phys = (lp < p.max_pages) ? __ldg(p.block_table + (size_t)b * p.max_pages + lp) : -1;
+          int phys = (lp < p.max_pages) ? load_written(p.block_table + (size_t)b * p.max_pages + lp) : -1;
           if (phys < 0 || phys >= p.num_pages) {
             if (key < kvl) record_status(p.control, -7, kSitePlanRange + 4);
             phys = 0;
