@@ -85,9 +85,13 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
   int* s_page = resize_s + 3 * n;
   __shared__ int warp_s[33];
   __shared__ int s_pairs;
+  __shared__ unsigned long long s_need;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = c.max_pages * c.page;
-  if (tid == 0) s_pairs = 0;
+  if (tid == 0) {
+    s_pairs = 0;
+    s_need = 0;
+  }
   for (int i = tid; i < n; i += kThreads) {
     const int s = seqs ? __ldg(seqs + i) : i, want = __ldg(new_lens + i);
     const bool known = s >= 0 && s < c.max_seqs;
@@ -187,6 +191,11 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
   }
   int total;
   int off = block_scan(sum, warp_s, total);
+  if (__syncthreads_or(sum > (1 << 20))) {  // (4096 tables of 2^26 entries: the sum may pass 32 bits)
+    atomicAdd(&s_need, (unsigned long long)sum);
+    __syncthreads();
+    total = (int)min(s_need, 0x7fffffffull);
+  }
   // From here on s_page: where an item's pages start in the list, and in the
   // sign bit whether the first of them replaces the shared page.
 #pragma unroll

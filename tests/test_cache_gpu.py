@@ -664,6 +664,16 @@ def test_two_threads_on_the_default_stream(bsa):
     assert not bad, bad[:3]
 
 
+def test_growth_past_32_bits_of_pages_is_refused(bsa):
+    # 64 sequences of 2^26 pages each: 2^32 in all, for a pool of 8.
+    c = bsa.cache_create(8, 1, 16, 64, 64, 1 << 26)
+    bsa.cache_resize(c, i32(40), i32(5))
+    bsa.cache_resize(c, torch.full((64,), 1 << 30, dtype=torch.int32, device="cuda"))
+    assert bsa.cache_status(c) == (-5, (1 << 31) - 1 - 5)
+    assert c.lens.tolist() == [0] * 5 + [40] + [0] * 58 and c.refs.tolist() == [1] * 3 + [0] * 5
+    assert c.block_table[5, :4].tolist() == [0, 1, 2, -1] and int(c.block_table[6].max()) == -1
+
+
 def test_append_leaves_shared_pages_alone(bsa):
     gen = torch.Generator().manual_seed(71)
     m = OC.CacheModel(12, 2, 16, 64, 4, 4, seed=7)
