@@ -250,7 +250,8 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
         with _kept_lock:  # the call's kernels are enqueued one after another
             ws = _kept.get(c._index)
             if ws is None:
-                ws = _kept[c._index] = torch.empty(_KEPT_BYTES, dtype=torch.uint8, device=c.device)
+                with torch.cuda.stream(torch.cuda.default_stream(c.device)):  # (not a given stream's caller's)
+                    ws = _kept[c._index] = torch.empty(_KEPT_BYTES, dtype=torch.uint8, device=c.device)
             _call(c, "attention", *args, ws.data_ptr(), need, handle)
     else:
         ws = _scratch(c, need, stream)

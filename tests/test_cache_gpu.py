@@ -637,6 +637,31 @@ def test_calls_on_another_stream_use_memory_of_their_own(bsa):
             assert torch.equal(x, y)
 
 
+def test_scratch_of_the_default_stream_is_its_own(bsa):
+    """A first call on the (given) default stream, from another current stream
+    with work under way on memory that it has given back: the scratch that
+    default-stream calls share must not be that memory."""
+    m, c = filled(bsa, [700, 30], 2, 64, 64, 128, "e4m3", 12, seed=31)
+    q = rand(torch.Generator().manual_seed(32), 2, 8, 1, 128).cuda()
+    want = bsa.cache_attention(c, q)
+    torch.cuda.synchronize()
+    from block_sparse_attention_plan_gb300 import _cache
+    was, _cache._kept = _cache._kept, {}
+    try:
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            back = torch.empty(_cache._KEPT_BYTES, dtype=torch.uint8, device="cuda")
+            at = back.data_ptr()
+            del back
+            bsa.cache_attention(c, q, stream=torch.cuda.default_stream())
+        torch.cuda.synchronize()
+        assert _cache._kept[c.device.index].data_ptr() != at
+    finally:
+        _cache._kept = was
+    got = bsa.cache_attention(c, q)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_two_threads_on_the_default_stream(bsa):
     """Calls of two host threads on one stream share their scratch in turn."""
     import threading
