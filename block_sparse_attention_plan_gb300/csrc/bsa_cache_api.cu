@@ -222,6 +222,8 @@ bsa_status bsa_cache_attention(const bsa_cache* cache, const bsa_rows* q, const 
   AttnLayout l;
   if ((st = attn_layout(p.c, B, Hq, nq, NKB, bk, mask != nullptr, &l)) != BSA_OK) return st;
   if (!seqs && B > p.c.max_seqs) return BSA_ERR_INVALID_ARG;
+  // Rows that several CTAs write must not be one.
+  if ((B > 1 && !o->stride_b) || (Hq > 1 && !o->stride_h) || (nq > 1 && !o->stride_t)) return BSA_ERR_INVALID_ARG;
   if (workspace_bytes < l.bytes) return BSA_ERR_WORKSPACE;
   int dev = 0, sms = 0;
   if ((st = check_device(&dev)) != BSA_OK || (st = sms_of(dev, &sms)) != BSA_OK) return st;

@@ -349,8 +349,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       const int s = p.seqs ? __ldg(p.seqs + b) : b;
       if (s < -1 || s >= p.c.max_seqs) cache_error(p.c.control, BSA_ERR_INVALID_ARG, b);
     }
-    for (int i = tid; i < (h1 - h0) * p.M * (D / 4); i += kAttnThreads) {
-      const int c4 = i % (D / 4), r = i / (D / 4), m = r % p.M, h = h0 + r / p.M;
+    const int c4 = tid % (D / 4);
+    for (int r = tid / (D / 4); r < (h1 - h0) * p.M; r += kAttnThreads / (D / 4)) {
+      const int m = r % p.M, h = h0 + r / p.M;
       store2(p, o_row(p, b, h, m) + 4 * c4, make_float4(0.f, 0.f, 0.f, 0.f));
       if (c4 == 0 && p.lse) *lse_row(p, b, h, m) = -INFINITY;
     }

@@ -637,7 +637,8 @@ bsa_status bsa_cache_append(const bsa_cache* cache, const bsa_rows* k, const bsa
  *   O = sum_j p_j V_j / sum_j p_j, p_j = exp(scale <q, K_j> - m), over the keys
  * j below the sequence's length that the mask selects; O = 0 and LSE = -inf
  * where none is left.
- * q: [B][Hq][nq][d], o: the same shape (written), both of `dtype`; LSE: device
+ * q: [B][Hq][nq][d], o: the same shape (written; no stride of 0 between several
+ *   rows), both of `dtype`; LSE: device
  *   fp32 [B][Hq][nq] contiguous (written), or NULL.  Hq a multiple of Hkv.
  * seqs: device int32 [B] or NULL (sequences 0 .. B-1); the same sequence may
  *   be named several times.

@@ -85,6 +85,9 @@ def test_call_arguments(lib, buf):
     def att(q=r, o=r, lse=p, dt=0, mask=None, NKB=0, bk=0, B=1, Hq=2, nq=1, flags=0, scale=0.0, ws=p, n=1 << 30):
         return lib.bsa_cache_attention(c, q, o, lse, dt, None, mask, NKB, bk, B, Hq, nq, flags, scale, ws, n, None)
 
+    for n, bad in ((dict(B=2), C.RowsC(buf.at, 0, 128, 128)), (dict(Hq=4), C.RowsC(buf.at, 512, 0, 128)),
+                   (dict(nq=2), C.RowsC(buf.at, 512, 256, 0))):
+        assert att(o=bad, **n) == -1, n                         # rows of o that are one
     assert att(B=0) == -1 and att(Hq=3) == -1 and att(nq=0) == -1 and att(B=5) == -1
     assert att(flags=2) == -1 and att(dt=2) == -2 and att(scale=float("nan")) == -1 and att(scale=float("inf")) == -1
     assert att(mask=p, NKB=4, bk=48) == -2 and att(mask=p, NKB=0, bk=64) == -1
