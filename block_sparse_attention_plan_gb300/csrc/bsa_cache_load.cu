@@ -37,10 +37,10 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
   const int seq = p.seqs ? __ldg(p.seqs + b) : b;
   const bool known = seq >= 0 && seq < c.max_seqs;
   int len = known ? load_written(c.lens + seq) : 0;
-  len = min(max(len, 0), min(p.Nk, c.max_pages * c.page));
+  len = min(max(len, 0), c.max_pages * c.page);
   const bool isv = blockIdx.z != 0;
   if (blockIdx.x == 0 && h == 0 && tid == 0 && !isv) {
-    p.lens[b] = len;
+    p.lens[b] = len;  // (whole: the queries are the last tokens, of which Nk may leave out some)
     if (!known && seq != -1) cache_error(c.control, BSA_ERR_INVALID_ARG, b);
   }
   // What a forward resets ahead of its passes.
@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
   const long long all = (long long)gridDim.x * gridDim.y * gridDim.z * kThreads;
   for (long long i = at; i < p.rows; i += all) p.fb_flag[i] = 0;
   if (at < p.control_words) p.control[at] = 0;
+  len = min(len, p.Nk);
   const uint8_t* codes = isv ? c.v : c.k;
   const float* scales = isv ? c.vs : c.ks;
   uint16_t* out = (isv ? p.v : p.k) + (size_t)bh * p.Nk * D;

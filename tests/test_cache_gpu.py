@@ -538,6 +538,29 @@ def test_forward_over_the_cache(bsa, kind, bq, bk, d, page, causal):
     assert_attention_close(o, lse, np.stack([r[0] for r in refs]), np.stack([r[1] for r in refs]), f"{kind} {bq} {d}")
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_forward_over_the_first_tokens(bsa, causal):
+    """A plan of fewer keys than the sequences hold: the queries stay the last
+    tokens, so causality leaves out none, some or (300 of 512) more keys."""
+    m, c = filled(bsa, [900, 600, 300], 2, 64, 32, 64, "e4m3", 16, seed=44)
+    Nq, Nk = 128, 512
+    gen = torch.Generator().manual_seed(45)
+    mask = (torch.rand(3, 2, 2, 8, generator=gen) < 0.7).to(torch.uint8)
+    q = rand(gen, 3, 2, Nq, 64)
+    p = bsa.plan(mask.cuda(), 64, 64, 1)
+    o, lse = bsa.cache_forward(p, c, q.cuda(), causal=causal)
+    assert bsa.sync_status(p)[0] == 0 and bsa.cache_status(c) == (0, 0)
+    from compare import assert_attention_close
+    refs = []
+    for b in range(3):
+        k, v = m.values(b)
+        n = min(k.shape[1], Nk)
+        keep = keep_of(k.shape[1], Nq, 2, causal)[:, :, :n]
+        keep &= mask[b].numpy().astype(bool).repeat(64, 1).repeat(64, 2)[:, :, :n]
+        refs.append(OC.attention(q[b].double().numpy(), k[:, :n], v[:, :n], keep)[:2])
+    assert_attention_close(o, lse, np.stack([r[0] for r in refs]), np.stack([r[1] for r in refs]), f"{causal}")
+
+
 # ------------------------------------------------------- a run of them together
 
 def test_serving_steps_together_and_captured(bsa):
