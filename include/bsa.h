@@ -671,7 +671,10 @@ bsa_status bsa_cache_attention(const bsa_cache* cache, const bsa_rows* q, const 
  * Q, O: device bf16 [B][Hq][Nq][d]; LSE fp32 [B][Hq][Nq]; flags as
  *   bsa_forward_ex; workspace: device, 256-byte aligned,
  *   bsa_cache_forward_workspace_bytes bytes (the keys and values in bf16).
- * Scales other than powers of two round the values to bf16.
+ * Scales other than powers of two round the values to bf16.  As in bsa_forward,
+ * a NaN among the values (not the keys) of a tile that some row of a 128-row
+ * q-tile selects reaches the other rows of the q-tile too; bsa_cache_attention
+ * keeps it to the rows that attend it.
  * Other errors as bsa_forward_ex; BSA_ERR_PLAN_MISMATCH for a plan of other
  * heads.  Kernel errors are reported by bsa_sync_status (the plan's) and
  * bsa_cache_status (the table's).
