@@ -169,7 +169,7 @@ def _list(c: Cache, t: Optional[torch.Tensor], name: str, n: Optional[int] = Non
     """Pointer of an int32 list on the cache's device (None stays None)."""
     if t is None:
         return None
-    if (t.dtype != torch.int32 or t.device != c.device or t.dim() != 1 or not t.is_contiguous()
+    if (t.dtype != torch.int32 or t.get_device() != c._index or t.dim() != 1 or not t.is_contiguous()
             or (n is not None and t.shape[0] != n)):
         raise ValueError(f"{name} must be a contiguous CUDA int32 tensor" + (f" [{n}]" if n is not None else ""))
     return t.data_ptr()
@@ -177,7 +177,7 @@ def _list(c: Cache, t: Optional[torch.Tensor], name: str, n: Optional[int] = Non
 
 def _rows(c: Cache, t: torch.Tensor, name: str):
     """bsa_rows of a tensor [batch, heads, tokens, d], by reference."""
-    if t.dtype not in _ELEMENTS or t.device != c.device or t.dim() != 4 or t.stride(3) != 1:
+    if t.dtype not in _ELEMENTS or t.get_device() != c._index or t.dim() != 4 or t.stride(3) != 1:
         raise ValueError(f"{name} must be a 4-dimensional CUDA bfloat16 or float16 tensor with contiguous rows")
     b, h, r, _ = t.stride()
     if (b | h | r) & 7:  # a dimension of one element has no stride of its own
@@ -198,8 +198,8 @@ def cache_append(c: Cache, k: torch.Tensor, v: torch.Tensor, seqs: Optional[torc
     if h != c.heads or d != c.d:
         raise ValueError("k and v must be [n, Hkv, T, d] of the cache's Hkv and d")
     _call(c, "append", c._ref, _rows(c, k, "k"), _rows(c, v, "v"), _ELEMENTS[k.dtype],
-          _list(c, seqs, "seqs", n), _list(c, counts, "counts", n), _list(c, start, "start", n), n, T,
-          _stream(c, stream))
+          seqs if seqs is None else _list(c, seqs, "seqs", n), counts if counts is None else _list(c, counts, "counts", n),
+          start if start is None else _list(c, start, "start", n), n, T, _stream(c, stream))
 
 
 def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = None,
@@ -244,8 +244,9 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
             c._workspace_bytes.clear()
         c._workspace_bytes[key] = need
     handle = _stream(c, stream)
-    args = (c._ref, qr, _rows(c, out, "out"), lse.data_ptr(), _ELEMENTS[q.dtype], _list(c, seqs, "seqs", B), mptr, NKB,
-            bk, B, Hq, nq, CACHE_CAUSAL if causal else 0, 0.0 if scale is None else scale)
+    args = (c._ref, qr, _rows(c, out, "out"), lse.data_ptr(), _ELEMENTS[q.dtype],
+            seqs if seqs is None else _list(c, seqs, "seqs", B), mptr, NKB, bk, B, Hq, nq,
+            CACHE_CAUSAL if causal else 0, 0.0 if scale is None else scale)
     if handle == 0 and need <= _KEPT_BYTES:
         with _kept_lock:  # the call's kernels are enqueued one after another
             ws = _kept.get(c._index)
