@@ -64,6 +64,21 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float inv, bool finite)
   return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
+// a * b and a / b rounded to odd (towards zero, the last bit set if anything was
+// cut off): a rounding to the codes' few bits then gives what it would of the
+// exact value, ties included.
+__device__ __forceinline__ float odd_if(float x, float rest) {
+  return rest != 0.f && fabsf(x) < INFINITY ? __uint_as_float(__float_as_uint(x) | 1u) : x;
+}
+__device__ __forceinline__ float mul_odd(float a, float b) {
+  const float p = __fmul_rz(a, b);
+  return odd_if(p, fmaf(a, b, -p));
+}
+__device__ __forceinline__ float div_odd(float a, float b) {
+  const float q = __fdiv_rz(a, b);
+  return odd_if(q, fmaf(-q, b, a));
+}
+
 // The same for a scale that is no power of two (a cache filled by others).
 template <int KIND, bool FP16>
 __device__ __noinline__ uint2 encode8_div(uint4 x, float scale) {
@@ -72,7 +87,7 @@ __device__ __noinline__ uint2 encode8_div(uint4 x, float scale) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 f = elems_to_float2(w[e], FP16);
-    q[e] = encode2<KIND>(f.x / scale, f.y / scale);
+    q[e] = encode2<KIND>(div_odd(f.x, scale), div_odd(f.y, scale));
   }
   return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
@@ -85,8 +100,8 @@ __device__ __noinline__ uint2 recode8(uint2 old, float ratio) {
   for (int e = 0; e < 2; ++e) {
     const uint2 hh = codes_to_half4<KIND>(e ? old.y : old.x);
     const float2 f0 = half2_to_float2(hh.x), f1 = half2_to_float2(hh.y);
-    q[2 * e] = encode2<KIND>(f0.x * ratio, f0.y * ratio);
-    q[2 * e + 1] = encode2<KIND>(f1.x * ratio, f1.y * ratio);
+    q[2 * e] = encode2<KIND>(mul_odd(f0.x, ratio), mul_odd(f0.y, ratio));
+    q[2 * e + 1] = encode2<KIND>(mul_odd(f1.x, ratio), mul_odd(f1.y, ratio));
   }
   return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }

@@ -722,6 +722,41 @@ def test_growth_past_32_bits_of_pages_is_refused(bsa):
     assert c.block_table[5, :4].tolist() == [0, 1, 2, -1] and int(c.block_table[6].max()) == -1
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_rounds_once_at_scales_of_others(bsa, kind):
+    """Scales that are no powers of two, where fp32 would round code * was /
+    scale, or x / scale, to a tie that the exact value is not."""
+    ratio = {}  # odd codes c, ratios r in [1/2, 1): c r is not, but rounds to, k + 1/2
+    for c in range(5, 127, 2):
+        for k in range(c // 2, c):
+            r = np.float32((k + 0.5) / c)
+            if 0.5 <= r < 1 and float(r) * c != k + 0.5 and np.float32(r * np.float32(c)) == k + 0.5:
+                ratio[float(r)] = c
+    ratios = np.array(sorted(ratio), np.float32)[:128]
+    assert len(ratios) == 128
+    m = OC.CacheModel(128, 1, 16, 128, 128, 1, kind, seed=3)
+    assert m.resize([16] * 128) == 0
+    vals = np.arange(1, 128) if kind == "int8" else np.arange(1, 0x7f)
+    for w in range(2):  # every code, either sign, at a scale that grows to 1
+        m.codes[w][..., :len(vals)] = vals.astype(np.uint8)
+        m.codes[w][:, :, 8:, :len(vals)] = (-vals).astype(np.int8).view(np.uint8) if kind == "int8" else vals + 0x80
+        m.scales[w][m.table[:, 0], 0, 0] = ratios
+    c = upload(bsa, m)
+    x = torch.full((128, 1, 1, 128), 1.0 * OC.TOP[kind]).to(torch.bfloat16)
+    m.append(x.double().numpy(), x.double().numpy(), range(128), None, [5] * 128)
+    bsa.cache_append(c, x.cuda(), x.cuda(), start=i32(*[5] * 128))
+    assert (m.scales[0][m.table[:, 0]] == 1).all()
+    assert_state(c, m)
+    # x / scale, the scale kept: every bf16 number from 2^-3 to 2^5 on each scale in [1/2, 1).
+    m.scales[0][m.table[:, 0], 0, 0] = m.scales[1][m.table[:, 0], 0, 0] = ratios
+    c = upload(bsa, m)
+    x = (torch.arange(1024, dtype=torch.int16) + 0x3e00).view(torch.bfloat16).reshape(1, 1, 8, 128).repeat(128, 1, 1, 1)
+    m.append(x.double().numpy(), -x.double().numpy(), range(128), None, [0] * 128)
+    bsa.cache_append(c, x.cuda(), -x.cuda(), start=i32(*[0] * 128))
+    assert_state(c, m)
+    assert bsa.cache_status(c) == (0, 0)
+
+
 def test_append_leaves_shared_pages_alone(bsa):
     gen = torch.Generator().manual_seed(71)
     m = OC.CacheModel(12, 2, 16, 64, 4, 4, seed=7)
