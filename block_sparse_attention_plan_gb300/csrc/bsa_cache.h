@@ -17,6 +17,7 @@ constexpr int kCacheStatus = 0;
 constexpr int kCacheDetail = 1;
 constexpr int kCacheLive = 2;    // held pages the last compaction found
 constexpr int kCachePairs = 3;   // page copies queued for the copy kernel
+constexpr int kCacheTaken = 4;   // pages that the last resize took: entries of list_a
 constexpr int kCacheScratch = 16;
 
 // Device view of a cache, by value to every kernel.

@@ -230,7 +230,10 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
     }
     if (active && refs <= 1) {
       float scale = scale_for<KIND>(amax);
-      if (others) scale = fmaxf(scale, was);
+      // 0: nothing has been stored in the block since the sequence entered it
+      // (the same for what no scale is: memory that was never written).
+      const bool stored = was > 0.f && was < INFINITY;
+      if (stored) scale = fmaxf(scale, was);
       const bool grown = others && scale != was;
       if (ut == 0 && (!others || grown)) *scale_p = scale;
       uint8_t* at = (isv ? c.v : c.k) + first * c.d + ut * 8;
@@ -244,12 +247,12 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
         for (int j = 0; j < kVec; ++j)
           if (fresh >> j & 1u) *reinterpret_cast<uint2*>(at + j * tpu * 8) = encode8_div<KIND, FP16>(x[j], scale);
       }
-      if (grown && old) {  // the codes of the other tokens move to the larger scale
+      if (grown && old) {  // the codes of the other tokens move to the larger scale, or become 0
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
           if (old >> j & 1u) {
             uint2* o = reinterpret_cast<uint2*>(at + j * tpu * 8);
-            *o = recode8<KIND>(*o, was / scale);
+            *o = stored ? recode8<KIND>(*o, was / scale) : make_uint2(0u, 0u);
           }
       }
     }

@@ -65,6 +65,11 @@ __device__ __forceinline__ unsigned held_pages(const CacheDev& c, int p0) {
   return bits;
 }
 
+// A block that a sequence enters (one wholly past its old length) gets scale 0,
+// "nothing stored": what the page's last holder left there is no scale of the
+// tokens to come.  A growth by one token, a step of decoding, writes none: the
+// token is alone in such a block, so storing it sets the scale.
+//
 // One CTA.  Everything the decisions need is read once, into shared memory, so
 // that a step of a serving loop (a token more for each sequence, no page more)
 // is a chain of four reads: list, length, last page, its count.
@@ -227,6 +232,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
     if (tid == 0) {
       cache_error(c.control, BSA_ERR_WORKSPACE, total - found);
       c.control[kCachePairs] = 0;
+      c.control[kCacheTaken] = 0;
     }
     return;
   }
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
     if (s < 0) continue;
     const int want = s_want[i], hp = pages_of(s_have[i], c.page), wp = pages_of(want, c.page);
     int32_t* row = c.table + (size_t)s * c.max_pages;
-    const int32_t* list = c.list_a() + (s_page[i] & 0x7fffffff);
+    int32_t* list = c.list_a() + (s_page[i] & 0x7fffffff);
     const int replaced = s_page[i] < 0 ? 1 : 0;
     if (replaced && lane == 0) {
       const int old = __ldcg(row + hp - 1), fresh = __ldcg(list);
@@ -252,10 +258,39 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
       row[j] = p;
     }
     for (int j = wp + lane; j < hp; j += 32) row[j] = -1;
-    if (lane == 0) c.lens[s] = want;
+    if (lane == 0) {
+      c.lens[s] = want;
+      // Left in the list are the pages whose scales the copy kernel clears: not a
+      // copied one, and not that of a growth by one token (lane 0 has read it).
+      if (replaced || (wp > hp && want == s_have[i] + 1)) list[0] = -1;
+    }
   }
   __syncthreads();
-  if (tid == 0) c.control[kCachePairs] = s_pairs;
+  // Scales of the copied pages, then (others may be copying from the page that
+  // one keeps) 0 for the blocks past the old length of pages that were held.
+  const int blocks = c.page / c.sb, scales = c.Hkv * blocks;
+  for (long long x = tid; x < (long long)s_pairs * scales; x += kThreads) {
+    const int pr = (int)(x / scales), q = (int)(x - (long long)pr * scales);
+    const size_t from = (size_t)__ldcg(c.pair_src() + pr) * scales + q, to = (size_t)__ldcg(c.pair_dst() + pr) * scales + q;
+    c.ks[to] = c.ks[from];
+    c.vs[to] = c.vs[from];
+  }
+  __syncthreads();
+  for (int i = warp; i < n; i += kThreads / 32) {
+    const int s = s_seq[i], have = s_have[i], kept = (have % c.page + c.sb - 1) / c.sb;
+    if (s < 0 || s_want[i] <= have + 1 || kept == 0 || kept == blocks) continue;
+    const int p = __ldcg(c.table + (size_t)s * c.max_pages + have / c.page);
+    if (p < 0 || p >= c.num_pages) continue;
+    for (int x = lane; x < c.Hkv * (blocks - kept); x += 32) {
+      const size_t at = ((size_t)p * c.Hkv + x / (blocks - kept)) * blocks + kept + x % (blocks - kept);
+      c.ks[at] = 0.f;
+      c.vs[at] = 0.f;
+    }
+  }
+  if (tid == 0) {
+    c.control[kCachePairs] = s_pairs;
+    c.control[kCacheTaken] = total;
+  }
 }
 
 // Freeing sequences needs no order: one CTA per item, which is skipped if an
@@ -416,20 +451,22 @@ __global__ void __launch_bounds__(kThreads) check_pairs_kernel(const CacheDev ds
 }
 
 // Moves the contents of the queued pairs (and, after a compaction, rewrites the
-// table).  Work items of 16 KB of codes: 256 threads x 4 independent 16-byte
-// copies, so that eight CTAs keep 128 KB in flight per SM; a pair's scales are
-// one more item.
+// table; after a resize, which has copied the pairs' scales, clears those of the
+// pages taken).  Work items of 16 KB of codes: 256 threads x 4 independent
+// 16-byte copies, so that eight CTAs keep 128 KB in flight per SM; a pair's
+// scales are one more item.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyBytes = kCopyThreads * 16 * 4;
+enum class CopyFor { kPages, kResize, kCompact };
 
-__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CacheDev dst, const CacheDev src, int remap) {
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CacheDev dst, const CacheDev src, CopyFor what) {
   next_may_launch();
   wait_for_previous();
   const int tid = threadIdx.x;
   const int pairs = __ldcg(dst.control + kCachePairs);
   const long long bytes = (long long)dst.Hkv * dst.page * dst.d;  // of a page of K or V: a multiple of 1 KB
   const int chunks = (int)((bytes + kCopyBytes - 1) / kCopyBytes);
-  const int per = 2 * chunks + 1;
+  const int per = 2 * chunks + (what == CopyFor::kResize ? 0 : 1);
   const int scales = dst.Hkv * (dst.page / dst.sb);
   const long long items = (long long)pairs * per;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
@@ -453,7 +490,16 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CacheDev dst, 
       }
     }
   }
-  if (remap && pairs > 0) {
+  if (what == CopyFor::kResize) {
+    const int all = __ldcg(dst.control + kCacheTaken) * scales;  // (below 2^31: pool rows are)
+    for (int x = blockIdx.x * kCopyThreads + tid; x < all; x += gridDim.x * kCopyThreads) {
+      const int p = __ldcg(dst.list_a() + x / scales);
+      if (p < 0) continue;
+      dst.ks[(size_t)p * scales + x % scales] = 0.f;
+      dst.vs[(size_t)p * scales + x % scales] = 0.f;
+    }
+  }
+  if (what == CopyFor::kCompact && pairs > 0) {
     const int L = __ldcg(dst.control + kCacheLive);
     const long long entries = (long long)dst.max_seqs * dst.max_pages;
     for (long long e = (long long)blockIdx.x * kCopyThreads + tid; e < entries; e += (long long)gridDim.x * kCopyThreads) {
@@ -493,7 +539,7 @@ cudaError_t launch_cache_resize(const CacheDev& c, const int32_t* seqs, const in
   if (e != cudaSuccess) return e;
   e = launch_after(resize_kernel, dim3(1), dim3(kThreads), smem, s, c, seqs, new_lens, n);
   if (e != cudaSuccess) return e;
-  return launch_after(copy_kernel, dim3(copy_grid(c, n, sm_count())), dim3(kCopyThreads), 0, s, c, c, 0);
+  return launch_after(copy_kernel, dim3(copy_grid(c, n, sm_count())), dim3(kCopyThreads), 0, s, c, c, CopyFor::kResize);
 }
 
 cudaError_t launch_cache_fork(const CacheDev& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
@@ -503,7 +549,7 @@ cudaError_t launch_cache_fork(const CacheDev& c, const int32_t* src, const int32
 cudaError_t launch_cache_compact(const CacheDev& c, int sms, cudaStream_t s) {
   const cudaError_t e = launch_after(compact_kernel, dim3(1), dim3(kThreads), 0, s, c);
   if (e != cudaSuccess) return e;
-  return launch_after(copy_kernel, dim3(copy_grid(c, c.num_pages / 2 + 1, sms)), dim3(kCopyThreads), 0, s, c, c, 1);
+  return launch_after(copy_kernel, dim3(copy_grid(c, c.num_pages / 2 + 1, sms)), dim3(kCopyThreads), 0, s, c, c, CopyFor::kCompact);
 }
 
 cudaError_t launch_cache_copy(const CacheDev& dst, const CacheDev& src, const int32_t* dst_pages,
@@ -512,7 +558,7 @@ cudaError_t launch_cache_copy(const CacheDev& dst, const CacheDev& src, const in
   const cudaError_t e =
       launch_after(check_pairs_kernel, dim3(1), dim3(kThreads), 0, s, dst, src, same, dst_pages, src_pages, n);
   if (e != cudaSuccess) return e;
-  return launch_after(copy_kernel, dim3(copy_grid(dst, n, sm_count())), dim3(kCopyThreads), 0, s, dst, src, 0);
+  return launch_after(copy_kernel, dim3(copy_grid(dst, n, sm_count())), dim3(kCopyThreads), 0, s, dst, src, CopyFor::kPages);
 }
 
 }  // namespace bsa

@@ -490,7 +490,8 @@ bsa_status bsa_attention_host(const uint8_t* mask, int B, int H, int NQB, int NK
  * is read on the host; every pointer in it is a device buffer owned by the
  * caller:
  *   k, v         1-byte codes [num_pages][Hkv][page_size][d], 16-byte aligned
- *   k_scale, v_scale  fp32 [num_pages][Hkv][page_size / scale_block]
+ *   k_scale, v_scale  fp32 [num_pages][Hkv][page_size / scale_block], finite and
+ *                positive; 0: the sequence has stored nothing in the block
  *   block_table  int32 [max_seqs][max_pages], -1 = no page
  *   seq_lens     int32 [max_seqs], tokens held by each sequence
  *   page_refs    int32 [num_pages], sequences that hold each page (0 = free)
@@ -564,8 +565,11 @@ bsa_status bsa_cache_status(const bsa_cache* cache, void* stream, int32_t* detai
  * which other sequences hold too gets a page of its own there, with the
  * contents copied (of several such sequences in one call, those later in the
  * list come last, and the one that is left alone with the page keeps it).
- * New tokens' contents are what bsa_cache_append then stores.  If the free
- * pages do not suffice nothing is changed.  n <= 4096 (any n if both lists are
+ * New tokens' contents are what bsa_cache_append then stores: scales of blocks
+ * wholly past the old length become 0, whatever the pages' last holders left
+ * there.  (A growth by a single token leaves them as they are, for storing the
+ * token sets the one of its block; store it before the sequence grows further.)
+ * If the free pages do not suffice nothing is changed.  n <= 4096 (any n if both lists are
  * NULL).
  * Two kernels (one if new_lens is NULL), no synchronisation.
  */
@@ -618,7 +622,9 @@ bsa_status bsa_cache_copy_pages(const bsa_cache* dst, const bsa_cache* src, cons
  * Scale of a block: the smallest power of two, at least 2^-100, that takes the
  * largest finite |x| of the stored tokens into the codes' range; if the
  * sequence has other tokens in the block, the larger of that and the block's
- * scale, and if that grows their codes are re-rounded to it.  Codes are
+ * scale, and if that grows their codes are re-rounded to it (tokens that a block
+ * of scale 0, infinity or NaN holds have not been stored: their codes become 0).
+ * Codes are
  * rounded to nearest, ties to even; infinities saturate; NaN is stored as NaN
  * (E4M3) or 0 (INT8).  Rows of pages that hold no token of the sequence are
  * left as they were.  One kernel.

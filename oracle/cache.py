@@ -112,6 +112,11 @@ class CacheModel:
                 x[p] = x[old]
         self.refs, self.table = refs, table
         for s, n in items:
+            have = int(self.lens[s])
+            if n > have + 1:  # blocks wholly past the old length hold nothing yet: scale 0
+                for b in range(-(-have // self.sb), self._pages(n) * self.page // self.sb):
+                    for x in self.scales:
+                        x[table[s, b * self.sb // self.page], :, b % (self.page // self.sb)] = 0
             self.lens[s] = n
         return 0
 
@@ -162,9 +167,12 @@ class CacheModel:
                         rows = self.codes[w][page, h, r0:r0 + self.sb]
                         if others:
                             was = float(self.scales[w][page, h, r0 // self.sb])
-                            sc = max(sc, was)
-                            if sc != was:
-                                rows[others] = encode(decode(rows[others], self.kind) * (was / sc), self.kind)
+                            if 0 < was < math.inf:
+                                sc = max(sc, was)
+                                if sc != was:
+                                    rows[others] = encode(decode(rows[others], self.kind) * (was / sc), self.kind)
+                            else:  # nothing is stored in the block yet
+                                rows[others] = 0
                         rows[a - b0:b - b0] = encode(new / sc, self.kind)
                         self.scales[w][page, h, r0 // self.sb] = sc
                 a = b

@@ -1,0 +1,186 @@
+"""GPU tests of what the 8-bit cache promises beyond the plain path: pages that
+were used before, lists that are the cache's own, tables and lengths that are
+wrong, values and scales in masked places, long contexts."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as OC
+from test_cache_gpu import KINDS, i32, rand, upload
+
+pytestmark = pytest.mark.gpu
+
+
+def assert_state(c, m, what=""):
+    """Every array of the cache, bit for bit (scales may be NaN)."""
+    bits = lambda a: np.ascontiguousarray(a).view(np.uint8)
+    for name, got, want in (("table", c.block_table, m.table), ("lens", c.lens, m.lens), ("refs", c.refs, m.refs),
+                            ("k", c.k, m.codes[0]), ("v", c.v, m.codes[1]), ("k_scale", c.k_scale, m.scales[0]),
+                            ("v_scale", c.v_scale, m.scales[1])):
+        got = got.view(torch.uint8) if name in "kv" else got
+        assert np.array_equal(bits(got.cpu().numpy()), bits(want)), (what, name)
+
+
+def append_both(bsa, m, c, k, v, seqs, start, counts=None):
+    m.append(k.double().numpy(), v.double().numpy(), seqs, counts, start)
+    bsa.cache_append(c, k.cuda(), v.cuda(), seqs=i32(*seqs), start=i32(*start),
+                     counts=None if counts is None else i32(*counts))
+
+
+def assert_scales_of_their_tokens(c, seq, x, sb, kind, first=0):
+    """Every block of the sequence (from token `first` on) has the scale that its tokens x [heads, n, d]
+    need, and each value is off by two roundings at most: half a step each, 2^-4
+    of the value (or half the scale's smallest step, 2^-10) for E4M3, half the
+    scale for INT8."""
+    page, n = c.page_size, x.shape[1]
+    table = c.block_table[seq].tolist()
+    codes = c.k.view(torch.uint8).cpu().numpy()
+    for b0 in range(first, n, sb):
+        p, r = table[b0 // page], b0 % page
+        for h in range(x.shape[0]):
+            new = x[h, b0:b0 + sb].double().numpy()
+            sc = OC.scale_for(np.abs(new).max(), kind)
+            assert float(c.k_scale[p, h, r // sb]) == sc, (b0, h)
+            got = OC.decode(codes[p, h, r:r + new.shape[0]], kind) * sc
+            step = np.maximum(np.abs(new) * 2.0 ** -4, sc * 2.0 ** -10) if kind == "e4m3" else 0.5 * sc
+            assert (np.abs(got - new) <= 2.2 * step).all(), (b0, h)
+
+
+# ------------------------------------------------------- pages used before
+
+PIECES = [[(0, 100), (100, 28)], [(0, 32), (32, 32), (64, 64)], [(64, 64), (0, 64)], [(100, 28), (33, 67), (0, 33)]]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("pieces", PIECES)
+@pytest.mark.parametrize("page,sb,d", [(64, 64, 128), (32, 16, 64), (256, 128, 64)])
+def test_room_filled_in_pieces_on_used_pages(bsa, kind, pieces, page, sb, d):
+    m = OC.CacheModel(2 * 128 // page + 2, 2, page, d, 2, 8, kind, sb, seed=page)
+    c = upload(bsa, m)
+    g = torch.Generator().manual_seed(page)
+    full = 2 * max(128, page)
+    assert m.resize([full], [0]) == 0
+    bsa.cache_resize(c, i32(full), i32(0))
+    big = rand(g, 1, 2, full, d) * 2.0 ** 20
+    append_both(bsa, m, c, big, big, [0], [0])
+    m.resize([0], [0])
+    bsa.cache_free(c, i32(0))
+    assert m.resize([128], [1]) == 0
+    bsa.cache_resize(c, i32(128), i32(1))
+    assert_state(c, m, "handed out")
+    x = rand(g, 1, 2, 128, d)
+    for at, n in pieces:
+        append_both(bsa, m, c, x[:, :, at:at + n], x[:, :, at:at + n], [1], [at])
+        assert_state(c, m, f"piece {at}")
+    assert_scales_of_their_tokens(c, 1, x[0], sb, kind)
+    assert bsa.cache_status(c) == (0, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), 0.0, 1e30])
+def test_pools_that_were_never_written(bsa, kind, fill):
+    page, sb, d = 32, 16, 64
+    m = OC.CacheModel(8, 2, page, d, 2, 4, kind, sb, seed=3)
+    for s in m.scales:
+        s[:] = fill
+    c = upload(bsa, m)
+    g = torch.Generator().manual_seed(3)
+    x = rand(g, 1, 2, 90, d)
+    assert m.resize([90], [0]) == 0
+    bsa.cache_resize(c, i32(90), i32(0))
+    for at, n in ((0, 5), (5, 20), (60, 30), (25, 35)):
+        append_both(bsa, m, c, x[:, :, at:at + n], x[:, :, at:at + n], [0], [at])
+        assert_state(c, m, f"piece {at}")
+    assert_scales_of_their_tokens(c, 0, x[0], sb, kind)
+    # A step of one token at a time, into blocks whose scale nobody has written.
+    y = rand(g, 40, 1, 2, 1, d)
+    for i in range(30):
+        assert m.resize([i + 1], [1]) == 0
+        bsa.cache_resize(c, i32(i + 1), i32(1))
+        append_both(bsa, m, c, y[i], y[i], [1], [i])
+    assert_state(c, m, "steps")
+    assert bsa.cache_status(c) == (0, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_held_tokens_of_no_scale(bsa, kind):
+    """A table made by hand over memory that was never written: what lies in the
+    block counts for nothing, the first tokens stored set its scale."""
+    for fill in (float("nan"), float("inf"), -float("inf"), -2.0, 0.0):
+        m = OC.CacheModel(3, 2, 64, 64, 1, 2, kind, 64, seed=5)
+        m.table[0, :2], m.refs[:2], m.lens[0] = (1, 0), 1, 100
+        for s in m.scales:
+            s[:] = fill
+        c = upload(bsa, m)
+        x = rand(torch.Generator().manual_seed(5), 1, 2, 100, 64)
+        for at, n in ((10, 20), (70, 3), (0, 64), (64, 36)):
+            append_both(bsa, m, c, x[:, :, at:at + n], x[:, :, at:at + n], [0], [at])
+            assert_state(c, m, f"{fill} {at}")
+        assert_scales_of_their_tokens(c, 0, x[0], 64, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_blocks_past_a_shrunk_length(bsa, kind):
+    """What a sequence (or one that shares its page) stored past its present
+    length is no scale of what comes next; sharers keep theirs."""
+    m = OC.CacheModel(12, 2, 64, 64, 3, 3, kind, 16, seed=7)
+    c = upload(bsa, m)
+    g = torch.Generator().manual_seed(7)
+
+    def both(lens, seqs):
+        assert m.resize(lens, seqs) == 0
+        bsa.cache_resize(c, i32(*lens), i32(*seqs))
+        assert_state(c, m, f"resize {lens} {seqs}")
+
+    both([60], [0])
+    big = rand(g, 1, 2, 60, 64) * 2.0 ** 20
+    big[:, :, :20] *= 2.0 ** -20
+    append_both(bsa, m, c, big, big, [0], [0])
+    bsa.cache_fork(c, i32(0, 0), i32(1, 2))
+    m.fork([0, 0], [1, 2])
+    both([20, 33], [1, 2])
+    # In one call: 0 takes a copy (with all its blocks), 2 takes one (three blocks),
+    # 1 keeps the page; 1's and 2's other blocks begin anew, 0's stay.
+    both([70, 64, 50], [0, 2, 1])
+    x = rand(g, 1, 2, 60, 64)
+    x[:, :, :20] = big[:, :, :20]
+    append_both(bsa, m, c, x[:, :, 20:30], x[:, :, 20:30], [1], [20])
+    append_both(bsa, m, c, x[:, :, 40:50], x[:, :, 40:50], [1], [40])
+    append_both(bsa, m, c, x[:, :, 30:40], x[:, :, 30:40], [1], [30])
+    assert_state(c, m)
+    # (tokens 16 .. 19 were stored beside larger ones: that block's scale stays)
+    assert_scales_of_their_tokens(c, 1, x[0, :, :50], 16, kind, 32)
+    k = m.values(0)[0][:, 40:60]
+    want = big[0, :, 40:60].double().numpy()
+    assert np.abs(k - want).max() <= np.abs(want).max() * 2.0 ** -3
+    # Alone with its page: shrunk and grown again.
+    both([5], [2])
+    both([64], [2])
+    append_both(bsa, m, c, x[:, :, 16:26], x[:, :, 16:26], [2], [16])
+    append_both(bsa, m, c, x[:, :, 26:32], x[:, :, 26:32], [2], [26])
+    assert_state(c, m)
+    p = int(m.table[2, 0])
+    for h in range(2):
+        sc = OC.scale_for(float(x[0, h, 16:32].abs().max()), kind)
+        assert float(c.k_scale[p, h, 1]) == sc and float(c.v_scale[p, h, 1]) == sc
+    assert bsa.cache_status(c) == (0, 0)
+
+
+def test_scales_of_many_pages_and_copies(bsa):
+    """Growth of many sequences over many pages with many scales each: all those
+    of the pages taken are 0, all those of copied pages are the copied ones."""
+    rng = np.random.default_rng(12)
+    m = OC.CacheModel(3000, 3, 128, 64, 400, 12, "int8", 16, seed=12)
+    lens = rng.integers(1, 300, 200).astype(np.int32)
+    assert m.resize(lens) == 0
+    m.fork(range(200), range(200, 400))
+    for s in m.scales:
+        s[:] = np.exp2(rng.integers(-9, 9, s.shape))
+    c = upload(bsa, m)
+    seqs = rng.permutation(400).astype(np.int32)
+    want = np.concatenate([lens, lens])[seqs] + rng.integers(0, 500, 400).astype(np.int32)
+    want = np.minimum(want, 12 * 128).astype(np.int32)
+    bsa.cache_resize(c, torch.from_numpy(want).cuda(), torch.from_numpy(seqs).cuda())
+    assert m.resize(want, seqs) == 0
+    assert_state(c, m)
+    assert bsa.cache_status(c) == (0, 0)
