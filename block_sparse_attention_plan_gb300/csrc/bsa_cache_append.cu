@@ -28,6 +28,7 @@ namespace {
 using namespace dev;
 
 constexpr int kVec = 4;  // 16-byte chunks (8 elements) per thread and unit
+constexpr float kInvertible = 0x1p127f;  // scales below it have a normal reciprocal (a cache filled by others may hold it)
 
 // Larger of each two elements' magnitudes, as integers: of elements of one sign
 // these compare like the numbers, with infinity and then NaN above all others.
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
       const bool grown = others && scale != was;
       if (ut == 0 && (!others || grown)) *scale_p = scale;
       uint8_t* at = (isv ? c.v : c.k) + first * c.d + ut * 8;
-      if ((__float_as_uint(scale) & 0x7fffffu) == 0) {
+      if ((__float_as_uint(scale) & 0x7fffffu) == 0 && scale < kInvertible) {
         const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 2^-e of 2^e
 #pragma unroll
         for (int j = 0; j < kVec; ++j)

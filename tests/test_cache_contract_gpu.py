@@ -184,3 +184,20 @@ def test_scales_of_many_pages_and_copies(bsa):
     assert m.resize(want, seqs) == 0
     assert_state(c, m)
     assert bsa.cache_status(c) == (0, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_beside_tokens_of_the_largest_scales(bsa, kind):
+    """Scales up to 2^127 are powers of two too (a cache filled by others)."""
+    for e in (125, 126, 127):
+        m = OC.CacheModel(2, 1, 16, 64, 1, 1, kind, 16, seed=9)
+        assert m.resize([16]) == 0
+        for s in m.scales:
+            s[:] = 2.0 ** e
+        for x in m.codes:
+            x[:] = 0x08
+        c = upload(bsa, m)
+        x = rand(torch.Generator().manual_seed(e), 1, 1, 3, 64).clamp(-1.9, 1.9) * 2.0 ** 127
+        append_both(bsa, m, c, x, x * 2.0 ** -3, [0], [7])
+        assert OC.decode(m.codes[0][m.table[0, 0], 0, 7:10], kind).any()
+        assert_state(c, m, f"2^{e}")
