@@ -135,17 +135,17 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ca
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int unit_in = tid / tpu, ut = tid - unit_in * tpu;
   const int row = blockIdx.x / p.blocks, blk = blockIdx.x - row * p.blocks;
-  const int seq = LIST ? __ldg(p.seqs + row) : row;
+  const int seq = LIST ? load_written(p.seqs + row) : row;
   if constexpr (LIST) {
     bool twice = false;  // named by an earlier row: both would write one block
-    for (int j = tid; j < row; j += blockDim.x) twice |= __ldg(p.seqs + j) == seq;
+    for (int j = tid; j < row; j += blockDim.x) twice |= load_written(p.seqs + j) == seq;
     if (__syncthreads_or(twice && seq != -1)) {
       if (blk == 0 && blockIdx.y == 0 && tid == 0) cache_error(c.control, BSA_ERR_INVALID_ARG, row);
       return;
     }
   }
-  const int count = p.counts ? __ldg(p.counts + row) : p.T;
-  const int given = p.start ? __ldg(p.start + row) : 0;
+  const int count = p.counts ? load_written(p.counts + row) : p.T;
+  const int given = p.start ? load_written(p.start + row) : 0;
   const bool known = seq >= 0 && seq < c.max_seqs;
   const int len = known ? load_written(c.lens + seq) : 0;
   const int pos = p.start ? given : len - count;

@@ -113,7 +113,7 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
 
 // Length of batch row b's sequence (0 for a padded row or one out of range).
 __device__ __forceinline__ int seq_of(const CacheAttnParams& p, int b) {
-  const int s = p.seqs ? __ldg(p.seqs + b) : b;
+  const int s = p.seqs ? load_written(p.seqs + b) : b;
   return s >= 0 && s < p.c.max_seqs ? s : -1;
 }
 __device__ __forceinline__ int len_of(const CacheAttnParams& p, int b) {
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     const int b = p.mask ? e / p.c.Hkv : e;
     const int h0 = p.mask ? e % p.c.Hkv : 0, h1 = p.mask ? h0 + 1 : p.c.Hkv;
     if (tid == 0) {
-      const int s = p.seqs ? __ldg(p.seqs + b) : b;
+      const int s = p.seqs ? load_written(p.seqs + b) : b;
       if (s < -1 || s >= p.c.max_seqs) cache_error(p.c.control, BSA_ERR_INVALID_ARG, b);
     }
     const int c4 = tid % (D / 4);
@@ -492,10 +492,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     }
     if (p.mask && lane < 8 * NT) {
       const int k0 = tile * TK >> lbk;
-      if (k0 < p.NKB) sel.x = __ldg(f.mask + k0);
+      if (k0 < p.NKB) sel.x = load_written(f.mask + k0);
       if (TK > 32) {
         const int k1 = (tile * TK + 32) >> lbk;
-        if (k1 < p.NKB) sel.y = __ldg(f.mask + k1);
+        if (k1 < p.NKB) sel.y = load_written(f.mask + k1);
       }
     }
     return tile;
@@ -956,7 +956,7 @@ __global__ void __launch_bounds__(kTilesThreads) tiles_kernel(const __grid_const
     if (t < tiles) {
       const int k0 = t * p.tile >> lbk, k1 = p.bk < p.tile ? min(k0 + 1, p.NKB - 1) : k0;
 #pragma unroll 8
-      for (int i = 0; i < p.g; ++i) on |= __ldg(mrow + (size_t)i * p.NKB + k0) | __ldg(mrow + (size_t)i * p.NKB + k1);
+      for (int i = 0; i < p.g; ++i) on |= load_written(mrow + (size_t)i * p.NKB + k0) | load_written(mrow + (size_t)i * p.NKB + k1);
     }
     const unsigned bal = __ballot_sync(0xffffffffu, on != 0u);
     if (lane == 0) warp_s[warp] = __popc(bal);

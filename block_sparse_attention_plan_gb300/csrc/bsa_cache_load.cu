@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
   const CacheDev& c = p.c;
   const int tid = threadIdx.x;
   const int bh = blockIdx.y, b = bh / c.Hkv, h = bh % c.Hkv;
-  const int seq = p.seqs ? __ldg(p.seqs + b) : b;
+  const int seq = p.seqs ? load_written(p.seqs + b) : b;
   const bool known = seq >= 0 && seq < c.max_seqs;
   int len = known ? load_written(c.lens + seq) : 0;
   len = min(max(len, 0), c.max_pages * c.page);

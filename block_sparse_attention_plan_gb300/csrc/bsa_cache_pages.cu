@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
     s_need = 0;
   }
   for (int i = tid; i < n; i += kThreads) {
-    const int s = seqs ? __ldg(seqs + i) : i, want = __ldg(new_lens + i);
+    const int s = seqs ? load_written(seqs + i) : i, want = load_written(new_lens + i);
     const bool known = s >= 0 && s < c.max_seqs;
     const int have = known ? __ldcg(c.lens + s) : -1;
     const bool ok = known && want >= 0 && want <= cap && have >= 0 && have <= cap;
@@ -299,11 +299,11 @@ __global__ void __launch_bounds__(256) free_kernel(const CacheDev c, const int32
   next_may_launch();
   wait_for_previous();
   const int i = blockIdx.x, tid = threadIdx.x;
-  const int s = seqs ? __ldg(seqs + i) : i;
+  const int s = seqs ? load_written(seqs + i) : i;
   if (s == -1) return;
   bool ok = s >= 0 && s < c.max_seqs;
   if (seqs && ok)
-    for (int j = tid; j < i; j += 256) ok = ok && __ldg(seqs + j) != s;
+    for (int j = tid; j < i; j += 256) ok = ok && load_written(seqs + j) != s;
   const int len = s >= 0 && s < c.max_seqs ? c.lens[s] : 0;
   ok = ok && len >= 0 && len <= c.max_pages * c.page;
   if (!__syncthreads_and(ok)) {
@@ -327,11 +327,11 @@ __global__ void __launch_bounds__(256) fork_kernel(const CacheDev c, const int32
   next_may_launch();
   wait_for_previous();
   const int i = blockIdx.x, tid = threadIdx.x;
-  const int a = __ldg(src + i), b = __ldg(dst + i);
+  const int a = load_written(src + i), b = load_written(dst + i);
   if (a == -1 || b == -1) return;
   bool ok = a >= 0 && a < c.max_seqs && b >= 0 && b < c.max_seqs;
   for (int j = tid; ok && j < n; j += 256) {
-    const int sj = __ldg(src + j), dj = __ldg(dst + j);
+    const int sj = load_written(src + j), dj = load_written(dst + j);
     if (sj == -1 || dj == -1) continue;
     if ((dj == b && j < i) || sj == b) ok = false;
   }

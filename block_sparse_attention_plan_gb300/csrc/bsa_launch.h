@@ -28,9 +28,11 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, int s
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// A load of what an earlier kernel of the stream may have written: a kernel that
-// launch_after starts may be resident while that one writes, which rules out the
-// read-only path (__ldg) for it.
+// A load of what an earlier kernel of the stream may have written (the library's
+// or the caller's: every list, mask and table that a call is given): a kernel
+// that launch_after starts may be resident while that one writes, which rules
+// out the read-only path (__ldg) for it, whose loads need not stay behind
+// wait_for_previous() either.
 template <class T>
 __device__ __forceinline__ T load_written(const T* p) {
   return *p;

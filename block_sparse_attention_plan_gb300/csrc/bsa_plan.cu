@@ -63,10 +63,10 @@ __device__ __forceinline__ Raw raw_load(const uint8_t* row, int w, int sk_sh) {
   Raw r;
   if (sk_sh == 0) {
     const uint4* s = reinterpret_cast<const uint4*>(row + 32 * (size_t)w);
-    r.a = __ldg(s);
-    r.b = __ldg(s + 1);
+    r.a = load_written(s);
+    r.b = load_written(s + 1);
   } else {
-    r.a = __ldg(reinterpret_cast<const uint4*>(row + 16 * (size_t)w));
+    r.a = load_written(reinterpret_cast<const uint4*>(row + 16 * (size_t)w));
     r.b = make_uint4(0u, 0u, 0u, 0u);
   }
   return r;
@@ -90,7 +90,7 @@ __device__ uint32_t slow_bits(const uint8_t* row, const PlanDev& p, int w, int s
   uint32_t bits = 0;
   for (int t = 0; t < 32; ++t) {
     const int y = 32 * w + t;
-    if (y < p.NKU && __ldg(row + (y >> sk_sh)) != 0) bits |= 1u << t;
+    if (y < p.NKU && load_written(row + (y >> sk_sh)) != 0) bits |= 1u << t;
   }
   return bits;
 }
@@ -120,8 +120,8 @@ __device__ __forceinline__ void head_segments(const PlanDev& p, int h, int& s0, 
   s0 = 0;
   s1 = 0;
   if (p.seg_ptr == nullptr) return;
-  s0 = max(__ldg(p.seg_ptr + h), 0);
-  s1 = min(__ldg(p.seg_ptr + h + 1), p.nseg);
+  s0 = max(load_written(p.seg_ptr + h), 0);
+  s1 = min(load_written(p.seg_ptr + h + 1), p.nseg);
 }
 
 __device__ __forceinline__ int floor_div(int a, int b) {  // b > 0
@@ -144,7 +144,7 @@ __device__ uint32_t segment_word(const PlanDev& p, int s0, int s1, int qb, int w
   const uint32_t unit_bits = sk_sh ? 3u : 1u;
   uint32_t bits = 0u;
   for (int s = s0; s < s1; ++s) {
-    const int4 sg = __ldg(reinterpret_cast<const int4*>(p.seg) + s);  // a, b, stride, count
+    const int4 sg = load_written(reinterpret_cast<const int4*>(p.seg) + s);  // a, b, stride, count
     if (sg.w <= 0) continue;
     long long start = (long long)sg.x * qb + sg.y;
     long long stride = sg.z, count = sg.w;

@@ -201,3 +201,36 @@ def test_append_beside_tokens_of_the_largest_scales(bsa, kind):
         append_both(bsa, m, c, x, x * 2.0 ** -3, [0], [7])
         assert OC.decode(m.codes[0][m.table[0, 0], 0, 7:10], kind).any()
         assert_state(c, m, f"2^{e}")
+
+
+# ------------------------------------------- lists that are the cache's own
+
+def test_lists_that_are_the_lengths_of_a_cache(bsa):
+    """The lengths that a resize is still writing, as the counts of the append
+    behind it and as the new lengths of another cache."""
+    heads, page, d, n = 2, 16, 64, 700
+    g = torch.Generator().manual_seed(13)
+    rng = np.random.default_rng(13)
+    c = bsa.cache_create(4 * n, heads, page, d, n, 4)
+    other = bsa.cache_create(4 * n, heads, page, d, n, 4)
+    x = rand(g, n, heads, 4 * page, d)
+    xd = x.cuda()
+    for turn in range(20):
+        lens = torch.from_numpy(rng.integers(1, 4 * page + 1, n).astype(np.int32)).cuda()
+        bsa.cache_free(c)
+        bsa.cache_resize(c, lens)
+        bsa.cache_append(c, xd, xd, counts=c.lens)
+        bsa.cache_resize(other, c.lens)
+        assert bsa.cache_status(c) == (0, 0) and bsa.cache_status(other) == (0, 0), turn
+        assert torch.equal(c.lens, lens) and torch.equal(other.lens, lens), turn
+        if turn % 10 == 9:
+            m = OC.CacheModel(4 * n, heads, page, d, n, 4, seed=0)
+            m.resize(lens.cpu().numpy())
+            m.append(x.double().numpy(), x.double().numpy(), counts=lens.cpu().numpy())
+            for s in range(0, n, 37):
+                k = m.values(s)[0]
+                p, L = c.block_table[s].cpu().numpy(), int(lens[s])
+                got = np.concatenate([OC.decode(c.k[int(j)].view(torch.uint8).cpu().numpy(), "e4m3")
+                                      * c.k_scale[int(j)].double().cpu().numpy().repeat(16, 1)[..., None]
+                                      for j in p[:-(-L // page)]], 1)[:, :L]
+                assert np.array_equal(got, k), s

@@ -1,0 +1,33 @@
+"""Rules that the CUDA sources keep."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_sparse_attention_plan_gb300", "csrc")
+
+
+def sources():
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith((".cu", ".cuh", ".h")):
+            with open(os.path.join(CSRC, name)) as f:
+                yield name, re.sub(r"//[^\n]*", "", f.read())
+
+
+def test_overlapping_launches_read_nothing_through_the_read_only_path():
+    """A kernel that launch_after starts may be resident while the one ahead of
+    it, or the caller's, still writes what it is given: its loads are plain ones,
+    behind the wait.  Only kernels launched the ordinary way may use __ldg."""
+    seen = 0
+    for name, text in sources():
+        ordinary = "launch_after(" not in text and "<<<" in text
+        if not ordinary:
+            assert not re.search(r"__ldg\b|ld\.global\.nc|__restrict__", text), name
+            seen += "launch_after(" in text
+    assert seen >= 7
+
+
+def test_kernels_that_overlap_wait_before_they_read():
+    """next_may_launch() and wait_for_previous() come as a pair, in every file
+    whose kernels launch_after starts."""
+    for name, text in sources():
+        if name != "bsa_launch.h" and "launch_after(" in text:
+            assert text.count("next_may_launch();") == text.count("wait_for_previous();") > 0, name
