@@ -111,9 +111,16 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   return r;
 }
 
+// Lists and masks of the caller: coherent loads like load_written's, which the
+// compiler leaves where they are (moved about, they cost the kernel 2 %).
+template <class T>
+__device__ __forceinline__ T load_given(const T* p) {
+  return __ldca(p);
+}
+
 // Length of batch row b's sequence (0 for a padded row or one out of range).
 __device__ __forceinline__ int seq_of(const CacheAttnParams& p, int b) {
-  const int s = p.seqs ? load_written(p.seqs + b) : b;
+  const int s = p.seqs ? load_given(p.seqs + b) : b;
   return s >= 0 && s < p.c.max_seqs ? s : -1;
 }
 __device__ __forceinline__ int len_of(const CacheAttnParams& p, int b) {
@@ -256,8 +263,11 @@ __device__ __forceinline__ void take_nans(uint32_t (&v)[4][DV / 4], float (&o)[N
 }
 
 // A warp's requests for tiles: where it is in the line, and for the next (up to)
-// 32 tiles of the piece a lane each with the tile's number and the pool row of
-// each of its boxes (-1: no token in it).
+// 32 tiles of the piece a lane each with the tile's number (bits from kNoBox on:
+// its boxes that are not read) and the pool row of each of its boxes (-1: no
+// token in it, or the table has no page for them).
+constexpr int kNoBox = 25;  // (tiles are below 2^25: sequences end at 2^30 tokens)
+constexpr int kTileMask = (1 << kNoBox) - 1;
 struct Feed {
   Walk w;
   int pos, n, i;    // first tile of the batch (within the unit), its size, the next one to request
@@ -346,7 +356,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     const int b = p.mask ? e / p.c.Hkv : e;
     const int h0 = p.mask ? e % p.c.Hkv : 0, h1 = p.mask ? h0 + 1 : p.c.Hkv;
     if (tid == 0) {
-      const int s = p.seqs ? load_written(p.seqs + b) : b;
+      const int s = p.seqs ? load_given(p.seqs + b) : b;
       if (s < -1 || s >= p.c.max_seqs) cache_error(p.c.control, BSA_ERR_INVALID_ARG, b);
     }
     const int c4 = tid % (D / 4);
@@ -443,25 +453,25 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     for (int j = 0; j < 4; ++j) f.pr[j] = -1;
     if (lane < f.n) {
       const int t = f.pos + lane * KL;
-      f.tile = p.mask ? load_written(p.list + (size_t)f.w.e * p.max_tiles + t) : t;
+      const int tile = p.mask ? load_written(p.list + (size_t)f.w.e * p.max_tiles + t) : t;
+      f.tile = tile;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = f.tile * TK + (j << lcs);
+        const int key = tile * TK + (j << lcs);
         if (j < nc && key < f.len) {
-          int ph = load_written(row + (key >> lpage));
-          if (ph < 0 || ph >= p.c.num_pages) {
-            cache_error(p.c.control, BSA_ERR_PLAN_MISMATCH, seq);
-            ph = 0;  // (some page, so that the row ends like any other)
-          }
-          f.pr[j] = (ph * p.c.Hkv + u.h) * p.c.page + (key & (p.c.page - 1));
+          const int ph = load_written(row + (key >> lpage));
+          if (ph >= 0 && ph < p.c.num_pages) f.pr[j] = (ph * p.c.Hkv + u.h) * p.c.page + (key & (p.c.page - 1));
+          else cache_error(p.c.control, BSA_ERR_PLAN_MISMATCH, seq);  // not attended
         }
+        if (j < nc && f.pr[j] < 0) f.tile |= 1 << (kNoBox + j);
       }
     }
   };
-  // Request the warp's next tile into stage s.  Returns its number (-1: there is
-  // none); `scale` gets this lane's scale of it: lanes 0 .. kGroups - 1 K's of 16
-  // keys each, the next kGroups V's (0 where the keys lie past the length);
-  // `sel` the mask's bytes of query row `lane` for the tile's halves of 32 keys.
+  // Request the warp's next tile into stage s.  Returns its number with the bits
+  // of boxes that are not read (-1: there is none); `scale` gets this lane's
+  // scale of it: lanes 0 .. kGroups - 1 K's of 16 keys each, the next kGroups V's
+  // (0 where no key is read); `sel` the mask's bytes of query row `lane` for the
+  // tile's halves of 32 keys.
   auto request = [&](int s, float& scale, uchar2& sel) -> int {
     scale = 0.f;
     sel = make_uchar2(0, 0);
@@ -470,7 +480,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     int box[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) box[j] = __shfl_sync(0xffffffffu, f.pr[j], f.i);
-    const int tile = __shfl_sync(0xffffffffu, f.tile, f.i);
+    const int tagged = __shfl_sync(0xffffffffu, f.tile, f.i), tile = tagged & kTileMask;
     ++f.i;
     if (lane == 0) {
       uint32_t bytes = 0;
@@ -487,18 +497,18 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     if (lane < 2 * C::kGroups) {
       const int gr = lane % C::kGroups, jb = (16 * gr) >> lcs;
       const int sbox = jb == 0 ? box[0] : (jb == 1 ? box[1] : (jb == 2 ? box[2] : box[3]));
-      if (tile * TK + 16 * gr < f.len)
+      if (tile * TK + 16 * gr < f.len && sbox >= 0)
         scale = load_written((lane < C::kGroups ? p.c.ks : p.c.vs) + ((size_t)(unsigned)(sbox + ((16 * gr) & (cs - 1))) >> lsb));
     }
     if (p.mask && lane < 8 * NT) {
       const int k0 = tile * TK >> lbk;
-      if (k0 < p.NKB) sel.x = load_written(f.mask + k0);
+      if (k0 < p.NKB) sel.x = load_given(f.mask + k0);
       if (TK > 32) {
         const int k1 = (tile * TK + 32) >> lbk;
-        if (k1 < p.NKB) sel.y = load_written(f.mask + k1);
+        if (k1 < p.NKB) sel.y = load_given(f.mask + k1);
       }
     }
-    return tile;
+    return tagged;
   };
   // Tiles and scales of the stages, the one to be used next first.
   int tq[C::kStages];
@@ -573,13 +583,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
 
     int t = first_of(w);
     for (; t < w.t1 && ok; t += KL) {
-      const int key0 = tq[0] * TK;
+      const int key0 = (tq[0] & kTileMask) * TK;
       if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, phase, wd, kSiteTileFull))) {
         ok = false;  // recorded; these rows' results are void, the walk goes on so that no barrier is missed
         break;
       }
       const uint32_t ks = ring + stage * C::kStageBytes, vs = ks + C::kTileBytes;
       const bool tail = key0 + TK > len;
+      const uint32_t unread = (uint32_t)tq[0] >> kNoBox;  // boxes of the tile
+      auto box_read = [&](int r) { return (unread >> (r >> lcs) & 1u) == 0u; };  // that of the tile's key r
       // The tile's computation, for tiles that every row attends wholly and for
       // the others: the code of the masks, in the loop that most tiles take,
       // would cost those a tenth (registers, and the loop outgrows the
@@ -646,7 +658,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
               for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
                 for (int hi8 = 0; hi8 < 2; ++hi8) {
-                  const bool keep = 16 * kg + g + 8 * hi8 < end && (sel[(kb16 + 16 * kg) >> 5] >> row & 1u);
+                  const bool keep = 16 * kg + g + 8 * hi8 < end && (sel[(kb16 + 16 * kg) >> 5] >> row & 1u) &&
+                                      box_read(kb16 + 16 * kg);
                   if (!keep) {
                     x[kg][nt][2 * hi8 + c] = -INFINITY;
                     kept &= ~(1u << ((kg * NT + nt) * 4 + 2 * hi8 + c));
@@ -731,8 +744,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
               v[kg][e][0] = y.x;
               v[kg][e][1] = y.y;
             }
-            // Rows past the sequence hold anything: weight 0 would not stop a NaN.
-            if (kMasked && tail && key0 + r >= len) {
+            // Rows past the sequence, and of boxes that were not read, hold
+            // anything: weight 0 would not stop a NaN.
+            if (kMasked && ((tail && key0 + r >= len) || !box_read(kb16 + 16 * kg))) {
 #pragma unroll
               for (int q = 0; q < DV / 4; ++q) v[kg][e][q] = 0u;
             }
@@ -768,7 +782,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         }
       }
       };
-      if (key0 + TK > first_limit || p.mask != nullptr) compute(std::true_type{});
+      if (key0 + TK > first_limit || p.mask != nullptr || unread != 0u) compute(std::true_type{});
       else compute(std::false_type{});
       __syncwarp();  // every lane has read the stage
 #pragma unroll

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import cache as OC
-from test_cache_gpu import KINDS, i32, rand, upload
+from test_cache_gpu import KINDS, assert_close, filled, i32, keep_of, rand, upload
 
 pytestmark = pytest.mark.gpu
 
@@ -234,3 +234,37 @@ def test_lists_that_are_the_lengths_of_a_cache(bsa):
                                       * c.k_scale[int(j)].double().cpu().numpy().repeat(16, 1)[..., None]
                                       for j in p[:-(-L // page)]], 1)[:, :L]
                 assert np.array_equal(got, k), s
+
+
+# ------------------------------------- tables and lengths that are wrong
+
+@pytest.mark.parametrize("kind,page,sb,d,nq", [("e4m3", 64, 32, 128, 1), ("int8", 16, 16, 64, 3), ("e4m3", 16, 16, 128, 5),
+                                               ("int8", 256, 64, 128, 1), ("e4m3", 32, 16, 64, 30)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_keys_of_no_page_are_not_attended(bsa, kind, page, sb, d, nq, masked):
+    lens = [700, 700, 333, 2000]
+    m, c = filled(bsa, lens, 2, page, sb, d, kind, -(-2000 // page), seed=17)
+    c.k_scale.mul_(torch.where(torch.arange(c.num_pages, device="cuda") == 0, 4.0, 1.0).view(-1, 1, 1))
+    m.scales[0] = c.k_scale.cpu().numpy()
+    g = torch.Generator().manual_seed(17)
+    q = rand(g, 4, 4, nq, d)
+    mask = (torch.rand(4, 4, 2000 // 64, generator=g) < 0.7).to(torch.uint8) if masked else None
+    good = bsa.cache_attention(c, q.cuda(), mask=None if mask is None else mask.cuda(), bk=64, causal=nq > 1)
+    bad = {0: [0], 1: [-(-700 // page) - 1, 1], 3: range(0, -(-2000 // page), 2)}
+    for s, js in bad.items():
+        for i, j in enumerate(js):
+            c.block_table[s, j] = (-1, c.num_pages, 1 << 30, -(1 << 31))[i % 4]
+    o, lse = bsa.cache_attention(c, q.cuda(), mask=None if mask is None else mask.cuda(), bk=64, causal=nq > 1)
+    st, det = bsa.cache_status(c)
+    assert st == -7 and det in bad
+    assert torch.equal(o[2], good[0][2]) and torch.equal(lse[2], good[1][2])
+    for s in (0, 1, 3):
+        k, v = m.values(s)
+        keep = keep_of(k.shape[1], nq, 4, nq > 1, None if mask is None else mask[s].numpy(), 64)
+        for j in bad[s]:
+            keep[:, :, j * page:(j + 1) * page] = False
+        assert_close(o[s], lse[s], OC.attention(q[s].double().numpy(), k, v, keep), q, k.shape[1], f"sequence {s}")
+    c.block_table[3] = -1  # no page at all
+    o, lse = bsa.cache_attention(c, q.cuda(), causal=nq > 1)
+    assert not o[3].any() and torch.isneginf(lse[3]).all()
+    assert bsa.cache_status(c)[0] == -7
