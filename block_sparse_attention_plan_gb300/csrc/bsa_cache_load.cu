@@ -39,9 +39,20 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
   int len = known ? load_written(c.lens + seq) : 0;
   len = min(max(len, 0), c.max_pages * c.page);
   const bool isv = blockIdx.z != 0;
-  if (blockIdx.x == 0 && h == 0 && tid == 0 && !isv) {
-    p.lens[b] = len;  // (whole: the queries are the last tokens, of which Nk may leave out some)
-    if (!known && seq != -1) cache_error(c.control, BSA_ERR_INVALID_ARG, b);
+  if (blockIdx.x == 0 && h == 0 && !isv) {
+    // A sequence with a token in no page is skipped: the forward masks keys by
+    // their number alone, so it gets a length of 0.
+    const int pages = (min(len, p.Nk) + c.page - 1) / c.page;
+    bool gap = false;
+    for (int j = tid; j < pages; j += kThreads) {
+      const int ph = load_written(c.table + (size_t)seq * c.max_pages + j);
+      gap |= ph < 0 || ph >= c.num_pages;
+    }
+    gap = __syncthreads_or(gap);
+    if (tid == 0) {
+      p.lens[b] = gap ? 0 : len;  // (whole: the queries are the last tokens, of which Nk may leave out some)
+      if (!known && seq != -1) cache_error(c.control, BSA_ERR_INVALID_ARG, b);
+    }
   }
   // What a forward resets ahead of its passes.
   const long long at = ((long long)(blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + tid;

@@ -268,3 +268,25 @@ def test_keys_of_no_page_are_not_attended(bsa, kind, page, sb, d, nq, masked):
     o, lse = bsa.cache_attention(c, q.cuda(), causal=nq > 1)
     assert not o[3].any() and torch.isneginf(lse[3]).all()
     assert bsa.cache_status(c)[0] == -7
+
+
+def test_forward_of_a_sequence_with_no_page(bsa):
+    m, c = filled(bsa, [600, 512, 600, 300], 2, 32, 32, 64, "e4m3", 20, seed=19)
+    g = torch.Generator().manual_seed(19)
+    p = bsa.plan(torch.ones(4, 4, 2, 8, dtype=torch.uint8, device="cuda"), 64, 64, 2)
+    q = rand(g, 4, 4, 128, 64).cuda()
+    good = bsa.cache_forward(p, c, q, causal=True)
+    for s, j in ((1, 0), (2, 15)):
+        was = int(c.block_table[s, j])
+        for x in (-1, c.num_pages, 1 << 30):
+            c.block_table[s, j] = x
+            o, lse = bsa.cache_forward(p, c, q, causal=True)
+            assert bsa.cache_status(c) == (-7, s) and bsa.sync_status(p)[0] == 0
+            assert not o[s].any() and torch.isneginf(lse[s]).all()
+            for b in {0, 1, 2, 3} - {s}:
+                assert torch.equal(o[b], good[0][b]) and torch.equal(lse[b], good[1][b])
+        c.block_table[s, j] = was
+    c.block_table[2, 17] = -1  # past the plan's keys
+    o, lse = bsa.cache_forward(p, c, q, causal=True)
+    assert bsa.cache_status(c) == (0, 0)
+    assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
