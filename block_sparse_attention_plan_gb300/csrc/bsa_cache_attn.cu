@@ -118,7 +118,8 @@ __device__ __forceinline__ T load_given(const T* p) {
   return __ldca(p);
 }
 
-// Length of batch row b's sequence (0 for a padded row or one out of range).
+// Length of batch row b's sequence (0 for a padded row, and where the sequence or
+// its length is out of range: recorded with the empty rows).
 __device__ __forceinline__ int seq_of(const CacheAttnParams& p, int b) {
   const int s = p.seqs ? load_given(p.seqs + b) : b;
   return s >= 0 && s < p.c.max_seqs ? s : -1;
@@ -126,7 +127,8 @@ __device__ __forceinline__ int seq_of(const CacheAttnParams& p, int b) {
 __device__ __forceinline__ int len_of(const CacheAttnParams& p, int b) {
   const int s = seq_of(p, b);
   if (s < 0) return 0;
-  return min(max(load_written(p.c.lens + s), 0), p.c.max_pages * p.c.page);
+  const int n = load_written(p.c.lens + s);
+  return n >= 0 && n <= p.c.max_pages * p.c.page ? n : 0;
 }
 
 // The line of tiles: entry e is a batch row with its Hkv heads (no mask) or one
@@ -357,7 +359,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
     const int h0 = p.mask ? e % p.c.Hkv : 0, h1 = p.mask ? h0 + 1 : p.c.Hkv;
     if (tid == 0) {
       const int s = p.seqs ? load_given(p.seqs + b) : b;
-      if (s < -1 || s >= p.c.max_seqs) cache_error(p.c.control, BSA_ERR_INVALID_ARG, b);
+      const int n = s >= 0 && s < p.c.max_seqs ? load_written(p.c.lens + s) : (s == -1 ? 0 : -1);
+      if (n < 0 || n > p.c.max_pages * p.c.page) cache_error(p.c.control, BSA_ERR_INVALID_ARG, b);
     }
     const int c4 = tid % (D / 4);
     for (int r = tid / (D / 4); r < (h1 - h0) * p.M; r += kAttnThreads / (D / 4)) {

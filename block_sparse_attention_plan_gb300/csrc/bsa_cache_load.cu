@@ -35,9 +35,10 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
   const int tid = threadIdx.x;
   const int bh = blockIdx.y, b = bh / c.Hkv, h = bh % c.Hkv;
   const int seq = p.seqs ? load_written(p.seqs + b) : b;
-  const bool known = seq >= 0 && seq < c.max_seqs;
-  int len = known ? load_written(c.lens + seq) : 0;
-  len = min(max(len, 0), c.max_pages * c.page);
+  // (a sequence or a length out of range: an empty one, recorded)
+  int len = seq >= 0 && seq < c.max_seqs ? load_written(c.lens + seq) : (seq == -1 ? 0 : -1);
+  const bool known = len >= 0 && len <= c.max_pages * c.page;
+  if (!known) len = 0;
   const bool isv = blockIdx.z != 0;
   if (blockIdx.x == 0 && h == 0 && !isv) {
     // A sequence with a token in no page is skipped: the forward masks keys by
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
     gap = __syncthreads_or(gap);
     if (tid == 0) {
       p.lens[b] = gap ? 0 : len;  // (whole: the queries are the last tokens, of which Nk may leave out some)
-      if (!known && seq != -1) cache_error(c.control, BSA_ERR_INVALID_ARG, b);
+      if (!known) cache_error(c.control, BSA_ERR_INVALID_ARG, b);
     }
   }
   // What a forward resets ahead of its passes.

@@ -290,3 +290,29 @@ def test_forward_of_a_sequence_with_no_page(bsa):
     o, lse = bsa.cache_forward(p, c, q, causal=True)
     assert bsa.cache_status(c) == (0, 0)
     assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
+
+
+def test_lengths_out_of_range_are_reported(bsa):
+    m, c = filled(bsa, [600, 512, 300], 2, 32, 32, 64, "e4m3", 20, seed=23)
+    g = torch.Generator().manual_seed(23)
+    p = bsa.plan(torch.ones(3, 4, 2, 10, dtype=torch.uint8, device="cuda"), 64, 64, 2)
+    q1, q2 = rand(g, 3, 4, 1, 64).cuda(), rand(g, 3, 4, 128, 64).cuda()
+    mask = torch.ones(3, 4, 10, dtype=torch.uint8, device="cuda")
+    calls = (lambda: bsa.cache_attention(c, q1), lambda: bsa.cache_attention(c, q1, mask=mask, bk=64),
+             lambda: bsa.cache_forward(p, c, q2, causal=True))
+    good = [f() for f in calls]
+    assert bsa.cache_status(c) == (0, 0)
+    for s, n in ((1, 641), (1, -1), (0, 2 ** 31 - 1), (2, -2 ** 31)):
+        was = int(c.lens[s])
+        c.lens[s] = n
+        for f, want in zip(calls, good):
+            o, lse = f()
+            assert bsa.cache_status(c) == (-1, s), n
+            assert not o[s].any() and torch.isneginf(lse[s]).all()
+            for b in {0, 1, 2} - {s}:
+                assert torch.equal(o[b], want[0][b]) and torch.equal(lse[b], want[1][b])
+        c.lens[s] = was
+    c.lens[1] = 640  # the most there is room for
+    c.block_table[1] = c.block_table[0]
+    bsa.cache_attention(c, q1)
+    assert bsa.cache_status(c)[0] != -1
