@@ -124,8 +124,10 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
         s_have[i] = -1;
       }
   }
-  for (int i = tid; i < n; i += kThreads)
+  for (int i = tid; i < n; i += kThreads) {
     if (s_have[i] < 0) s_seq[i] = -1;  // (a skipped item's own entry only: no other thread reads it before the barrier)
+    s_page[i] = 0;
+  }
   bool shrinks = false;
   for (int i = tid; i < n; i += kThreads)
     shrinks |= s_seq[i] >= 0 && pages_of(s_want[i], c.page) < pages_of(s_have[i], c.page);
@@ -153,6 +155,24 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
   };
   shrinks = __syncthreads_or(shrinks);
   if (shrinks) {
+    // An item with an entry among them that is no page is skipped; a sequence that
+    // is freed gives back those that are.
+    for (int i = tid >> 3; i < n; i += kThreads / 8) {
+      const int s = s_seq[i];
+      if (s < 0 || s_want[i] == 0) continue;
+      const int hp = pages_of(s_have[i], c.page);
+      for (int j = pages_of(s_want[i], c.page) + (tid & 7); j < hp; j += 8) {
+        const int p = __ldcg(c.table + (size_t)s * c.max_pages + j);
+        if (p < 0 || p >= c.num_pages) s_page[i] = 1;
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads)
+      if (s_page[i]) {
+        cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s_seq[i]);
+        s_seq[i] = -1;
+      }
+    __syncthreads();
     release(-1);
     __syncthreads();
   }
@@ -163,8 +183,12 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
     const int s = s_seq[i], have = s_have[i];
     if (s >= 0 && s_want[i] > have && have % c.page) {
       const int p = __ldcg(c.table + (size_t)s * c.max_pages + have / c.page);
-      if (p < 0 || p >= c.num_pages) cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s);
-      else if (__ldcg(c.refs + p) > 1) shared_page = p;
+      if (p < 0 || p >= c.num_pages) {
+        cache_error(c.control, BSA_ERR_PLAN_MISMATCH, s);
+        s_seq[i] = -1;  // skipped
+      } else if (__ldcg(c.refs + p) > 1) {
+        shared_page = p;
+      }
     }
     s_page[i] = shared_page;
     cow |= shared_page >= 0;
@@ -347,11 +371,16 @@ __global__ void __launch_bounds__(256) fork_kernel(const CacheDev c, const int32
   const int held = pages_of(len, c.page);
   const int32_t* from = c.table + (size_t)a * c.max_pages;
   int32_t* to = c.table + (size_t)b * c.max_pages;
+  bool whole = true;
+  for (int j = tid; j < held; j += 256) whole &= from[j] >= 0 && from[j] < c.num_pages;
+  if (!__syncthreads_and(whole)) {
+    if (tid == 0) cache_error(c.control, BSA_ERR_PLAN_MISMATCH, a);
+    return;
+  }
   for (int j = tid; j < held; j += 256) {
     const int p = from[j];
     to[j] = p;
-    if (p >= 0 && p < c.num_pages) atomicAdd(c.refs + p, 1);
-    else cache_error(c.control, BSA_ERR_PLAN_MISMATCH, a);
+    atomicAdd(c.refs + p, 1);
   }
   if (tid == 0) c.lens[b] = len;  // (every thread has read lens[b]: the barrier above)
 }

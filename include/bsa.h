@@ -513,8 +513,10 @@ bsa_status bsa_attention_host(const uint8_t* mask, int B, int H, int NQB, int NK
  * sequence); too few free pages (BSA_ERR_WORKSPACE, detail = pages missing).
  * Such an item is skipped (for BSA_ERR_WORKSPACE the whole call is): tokens of
  * no page are not attended by bsa_cache_attention, and a sequence that has some
- * among the plan's keys is an empty one to bsa_cache_forward.  Memory outside
- * the cache is never touched.
+ * among the plan's keys is an empty one to bsa_cache_forward; a sequence is not
+ * forked with such tokens, not shrunk by them nor grown behind them in their
+ * page (but may be freed, which gives back the pages that it has).  Memory
+ * outside the cache is never touched.
  */
 #define BSA_CACHE_E4M3 0 /* 8-bit floating point: 4 exponent bits, 3 mantissa bits, largest 448 */
 #define BSA_CACHE_INT8 1 /* -127 .. 127 */

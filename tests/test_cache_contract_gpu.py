@@ -316,3 +316,54 @@ def test_lengths_out_of_range_are_reported(bsa):
     c.block_table[1] = c.block_table[0]
     bsa.cache_attention(c, q1)
     assert bsa.cache_status(c)[0] != -1
+
+
+def test_page_operations_skip_sequences_of_bad_tables(bsa):
+    for bad in (-1, 20, 1 << 30):
+        m = OC.CacheModel(20, 1, 16, 64, 5, 6, seed=4)
+        assert m.resize([60, 40, 20, 33]) == 0
+        c = upload(bsa, m)
+
+        def same(what, skip=None):
+            t, w = c.block_table.cpu().numpy(), m.table.copy()
+            if skip is not None:
+                w[skip] = bad
+            assert np.array_equal(t, w), (what, bad)
+            assert np.array_equal(c.lens.cpu().numpy(), m.lens) and np.array_equal(c.refs.cpu().numpy(), m.refs), (what, bad)
+
+        c.block_table[0, 2] = bad
+        bsa.cache_resize(c, i32(20, 50), i32(0, 1))      # would give the bad page back
+        assert m.resize([50], [1]) == 0
+        assert bsa.cache_status(c) == (-7, 0)
+        same("shrink", (0, 2))
+        bsa.cache_fork(c, i32(0, 2), i32(4, 0))          # (0 is a source)
+        assert bsa.cache_status(c)[0] == -1
+        bsa.cache_fork(c, i32(0), i32(4))
+        assert bsa.cache_status(c) == (-7, 0)
+        same("fork", (0, 2))
+        bsa.cache_resize(c, i32(49), i32(0))             # the bad page stays
+        m.resize([49], [0])
+        assert bsa.cache_status(c) == (0, 0)
+        same("shrink behind it", (0, 2))
+        c.block_table[0, 2] = int(m.table[0, 2])
+        c.block_table[3, 2] = bad                        # its partly filled last page
+        bsa.cache_resize(c, i32(34, 21), i32(3, 2))
+        assert m.resize([21], [2]) == 0
+        assert bsa.cache_status(c) == (-7, 3)
+        same("grow", (3, 2))
+        # Freed, by either call, a sequence gives back what pages it has.
+        bsa.cache_resize(c, i32(0), i32(3))
+        assert bsa.cache_status(c) == (-7, 3)
+        held = m.table[3, 2]
+        m.resize([0], [3])
+        m.refs[held] = 1
+        same("free")
+        c.refs[int(held)] = 0
+        m.refs[held] = 0
+        c.block_table[1, 1] = bad
+        bsa.cache_free(c, i32(1))
+        assert bsa.cache_status(c) == (-7, 1)
+        held = m.table[1, 1]
+        m.resize([0], [1])
+        m.refs[held] = 1
+        same("free of a list")
