@@ -5,15 +5,18 @@
 //   x[key][row] = S_k(key) * qs(row) * sum_d kcode[key][d] * q16[row][d]
 // with q16 the row divided by a power of two that brings its largest element
 // into [1, 2) (exact in fp16 to 2^-25 of that element) and qs that power times
-// scale * log2(e); p = 2^(x - m) rounded to fp16, and
+// scale * log2(e); p = 2^(x - m + 7) rounded to fp16, and
 //   O[d][row] += S_v * sum over 16 keys of vcode[key][d] * p[key][row]
 // where the 16 keys of one matrix instruction lie in one scale block.  Both
 // products are mma.m16n8k16 with the codes as the 16-row operand (S^T = K Q^T
 // and O^T = V^T P^T): with 1 to 8 rows nothing of the instruction is wasted on
 // the codes' side, codes convert to fp16 exactly, and S^T's accumulators become
 // P^T's operand by one movmatrix per 8 keys.  m is a running reference that is
-// moved only when a score passes it by more than 2^8 (then O and the sums are
-// rescaled), so fp16 weights keep 11 bits.
+// moved only when a score passes it by more than 8 (then O and the sums are
+// rescaled), so fp16 weights keep 11 bits.  The 7 puts the largest of them, 2^15,
+// under fp16's 2^16, and what becomes 0 in the products (below 2^-25) at 2^-32 of
+// the reference: a tail of n keys just below that loses n 2^-32 of O.  m is a
+// whole number, so that 7 - m and the differences of references are exact.
 //
 // What bounds it: 2 d bytes per key and K/V head at the memory's rate (32
 // sequences of up to 32768 tokens, 8 heads of 128, 4 rows: 1.11 GB in 171 us,
@@ -56,7 +59,9 @@ constexpr int kWarps = 4;
 constexpr int kAttnThreads = 32 * kWarps;
 constexpr int kMaxNT = 3;  // 8-row column tiles per warp at most
 static_assert(kCacheUnitRows == 8 * kMaxNT * kWarps, "24 query rows for each warp of a full unit");
-constexpr float kMoveReference = 8.f;  // log2: weights stay <= 2^8
+constexpr float kMoveReference = 8.f;  // log2: weights stay <= 2^(8 + kShift)
+constexpr float kShift = 7.f;          // log2 of the weight of a score at the reference
+constexpr float kUnshift = 0x1p-7f;    // taken out of the sums: values may be as large as ever
 
 enum CacheSite : int { kSiteTileFull = 0x50 };
 
@@ -693,6 +698,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
               f[c] = 1.f;
+              v = floorf(v);
               if (v > m_ref[nt][c]) {
                 f[c] = ex2_approx(m_ref[nt][c] - v);  // 0 from -inf
                 m_ref[nt][c] = v;
@@ -709,8 +715,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         uint32_t pf[KG][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint64_t ref = f2_make(m_ref[nt][0] == -INFINITY ? 0.f : -m_ref[nt][0],
-                                       m_ref[nt][1] == -INFINITY ? 0.f : -m_ref[nt][1]);
+          const uint64_t ref = f2_make(m_ref[nt][0] == -INFINITY ? 0.f : kShift - m_ref[nt][0],
+                                       m_ref[nt][1] == -INFINITY ? 0.f : kShift - m_ref[nt][1]);
           uint64_t l2 = f2_make(l_sum[nt][0], l_sum[nt][1]);
 #pragma unroll
           for (int kg = 0; kg < KG; ++kg) {
@@ -731,7 +737,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         uint32_t v[KG][4][DV / 4];
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg) {
-          sv[kg] = __shfl_sync(0xffffffffu, sq[0], C::kGroups + kb16 / 16 + kg);
+          sv[kg] = __shfl_sync(0xffffffffu, sq[0], C::kGroups + kb16 / 16 + kg) * kUnshift;
           const int ra = kb16 + 16 * kg + 2 * t4;  // keys 2 t4, + 1, + 8, + 9 of the 16
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -821,7 +827,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
         const int row = warp * 8 + 2 * t4 + c;
         if (g == 0) {
           ml[row * 2] = m_ref[nt][c];
-          ml[row * 2 + 1] = l;
+          ml[row * 2 + 1] = l * kUnshift;
         }
         float* mr = merge + (size_t)row * D + g * DV;
 #pragma unroll

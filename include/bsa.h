@@ -660,7 +660,8 @@ bsa_status bsa_cache_append(const bsa_cache* cache, const bsa_rows* k, const bsa
  * workspace: device, 16-byte aligned, bsa_cache_attention_workspace_bytes
  *   bytes; scratch of this call (calls that overlap in time need their own).
  * Q is used as given, codes and scales exactly; weights are rounded to fp16
- * relative to (at most 2^8 times) the row's largest, sums are fp32.
+ * relative to (at most 2^8 times) the row's largest, sums are fp32.  In O, not in
+ * LSE, a weight below 2^-32 of the largest may count as 0.
  * Two kernels, three with a mask.
  */
 size_t bsa_cache_attention_workspace_bytes(const bsa_cache* cache, int B, int Hq, int nq, int NKB,

@@ -367,3 +367,66 @@ def test_page_operations_skip_sequences_of_bad_tables(bsa):
         m.resize([0], [1])
         m.refs[held] = 1
         same("free of a list")
+
+
+# -------------------------------------------------- small weights, long rows
+
+@pytest.mark.parametrize("kind,d", [("int8", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("octaves", [25.05, 28.0, 30.0])
+def test_a_long_tail_below_a_sink(bsa, kind, d, octaves):
+    """Keys ahead that outweigh every other one 2^octaves times, then a flat
+    tail, long enough to count.  A weight is off by half of fp16's least step at
+    2^7 times the row's reference, 2^-32 of that, so the tail's part by n 2^-32;
+    the scores by what assert_close derives; and half a step of bf16."""
+    n, B = 1 << 17, 320  # (rows enough that a piece of the work is a whole row)
+    tile = 4096 // d
+    c = bsa.cache_create(n // 256, 1, 256, d, 1, n // 256, kind, 256)
+    c.block_table[0] = torch.arange(n // 256, dtype=torch.int32)
+    c.refs.fill_(1)
+    c.lens[0] = n
+    one = {"int8": 1, "e4m3": 0x38}[kind]
+    sinks = torch.arange(4) * tile                       # one for each warp
+    k, v = (x.view(torch.uint8).view(-1, d) for x in (c.k, c.v))
+    k[sinks, 0] = one
+    v.fill_(one)
+    v[sinks] = 0
+    c.k_scale.fill_(1.0)
+    c.v_scale.fill_(1.0)
+    q = torch.zeros(B, 1, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    scale = octaves * float(np.log(2.0))
+    o, lse = bsa.cache_attention(c, q, seqs=torch.zeros(B, dtype=torch.int32, device="cuda"), scale=scale)
+    tail = (n - 4) * 2.0 ** -octaves
+    want = tail / (4 + tail)
+    bound = want * (2.0 ** -8 + 4 * scale * 2.0 ** -23 + 2.0 ** -11) + n * 2.0 ** -32 / (4 + tail) + 2.0 ** -25
+    assert bound < want / 2
+    err = (o.double() - want).abs().max().item()
+    assert err <= bound, (err / bound, err / want)
+    # A thread sums n / 32 of a row's weights (4 warps, 8 threads to a row); where
+    # the sink is its first, each addition is off by half a unit of fp32's last
+    # place, 2^-24 of the sum.
+    lse_bound = n / 32 * 2.0 ** -24 + 1e-5
+    assert (lse.double() - (scale + np.log(4 + tail))).abs().max().item() <= lse_bound
+    assert bsa.cache_status(c) == (0, 0)
+
+
+@pytest.mark.parametrize("kind,d", [("int8", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("nq", [1, 20])
+def test_long_flat_rows(bsa, kind, d, nq):
+    """Rows whose keys all weigh about the same, with a bound that an output of
+    zeros fails: weights lose 2^-11 of themselves (they are far above 2^-14 of
+    the reference), so O half a step and 2^-11 of the mean of |v|."""
+    n = 30000
+    m, c = filled(bsa, [n, 777], 2, 64, 64, d, kind, -(-n // 64), seed=41)
+    g = torch.Generator().manual_seed(41)
+    q = rand(g, 2, 4, nq, d) * 2.0 ** -4
+    o, lse = bsa.cache_attention(c, q.cuda(), causal=nq > 1)
+    for b in range(2):
+        k, v = m.values(b)
+        O, L, A, mag = OC.attention(q[b].double().numpy(), k, v, keep_of(k.shape[1], nq, 4, nq > 1))
+        ds = mag * (d + 4) * 2.0 ** -23 + 2.0 ** -21
+        bound = 2.0 ** -8 * np.abs(O) + (2.0 ** -11 + 2 * ds[..., None]) * 2 * A
+        assert b == 1 or np.median(bound / np.abs(O)) < 0.5
+        err = np.abs(o[b].double().cpu().numpy() - O)
+        assert (err <= bound).all(), float((err / bound).max())
+        assert (np.abs(lse[b].double().cpu().numpy() - L) <= ds + k.shape[1] * 2.0 ** -24 + 1e-5).all()
