@@ -430,3 +430,48 @@ def test_long_flat_rows(bsa, kind, d, nq):
         err = np.abs(o[b].double().cpu().numpy() - O)
         assert (err <= bound).all(), float((err / bound).max())
         assert (np.abs(lse[b].double().cpu().numpy() - L) <= ds + k.shape[1] * 2.0 ** -24 + 1e-5).all()
+
+
+# --------------------------------------------- scales in places not attended
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,sb", [(64, 16), (64, 64), (128, 16), (128, 32)])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+def test_scales_of_blocks_that_a_row_does_not_attend(bsa, kind, d, sb, fill):
+    """The scales of a block reach only the rows that attend a key of it: rows
+    cut off by causality or by a mask of blocks, beside rows that are not."""
+    lens = [200, 128 + sb]
+    m, c = filled(bsa, lens, 1, 64, sb, d, kind, 4, seed=47)
+    g = torch.Generator().manual_seed(47)
+    per = 64 // sb
+
+    def spoil(seq, key):
+        p = int(m.table[seq, key // 64])
+        c.v_scale[p, :, key % 64 // sb] = fill
+        return p
+
+    # Causal: the last sb keys in a block of their own, seen by the last queries only.
+    q = rand(g, 1, 2, sb + 4, d)
+    spoil(1, 128)
+    o, lse = bsa.cache_attention(c, q.cuda(), seqs=i32(1), causal=True)
+    assert torch.isfinite(o[:, :, :4]).all() and not torch.isfinite(o[:, :, 4:]).any()
+    k, v = m.values(1)
+    ref = OC.attention(q[0].double().numpy(), k, v, keep_of(128 + sb, sb + 4, 2, True))
+    assert_close(o[0, :, :4], lse[0, :, :4], [x[:, :4] for x in ref], q, 128 + sb, "causal")
+    # A mask of 32 keys: head 0 leaves out what head 1 attends.
+    if sb <= 32:
+        q = rand(g, 1, 2, 1, d)
+        spoil(0, 32)
+        mask = torch.ones(1, 2, 7, dtype=torch.uint8)
+        mask[0, 0, 1] = 0
+        o, lse = bsa.cache_attention(c, q.cuda(), seqs=i32(0), mask=mask.cuda(), bk=32)
+        assert torch.isfinite(o[0, 0]).all() and not torch.isfinite(o[0, 1]).any()
+        k, v = m.values(0)
+        ref = OC.attention(q[0].double().numpy(), k, v, keep_of(200, 1, 2, False, mask[0].numpy(), 32))
+        assert_close(o[0, :1], lse[0, :1], [x[:1] for x in ref], q, 200, "mask")
+        # Nobody attends it: nobody sees it.
+        mask[0, 1, 1] = 0
+        o, lse = bsa.cache_attention(c, q.cuda(), seqs=i32(0), mask=mask.cuda(), bk=32)
+        ref = OC.attention(q[0].double().numpy(), k, v, keep_of(200, 1, 2, False, mask[0].numpy(), 32))
+        assert_close(o[0], lse[0], ref, q, 200, "nobody")
+    assert bsa.cache_status(c) == (0, 0)
