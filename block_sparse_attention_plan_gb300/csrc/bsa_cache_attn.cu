@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       // 2^e with amax in [2^e, 2^(e+1)); rows of zeros and of infinities keep 1.
       int e = (int)(__float_as_uint(amax) >> 23) - 127;
       if (!(amax > 0.f) || amax == INFINITY) e = 0;
-      e = max(e, -100);
+      e = max(e, -126);  // (the least power that is normal)
       const float down = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
       const float up = __uint_as_float((uint32_t)(127 + min(e, 126)) << 23);
 #pragma unroll

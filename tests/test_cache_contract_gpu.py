@@ -475,3 +475,18 @@ def test_scales_of_blocks_that_a_row_does_not_attend(bsa, kind, d, sb, fill):
         ref = OC.attention(q[0].double().numpy(), k, v, keep_of(200, 1, 2, False, mask[0].numpy(), 32))
         assert_close(o[0], lse[0], ref, q, 200, "nobody")
     assert bsa.cache_status(c) == (0, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_down_to_the_least_numbers(bsa, d):
+    """Rows of q below 2^-100 with a scale to match keep their bits."""
+    m, c = filled(bsa, [300, 90], 1, 32, 32, d, "int8", 10, seed=53)
+    g = torch.Generator().manual_seed(53)
+    for e in (-105, -114, -119):
+        q = rand(g, 2, 4, 1, d) * 2.0 ** e
+        scale = 2.0 ** (-e - 3)
+        o, lse = bsa.cache_attention(c, q.cuda(), scale=scale)
+        for b in range(2):
+            k, v = m.values(b)
+            ref = OC.attention(q[b].double().numpy(), k, v, keep_of(k.shape[1], 1, 4), scale)
+            assert_close(o[b], lse[b], ref, q, k.shape[1], f"2^{e}")
