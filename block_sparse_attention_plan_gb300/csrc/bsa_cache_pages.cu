@@ -563,8 +563,10 @@ cudaError_t launch_cache_resize(const CacheDev& c, const int32_t* seqs, const in
   }
   const int smem = 4 * n * (int)sizeof(int);
   cudaError_t e = cudaSuccess;
+  // (one limit for every call: the attribute is the kernel's, shared by host threads)
   if (smem > 48 * 1024 - 256)
-    e = cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             4 * kCacheListMax * (int)sizeof(int));
   if (e != cudaSuccess) return e;
   e = launch_after(resize_kernel, dim3(1), dim3(kThreads), smem, s, c, seqs, new_lens, n);
   if (e != cudaSuccess) return e;

@@ -490,3 +490,31 @@ def test_queries_down_to_the_least_numbers(bsa, d):
             k, v = m.values(b)
             ref = OC.attention(q[b].double().numpy(), k, v, keep_of(k.shape[1], 1, 4), scale)
             assert_close(o[b], lse[b], ref, q, k.shape[1], f"2^{e}")
+
+
+def test_two_threads_resize_caches_by_long_lists(bsa):
+    """Lists whose sizes need different amounts of shared memory, at once."""
+    import threading
+    caches = [bsa.cache_create(16, 1, 16, 64, 4096, 1) for _ in range(2)]
+    lists = [torch.full((n,), 0, dtype=torch.int32, device="cuda") for n in (4096, 3500)]
+    torch.cuda.synchronize()
+    bad = []
+    start = threading.Barrier(2)
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        try:
+            start.wait()
+            for _ in range(1000):
+                bsa.cache_resize(caches[i], lists[i], stream=stream)
+        except Exception as e:
+            bad.append(repr(e))
+        torch.cuda.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+    assert all(bsa.cache_status(c) == (0, 0) for c in caches)

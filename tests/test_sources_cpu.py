@@ -31,3 +31,19 @@ def test_kernels_that_overlap_wait_before_they_read():
     for name, text in sources():
         if name != "bsa_launch.h" and "launch_after(" in text:
             assert text.count("next_may_launch();") == text.count("wait_for_previous();") > 0, name
+
+
+def test_shared_memory_limits_are_constants():
+    """A kernel's limit of dynamic shared memory belongs to the kernel, which host
+    threads share: set to what one call needs, it may be too small for another's
+    launch.  Every setting is a constant expression."""
+    found = 0
+    for name, text in sources():
+        for m in re.finditer(r"cudaFuncAttributeMaxDynamicSharedMemorySize,\s*([^;]*?)\);", text):
+            found += 1
+            value = m.group(1).replace("(int)", "")
+            if re.fullmatch(r"\w+", value) and not value.startswith("k"):  # a variable: what it is set to
+                value = re.search(r"int %s = ([^;]*);" % value, text).group(1)
+            names = [w for w in re.findall(r"[A-Za-z_]\w*", value) if w not in ("sizeof", "int")]
+            assert any(w.startswith("k") for w in names) and "n" not in names, (name, value)
+    assert found >= 5
