@@ -89,6 +89,22 @@ bsa_status compute_layout(int B, int H, int NQB, int NKB, int bq, int bk, int g,
   return BSA_OK;
 }
 
+// A driver function by its name (null if the driver has none).
+void* driver_entry(const char* name) {
+  void* f = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion(name, &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return f;
+}
+
+bool context_is_current() {
+  static const auto get = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(driver_entry("cuCtxGetCurrent"));
+  CUcontext ctx = nullptr;
+  return get && get(&ctx) == CUDA_SUCCESS && ctx != nullptr;
+}
+
 // Device capability check, cached per device.
 bsa_status check_arch(int* dev_out) {
   int dev = 0;
@@ -108,26 +124,18 @@ bsa_status check_arch(int* dev_out) {
   if (cache[dev] != 1) return BSA_ERR_ARCH;
   // A host thread's first call: make the device's context current, which the
   // runtime does by itself only for calls that need it, and the driver's tensor
-  // map encoder, called before any of those, asks for.
+  // map encoder, called before any of those, asks for.  A context that is current
+  // already (a caller's own, made with the driver's API) stays.
   static thread_local int current = -1;
   if (current != dev) {
-    if (cudaSetDevice(dev) != cudaSuccess) return BSA_ERR_CUDA;
+    if (!context_is_current() && cudaSetDevice(dev) != cudaSuccess) return BSA_ERR_CUDA;
     current = dev;
   }
   return BSA_OK;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
+  static const auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_entry("cuTensorMapEncodeTiled"));
   return fn;
 }
 

@@ -518,3 +518,37 @@ def test_two_threads_resize_caches_by_long_lists(bsa):
         t.join()
     assert not bad, bad
     assert all(bsa.cache_status(c) == (0, 0) for c in caches)
+
+
+def test_a_context_of_the_callers_own_stays_current(bsa):
+    """A thread that works in a context made with the driver's API: its first
+    call runs there, and leaves it current."""
+    import ctypes
+    import threading
+    from block_sparse_attention_plan_gb300 import _cache
+    lib, cu = _cache._library(), ctypes.CDLL("libcuda.so.1")
+    out = {}
+
+    def work():
+        ctx, now, at = ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_uint64()
+        ok = [cu.cuInit(0), cu.cuCtxCreate_v2(ctypes.byref(ctx), 0, 0), cu.cuMemAlloc_v2(ctypes.byref(at), 4096)]
+        if any(ok):
+            out["skip"] = ok
+            return
+        f = lambda o: ctypes.c_void_p(at.value + o)
+        c = _cache.CacheC(f(0), f(0), f(0), f(0), f(256), f(512), f(768), f(1024), 0, 8, 1, 16, 64, 16, 4, 4)
+        out["status"] = lib.bsa_cache_init(ctypes.byref(c), None)
+        cu.cuCtxGetCurrent(ctypes.byref(now))
+        out["same"] = now.value == ctx.value
+        table = (ctypes.c_int32 * 16)()
+        out["copied"] = cu.cuMemcpyDtoH_v2(table, ctypes.c_uint64(at.value + 256), 64)
+        out["table"] = list(table)
+        cu.cuMemFree_v2(at)
+        cu.cuCtxDestroy_v2(ctx)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    if "skip" in out:
+        pytest.skip(f"no context: {out['skip']}")
+    assert out == {"status": 0, "same": True, "copied": 0, "table": [-1] * 16}
