@@ -552,3 +552,125 @@ def test_a_context_of_the_callers_own_stays_current(bsa):
     if "skip" in out:
         pytest.skip(f"no context: {out['skip']}")
     assert out == {"status": 0, "same": True, "copied": 0, "table": [-1] * 16}
+
+
+# ------------------------------------------------- forms that no test above has
+
+@pytest.mark.parametrize("kind,page,sb,d,g,nq,bk", [
+    ("int8", 16, 16, 64, 4, 1, 32), ("e4m3", 32, 32, 64, 8, 1, 64), ("int8", 32, 16, 64, 2, 13, 128),
+    ("int8", 64, 64, 128, 4, 30, 32), ("e4m3", 16, 16, 64, 7, 20, 32), ("e4m3", 128, 64, 64, 2, 60, 256),
+    ("int8", 256, 256, 128, 1, 5, 64)])
+def test_block_masks_of_every_form(bsa, kind, page, sb, d, g, nq, bk):
+    """Masks in values: tiles over two mask blocks (d 64), both code types, small
+    pages, more than 96 rows; the mask ends before the longest sequence, at an
+    odd number of blocks."""
+    lens = [1000, 130, 641, 1, 0, 33]
+    m, c = filled(bsa, lens, 2, page, sb, d, kind, -(-1000 // page), seed=bk + nq)
+    gen = torch.Generator().manual_seed(bk + nq)
+    mask = (torch.rand(6, 2 * g, 960 // bk | 1, generator=gen) < 0.4).to(torch.uint8) * 5
+    mask[0, 0], mask[2, g:] = 0, 0
+    q = rand(gen, 6, 2 * g, nq, d)
+    for causal in (False, True):
+        o, lse = bsa.cache_attention(c, q.cuda(), mask=mask.cuda(), bk=bk, causal=causal)
+        assert bsa.cache_status(c) == (0, 0)
+        for b, n in enumerate(lens):
+            k, v = m.values(b)
+            ref = OC.attention(q[b].double().numpy(), k, v, keep_of(n, nq, 2 * g, causal, mask[b].numpy(), bk))
+            assert_close(o[b], lse[b], ref, q, n, f"row {b} causal {causal}")
+
+
+def test_forward_with_split_weights(bsa):
+    m, c = filled(bsa, [400, 256], 2, 64, 64, 128, "e4m3", 8, seed=61)
+    g = torch.Generator().manual_seed(61)
+    mask = (torch.rand(2, 4, 2, 4, generator=g) < 0.8).to(torch.uint8)
+    mask[:, :, :, 0] = 1
+    p = bsa.plan(mask.cuda(), 64, 128, 2)
+    q = rand(g, 2, 4, 128, 128)
+    o, lse = bsa.cache_forward(p, c, q.cuda(), causal=True, split=True)
+    assert bsa.sync_status(p)[0] == 0 and bsa.cache_status(c) == (0, 0)
+    from compare import assert_attention_close
+    refs = []
+    for b in range(2):
+        k, v = m.values(b)
+        keep = keep_of(k.shape[1], 128, 4, True)
+        keep &= mask[b].numpy().astype(bool).repeat(64, 1).repeat(128, 2)[:, :, :k.shape[1]]
+        refs.append(OC.attention(q[b].double().numpy(), k, v, keep)[:2])
+    assert_attention_close(o, lse, np.stack([r[0] for r in refs]), np.stack([r[1] for r in refs]), "split")
+
+
+def test_too_few_pages_take_the_releases_back(bsa):
+    """A list that gives pages back (shared ones too) and still lacks some
+    changes nothing at all."""
+    m = OC.CacheModel(10, 2, 16, 64, 5, 6, "e4m3", 16, seed=4)
+    assert m.resize([60, 40, 20]) == 0
+    m.fork([0], [3])
+    c = upload(bsa, m)
+    for lens, seqs in (([16, 0, 96, 70], [0, 1, 2, 3]), ([0, 96, 96], [3, 1, 2]), ([0, 0, 96, 96], [0, 1, 2, 4])):
+        before = m.refs.copy()
+        missing = m.resize(lens, seqs)
+        assert missing > 0 and np.array_equal(m.refs, before)
+        bsa.cache_resize(c, i32(*lens), i32(*seqs))
+        assert bsa.cache_status(c) == (-5, missing)
+        assert_state(c, m, f"{lens} {seqs}")
+    assert m.resize([16, 0, 50], [0, 1, 2]) == 0
+    bsa.cache_resize(c, i32(16, 0, 50), i32(0, 1, 2))
+    assert_state(c, m)
+
+
+@pytest.mark.parametrize("kind,page,sb", [("e4m3", 32, 16), ("int8", 64, 16), ("int8", 16, 16)])
+def test_page_operations_and_tokens_in_a_small_pool(bsa, kind, page, sb):
+    """A seeded run of every operation in a pool that is often too small."""
+    rng = np.random.default_rng(page + sb)
+    gen = torch.Generator().manual_seed(page + sb)
+    m = OC.CacheModel(24, 2, page, 64, 8, 7, kind, sb, seed=2)
+    c = upload(bsa, m)
+    refused = 0
+    for step in range(150):
+        op = int(rng.integers(6))
+        live, empty = np.nonzero(m.lens)[0], np.nonzero(m.lens == 0)[0]
+        if op <= 1:
+            n = int(rng.integers(1, 6))
+            seqs = rng.choice(8, n, replace=False)
+            lens = m.lens[seqs] + rng.integers(0, 3, n) if op else rng.integers(0, 7 * page + 1, n)
+            lens = np.minimum(lens, 7 * page)
+            missing = m.resize(lens, seqs)
+            bsa.cache_resize(c, i32(*lens.tolist()), i32(*seqs.tolist()))
+            assert bsa.cache_status(c) == ((-5, missing) if missing else (0, 0)), step
+            refused += missing > 0
+        elif op == 2 and len(live) and len(empty):
+            n = int(rng.integers(1, len(empty) + 1))
+            src, dst = rng.choice(live, n).tolist(), rng.choice(empty, n, replace=False).tolist()
+            m.fork(src, dst)
+            bsa.cache_fork(c, i32(*src), i32(*dst))
+        elif op == 3:
+            m.compact()
+            bsa.cache_compact(c)
+        elif op == 4:
+            s = int(rng.integers(8))
+            m.resize([0], [s])
+            bsa.cache_free(c, i32(s))
+        elif len(live):
+            s = int(rng.choice(live))
+            n = int(rng.integers(1, m.lens[s] + 1))
+            at = int(rng.integers(0, m.lens[s] - n + 1))
+            x = rand(gen, 1, 2, n, 64) * 2.0 ** float(rng.integers(-8, 8))
+            append_both(bsa, m, c, x, -x, [s], [at])
+            bsa.cache_status(c)  # (tokens for shared pages are refused)
+        assert_state(c, m, f"step {step} op {op}")
+    assert refused >= 5
+
+
+def test_tokens_and_queries_of_fp16(bsa):
+    m = OC.CacheModel(8, 2, 32, 64, 2, 4, "e4m3", 16, seed=8)
+    assert m.resize([100, 31]) == 0
+    c = upload(bsa, m)
+    g = torch.Generator().manual_seed(8)
+    x = rand(g, 2, 2, 100, 64, dtype=torch.float16)
+    append_both(bsa, m, c, x, x, [0, 1], [0, 0], [100, 31])
+    assert_state(c, m)
+    q = rand(g, 2, 8, 2, 64, dtype=torch.float16)
+    o, lse = bsa.cache_attention(c, q.cuda(), causal=True)
+    assert o.dtype == torch.float16
+    for b, n in enumerate((100, 31)):
+        k, v = m.values(b)
+        assert_close(o[b], lse[b], OC.attention(q[b].double().numpy(), k, v, keep_of(n, 2, 8, True)), q, n, f"row {b}")
