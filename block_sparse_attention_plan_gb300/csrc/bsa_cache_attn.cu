@@ -600,13 +600,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       const bool tail = key0 + TK > len;
       const uint32_t unread = (uint32_t)tq[0] >> kNoBox;  // boxes of the tile
       auto box_read = [&](int r) { return (unread >> (r >> lcs) & 1u) == 0u; };  // that of the tile's key r
-      // The tile's computation, for tiles that every row attends wholly, for the
-      // others, and for those among them with a scale that is no number: the code
-      // of the masks, in the loop that most tiles take, would cost those a tenth
-      // (registers, and the loop outgrows the instruction cache), that of the
-      // scales 2 % of the masked ones.
-      auto compute = [&](auto masked_c, auto nans_c) {
-      constexpr bool kMasked = decltype(masked_c)::value, kNans = decltype(nans_c)::value;
+      // The tile's computation, for tiles that every row attends wholly and for
+      // the others: the code of the masks, in the loop that most tiles take,
+      // would cost those a tenth (registers, and the loop outgrows the
+      // instruction cache).
+      auto compute = [&](auto masked_c) {
+      constexpr bool kMasked = decltype(masked_c)::value;
 #pragma unroll 1
       for (int kb16 = 0; kb16 < TK; kb16 += 16 * KG) {
         // ---- S^T = K Q^T: 16 keys a time
@@ -762,26 +761,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
             }
           }
           if constexpr (KIND == BSA_CACHE_E4M3 && kMasked) take_nans<NT, DV, MT>(v[kg], o, kept, kg);
-          if constexpr (kNans) {
-            if (!(fabsf(sv[kg]) < INFINITY)) {
-              // No number: it reaches the rows that attend a key of the 16 (times a
-              // weight of 0 it would reach the others too).
-              uint32_t attends = kept >> (kg * NT * 4);
-              attends |= __shfl_xor_sync(0xffffffffu, attends, 4);
-              attends |= __shfl_xor_sync(0xffffffffu, attends, 8);
-              attends |= __shfl_xor_sync(0xffffffffu, attends, 16);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                  if (attends >> (4 * nt + c) & 5u) {
-#pragma unroll
-                    for (int k = 0; k < MT; ++k)
-                      o[nt][k][c] = o[nt][k][c + 2] = __uint_as_float(0x7fffffffu);
-                  }
-              sv[kg] = 0.f;
-            }
-          }
         }
         // Pairs of keys of one element: {a0 b0 a1 b1}, {a2 b2 a3 b3}.
 #pragma unroll
@@ -813,10 +792,33 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
       }
       };
       if (key0 + TK > first_limit || p.mask != nullptr || unread != 0u) {
-        if (__any_sync(0xffffffffu, !(fabsf(sq[0]) < INFINITY))) compute(std::true_type{}, std::true_type{});
-        else compute(std::true_type{}, std::false_type{});
+        if (__any_sync(0xffffffffu, !(fabsf(sq[0]) < INFINITY))) {
+          // A scale of values that is no number reaches the rows that attend a key
+          // of its 16 (times a weight of 0 it would reach the others too).
+          const uint32_t sel0 = p.mask ? __ballot_sync(0xffffffffu, mq[0].x != 0) : 0xffffffffu;
+          const uint32_t sel1 = p.mask ? __ballot_sync(0xffffffffu, mq[0].y != 0) : 0xffffffffu;
+#pragma unroll 1
+          for (int gr = 0; gr < C::kGroups; ++gr) {
+            const float sv = __shfl_sync(0xffffffffu, sq[0], C::kGroups + gr);
+            if (fabsf(sv) < INFINITY || !box_read(16 * gr)) continue;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int row = 8 * nt + 2 * t4 + c;
+                const bool attends = key0 + 16 * gr < __shfl_sync(0xffffffffu, lim, row) &&
+                                     ((16 * gr < 32 ? sel0 : sel1) >> row & 1u);
+                if (attends) {
+#pragma unroll
+                  for (int k = 0; k < MT; ++k) o[nt][k][c] = o[nt][k][c + 2] = __uint_as_float(0x7fffffffu);
+                }
+              }
+          }
+          if (lane >= C::kGroups && !(fabsf(sq[0]) < INFINITY)) sq[0] = 0.f;
+        }
+        compute(std::true_type{});
       } else {
-        compute(std::false_type{}, std::false_type{});
+        compute(std::false_type{});
       }
       __syncwarp();  // every lane has read the stage
 #pragma unroll
