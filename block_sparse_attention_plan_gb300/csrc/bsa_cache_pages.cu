@@ -177,10 +177,11 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
     __syncthreads();
   }
   // Growth into a partly filled last page that others hold too.
-  bool cow = false;
+  bool cow = false, enters = false;  // enters: blocks past the old length, in a page held already
   for (int i = tid; i < n; i += kThreads) {
     int shared_page = -1;
     const int s = s_seq[i], have = s_have[i];
+    enters |= s >= 0 && s_want[i] > have + 1 && (have & (c.page - 1)) != 0;
     if (s >= 0 && s_want[i] > have && have % c.page) {
       const int p = __ldcg(c.table + (size_t)s * c.max_pages + have / c.page);
       if (p < 0 || p >= c.num_pages) {
@@ -292,23 +293,25 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const CacheDev c, cons
   __syncthreads();
   // Scales of the copied pages, then (others may be copying from the page that
   // one keeps) 0 for the blocks past the old length of pages that were held.
-  const int blocks = c.page / c.sb, scales = c.Hkv * blocks;
-  for (long long x = tid; x < (long long)s_pairs * scales; x += kThreads) {
-    const int pr = (int)(x / scales), q = (int)(x - (long long)pr * scales);
+  const int lsb = 31 - __clz(c.sb), blocks = c.page >> lsb, scales = c.Hkv * blocks;
+  for (int x = tid; x < s_pairs * scales; x += kThreads) {  // (below 2^31: pool rows are)
+    const int pr = x / scales, q = x - pr * scales;
     const size_t from = (size_t)__ldcg(c.pair_src() + pr) * scales + q, to = (size_t)__ldcg(c.pair_dst() + pr) * scales + q;
-    c.ks[to] = c.ks[from];
-    c.vs[to] = c.vs[from];
+    const float k = c.ks[from], v = c.vs[from];
+    c.ks[to] = k;
+    c.vs[to] = v;
   }
-  __syncthreads();
-  for (int i = warp; i < n; i += kThreads / 32) {
-    const int s = s_seq[i], have = s_have[i], kept = (have % c.page + c.sb - 1) / c.sb;
-    if (s < 0 || s_want[i] <= have + 1 || kept == 0 || kept == blocks) continue;
-    const int p = __ldcg(c.table + (size_t)s * c.max_pages + have / c.page);
-    if (p < 0 || p >= c.num_pages) continue;
-    for (int x = lane; x < c.Hkv * (blocks - kept); x += 32) {
-      const size_t at = ((size_t)p * c.Hkv + x / (blocks - kept)) * blocks + kept + x % (blocks - kept);
-      c.ks[at] = 0.f;
-      c.vs[at] = 0.f;
+  if (__syncthreads_or(enters)) {
+    for (int i = warp; i < n; i += kThreads / 32) {
+      const int s = s_seq[i], have = s_have[i], kept = ((have & (c.page - 1)) + c.sb - 1) >> lsb;
+      if (s < 0 || s_want[i] <= have + 1 || kept == 0 || kept == blocks) continue;
+      const int p = __ldcg(c.table + (size_t)s * c.max_pages + have / c.page);
+      if (p < 0 || p >= c.num_pages) continue;
+      for (int x = lane; x < c.Hkv * (blocks - kept); x += 32) {
+        const size_t at = ((size_t)p * c.Hkv + x / (blocks - kept)) * blocks + kept + x % (blocks - kept);
+        c.ks[at] = 0.f;
+        c.vs[at] = 0.f;
+      }
     }
   }
   if (tid == 0) {
