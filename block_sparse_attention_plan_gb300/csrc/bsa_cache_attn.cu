@@ -19,14 +19,18 @@
 // whole number, so that 7 - m and the differences of references are exact.
 //
 // What bounds it: 2 d bytes per key and K/V head at the memory's rate (32
-// sequences of up to 32768 tokens, 8 heads of 128, 4 rows: 1.11 GB in 171 us,
-// 6.5 TB/s) up to about 16 rows, the warps' issue and latency above (16
-// sequences of up to 16000, 8 heads of 64, 20 rows: 61 us, 2.4 TB/s); an SM's
+// sequences of up to 32768 tokens, 8 heads of 128, 4 rows: 1.11 GB in 170 to
+// 173 us, 6.5 TB/s) up to about 16 rows, the warps' issue and latency above (16
+// sequences of up to 16000, 8 heads of 64, 20 rows: 63 us, 2.4 TB/s); an SM's
 // share is 23 bytes per cycle, against which a tile of 8 KB costs 250 to 800 warp
 // instructions (8 to 24 rows) of the 1400 that the SM can issue meanwhile.
-// Hence mma.sync and not tcgen05: the products are at most 96 rows wide and far
-// from the tensor pipe's limit, and the codes have to pass through registers
-// to be converted anyway.
+// mma.sync and not tcgen05: at the memory's rate the products are 2 flops per row
+// and byte, 6 % of the tensor pipe's measured rate at 8 rows and 17 % at 24, and
+// the codes have to pass through registers to be converted anyway.  That holds
+// for the rows of one row tile.  With more, every row tile reads and converts a
+// tile again, and at 96 rows the products alone are two thirds of the pipe's
+// rate: there converting once and tcgen05 would be the faster way, which this
+// kernel does not take (24 queries of 16 sequences, 4 heads a group: 329 us).
 //
 // Work split: the tiles (8 KB: 32 keys at d = 128, 64 at d = 64) of all (sequence, K/V head) pairs form one line
 // which the CTAs cut into equal pieces, so that ragged lengths and few long
@@ -288,10 +292,10 @@ template <int D, int KIND, int NT>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = AttnCfg<D>;
   constexpr int TK = C::TK;
-  // Groups of 16 keys whose scores are held at once, as registers allow (d = 128
-  // with 16 rows: 67.3 us with one, 68.6 with two and its spills; d = 64: 46.6
-  // and 43.9).
-  constexpr int KG = NT * D <= 64 ? 4 : (NT * D <= 128 ? 2 : 1);
+  // Groups of 16 keys whose scores are held at once, as registers allow (16 rows
+  // of 16 sequences, one and two groups, E4M3 / INT8: d = 128 70.8 / 73.1 and 69.7
+  // / 71.7 us, d = 64 48.1 / 50.9 and 45.0 / 47.5 us).
+  constexpr int KG = NT * D <= 64 ? 4 : (NT < 3 ? 2 : 1);
   extern __shared__ __align__(1024) uint8_t smem[];
   int* s_prefix = reinterpret_cast<int*>(smem + C::kOffMerge);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
@@ -781,7 +785,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const __grid_cons
                   const uint64_t f = f2_make(sv[kg], sv[kg]);
                   f2_split(ffma2(f, f2_make(y[0], y[1]), f2_make(acc[0], acc[1])), acc[0], acc[1]);
                   f2_split(ffma2(f, f2_make(y[2], y[3]), f2_make(acc[2], acc[3])), acc[2], acc[3]);
-                } else {  // (pairs cost the fullest variant registers: 102 against 96 us for 20 rows)
+                } else {  // (pairs cost the fullest variant registers: 335 against 329 us for 96 rows)
 #pragma unroll
                   for (int e = 0; e < 4; ++e) acc[e] = fmaf(sv[kg], y[e], acc[e]);
                 }
