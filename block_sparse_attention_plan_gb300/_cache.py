@@ -188,8 +188,8 @@ def _rows(c: Cache, t: torch.Tensor, name: str):
 def cache_append(c: Cache, k: torch.Tensor, v: torch.Tensor, seqs: Optional[torch.Tensor] = None,
                  counts: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
                  stream: Optional[torch.cuda.Stream] = None) -> None:
-    """Quantise and store tokens (bsa_cache_append): k, v [n, Hkv, T, d] (any
-    strides between rows), of which the first ``counts[i]`` of row i become the
+    """Quantise and store tokens (bsa_cache_append): k, v [n, Hkv, T, d], bfloat16
+    or float16 (any strides between rows), of which the first ``counts[i]`` of row i become the
     tokens ``start[i]``.. of sequence ``seqs[i]``; by default all T, as the
     sequence's last ones, sequences 0 .. n-1."""
     n, h, T, d = k.shape
@@ -207,8 +207,8 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                     lse: Optional[torch.Tensor] = None,
                     stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Attention of q [B, Hq, nq, d] over the cached tokens of sequences
-    ``seqs`` (default 0 .. B-1) (bsa_cache_attention).  ``mask`` u8 [B, Hq, NKB]
+    """Attention of q [B, Hq, nq, d], bfloat16 or float16, over the cached tokens
+    of sequences ``seqs`` (default 0 .. B-1) (bsa_cache_attention).  ``mask`` u8 [B, Hq, NKB]
     selects blocks of ``bk`` keys per query head; ``causal``: the queries are
     the sequence's last nq tokens.  Returns (O, LSE)."""
     B, Hq, nq, d = q.shape
@@ -285,7 +285,8 @@ def cache_forward(p: Plan, c: Cache, q: torch.Tensor, seqs: Optional[torch.Tenso
     """``forward`` of plan ``p`` with keys and values from the cache's
     sequences ``seqs`` (default 0 .. B-1) (bsa_cache_forward): key lengths are
     the sequences', and with ``causal`` the queries are their last Nq tokens.
-    Returns (O, LSE)."""
+    Queries and O are bfloat16, as everywhere in the forward; float16 is for
+    ``cache_append`` and ``cache_attention`` alone.  Returns (O, LSE)."""
     L = p.layout
     if (q.dtype != torch.bfloat16 or q.device != c.device or not q.is_contiguous()
             or tuple(q.shape) != (L.B, L.H, L.NQB * L.bq, c.d)):
@@ -315,7 +316,8 @@ def cache_forward(p: Plan, c: Cache, q: torch.Tensor, seqs: Optional[torch.Tenso
 
 def cache_resize(c: Cache, new_lens: torch.Tensor, seqs: Optional[torch.Tensor] = None,
                  stream: Optional[torch.cuda.Stream] = None) -> None:
-    """Set sequences' lengths, taking and giving back pages (bsa_cache_resize)."""
+    """Set sequences' lengths, taking and giving back pages (bsa_cache_resize);
+    blocks that a sequence enters hold nothing until ``cache_append`` stores it."""
     n = new_lens.shape[0]
     _call(c, "resize", c._ref, _list(c, seqs, "seqs", n), _list(c, new_lens, "new_lens"), n, _stream(c, stream))
 

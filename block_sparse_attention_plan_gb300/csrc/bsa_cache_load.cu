@@ -3,12 +3,13 @@
 //
 // The forward's products are bound by the tensor pipe and read each K/V tile
 // once per query tile that selects it, so the codes are converted once, by a
-// pass near the memory's rate (1 byte read and 2 written per element; issue is
-// at 75 %), and not again in every tile's inner loop.  The largest key norm and
+// pass of its own (1 byte read and 2 written per element), and not again in
+// every tile's inner loop.  Issue bounds it, at 76 %: what it writes stays in
+// L2, and DRAM is at 28 %.  The largest key norm and
 // the largest value of every K/V unit (see bsa_prep.cu) are taken while the
 // elements are in registers: a pass over the 2-byte copies costs as much again
-// (16384 keys of 8 heads, d 128: 18.7 us, 5.4 TB/s of what it reads and writes,
-// against 20 + 18 us in two passes).  Positions at and past a sequence's length
+// (16384 keys of 8 heads, d 128: 18.7 us, 5.4 TB/s of what it reads and writes
+// together, against 20 + 18 us in two passes).  Positions at and past a sequence's length
 // become zero: the forward masks them but multiplies what they hold.
 #include "bsa_cache.h"
 #include "bsa_cache_codes.cuh"

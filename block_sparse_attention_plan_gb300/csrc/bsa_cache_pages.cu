@@ -8,8 +8,8 @@
 // kernel moves the page contents it queued.  The copies are what costs: a page
 // of 64 tokens and 8 heads is 131 KB.  Compacting 5280 held pages of 8000 moves
 // 471 MB in 91 us, of which the copy takes 74 (6.4 TB/s); a step of a few pages
-// is the bookkeeping's chain of reads and scans, 5 us to compact 600 pages, 11 and
-// 19 us to grow 16 and 256 forked sequences by a token.
+// is the bookkeeping's chain of reads and scans, 6 us to compact 600 pages, 13 and
+// 22 us to grow 16 and 256 forked sequences by a token.
 #include "bsa_cache.h"
 
 namespace bsa {

@@ -679,7 +679,7 @@ bsa_status bsa_cache_attention(const bsa_cache* cache, const bsa_rows* q, const 
  * sequence's queries are its last Nq tokens).  The plan's Nk may be larger or
  * smaller than the lengths (tokens past Nk are not attended).  d and Hkv are
  * the cache's; 128-row q-tiles only.
- * Q, O: device bf16 [B][Hq][Nq][d]; LSE fp32 [B][Hq][Nq]; flags as
+ * Q, O: device bf16 (not fp16) [B][Hq][Nq][d]; LSE fp32 [B][Hq][Nq]; flags as
  *   bsa_forward_ex; workspace: device, 256-byte aligned,
  *   bsa_cache_forward_workspace_bytes bytes (the keys and values in bf16).
  * Scales other than powers of two round the values to bf16.  As in bsa_forward,
