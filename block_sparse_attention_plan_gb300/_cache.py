@@ -317,7 +317,9 @@ def cache_forward(p: Plan, c: Cache, q: torch.Tensor, seqs: Optional[torch.Tenso
 def cache_resize(c: Cache, new_lens: torch.Tensor, seqs: Optional[torch.Tensor] = None,
                  stream: Optional[torch.cuda.Stream] = None) -> None:
     """Set sequences' lengths, taking and giving back pages (bsa_cache_resize);
-    blocks that a sequence enters hold nothing until ``cache_append`` stores it."""
+    blocks that a sequence enters hold nothing until ``cache_append`` stores it.
+    A token that a growth by one takes is to be stored before the sequence grows
+    further."""
     n = new_lens.shape[0]
     _call(c, "resize", c._ref, _list(c, seqs, "seqs", n), _list(c, new_lens, "new_lens"), n, _stream(c, stream))
 

@@ -508,9 +508,9 @@ bsa_status bsa_attention_host(const uint8_t* mask, int B, int H, int NQB, int NK
  * What the kernels find wrong in device data is recorded in the control words,
  * the first of its kind kept, and reported by bsa_cache_status: a sequence
  * index or length out of range, a sequence named twice, a fork onto a sequence
- * that holds tokens, tokens for a shared page (BSA_ERR_INVALID_ARG, detail = index in the list); a held
- * token whose table entry is no page (BSA_ERR_PLAN_MISMATCH, detail = the
- * sequence); too few free pages (BSA_ERR_WORKSPACE, detail = pages missing).
+ * that holds tokens, tokens for a shared page (BSA_ERR_INVALID_ARG, detail =
+ * index in the list); a held token whose table entry is no page
+ * (BSA_ERR_PLAN_MISMATCH, detail = the sequence); too few free pages (BSA_ERR_WORKSPACE, detail = pages missing).
  * Such an item is skipped (for BSA_ERR_WORKSPACE the whole call is): tokens of
  * no page are not attended by bsa_cache_attention, and a sequence that has some
  * among the plan's keys is an empty one to bsa_cache_forward; a sequence is not
@@ -573,8 +573,8 @@ bsa_status bsa_cache_status(const bsa_cache* cache, void* stream, int32_t* detai
  * wholly past the old length become 0, whatever the pages' last holders left
  * there.  (A growth by a single token leaves them as they are, for storing the
  * token sets the one of its block; store it before the sequence grows further.)
- * If the free pages do not suffice nothing is changed.  n <= 4096 (any n if both lists are
- * NULL).
+ * If the free pages do not suffice nothing is changed.  n <= 4096 (any n if both
+ * lists are NULL).
  * Two kernels (one if new_lens is NULL), no synchronisation.
  */
 bsa_status bsa_cache_resize(const bsa_cache* cache, const int32_t* seqs, const int32_t* new_lens,
@@ -627,11 +627,10 @@ bsa_status bsa_cache_copy_pages(const bsa_cache* dst, const bsa_cache* src, cons
  * largest finite |x| of the stored tokens into the codes' range; if the
  * sequence has other tokens in the block, the larger of that and the block's
  * scale, and if that grows their codes are re-rounded to it (tokens that a block
- * of scale 0, infinity or NaN holds have not been stored: their codes become 0).
- * Codes are
- * rounded to nearest, ties to even; infinities saturate; NaN is stored as NaN
- * (E4M3) or 0 (INT8).  Rows of pages that hold no token of the sequence are
- * left as they were.  One kernel.
+ * whose scale is not finite and positive holds have not been stored: their codes
+ * become 0).  Codes are rounded to nearest, ties to even; infinities saturate;
+ * NaN is stored as NaN (E4M3) or 0 (INT8).  Rows of pages that hold no token of
+ * the sequence are left as they were.  One kernel.
  */
 bsa_status bsa_cache_append(const bsa_cache* cache, const bsa_rows* k, const bsa_rows* v, int dtype,
                             const int32_t* seqs, const int32_t* counts, const int32_t* start, int n,

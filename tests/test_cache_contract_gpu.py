@@ -443,7 +443,6 @@ def test_scales_of_blocks_that_a_row_does_not_attend(bsa, kind, d, sb, fill):
     lens = [200, 128 + sb]
     m, c = filled(bsa, lens, 1, 64, sb, d, kind, 4, seed=47)
     g = torch.Generator().manual_seed(47)
-    per = 64 // sb
 
     def spoil(seq, key):
         p = int(m.table[seq, key // 64])
