@@ -50,11 +50,15 @@ def _library() -> ctypes.CDLL:
     lib.bsa_cache_attention_workspace_bytes.argtypes = [C, I, I, I, I, I]
     lib.bsa_cache_forward_workspace_bytes.restype = N
     lib.bsa_cache_forward_workspace_bytes.argtypes = [P, C]
+    lib.bsa_cache_evict_workspace_bytes.restype = N
+    lib.bsa_cache_evict_workspace_bytes.argtypes = [I]
     for name, args in {
             "init": [C, VP], "status": [C, VP, ctypes.POINTER(ctypes.c_int32)], "resize": [C, VP, VP, I, VP],
             "fork": [C, VP, VP, I, VP], "compact": [C, VP], "copy_pages": [C, C, VP, VP, I, VP],
             "append": [C, R, R, I, VP, VP, VP, I, I, VP],
             "attention": [C, R, R, VP, I, VP, VP, I, I, I, I, I, I, F, VP, N, VP],
+            "weigh": [C, R, VP, I, VP, VP, I, I, I, I, I, I, F, I, VP, I, VP],
+            "evict": [C, VP, I, VP, VP, I, I, VP, I, I, VP, N, VP],
             "forward": [P, C, VP, VP, I, VP, VP, F, VP, N, VP]}.items():
         f = getattr(lib, "bsa_cache_" + name)
         f.restype = I
@@ -215,14 +219,7 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
     if d != c.d:
         raise ValueError("q must be [B, Hq, nq, d] of the cache's d")
     qr = _rows(c, q, "q")
-    NKB, mptr = 0, None
-    if mask is not None:
-        if (mask.dtype != torch.uint8 or mask.device != c.device or mask.dim() != 3
-                or mask.shape[:2] != q.shape[:2] or not mask.is_contiguous()):
-            raise ValueError("mask must be a contiguous CUDA uint8 tensor [B, Hq, NKB]")
-        NKB, mptr = mask.shape[2], mask.data_ptr()
-        if NKB == 0:
-            raise ValueError("mask has no key blocks")
+    NKB, mptr = _mask(c, q, mask)
     if stream is not None and (out is None or lse is None):
         with torch.cuda.stream(stream):  # memory that this stream may write
             out = torch.empty_like(q) if out is None else out
@@ -258,6 +255,18 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
         ws = _scratch(c, need, stream)
         _call(c, "attention", *args, ws.data_ptr(), need, handle)
     return out, lse
+
+
+def _mask(c: Cache, q: torch.Tensor, mask: Optional[torch.Tensor]):
+    """(NKB, pointer) of a block mask of q's batch rows and heads."""
+    if mask is None:
+        return 0, None
+    if (mask.dtype != torch.uint8 or mask.device != c.device or mask.dim() != 3
+            or mask.shape[:2] != q.shape[:2] or not mask.is_contiguous()):
+        raise ValueError("mask must be a contiguous CUDA uint8 tensor [B, Hq, NKB]")
+    if mask.shape[2] == 0:
+        raise ValueError("mask has no key blocks")
+    return mask.shape[2], mask.data_ptr()
 
 
 # Scratch of calls on a device's default stream: they are in order with each
@@ -312,6 +321,60 @@ def cache_forward(p: Plan, c: Cache, q: torch.Tensor, seqs: Optional[torch.Tenso
           (_lib.FWD_CAUSAL if causal else 0) | (_lib.FWD_SPLIT_P if split else 0), out.data_ptr(), lse.data_ptr(),
           0.0 if scale is None else scale, ws.data_ptr(), ws.numel(), _stream(c, stream))
     return out, lse
+
+
+def _weights(c: Cache, t: torch.Tensor) -> Tuple[int, int]:
+    """(pointer, tokens) of a tensor of weights."""
+    if (t.dtype != torch.float32 or t.get_device() != c._index or t.dim() != 3 or not t.is_contiguous()
+            or t.shape[0] != c.max_seqs or t.shape[1] != c.heads):
+        raise ValueError("weights must be a contiguous CUDA float32 tensor [max_seqs, Hkv, tokens]")
+    return t.data_ptr(), t.shape[2]
+
+
+def cache_weigh(c: Cache, q: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor,
+                seqs: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None, bk: int = 0,
+                causal: bool = False, scale: Optional[float] = None, fresh: Optional[int] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Add the attention weight that each cached token gathers over q [B, Hq, nq, d] to ``weights`` float32
+    [max_seqs, Hkv, tokens] (bsa_cache_weigh); q, ``seqs`` (each at most once), ``mask``, ``bk``, ``causal`` and
+    ``scale`` as ``cache_attention`` was given them, ``lse`` what it returned.  The last ``fresh`` tokens of each
+    sequence begin at 0 (default nq: the queries' own tokens, new in a step of decoding; 1 << 30 for a prompt's
+    first call: all of them)."""
+    B, Hq, nq, d = q.shape
+    if d != c.d:
+        raise ValueError("q must be [B, Hq, nq, d] of the cache's d")
+    if lse.dtype != torch.float32 or lse.get_device() != c._index or lse.shape != q.shape[:3] or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous CUDA float32 tensor [B, Hq, nq]")
+    NKB, mptr = _mask(c, q, mask)
+    wptr, tokens = _weights(c, weights)
+    _call(c, "weigh", c._ref, _rows(c, q, "q"), lse.data_ptr(), _ELEMENTS[q.dtype],
+          seqs if seqs is None else _list(c, seqs, "seqs", B), mptr, NKB, bk, B, Hq, nq, CACHE_CAUSAL if causal else 0,
+          0.0 if scale is None else scale, nq if fresh is None else fresh, wptr, tokens, _stream(c, stream))
+
+
+def cache_evict(c: Cache, weights: torch.Tensor, keep: torch.Tensor, seqs: Optional[torch.Tensor] = None,
+                sink: int = 0, recent: int = 0, kept: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Cut sequences ``seqs`` (default 0 .. n-1) to ``keep`` int32 [n] tokens each (bsa_cache_evict): every K/V
+    head keeps the first ``sink``, the last ``recent`` and those of largest ``weights`` between, in their order.
+    Returns ``kept`` int32 [n, Hkv, keep_max] (made here, as wide as sequences may be, when None): where the tokens
+    of each row were; entries behind its length are not written."""
+    n = keep.shape[0]
+    wptr, tokens = _weights(c, weights)
+    if kept is None:
+        shape = (n, c.heads, min(tokens, c.max_pages * c.page_size))
+        if stream is None:
+            kept = torch.empty(shape, dtype=torch.int32, device=c.device)
+        else:
+            with torch.cuda.stream(stream):  # memory that this stream may write
+                kept = torch.empty(shape, dtype=torch.int32, device=c.device)
+    elif (kept.dtype != torch.int32 or kept.get_device() != c._index or kept.dim() != 3 or not kept.is_contiguous()
+          or tuple(kept.shape[:2]) != (n, c.heads)):
+        raise ValueError("kept must be a contiguous CUDA int32 tensor [n, Hkv, keep_max]")
+    ws = _scratch(c, int(_bound.bsa_cache_evict_workspace_bytes(n)), stream)
+    _call(c, "evict", c._ref, wptr, tokens, seqs if seqs is None else _list(c, seqs, "seqs", n), _list(c, keep, "keep"),
+          sink, recent, kept.data_ptr(), kept.shape[2], n, ws.data_ptr(), ws.numel(), _stream(c, stream))
+    return kept
 
 
 def cache_resize(c: Cache, new_lens: torch.Tensor, seqs: Optional[torch.Tensor] = None,

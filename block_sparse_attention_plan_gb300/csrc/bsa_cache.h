@@ -109,6 +109,33 @@ struct CacheLoadParams {
   int device;  // the plan's
 };
 
+// Attention weight of cached tokens (bsa_cache_weigh.cu).
+struct CacheWeighParams {
+  CacheDev c;
+  CacheRows q;
+  const float* lse;     // [B][Hq][nq]
+  float* weights;       // [max_seqs][Hkv][stride]
+  long long stride;
+  const int32_t* seqs;
+  const uint8_t* mask;  // [B][Hq][NKB]
+  int fp16, B, Hq, g, nq, M, NKB, bk, causal, fresh;
+  float scale;
+};
+
+// Eviction of cached tokens (bsa_cache_evict.cu).
+struct CacheEvictParams {
+  CacheDev c;
+  float* weights;       // [max_seqs][Hkv][stride]
+  long long stride;
+  const int32_t* seqs;
+  const int32_t* keep;  // [n]
+  int32_t* kept;        // [n][Hkv][keep_max]: where kept tokens were
+  int32_t* cut;         // [n]: the length a sequence is cut to, -1: it is left as it is
+  int n, sink, recent, keep_max;
+};
+
+cudaError_t launch_cache_evict(const CacheEvictParams& p, int sms, cudaStream_t s);
+cudaError_t launch_cache_weigh(const CacheWeighParams& p, int sms, cudaStream_t s);
 cudaError_t launch_cache_resize(const CacheDev& c, const int32_t* seqs, const int32_t* new_lens, int n,
                                 cudaStream_t s);
 cudaError_t launch_cache_fork(const CacheDev& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);

@@ -266,6 +266,74 @@ bsa_status bsa_cache_attention(const bsa_cache* cache, const bsa_rows* q, const 
   return launch_cache_attention(p, grid, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
+bsa_status bsa_cache_weigh(const bsa_cache* cache, const bsa_rows* q, const float* LSE, int dtype, const int32_t* seqs,
+                           const uint8_t* mask, int NKB, int bk, int B, int Hq, int nq, int flags, float scale,
+                           int fresh, float* weights, int weights_tokens, void* stream) {
+  CacheWeighParams p;
+  std::memset(&p, 0, sizeof(p));
+  bsa_status st = check_cache(cache, &p.c);
+  if (st != BSA_OK) return st;
+  if (!good_rows(q) || !LSE || !aligned(LSE, 4) || !weights || !aligned(weights, 4) || weights_tokens < 1 ||
+      !list_ok(seqs))
+    return BSA_ERR_INVALID_ARG;
+  if ((flags & ~BSA_CACHE_CAUSAL) || fresh < 0) return BSA_ERR_INVALID_ARG;
+  if (dtype != BSA_BF16 && dtype != BSA_FP16) return BSA_ERR_UNSUPPORTED;
+  if (!(scale == scale) || std::isinf(scale)) return BSA_ERR_INVALID_ARG;
+  AttnLayout l;  // (the same limits on sizes)
+  if ((st = attn_layout(p.c, B, Hq, nq, NKB, bk, mask != nullptr, &l)) != BSA_OK) return st;
+  if (!seqs && B > p.c.max_seqs) return BSA_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  if ((st = check_device(&dev)) != BSA_OK || (st = sms_of(dev, &sms)) != BSA_OK) return st;
+  p.q = rows_of(q);
+  p.lse = LSE;
+  p.weights = weights;
+  p.stride = weights_tokens;
+  p.seqs = seqs;
+  p.mask = mask;
+  p.fp16 = dtype == BSA_FP16;
+  p.B = B;
+  p.Hq = Hq;
+  p.g = Hq / p.c.Hkv;
+  p.nq = nq;
+  p.M = p.g * nq;
+  p.NKB = NKB;
+  p.bk = bk;
+  p.causal = flags & BSA_CACHE_CAUSAL ? 1 : 0;
+  p.fresh = fresh;
+  p.scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)p.c.d));
+  return launch_cache_weigh(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+size_t bsa_cache_evict_workspace_bytes(int n) { return n < 1 || n > kCacheListMax ? 0 : align256(4ull * n); }
+
+bsa_status bsa_cache_evict(const bsa_cache* cache, float* weights, int weights_tokens, const int32_t* seqs,
+                           const int32_t* keep, int sink, int recent, int32_t* kept, int keep_max, int n,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  CacheEvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  bsa_status st = check_cache(cache, &p.c);
+  if (st != BSA_OK) return st;
+  if (!weights || !aligned(weights, 4) || weights_tokens < 1 || !keep || !list_ok(keep) || !list_ok(seqs) || !kept ||
+      !list_ok(kept) || keep_max < 1 || n < 1 || sink < 0 || recent < 0 || (!seqs && n > p.c.max_seqs) || !workspace ||
+      !aligned(workspace, 4))
+    return BSA_ERR_INVALID_ARG;
+  if (n > kCacheListMax || (long long)n * p.c.Hkv > (1ll << 24)) return BSA_ERR_UNSUPPORTED;
+  if (workspace_bytes < bsa_cache_evict_workspace_bytes(n)) return BSA_ERR_WORKSPACE;
+  int dev = 0, sms = 0;
+  if ((st = check_device(&dev)) != BSA_OK || (st = sms_of(dev, &sms)) != BSA_OK) return st;
+  p.weights = weights;
+  p.stride = weights_tokens;
+  p.seqs = seqs;
+  p.keep = keep;
+  p.kept = kept;
+  p.cut = static_cast<int32_t*>(workspace);
+  p.n = n;
+  p.sink = sink;
+  p.recent = recent;
+  p.keep_max = keep_max;
+  return launch_cache_evict(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
 size_t bsa_cache_forward_workspace_bytes(const bsa_plan* plan, const bsa_cache* cache) {
   bsa_plan_layout L;
   CacheDev c;

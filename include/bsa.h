@@ -33,7 +33,9 @@
  * Serving: a paged K/V cache held in 8 bits (bsa_cache): bsa_cache_append
  * (quantise and store tokens), bsa_cache_attention (single tokens and short
  * drafts), bsa_cache_forward (a plan's forward over it: chunked prefill) and
- * its pages (bsa_cache_resize, _fork, _compact, _copy_pages).
+ * its pages (bsa_cache_resize, _fork, _compact, _copy_pages), and its bounds:
+ * bsa_cache_weigh (the attention weight each token gathers), bsa_cache_evict.
+ * Prompts' rows ahead of both: bsa_rope_apply (rotary positions).
  *
  * Conventions
  *   - Every pointer argument named "device" is a CUDA device pointer owned by
@@ -671,6 +673,59 @@ bsa_status bsa_cache_attention(const bsa_cache* cache, const bsa_rows* q, const 
                                size_t workspace_bytes, void* stream);
 
 /*
+ * bsa_cache_weigh -- the attention weight that each cached token gathers over the
+ * query rows of its K/V head, from the attention's own LSE:
+ *   weights[seq][hkv][j] (+)= sum over heads h of the group and queries i of
+ *                             exp(scale <q[h][i], K_j> - LSE[h][i]),
+ * over the queries that see key j (length, causality, mask: as bsa_cache_attention
+ * was given).  A row whose LSE is -inf gives nothing.  What bsa_cache_evict goes by.
+ * weights: device fp32 [max_seqs][Hkv][weights_tokens], caller-owned; a sequence
+ *   longer than weights_tokens is skipped and recorded (BSA_ERR_INVALID_ARG).  Of
+ *   a sequence's row only its tokens' are written.
+ * fresh: the last `fresh` tokens of each sequence begin at 0, whatever lies there
+ *   (new tokens: nq after a step of decoding, any number from the length on for a
+ *   prompt's first call); the others are added to.
+ * seqs: as for bsa_cache_attention, but each sequence at most once (a later row
+ *   that names one with tokens again is skipped and recorded, BSA_ERR_INVALID_ARG).
+ * LSE: device fp32 [B][Hq][nq] contiguous.  Other arguments as
+ *   bsa_cache_attention.  Tokens whose table entry is no page gather nothing and are
+ *   recorded (BSA_ERR_PLAN_MISMATCH).
+ * Scores and sums are fp32; the result does not depend on timing.  One kernel.
+ */
+bsa_status bsa_cache_weigh(const bsa_cache* cache, const bsa_rows* q, const float* LSE, int dtype, const int32_t* seqs,
+                           const uint8_t* mask, int NKB, int bk, int B, int Hq, int nq, int flags, float scale,
+                           int fresh, float* weights, int weights_tokens, void* stream);
+
+/*
+ * bsa_cache_evict -- cut sequences to budgets: a sequence of more than k = keep[i]
+ * tokens keeps k of them, each K/V head its own: the last r = min(recent, k), the
+ * first s = min(sink, k - r), and of those between the k - r - s of largest
+ * weight (of equal ones the first; a NaN is below all numbers).  They become tokens 0 .. k - 1 in
+ * their order, their weights move with them, the length becomes k and the pages
+ * behind are given back.  (Keys keep the rotary positions they were stored with.)
+ * The scale of a block in which tokens come to lie is the largest of theirs, and
+ * codes of smaller scales are re-rounded to it; tokens of a block whose scale is not
+ * finite and positive have not been stored (code 0).  Blocks whose tokens all
+ * stay where they are, and rows and weights behind the last token, are left alone.
+ * weights: as bsa_cache_weigh's.  seqs: device int32 [n] or NULL (0 .. n-1), each at
+ *   most once (a later row that names it again is skipped and recorded).
+ * keep: device int32 [n].  sink, recent >= 0.
+ * kept: device int32 [n][Hkv][keep_max] (written): where the tokens were, for the
+ *   caller's own arrays: the first `length` entries of a row, up to keep_max of a sequence that is not cut.
+ *   Must not be `keep` or `seqs`.
+ * A sequence that is cut to more than keep_max, of a length or budget out of
+ * range, or one of whose pages [0, ceil(k / page_size)) other sequences hold too, is
+ * skipped and recorded (BSA_ERR_INVALID_ARG, detail = i), as is one with a
+ * token in no page (BSA_ERR_PLAN_MISMATCH, detail = the sequence).
+ * n <= 4096.  workspace: device, 4-byte aligned, bsa_cache_evict_workspace_bytes(n)
+ * bytes; calls that overlap in time need their own.  Three kernels.
+ */
+size_t bsa_cache_evict_workspace_bytes(int n);
+bsa_status bsa_cache_evict(const bsa_cache* cache, float* weights, int weights_tokens, const int32_t* seqs,
+                           const int32_t* keep, int sink, int recent, int32_t* kept, int keep_max, int n,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * bsa_cache_forward -- bsa_forward_ex over a cache: the plan's B sequences are
  * cache sequences seqs[b] (NULL: 0 .. B-1), key positions are their tokens,
  * keys at or past a sequence's length are dropped, and with BSA_FWD_CAUSAL
@@ -693,6 +748,63 @@ size_t bsa_cache_forward_workspace_bytes(const bsa_plan* plan, const bsa_cache* 
 bsa_status bsa_cache_forward(const bsa_plan* plan, const bsa_cache* cache, const int32_t* seqs,
                              const void* Q, int flags, void* O, float* LSE, float scale,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ------------------------------------------------------------ prompts' rows
+ * bsa_rope -- rotary positions of queries and keys, what an attention's rows
+ * pass before it (and before bsa_cache_append).  Pair i of a row at position t,
+ * elements (x_a, x_b), becomes
+ *     y_a = amplitude (x_a cos(t f_i) - x_b sin(t f_i)),
+ *     y_b = amplitude (x_b cos(t f_i) + x_a sin(t f_i)),
+ * for i < rot / 2; elements from rot on stay as they are.  Pairs are (i, i + rot/2)
+ * with BSA_ROPE_HALF, (2i, 2i + 1) with BSA_ROPE_NEIGHBOURS.
+ *   steps   device uint64 [rot / 2], 8-byte aligned: f_i / (2 pi) in 2^-64 turns,
+ *           so that an angle is exact to 2^-31 turns at every position
+ * rot: a multiple of 16, at most d.
+ */
+#define BSA_ROPE_HALF 0
+#define BSA_ROPE_NEIGHBOURS 1
+typedef struct bsa_rope {
+  const uint64_t* steps;
+  float amplitude;
+  int32_t rot;
+  int32_t pairs; /* BSA_ROPE_HALF or BSA_ROPE_NEIGHBOURS */
+} bsa_rope;
+
+/* How the frequencies f_i = base^(-2 i / rot) are scaled for contexts `factor` (>= 1)
+ * times as long as the trained one: */
+#define BSA_ROPE_NONE 0
+#define BSA_ROPE_LINEAR 1 /* f_i / factor */
+#define BSA_ROPE_BASE 2   /* base * factor^(rot / (rot - 2)) in the base's place */
+/* by parts: with r = original f_i / (2 pi) turns over the `original` context, pairs of
+ * r >= 32 stay, those of r <= 1 become f_i / factor, those between are mixed
+ * linearly in r; the amplitude is 0.1 ln(factor) + 1 (otherwise 1) */
+#define BSA_ROPE_PARTS 3
+/*
+ * bsa_rope_steps -- the steps and the amplitude of these frequencies, into HOST
+ * memory (rot / 2 words), for the caller to copy to the device.  rot a multiple of
+ * 16 from 16 to 128; base > 1; factor is read where there is a scaling, original
+ * (>= 1) by parts.  Touches no device.
+ */
+bsa_status bsa_rope_steps(int rot, double base, int scaling, double factor, double original, uint64_t* steps,
+                          float* amplitude);
+
+/* Turn by minus the angles: the transpose of the operator, which gives the
+ * gradients of its inputs from those of its outputs (and, with amplitude 1,
+ * undoes it). */
+#define BSA_ROPE_INVERSE 0x1
+/*
+ * bsa_rope_apply -- rotary positions of q [B][Hq][T][d] and k [B][Hk][T][d] in one
+ * call (bsa_rows of `dtype`; k and k_out are not read where Hk is 0).  Packed rows
+ * [T][H][d] are a batch of 1.  An output is the input's own rows (in place) or rows that share no
+ * memory with any input; no stride of 0 between several of its rows.
+ * positions: device int32 [B][T] (any value, also negative), or NULL: 0 .. T-1.
+ * flags: 0 or BSA_ROPE_INVERSE.  Angles, sines and products are fp32 or better, each
+ * element is rounded once.  One kernel.
+ */
+bsa_status bsa_rope_apply(const bsa_rope* rope, const bsa_rows* q, const bsa_rows* q_out, int Hq, const bsa_rows* k,
+                          const bsa_rows* k_out, int Hk, int dtype, const int32_t* positions, int B, int T, int d,
+                          int flags, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* bsa_status_string(int status);

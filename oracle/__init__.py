@@ -24,10 +24,12 @@ Modules:
 
 * ``oracle.cache`` -- the paged K/V cache in 8 bits as a model of its state:
   page bookkeeping, appending (block scales, rounding), attention over the
-  stored values.
+  stored values, gathered weights and eviction.
+
+* ``oracle.prompt`` -- rotary positions and the attention of packed prompts.
 
 Pins (what each part is checked against, other than itself) are listed in each
 module's docstring or its test file.  Parity status: attention -- pinned;
-plan -- pinned; cache -- pinned.
+plan -- pinned; cache -- pinned; prompt -- pinned.
 """
-from . import attention, cache, plan  # noqa: F401
+from . import attention, cache, plan, prompt  # noqa: F401

@@ -177,6 +177,77 @@ class CacheModel:
                         self.scales[w][page, h, r0 // self.sb] = sc
                 a = b
 
+    # ---- weights and eviction
+    def weigh(self, weights, q, lse, seqs=None, keep=None, fresh=0, scale=None):
+        """weights[s, h, j] (fp64 array, in place) gather exp(scale q.K_j - lse) over the
+        group's rows; q [B, Hq, nq, d], lse [B, Hq, nq], keep(b, h, i, j) -> bool."""
+        B, Hq, nq, d = q.shape
+        g = Hq // weights.shape[1]
+        sc = 1.0 / math.sqrt(d) if scale is None else scale
+        for b in range(B):
+            s = b if seqs is None else int(seqs[b])
+            if s < 0:
+                continue
+            n = int(self.lens[s])
+            k = self.values(s)[0]
+            weights[s, :, max(0, n - fresh):n] = 0
+            for h in range(Hq):
+                for i in range(nq):
+                    z = float(lse[b, h, i])
+                    if z == -math.inf:
+                        continue
+                    p = np.exp(sc * (k[h // g] @ q[b, h, i]) - z)
+                    see = np.ones(n, bool) if keep is None else np.array([keep(b, h, i, j) for j in range(n)], bool)
+                    weights[s, h // g, :n] += np.where(see, p, 0.0)
+
+    def evict(self, weights, budgets, seqs=None, sink=0, recent=0):
+        """Cuts sequences to budgets; `weights` [max_seqs, heads, tokens] in place.
+        Returns the kept positions, [rows][heads] lists."""
+        out = []
+        for i, k in enumerate(budgets):
+            s, k = i if seqs is None else int(seqs[i]), int(k)
+            heads = weights.shape[1]
+            if s < 0:
+                out.append(None)
+                continue
+            n = int(self.lens[s])
+            if n <= k:
+                out.append([list(range(n))] * heads)
+                continue
+            r = min(recent, k)
+            a = min(sink, k - r)
+            rows = []
+            for h in range(heads):
+                w = weights[s, h]
+                between = sorted(range(a, n - r), key=lambda j: (math.isnan(w[j]), -w[j] if w[j] == w[j] else 0.0, j))
+                stay = list(range(a)) + sorted(between[:k - r - a]) + list(range(n - r, n))
+                rows.append(stay)
+                weights[s, h, :k] = w[stay].copy()
+                at = lambda j: (int(self.table[s, j // self.page]), h, j % self.page)
+                for codes, scales in zip(self.codes, self.scales):
+                    of = lambda j: float(scales[at(j)[0], h, at(j)[2] // self.sb])
+                    got = [(codes[at(j)].copy(), of(j)) for j in stay]
+                    for b0 in range(0, k, self.sb):
+                        b1 = min(k, b0 + self.sb)
+                        if stay[b0:b1] == list(range(b0, b1)):
+                            continue
+                        good = [sc for _, sc in got[b0:b1] if 0 < sc < math.inf]
+                        top = max(good, default=0.0)
+                        for j in range(b0, b1):
+                            c, sc = got[j]
+                            if not 0 < sc < math.inf:
+                                c = np.zeros_like(c)
+                            elif sc != top:
+                                c = encode(decode(c, self.kind) * (sc / top), self.kind)
+                            codes[at(j)] = c
+                        scales[at(b0)[0], h, at(b0)[2] // self.sb] = top
+            for j in range(self._pages(k), self._pages(n)):
+                self.refs[self.table[s, j]] -= 1
+                self.table[s, j] = -1
+            self.lens[s] = k
+            out.append(rows)
+        return out
+
     def values(self, seq):
         """fp64 (K, V), each [heads, length, d], of a sequence."""
         n = int(self.lens[seq])
