@@ -1,4 +1,4 @@
-"""ctypes binding of the operators on prompts' rows (bsa_rope_* in
+"""ctypes binding of the operators on prompts' rows (bsa_rope_*, bsa_prompt_* in
 include/bsa.h).  Argument marshalling only: every step runs in the library's
 CUDA kernels."""
 from __future__ import annotations
@@ -15,6 +15,7 @@ _ELEMENTS = {torch.bfloat16: 0, torch.float16: 1}
 _PAIRS = {"half": 0, "neighbours": 1}
 _SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 ROPE_INVERSE = 0x1
+PROMPT_CAUSAL = 0x1
 
 
 class RopeC(ctypes.Structure):
@@ -31,10 +32,14 @@ def _library() -> ctypes.CDLL:
     if _bound is not None:
         return _bound
     lib = library()
-    I, D, VP = ctypes.c_int, ctypes.c_double, ctypes.c_void_p
+    I, D, F, VP, N = ctypes.c_int, ctypes.c_double, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
     R = ctypes.POINTER(RowsC)
+    lib.bsa_prompt_workspace_bytes.restype = N
+    lib.bsa_prompt_workspace_bytes.argtypes = [I, I, I, I]
     for name, args in {
             "bsa_rope_steps": [I, D, I, D, D, VP, ctypes.POINTER(ctypes.c_float)],
+            "bsa_prompt_attention": [R, R, R, R, VP, I, VP, I, I, I, I, I, I, F, VP, N, VP],
+            "bsa_prompt_status": [VP, VP, ctypes.POINTER(ctypes.c_int32)],
             "bsa_rope_apply": [ctypes.POINTER(RopeC), R, R, I, R, R, I, I, VP, I, I, I, I, VP]}.items():
         f = getattr(lib, name)
         f.restype = I
@@ -152,3 +157,65 @@ def rope(r: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None, positions: 
           pptr, B, T, q.shape[-1], ROPE_INVERSE if inverse else 0,
           _raw_stream(r._index) if stream is None else stream.cuda_stream)
     return out_q, out_k
+
+
+def prompt_workspace_bytes(n: int, T: int, Hq: int, Hkv: int) -> int:
+    """Workspace bytes of a call on n prompts of T tokens together (bsa_prompt_workspace_bytes; 0 for bad
+    arguments)."""
+    return int(_library().bsa_prompt_workspace_bytes(n, T, Hq, Hkv))
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, causal: bool = True,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of whole prompts packed behind one another (bsa_prompt_attention): q [T, Hq, d], k, v
+    [T, Hkv, d], bfloat16 or float16 with any strides between rows; ``offsets`` int32 [n + 1]: prompt i has rows
+    offsets[i] .. offsets[i + 1] - 1.  ``workspace`` (uint8, prompt_workspace_bytes) is taken from the allocator when
+    None; one that is given can be asked what the kernels recorded (``prompt_status``).  Returns (O [T, Hq, d],
+    LSE [T, Hq]); rows of no prompt are not written."""
+    index = q.get_device()
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dtype not in _ELEMENTS or not t.is_cuda or t.get_device() != index or t.dim() != 3 or t.stride(2) != 1:
+            raise ValueError(f"{name} must be a CUDA bfloat16 or float16 tensor [T, H, d] with contiguous rows")
+    T, Hq, d = q.shape
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != d or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("k and v must be [T, Hkv, d] of q's T, d and type")
+    if (offsets.dtype != torch.int32 or offsets.get_device() != index or offsets.dim() != 1 or offsets.shape[0] < 2
+            or not offsets.is_contiguous()):
+        raise ValueError("offsets must be a contiguous CUDA int32 tensor [n + 1]")
+    n, Hkv = offsets.shape[0] - 1, k.shape[1]
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index or out.stride(2) != 1):
+        raise ValueError("out must have q's shape, type and device, and contiguous rows")
+    if lse is not None and (lse.dtype != torch.float32 or lse.get_device() != index or tuple(lse.shape) != (T, Hq)
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous CUDA float32 tensor [T, Hq]")
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
+    lib = _library()
+    if out is None:
+        out = _new(q, stream)
+    if lse is None or workspace is None:
+        need = int(lib.bsa_prompt_workspace_bytes(n, T, Hq, Hkv)) if workspace is None else 0
+        with torch.cuda.stream(stream):  # (None: the current one)
+            if lse is None:
+                lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+            if workspace is None:
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    if q.numel() == 0:
+        return out, lse
+    _call(index, "bsa_prompt_attention", _rows(q), _rows(k), _rows(v), _rows(out), lse.data_ptr(), _ELEMENTS[q.dtype],
+          offsets.data_ptr(), n, T, Hq, Hkv, d, PROMPT_CAUSAL if causal else 0, 0.0 if scale is None else scale,
+          workspace.data_ptr(), workspace.numel(), _raw_stream(index) if stream is None else stream.cuda_stream)
+    return out, lse
+
+
+def prompt_status(workspace: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> Tuple[int, int]:
+    """(status, detail) that the kernels of the last ``prompt_attention`` with this workspace recorded;
+    synchronises (bsa_prompt_status)."""
+    det = ctypes.c_int32(0)
+    index = workspace.get_device()
+    with torch.cuda.device(index):
+        st = _library().bsa_prompt_status(workspace.data_ptr(), _raw_stream(index) if stream is None else stream.cuda_stream,
+                                          ctypes.byref(det))
+    return st, det.value

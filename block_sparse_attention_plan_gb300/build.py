@@ -20,7 +20,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsa.so")
 SOURCES = ["bsa_api.cu", "bsa_plan.cu", "bsa_prep.cu", "bsa_forward.cu", "bsa_forward_q64.cu", "bsa_noalloc.cu",
            "bsa_pipeline.cu", "bsa_cache_api.cu", "bsa_cache_pages.cu", "bsa_cache_append.cu", "bsa_cache_attn.cu",
-           "bsa_cache_load.cu", "bsa_cache_weigh.cu", "bsa_cache_evict.cu", "bsa_prompt_api.cu", "bsa_rope.cu"]
+           "bsa_cache_load.cu", "bsa_cache_weigh.cu", "bsa_cache_evict.cu", "bsa_prompt_api.cu", "bsa_prompt_attn.cu",
+           "bsa_rope.cu"]
 HEADERS = ["bsa_internal.h", "bsa_device.cuh", "bsa_fwd_common.cuh", "bsa_regime_table.h", "bsa_cache.h", "bsa_launch.h",
            "bsa_cache_codes.cuh", "bsa_prompt.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -201,6 +201,19 @@ bool encode_lines_map(CUtensorMap* m, const void* base, uint64_t lines, int box_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_packed_map(CUtensorMap* m, const bsa_rows& rows, int T, int H, int d, int heads, int tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = 2ull * (uint64_t)d;  // (a dimension of one has no stride of its own)
+  cuuint64_t dims[4] = {64u, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)(d / 64)};
+  cuuint64_t strides[3] = {H > 1 ? 2ull * (uint64_t)rows.stride_h : row, T > 1 ? 2ull * (uint64_t)rows.stride_t : row, 128u};
+  cuuint32_t box[4] = {64u, (cuuint32_t)heads, (cuuint32_t)tokens, (cuuint32_t)(d / 64)};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, rows.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Forward parameters of one plan (layout L, device views pd, workspace ws)
 // for the given tensors: the TMA views of Q (128-row and q-unit boxes), K and
 // V (contiguous or paged pools), the plan and scratch pointers, the element

@@ -202,6 +202,10 @@ bsa_status check_device(int* dev_out);
 long long watchdog_limit_ns();
 // Tensor map of `lines` lines of 128 bytes, box {128, box_lines}, 128-byte swizzle.
 bool encode_lines_map(CUtensorMap* m, const void* base, uint64_t lines, int box_lines);
+// Tensor map of packed rows [T][H][d] as [halves][T][H][64], box {64, heads, tokens,
+// halves}, 128-byte swizzle: in shared memory the rows' first 64 columns, a token's
+// heads together, then their others.
+bool encode_packed_map(CUtensorMap* m, const bsa_rows& rows, int T, int H, int d, int heads, int tokens);
 cudaError_t launch_watchdog_selftest(int32_t* status, long long limit_ns, cudaStream_t stream);
 
 }  // namespace bsa

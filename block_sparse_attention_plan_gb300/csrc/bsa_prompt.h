@@ -30,6 +30,29 @@ struct RopeParams {
   int tail;                  // the elements past rot are copied (not in place)
 };
 
+// Attention of packed prompts (bsa_prompt_attn.cu).
+constexpr int kPromptRows = 256;   // query rows of a work item: two tiles of 128
+constexpr int kPromptCtlTiles = 3; // control word: work items of a group of heads (0-2: as a plan's)
+struct PromptParams {
+  CUtensorMap tmQ;         // q as [halves][T][Hq][64], box {64, gp, 128 / gp, halves}: 128 rows, a token's heads together
+  CUtensorMap tmK, tmV;    // k, v as [halves][T][Hkv][64], box {64, 1, 128, halves}
+  const uint16_t* v;       // (values that are no numbers are looked up again)
+  long long v_st, v_sh;
+  uint16_t* o;
+  long long o_st, o_sh;
+  float* lse;              // [T][Hq] or nullptr
+  const int32_t* offsets;  // [n + 1]
+  int32_t* control;        // [16]
+  int32_t* tile_ptr;       // [n + 1]: work items ahead of each prompt
+  int4* tiles;             // {first row, length, first token, 0}, longest first
+  int n, T, Hq, Hkv, g;
+  int gp_shift;            // log2 of the heads of a tile
+  int causal, fp16, o_v8;
+  float scale_log2;
+  long long watchdog_ns;
+};
+cudaError_t launch_prompt(const PromptParams& p, int d, int sms, cudaStream_t s);
+
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t s);
 int rope_heads_per_round(int d);
 

@@ -32,9 +32,101 @@ bool in_place(const RopeRows& r, int B, int H, int T) {
   return r.p == r.o && (B == 1 || r.sb == r.ob) && (H == 1 || r.sh == r.oh) && (T == 1 || r.st == r.ot);
 }
 
+// Packed rows [T][H][d]: rows of their own.
+bool good_packed(const bsa_rows* r, int T, int H) {
+  return good_rows(r) && (T == 1 || (r->stride_t && r->stride_t < (1ll << 38))) &&
+         (H == 1 || (r->stride_h && r->stride_h < (1ll << 38)));
+}
+
+struct PromptLayout {
+  size_t off_ptr, off_tiles, bytes;
+  int gp_shift;
+};
+bsa_status prompt_layout(int n, int T, int Hq, int Hkv, PromptLayout* out) {
+  if (n < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv) return BSA_ERR_INVALID_ARG;
+  PromptLayout l;
+  const int g = Hq / Hkv;
+  l.gp_shift = 0;
+  while (l.gp_shift < 4 && !(g >> l.gp_shift & 1)) ++l.gp_shift;
+  const long long tiles = (long long)T / (kPromptRows >> l.gp_shift) + n;
+  if (T > (1 << 30) || Hq > 65536 || tiles * (Hq >> l.gp_shift) >= (1ll << 31)) return BSA_ERR_UNSUPPORTED;
+  size_t off = align256(64);
+  l.off_ptr = off;   off = align256(off + 4ull * ((uint64_t)n + 1));
+  l.off_tiles = off; off = align256(off + 16ull * (uint64_t)tiles);
+  l.bytes = off;
+  *out = l;
+  return BSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t bsa_prompt_workspace_bytes(int n, int T, int Hq, int Hkv) {
+  PromptLayout l;
+  return prompt_layout(n, T, Hq, Hkv, &l) == BSA_OK ? l.bytes : 0;
+}
+
+bsa_status bsa_prompt_attention(const bsa_rows* q, const bsa_rows* k, const bsa_rows* v, const bsa_rows* o, float* LSE,
+                                int dtype, const int32_t* offsets, int n, int T, int Hq, int Hkv, int d, int flags,
+                                float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  PromptParams p;
+  std::memset(&p, 0, sizeof(p));
+  PromptLayout l;
+  bsa_status st = prompt_layout(n, T, Hq, Hkv, &l);
+  if (st != BSA_OK) return st;
+  if (!good_packed(q, T, Hq) || !good_packed(k, T, Hkv) || !good_packed(v, T, Hkv) || !good_packed(o, T, Hq) ||
+      !offsets || !aligned(offsets, 4) || !aligned(LSE, 4) || !workspace || !aligned(workspace, 16))
+    return BSA_ERR_INVALID_ARG;
+  if (flags & ~BSA_PROMPT_CAUSAL) return BSA_ERR_INVALID_ARG;
+  if (!(scale == scale) || std::isinf(scale)) return BSA_ERR_INVALID_ARG;
+  if (dtype != BSA_BF16 && dtype != BSA_FP16) return BSA_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
+  if (workspace_bytes < l.bytes) return BSA_ERR_WORKSPACE;
+  int dev = 0, sms = 0;
+  if ((st = check_device(&dev)) != BSA_OK) return st;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return BSA_ERR_CUDA;
+  if (!encode_packed_map(&p.tmQ, *q, T, Hq, d, 1 << l.gp_shift, 128 >> l.gp_shift) ||
+      !encode_packed_map(&p.tmK, *k, T, Hkv, d, 1, 128) || !encode_packed_map(&p.tmV, *v, T, Hkv, d, 1, 128))
+    return BSA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.v = static_cast<const uint16_t*>(v->data);
+  p.v_st = v->stride_t;
+  p.v_sh = v->stride_h;
+  p.o = static_cast<uint16_t*>(o->data);
+  p.o_st = o->stride_t;
+  p.o_sh = o->stride_h;
+  p.o_v8 = aligned(o->data, 32) && o->stride_t % 16 == 0 && o->stride_h % 16 == 0;
+  p.lse = LSE;
+  p.offsets = offsets;
+  p.control = reinterpret_cast<int32_t*>(ws);
+  p.tile_ptr = reinterpret_cast<int32_t*>(ws + l.off_ptr);
+  p.tiles = reinterpret_cast<int4*>(ws + l.off_tiles);
+  p.n = n;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.g = Hq / Hkv;
+  p.gp_shift = l.gp_shift;
+  p.causal = flags & BSA_PROMPT_CAUSAL ? 1 : 0;
+  p.fp16 = dtype == BSA_FP16;
+  const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)d);
+  p.scale_log2 = (float)(sc * 1.4426950408889634);
+  p.watchdog_ns = watchdog_limit_ns();
+  return launch_prompt(p, d, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+bsa_status bsa_prompt_status(const void* workspace, void* stream, int32_t* detail) {
+  if (!workspace || !aligned(workspace, 16)) return BSA_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t word[2] = {0, 0};
+  if (cudaMemcpyAsync(word, static_cast<const int32_t*>(workspace) + kCtlStatus, sizeof(word), cudaMemcpyDeviceToHost, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return BSA_ERR_CUDA;
+  if (detail) *detail = word[1];
+  return static_cast<bsa_status>(word[0]);
+}
 
 bsa_status bsa_rope_steps(int rot, double base, int scaling, double factor, double original, uint64_t* steps,
                           float* amplitude) {

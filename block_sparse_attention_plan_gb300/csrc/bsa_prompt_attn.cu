@@ -1,0 +1,700 @@
+// Attention of packed prompts: softmax(scale Q K^T) V within each prompt, causal
+// or not, heads grouped over K/V heads.
+//
+// Work items are 256 query rows of one prompt: two 128-row tiles, whose rows are
+// 256 / gp tokens of gp heads that share a K/V head (gp: the largest power of two
+// in the group, at most 16).  A schedule kernel lists the items of all prompts,
+// those with the most key blocks first; the attention kernel's CTAs (one per SM) take
+// them, for one group of heads after the other, from a counter.
+//
+// One CTA (384 threads):
+//   warp 0    takes work items, publishes them, loads both Q tiles and the K and
+//             V blocks (128 keys) into one ring, in the order they are used;
+//   warp 1    (one thread) issues S = Q K^T and O += P V of the two tiles in turn,
+//               PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) ...,
+//             so that one tile's products run while the other tile's softmax does;
+//   warps 2, 3  look over the values of every block that some row of the item does not
+//             attend as a whole (below);
+//   warps 4-7, 8-11  the softmax of tile A and of tile B, a thread per row, with a
+//             running maximum that is moved only when a score passes it by more
+//             than kMove (then O is rescaled), and the epilogue.
+//
+// Tensor memory (512 columns): S_A, S_B (128 each), O_A, O_B (d each).  P takes the
+// first 64 columns of its tile's S: a warp has read its rows' scores before it writes
+// their weights, and S_x(j+1) is issued behind PV_x(j), which reads them: the
+// instructions of one thread run in their order.  For the same reason the arrival of
+// S_x(j+1) tells the softmax that PV_x(j) is done with O.
+//
+// Keys that a row does not attend get weight 0, which keeps a score of any kind out,
+// but 0 times a value that is infinite or NaN is NaN: a later token's, or (past the
+// prompt's end) another prompt's.  So in blocks that some row attends in part such
+// values are replaced by 0 in shared memory before the product, and an item that had
+// any adds them to the rows that do attend them at its end, from global memory.
+//
+// What bounds it: the tensor cores, 2 * 2 * 128 * 128 d flops a block and tile, and
+// the exponentials, 128 * 128.
+#include <cstdint>
+
+#include "bsa_device.cuh"
+#include "bsa_internal.h"
+#include "bsa_prompt.h"
+
+namespace bsa {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 384;
+// 128 x kRegsControl + 256 x kRegsSoftmax within the 384 x 168 of the launch.
+constexpr int kRegsControl = 72;
+constexpr int kRegsSoftmax = 208;
+static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split");
+constexpr int kSlots = 4;                   // work items published ahead
+constexpr int kConsumers = 1 + 2 + 8;       // MMA thread, two scanning warps, eight softmax warps
+constexpr float kMove = 8.f;                // log2: weights stay <= 2^(8 + kShift)
+
+enum PromptSite : int { kSitePromptOffsets = 0x60 };
+
+template <int D_>
+struct Cfg {
+  static constexpr int D = D_;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kChunkBytes = 128 * 128;    // 128 rows of 64 elements
+  static constexpr int kQBufs = D == 128 ? 1 : 2;  // of two tiles
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffKV = kQBufs * 2 * kTileBytes;
+  static constexpr int kOffBar = kOffKV + kStages * kTileBytes;
+  static constexpr int kQFull = 0, kQEmpty = 2;
+  static constexpr int kFull = 4;
+  static constexpr int kEmpty = kFull + kStages;
+  static constexpr int kClean = kEmpty + kStages;
+  static constexpr int kSFull = kClean + kStages;  // [2]
+  static constexpr int kPFull = kSFull + 2;        // [2]
+  static constexpr int kOFull = kPFull + 2;        // [2]
+  static constexpr int kOFree = kOFull + 2;        // [2]
+  static constexpr int kDrain = kOFree + 2;
+  static constexpr int kSchedFull = kDrain + 1;
+  static constexpr int kSchedEmpty = kSchedFull + kSlots;
+  static constexpr int kNumBars = kSchedEmpty + kSlots;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag
+  static constexpr int kOffSched = kOffMisc + 16;           // int [kSlots][8]
+  static constexpr int kOffDirty = kOffSched + 32 * kSlots; // int [2 kSlots][2]
+  static constexpr int kSmem = kOffDirty + 16 * kSlots;
+  // How often ring entry r's stage has held values before (entries alternate keys and
+  // values, so with an odd number of stages a stage does).
+  __device__ static __forceinline__ uint32_t uses(uint32_t r) {
+    return r / (uint32_t)(kStages % 2 ? 2 * kStages : kStages);
+  }
+  static_assert(kSmem <= 232448, "shared memory");
+  static constexpr uint32_t kColS = 0, kColO = 256;  // tile x at + 128 x
+};
+
+template <class C>
+struct Smem {
+  uint32_t base;
+  __device__ __forceinline__ uint32_t bar(int i) const { return base + C::kOffBar + 8u * (uint32_t)i; }
+  __device__ __forceinline__ uint32_t q(int buf, int x) const { return base + (uint32_t)((buf * 2 + x) * C::kTileBytes); }
+  __device__ __forceinline__ uint32_t kv(uint32_t s) const { return base + C::kOffKV + s * (uint32_t)C::kTileBytes; }
+};
+
+struct Item {
+  int it;        // < 0: no more
+  int row0;      // first row of the prompt
+  int len;       // its tokens
+  int t0;        // first token of the item
+  int unit;      // group of gp heads
+};
+// Key blocks of tile x of an item (0: the tile has no token).
+__device__ __forceinline__ int blocks_of(const PromptParams& p, const Item& m, int x) {
+  const int half = 128 >> p.gp_shift, first = m.t0 + x * half;
+  if (first >= m.len) return 0;
+  const int end = p.causal ? min(m.len, first + half) : m.len;
+  return (end + 127) >> 7;
+}
+// The first key block that some row of the item does not attend as a whole.
+__device__ __forceinline__ int masked_from(const PromptParams& p, const Item& m) {
+  return p.causal ? min((m.t0 + 1) >> 7, m.len >> 7) : m.len >> 7;
+}
+
+template <class C>
+__device__ __forceinline__ Item take(const Smem<C>& sm, const uint8_t* smem, uint32_t t, bool arrives, bool warp_sync,
+                                     const Watchdog& wd) {
+  Item m{-2, 0, 0, 0, 0};
+  const int slot = (int)(t % kSlots);
+  bool ok = mbar_wait(sm.bar(C::kSchedFull + slot), (t / kSlots) & 1u, wd, kSiteSched);
+  if (warp_sync) ok = __all_sync(0xffffffffu, ok);
+  if (!ok) return m;
+  const volatile int* e = reinterpret_cast<const volatile int*>(smem + C::kOffSched) + slot * 8;
+  m.it = e[0];
+  m.row0 = e[1];
+  m.len = e[2];
+  m.t0 = e[3];
+  m.unit = e[4];
+  if (warp_sync) __syncwarp();
+  if (arrives) mbar_arrive(sm.bar(C::kSchedEmpty + slot));
+  return m;
+}
+
+// Bounded wait of the teardown: goes by no abort flag.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const Watchdog& wd) {
+  volatile int no_abort = 0;
+  Watchdog quick{&no_abort, wd.status, wd.detail, 100000000ll};
+  mbar_wait(bar, parity, quick, kSiteDrain);
+}
+
+// ------------------------------------------------------------------ producer
+template <int D>
+__device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, const Smem<Cfg<D>> sm, const Watchdog wd) {
+  using C = Cfg<D>;
+  tma_prefetch_desc(&p.tmQ);
+  tma_prefetch_desc(&p.tmK);
+  tma_prefetch_desc(&p.tmV);
+  const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
+  const int units = p.Hq >> p.gp_shift, half = 128 >> p.gp_shift;
+  const int tiles = *reinterpret_cast<const volatile int32_t*>(p.control + kPromptCtlTiles);
+  const int work = tiles * units;
+  uint32_t q_it = 0, kv_it = 0;
+  bool ok = true;
+  for (uint32_t t = 0; ok; ++t) {
+    const int slot = (int)(t % kSlots);
+    if (!mbar_wait(sm.bar(C::kSchedEmpty + slot), ((t / kSlots) & 1u) ^ 1u, wd, kSiteSched)) break;
+    Item m{-1, 0, 0, 0, 0};
+    const int it = atomicAdd(p.control + kCtlWorkCounter, 1);
+    if (it < work) {
+      const int4 e = load_written(p.tiles + it / units);
+      m = Item{it, e.x, e.y, e.z, it % units};
+    }
+    volatile int* e = reinterpret_cast<volatile int*>(smem + C::kOffSched) + slot * 8;
+    e[0] = m.it;
+    e[1] = m.row0;
+    e[2] = m.len;
+    e[3] = m.t0;
+    e[4] = m.unit;
+    mbar_arrive(sm.bar(C::kSchedFull + slot));
+    if (m.it < 0) break;
+    const int nb = max(blocks_of(p, m, 0), blocks_of(p, m, 1));
+    const bool two = blocks_of(p, m, 1) > 0;
+    const int h0 = m.unit << p.gp_shift, kvh = h0 / p.g;
+    const int qb = (int)(q_it % C::kQBufs);
+    if (!mbar_wait(sm.bar(C::kQEmpty + qb), ((q_it / C::kQBufs) & 1u) ^ 1u, wd, kSiteQEmpty)) break;
+    const uint32_t qf = sm.bar(C::kQFull + qb);
+    mbar_arrive_expect_tx(qf, two ? 2 * C::kTileBytes : C::kTileBytes);
+    tma_load_4d(sm.q(qb, 0), &p.tmQ, 0, h0, m.row0 + m.t0, 0, qf, pol_q);
+    if (two) tma_load_4d(sm.q(qb, 1), &p.tmQ, 0, h0, m.row0 + m.t0 + half, 0, qf, pol_q);
+    ++q_it;
+    for (int j = 0; j < 2 * nb; ++j) {
+      const uint32_t s = kv_it % C::kStages;
+      if (!mbar_wait(sm.bar(C::kEmpty + (int)s), ((kv_it / C::kStages) & 1u) ^ 1u, wd, kSiteKvEmpty)) {
+        ok = false;
+        break;
+      }
+      const uint32_t full = sm.bar(C::kFull + (int)s);
+      mbar_arrive_expect_tx(full, C::kTileBytes);
+      tma_load_4d(sm.kv(s), j & 1 ? &p.tmV : &p.tmK, 0, kvh, m.row0 + (j >> 1) * 128, 0, full, pol_kv);
+      ++kv_it;
+    }
+  }
+  if (*wd.abort_flag) {  // copies already issued land before the shared memory goes away
+    const uint32_t nk = kv_it < (uint32_t)C::kStages ? kv_it : (uint32_t)C::kStages;
+    for (uint32_t t = kv_it - nk; t < kv_it; ++t)
+      drain_wait(sm.bar(C::kFull + (int)(t % C::kStages)), (t / C::kStages) & 1u, wd);
+    const uint32_t nq = q_it < (uint32_t)C::kQBufs ? q_it : (uint32_t)C::kQBufs;
+    for (uint32_t t = q_it - nq; t < q_it; ++t)
+      drain_wait(sm.bar(C::kQFull + (int)(t % C::kQBufs)), (t / C::kQBufs) & 1u, wd);
+  }
+}
+
+// ------------------------------------------------------------------ matrix products
+template <int D, bool FP16>
+__device__ __noinline__ void issuer(const PromptParams& p, const uint8_t* smem, const Smem<Cfg<D>> sm, uint32_t tmem,
+                                    const Watchdog wd) {
+  using C = Cfg<D>;
+  constexpr uint32_t kIdescS = FP16 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false);
+  constexpr uint32_t kIdescO = FP16 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, true);
+  const uint64_t qd0 = smem_desc_sw128(sm.q(0, 0), 16, 1024);
+  const uint64_t kd0 = smem_desc_sw128(sm.kv(0), 16, 1024);
+  const uint64_t vd0 = smem_desc_sw128(sm.kv(0), C::kChunkBytes, 1024);
+  constexpr uint64_t kStep = (uint64_t)(C::kTileBytes >> 4);
+  uint32_t q_it = 0, ring = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
+  bool ok = true;
+  auto stage = [](uint32_t r) { return r % (uint32_t)C::kStages; };
+  auto full = [&](uint32_t r) {
+    return mbar_wait(sm.bar(C::kFull + (int)stage(r)), (r / C::kStages) & 1u, wd, kSiteKvFull);
+  };
+  auto issue_s = [&](int x, int qb, uint32_t r) {
+    const uint64_t qd = qd0 + (uint64_t)(qb * 2 + x) * kStep, kd = kd0 + (uint64_t)stage(r) * kStep;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint64_t off = (uint64_t)(((kk / 4) * C::kChunkBytes + (kk % 4) * 32) >> 4);
+      mma_ss(tmem + C::kColS + 128u * (uint32_t)x, qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
+    }
+    mma_commit(sm.bar(C::kSFull + x));
+  };
+  for (uint32_t t = 0; ok; ++t) {
+    const Item m = take<C>(sm, smem, t, true, false, wd);
+    if (m.it < 0) break;
+    const int nx[2] = {blocks_of(p, m, 0), blocks_of(p, m, 1)};
+    const int nb = max(nx[0], nx[1]);
+    const int qb = (int)(q_it % C::kQBufs);
+    ok = mbar_wait(sm.bar(C::kQFull + qb), (q_it / C::kQBufs) & 1u, wd, kSiteQFull) && full(ring);
+    if (!ok) break;
+    tc_fence_after();
+    issue_s(0, qb, ring);
+    if (nx[1] > 0) issue_s(1, qb, ring);
+    mma_commit(sm.bar(C::kEmpty + (int)stage(ring)));
+    if (nb == 1) mma_commit(sm.bar(C::kQEmpty + qb));
+    for (int j = 0; j < nb && ok; ++j) {
+      const uint32_t rv = ring + 2 * (uint32_t)j + 1;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (j >= nx[x] || !ok) continue;
+        ok = full(rv) && mbar_wait(sm.bar(C::kClean + (int)stage(rv)), C::uses(rv) & 1u, wd, kSiteKvFull) &&
+             mbar_wait(sm.bar(C::kPFull + x), pc[x] & 1u, wd, kSitePFull);
+        if (ok && j == 0 && oc[x] > 0) ok = mbar_wait(sm.bar(C::kOFree + x), (oc[x] - 1) & 1u, wd, kSiteODone);
+        if (!ok) continue;
+        ++pc[x];
+        tc_fence_after();
+        const uint64_t vd = vd0 + (uint64_t)stage(rv) * kStep;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + C::kColO + 128u * (uint32_t)x, tmem + C::kColS + 128u * (uint32_t)x + 8u * (uint32_t)kk,
+                 vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+        if (j + 1 < nx[x]) {
+          if (!(ok = full(rv + 1))) continue;
+          tc_fence_after();
+          issue_s(x, qb, rv + 1);
+        } else {
+          mma_commit(sm.bar(C::kOFull + x));
+          ++oc[x];
+        }
+      }
+      if (!ok) break;
+      mma_commit(sm.bar(C::kEmpty + (int)stage(rv)));
+      if (j + 1 < nb) mma_commit(sm.bar(C::kEmpty + (int)stage(rv + 1)));
+      if (j + 2 == nb) mma_commit(sm.bar(C::kQEmpty + qb));
+    }
+    ring += 2 * (uint32_t)nb;
+    ++q_it;
+  }
+  mma_commit(sm.bar(C::kDrain));
+  drain_wait(sm.bar(C::kDrain), 0, wd);
+}
+
+// ------------------------------------------------------------------ values
+// 0xffff in the halves of w that are infinite or NaN.
+template <bool FP16>
+__device__ __forceinline__ uint32_t no_numbers(uint32_t w) {
+  constexpr uint32_t kExp = FP16 ? 0x7c007c00u : 0x7f807f80u;
+  return __vcmpeq2(w & kExp, kExp);
+}
+
+template <int D, bool FP16>
+__device__ __forceinline__ void scanner(const PromptParams& p, uint8_t* smem, const Smem<Cfg<D>>& sm, const Watchdog& wd,
+                                        int who) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  volatile int* dirty = reinterpret_cast<volatile int*>(smem + C::kOffDirty);
+  uint32_t ring = 0;
+  for (uint32_t t = 0;; ++t) {
+    const Item m = take<C>(sm, smem, t, lane == 0, true, wd);
+    if (m.it < 0) return;
+    const int nb = max(blocks_of(p, m, 0), blocks_of(p, m, 1)), first = masked_from(p, m);
+    if (lane == 0) dirty[(t % (2 * kSlots)) * 2 + who] = 0;
+    for (int j = 0; j < nb; ++j) {
+      const uint32_t r = ring + 2 * (uint32_t)j + 1, s = r % C::kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(C::kFull + (int)s), (r / C::kStages) & 1u, wd, kSiteKvFull))) return;
+      if (j >= first) {
+        bool here = false;
+        const uint32_t at = sm.kv(s) + (uint32_t)(who * (C::kTileBytes / 2) + lane * 16);
+#pragma unroll 8
+        for (int q = 0; q < C::kTileBytes / 2; q += 512) {
+          const uint4 w = ld_shared_v4(at + q);
+          const uint32_t a = no_numbers<FP16>(w.x), b = no_numbers<FP16>(w.y), c = no_numbers<FP16>(w.z),
+                         d = no_numbers<FP16>(w.w);
+          if (a | b | c | d) {
+            st_shared_v4(at + q, w.x & ~a, w.y & ~b, w.z & ~c, w.w & ~d);
+            here = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, here)) {
+          fence_proxy_async_smem();  // the product reads what was written
+          if (lane == 0) dirty[(t % (2 * kSlots)) * 2 + who] = 1;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.bar(C::kClean + (int)s));
+    }
+    ring += 2 * (uint32_t)nb;
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+// Values that were replaced by 0, to the rows of the item that attend them: an
+// infinity or NaN among a row's values is one in its output, whatever its weight.  A
+// warp mends its own 32 rows (of tokens tok0 .. ), a lane D / 32 columns.
+template <int D, bool FP16>
+__device__ __noinline__ void add_no_numbers(const PromptParams& p, const Item m, int tok0, int row0) {
+  constexpr int kCols = D / 32;
+  constexpr uint32_t kExp = FP16 ? 0x7c00u : 0x7f80u;
+  const int c0 = (int)(threadIdx.x & 31) * kCols;
+  const int h0 = m.unit << p.gp_shift, gp = 1 << p.gp_shift, rows = gp < 32 ? gp : 32;
+  const int end = min(m.len, tok0 + (32 >> p.gp_shift)), from = masked_from(p, m) << 7;
+  const uint16_t* v = p.v + (long long)(h0 / p.g) * p.v_sh + c0;
+  uint32_t seen[kCols];  // +inf 1, -inf 2, NaN 4
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) seen[c] = 0u;
+  auto what = [](uint32_t w) -> uint32_t {
+    return (w & kExp) != kExp ? 0u : ((w & 0x7fffu) == kExp ? 1u << (w >> 15) : 4u);
+  };
+  auto look = [&](int t) {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) seen[c] |= what(load_written(v + (long long)(m.row0 + t) * p.v_st + c));
+  };
+  auto add = [&](int t) {
+    for (int h = 0; h < rows; ++h) {
+      uint16_t* o = p.o + (long long)(m.row0 + t) * p.o_st + (long long)(h0 + (row0 & (gp - 1)) + h) * p.o_sh + c0;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        if (!seen[c]) continue;
+        const uint32_t s = seen[c] | what(o[c]);
+        o[c] = (uint16_t)(s == 1u ? kExp : (s == 2u ? kExp | 0x8000u : 0x7fffu));
+      }
+    }
+  };
+  __syncwarp();  // the rows are written
+  if (p.causal) {
+    for (int t = from; t < end; ++t) {
+      look(t);
+      if (t >= tok0) add(t);
+    }
+  } else {
+    for (int t = from; t < m.len; ++t) look(t);
+    for (int t = tok0; t < end; ++t) add(t);
+  }
+  __syncwarp();
+}
+
+template <int D, bool FP16>
+__device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, const Smem<Cfg<D>>& sm, uint32_t tmem,
+                                        const Watchdog& wd) {
+  using C = Cfg<D>;
+  // fp16 weights are kept at 2^7 of their size: the largest, 2^15, is under 2^16, and
+  // what falls below fp16's range is 2^-31 of the reference.
+  constexpr float kShift = FP16 ? 7.f : 0.f;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int x = (warp - 4) >> 2, quad = warp & 3;
+  const int row = quad * 32 + lane;
+  const uint32_t tl = (uint32_t)(quad * 32) << 16;
+  const uint32_t scol = tmem + tl + C::kColS + 128u * (uint32_t)x, ocol = tmem + tl + C::kColO + 128u * (uint32_t)x;
+  const int half = 128 >> p.gp_shift, gp = 1 << p.gp_shift;
+  const volatile int* dirty = reinterpret_cast<const volatile int*>(smem + C::kOffDirty);
+  const float sl2 = p.scale_log2;
+  const uint64_t sl2x2 = f2_make(sl2, sl2);
+  uint32_t sc = 0, oc = 0;
+  for (uint32_t t = 0;; ++t) {
+    const Item m = take<C>(sm, smem, t, lane == 0, true, wd);
+    if (m.it < 0) return;
+    const int n = blocks_of(p, m, x);
+    if (n == 0) continue;
+    const int first = m.t0 + x * half, tok = first + (row >> p.gp_shift);
+    // Last key of this row, and the key below which all rows of the tile attend.
+    const int lim = p.causal ? min(tok, m.len - 1) : m.len - 1;
+    const int whole = p.causal ? min(first + 1, m.len) : m.len;
+    float m_ref = -INFINITY, l = 0.f;
+    for (int j = 0; j < n; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(C::kSFull + x), sc & 1u, wd, kSiteSFull))) return;
+      ++sc;
+      tc_fence_after();
+      uint32_t v[128];
+      tmem_ld32_at<0>(scol, v);
+      tmem_ld32_at<32>(scol + 32u, v);
+      tmem_ld32_at<64>(scol + 64u, v);
+      tmem_ld32_at<96>(scol + 96u, v);
+      tmem_wait_ld();
+      if ((j + 1) * 128 > whole) {
+        const int rel = lim - j * 128;  // the last element that counts
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e > rel) v[e] = __float_as_uint(-INFINITY);
+      }
+      float mx4[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+#pragma unroll
+      for (int e = 8; e < 128; e += 8) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mx4[c] = fmax3(mx4[c], __uint_as_float(v[e + 2 * c]), __uint_as_float(v[e + 2 * c + 1]));
+      }
+      const float m_new = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+      float factor = 1.f;
+      if (j == 0) {
+        m_ref = m_new;
+      } else if (__any_sync(0xffffffffu, m_new > m_ref + kMove)) {
+        if (m_new > m_ref + kMove) {
+          factor = ex2_approx(m_ref - m_new);
+          m_ref = m_new;
+        }
+        // (this block's scores have arrived, so the products before them are done with O)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(ocol + 32u * (uint32_t)c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+          tmem_st32(ocol + 32u * (uint32_t)c, o);
+        }
+      }
+      const float mb = kShift - (m_ref == -INFINITY ? 0.f : m_ref);
+      const uint64_t mbx2 = f2_make(mb, mb);
+      uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+      uint32_t pk[64];
+#pragma unroll
+      for (int e = 0; e < 64; ++e) {
+        float x0, x1;
+        f2_split(ffma2(f2_make(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2x2, mbx2), x0, x1);
+        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+        pk[e] = FP16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+        acc2[e & 3] = fadd2(acc2[e & 3], f2_make(p0, p1));
+      }
+      tmem_st32_at<0>(scol, pk);
+      tmem_st32_at<32>(scol + 32u, pk);
+      float s0, s1;
+      f2_split(fadd2(fadd2(acc2[0], acc2[1]), fadd2(acc2[2], acc2[3])), s0, s1);
+      l = l * factor + (s0 + s1);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.bar(C::kPFull + x));
+    }
+    // ------------------------------------------------------------ epilogue
+    if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(C::kOFull + x), oc & 1u, wd, kSiteODone))) return;
+    ++oc;
+    tc_fence_after();
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
+    const int head = (m.unit << p.gp_shift) + (row & (gp - 1));
+    const bool real = tok < m.len;
+    uint16_t* out = p.o + (long long)(m.row0 + tok) * p.o_st + (long long)head * p.o_sh;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32], pk[16];
+      tmem_ld32(ocol + 32u * (uint32_t)c, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float a = __uint_as_float(o[2 * e]) * inv, b = __uint_as_float(o[2 * e + 1]) * inv;
+        pk[e] = FP16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+      }
+      if (real && p.o_v8) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w8[e] = pk[8 * q + e];
+          st_global_v8(out + 32 * c + 16 * q, w8);
+        }
+      } else if (real) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(out + 32 * c + 8 * q) = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm.bar(C::kOFree + x));
+    if (real && p.lse)
+      p.lse[(long long)(m.row0 + tok) * p.Hq + head] =
+          l == 0.f ? -INFINITY : (m_ref - kShift + __log2f(l)) * 0.69314718055994531f;
+    const int slot = (int)(t % (2 * kSlots)) * 2;
+    if (dirty[slot] | dirty[slot + 1]) add_no_numbers<D, FP16>(p, m, first + ((quad * 32) >> p.gp_shift), quad * 32);
+  }
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const Smem<C> sm{smem_u32(smem)};
+  volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  const Watchdog wd{abort_flag, p.control + kCtlStatus, p.control + kCtlDetail, p.watchdog_ns};
+  next_may_launch();
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sm.bar(C::kQFull + i), 1);
+      mbar_init(sm.bar(C::kQEmpty + i), 1);
+      mbar_init(sm.bar(C::kSFull + i), 1);
+      mbar_init(sm.bar(C::kPFull + i), 4);
+      mbar_init(sm.bar(C::kOFull + i), 1);
+      mbar_init(sm.bar(C::kOFree + i), 4);
+    }
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(sm.bar(C::kFull + i), 1);
+      mbar_init(sm.bar(C::kEmpty + i), 1);
+      mbar_init(sm.bar(C::kClean + i), 2);
+    }
+    mbar_init(sm.bar(C::kDrain), 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(sm.bar(C::kSchedFull + i), 1);
+      mbar_init(sm.bar(C::kSchedEmpty + i), kConsumers);
+    }
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 2) {
+    tmem_alloc(sm.base + C::kOffMisc, 512);
+    tmem_relinquish();
+  }
+  wait_for_previous();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  if (threadIdx.x == 0 && (sm.base & 1023u)) record_failure(wd, BSA_ERR_CUDA, 0);  // the swizzle's layout needs it
+  __syncthreads();
+  if (warp >= 4) {
+    regs_inc<kRegsSoftmax>();
+    if (!*abort_flag) softmax<D, FP16>(p, smem, sm, tmem, wd);
+  } else {
+    regs_dec<kRegsControl>();
+    if (!*abort_flag) {
+      if (warp >= 2) scanner<D, FP16>(p, smem, sm, wd, warp - 2);
+      else if (lane == 0 && warp == 0) producer<D>(p, smem, sm, wd);
+      else if (lane == 0) issuer<D, FP16>(p, smem, sm, tmem, wd);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ schedule
+// The work items of all prompts, those with the most key blocks first (a counting
+// sort by blocks).  Offsets that do not ascend within [0, T] leave no item: prompts
+// would overlap.
+constexpr int kScheduleThreads = 1024;
+constexpr int kBuckets = 1024;
+
+__global__ void __launch_bounds__(kScheduleThreads) prompt_schedule_kernel(const __grid_constant__ PromptParams p) {
+  __shared__ int s_warp[32];
+  __shared__ int s_bucket[kBuckets];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  next_may_launch();
+  wait_for_previous();
+  const int tq = kPromptRows >> p.gp_shift;  // tokens of an item
+  // Exclusive scan of one int per thread; returns the total too.
+  auto scan = [&](int x, int& total) {
+    int inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+      const int y = s_warp[w];
+      before += w < warp ? y : 0;
+      all += y;
+    }
+    __syncthreads();
+    total = all;
+    return before + inc - x;
+  };
+  bool bad = false;
+  int base = 0, longest = 0;
+  for (int i0 = 0; i0 < p.n; i0 += kScheduleThreads) {
+    const int i = i0 + tid;
+    int tiles = 0;
+    if (i < p.n) {
+      const int a = load_written(p.offsets + i), b = load_written(p.offsets + i + 1);
+      if (a < 0 || b < a || b > p.T) {
+        bad = true;
+      } else {
+        tiles = (b - a + tq - 1) / tq;
+        longest = max(longest, b - a);
+      }
+    }
+    int total;
+    const int at = scan(tiles, total);
+    if (i < p.n) p.tile_ptr[i] = base + at;
+    base += total;
+  }
+  s_bucket[tid] = 0;
+  bad = __syncthreads_or(bad);
+  if (tid == 0) {
+    p.control[kCtlWorkCounter] = 0;
+    p.control[kCtlStatus] = bad ? BSA_ERR_INVALID_ARG : BSA_OK;
+    p.control[kCtlDetail] = bad ? kSitePromptOffsets : 0;
+    p.control[kPromptCtlTiles] = bad ? 0 : base;
+    p.tile_ptr[p.n] = base;
+  }
+  if (bad) return;
+  // Blocks of a bucket: so many that the longest prompt's fit.
+#pragma unroll
+  for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  if (lane == 0) s_warp[warp] = longest;
+  __syncthreads();
+  for (int w = 0; w < 32; ++w) longest = max(longest, s_warp[w]);
+  int shift = 0;
+  while (((longest + 127) >> 7) >> shift >= kBuckets) ++shift;
+  // Item e of the line: its prompt (the last that begins at or before it) and bucket.
+  auto item = [&](int e, int& bucket) {
+    int lo = 0, hi = p.n;  // tile_ptr[lo] <= e < tile_ptr[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.tile_ptr[mid] <= e) lo = mid;
+      else hi = mid;
+    }
+    const int a = load_written(p.offsets + lo), len = load_written(p.offsets + lo + 1) - a;
+    const int t0 = (e - p.tile_ptr[lo]) * tq;
+    const int keys = p.causal ? min(len, t0 + tq) : len;
+    bucket = kBuckets - 1 - (((keys + 127) >> 7) >> shift);
+    return make_int4(a, len, t0, 0);
+  };
+  for (int e = tid; e < base; e += kScheduleThreads) {
+    int b;
+    item(e, b);
+    atomicAdd(&s_bucket[b], 1);
+  }
+  __syncthreads();
+  int total;
+  const int at = scan(s_bucket[tid], total);
+  s_bucket[tid] = at;
+  __syncthreads();
+  for (int e = tid; e < base; e += kScheduleThreads) {
+    int b;
+    const int4 x = item(e, b);
+    p.tiles[atomicAdd(&s_bucket[b], 1)] = x;
+  }
+}
+
+template <int D, bool FP16>
+cudaError_t launch(const PromptParams& p, int sms, cudaStream_t s) {
+  constexpr int kSmem = Cfg<D>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const long long most = ((long long)p.T / (kPromptRows >> p.gp_shift) + p.n) * (p.Hq >> p.gp_shift);
+  return launch_after(prompt_kernel<D, FP16>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), kSmem, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(const PromptParams& p, int d, int sms, cudaStream_t s) {
+  cudaError_t e = launch_after(prompt_schedule_kernel, dim3(1), dim3(kScheduleThreads), 0, s, p);
+  if (e != cudaSuccess) return e;
+  if (d == 64) return p.fp16 ? launch<64, true>(p, sms, s) : launch<64, false>(p, sms, s);
+  return p.fp16 ? launch<128, true>(p, sms, s) : launch<128, false>(p, sms, s);
+}
+
+}  // namespace bsa

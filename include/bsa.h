@@ -35,7 +35,8 @@
  * drafts), bsa_cache_forward (a plan's forward over it: chunked prefill) and
  * its pages (bsa_cache_resize, _fork, _compact, _copy_pages), and its bounds:
  * bsa_cache_weigh (the attention weight each token gathers), bsa_cache_evict.
- * Prompts' rows ahead of both: bsa_rope_apply (rotary positions).
+ * Prompts' rows ahead of both: bsa_rope_apply (rotary positions),
+ * bsa_prompt_attention (whole prompts, packed, without a plan).
  *
  * Conventions
  *   - Every pointer argument named "device" is a CUDA device pointer owned by
@@ -805,6 +806,39 @@ bsa_status bsa_rope_steps(int rot, double base, int scaling, double factor, doub
 bsa_status bsa_rope_apply(const bsa_rope* rope, const bsa_rows* q, const bsa_rows* q_out, int Hq, const bsa_rows* k,
                           const bsa_rows* k_out, int Hk, int dtype, const int32_t* positions, int B, int T, int d,
                           int flags, void* stream);
+
+/* Causal: token t of a prompt sees its tokens 0 .. t; without it, all of them. */
+#define BSA_PROMPT_CAUSAL 0x1
+/*
+ * bsa_prompt_attention -- attention of whole prompts, packed behind one another:
+ *   O[t] = sum_j p_j V_j / sum_j p_j, p_j = exp(scale <Q_t, K_j> - m), over the tokens
+ * j of t's own prompt (j <= t if causal), as bsa_forward with a mask of ones gives it,
+ * for prompts of any length (0 too) without padding.
+ * q, o: [T][Hq][d], k, v: [T][Hkv][d] of `dtype` (bsa_rows; stride_b is not read; no
+ *   stride of 0 between several rows); Hq a multiple of Hkv; d in {64, 128}.
+ *   LSE: device fp32 [T][Hq] (written), or NULL.  o shares no memory with q, k or v.
+ * offsets: device int32 [n + 1], ascending within [0, T]: prompt i has rows
+ *   offsets[i] .. offsets[i + 1] - 1.  Rows of no prompt are not read for any output
+ *   and not written.  Offsets that do not ascend within [0, T] are recorded
+ *   (BSA_ERR_INVALID_ARG) and nothing is written.
+ * flags: 0 or BSA_PROMPT_CAUSAL.  scale <= 0 selects 1/sqrt(d).
+ * workspace: device, 16-byte aligned, bsa_prompt_workspace_bytes bytes; scratch and
+ *   status of this call (calls that overlap in time need their own).
+ * Scores, sums and accumulators are fp32, weights are rounded to `dtype` relative to
+ * (at most 2^8 times) their row's largest so far.  An infinity or NaN among the keys
+ * or values reaches the rows that attend it and no other.  Two kernels.
+ */
+size_t bsa_prompt_workspace_bytes(int n, int T, int Hq, int Hkv);
+bsa_status bsa_prompt_attention(const bsa_rows* q, const bsa_rows* k, const bsa_rows* v, const bsa_rows* o, float* LSE,
+                                int dtype, const int32_t* offsets, int n, int T, int Hq, int Hkv, int d, int flags,
+                                float scale, void* workspace, size_t workspace_bytes, void* stream);
+/*
+ * bsa_prompt_status -- synchronise `stream`, then report what the kernels of the last
+ * bsa_prompt_attention with this workspace recorded: BSA_OK, BSA_ERR_INVALID_ARG (its
+ * offsets) or BSA_ERR_TIMEOUT (a wait ran past the watchdog limit; the kernel stopped
+ * cleanly).  *detail (may be NULL) receives (block << 8) | wait-site.
+ */
+bsa_status bsa_prompt_status(const void* workspace, void* stream, int32_t* detail);
 
 /* Human-readable name of a status code (static string). */
 const char* bsa_status_string(int status);
