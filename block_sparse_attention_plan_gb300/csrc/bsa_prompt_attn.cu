@@ -10,10 +10,16 @@
 // One CTA (384 threads):
 //   warp 0    takes work items, publishes them, loads both Q tiles and the K and
 //             V blocks (128 keys) into one ring, in the order they are used;
-//   warp 1    (one thread) issues S = Q K^T and O += P V of the two tiles in turn,
-//               PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) ...,
-//             so that one tile's products run while the other tile's softmax does;
-//   warps 2, 3  look over the values of every block that some row of the item does not
+//   warps 1, 2  issue S = Q K^T and O += P V of tile A and of tile B, in turns:
+//               PV_A(j) S_A(j+1) | PV_B(j) S_B(j+1) | PV_A(j+1) ...,
+//             so that one tile's products run while the other tile's softmax does.
+//             Each has done its waiting when its turn comes, while the other's products
+//             keep the tensor cores busy.  (One thread for both: 350 to 1000 cycles of
+//             waits with nothing queued, a prompt of 12007 tokens, 32 / 8 heads of 128,
+//             859 us, and 953 with descriptors in one thread's registers; two without
+//             turns fall into step, products and softmax of both tiles by turns: 994;
+//             in turns: 749.)
+//   warp 3    looks over the values of every block that some row of the item does not
 //             attend as a whole (below);
 //   warps 4-7, 8-11  the softmax of tile A and of tile B, a thread per row, with a
 //             running maximum that is moved only when a score passes it by more
@@ -50,10 +56,10 @@ constexpr int kRegsControl = 72;
 constexpr int kRegsSoftmax = 208;
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split");
 constexpr int kSlots = 4;                   // work items published ahead
-constexpr int kConsumers = 1 + 2 + 8;       // MMA thread, two scanning warps, eight softmax warps
+constexpr int kConsumers = 2 + 1 + 8;       // issuing warps, scanning warp, eight softmax warps
 constexpr float kMove = 8.f;                // log2: weights stay <= 2^(8 + kShift)
 
-enum PromptSite : int { kSitePromptOffsets = 0x60 };
+enum PromptSite : int { kSitePromptOffsets = 0x60, kSiteTurn };
 
 template <int D_>
 struct Cfg {
@@ -66,20 +72,23 @@ struct Cfg {
   static constexpr int kOffBar = kOffKV + kStages * kTileBytes;
   static constexpr int kQFull = 0, kQEmpty = 2;
   static constexpr int kFull = 4;
-  static constexpr int kEmpty = kFull + kStages;
-  static constexpr int kClean = kEmpty + kStages;
+  static constexpr int kClean = kFull + kStages;
   static constexpr int kSFull = kClean + kStages;  // [2]
   static constexpr int kPFull = kSFull + 2;        // [2]
   static constexpr int kOFull = kPFull + 2;        // [2]
   static constexpr int kOFree = kOFull + 2;        // [2]
-  static constexpr int kDrain = kOFree + 2;
-  static constexpr int kSchedFull = kDrain + 1;
+  static constexpr int kTurn = kOFree + 2;         // [2]
+  // Both tiles are done with block b (of the CTA's): its values and the next keys.
+  static constexpr int kBlocks = 8;                // more blocks than the ring's entries belong to
+  static constexpr int kDone = kTurn + 2;
+  static constexpr int kDrain = kDone + kBlocks;   // [2]
+  static constexpr int kSchedFull = kDrain + 2;
   static constexpr int kSchedEmpty = kSchedFull + kSlots;
   static constexpr int kNumBars = kSchedEmpty + kSlots;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag
   static constexpr int kOffSched = kOffMisc + 16;           // int [kSlots][8]
-  static constexpr int kOffDirty = kOffSched + 32 * kSlots; // int [2 kSlots][2]
-  static constexpr int kSmem = kOffDirty + 16 * kSlots;
+  static constexpr int kOffDirty = kOffSched + 32 * kSlots; // int [2 kSlots]
+  static constexpr int kSmem = kOffDirty + 8 * kSlots;
   // How often ring entry r's stage has held values before (entries alternate keys and
   // values, so with an odd number of stages a stage does).
   __device__ static __forceinline__ uint32_t uses(uint32_t r) {
@@ -153,7 +162,10 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
   const int units = p.Hq >> p.gp_shift, half = 128 >> p.gp_shift;
   const int tiles = *reinterpret_cast<const volatile int32_t*>(p.control + kPromptCtlTiles);
   const int work = tiles * units;
-  uint32_t q_it = 0, kv_it = 0;
+  uint32_t q_it = 0, kv_it = 0, block = 0;
+  // Blocks that the entries of the ring belong to, a byte each, the oldest lowest: entry
+  // e holds keys or values until both tiles are done with that block.
+  uint64_t belongs = 0;
   bool ok = true;
   for (uint32_t t = 0; ok; ++t) {
     const int slot = (int)(t % kSlots);
@@ -184,15 +196,23 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
     ++q_it;
     for (int j = 0; j < 2 * nb; ++j) {
       const uint32_t s = kv_it % C::kStages;
-      if (!mbar_wait(sm.bar(C::kEmpty + (int)s), ((kv_it / C::kStages) & 1u) ^ 1u, wd, kSiteKvEmpty)) {
-        ok = false;
-        break;
+      // Values j / 2 and the keys behind them belong to block j / 2, as do the first keys.
+      const uint32_t mine = block + (uint32_t)(j > 0 ? (j - 1) / 2 : 0);
+      if (kv_it >= (uint32_t)C::kStages) {
+        // (blocks differ by less than 128: the low byte tells which of them it was)
+        const uint32_t was = mine - ((mine - (uint32_t)(belongs & 0xff)) & 0xffu);
+        if (!mbar_wait(sm.bar(C::kDone + (int)(was % C::kBlocks)), (was / C::kBlocks) & 1u, wd, kSiteKvEmpty)) {
+          ok = false;
+          break;
+        }
       }
+      belongs = belongs >> 8 & ~(0xffull << 8 * (C::kStages - 1)) | (uint64_t)(mine & 0xff) << 8 * (C::kStages - 1);
       const uint32_t full = sm.bar(C::kFull + (int)s);
       mbar_arrive_expect_tx(full, C::kTileBytes);
       tma_load_4d(sm.kv(s), j & 1 ? &p.tmV : &p.tmK, 0, kvh, m.row0 + (j >> 1) * 128, 0, full, pol_kv);
       ++kv_it;
     }
+    block += (uint32_t)nb;
   }
   if (*wd.abort_flag) {  // copies already issued land before the shared memory goes away
     const uint32_t nk = kv_it < (uint32_t)C::kStages ? kv_it : (uint32_t)C::kStages;
@@ -205,79 +225,105 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
 }
 
 // ------------------------------------------------------------------ matrix products
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// The products of tile x, run by a whole warp, so that the descriptors are uniform
+// values; one lane issues.
 template <int D, bool FP16>
-__device__ __noinline__ void issuer(const PromptParams& p, const uint8_t* smem, const Smem<Cfg<D>> sm, uint32_t tmem,
-                                    const Watchdog wd) {
+__device__ __forceinline__ void issuer(const PromptParams& p, const uint8_t* smem, const Smem<Cfg<D>>& sm, uint32_t tmem_,
+                                       const Watchdog& wd, int x) {
   using C = Cfg<D>;
   constexpr uint32_t kIdescS = FP16 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false);
   constexpr uint32_t kIdescO = FP16 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, true);
-  const uint64_t qd0 = smem_desc_sw128(sm.q(0, 0), 16, 1024);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_, 0);
+  const uint32_t scol = tmem + C::kColS + 128u * (uint32_t)x, ocol = tmem + C::kColO + 128u * (uint32_t)x;
+  const uint64_t qd0 = smem_desc_sw128(sm.q(0, x), 16, 1024);
   const uint64_t kd0 = smem_desc_sw128(sm.kv(0), 16, 1024);
   const uint64_t vd0 = smem_desc_sw128(sm.kv(0), C::kChunkBytes, 1024);
-  constexpr uint64_t kStep = (uint64_t)(C::kTileBytes >> 4);
-  uint32_t q_it = 0, ring = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
+  constexpr uint32_t kStep = (uint32_t)(C::kTileBytes >> 4);
+  // Items, ring entries and blocks so far; those of tile x; turns.
+  uint32_t q_it = 0, ring = 0, block = 0, pc = 0, oc = 0, turn = 0;
   bool ok = true;
   auto stage = [](uint32_t r) { return r % (uint32_t)C::kStages; };
-  auto full = [&](uint32_t r) {
-    return mbar_wait(sm.bar(C::kFull + (int)stage(r)), (r / C::kStages) & 1u, wd, kSiteKvFull);
+  auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+    ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, site));
+    return ok;
   };
-  auto issue_s = [&](int x, int qb, uint32_t r) {
-    const uint64_t qd = qd0 + (uint64_t)(qb * 2 + x) * kStep, kd = kd0 + (uint64_t)stage(r) * kStep;
+  auto full = [&](uint32_t r) { return wait(sm.bar(C::kFull + (int)stage(r)), (r / C::kStages) & 1u, kSiteKvFull); };
+  auto issue_s = [&](int qb, uint32_t r) {
+    const uint64_t qd = qd0 + (uint64_t)((uint32_t)(qb * 2) * kStep), kd = kd0 + (uint64_t)(stage(r) * kStep);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint64_t off = (uint64_t)(((kk / 4) * C::kChunkBytes + (kk % 4) * 32) >> 4);
-      mma_ss(tmem + C::kColS + 128u * (uint32_t)x, qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
+      mma_ss(scol, qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
     }
-    mma_commit(sm.bar(C::kSFull + x));
   };
   for (uint32_t t = 0; ok; ++t) {
-    const Item m = take<C>(sm, smem, t, true, false, wd);
-    if (m.it < 0) break;
-    const int nx[2] = {blocks_of(p, m, 0), blocks_of(p, m, 1)};
-    const int nb = max(nx[0], nx[1]);
+    const Item got = take<C>(sm, smem, t, (threadIdx.x & 31) == 0, true, wd);
+    if (__shfl_sync(0xffffffffu, got.it, 0) < 0) break;
+    const int nx = __shfl_sync(0xffffffffu, blocks_of(p, got, x), 0);
+    const int nb = max(nx, __shfl_sync(0xffffffffu, blocks_of(p, got, x ^ 1), 0));
     const int qb = (int)(q_it % C::kQBufs);
-    ok = mbar_wait(sm.bar(C::kQFull + qb), (q_it / C::kQBufs) & 1u, wd, kSiteQFull) && full(ring);
-    if (!ok) break;
-    tc_fence_after();
-    issue_s(0, qb, ring);
-    if (nx[1] > 0) issue_s(1, qb, ring);
-    mma_commit(sm.bar(C::kEmpty + (int)stage(ring)));
-    if (nb == 1) mma_commit(sm.bar(C::kQEmpty + qb));
-    for (int j = 0; j < nb && ok; ++j) {
+    // (also where the tile has no token: a buffer is released once in each of its turns)
+    if (!wait(sm.bar(C::kQFull + qb), (q_it / C::kQBufs) & 1u, kSiteQFull)) break;
+    if (nx > 0) {
+      if (!full(ring)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_s(qb, ring);
+        mma_commit(sm.bar(C::kSFull + x));
+        if (nx == 1) mma_commit(sm.bar(C::kQEmpty + qb));
+      }
+    } else if (elect_one()) {
+      mbar_arrive(sm.bar(C::kQEmpty + qb));
+    }
+    __syncwarp();
+    for (int j = 0; j < nb; ++j, ++block, ++turn) {
       const uint32_t rv = ring + 2 * (uint32_t)j + 1;
+      const bool mine = j < nx, more = j + 1 < nx;
+      // (a tile without this block waits for it all the same: released in its turn)
+      if (!full(rv) || (j + 1 < nb && !full(rv + 1))) break;
+      if (mine) {
+        if (!wait(sm.bar(C::kClean + (int)stage(rv)), C::uses(rv) & 1u, kSiteKvFull)) break;
+        if (j == 0 && oc > 0 && !wait(sm.bar(C::kOFree + x), (oc - 1) & 1u, kSiteODone)) break;
+        if (!wait(sm.bar(C::kPFull + x), pc & 1u, kSitePFull)) break;
+        ++pc;
+      }
+      if (!wait(sm.bar(C::kTurn + x), (turn & 1u) ^ (x ? 0u : 1u), kSiteTurn)) break;
+      tc_fence_after();
+      const uint64_t vd = vd0 + (uint64_t)(stage(rv) * kStep);
+      if (elect_one()) {
+        if (mine) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (j >= nx[x] || !ok) continue;
-        ok = full(rv) && mbar_wait(sm.bar(C::kClean + (int)stage(rv)), C::uses(rv) & 1u, wd, kSiteKvFull) &&
-             mbar_wait(sm.bar(C::kPFull + x), pc[x] & 1u, wd, kSitePFull);
-        if (ok && j == 0 && oc[x] > 0) ok = mbar_wait(sm.bar(C::kOFree + x), (oc[x] - 1) & 1u, wd, kSiteODone);
-        if (!ok) continue;
-        ++pc[x];
-        tc_fence_after();
-        const uint64_t vd = vd0 + (uint64_t)stage(rv) * kStep;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + C::kColO + 128u * (uint32_t)x, tmem + C::kColS + 128u * (uint32_t)x + 8u * (uint32_t)kk,
-                 vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-        if (j + 1 < nx[x]) {
-          if (!(ok = full(rv + 1))) continue;
-          tc_fence_after();
-          issue_s(x, qb, rv + 1);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(ocol, scol + 8u * (uint32_t)kk, vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (more) issue_s(qb, rv + 1);
+        mbar_arrive(sm.bar(C::kTurn + (x ^ 1)));
+        if (mine) {
+          mma_commit(sm.bar(more ? C::kSFull + x : C::kOFull + x));
+          mma_commit(sm.bar(C::kDone + (int)(block % C::kBlocks)));
+          if (j + 2 == nx) mma_commit(sm.bar(C::kQEmpty + qb));
         } else {
-          mma_commit(sm.bar(C::kOFull + x));
-          ++oc[x];
+          mbar_arrive(sm.bar(C::kDone + (int)(block % C::kBlocks)));
         }
       }
-      if (!ok) break;
-      mma_commit(sm.bar(C::kEmpty + (int)stage(rv)));
-      if (j + 1 < nb) mma_commit(sm.bar(C::kEmpty + (int)stage(rv + 1)));
-      if (j + 2 == nb) mma_commit(sm.bar(C::kQEmpty + qb));
+      __syncwarp();
+      if (mine && !more) ++oc;
     }
+    if (!ok) break;
     ring += 2 * (uint32_t)nb;
     ++q_it;
   }
-  mma_commit(sm.bar(C::kDrain));
-  drain_wait(sm.bar(C::kDrain), 0, wd);
+  if (elect_one()) {
+    mma_commit(sm.bar(C::kDrain + x));
+    drain_wait(sm.bar(C::kDrain + x), 0, wd);
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ values
@@ -290,24 +336,23 @@ __device__ __forceinline__ uint32_t no_numbers(uint32_t w) {
 
 template <int D, bool FP16>
 __device__ __forceinline__ void scanner(const PromptParams& p, uint8_t* smem, const Smem<Cfg<D>>& sm, const Watchdog& wd,
-                                        int who) {
+                                        int lane) {
   using C = Cfg<D>;
-  const int lane = threadIdx.x & 31;
   volatile int* dirty = reinterpret_cast<volatile int*>(smem + C::kOffDirty);
   uint32_t ring = 0;
   for (uint32_t t = 0;; ++t) {
     const Item m = take<C>(sm, smem, t, lane == 0, true, wd);
     if (m.it < 0) return;
     const int nb = max(blocks_of(p, m, 0), blocks_of(p, m, 1)), first = masked_from(p, m);
-    if (lane == 0) dirty[(t % (2 * kSlots)) * 2 + who] = 0;
+    if (lane == 0) dirty[t % (2 * kSlots)] = 0;
     for (int j = 0; j < nb; ++j) {
       const uint32_t r = ring + 2 * (uint32_t)j + 1, s = r % C::kStages;
       if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(C::kFull + (int)s), (r / C::kStages) & 1u, wd, kSiteKvFull))) return;
       if (j >= first) {
         bool here = false;
-        const uint32_t at = sm.kv(s) + (uint32_t)(who * (C::kTileBytes / 2) + lane * 16);
+        const uint32_t at = sm.kv(s) + (uint32_t)(lane * 16);
 #pragma unroll 8
-        for (int q = 0; q < C::kTileBytes / 2; q += 512) {
+        for (int q = 0; q < C::kTileBytes; q += 512) {
           const uint4 w = ld_shared_v4(at + q);
           const uint32_t a = no_numbers<FP16>(w.x), b = no_numbers<FP16>(w.y), c = no_numbers<FP16>(w.z),
                          d = no_numbers<FP16>(w.w);
@@ -318,7 +363,7 @@ __device__ __forceinline__ void scanner(const PromptParams& p, uint8_t* smem, co
         }
         if (__any_sync(0xffffffffu, here)) {
           fence_proxy_async_smem();  // the product reads what was written
-          if (lane == 0) dirty[(t % (2 * kSlots)) * 2 + who] = 1;
+          if (lane == 0) dirty[t % (2 * kSlots)] = 1;
         }
       }
       __syncwarp();
@@ -507,8 +552,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
     if (real && p.lse)
       p.lse[(long long)(m.row0 + tok) * p.Hq + head] =
           l == 0.f ? -INFINITY : (m_ref - kShift + __log2f(l)) * 0.69314718055994531f;
-    const int slot = (int)(t % (2 * kSlots)) * 2;
-    if (dirty[slot] | dirty[slot + 1]) add_no_numbers<D, FP16>(p, m, first + ((quad * 32) >> p.gp_shift), quad * 32);
+    if (dirty[t % (2 * kSlots)]) add_no_numbers<D, FP16>(p, m, first + ((quad * 32) >> p.gp_shift), quad * 32);
   }
 }
 
@@ -526,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     *abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(sm.bar(C::kQFull + i), 1);
-      mbar_init(sm.bar(C::kQEmpty + i), 1);
+      mbar_init(sm.bar(C::kQEmpty + i), 2);
       mbar_init(sm.bar(C::kSFull + i), 1);
       mbar_init(sm.bar(C::kPFull + i), 4);
       mbar_init(sm.bar(C::kOFull + i), 1);
@@ -534,10 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(sm.bar(C::kFull + i), 1);
-      mbar_init(sm.bar(C::kEmpty + i), 1);
-      mbar_init(sm.bar(C::kClean + i), 2);
+      mbar_init(sm.bar(C::kClean + i), 1);
     }
-    mbar_init(sm.bar(C::kDrain), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sm.bar(C::kTurn + i), 1);
+      mbar_init(sm.bar(C::kDrain + i), 1);
+    }
+    for (int i = 0; i < C::kBlocks; ++i) mbar_init(sm.bar(C::kDone + i), 2);
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(sm.bar(C::kSchedFull + i), 1);
       mbar_init(sm.bar(C::kSchedEmpty + i), kConsumers);
@@ -562,9 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   } else {
     regs_dec<kRegsControl>();
     if (!*abort_flag) {
-      if (warp >= 2) scanner<D, FP16>(p, smem, sm, wd, warp - 2);
-      else if (lane == 0 && warp == 0) producer<D>(p, smem, sm, wd);
-      else if (lane == 0) issuer<D, FP16>(p, smem, sm, tmem, wd);
+      if (warp == 3) scanner<D, FP16>(p, smem, sm, wd, lane);
+      else if (warp >= 1) issuer<D, FP16>(p, smem, sm, tmem, wd, warp - 1);
+      else if (lane == 0) producer<D>(p, smem, sm, wd);
     }
   }
   __syncwarp();
