@@ -120,6 +120,7 @@ struct CacheWeighParams {
   const uint8_t* mask;  // [B][Hq][NKB]
   int fp16, B, Hq, g, nq, M, NKB, bk, causal, fresh;
   float scale;
+  long long watchdog_ns;
 };
 
 // Eviction of cached tokens (bsa_cache_evict.cu).
@@ -131,6 +132,7 @@ struct CacheEvictParams {
   const int32_t* keep;  // [n]
   int32_t* kept;        // [n][Hkv][keep_max]: where kept tokens were
   int32_t* cut;         // [n]: the length a sequence is cut to, -1: it is left as it is
+  int32_t* done;        // [n]: CTAs that have moved their part of it
   int n, sink, recent, keep_max;
 };
 

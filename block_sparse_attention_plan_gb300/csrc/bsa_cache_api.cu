@@ -300,11 +300,12 @@ bsa_status bsa_cache_weigh(const bsa_cache* cache, const bsa_rows* q, const floa
   p.bk = bk;
   p.causal = flags & BSA_CACHE_CAUSAL ? 1 : 0;
   p.fresh = fresh;
+  p.watchdog_ns = watchdog_limit_ns();
   p.scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)p.c.d));
   return launch_cache_weigh(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
-size_t bsa_cache_evict_workspace_bytes(int n) { return n < 1 || n > kCacheListMax ? 0 : align256(4ull * n); }
+size_t bsa_cache_evict_workspace_bytes(int n) { return n < 1 || n > kCacheListMax ? 0 : align256(8ull * n); }
 
 bsa_status bsa_cache_evict(const bsa_cache* cache, float* weights, int weights_tokens, const int32_t* seqs,
                            const int32_t* keep, int sink, int recent, int32_t* kept, int keep_max, int n,
@@ -327,6 +328,7 @@ bsa_status bsa_cache_evict(const bsa_cache* cache, float* weights, int weights_t
   p.keep = keep;
   p.kept = kept;
   p.cut = static_cast<int32_t*>(workspace);
+  p.done = p.cut + n;
   p.n = n;
   p.sink = sink;
   p.recent = recent;

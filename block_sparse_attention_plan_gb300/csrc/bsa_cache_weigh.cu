@@ -11,15 +11,16 @@
 //
 // What bounds it: d bytes per key and K/V head at the memory's rate, and the 8
 // of its weight.  Tokens' sums are independent of each other, so there is
-// nothing to join: the tiles (32 keys at d = 128, 64 at d = 64: 4 KB) of all
+// nothing to join: the tiles (4 KB: 32 keys at d = 128, 64 at d = 64) of all
 // (sequence, K/V head) pairs form one line that the CTAs cut evenly, and in a
 // CTA's piece of a pair the warps take tiles in turn (a window of selected
-// blocks is spread over them).  Keys go from global memory to registers, 16
-// bytes a lane: the order of a row's elements in the product is free, so a lane
-// takes the words it has loaded; a tile's registers are refilled for the next
-// tile as soon as they are converted, which keeps 4 KB a warp and 64 KB an SM
-// on their way.  The rows wait in shared memory, prepared once per pair; with
-// more than kWeighRows of them a piece is gone over again for the next ones.
+// blocks is spread over them).  Each warp feeds itself: a ring of three tiles in shared
+// memory, filled by bulk copies of a page's rows, the next one requested as soon as a
+// tile is in registers.  The order of a row's elements in the product is free, so a
+// lane takes 16-byte vectors as they lie (at d = 128 odd rows their halves the other
+// way round: no bank conflicts).  The rows wait in shared memory, prepared once per
+// pair.  From 33 rows on the products are what costs (128 rows a pass, pieces are gone
+// over again for more): tiles of 16 keys, so that few tokens spread over all warps.
 #include "bsa_cache.h"
 #include "bsa_cache_codes.cuh"
 #include "bsa_device.cuh"
@@ -31,27 +32,42 @@ using namespace dev;
 
 constexpr int kWeighWarps = 8;
 constexpr int kWeighThreads = 32 * kWeighWarps;
-constexpr int kWeighRows = 128;  // query rows in shared memory at a time
 
-template <int D>
+// ROWS: query rows in shared memory at a time.
+template <int D, int ROWS>
 struct WeighCfg {
-  static constexpr int TK = 4096 / D;          // keys of a tile
-  static constexpr int kGroups = TK / 16;      // keys of one matrix instruction, one scale each
+  static constexpr int kGroups = ROWS <= 32 ? 256 / D : 1;  // of 16 keys: one matrix instruction, one scale each
+  static constexpr int TK = 16 * kGroups;      // keys of a tile
+  static constexpr int kTileBytes = TK * D;
+  static constexpr int kStages = 3;            // of a warp
   static constexpr int kVecs = D / 64;         // 16-byte vectors of a lane in a row of codes
+  static constexpr int kCols = (TK + 31) / 32; // tokens that a lane writes
   static constexpr int kRowBytes = 2 * D + 16; // of a prepared query row (16: no bank conflicts)
-  static constexpr int kOffConst = kWeighRows * kRowBytes;       // {qs, lse} of each row
-  static constexpr int kOffLim = kOffConst + kWeighRows * 8;     // last key position of each row (causal)
-  static constexpr int kOffHead = kOffLim + kWeighRows * 4;      // head in the group
-  static constexpr int kOffScan = kOffHead + kWeighRows * 4;     // prefix of the threads' tiles
-  static constexpr int kSmem = kOffScan + (kWeighThreads + kWeighWarps + 1) * 4;
-  static_assert(kSmem <= 48 * 1024, "no attribute needed");
+  static constexpr int kOffRows = kWeighWarps * kStages * kTileBytes;
+  static constexpr int kOffConst = kOffRows + ROWS * kRowBytes;  // {qs, lse} of each row
+  static constexpr int kOffLim = kOffConst + ROWS * 8;           // last key position of each row (causal)
+  static constexpr int kOffHead = kOffLim + ROWS * 4;            // head in the group
+  static constexpr int kOffBar = kOffHead + ROWS * 4;            // full [warps][stages]
+  static constexpr int kOffTile = kOffBar + kWeighWarps * kStages * 8;  // [warps][stages][8]: tile, pool rows of its groups
+  static constexpr int kOffScan = kOffTile + kWeighWarps * kStages * 32;  // prefix of the threads' tiles
+  static constexpr int kOffAbort = kOffScan + (kWeighThreads + kWeighWarps) * 4;
+  static constexpr int kSmem = kOffAbort + 16;
+  static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
 };
+enum WeighSite : int { kSiteWeighTile = 0x58 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Bulk copy of `bytes` (a multiple of 16) into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 
 // Sequence of batch row b (-1: none, or out of range), and its length (0 where
@@ -68,19 +84,31 @@ __device__ __forceinline__ int weigh_len(const CacheWeighParams& p, int b) {
   return n;
 }
 
-template <int D, int KIND>
+template <int D, int KIND, int ROWS>
 __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_constant__ CacheWeighParams p) {
-  using C = WeighCfg<D>;
+  using C = WeighCfg<D, ROWS>;
   constexpr int TK = C::TK, G = C::kGroups, NV = C::kVecs;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   const CacheDev& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int l4 = lane & 3, r8 = lane >> 2;
+  uint8_t* s_rows = smem + C::kOffRows;
   float* s_const = reinterpret_cast<float*>(smem + C::kOffConst);
   int* s_lim = reinterpret_cast<int*>(smem + C::kOffLim);
   int* s_head = reinterpret_cast<int*>(smem + C::kOffHead);
+  int* s_tile = reinterpret_cast<int*>(smem + C::kOffTile) + warp * C::kStages * 8;
   int* s_scan = reinterpret_cast<int*>(smem + C::kOffScan);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * C::kStages * C::kTileBytes);
+  const uint32_t bars = smem_u32(smem) + C::kOffBar + (uint32_t)(warp * C::kStages * 8);
+  const Watchdog wd{s_abort, c.control + kCacheStatus, c.control + kCacheDetail, p.watchdog_ns};
   const int lpage = 31 - __clz(c.page), lsb = 31 - __clz(c.sb), lbk = p.mask ? 31 - __clz(p.bk) : 0;
+  if (tid == 0) {
+    *s_abort = 0;
+    for (int i = 0; i < kWeighWarps * C::kStages; ++i) mbar_init(smem_u32(smem) + C::kOffBar + 8 * i, 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
   next_may_launch();
   wait_for_previous();
 
@@ -140,6 +168,8 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
   int h = (int)((lo - base) / tiles);
   base += (long long)h * tiles;  // place where the pair (b, h) begins
 
+  uint32_t asked = 0, used = 0;  // tiles requested and taken by this warp
+  bool gave_up = false;          // a wait of this warp ran out: it requests nothing more
   for (; base < hi;) {
     // Tiles [t0, t1) of the pair.
     const int t0 = (int)(lo > base ? lo - base : 0), t1 = (int)(hi - base < tiles ? hi - base : tiles);
@@ -156,37 +186,11 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
       const uint8_t* mask = p.mask ? p.mask + ((size_t)b * p.Hq + (size_t)h * p.g) * p.NKB : nullptr;
       const int fresh0 = len > p.fresh ? len - p.fresh : 0;  // weights from here on begin at 0
       const int free_end = p.causal ? len - p.nq + 1 : len;  // keys below it are seen by every query
-      for (int m0 = 0; m0 < p.M; m0 += kWeighRows) {
-        const int rows = min(p.M - m0, kWeighRows);
-        // ------------------------------------------------------------ a tile's keys
-        uint4 kv[G][2][NV];
-        float sc[G];
-        bool held[G];
-        // Keys of group gr of tile t into its registers (nothing of no page).
-        auto load_group = [&](int t, int gr) {
-          const int j = t * TK + gr * 16;
-          const int pg = j < len ? load_written(table + (j >> lpage)) : -1;
-          held[gr] = pg >= 0 && pg < c.num_pages;
-          sc[gr] = 0.f;
-          if (!held[gr]) {
-            if (j < len && lane == 0) cache_error(c.control, BSA_ERR_PLAN_MISMATCH, seq);
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int v = 0; v < NV; ++v) kv[gr][x][v] = make_uint4(0u, 0u, 0u, 0u);
-            return;
-          }
-          const size_t row = ((size_t)pg * c.Hkv + h) * c.page + (j & (c.page - 1));
-          sc[gr] = load_written(c.ks + (row >> lsb));
-          const uint8_t* at = c.k + (row + r8) * D + 16 * l4;
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-              kv[gr][x][v] = load_written(reinterpret_cast<const uint4*>(at + (size_t)x * 8 * D + 64 * v));
-        };
-        // The next tile at or past t that has something to do; bit x of `active`:
-        // tile t32 + x kWeighWarps.
+      for (int m0 = 0; m0 < p.M; m0 += ROWS) {
+        const int rows = min(p.M - m0, ROWS);
+        // ------------------------------------------------------------ requests
+        // The next tile that has something to do; bit x of `active`: tile
+        // t32 + x kWeighWarps.
         int t32 = t0 + warp;
         uint32_t active = 0u;
         auto look = [&]() {
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
             some = false;
             for (int x = 0; x < p.g && !some; ++x)
 #pragma unroll
-              for (int q = 0; q < TK / 32; ++q) {
+              for (int q = 0; q < C::kCols; ++q) {
                 const int kb = (t * TK + 32 * q) >> lbk;
                 if (kb < p.NKB) some |= load_written(mask + (size_t)x * p.NKB + kb) != 0;
               }
@@ -204,21 +208,58 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
           active = __ballot_sync(0xffffffffu, some);
         };
         look();
-        auto next_tile = [&]() -> int {  // -1: none is left
+        int waiting = 0;  // tiles on their way
+        // Requests the next tile into the stage after the last one's: lane g looks up
+        // group g's page, the first lane of a page's groups copies them.
+        const int run = min(c.page, TK);
+        auto request = [&]() {
+          if (gave_up) return;
           while (!active) {
             t32 += 32 * kWeighWarps;
-            if (t32 >= t1) return -1;
+            if (t32 >= t1) return;
             look();
           }
           const int x = __ffs(active) - 1;
           active &= active - 1;
-          return t32 + x * kWeighWarps;
+          const int t = t32 + x * kWeighWarps;
+          const uint32_t s = asked % C::kStages, bar = bars + 8 * s;
+          int row = -1;
+          if (lane < G) {
+            const int j = t * TK + 16 * lane;
+            if (j < len) {
+              const int pg = load_written(table + (j >> lpage));
+              if (pg >= 0 && pg < c.num_pages) row = (pg * c.Hkv + h) * c.page + (j & (c.page - 1));
+              else cache_error(c.control, BSA_ERR_PLAN_MISMATCH, seq);
+            }
+            s_tile[s * 8 + 1 + lane] = row;
+          }
+          const bool copies = row >= 0 && ((16 * lane) & (run - 1)) == 0;
+          const int parts = __popc(__ballot_sync(0xffffffffu, copies));
+          if (lane == 0) {
+            s_tile[s * 8] = t;
+            if (parts) mbar_arrive_expect_tx(bar, (uint32_t)(parts * run * D));
+            else mbar_arrive(bar);
+          }
+          __syncwarp();
+          if (copies)
+            bulk_load(ring + s * C::kTileBytes + (uint32_t)(16 * lane * D), c.k + (size_t)row * D, (uint32_t)(run * D), bar);
+          ++asked;
+          ++waiting;
         };
-        int t = next_tile();
-        if (t >= 0) {
+#pragma unroll 1
+        for (int i = 0; i < C::kStages; ++i) request();
+        // Scales of the groups of the next tile.
+        float sc_next[G];
+        auto scales = [&]() {
+          const int* e = s_tile + (used % C::kStages) * 8 + 1;
 #pragma unroll
-          for (int gr = 0; gr < G; ++gr) load_group(t, gr);
-        }
+          for (int gr = 0; gr < G; ++gr) {
+            const int row = e[gr];
+            sc_next[gr] = row >= 0 ? load_written(c.ks + (row >> lsb)) : 0.f;
+          }
+        };
+        __syncwarp();
+        if (waiting) scales();
         // ------------------------------------------------------------ the rows
         __syncthreads();  // (those before them are used up)
         for (int m = warp * 8 + r8; m < ((rows + 7) & ~7); m += 8 * kWeighWarps) {
@@ -249,7 +290,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
           // at least 2^-133 and keep their bits).
           const int e = max(min((int)(top >> 23), 254), 1) - 127;
           const float inv = e == 127 ? 0x1p-127f : __uint_as_float((uint32_t)(127 - e) << 23);
-          uint8_t* dst = smem + m * C::kRowBytes + 32 * l4;
+          uint8_t* dst = s_rows + m * C::kRowBytes + 32 * l4;
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
             uint32_t o[8];
@@ -262,22 +303,30 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
             *reinterpret_cast<uint4*>(dst + 128 * v + 16) = make_uint4(o[4], o[5], o[6], o[7]);
           }
           if (l4 == 0) {
+            // A row that attends nothing, and one that is none, give nothing: e^-inf.
             const float z = real ? load_written(p.lse + ((size_t)b * p.Hq + h * p.g + hd) * p.nq + i) : INFINITY;
             s_const[2 * m] = real ? p.scale * __uint_as_float((uint32_t)(e + 127) << 23) : 0.f;
-            s_const[2 * m + 1] = z == -INFINITY ? INFINITY : z;  // a row that attends nothing gives nothing
+            s_const[2 * m + 1] = z == -INFINITY ? INFINITY : z;
             s_lim[m] = p.causal ? len - p.nq + i : 0x7fffffff;
             s_head[m] = hd;
           }
         }
         __syncthreads();
         // ------------------------------------------------------------ the tiles
-        while (t >= 0) {
-          const int key0 = t * TK;
-          const int tn = next_tile();
-          // Heads of the group that select the tile, for each 32 keys.
-          uint32_t sel[TK / 32];
+        for (; waiting; --waiting) {
+          const uint32_t s = used % C::kStages;
+          const int key0 = s_tile[s * 8] * TK;
+          // Weights so far of the tokens that this lane writes: token 8 (l4 + 4 x) + r8.
+          float w[C::kCols];
 #pragma unroll
-          for (int q = 0; q < TK / 32; ++q) {
+          for (int x = 0; x < C::kCols; ++x) {
+            const int to = 8 * (l4 + 4 * x) + r8, j = key0 + to;
+            w[x] = to < TK && j < len && (m0 > 0 || j < fresh0) ? weights[j] : 0.f;
+          }
+          // Heads of the group that select the tile, for each 32 keys.
+          uint32_t sel[C::kCols];
+#pragma unroll
+          for (int q = 0; q < C::kCols; ++q) {
             sel[q] = 0xffffffffu;
             if (p.mask) {
               const int kb = (key0 + 32 * q) >> lbk;
@@ -287,13 +336,32 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
               sel[q] = __ballot_sync(0xffffffffu, on);
             }
           }
-          // Weights so far of the tokens that this lane writes: token 8 (l4 + 4 x) + r8.
-          float w[TK / 32];
+          if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * s, (used / C::kStages) & 1u, wd, kSiteWeighTile))) break;
+          uint4 kv[G][2][NV];
+          float sc[G];
+          bool held[G];
 #pragma unroll
-          for (int x = 0; x < TK / 32; ++x) {
-            const int j = key0 + 8 * (l4 + 4 * x) + r8;
-            w[x] = j < len && (m0 > 0 || j < fresh0) ? weights[j] : 0.f;
+          for (int gr = 0; gr < G; ++gr) {
+            sc[gr] = sc_next[gr];
+            held[gr] = s_tile[s * 8 + 1 + gr] >= 0;
+            const uint32_t at = ring + s * C::kTileBytes + (uint32_t)((16 * gr + r8) * D + 16 * l4);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if constexpr (NV == 2) {
+                const uint32_t o = (uint32_t)(r8 & 1) * 64u;  // (rows r8 and r8 + 8 alike)
+                const uint4 y = ld_shared_v4(at + x * 8 * D + o), z = ld_shared_v4(at + x * 8 * D + (o ^ 64u));
+                kv[gr][x][0] = o ? z : y;
+                kv[gr][x][1] = o ? y : z;
+              } else {
+                kv[gr][x][0] = ld_shared_v4(at + x * 8 * D);
+              }
+            }
           }
+          ++used;
+          __syncwarp();  // the stage has been read: refill it
+          request();
+          __syncwarp();
+          if (waiting > 1) scales();
 #pragma unroll
           for (int gr = 0; gr < G; ++gr) {
             uint32_t a[NV][4][4];
@@ -302,39 +370,39 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
               const uint32_t lo4[4] = {kv[gr][0][v].x, kv[gr][0][v].y, kv[gr][0][v].z, kv[gr][0][v].w};
               const uint32_t hi4[4] = {kv[gr][1][v].x, kv[gr][1][v].y, kv[gr][1][v].z, kv[gr][1][v].w};
 #pragma unroll
-              for (int s = 0; s < 4; ++s) {
-                const uint2 x = codes_to_half4<KIND>(lo4[s]), y = codes_to_half4<KIND>(hi4[s]);
-                a[v][s][0] = x.x;
-                a[v][s][1] = y.x;
-                a[v][s][2] = x.y;
-                a[v][s][3] = y.y;
+              for (int s4 = 0; s4 < 4; ++s4) {
+                const uint2 x = codes_to_half4<KIND>(lo4[s4]), y = codes_to_half4<KIND>(hi4[s4]);
+                a[v][s4][0] = x.x;
+                a[v][s4][1] = y.x;
+                a[v][s4][2] = x.y;
+                a[v][s4][3] = y.y;
               }
             }
             const float scale = sc[gr];
-            const bool there = held[gr];
-            if (tn >= 0) load_group(tn, gr);
             const int j0 = key0 + gr * 16 + r8;  // this lane's keys: j0, j0 + 8
+            const bool some = p.mask != nullptr, late = key0 + gr * 16 + 15 >= free_end;
             float acc0 = 0.f, acc1 = 0.f;
-            if (there && sel[gr / 2]) {
+            if (held[gr] && sel[gr / 2]) {
+#pragma unroll(ROWS > 32 ? 2 : 1)
               for (int n = 0; n < rows; n += 8) {
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
-                const uint8_t* br = smem + (n + r8) * C::kRowBytes + 32 * l4;
+                float x4[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint8_t* br = s_rows + (n + r8) * C::kRowBytes + 32 * l4;
 #pragma unroll
                 for (int v = 0; v < NV; ++v)
 #pragma unroll
                   for (int x = 0; x < 2; ++x) {
                     const uint4 bw = *reinterpret_cast<const uint4*>(br + 128 * v + 16 * x);
-                    mma16816(s, a[v][2 * x][0], a[v][2 * x][1], a[v][2 * x][2], a[v][2 * x][3], bw.x, bw.y);
-                    mma16816(s, a[v][2 * x + 1][0], a[v][2 * x + 1][1], a[v][2 * x + 1][2], a[v][2 * x + 1][3], bw.z,
+                    mma16816(x4, a[v][2 * x][0], a[v][2 * x][1], a[v][2 * x][2], a[v][2 * x][3], bw.x, bw.y);
+                    mma16816(x4, a[v][2 * x + 1][0], a[v][2 * x + 1][1], a[v][2 * x + 1][2], a[v][2 * x + 1][3], bw.z,
                              bw.w);
                   }
                 const float4 cst = *reinterpret_cast<const float4*>(s_const + 2 * (n + 2 * l4));
                 constexpr float kLog2e = 1.4426950408889634f;
-                float p00 = ex2_approx(fmaf(s[0], scale * cst.x, -cst.y) * kLog2e);
-                float p01 = ex2_approx(fmaf(s[1], scale * cst.z, -cst.w) * kLog2e);
-                float p10 = ex2_approx(fmaf(s[2], scale * cst.x, -cst.y) * kLog2e);
-                float p11 = ex2_approx(fmaf(s[3], scale * cst.z, -cst.w) * kLog2e);
-                if (p.mask) {
+                float p00 = ex2_approx(fmaf(x4[0], scale * cst.x, -cst.y) * kLog2e);
+                float p01 = ex2_approx(fmaf(x4[1], scale * cst.z, -cst.w) * kLog2e);
+                float p10 = ex2_approx(fmaf(x4[2], scale * cst.x, -cst.y) * kLog2e);
+                float p11 = ex2_approx(fmaf(x4[3], scale * cst.z, -cst.w) * kLog2e);
+                if (some) {
                   const int h0 = s_head[n + 2 * l4], h1 = s_head[n + 2 * l4 + 1];
                   bool on0, on1;
                   if (p.g <= 32) {
@@ -348,15 +416,13 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
                   if (!on0) p00 = p10 = 0.f;
                   if (!on1) p01 = p11 = 0.f;
                 }
-                if (j0 + 8 >= free_end) {  // (also keys past the length: their sums are not stored)
+                if (late) {  // (also keys past the length: their sums are not stored)
                   const int2 lim = *reinterpret_cast<const int2*>(s_lim + n + 2 * l4);
                   if (j0 > lim.x) p00 = 0.f;
                   if (j0 > lim.y) p01 = 0.f;
                   if (j0 + 8 > lim.x) p10 = 0.f;
                   if (j0 + 8 > lim.y) p11 = 0.f;
                 }
-                if (n + 2 * l4 >= rows) p00 = p10 = 0.f;
-                if (n + 2 * l4 + 1 >= rows) p01 = p11 = 0.f;
                 acc0 += p00 + p01;
                 acc1 += p10 + p11;
               }
@@ -365,16 +431,24 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
               acc0 += __shfl_xor_sync(0xffffffffu, acc0, 2);
               acc1 += __shfl_xor_sync(0xffffffffu, acc1, 2);
             }
-            // Keys 0-7 of group gr are column 2 gr of the tile's eights, keys 8-15 the next.
+            // Keys 0-7 of group gr are eight 2 gr of the tile's, keys 8-15 the next.
             if ((2 * gr & 3) == l4) w[gr / 2] += acc0;
             if (((2 * gr + 1) & 3) == l4) w[gr / 2] += acc1;
           }
 #pragma unroll
-          for (int x = 0; x < TK / 32; ++x) {
-            const int j = key0 + 8 * (l4 + 4 * x) + r8;
-            if (j < len) weights[j] = w[x];
+          for (int x = 0; x < C::kCols; ++x) {
+            const int to = 8 * (l4 + 4 * x) + r8, j = key0 + to;
+            if (to < TK && j < len) weights[j] = w[x];
           }
-          t = tn;
+        }
+        if (waiting) {  // what was requested lands
+          gave_up = true;
+          for (; used < asked; ++used) {
+            volatile int no_abort = 0;
+            mbar_wait(bars + 8 * (used % C::kStages), (used / C::kStages) & 1u,
+                      Watchdog{&no_abort, wd.status, wd.detail, 100000000ll}, kSiteWeighTile);
+          }
+          waiting = 0;
         }
       }
     }
@@ -391,16 +465,21 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
   }
 }
 
+template <int D, int ROWS>
+cudaError_t launch(const CacheWeighParams& p, int sms, cudaStream_t s) {
+  constexpr int kSmem = WeighCfg<D, ROWS>::kSmem;
+  auto go = [&](auto kernel) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return e != cudaSuccess ? e : launch_after(kernel, dim3(2 * sms), dim3(kWeighThreads), kSmem, s, p);
+  };
+  return p.c.kind == BSA_CACHE_INT8 ? go(weigh_kernel<D, BSA_CACHE_INT8, ROWS>) : go(weigh_kernel<D, BSA_CACHE_E4M3, ROWS>);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_weigh(const CacheWeighParams& p, int sms, cudaStream_t s) {
-  auto go = [&](auto kernel, int smem) { return launch_after(kernel, dim3(2 * sms), dim3(kWeighThreads), smem, s, p); };
-  const bool i8 = p.c.kind == BSA_CACHE_INT8;
-  if (p.c.d == 64)
-    return i8 ? go(weigh_kernel<64, BSA_CACHE_INT8>, WeighCfg<64>::kSmem)
-              : go(weigh_kernel<64, BSA_CACHE_E4M3>, WeighCfg<64>::kSmem);
-  return i8 ? go(weigh_kernel<128, BSA_CACHE_INT8>, WeighCfg<128>::kSmem)
-            : go(weigh_kernel<128, BSA_CACHE_E4M3>, WeighCfg<128>::kSmem);
+  if (p.c.d == 64) return p.M <= 32 ? launch<64, 32>(p, sms, s) : launch<64, 128>(p, sms, s);
+  return p.M <= 32 ? launch<128, 32>(p, sms, s) : launch<128, 128>(p, sms, s);
 }
 
 }  // namespace bsa

@@ -719,7 +719,7 @@ bsa_status bsa_cache_weigh(const bsa_cache* cache, const bsa_rows* q, const floa
  * skipped and recorded (BSA_ERR_INVALID_ARG, detail = i), as is one with a
  * token in no page (BSA_ERR_PLAN_MISMATCH, detail = the sequence).
  * n <= 4096.  workspace: device, 4-byte aligned, bsa_cache_evict_workspace_bytes(n)
- * bytes; calls that overlap in time need their own.  Three kernels.
+ * bytes; calls that overlap in time need their own.  Two kernels.
  */
 size_t bsa_cache_evict_workspace_bytes(int n);
 bsa_status bsa_cache_evict(const bsa_cache* cache, float* weights, int weights_tokens, const int32_t* seqs,

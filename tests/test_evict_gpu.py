@@ -255,6 +255,20 @@ def test_eviction_against_the_model(bsa, kind, page, sb, d, lens, keep, sink, re
     assert bsa.cache_status(c) == (0, 0)
 
 
+@pytest.mark.parametrize("lens,keep,H,page", [
+    ([100000], [3001], 2, 256),                     # shares of a cluster's CTAs
+    ([400007], [2500], 1, 256),                     # longer than a cluster holds
+    ([50001] + [9] * 310, [2000] + [4] * 310, 1, 64)])  # a CTA each, one with more than it holds
+def test_long_sequences(bsa, lens, keep, H, page):
+    m = filled("int8", lens, H, page, 16, 64, seed=6)
+    c = upload(bsa, m)
+    w = heavy(torch.Generator().manual_seed(1), len(lens), H, m.table.shape[1] * page)
+    w[0, 0, :5000] = 1.0                            # ties over the border of shares
+    w[0, 0, 20000:45000] = 1.0
+    evict_both(bsa, m, c, w, keep, sink=3, recent=5, keep_max=max(keep))
+    assert bsa.cache_status(c) == (0, 0)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_ties_zeros_nan_and_negative_weights(bsa, kind):
     rng = np.random.default_rng(4)
