@@ -279,8 +279,9 @@ bsa_status bsa_cache_weigh(const bsa_cache* cache, const bsa_rows* q, const floa
   if ((flags & ~BSA_CACHE_CAUSAL) || fresh < 0) return BSA_ERR_INVALID_ARG;
   if (dtype != BSA_BF16 && dtype != BSA_FP16) return BSA_ERR_UNSUPPORTED;
   if (!(scale == scale) || std::isinf(scale)) return BSA_ERR_INVALID_ARG;
-  AttnLayout l;  // (the same limits on sizes)
+  AttnLayout l;  // (the same limits on sizes; and the line of tiles of 16 keys is 32-bit)
   if ((st = attn_layout(p.c, B, Hq, nq, NKB, bk, mask != nullptr, &l)) != BSA_OK) return st;
+  if ((double)B * ((double)p.c.max_pages * p.c.page / 16 + 32) >= 2147483648.0) return BSA_ERR_UNSUPPORTED;
   if (!seqs && B > p.c.max_seqs) return BSA_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   if ((st = check_device(&dev)) != BSA_OK || (st = sms_of(dev, &sms)) != BSA_OK) return st;

@@ -32,7 +32,6 @@ namespace {
 
 using namespace dev;
 
-constexpr int kSelectThreads = 1024;
 constexpr int kDigit = 11;
 constexpr int kBins = 1 << kDigit;
 
@@ -74,16 +73,33 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr, int rank) {
   return v;
 }
 
+__device__ __forceinline__ int2 ld_cluster2(uint32_t addr, int rank) {
+  uint32_t at;
+  int2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+
 // Tokens of a CTA whose weights are held in shared memory: two sizes, the smaller one
 // lets two CTAs share an SM.
 constexpr int kHeldSmall = 12288, kHeldLarge = 49152;
+constexpr int kList = 128;        // tokens of a bin that are ranked one against another
+// Tokens of a CTA on its own for which 512 threads do (fewer warps meet sooner; 32
+// sequences of 2304 tokens, 8 heads: 256, 512, 1024 threads 78, 67, 80 us in all).
+constexpr int kFewTokens = 12288;
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ CacheEvictParams p, int cluster,
+template <int kSelectThreads>
+__global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_select_kernel(const __grid_constant__ CacheEvictParams p, int cluster,
                                                                       int hold) {
+  constexpr int kWarps = kSelectThreads / 32, kMine = kBins / kSelectThreads;  // bins of a thread
   extern __shared__ float s_w[];  // [hold]
   __shared__ int s_hist[2][kBins];  // the digits in turn: others may still read the last one's
   __shared__ int s_warp[2][33];
-  __shared__ int s_pick[2];
+  __shared__ int s_pick[3];         // bin, how many of it are to be taken, how many there are
+  __shared__ uint2 s_list[kList];   // keys and places of a bin's tokens, all CTAs'
+  __shared__ uint2 s_other[kList];
+  __shared__ int s_listed;
   __shared__ int s_count[2];        // tokens of this CTA that stay in any case, that tie
   const CacheDev& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -115,7 +131,19 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   const int n = cuts ? x.have : 0, k = x.want;
   const int share = ((n + cluster - 1) / cluster + 31) & ~31, first = min(n, rank * share), count = min(n, first + share) - first;
   const float* w = p.weights + ((size_t)(good ? x.seq : 0) * c.Hkv + h) * p.stride + first;
-  for (int j = tid; j < min(count, hold); j += kSelectThreads) s_w[j] = load_written(w + j);
+  const int r = min(p.recent, k), s = min(p.sink, k - r), need = cuts ? k - r - s : 0;
+  // Candidates of this CTA: [lo, hi) of its tokens; the others stay.
+  const int lo = min(max(s - first, 0), count), hi = max(min(n - r - first, count), lo);
+  for (int q = tid; q < kBins; q += kSelectThreads) s_hist[0][q] = 0;
+  if (tid == 0) s_listed = 0;
+  __syncthreads();
+  // Weights into shared memory, and the first digit's histogram.
+#pragma unroll 4
+  for (int j = tid; j < count; j += kSelectThreads) {
+    const float v = load_written(w + j);
+    if (j < hold) s_w[j] = v;
+    if (j >= lo && j < hi) atomicAdd(&s_hist[0][order_key(v) >> (32 - kDigit)], 1);
+  }
   int detail = i;
   const int wrong = __syncthreads_or((twice ? 1 : 0) | (missing ? 2 : 0) | (shared ? 4 : 0));  // (zero or not)
   if (wrong) {
@@ -136,9 +164,6 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     return;
   }
   auto weight = [&](int j) { return j < hold ? s_w[j] : load_written(w + j); };  // of token first + j
-  const int r = min(p.recent, k), s = min(p.sink, k - r), need = k - r - s;
-  // Candidates of this CTA: [lo, hi) of its tokens; the others stay.
-  const int lo = min(max(s - first, 0), count), hi = max(min(n - r - first, count), lo);
   // The key of the last of `need` candidates (larger ones are all kept), digit by
   // digit from the top: bits of the key found so far, how many of those that have
   // them are still to be taken.
@@ -148,31 +173,43 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     int turn = 0;
     for (int shift = 32 - kDigit, bits = kDigit;; turn ^= 1) {
       int* hist = s_hist[turn];
-      for (int q = tid; q < kBins; q += kSelectThreads) hist[q] = 0;
-      __syncthreads();
-      const uint32_t above = shift + bits == 32 ? 0u : ~0u << (shift + bits);
       const uint32_t digit = (1u << bits) - 1u;
-      for (int j = lo + tid; j < hi; j += kSelectThreads) {
-        const uint32_t key = order_key(weight(j));
-        if (((key ^ found) & above) == 0u) atomicAdd(&hist[key >> shift & digit], 1);
+      if (shift < 32 - kDigit) {  // (the first one's has been taken with the loads)
+        for (int q = tid; q < kBins; q += kSelectThreads) hist[q] = 0;
+        __syncthreads();
+        const uint32_t above = ~0u << (shift + bits);
+        for (int j = lo + tid; j < hi; j += kSelectThreads) {
+          const uint32_t key = order_key(weight(j));
+          if (((key ^ found) & above) == 0u) atomicAdd(&hist[key >> shift & digit], 1);
+        }
       }
-      // Sums from the top: thread t has bins kBins - 1 - 2 t and the one below.
-      int top, low;
+      // Sums from the top: thread t has the kMine bins below kBins - kMine t.
+      int mine[kMine], sum = 0;
+      const int bin0 = kBins - kMine * (tid + 1);
       if (cluster > 1) {
         cluster_arrive();
         cluster_wait();
-        const uint32_t at = smem_u32(hist + kBins - 2 - 2 * tid);
-        top = low = 0;
-        for (int q = 0; q < cluster; ++q) {
-          low += ld_cluster(at, q);
-          top += ld_cluster(at + 4, q);
+        const uint32_t at = smem_u32(hist + bin0);
+#pragma unroll
+        for (int e = 0; e < kMine; e += 2) {
+          int2 got[8];  // (all on their way at once)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) got[q] = q < cluster ? ld_cluster2(at + 4 * e, q) : make_int2(0, 0);
+          mine[e] = mine[e + 1] = 0;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            mine[e] += got[q].x;
+            mine[e + 1] += got[q].y;
+          }
         }
       } else {
         __syncthreads();
-        top = hist[kBins - 1 - 2 * tid];
-        low = hist[kBins - 2 - 2 * tid];
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) mine[e] = hist[bin0 + e];
       }
-      int inc = top + low;
+#pragma unroll
+      for (int e = 0; e < kMine; ++e) sum += mine[e];
+      int inc = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -180,29 +217,92 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
       }
       if (lane == 31) s_warp[0][warp] = inc;
       __syncthreads();
-      int before = inc - top - low;
-      {
-        const int y = s_warp[0][lane];
-        before += __reduce_add_sync(0xffffffffu, lane < warp ? y : 0);
-      }
-      if (before < left && before + top >= left) {
-        s_pick[0] = kBins - 1 - 2 * tid;
-        s_pick[1] = left - before;
-      } else if (before + top < left && before + top + low >= left) {
-        s_pick[0] = kBins - 2 - 2 * tid;
-        s_pick[1] = left - before - top;
+      int before = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[0][lane] : 0);
+      if (before < left && before + sum >= left) {  // (one thread)
+#pragma unroll
+        for (int e = kMine - 1; e >= 0; --e) {
+          if (before < left && before + mine[e] >= left) {
+            s_pick[0] = bin0 + e;
+            s_pick[1] = left - before;
+            s_pick[2] = mine[e];
+          }
+          before += mine[e];
+        }
       }
       __syncthreads();
       found |= (uint32_t)s_pick[0] << shift;
       left = s_pick[1];
       if (shift == 0) break;
+      const int members = s_pick[2];
+      if (members <= kList) {
+        // Few enough to be ranked one against another: the last to be taken is the one
+        // that left - 1 of them come before.  CTAs put theirs into each other's lists.
+        const uint32_t same = ~0u << shift;
+        for (int j = lo + tid; j < hi; j += kSelectThreads) {
+          const uint32_t key = order_key(weight(j));
+          if (((key ^ found) & same) == 0u) {
+            const int at = atomicAdd(&s_listed, 1);
+            s_list[at] = make_uint2(key, (uint32_t)(first + j));
+          }
+        }
+        if (cluster > 1) {
+          cluster_arrive();
+          cluster_wait();
+          int filled = s_listed;  // (this CTA's own lie in front)
+          const int own = filled;
+          for (int q = 0; q < cluster; ++q) {
+            if (q == rank) continue;
+            const int theirs = ld_cluster(smem_u32(&s_listed), q);
+            for (int e = tid; e < theirs; e += kSelectThreads) {
+              const int2 v = ld_cluster2(smem_u32(s_list + e), q);
+              s_other[filled - own + e] = make_uint2((uint32_t)v.x, (uint32_t)v.y);
+            }
+            filled += theirs;
+          }
+          __syncthreads();
+          for (int e = tid; e < members; e += kSelectThreads) {
+            const uint2 me = e < own ? s_list[e] : s_other[e - own];
+            int ahead = 0, equal = 0;
+            for (int o = 0; o < members; ++o) {
+              const uint2 y = o < own ? s_list[o] : s_other[o - own];
+              const bool tie = y.x == me.x && y.y < me.y;
+              ahead += y.x > me.x || tie;
+              equal += tie;
+            }
+            if (ahead == left - 1) {
+              s_pick[0] = (int)me.x;
+              s_pick[1] = equal + 1;
+            }
+          }
+        } else {
+          __syncthreads();
+          for (int e = tid; e < members; e += kSelectThreads) {
+            const uint2 me = s_list[e];
+            int ahead = 0, equal = 0;
+            for (int o = 0; o < members; ++o) {
+              const uint2 y = s_list[o];
+              const bool tie = y.x == me.x && y.y < me.y;
+              ahead += y.x > me.x || tie;
+              equal += tie;
+            }
+            if (ahead == left - 1) {
+              s_pick[0] = (int)me.x;
+              s_pick[1] = equal + 1;
+            }
+          }
+        }
+        __syncthreads();
+        found = (uint32_t)s_pick[0];
+        left = s_pick[1];
+        break;
+      }
       bits = min(kDigit, shift);
       shift -= bits;
     }
   }
   // The list: a warp goes over consecutive tokens; counts first, then places.
   // `left` tokens of the found key are kept, the first ones.
-  const int span = ((count + 31) / 32 + 31) & ~31, j0 = min(count, warp * span), j1 = min(count, j0 + span);
+  const int span = ((count + kWarps - 1) / kWarps + 31) & ~31, j0 = min(count, warp * span), j1 = min(count, j0 + span);
   auto kind_of = [&](int j, bool& stays, bool& tie) {
     stays = j < lo || j >= hi;
     tie = false;
@@ -227,7 +327,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     s_warp[1][warp] = ties;
   }
   __syncthreads();
-  const int stay_w = s_warp[0][lane], ties_w = s_warp[1][lane];
+  const int stay_w = lane < kWarps ? s_warp[0][lane] : 0, ties_w = lane < kWarps ? s_warp[1][lane] : 0;
   int at = __reduce_add_sync(0xffffffffu, lane < warp ? stay_w : 0), tied = __reduce_add_sync(0xffffffffu, lane < warp ? ties_w : 0);
   if (cluster > 1) {  // those of the CTAs ahead
     if (warp == 0) {
@@ -293,7 +393,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
 
 // ------------------------------------------------------------------ codes and scales
 constexpr int kMoveThreads = 256;
-constexpr int kMoveTokens = 256;  // of a CTA in a round: a thread finds one, 32 KB at d = 128
+constexpr int kMoveTable = 1024;  // entries of the page table in shared memory
 
 template <int D, int KIND>
 __device__ __forceinline__ uint4 recode16(uint4 x, float ratio) {
@@ -309,13 +409,16 @@ __device__ __forceinline__ uint4 recode16(uint4 x, float ratio) {
 
 template <int D, int KIND>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ CacheEvictParams p, int cluster) {
-  constexpr int kVec = kMoveTokens * D / 16 / kMoveThreads;  // 16-byte vectors of a thread
-  constexpr int kLanes = D / 16;                             // threads of a token
-  __shared__ long long s_from[kMoveTokens];  // pool rows
-  __shared__ long long s_to[kMoveTokens];
-  __shared__ float s_scale[kMoveTokens];     // of a token; 0: nothing stored
-  __shared__ uint32_t s_tops[2][kMoveTokens / 16];  // bits of the largest of a block; rounds in turn
-  __shared__ int s_moved[2][kMoveTokens / 16];      // a token of the block moves
+  constexpr int kTokens = 32768 / D;                   // of a CTA in a round: 32 KB
+  constexpr int kPer = kTokens / kMoveThreads;         // a thread looks up
+  constexpr int kVec = kTokens * D / 16 / kMoveThreads;  // 16-byte vectors of a thread
+  constexpr int kLanes = D / 16;                       // threads of a token
+  // Rounds in turn.
+  __shared__ int s_from[2][kTokens], s_to[2][kTokens];  // pool rows; -1: no token
+  __shared__ float s_scale[2][kTokens];                 // of a token; 0: nothing stored
+  __shared__ uint32_t s_top[2][kTokens / 16];           // bits of the largest of a block
+  __shared__ int s_moves[2][kTokens / 16];              // a token of the block moves
+  __shared__ int s_table[kMoveTable];
   const CacheDev& c = p.c;
   const int tid = threadIdx.x;
   const int unit = blockIdx.x / cluster, rank = blockIdx.x - unit * cluster;
@@ -323,64 +426,105 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   uint8_t* pool = x & 1 ? c.v : c.k;
   float* scales = x & 1 ? c.vs : c.ks;
   const int lpage = 31 - __clz(c.page), lsb = 31 - __clz(c.sb);
+  if (tid < 2 * (kTokens / 16)) {
+    s_top[0][tid] = 0u;
+    s_moves[0][tid] = 0;
+  }
   next_may_launch();
   wait_for_previous();
   const int k = load_written(p.cut + i);
   if (k < 0) return;  // (the whole cluster)
   const int seq = p.seqs ? load_written(p.seqs + i) : i;
-  const int32_t* table = c.table + (size_t)seq * c.max_pages;
+  const int n = load_written(c.lens + seq);
+  const int hp = (n + c.page - 1) >> lpage, wp = (k + c.page - 1) >> lpage;
+  int32_t* table = c.table + (size_t)seq * c.max_pages;
   const int32_t* kept = p.kept + ((size_t)i * c.Hkv + h) * p.keep_max;
-  const int rounds = (k + kMoveTokens * cluster - 1) / (kMoveTokens * cluster);
-  for (int round = 0; round < rounds; ++round) {
-    const int j0 = (round * cluster + rank) * kMoveTokens;
-    uint32_t* s_top = s_tops[round & 1];
-    int* s_moves = s_moved[round & 1];
-    // Where this thread's token comes from and goes to.
-    if (tid < kMoveTokens / 16) {
-      s_top[tid] = 0u;
-      s_moves[tid] = 0;
+  const int rounds = (k + kTokens * cluster - 1) / (kTokens * cluster);
+  if (rounds > 0)
+    for (int j = tid; j < min(hp, kMoveTable); j += kMoveThreads) s_table[j] = load_written(table + j);
+  // Where this thread's tokens of a round come from and go to, and their scales.
+  int src[kPer], from[kPer], to[kPer];
+  float sc[kPer];
+  auto list = [&](int round) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int j = (round * cluster + rank) * kTokens + e * kMoveThreads + tid;
+      src[e] = j < k ? load_written(kept + j) : -1;
     }
-    __syncthreads();  // (also: the last round's places are used up)
-    {
-      const int j = j0 + tid;
-      long long from = -1, to = 0;
-      float sc = 0.f;
-      if (j < k) {
-        const int src = load_written(kept + j);
-        from = ((long long)load_written(table + (src >> lpage)) * c.Hkv + h) * c.page + (src & (c.page - 1));
-        to = ((long long)load_written(table + (j >> lpage)) * c.Hkv + h) * c.page + (j & (c.page - 1));
-        sc = load_written(scales + (from >> lsb));
-        if (!(sc > 0.f && sc < INFINITY)) sc = 0.f;
-        if (sc > 0.f) atomicMax(&s_top[tid >> lsb], __float_as_uint(sc));
-        if (from != to) s_moves[tid >> lsb] = 1;
-      }
-      s_from[tid] = from;
-      s_to[tid] = to;
-      s_scale[tid] = sc;
+  };
+  auto row_of = [&](int j) {
+    const int pg = j >> lpage;
+    return ((pg < kMoveTable ? s_table[pg] : load_written(table + pg)) * c.Hkv + h) * c.page + (j & (c.page - 1));
+  };
+  auto find = [&](int round) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int j = (round * cluster + rank) * kTokens + e * kMoveThreads + tid;
+      from[e] = src[e] >= 0 ? row_of(src[e]) : -1;
+      to[e] = src[e] >= 0 ? row_of(j) : 0;
+      sc[e] = src[e] >= 0 ? load_written(scales + (from[e] >> lsb)) : 0.f;
     }
+  };
+  auto note = [&](int side) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int t = e * kMoveThreads + tid;
+      const bool stored = sc[e] > 0.f && sc[e] < INFINITY;
+      s_from[side][t] = from[e];
+      s_to[side][t] = to[e];
+      s_scale[side][t] = stored ? sc[e] : 0.f;
+      if (stored) atomicMax(&s_top[side][t >> lsb], __float_as_uint(sc[e]));
+      if (from[e] >= 0 && from[e] != to[e]) s_moves[side][t >> lsb] = 1;
+    }
+  };
+  if (rounds > 0) {
+    list(0);
     __syncthreads();
+    find(0);
+    list(1);
+    note(0);
+  }
+  for (int round = 0; round < rounds; ++round) {
+    const int side = round & 1, j0 = (round * cluster + rank) * kTokens;
+    __syncthreads();  // the round's places are there, the last one's are used up
+    if (tid < kTokens / 16) {
+      s_top[side ^ 1][tid] = 0u;
+      s_moves[side ^ 1][tid] = 0;
+    }
     uint4 v[kVec];
 #pragma unroll
     for (int q = 0; q < kVec; ++q) {
       const int t = q * (kMoveThreads / kLanes) + tid / kLanes;
       v[q] = make_uint4(0u, 0u, 0u, 0u);
-      if (s_from[t] >= 0 && s_moves[t >> lsb])
-        v[q] = load_written(reinterpret_cast<const uint4*>(pool + s_from[t] * D + 16 * (tid % kLanes)));
+      if (s_from[side][t] >= 0 && s_moves[side][t >> lsb])
+        v[q] = load_written(reinterpret_cast<const uint4*>(pool + (size_t)s_from[side][t] * D + 16 * (tid % kLanes)));
     }
-    cluster_arrive();
-    cluster_wait();
+    // (The next rounds' tokens, lists and scales lie behind every place that this one writes.)
+    find(round + 1);
+    list(round + 2);
+    if (cluster > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
 #pragma unroll
     for (int q = 0; q < kVec; ++q) {
       const int t = q * (kMoveThreads / kLanes) + tid / kLanes;
-      if (s_from[t] < 0 || !s_moves[t >> lsb]) continue;
-      const float was = s_scale[t], now = __uint_as_float(s_top[t >> lsb]);
+      if (s_from[side][t] < 0 || !s_moves[side][t >> lsb]) continue;
+      const float was = s_scale[side][t], now = __uint_as_float(s_top[side][t >> lsb]);
       uint4 y = v[q];
       if (!(was > 0.f)) y = make_uint4(0u, 0u, 0u, 0u);
       else if (was != now) y = recode16<D, KIND>(y, was / now);
-      *reinterpret_cast<uint4*>(pool + s_to[t] * D + 16 * (tid % kLanes)) = y;
+      *reinterpret_cast<uint4*>(pool + (size_t)s_to[side][t] * D + 16 * (tid % kLanes)) = y;
     }
-    if ((tid & (c.sb - 1)) == 0 && j0 + tid < k && s_moves[tid >> lsb])
-      scales[s_to[tid] >> lsb] = __uint_as_float(s_top[tid >> lsb]);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int t = e * kMoveThreads + tid;
+      if ((t & (c.sb - 1)) == 0 && j0 + t < k && s_moves[side][t >> lsb])
+        scales[s_to[side][t] >> lsb] = __uint_as_float(s_top[side][t >> lsb]);
+    }
+    note(side ^ 1);
   }
   // The last CTA of the sequence to get here: nobody reads its table any more.
   __shared__ bool s_last;
@@ -392,12 +536,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  const int n = load_written(c.lens + seq);
-  int32_t* row = c.table + (size_t)seq * c.max_pages;
-  const int hp = (n + c.page - 1) >> lpage, wp = (k + c.page - 1) >> lpage;
   for (int j = wp + tid; j < hp; j += kMoveThreads) {
-    atomicSub(c.refs + load_written(row + j), 1);
-    row[j] = -1;
+    atomicSub(c.refs + load_written(table + j), 1);
+    table[j] = -1;
   }
   __syncthreads();
   if (tid == 0) c.lens[seq] = k;
@@ -422,9 +563,9 @@ cudaError_t launch_clusters(void (*kernel)(Params...), unsigned grid, int thread
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
-// CTAs of a cluster, 1 to 8: as many as keep `places` CTAs busy.
-int cluster_of(long long units, long long places) {
-  int x = 8;
+// CTAs of a cluster, 1 to `most`: as many as keep `places` CTAs busy.
+int cluster_of(long long units, long long places, int most) {
+  int x = most;
   while (x > 1 && units * x > places) x >>= 1;
   return x;
 }
@@ -434,15 +575,21 @@ int cluster_of(long long units, long long places) {
 cudaError_t launch_cache_evict(const CacheEvictParams& p, int sms, cudaStream_t s) {
   const long long units = (long long)p.n * p.c.Hkv;
   const long long room = (long long)p.c.max_pages * p.c.page < p.stride ? (long long)p.c.max_pages * p.c.page : p.stride;
-  const int select = cluster_of(units, 2ll * sms);  // two CTAs of 1024 threads an SM
+  const int select = cluster_of(units, 2ll * sms, 8);
   const int hold = room <= (long long)select * kHeldSmall ? kHeldSmall : kHeldLarge;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldLarge * 4);
+  auto choose = [&](auto kernel, int threads) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldLarge * 4);
+    return e != cudaSuccess ? e : launch_clusters(kernel, (unsigned)(units * select), threads, select, hold * 4, s, p, select, hold);
+  };
+  cudaError_t e = select == 1 && room <= kFewTokens ? choose(evict_select_kernel<512>, 512)
+                                                    : choose(evict_select_kernel<1024>, 1024);
   if (e != cudaSuccess) return e;
-  e = launch_clusters(evict_select_kernel, (unsigned)(units * select), kSelectThreads, select, hold * 4, s, p, select, hold);
-  if (e != cudaSuccess) return e;
-  const int move = cluster_of(2 * units, 8ll * sms);  // (twice the four CTAs an SM that registers allow)
+  const int move = cluster_of(2 * units, 4ll * sms, 16);
   const unsigned grid = (unsigned)(2 * units * move);
-  auto go = [&](auto kernel) { return launch_clusters(kernel, grid, kMoveThreads, move, 0, s, p, move); };
+  auto go = [&](auto kernel) {  // (16 CTAs of this size find their places in every GPC)
+    const cudaError_t x = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return x != cudaSuccess ? x : launch_clusters(kernel, grid, kMoveThreads, move, 0, s, p, move);
+  };
   const bool i8 = p.c.kind == BSA_CACHE_INT8;
   if (p.c.d == 64) return i8 ? go(evict_move_kernel<64, BSA_CACHE_INT8>) : go(evict_move_kernel<64, BSA_CACHE_E4M3>);
   return i8 ? go(evict_move_kernel<128, BSA_CACHE_INT8>) : go(evict_move_kernel<128, BSA_CACHE_E4M3>);

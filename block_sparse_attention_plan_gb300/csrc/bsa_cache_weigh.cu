@@ -17,8 +17,8 @@
 // blocks is spread over them).  Each warp feeds itself: a ring of three tiles in shared
 // memory, filled by bulk copies of a page's rows, the next one requested as soon as a
 // tile is in registers.  The order of a row's elements in the product is free, so a
-// lane takes 16-byte vectors as they lie (at d = 128 odd rows their halves the other
-// way round: no bank conflicts).  The rows wait in shared memory, prepared once per
+// lane takes 16-byte vectors as they lie (at d = 128 with two lanes to a bank, which
+// costs less than turning halves about).  Pages, scales and weights are read a tile ahead.  The rows wait in shared memory, prepared once per
 // pair.  From 33 rows on the products are what costs (128 rows a pass, pieces are gone
 // over again for more): tiles of 16 keys, so that few tokens spread over all warps.
 #include "bsa_cache.h"
@@ -32,6 +32,8 @@ using namespace dev;
 
 constexpr int kWeighWarps = 8;
 constexpr int kWeighThreads = 32 * kWeighWarps;
+// What a pair's beginning (its rows, the first tiles' way) costs a CTA, in tiles.
+constexpr int kHead = 16;
 
 // ROWS: query rows in shared memory at a time.
 template <int D, int ROWS>
@@ -125,12 +127,16 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
       if (bad) cache_error(c.control, BSA_ERR_INVALID_ARG, b);
     }
   }
-  // This CTA's piece of the line of tiles.
+  // This CTA's piece of the line: kHead places and the tiles of every pair that has some.
   const int per = (p.B + kWeighThreads - 1) / kWeighThreads;
+  auto places_of = [&](int row) {
+    const int t = (weigh_len(p, row) + TK - 1) / TK;
+    return t > 0 ? t + kHead : 0;
+  };
   int sum = 0;
   for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < p.B) sum += (weigh_len(p, b) + TK - 1) / TK;
+    const int row = tid * per + i;
+    if (row < p.B) sum += places_of(row);
   }
   int inc = sum;
 #pragma unroll
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     if (w < warp) before += x;
     total += x;
   }
-  s_scan[tid] = before + inc - sum;  // tiles of a head ahead of this thread's rows
+  s_scan[tid] = before + inc - sum;  // places of a head ahead of this thread's rows
   __syncthreads();
   const long long line = (long long)total * c.Hkv;
   const long long lo = line * blockIdx.x / gridDim.x, hi = line * (blockIdx.x + 1) / gridDim.x;
@@ -158,29 +164,29 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
     if ((long long)s_scan[first + step] * c.Hkv <= lo) first += step;
   int b = first * per;
   long long base = (long long)s_scan[first] * c.Hkv;  // place where row b begins
-  int len = b < p.B ? weigh_len(p, b) : 0;
-  int tiles = (len + TK - 1) / TK;
-  while (base + (long long)tiles * c.Hkv <= lo) {
-    base += (long long)tiles * c.Hkv;
-    len = weigh_len(p, ++b);
-    tiles = (len + TK - 1) / TK;
+  int places = b < p.B ? places_of(b) : 0;
+  while (base + (long long)places * c.Hkv <= lo) {
+    base += (long long)places * c.Hkv;
+    places = places_of(++b);
   }
-  int h = (int)((lo - base) / tiles);
-  base += (long long)h * tiles;  // place where the pair (b, h) begins
+  int h = (int)((lo - base) / places);
+  base += (long long)h * places;  // place where the pair (b, h) begins
+  int len = weigh_len(p, b);
 
   uint32_t asked = 0, used = 0;  // tiles requested and taken by this warp
   bool gave_up = false;          // a wait of this warp ran out: it requests nothing more
   for (; base < hi;) {
     // Tiles [t0, t1) of the pair.
-    const int t0 = (int)(lo > base ? lo - base : 0), t1 = (int)(hi - base < tiles ? hi - base : tiles);
+    const long long row0 = base + kHead;
+    const int t0 = (int)(lo > row0 ? lo - row0 : 0), t1 = (int)(hi - row0 < places - kHead ? hi - row0 : places - kHead);
     const int seq = weigh_seq(p, b);
     bool twice = false;
     if (p.seqs) {
       for (int a = tid; a < b; a += kWeighThreads) twice |= load_written(p.seqs + a) == seq;
       twice = __syncthreads_or(twice);
-      if (twice && t0 == 0 && h == 0 && tid == 0) cache_error(c.control, BSA_ERR_INVALID_ARG, b);
+      if (twice && lo <= base && h == 0 && tid == 0) cache_error(c.control, BSA_ERR_INVALID_ARG, b);
     }
-    if (!twice) {
+    if (!twice && t0 < t1) {
       const int32_t* table = c.table + (size_t)seq * c.max_pages;
       float* weights = p.weights + ((size_t)seq * c.Hkv + h) * p.stride;
       const uint8_t* mask = p.mask ? p.mask + ((size_t)b * p.Hq + (size_t)h * p.g) * p.NKB : nullptr;
@@ -208,12 +214,11 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
           active = __ballot_sync(0xffffffffu, some);
         };
         look();
-        int waiting = 0;  // tiles on their way
-        // Requests the next tile into the stage after the last one's: lane g looks up
-        // group g's page, the first lane of a page's groups copies them.
-        const int run = min(c.page, TK);
-        auto request = [&]() {
-          if (gave_up) return;
+        // The tile to request next (-1: none is left) and, in lane g, the page of its
+        // group g, read a request ahead.
+        int t_next, pg_next;
+        auto advance = [&]() {
+          t_next = -1;
           while (!active) {
             t32 += 32 * kWeighWarps;
             if (t32 >= t1) return;
@@ -221,14 +226,22 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
           }
           const int x = __ffs(active) - 1;
           active &= active - 1;
-          const int t = t32 + x * kWeighWarps;
+          t_next = t32 + x * kWeighWarps;
+          const int j = t_next * TK + 16 * lane;
+          pg_next = lane < G && j < len ? load_written(table + (j >> lpage)) : -1;
+        };
+        int waiting = 0;  // tiles on their way
+        // Requests the next tile into the stage after the last one's; the first lane of a
+        // page's groups copies them.
+        const int run = min(c.page, TK);
+        auto request = [&]() {
+          if (t_next < 0 || gave_up) return;
           const uint32_t s = asked % C::kStages, bar = bars + 8 * s;
           int row = -1;
           if (lane < G) {
-            const int j = t * TK + 16 * lane;
+            const int j = t_next * TK + 16 * lane;
             if (j < len) {
-              const int pg = load_written(table + (j >> lpage));
-              if (pg >= 0 && pg < c.num_pages) row = (pg * c.Hkv + h) * c.page + (j & (c.page - 1));
+              if (pg_next >= 0 && pg_next < c.num_pages) row = (pg_next * c.Hkv + h) * c.page + (j & (c.page - 1));
               else cache_error(c.control, BSA_ERR_PLAN_MISMATCH, seq);
             }
             s_tile[s * 8 + 1 + lane] = row;
@@ -236,7 +249,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
           const bool copies = row >= 0 && ((16 * lane) & (run - 1)) == 0;
           const int parts = __popc(__ballot_sync(0xffffffffu, copies));
           if (lane == 0) {
-            s_tile[s * 8] = t;
+            s_tile[s * 8] = t_next;
             if (parts) mbar_arrive_expect_tx(bar, (uint32_t)(parts * run * D));
             else mbar_arrive(bar);
           }
@@ -245,21 +258,29 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
             bulk_load(ring + s * C::kTileBytes + (uint32_t)(16 * lane * D), c.k + (size_t)row * D, (uint32_t)(run * D), bar);
           ++asked;
           ++waiting;
+          advance();
         };
+        advance();
 #pragma unroll 1
         for (int i = 0; i < C::kStages; ++i) request();
-        // Scales of the groups of the next tile.
-        float sc_next[G];
-        auto scales = [&]() {
-          const int* e = s_tile + (used % C::kStages) * 8 + 1;
+        // Of the next tile, read a tile ahead: the scales of its groups, and the weights so far of
+        // the tokens that this lane writes (token 8 (l4 + 4 x) + r8).
+        float sc_next[G], w_next[C::kCols];
+        auto ahead = [&]() {
+          const int* e = s_tile + (used % C::kStages) * 8;
 #pragma unroll
           for (int gr = 0; gr < G; ++gr) {
-            const int row = e[gr];
+            const int row = e[1 + gr];
             sc_next[gr] = row >= 0 ? load_written(c.ks + (row >> lsb)) : 0.f;
+          }
+#pragma unroll
+          for (int x = 0; x < C::kCols; ++x) {
+            const int to = 8 * (l4 + 4 * x) + r8, j = e[0] * TK + to;
+            w_next[x] = to < TK && j < len && (m0 > 0 || j < fresh0) ? weights[j] : 0.f;
           }
         };
         __syncwarp();
-        if (waiting) scales();
+        if (waiting) ahead();
         // ------------------------------------------------------------ the rows
         __syncthreads();  // (those before them are used up)
         for (int m = warp * 8 + r8; m < ((rows + 7) & ~7); m += 8 * kWeighWarps) {
@@ -312,17 +333,57 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
           }
         }
         __syncthreads();
+        // Up to 8 rows stay in registers: this lane's elements of row r8, and what rows
+        // 2 l4 and 2 l4 + 1 are finished with.
+        uint4 rb[ROWS == 8 ? 2 * NV : 1];
+        float4 rc = make_float4(0.f, 0.f, 0.f, 0.f);
+        int2 rl = make_int2(0, 0), rh = make_int2(0, 0);
+        if constexpr (ROWS == 8) {
+#pragma unroll
+          for (int v = 0; v < 2 * NV; ++v)
+            rb[v] = *reinterpret_cast<const uint4*>(s_rows + r8 * C::kRowBytes + 32 * l4 + 128 * (v >> 1) + 16 * (v & 1));
+          rc = *reinterpret_cast<const float4*>(s_const + 4 * l4);
+          rl = *reinterpret_cast<const int2*>(s_lim + 2 * l4);
+          rh = *reinterpret_cast<const int2*>(s_head + 2 * l4);
+        }
+        // Weights of keys j0, j0 + 8 for two rows, from their products x4; their sums.
+        auto weigh2 = [&](const float (&x4)[4], float scale, const float4& cst, const int2& lim, const int2& hd, int j0,
+                          uint32_t sel, bool late, float& s0, float& s1) {
+          constexpr float kLog2e = 1.4426950408889634f;
+          const float q0 = scale * cst.x, q1 = scale * cst.z;
+          float p00 = ex2_approx(fmaf(x4[0], q0, -cst.y) * kLog2e);
+          float p01 = ex2_approx(fmaf(x4[1], q1, -cst.w) * kLog2e);
+          float p10 = ex2_approx(fmaf(x4[2], q0, -cst.y) * kLog2e);
+          float p11 = ex2_approx(fmaf(x4[3], q1, -cst.w) * kLog2e);
+          if (p.mask) {
+            bool on0, on1;
+            if (p.g <= 32) {
+              on0 = sel >> hd.x & 1u;
+              on1 = sel >> hd.y & 1u;
+            } else {
+              const int kb = j0 >> lbk;
+              on0 = kb < p.NKB && load_written(mask + (size_t)hd.x * p.NKB + kb) != 0;
+              on1 = kb < p.NKB && load_written(mask + (size_t)hd.y * p.NKB + kb) != 0;
+            }
+            if (!on0) p00 = p10 = 0.f;
+            if (!on1) p01 = p11 = 0.f;
+          }
+          if (late) {  // (also keys past the length: their sums are not stored)
+            if (j0 > lim.x) p00 = 0.f;
+            if (j0 > lim.y) p01 = 0.f;
+            if (j0 + 8 > lim.x) p10 = 0.f;
+            if (j0 + 8 > lim.y) p11 = 0.f;
+          }
+          s0 += p00 + p01;
+          s1 += p10 + p11;
+        };
         // ------------------------------------------------------------ the tiles
         for (; waiting; --waiting) {
           const uint32_t s = used % C::kStages;
           const int key0 = s_tile[s * 8] * TK;
-          // Weights so far of the tokens that this lane writes: token 8 (l4 + 4 x) + r8.
           float w[C::kCols];
 #pragma unroll
-          for (int x = 0; x < C::kCols; ++x) {
-            const int to = 8 * (l4 + 4 * x) + r8, j = key0 + to;
-            w[x] = to < TK && j < len && (m0 > 0 || j < fresh0) ? weights[j] : 0.f;
-          }
+          for (int x = 0; x < C::kCols; ++x) w[x] = w_next[x];
           // Heads of the group that select the tile, for each 32 keys.
           uint32_t sel[C::kCols];
 #pragma unroll
@@ -347,93 +408,112 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
             const uint32_t at = ring + s * C::kTileBytes + (uint32_t)((16 * gr + r8) * D + 16 * l4);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if constexpr (NV == 2) {
-                const uint32_t o = (uint32_t)(r8 & 1) * 64u;  // (rows r8 and r8 + 8 alike)
-                const uint4 y = ld_shared_v4(at + x * 8 * D + o), z = ld_shared_v4(at + x * 8 * D + (o ^ 64u));
-                kv[gr][x][0] = o ? z : y;
-                kv[gr][x][1] = o ? y : z;
-              } else {
-                kv[gr][x][0] = ld_shared_v4(at + x * 8 * D);
-              }
+#pragma unroll
+              for (int v = 0; v < NV; ++v) kv[gr][x][v] = ld_shared_v4(at + x * 8 * D + 64 * v);
             }
           }
           ++used;
           __syncwarp();  // the stage has been read: refill it
           request();
           __syncwarp();
-          if (waiting > 1) scales();
+          if (waiting > 1) ahead();
+          // Sums of the tile's eights of keys: 2 gr and 2 gr + 1 are those of group gr.
+          float eights[2 * G];
 #pragma unroll
           for (int gr = 0; gr < G; ++gr) {
-            uint32_t a[NV][4][4];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              const uint32_t lo4[4] = {kv[gr][0][v].x, kv[gr][0][v].y, kv[gr][0][v].z, kv[gr][0][v].w};
-              const uint32_t hi4[4] = {kv[gr][1][v].x, kv[gr][1][v].y, kv[gr][1][v].z, kv[gr][1][v].w};
-#pragma unroll
-              for (int s4 = 0; s4 < 4; ++s4) {
-                const uint2 x = codes_to_half4<KIND>(lo4[s4]), y = codes_to_half4<KIND>(hi4[s4]);
-                a[v][s4][0] = x.x;
-                a[v][s4][1] = y.x;
-                a[v][s4][2] = x.y;
-                a[v][s4][3] = y.y;
-              }
-            }
             const float scale = sc[gr];
             const int j0 = key0 + gr * 16 + r8;  // this lane's keys: j0, j0 + 8
-            const bool some = p.mask != nullptr, late = key0 + gr * 16 + 15 >= free_end;
+            const bool late = key0 + gr * 16 + 15 >= free_end;
             float acc0 = 0.f, acc1 = 0.f;
-            if (held[gr] && sel[gr / 2]) {
-#pragma unroll(ROWS > 32 ? 2 : 1)
-              for (int n = 0; n < rows; n += 8) {
-                float x4[4] = {0.f, 0.f, 0.f, 0.f};
+            // This lane's word s4 of vector v as operand registers.
+            auto operand = [&](int v, int s4, uint32_t (&a)[4]) {
+              const uint4 lo = kv[gr][0][v], hi = kv[gr][1][v];
+              const uint2 x = codes_to_half4<KIND>(s4 == 0 ? lo.x : s4 == 1 ? lo.y : s4 == 2 ? lo.z : lo.w);
+              const uint2 y = codes_to_half4<KIND>(s4 == 0 ? hi.x : s4 == 1 ? hi.y : s4 == 2 ? hi.z : hi.w);
+              a[0] = x.x;
+              a[1] = y.x;
+              a[2] = x.y;
+              a[3] = y.y;
+            };
+            if constexpr (ROWS == 8) {
+              float x4[4] = {0.f, 0.f, 0.f, 0.f}, y4[4] = {0.f, 0.f, 0.f, 0.f};  // (two chains of products)
+#pragma unroll
+              for (int v = 0; v < 2 * NV; ++v) {
+                uint32_t a[4];
+                operand(v >> 1, 2 * (v & 1), a);
+                mma16816(x4, a[0], a[1], a[2], a[3], rb[v].x, rb[v].y);
+                operand(v >> 1, 2 * (v & 1) + 1, a);
+                mma16816(y4, a[0], a[1], a[2], a[3], rb[v].z, rb[v].w);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x4[e] += y4[e];
+              weigh2(x4, scale, rc, rl, rh, j0, sel[gr / 2], late, acc0, acc1);
+              if (!held[gr]) acc0 = acc1 = 0.f;
+            } else if (held[gr] && sel[gr / 2]) {
+              uint32_t a[NV][4][4];
+#pragma unroll
+              for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int s4 = 0; s4 < 4; ++s4) operand(v, s4, a[v][s4]);
+              auto products = [&](int n, float (&x4)[4]) {
+                float y4[4] = {0.f, 0.f, 0.f, 0.f};
                 const uint8_t* br = s_rows + (n + r8) * C::kRowBytes + 32 * l4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x4[e] = 0.f;
 #pragma unroll
                 for (int v = 0; v < NV; ++v)
 #pragma unroll
                   for (int x = 0; x < 2; ++x) {
                     const uint4 bw = *reinterpret_cast<const uint4*>(br + 128 * v + 16 * x);
                     mma16816(x4, a[v][2 * x][0], a[v][2 * x][1], a[v][2 * x][2], a[v][2 * x][3], bw.x, bw.y);
-                    mma16816(x4, a[v][2 * x + 1][0], a[v][2 * x + 1][1], a[v][2 * x + 1][2], a[v][2 * x + 1][3], bw.z,
+                    mma16816(y4, a[v][2 * x + 1][0], a[v][2 * x + 1][1], a[v][2 * x + 1][2], a[v][2 * x + 1][3], bw.z,
                              bw.w);
                   }
-                const float4 cst = *reinterpret_cast<const float4*>(s_const + 2 * (n + 2 * l4));
-                constexpr float kLog2e = 1.4426950408889634f;
-                float p00 = ex2_approx(fmaf(x4[0], scale * cst.x, -cst.y) * kLog2e);
-                float p01 = ex2_approx(fmaf(x4[1], scale * cst.z, -cst.w) * kLog2e);
-                float p10 = ex2_approx(fmaf(x4[2], scale * cst.x, -cst.y) * kLog2e);
-                float p11 = ex2_approx(fmaf(x4[3], scale * cst.z, -cst.w) * kLog2e);
-                if (some) {
-                  const int h0 = s_head[n + 2 * l4], h1 = s_head[n + 2 * l4 + 1];
-                  bool on0, on1;
-                  if (p.g <= 32) {
-                    on0 = sel[gr / 2] >> h0 & 1u;
-                    on1 = sel[gr / 2] >> h1 & 1u;
-                  } else {
-                    const int kb = j0 >> lbk;
-                    on0 = kb < p.NKB && load_written(mask + (size_t)h0 * p.NKB + kb) != 0;
-                    on1 = kb < p.NKB && load_written(mask + (size_t)h1 * p.NKB + kb) != 0;
-                  }
-                  if (!on0) p00 = p10 = 0.f;
-                  if (!on1) p01 = p11 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x4[e] += y4[e];
+              };
+              if (!p.mask && !late) {  // every row sees these keys
+#pragma unroll(ROWS > 32 ? 256 / D : 1)
+                for (int n = 0; n < rows; n += 8) {
+                  float x4[4];
+                  products(n, x4);
+                  const float4 cst = *reinterpret_cast<const float4*>(s_const + 2 * (n + 2 * l4));
+                  constexpr float kLog2e = 1.4426950408889634f;
+                  const float q0 = scale * cst.x, q1 = scale * cst.z;
+                  acc0 += ex2_approx(fmaf(x4[0], q0, -cst.y) * kLog2e) + ex2_approx(fmaf(x4[1], q1, -cst.w) * kLog2e);
+                  acc1 += ex2_approx(fmaf(x4[2], q0, -cst.y) * kLog2e) + ex2_approx(fmaf(x4[3], q1, -cst.w) * kLog2e);
                 }
-                if (late) {  // (also keys past the length: their sums are not stored)
-                  const int2 lim = *reinterpret_cast<const int2*>(s_lim + n + 2 * l4);
-                  if (j0 > lim.x) p00 = 0.f;
-                  if (j0 > lim.y) p01 = 0.f;
-                  if (j0 + 8 > lim.x) p10 = 0.f;
-                  if (j0 + 8 > lim.y) p11 = 0.f;
+              } else {
+#pragma unroll 1
+                for (int n = 0; n < rows; n += 8) {
+                  float x4[4];
+                  products(n, x4);
+                  weigh2(x4, scale, *reinterpret_cast<const float4*>(s_const + 2 * (n + 2 * l4)),
+                         *reinterpret_cast<const int2*>(s_lim + n + 2 * l4), *reinterpret_cast<const int2*>(s_head + n + 2 * l4),
+                         j0, sel[gr / 2], late, acc0, acc1);
                 }
-                acc0 += p00 + p01;
-                acc1 += p10 + p11;
               }
-              acc0 += __shfl_xor_sync(0xffffffffu, acc0, 1);
-              acc1 += __shfl_xor_sync(0xffffffffu, acc1, 1);
-              acc0 += __shfl_xor_sync(0xffffffffu, acc0, 2);
-              acc1 += __shfl_xor_sync(0xffffffffu, acc1, 2);
             }
-            // Keys 0-7 of group gr are eight 2 gr of the tile's, keys 8-15 the next.
-            if ((2 * gr & 3) == l4) w[gr / 2] += acc0;
-            if (((2 * gr + 1) & 3) == l4) w[gr / 2] += acc1;
+            eights[2 * gr] = acc0;
+            eights[2 * gr + 1] = acc1;
+          }
+          // Over the four lanes of a key: lane l4 gets the sum of eight l4 (+ 4 x).
+          if constexpr (G == 1) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              eights[e] += __shfl_xor_sync(0xffffffffu, eights[e], 1);
+              eights[e] += __shfl_xor_sync(0xffffffffu, eights[e], 2);
+            }
+            w[0] += l4 & 1 ? eights[1] : eights[0];
+          } else {
+#pragma unroll
+            for (int x = 0; x < C::kCols; ++x) {
+              const bool odd = l4 & 1, high = l4 & 2;
+              const float* e = eights + 4 * x;
+              const float a = (odd ? e[1] : e[0]) + __shfl_xor_sync(0xffffffffu, odd ? e[0] : e[1], 1);
+              const float c2 = (odd ? e[3] : e[2]) + __shfl_xor_sync(0xffffffffu, odd ? e[2] : e[3], 1);
+              w[x] += (high ? c2 : a) + __shfl_xor_sync(0xffffffffu, high ? a : c2, 2);
+            }
           }
 #pragma unroll
           for (int x = 0; x < C::kCols; ++x) {
@@ -453,14 +533,14 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
       }
     }
     // To the next pair with tiles.
-    base += tiles;
+    base += places;
     if (++h == c.Hkv) {
       h = 0;
       do {
         if (++b >= p.B) return;
-        len = weigh_len(p, b);
-        tiles = (len + TK - 1) / TK;
-      } while (tiles == 0);
+        places = places_of(b);
+      } while (places == 0);
+      len = weigh_len(p, b);
     }
   }
 }
@@ -478,6 +558,7 @@ cudaError_t launch(const CacheWeighParams& p, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_cache_weigh(const CacheWeighParams& p, int sms, cudaStream_t s) {
+  if (p.M <= 8) return p.c.d == 64 ? launch<64, 8>(p, sms, s) : launch<128, 8>(p, sms, s);
   if (p.c.d == 64) return p.M <= 32 ? launch<64, 32>(p, sms, s) : launch<64, 128>(p, sms, s);
   return p.M <= 32 ? launch<128, 32>(p, sms, s) : launch<128, 128>(p, sms, s);
 }
