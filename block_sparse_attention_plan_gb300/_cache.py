@@ -246,10 +246,7 @@ def cache_attention(c: Cache, q: torch.Tensor, seqs: Optional[torch.Tensor] = No
             CACHE_CAUSAL if causal else 0, 0.0 if scale is None else scale)
     if handle == 0 and need <= _KEPT_BYTES:
         with _kept_lock:  # the call's kernels are enqueued one after another
-            ws = _kept.get(c._index)
-            if ws is None:
-                with torch.cuda.stream(torch.cuda.default_stream(c.device)):  # (not a given stream's caller's)
-                    ws = _kept[c._index] = torch.empty(_KEPT_BYTES, dtype=torch.uint8, device=c.device)
+            ws = _kept_scratch(c._index, c.device)
             _call(c, "attention", *args, ws.data_ptr(), need, handle)
     else:
         ws = _scratch(c, need, stream)
@@ -276,6 +273,15 @@ def _mask(c: Cache, q: torch.Tensor, mask: Optional[torch.Tensor]):
 _KEPT_BYTES = 16 << 20
 _kept = {}
 _kept_lock = threading.Lock()
+
+
+def _kept_scratch(index: int, device) -> torch.Tensor:
+    """That piece (call with the lock held)."""
+    ws = _kept.get(index)
+    if ws is None:
+        with torch.cuda.stream(torch.cuda.default_stream(device)):  # (not a given stream's caller's)
+            ws = _kept[index] = torch.empty(_KEPT_BYTES, dtype=torch.uint8, device=device)
+    return ws
 
 
 def _scratch(c: Cache, need: int, stream) -> torch.Tensor:

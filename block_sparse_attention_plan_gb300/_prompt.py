@@ -8,7 +8,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._cache import RowsC, _device, _raw_stream
+from ._cache import _KEPT_BYTES, RowsC, _device, _kept_lock, _kept_scratch, _raw_stream
 from ._lib import _check, library
 
 _ELEMENTS = {torch.bfloat16: 0, torch.float16: 1}
@@ -69,17 +69,28 @@ def _new(t: torch.Tensor, stream) -> torch.Tensor:
         return _new(t, None)
 
 
-def _rows(t: torch.Tensor):
-    """bsa_rows of a tensor [batch, heads, tokens, d] or packed [tokens, heads, d], by reference."""
-    if t.dim() == 4:
-        b, h, r, _ = t.stride()
-        nb, nh, nr, _ = t.shape
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """Memory that ``stream`` may write."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t: torch.Tensor, index: int, name: str):
+    """bsa_rows of a tensor [batch, heads, tokens, d] or packed [tokens, heads, d] on device `index`, by reference."""
+    st = t.stride()
+    if t.dtype not in _ELEMENTS or t.get_device() != index or len(st) not in (3, 4) or st[-1] != 1:
+        raise ValueError(f"{name} must be a CUDA bfloat16 or float16 tensor [B, H, T, d] or [T, H, d] with contiguous rows")
+    if len(st) == 4:
+        b, h, r, _ = st
     else:
-        r, h, _ = t.stride()
-        nr, nh, _ = t.shape
-        b, nb = 0, 1
+        r, h, _ = st
+        b = 0
     if (b | h | r) & 7:  # a dimension of one element has no stride of its own
-        b, h, r = (x if n > 1 else 0 for x, n in ((b, nb), (h, nh), (r, nr)))
+        n = t.shape
+        nb, nh, nr = n[:3] if len(st) == 4 else (1, n[1], n[0])
+        b, h, r = (x if k > 1 else 0 for x, k in ((b, nb), (h, nh), (r, nr)))
     return ctypes.byref(RowsC(t.data_ptr(), b, h, r))
 
 
@@ -124,38 +135,42 @@ def rope(r: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None, positions: 
     ``positions`` int32 [B, T]; or packed [T, H, d] with ``positions`` [T] (bsa_rope_apply).  Without positions
     they are 0 .. T-1.  ``inverse`` turns back, which also takes gradients of the outputs to those of the inputs.
     ``out_q``, ``out_k``: where the results go, q and k themselves for a call in place.  Returns (q, k) turned."""
-    dims = q.dim()
-    for name, t, o in (("q", q, out_q), ("k", k, out_k)):
-        if t is None:
-            continue
-        if t.dtype not in _ELEMENTS or t.get_device() != r._index or t.dim() not in (3, 4) or t.stride(-1) != 1:
-            raise ValueError(f"{name} must be a CUDA bfloat16 or float16 tensor [B, H, T, d] or [T, H, d] with contiguous rows")
-        if o is not None and (o.shape != t.shape or o.dtype != t.dtype or o.get_device() != r._index or o.stride(-1) != 1):
-            raise ValueError(f"out_{name} must have {name}'s shape, type and device, and contiguous rows")
-    B, T, at = (1, q.shape[0], 1) if dims == 3 else (q.shape[0], q.shape[2], 1)
-    if k is not None and (k.dim() != dims or k.dtype != q.dtype
-                          or k.shape[:at] + k.shape[at + 1:] != q.shape[:at] + q.shape[at + 1:]):
-        raise ValueError("q and k differ in more than their heads")
-    pptr = None
+    index = r._index
+    qr = _rows(q, index, "q")
+    shape = q.shape
+    if len(shape) == 3:
+        B = 1
+        T, Hq, d = shape
+        where = (T,)
+    else:
+        B, Hq, T, d = shape
+        where = (B, T)
+    kr = ko = pptr = None
+    Hk = 0
+    if k is not None:
+        kr = _rows(k, index, "k")
+        ks = k.shape
+        if len(ks) != len(shape) or k.dtype != q.dtype or ks[0] != shape[0] or ks[2:] != shape[2:]:
+            raise ValueError("q and k differ in more than their heads")
+        Hk = ks[1]
+        if out_k is None:
+            out_k = _new(k, stream)
+        elif out_k.shape != ks or out_k.dtype != k.dtype:
+            raise ValueError("out_k must have k's shape and type")
+        ko = _rows(out_k, index, "out_k")
     if positions is not None:
-        if (positions.dtype != torch.int32 or positions.get_device() != r._index or not positions.is_contiguous()
-                or tuple(positions.shape) != ((T,) if dims == 3 else (B, T))):
-            raise ValueError("positions must be a contiguous CUDA int32 tensor " + ("[T]" if dims == 3 else "[B, T]"))
+        if (positions.dtype != torch.int32 or positions.get_device() != index or not positions.is_contiguous()
+                or positions.shape != where):
+            raise ValueError("positions must be a contiguous CUDA int32 tensor " + ("[T]" if len(where) == 1 else "[B, T]"))
         pptr = positions.data_ptr()
     if out_q is None:
         out_q = _new(q, stream)
-    if k is not None and out_k is None:
-        out_k = _new(k, stream)
-    if q.numel() == 0 and (k is None or k.numel() == 0):
+    elif out_q.shape != shape or out_q.dtype != q.dtype:
+        raise ValueError("out_q must have q's shape and type")
+    if B * T * d * (Hq + Hk) == 0:
         return out_q, out_k
-    if k is None:
-        kr = ko = None
-        Hk = 0
-    else:
-        kr, ko, Hk = _rows(k), _rows(out_k), k.shape[at]
-    _call(r._index, "bsa_rope_apply", r._ref, _rows(q), _rows(out_q), q.shape[at], kr, ko, Hk, _ELEMENTS[q.dtype],
-          pptr, B, T, q.shape[-1], ROPE_INVERSE if inverse else 0,
-          _raw_stream(r._index) if stream is None else stream.cuda_stream)
+    _call(index, "bsa_rope_apply", r._ref, qr, _rows(out_q, index, "out_q"), Hq, kr, ko, Hk, _ELEMENTS[q.dtype],
+          pptr, B, T, d, ROPE_INVERSE if inverse else 0, _raw_stream(index) if stream is None else stream.cuda_stream)
     return out_q, out_k
 
 
@@ -175,38 +190,44 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets:
     None; one that is given can be asked what the kernels recorded (``prompt_status``).  Returns (O [T, Hq, d],
     LSE [T, Hq]); rows of no prompt are not written."""
     index = q.get_device()
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype not in _ELEMENTS or not t.is_cuda or t.get_device() != index or t.dim() != 3 or t.stride(2) != 1:
-            raise ValueError(f"{name} must be a CUDA bfloat16 or float16 tensor [T, H, d] with contiguous rows")
-    T, Hq, d = q.shape
-    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != d or k.dtype != q.dtype or v.dtype != q.dtype:
+    rows = [_rows(q, index, "q"), _rows(k, index, "k"), _rows(v, index, "v")]
+    shape, ks = q.shape, k.shape
+    if len(shape) != 3 or index < 0:
+        raise ValueError("q must be a CUDA tensor [T, Hq, d]")
+    T, Hq, d = shape
+    if len(ks) != 3 or ks != v.shape or ks[0] != T or ks[2] != d or k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("k and v must be [T, Hkv, d] of q's T, d and type")
     if (offsets.dtype != torch.int32 or offsets.get_device() != index or offsets.dim() != 1 or offsets.shape[0] < 2
             or not offsets.is_contiguous()):
         raise ValueError("offsets must be a contiguous CUDA int32 tensor [n + 1]")
-    n, Hkv = offsets.shape[0] - 1, k.shape[1]
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index or out.stride(2) != 1):
-        raise ValueError("out must have q's shape, type and device, and contiguous rows")
-    if lse is not None and (lse.dtype != torch.float32 or lse.get_device() != index or tuple(lse.shape) != (T, Hq)
-                            or not lse.is_contiguous()):
+    n, Hkv = offsets.shape[0] - 1, ks[1]
+    if out is None:
+        out = _new(q, stream)
+    elif out.shape != shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and type")
+    rows.append(_rows(out, index, "out"))
+    if lse is None:
+        lse = _empty((T, Hq), torch.float32, q.device, stream)
+    elif (lse.dtype != torch.float32 or lse.get_device() != index or lse.shape != (T, Hq) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous CUDA float32 tensor [T, Hq]")
     if workspace is not None and (workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     lib = _library()
-    if out is None:
-        out = _new(q, stream)
-    if lse is None or workspace is None:
-        need = int(lib.bsa_prompt_workspace_bytes(n, T, Hq, Hkv)) if workspace is None else 0
-        with torch.cuda.stream(stream):  # (None: the current one)
-            if lse is None:
-                lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-            if workspace is None:
-                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    if q.numel() == 0:
+    if T * Hq * d == 0:
         return out, lse
-    _call(index, "bsa_prompt_attention", _rows(q), _rows(k), _rows(v), _rows(out), lse.data_ptr(), _ELEMENTS[q.dtype],
-          offsets.data_ptr(), n, T, Hq, Hkv, d, PROMPT_CAUSAL if causal else 0, 0.0 if scale is None else scale,
-          workspace.data_ptr(), workspace.numel(), _raw_stream(index) if stream is None else stream.cuda_stream)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    args = (*rows, lse.data_ptr(), _ELEMENTS[q.dtype], offsets.data_ptr(), n, T, Hq, Hkv, d, PROMPT_CAUSAL if causal else 0,
+            0.0 if scale is None else scale)
+    if workspace is not None:
+        _call(index, "bsa_prompt_attention", *args, workspace.data_ptr(), workspace.numel(), handle)
+        return out, lse
+    need = lib.bsa_prompt_workspace_bytes(n, T, Hq, Hkv)
+    if handle == 0 and need <= _KEPT_BYTES:
+        with _kept_lock:  # the call's kernels are enqueued one after another
+            _call(index, "bsa_prompt_attention", *args, _kept_scratch(index, q.device).data_ptr(), need, handle)
+    else:
+        ws = _empty((max(need, 16),), torch.uint8, q.device, stream)
+        _call(index, "bsa_prompt_attention", *args, ws.data_ptr(), need, handle)
     return out, lse
 
 
