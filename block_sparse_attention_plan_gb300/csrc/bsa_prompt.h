@@ -32,6 +32,9 @@ struct RopeParams {
 
 // Attention of packed prompts (bsa_prompt_attn.cu).
 constexpr int kPromptRows = 256;   // query rows of a work item: two tiles of 128
+// Up to so many prompts of so many tokens together find their items without the
+// schedule kernel.
+constexpr int kPromptFew = 64, kPromptFewTokens = 4096;
 constexpr int kPromptCtlTiles = 3; // control word: work items of a group of heads (0-2: as a plan's)
 struct PromptParams {
   CUtensorMap tmQ;         // q as [halves][T][Hq][64], box {64, gp, 128 / gp, halves}: 128 rows, a token's heads together
@@ -48,6 +51,7 @@ struct PromptParams {
   int n, T, Hq, Hkv, g;
   int gp_shift;            // log2 of the heads of a tile
   int causal, fp16, o_v8;
+  int few;                 // no schedule: n <= kPromptFew, T <= kPromptFewTokens
   float scale_log2;
   long long watchdog_ns;
 };

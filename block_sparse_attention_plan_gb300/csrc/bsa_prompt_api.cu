@@ -110,6 +110,7 @@ bsa_status bsa_prompt_attention(const bsa_rows* q, const bsa_rows* k, const bsa_
   p.gp_shift = l.gp_shift;
   p.causal = flags & BSA_PROMPT_CAUSAL ? 1 : 0;
   p.fp16 = dtype == BSA_FP16;
+  p.few = n <= kPromptFew && T <= kPromptFewTokens ? 1 : 0;
   const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)d);
   p.scale_log2 = (float)(sc * 1.4426950408889634);
   p.watchdog_ns = watchdog_limit_ns();

@@ -5,7 +5,10 @@
 // 256 / gp tokens of gp heads that share a K/V head (gp: the largest power of two
 // in the group, at most 16).  A schedule kernel lists the items of all prompts,
 // those with the most key blocks first; the attention kernel's CTAs (one per SM) take
-// them, for one group of heads after the other, from a counter.
+// them, for one group of heads after the other, from a counter.  For few prompts of few
+// tokens the schedule kernel would be a quarter of the time: there each CTA finds its own
+// items in the line of all prompts', from its end on (a prompt's last items are its
+// longest).
 //
 // One CTA (384 threads):
 //   warp 0    takes work items, publishes them, loads both Q tiles and the K and
@@ -21,9 +24,11 @@
 //             in turns: 749.)
 //   warp 3    looks over the values of every block that some row of the item does not
 //             attend as a whole (below);
-//   warps 4-7, 8-11  the softmax of tile A and of tile B, a thread per row, with a
-//             running maximum that is moved only when a score passes it by more
-//             than kMove (then O is rescaled), and the epilogue.
+//   warps 4-7, 8-11  the softmax of tile A and of tile B, a thread per row, against a
+//             reference that is the first block's maximum and moves (O is rescaled) only when
+//             a block's weights come to more than kMost: no maximum is taken of the others, a
+//             quarter of the time from S to P, which is what the two tiles wait for.  And the
+//             epilogue.
 //
 // Tensor memory (512 columns): S_A, S_B (128 each), O_A, O_B (d each).  P takes the
 // first 64 columns of its tile's S: a warp has read its rows' scores before it writes
@@ -57,7 +62,9 @@ constexpr int kRegsSoftmax = 208;
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split");
 constexpr int kSlots = 4;                   // work items published ahead
 constexpr int kConsumers = 2 + 1 + 8;       // issuing warps, scanning warp, eight softmax warps
-constexpr float kMove = 8.f;                // log2: weights stay <= 2^(8 + kShift)
+// A block's weights of a row that sum to more than this move the row's reference: in fp16
+// none of them is past its range of 2^16 then.
+constexpr float kMost = 32768.f;
 
 enum PromptSite : int { kSitePromptOffsets = 0x60, kSiteTurn };
 
@@ -88,7 +95,8 @@ struct Cfg {
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag
   static constexpr int kOffSched = kOffMisc + 16;           // int [kSlots][8]
   static constexpr int kOffDirty = kOffSched + 32 * kSlots; // int [2 kSlots]
-  static constexpr int kSmem = kOffDirty + 8 * kSlots;
+  static constexpr int kOffPtr = kOffDirty + 8 * kSlots;    // int [kPromptFew + 1]: items ahead of each prompt
+  static constexpr int kSmem = kOffPtr + 4 * (kPromptFew + 1);
   // How often ring entry r's stage has held values before (entries alternate keys and
   // values, so with an odd number of stages a stage does).
   __device__ static __forceinline__ uint32_t uses(uint32_t r) {
@@ -152,16 +160,62 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const 
 }
 
 // ------------------------------------------------------------------ producer
+// The prompt of item e of the line: the last that begins at or before it.
+__device__ __forceinline__ int prompt_of(const int* ptr, int n, int e) {
+  int lo = 0, hi = n;  // ptr[lo] <= e < ptr[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ptr[mid] <= e) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The items ahead of each of up to kPromptFew prompts, by one warp; returns how many
+// there are (0 where the offsets do not ascend within [0, T]).
+__device__ __forceinline__ int few_items(const PromptParams& p, int* ptr) {
+  const int lane = threadIdx.x & 31, tq = kPromptRows >> p.gp_shift;
+  bool bad = false;
+  int base = 0;
+  for (int i0 = 0; i0 < p.n; i0 += 32) {
+    const int i = i0 + lane;
+    int x = 0;
+    if (i < p.n) {
+      const int a = load_written(p.offsets + i), b = load_written(p.offsets + i + 1);
+      if (a < 0 || b < a || b > p.T) bad = true;
+      else x = (b - a + tq - 1) / tq;
+    }
+    int inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (i < p.n) ptr[i] = base + inc - x;
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) ptr[p.n] = base;
+  __syncwarp();
+  bad = __any_sync(0xffffffffu, bad);
+  if (blockIdx.x == 0 && lane == 0) {  // (a wait gives up a second later at the earliest)
+    p.control[kCtlStatus] = bad ? BSA_ERR_INVALID_ARG : BSA_OK;
+    p.control[kCtlDetail] = bad ? kSitePromptOffsets : 0;
+  }
+  return bad ? 0 : base;
+}
+
 template <int D>
-__device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, const Smem<Cfg<D>> sm, const Watchdog wd) {
+__device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, const Smem<Cfg<D>> sm, const Watchdog wd,
+                                      int few) {
   using C = Cfg<D>;
   tma_prefetch_desc(&p.tmQ);
   tma_prefetch_desc(&p.tmK);
   tma_prefetch_desc(&p.tmV);
   const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
   const int units = p.Hq >> p.gp_shift, half = 128 >> p.gp_shift;
-  const int tiles = *reinterpret_cast<const volatile int32_t*>(p.control + kPromptCtlTiles);
+  const int tiles = p.few ? few : *reinterpret_cast<const volatile int32_t*>(p.control + kPromptCtlTiles);
   const int work = tiles * units;
+  const int* ptr = reinterpret_cast<const int*>(smem + C::kOffPtr);
   uint32_t q_it = 0, kv_it = 0, block = 0;
   // Blocks that the entries of the ring belong to, a byte each, the oldest lowest: entry
   // e holds keys or values until both tiles are done with that block.
@@ -171,10 +225,18 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
     const int slot = (int)(t % kSlots);
     if (!mbar_wait(sm.bar(C::kSchedEmpty + slot), ((t / kSlots) & 1u) ^ 1u, wd, kSiteSched)) break;
     Item m{-1, 0, 0, 0, 0};
-    const int it = atomicAdd(p.control + kCtlWorkCounter, 1);
+    // (few: there and back over the CTAs, so that the longest item's gets the shortest next)
+    const int it = p.few ? (int)(t * gridDim.x + (t & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x))
+                         : atomicAdd(p.control + kCtlWorkCounter, 1);
     if (it < work) {
-      const int4 e = load_written(p.tiles + it / units);
-      m = Item{it, e.x, e.y, e.z, it % units};
+      if (p.few) {
+        const int x = tiles - 1 - it / units, i = prompt_of(ptr, p.n, x);
+        const int a = load_written(p.offsets + i), b = load_written(p.offsets + i + 1);
+        m = Item{it, a, b - a, (x - ptr[i]) * (kPromptRows >> p.gp_shift), it % units};
+      } else {
+        const int4 e = load_written(p.tiles + it / units);
+        m = Item{it, e.x, e.y, e.z, it % units};
+      }
     }
     volatile int* e = reinterpret_cast<volatile int*>(smem + C::kOffSched) + slot * 8;
     e[0] = m.it;
@@ -253,6 +315,13 @@ __device__ __forceinline__ void issuer(const PromptParams& p, const uint8_t* sme
     ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, site));
     return ok;
   };
+  // A wait that polls: a suspended try_wait is about 100 cycles later.
+  auto wait_spinning = [&](uint32_t bar, uint32_t parity, int site) {
+    bool there = false;
+    for (int i = 0; i < 64 && !there; ++i) there = mbar_test_wait(bar, parity);
+    if (__all_sync(0xffffffffu, there)) return true;
+    return wait(bar, parity, site);
+  };
   auto full = [&](uint32_t r) { return wait(sm.bar(C::kFull + (int)stage(r)), (r / C::kStages) & 1u, kSiteKvFull); };
   auto issue_s = [&](int qb, uint32_t r) {
     const uint64_t qd = qd0 + (uint64_t)((uint32_t)(qb * 2) * kStep), kd = kd0 + (uint64_t)(stage(r) * kStep);
@@ -290,10 +359,12 @@ __device__ __forceinline__ void issuer(const PromptParams& p, const uint8_t* sme
       if (mine) {
         if (!wait(sm.bar(C::kClean + (int)stage(rv)), C::uses(rv) & 1u, kSiteKvFull)) break;
         if (j == 0 && oc > 0 && !wait(sm.bar(C::kOFree + x), (oc - 1) & 1u, kSiteODone)) break;
-        if (!wait(sm.bar(C::kPFull + x), pc & 1u, kSitePFull)) break;
-        ++pc;
       }
       if (!wait(sm.bar(C::kTurn + x), (turn & 1u) ^ (x ? 0u : 1u), kSiteTurn)) break;
+      if (mine) {  // (last: what the softmax has written is awaited most)
+        if (!wait_spinning(sm.bar(C::kPFull + x), pc & 1u, kSitePFull)) break;
+        ++pc;
+      }
       tc_fence_after();
       const uint64_t vd = vd0 + (uint64_t)(stage(rv) * kStep);
       if (elect_one()) {
@@ -423,9 +494,9 @@ template <int D, bool FP16>
 __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, const Smem<Cfg<D>>& sm, uint32_t tmem,
                                         const Watchdog& wd) {
   using C = Cfg<D>;
-  // fp16 weights are kept at 2^7 of their size: the largest, 2^15, is under 2^16, and
-  // what falls below fp16's range is 2^-31 of the reference.
-  constexpr float kShift = FP16 ? 7.f : 0.f;
+  // fp16 weights are kept at 2^6 of their size: 128 at the reference sum to 2^13, and what
+  // falls below fp16's range is 2^-30 of the reference.
+  constexpr float kShift = FP16 ? 6.f : 0.f;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int x = (warp - 4) >> 2, quad = warp & 3;
   const int row = quad * 32 + lane;
@@ -450,64 +521,72 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
       if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(C::kSFull + x), sc & 1u, wd, kSiteSFull))) return;
       ++sc;
       tc_fence_after();
-      uint32_t v[128];
-      tmem_ld32_at<0>(scol, v);
-      tmem_ld32_at<32>(scol + 32u, v);
-      tmem_ld32_at<64>(scol + 64u, v);
-      tmem_ld32_at<96>(scol + 96u, v);
-      tmem_wait_ld();
-      if ((j + 1) * 128 > whole) {
-        const int rel = lim - j * 128;  // the last element that counts
+      uint32_t v[128], pk[64];
+      float sum, factor = 1.f;
+      // The first block sets the reference, m.  Later ones are weighed against it as it is:
+      // only where a row's weights come to more than kMost has a score passed it by so much
+      // that it has to move, and the scores (the weights are not stored yet) are read again.
+      for (bool move = j == 0;; move = true) {
+        tmem_ld32_at<0>(scol, v);
+        tmem_ld32_at<32>(scol + 32u, v);
+        tmem_ld32_at<64>(scol + 64u, v);
+        tmem_ld32_at<96>(scol + 96u, v);
+        tmem_wait_ld();
+        if ((j + 1) * 128 > whole) {
+          const int rel = lim - j * 128;  // the last element that counts
 #pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if (e > rel) v[e] = __float_as_uint(-INFINITY);
-      }
-      float mx4[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
-#pragma unroll
-      for (int e = 8; e < 128; e += 8) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          mx4[c] = fmax3(mx4[c], __uint_as_float(v[e + 2 * c]), __uint_as_float(v[e + 2 * c + 1]));
-      }
-      const float m_new = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
-      float factor = 1.f;
-      if (j == 0) {
-        m_ref = m_new;
-      } else if (__any_sync(0xffffffffu, m_new > m_ref + kMove)) {
-        if (m_new > m_ref + kMove) {
-          factor = ex2_approx(m_ref - m_new);
-          m_ref = m_new;
+          for (int e = 0; e < 128; ++e)
+            if (e > rel) v[e] = __float_as_uint(-INFINITY);
         }
-        // (this block's scores have arrived, so the products before them are done with O)
+        if (move) {
+          float mx4[4];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(ocol + 32u * (uint32_t)c, o);
-          tmem_wait_ld();
+          for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
-          tmem_st32(ocol + 32u * (uint32_t)c, o);
+          for (int e = 8; e < 128; e += 8) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              mx4[c] = fmax3(mx4[c], __uint_as_float(v[e + 2 * c]), __uint_as_float(v[e + 2 * c + 1]));
+          }
+          const float m_new = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+          if (j == 0) {
+            m_ref = m_new;
+          } else {
+            if (m_new > m_ref) {
+              factor = ex2_approx(m_ref - m_new);
+              m_ref = m_new;
+            }
+            // (this block's scores have arrived, so the products before them are done with O)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(ocol + 32u * (uint32_t)c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+              tmem_st32(ocol + 32u * (uint32_t)c, o);
+            }
+          }
         }
-      }
-      const float mb = kShift - (m_ref == -INFINITY ? 0.f : m_ref);
-      const uint64_t mbx2 = f2_make(mb, mb);
-      uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-      uint32_t pk[64];
+        const float mb = kShift - (m_ref == -INFINITY ? 0.f : m_ref);
+        const uint64_t mbx2 = f2_make(mb, mb);
+        uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-      for (int e = 0; e < 64; ++e) {
-        float x0, x1;
-        f2_split(ffma2(f2_make(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2x2, mbx2), x0, x1);
-        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-        pk[e] = FP16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-        acc2[e & 3] = fadd2(acc2[e & 3], f2_make(p0, p1));
+        for (int e = 0; e < 64; ++e) {
+          float x0, x1;
+          f2_split(ffma2(f2_make(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2x2, mbx2), x0, x1);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          pk[e] = FP16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          acc2[e & 3] = fadd2(acc2[e & 3], f2_make(p0, p1));
+        }
+        float s0, s1;
+        f2_split(fadd2(fadd2(acc2[0], acc2[1]), fadd2(acc2[2], acc2[3])), s0, s1);
+        sum = s0 + s1;
+        if (move || !__any_sync(0xffffffffu, sum > kMost || m_ref == -INFINITY)) break;
       }
       tmem_st32_at<0>(scol, pk);
       tmem_st32_at<32>(scol + 32u, pk);
-      float s0, s1;
-      f2_split(fadd2(fadd2(acc2[0], acc2[1]), fadd2(acc2[2], acc2[3])), s0, s1);
-      l = l * factor + (s0 + s1);
+      l = l * factor + sum;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -611,7 +690,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     if (!*abort_flag) {
       if (warp == 3) scanner<D, FP16>(p, smem, sm, wd, lane);
       else if (warp >= 1) issuer<D, FP16>(p, smem, sm, tmem, wd, warp - 1);
-      else if (lane == 0) producer<D>(p, smem, sm, wd);
+      else {
+        const int few = p.few ? few_items(p, reinterpret_cast<int*>(smem + C::kOffPtr)) : 0;
+        if (lane == 0) producer<D>(p, smem, sm, wd, few);
+      }
     }
   }
   __syncwarp();
@@ -695,14 +777,9 @@ __global__ void __launch_bounds__(kScheduleThreads) prompt_schedule_kernel(const
   for (int w = 0; w < 32; ++w) longest = max(longest, s_warp[w]);
   int shift = 0;
   while (((longest + 127) >> 7) >> shift >= kBuckets) ++shift;
-  // Item e of the line: its prompt (the last that begins at or before it) and bucket.
+  // Item e of the line, and its bucket.
   auto item = [&](int e, int& bucket) {
-    int lo = 0, hi = p.n;  // tile_ptr[lo] <= e < tile_ptr[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.tile_ptr[mid] <= e) lo = mid;
-      else hi = mid;
-    }
+    const int lo = prompt_of(p.tile_ptr, p.n, e);
     const int a = load_written(p.offsets + lo), len = load_written(p.offsets + lo + 1) - a;
     const int t0 = (e - p.tile_ptr[lo]) * tq;
     const int keys = p.causal ? min(len, t0 + tq) : len;
@@ -738,8 +815,10 @@ cudaError_t launch(const PromptParams& p, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_prompt(const PromptParams& p, int d, int sms, cudaStream_t s) {
-  cudaError_t e = launch_after(prompt_schedule_kernel, dim3(1), dim3(kScheduleThreads), 0, s, p);
-  if (e != cudaSuccess) return e;
+  if (!p.few) {
+    const cudaError_t e = launch_after(prompt_schedule_kernel, dim3(1), dim3(kScheduleThreads), 0, s, p);
+    if (e != cudaSuccess) return e;
+  }
   if (d == 64) return p.fp16 ? launch<64, true>(p, sms, s) : launch<64, false>(p, sms, s);
   return p.fp16 ? launch<128, true>(p, sms, s) : launch<128, false>(p, sms, s);
 }
