@@ -337,10 +337,11 @@ __device__ __forceinline__ void issuer(const PromptParams& p, const uint8_t* sme
     const int nx = __shfl_sync(0xffffffffu, blocks_of(p, got, x), 0);
     const int nb = max(nx, __shfl_sync(0xffffffffu, blocks_of(p, got, x ^ 1), 0));
     const int qb = (int)(q_it % C::kQBufs);
-    // (also where the tile has no token: a buffer is released once in each of its turns)
-    if (!wait(sm.bar(C::kQFull + qb), (q_it / C::kQBufs) & 1u, kSiteQFull)) break;
+    // (Also where the tile has no token.  A wait by parity is one for this phase only if
+    // the phase before it is known to be over: whoever waits on a barrier at all waits for
+    // each of its phases, in order.)
+    if (!wait(sm.bar(C::kQFull + qb), (q_it / C::kQBufs) & 1u, kSiteQFull) || !full(ring)) break;
     if (nx > 0) {
-      if (!full(ring)) break;
       tc_fence_after();
       if (elect_one()) {
         issue_s(qb, ring);
@@ -354,12 +355,9 @@ __device__ __forceinline__ void issuer(const PromptParams& p, const uint8_t* sme
     for (int j = 0; j < nb; ++j, ++block, ++turn) {
       const uint32_t rv = ring + 2 * (uint32_t)j + 1;
       const bool mine = j < nx, more = j + 1 < nx;
-      // (a tile without this block waits for it all the same: released in its turn)
       if (!full(rv) || (j + 1 < nb && !full(rv + 1))) break;
-      if (mine) {
-        if (!wait(sm.bar(C::kClean + (int)stage(rv)), C::uses(rv) & 1u, kSiteKvFull)) break;
-        if (j == 0 && oc > 0 && !wait(sm.bar(C::kOFree + x), (oc - 1) & 1u, kSiteODone)) break;
-      }
+      if (!wait(sm.bar(C::kClean + (int)stage(rv)), C::uses(rv) & 1u, kSiteKvFull)) break;
+      if (mine && j == 0 && oc > 0 && !wait(sm.bar(C::kOFree + x), (oc - 1) & 1u, kSiteODone)) break;
       if (!wait(sm.bar(C::kTurn + x), (turn & 1u) ^ (x ? 0u : 1u), kSiteTurn)) break;
       if (mine) {  // (last: what the softmax has written is awaited most)
         if (!wait_spinning(sm.bar(C::kPFull + x), pc & 1u, kSitePFull)) break;
@@ -416,9 +414,17 @@ __device__ __forceinline__ void scanner(const PromptParams& p, uint8_t* smem, co
     if (m.it < 0) return;
     const int nb = max(blocks_of(p, m, 0), blocks_of(p, m, 1)), first = masked_from(p, m);
     if (lane == 0) dirty[t % (2 * kSlots)] = 0;
+    auto full = [&](uint32_t r) {
+      return __all_sync(0xffffffffu,
+                        mbar_wait(sm.bar(C::kFull + (int)(r % C::kStages)), (r / C::kStages) & 1u, wd, kSiteKvFull));
+    };
+    // (The keys, too: a stage may alternate between keys and values, and a wait that
+    // skipped a phase would pass before the values are there.  Each wait comes ahead of the
+    // arrival that the stage's next use goes by.)
+    if (!full(ring)) return;
     for (int j = 0; j < nb; ++j) {
       const uint32_t r = ring + 2 * (uint32_t)j + 1, s = r % C::kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(C::kFull + (int)s), (r / C::kStages) & 1u, wd, kSiteKvFull))) return;
+      if (!full(r)) return;
       if (j >= first) {
         bool here = false;
         const uint32_t at = sm.kv(s) + (uint32_t)(lane * 16);
@@ -437,6 +443,7 @@ __device__ __forceinline__ void scanner(const PromptParams& p, uint8_t* smem, co
           if (lane == 0) dirty[t % (2 * kSlots)] = 1;
         }
       }
+      if (j + 1 < nb && !full(r + 1)) return;
       __syncwarp();
       if (lane == 0) mbar_arrive(sm.bar(C::kClean + (int)s));
     }

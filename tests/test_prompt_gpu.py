@@ -88,6 +88,27 @@ def test_long_prompts(bsa, dtype, d, Hq, Hkv):
                 assert (eo <= to).all() and (el <= tl).all(), (a, h, (eo / to).max(), (el / tl).max())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Hq,Hkv,d,lens", [(1, 1, 128, [6677, 6570, 6463, 6636]), (1, 1, 64, [5001, 4000]), (4, 1, 128, [3000] * 3),
+                                           (2, 2, 128, [129, 130, 128, 127, 1] * 20), (3, 1, 128, [20] * 40)])
+def test_cold_and_warm_inputs(bsa, dtype, Hq, Hkv, d, lens):
+    """Keys and values that come from memory, later ones now and then before earlier ones, and from L2: the same bits,
+    and no wait that runs out."""
+    T = sum(lens)
+    off = ptr(lens).cuda()
+    flush = torch.empty(400 << 20, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(bsa.prompt_workspace_bytes(len(lens), T, Hq, Hkv), dtype=torch.uint8, device="cuda")
+    for seed in range(6):
+        gen = torch.Generator("cuda").manual_seed(seed)
+        q, k, v = (torch.randn(T, h, d, device="cuda", generator=gen).to(dtype) for h in (Hq, Hkv, Hkv))
+        flush.fill_(seed)
+        a = bsa.prompt_attention(q, k, v, off, causal=seed != 3, workspace=ws)
+        assert bsa.prompt_status(ws) == (0, 0)
+        b = bsa.prompt_attention(q, k, v, off, causal=seed != 3, workspace=ws)
+        assert bsa.prompt_status(ws) == (0, 0)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.isfinite(a[0].float()).all()
+
+
 def test_many_prompts(bsa):
     """More prompts than a pass of the schedule takes, most of them empty or short."""
     rng = np.random.default_rng(0)
