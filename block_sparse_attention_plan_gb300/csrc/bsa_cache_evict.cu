@@ -347,21 +347,32 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_s
   at += min(tied, left);
   const bool held = share <= hold;  // by every CTA: weights may be written where they belong
   float* wk = p.weights + ((size_t)x.seq * c.Hkv + h) * p.stride;
-#pragma unroll 4
-  for (int j = j0 + lane; j - lane < j1; j += 32) {
-    bool a = false, b = false;
-    if (j < j1) kind_of(j, a, b);
-    const uint32_t all_b = __ballot_sync(0xffffffffu, b);
-    const uint32_t under = (1u << lane) - 1u;
-    if (b && tied + __popc(all_b & under) < left) a = true;
-    const uint32_t all_a = __ballot_sync(0xffffffffu, a);
+  auto put = [&](int j, bool a) {
+    const uint32_t all = __ballot_sync(0xffffffffu, a);
     if (a) {
-      const int to = at + __popc(all_a & under);
+      const int to = at + __popc(all & ((1u << lane) - 1u));
       kept[to] = first + j;
       if (held) wk[to] = s_w[j];
     }
-    at += __popc(all_a);
-    tied += __popc(all_b);
+    at += __popc(all);
+  };
+  if (tied >= left || tied + ties <= left) {  // none of this warp's ties are kept, or all
+    const uint32_t least = tied >= left ? found + 1u : found;
+#pragma unroll 8
+    for (int j = j0 + lane; j - lane < j1; j += 32) {
+      bool a = j < j1;
+      if (a && j >= lo && j < hi) a = need > 0 && order_key(weight(j)) >= least;
+      put(j, a);
+    }
+  } else {
+    for (int j = j0 + lane; j - lane < j1; j += 32) {
+      bool a = false, b = false;
+      if (j < j1) kind_of(j, a, b);
+      const uint32_t all_b = __ballot_sync(0xffffffffu, b);
+      if (b && tied + __popc(all_b & ((1u << lane) - 1u)) < left) a = true;
+      tied += __popc(all_b);
+      put(j, a);
+    }
   }
   // No CTA leaves while others may read its shared memory, nor (the weights' second
   // way) goes on before the list is there.
@@ -395,14 +406,31 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_s
 constexpr int kMoveThreads = 256;
 constexpr int kMoveTable = 1024;  // entries of the page table in shared memory
 
-template <int D, int KIND>
+// Codes of a block's smaller scale at its new one: rounded to nearest, ties to even.
+template <int KIND>
 __device__ __forceinline__ uint4 recode16(uint4 x, float ratio) {
   uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const uint2 hh = codes_to_half4<KIND>(w[e]);
-    const float2 a = half2_to_float2(hh.x), b = half2_to_float2(hh.y);
-    w[e] = encode2<KIND>(a.x * ratio, a.y * ratio) | encode2<KIND>(b.x * ratio, b.y * ratio) << 16;
+    if constexpr (KIND == BSA_CACHE_INT8) {
+      // A byte u under 0x4b0000 is fp32 2^23 + u; 1.5 2^23 + y holds y, rounded to a whole
+      // number, in its low byte.  ratio is at most 1: nothing to saturate.
+      const uint32_t u = w[e] ^ 0x80808080u;  // code + 128
+      float f[4];
+      f[0] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7650));
+      f[1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7651));
+      f[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7652));
+      f[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7653));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[q] = fmaf(f[q] - (8388608.f + 128.f), ratio, 12582912.f);
+      const uint32_t a = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040);
+      const uint32_t b = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040);
+      w[e] = __byte_perm(a, b, 0x5410);
+    } else {
+      const uint2 hh = codes_to_half4<KIND>(w[e]);
+      const float2 a = half2_to_float2(hh.x), b = half2_to_float2(hh.y);
+      w[e] = encode2<KIND>(a.x * ratio, a.y * ratio) | encode2<KIND>(b.x * ratio, b.y * ratio) << 16;
+    }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -515,7 +543,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
       const float was = s_scale[side][t], now = __uint_as_float(s_top[side][t >> lsb]);
       uint4 y = v[q];
       if (!(was > 0.f)) y = make_uint4(0u, 0u, 0u, 0u);
-      else if (was != now) y = recode16<D, KIND>(y, was / now);
+      else if (was != now) y = recode16<KIND>(y, was / now);
       *reinterpret_cast<uint4*>(pool + (size_t)s_to[side][t] * D + 16 * (tid % kLanes)) = y;
     }
 #pragma unroll
