@@ -4,6 +4,7 @@ CUDA kernels."""
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -77,8 +78,21 @@ def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Ten
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t: torch.Tensor, index: int, name: str):
-    """bsa_rows of a tensor [batch, heads, tokens, d] or packed [tokens, heads, d] on device `index`, by reference."""
+class _Rows(threading.local):
+    """The bsa_rows of a call: the library reads them while it is called, so a host thread has four that it fills
+    anew (building one costs a microsecond)."""
+
+    def __init__(self):
+        self.rows = [RowsC() for _ in range(4)]
+        self.refs = [ctypes.byref(r) for r in self.rows]
+
+
+_call_rows = _Rows()
+
+
+def _rows(t: torch.Tensor, index: int, name: str, slot: int):
+    """bsa_rows ``slot`` of the call: a tensor [batch, heads, tokens, d] or packed [tokens, heads, d] on device
+    `index`, by reference."""
     st = t.stride()
     if t.dtype not in _ELEMENTS or t.get_device() != index or len(st) not in (3, 4) or st[-1] != 1:
         raise ValueError(f"{name} must be a CUDA bfloat16 or float16 tensor [B, H, T, d] or [T, H, d] with contiguous rows")
@@ -91,7 +105,10 @@ def _rows(t: torch.Tensor, index: int, name: str):
         n = t.shape
         nb, nh, nr = n[:3] if len(st) == 4 else (1, n[1], n[0])
         b, h, r = (x if k > 1 else 0 for x, k in ((b, nb), (h, nh), (r, nr)))
-    return ctypes.byref(RowsC(t.data_ptr(), b, h, r))
+    c = _call_rows
+    o = c.rows[slot]
+    o.data, o.stride_b, o.stride_h, o.stride_t = t.data_ptr(), b, h, r
+    return c.refs[slot]
 
 
 class Rope:
@@ -136,7 +153,7 @@ def rope(r: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None, positions: 
     they are 0 .. T-1.  ``inverse`` turns back, which also takes gradients of the outputs to those of the inputs.
     ``out_q``, ``out_k``: where the results go, q and k themselves for a call in place.  Returns (q, k) turned."""
     index = r._index
-    qr = _rows(q, index, "q")
+    qr = _rows(q, index, "q", 0)
     shape = q.shape
     if len(shape) == 3:
         B = 1
@@ -148,7 +165,7 @@ def rope(r: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None, positions: 
     kr = ko = pptr = None
     Hk = 0
     if k is not None:
-        kr = _rows(k, index, "k")
+        kr = _rows(k, index, "k", 1)
         ks = k.shape
         if len(ks) != len(shape) or k.dtype != q.dtype or ks[0] != shape[0] or ks[2:] != shape[2:]:
             raise ValueError("q and k differ in more than their heads")
@@ -157,7 +174,7 @@ def rope(r: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None, positions: 
             out_k = _new(k, stream)
         elif out_k.shape != ks or out_k.dtype != k.dtype:
             raise ValueError("out_k must have k's shape and type")
-        ko = _rows(out_k, index, "out_k")
+        ko = _rows(out_k, index, "out_k", 2)
     if positions is not None:
         if (positions.dtype != torch.int32 or positions.get_device() != index or not positions.is_contiguous()
                 or positions.shape != where):
@@ -169,7 +186,7 @@ def rope(r: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None, positions: 
         raise ValueError("out_q must have q's shape and type")
     if B * T * d * (Hq + Hk) == 0:
         return out_q, out_k
-    _call(index, "bsa_rope_apply", r._ref, qr, _rows(out_q, index, "out_q"), Hq, kr, ko, Hk, _ELEMENTS[q.dtype],
+    _call(index, "bsa_rope_apply", r._ref, qr, _rows(out_q, index, "out_q", 3), Hq, kr, ko, Hk, _ELEMENTS[q.dtype],
           pptr, B, T, d, ROPE_INVERSE if inverse else 0, _raw_stream(index) if stream is None else stream.cuda_stream)
     return out_q, out_k
 
@@ -190,7 +207,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets:
     None; one that is given can be asked what the kernels recorded (``prompt_status``).  Returns (O [T, Hq, d],
     LSE [T, Hq]); rows of no prompt are not written."""
     index = q.get_device()
-    rows = [_rows(q, index, "q"), _rows(k, index, "k"), _rows(v, index, "v")]
+    rows = [_rows(q, index, "q", 0), _rows(k, index, "k", 1), _rows(v, index, "v", 2)]
     shape, ks = q.shape, k.shape
     if len(shape) != 3 or index < 0:
         raise ValueError("q must be a CUDA tensor [T, Hq, d]")
@@ -205,7 +222,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets:
         out = _new(q, stream)
     elif out.shape != shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and type")
-    rows.append(_rows(out, index, "out"))
+    rows.append(_rows(out, index, "out", 3))
     if lse is None:
         lse = _empty((T, Hq), torch.float32, q.device, stream)
     elif (lse.dtype != torch.float32 or lse.get_device() != index or lse.shape != (T, Hq) or not lse.is_contiguous()):

@@ -95,8 +95,8 @@ struct Cfg {
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag
   static constexpr int kOffSched = kOffMisc + 16;           // int [kSlots][8]
   static constexpr int kOffDirty = kOffSched + 32 * kSlots; // int [2 kSlots]
-  static constexpr int kOffPtr = kOffDirty + 8 * kSlots;    // int [kPromptFew + 1]: items ahead of each prompt
-  static constexpr int kSmem = kOffPtr + 4 * (kPromptFew + 1);
+  static constexpr int kOffPtr = kOffDirty + 8 * kSlots;    // int [2][kPromptFew + 1]: items ahead of each prompt, offsets
+  static constexpr int kSmem = kOffPtr + 8 * (kPromptFew + 1);
   // How often ring entry r's stage has held values before (entries alternate keys and
   // values, so with an odd number of stages a stage does).
   __device__ static __forceinline__ uint32_t uses(uint32_t r) {
@@ -121,13 +121,17 @@ struct Item {
   int t0;        // first token of the item
   int unit;      // group of gp heads
 };
-// Key blocks of tile x of an item (0: the tile has no token).
-__device__ __forceinline__ int blocks_of(const PromptParams& p, const Item& m, int x) {
+// Keys that some row of tile x of an item attends (0: the tile has no token), and blocks
+// of them.
+__device__ __forceinline__ int keys_of(const PromptParams& p, const Item& m, int x) {
   const int half = 128 >> p.gp_shift, first = m.t0 + x * half;
   if (first >= m.len) return 0;
-  const int end = p.causal ? min(m.len, first + half) : m.len;
-  return (end + 127) >> 7;
+  return p.causal ? min(m.len, first + half) : m.len;
 }
+__device__ __forceinline__ int blocks_of(const PromptParams& p, const Item& m, int x) { return (keys_of(p, m, x) + 127) >> 7; }
+// Matrix instructions of P V (16 keys each) for block j of `keys`: values behind them are
+// not read.
+__device__ __forceinline__ int steps_of(int keys, int j) { return min(8, (keys - 128 * j + 15) >> 4); }
 // The first key block that some row of the item does not attend as a whole.
 __device__ __forceinline__ int masked_from(const PromptParams& p, const Item& m) {
   return p.causal ? min((m.t0 + 1) >> 7, m.len >> 7) : m.len >> 7;
@@ -171,17 +175,19 @@ __device__ __forceinline__ int prompt_of(const int* ptr, int n, int e) {
   return lo;
 }
 
-// The items ahead of each of up to kPromptFew prompts, by one warp; returns how many
+// The items ahead of each of up to kPromptFew prompts and the offsets, by one warp; returns how many
 // there are (0 where the offsets do not ascend within [0, T]).
 __device__ __forceinline__ int few_items(const PromptParams& p, int* ptr) {
   const int lane = threadIdx.x & 31, tq = kPromptRows >> p.gp_shift;
+  int* off = ptr + kPromptFew + 1;
   bool bad = false;
   int base = 0;
   for (int i0 = 0; i0 < p.n; i0 += 32) {
     const int i = i0 + lane;
-    int x = 0;
+    int x = 0, a = 0, b = 0;
     if (i < p.n) {
-      const int a = load_written(p.offsets + i), b = load_written(p.offsets + i + 1);
+      a = load_written(p.offsets + i);
+      b = load_written(p.offsets + i + 1);
       if (a < 0 || b < a || b > p.T) bad = true;
       else x = (b - a + tq - 1) / tq;
     }
@@ -191,7 +197,11 @@ __device__ __forceinline__ int few_items(const PromptParams& p, int* ptr) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    if (i < p.n) ptr[i] = base + inc - x;
+    if (i < p.n) {
+      ptr[i] = base + inc - x;
+      off[i] = a;
+      off[i + 1] = b;  // (the next lane's own, the same)
+    }
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
   if (lane == 0) ptr[p.n] = base;
@@ -231,8 +241,8 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
     if (it < work) {
       if (p.few) {
         const int x = tiles - 1 - it / units, i = prompt_of(ptr, p.n, x);
-        const int a = load_written(p.offsets + i), b = load_written(p.offsets + i + 1);
-        m = Item{it, a, b - a, (x - ptr[i]) * (kPromptRows >> p.gp_shift), it % units};
+        const int* off = ptr + kPromptFew + 1;
+        m = Item{it, off[i], off[i + 1] - off[i], (x - ptr[i]) * (kPromptRows >> p.gp_shift), it % units};
       } else {
         const int4 e = load_written(p.tiles + it / units);
         m = Item{it, e.x, e.y, e.z, it % units};
@@ -334,7 +344,7 @@ __device__ __forceinline__ void issuer(const PromptParams& p, const uint8_t* sme
   for (uint32_t t = 0; ok; ++t) {
     const Item got = take<C>(sm, smem, t, (threadIdx.x & 31) == 0, true, wd);
     if (__shfl_sync(0xffffffffu, got.it, 0) < 0) break;
-    const int nx = __shfl_sync(0xffffffffu, blocks_of(p, got, x), 0);
+    const int keys = __shfl_sync(0xffffffffu, keys_of(p, got, x), 0), nx = (keys + 127) >> 7;
     const int nb = max(nx, __shfl_sync(0xffffffffu, blocks_of(p, got, x ^ 1), 0));
     const int qb = (int)(q_it % C::kQBufs);
     // (Also where the tile has no token.  A wait by parity is one for this phase only if
@@ -365,10 +375,15 @@ __device__ __forceinline__ void issuer(const PromptParams& p, const uint8_t* sme
       }
       tc_fence_after();
       const uint64_t vd = vd0 + (uint64_t)(stage(rv) * kStep);
+      const int steps = steps_of(keys, j);
       if (elect_one()) {
-        if (mine) {
+        if (mine && steps == 8) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
+            mma_ts(ocol, scol + 8u * (uint32_t)kk, vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+        } else if (mine) {
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk)
             mma_ts(ocol, scol + 8u * (uint32_t)kk, vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
         }
         if (more) issue_s(qb, rv + 1);
@@ -426,17 +441,23 @@ __device__ __forceinline__ void scanner(const PromptParams& p, uint8_t* smem, co
       const uint32_t r = ring + 2 * (uint32_t)j + 1, s = r % C::kStages;
       if (!full(r)) return;
       if (j >= first) {
+        // Of the rows that are read, those that every row of the item attends can stay.
         bool here = false;
-        const uint32_t at = sm.kv(s) + (uint32_t)(lane * 16);
-#pragma unroll 8
-        for (int q = 0; q < C::kTileBytes; q += 512) {
+        const int lo = p.causal ? max(0, m.t0 + 1 - 128 * j) : max(0, m.len - 128 * j);
+        const int end = 16 * steps_of(max(keys_of(p, m, 0), keys_of(p, m, 1)), j);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+        const uint32_t at = sm.kv(s) + (uint32_t)(c * C::kChunkBytes + lane * 16);
+#pragma unroll 4
+        for (int q = (lo & ~3) * 128; q < end * 128; q += 512) {
           const uint4 w = ld_shared_v4(at + q);
-          const uint32_t a = no_numbers<FP16>(w.x), b = no_numbers<FP16>(w.y), c = no_numbers<FP16>(w.z),
+          const uint32_t a = no_numbers<FP16>(w.x), b = no_numbers<FP16>(w.y), c2 = no_numbers<FP16>(w.z),
                          d = no_numbers<FP16>(w.w);
-          if (a | b | c | d) {
-            st_shared_v4(at + q, w.x & ~a, w.y & ~b, w.z & ~c, w.w & ~d);
+          if (a | b | c2 | d) {
+            st_shared_v4(at + q, w.x & ~a, w.y & ~b, w.z & ~c2, w.w & ~d);
             here = true;
           }
+        }
         }
         if (__any_sync(0xffffffffu, here)) {
           fence_proxy_async_smem();  // the product reads what was written
@@ -522,6 +543,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
     const int first = m.t0 + x * half, tok = first + (row >> p.gp_shift);
     // Last key of this row, and the key below which all rows of the tile attend.
     const int lim = p.causal ? min(tok, m.len - 1) : m.len - 1;
+    const int lim_warp = p.causal ? min(first + ((quad * 32) >> p.gp_shift), m.len - 1) : m.len - 1;  // its first row's
     const int whole = p.causal ? min(first + 1, m.len) : m.len;
     float m_ref = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
@@ -542,8 +564,12 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
         if ((j + 1) * 128 > whole) {
           const int rel = lim - j * 128;  // the last element that counts
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e > rel) v[e] = __float_as_uint(-INFINITY);
+          for (int c = 0; c < 4; ++c) {
+            if (lim_warp >= j * 128 + 32 * c + 31) continue;  // all of the warp's rows attend these
+#pragma unroll
+            for (int e = 32 * c; e < 32 * c + 32; ++e)
+              if (e > rel) v[e] = __float_as_uint(-INFINITY);
+          }
         }
         if (move) {
           float mx4[4];
