@@ -93,6 +93,7 @@ template <int kSelectThreads>
 __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_select_kernel(const __grid_constant__ CacheEvictParams p, int cluster,
                                                                       int hold) {
   constexpr int kWarps = kSelectThreads / 32, kMine = kBins / kSelectThreads;  // bins of a thread
+  constexpr bool kJoined = kSelectThreads == 1024;  // (512 threads: a CTA on its own)
   extern __shared__ float s_w[];  // [hold]
   __shared__ int s_hist[2][kBins];  // the digits in turn: others may still read the last one's
   __shared__ int s_warp[2][33];
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_s
       // Sums from the top: thread t has the kMine bins below kBins - kMine t.
       int mine[kMine], sum = 0;
       const int bin0 = kBins - kMine * (tid + 1);
-      if (cluster > 1) {
+      if (kJoined && cluster > 1) {
         cluster_arrive();
         cluster_wait();
         const uint32_t at = smem_u32(hist + bin0);
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_s
             s_list[at] = make_uint2(key, (uint32_t)(first + j));
           }
         }
-        if (cluster > 1) {
+        if (kJoined && cluster > 1) {
           cluster_arrive();
           cluster_wait();
           int filled = s_listed;  // (this CTA's own lie in front)
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_s
   __syncthreads();
   const int stay_w = lane < kWarps ? s_warp[0][lane] : 0, ties_w = lane < kWarps ? s_warp[1][lane] : 0;
   int at = __reduce_add_sync(0xffffffffu, lane < warp ? stay_w : 0), tied = __reduce_add_sync(0xffffffffu, lane < warp ? ties_w : 0);
-  if (cluster > 1) {  // those of the CTAs ahead
+  if (kJoined && cluster > 1) {  // those of the CTAs ahead
     if (warp == 0) {
       const int a = __reduce_add_sync(0xffffffffu, stay_w), b = __reduce_add_sync(0xffffffffu, ties_w);
       if (lane == 0) {
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_s
   }
   // No CTA leaves while others may read its shared memory, nor (the weights' second
   // way) goes on before the list is there.
-  if (cluster > 1) {
+  if (kJoined && cluster > 1) {
     if (!held) __threadfence();
     cluster_arrive();
     cluster_wait();
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   constexpr int kLanes = D / 16;                       // threads of a token
   // Rounds in turn.
   __shared__ int s_from[2][kTokens], s_to[2][kTokens];  // pool rows; -1: no token
-  __shared__ float s_scale[2][kTokens];                 // of a token; 0: nothing stored
+  __shared__ float s_scale[2][kTokens];                 // of a token, then over the largest; < 0: nothing stored
   __shared__ uint32_t s_top[2][kTokens / 16];           // bits of the largest of a block
   __shared__ int s_moves[2][kTokens / 16];              // a token of the block moves
   __shared__ int s_table[kMoveTable];
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
       const bool stored = sc[e] > 0.f && sc[e] < INFINITY;
       s_from[side][t] = from[e];
       s_to[side][t] = to[e];
-      s_scale[side][t] = stored ? sc[e] : 0.f;
+      s_scale[side][t] = stored ? sc[e] : -1.f;
       if (stored) atomicMax(&s_top[side][t >> lsb], __float_as_uint(sc[e]));
       if (from[e] >= 0 && from[e] != to[e]) s_moves[side][t >> lsb] = 1;
     }
@@ -527,6 +528,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
       if (s_from[side][t] >= 0 && s_moves[side][t >> lsb])
         v[q] = load_written(reinterpret_cast<const uint4*>(pool + (size_t)s_from[side][t] * D + 16 * (tid % kLanes)));
     }
+    // What becomes of a token's codes, for all threads that hold some of them.
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int t = e * kMoveThreads + tid;
+      const float was = s_scale[side][t];
+      if (was > 0.f) s_scale[side][t] = was / __uint_as_float(s_top[side][t >> lsb]);
+    }
     // (The next rounds' tokens, lists and scales lie behind every place that this one writes.)
     find(round + 1);
     list(round + 2);
@@ -540,10 +548,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     for (int q = 0; q < kVec; ++q) {
       const int t = q * (kMoveThreads / kLanes) + tid / kLanes;
       if (s_from[side][t] < 0 || !s_moves[side][t >> lsb]) continue;
-      const float was = s_scale[side][t], now = __uint_as_float(s_top[side][t >> lsb]);
+      const float ratio = s_scale[side][t];
       uint4 y = v[q];
-      if (!(was > 0.f)) y = make_uint4(0u, 0u, 0u, 0u);
-      else if (was != now) y = recode16<KIND>(y, was / now);
+      if (ratio < 0.f) y = make_uint4(0u, 0u, 0u, 0u);
+      else if (ratio != 1.f) y = recode16<KIND>(y, ratio);
       *reinterpret_cast<uint4*>(pool + (size_t)s_to[side][t] * D + 16 * (tid % kLanes)) = y;
     }
 #pragma unroll
