@@ -288,6 +288,8 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
           uint32_t w[NV][8];
           const bool real = m < rows;
           const int hd = real ? (m0 + m) / p.nq : 0, i = real ? (m0 + m) - hd * p.nq : 0;
+          // A row of no sum, and one that is none, give nothing: zeros, and e^-inf.
+          const float z = real ? load_written(p.lse + ((size_t)b * p.Hq + h * p.g + hd) * p.nq + i) : -INFINITY;
           const uint16_t* at = p.q.p + (long long)b * p.q.sb + (long long)(h * p.g + hd) * p.q.sh + (long long)i * p.q.st + 16 * l4;
           uint32_t top = 0u;
 #pragma unroll
@@ -297,6 +299,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
               x = load_written(reinterpret_cast<const uint4*>(at + 64 * v));
               y = load_written(reinterpret_cast<const uint4*>(at + 64 * v + 8));
             }
+            if (z == -INFINITY) x = y = make_uint4(0u, 0u, 0u, 0u);  // (whatever the row holds)
             const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -324,8 +327,6 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
             *reinterpret_cast<uint4*>(dst + 128 * v + 16) = make_uint4(o[4], o[5], o[6], o[7]);
           }
           if (l4 == 0) {
-            // A row that attends nothing, and one that is none, give nothing: e^-inf.
-            const float z = real ? load_written(p.lse + ((size_t)b * p.Hq + h * p.g + hd) * p.nq + i) : INFINITY;
             s_const[2 * m] = real ? p.scale * __uint_as_float((uint32_t)(e + 127) << 23) : 0.f;
             s_const[2 * m + 1] = z == -INFINITY ? INFINITY : z;
             s_lim[m] = p.causal ? len - p.nq + i : 0x7fffffff;

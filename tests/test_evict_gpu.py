@@ -188,6 +188,24 @@ def test_nan_and_infinities_stay_with_their_tokens(bsa):
     assert bad[20] and not bad[:20].any() and not bad[21:32].any() and not bad[48:].any() and (w[0, 0, 50:] == 0).all()
 
 
+@pytest.mark.parametrize("g,nq", [(4, 1), (3, 7), (8, 20)])
+def test_a_row_without_a_sum_gives_nothing_whatever_it_holds(bsa, g, nq):
+    gen = torch.Generator().manual_seed(g)
+    m = filled("e4m3", [75, 40], 2, 32, 32, 128, seed=8)
+    q = (torch.randn(2, 2 * g, nq, 128, generator=gen) * 0.2).to(torch.bfloat16)
+    lse = torch.randn(2, 2 * g, nq, generator=gen) + 3
+    lse[0, 1, -1] = lse[1, 0, 0] = lse[1, g, 0] = -math.inf
+    w0 = torch.rand(2, 2, 96, generator=gen)
+    plain = w0.cuda()
+    bsa.cache_weigh(upload(bsa, m), q.cuda(), lse.cuda(), plain, fresh=0)
+    q[0, 1, -1] = math.inf
+    q[1, 0, 0, 5] = math.nan
+    q[1, g, 0, ::2] = -math.inf
+    got = w0.cuda()
+    bsa.cache_weigh(upload(bsa, m), q.cuda(), lse.cuda(), got, fresh=0)
+    assert plain.isfinite().all() and torch.equal(plain, got)
+
+
 @pytest.mark.parametrize("kind,d", [("e4m3", 128), ("int8", 64)])
 def test_weights_of_a_batch_in_one_line(bsa, kind, d):
     """Many pairs cut over all CTAs: uneven lengths, several tiles a warp, against torch in fp64."""
