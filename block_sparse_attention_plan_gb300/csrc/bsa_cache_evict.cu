@@ -81,9 +81,8 @@ __device__ __forceinline__ int2 ld_cluster2(uint32_t addr, int rank) {
   return v;
 }
 
-// Tokens of a CTA whose weights are held in shared memory: two sizes, the smaller one
-// lets two CTAs share an SM.
-constexpr int kHeldSmall = 12288, kHeldLarge = 49152;
+// Tokens of a CTA whose weights are held in shared memory, at most.
+constexpr int kHeld = 49152;
 constexpr int kList = 128;        // tokens of a bin that are ranked one against another
 // Tokens of a CTA on its own for which 512 threads do (fewer warps meet sooner; 32
 // sequences of 2304 tokens, 8 heads: 256, 512, 1024 threads 78, 67, 80 us in all).
@@ -93,6 +92,7 @@ template <int kSelectThreads>
 __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_select_kernel(const __grid_constant__ CacheEvictParams p, int cluster,
                                                                       int hold) {
   constexpr int kWarps = kSelectThreads / 32, kMine = kBins / kSelectThreads;  // bins of a thread
+  static_assert(kMine % 2 == 0, "bins are read in pairs");
   constexpr bool kJoined = kSelectThreads == 1024;  // (512 threads: a CTA on its own)
   extern __shared__ float s_w[];  // [hold]
   __shared__ int s_hist[2][kBins];  // the digits in turn: others may still read the last one's
@@ -612,9 +612,11 @@ cudaError_t launch_cache_evict(const CacheEvictParams& p, int sms, cudaStream_t 
   const long long units = (long long)p.n * p.c.Hkv;
   const long long room = (long long)p.c.max_pages * p.c.page < p.stride ? (long long)p.c.max_pages * p.c.page : p.stride;
   const int select = cluster_of(units, 2ll * sms, 8);
-  const int hold = room <= (long long)select * kHeldSmall ? kHeldSmall : kHeldLarge;
+  // (no more than its share can be)
+  const long long share = (room + 32ll * select - 1) / (32ll * select) * 32;
+  const int hold = (int)(share < kHeld ? share : kHeld);
   auto choose = [&](auto kernel, int threads) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldLarge * 4);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4);
     return e != cudaSuccess ? e : launch_clusters(kernel, (unsigned)(units * select), threads, select, hold * 4, s, p, select, hold);
   };
   cudaError_t e = select == 1 && room <= kFewTokens ? choose(evict_select_kernel<512>, 512)
