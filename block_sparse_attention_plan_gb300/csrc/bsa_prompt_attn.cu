@@ -13,7 +13,8 @@
 // One CTA (384 threads):
 //   warp 0    takes work items, publishes them, loads both Q tiles and the K and
 //             V blocks (128 keys) into one ring, in the order they are used;
-//   warps 1, 2  issue S = Q K^T and O += P V of tile A and of tile B, in turns:
+//   warps 1, 2  issue the products.  At d = 128, where they are what takes the time:
+//             S = Q K^T and O += P V of tile A and of tile B, in turns:
 //               PV_A(j) S_A(j+1) | PV_B(j) S_B(j+1) | PV_A(j+1) ...,
 //             so that one tile's products run while the other tile's softmax does.
 //             Each has done its waiting when its turn comes, while the other's products
@@ -22,6 +23,13 @@
 //             859 us, and 953 with descriptors in one thread's registers; two without
 //             turns fall into step, products and softmax of both tiles by turns: 994;
 //             in turns: 749.)
+//             At d = 64, where a tile waits longer for its products' way (P's arrival, the
+//             issue, S's arrival: half of a block's time) than for the products: tensor
+//             memory has room for three buffers of scores, so warp 1 issues S up to three
+//             steps (A, B, A ..) ahead, warp 2 P V.  (A prompt of 8192 tokens, 32 / 8 heads of
+//             64: 258 us, 288 in turns; one warp for both: 382, a step's waits, commits and
+//             descriptors are some 1700 cycles of its instructions; blocks of 64 keys with
+//             two buffers a tile: 360; four tiles of them: 607, spilled registers.)
 //   warp 3    looks over the values of every block that some row of the item does not
 //             attend as a whole (below);
 //   warps 4-7, 8-11  the softmax of tile A and of tile B, a thread per row, against a
@@ -30,11 +38,13 @@
 //             quarter of the time from S to P, which is what the two tiles wait for.  And the
 //             epilogue.
 //
-// Tensor memory (512 columns): S_A, S_B (128 each), O_A, O_B (d each).  P takes the
+// Tensor memory (512 columns): S_A, S_B (128 each; three of them at d = 64), O_A, O_B (d
+// each).  P takes the
 // first 64 columns of its tile's S: a warp has read its rows' scores before it writes
 // their weights, and S_x(j+1) is issued behind PV_x(j), which reads them: the
-// instructions of one thread run in their order.  For the same reason the arrival of
-// S_x(j+1) tells the softmax that PV_x(j) is done with O.
+// instructions of one thread run in their order (at d = 64 S of step i + 3 waits for P V
+// of step i).  For the same reason the arrival of S_x(j+1) tells the softmax that PV_x(j) is
+// done with O (at d = 64 a softmax that rescales O waits for that).
 //
 // Keys that a row does not attend get weight 0, which keeps a score of any kind out,
 // but 0 times a value that is infinite or NaN is NaN: a later token's, or (past the
@@ -42,8 +52,9 @@
 // values are replaced by 0 in shared memory before the product, and an item that had
 // any adds them to the rows that do attend them at its end, from global memory.
 //
-// What bounds it: the tensor cores, 2 * 2 * 128 * 128 d flops a block and tile, and
-// the exponentials, 128 * 128.
+// What bounds it: the tensor cores, 2 * 2 * 128 * 128 d flops a block and tile (d = 128:
+// 72 % busy, 1680 TFLOP/s for 12007 tokens, 700 us), and the exponentials, 128 * 128, with
+// what a step costs the issuing warps (d = 64: 1065 TFLOP/s for 8192 tokens).
 #include <cstdint>
 
 #include "bsa_device.cuh"
@@ -71,24 +82,31 @@ enum PromptSite : int { kSitePromptOffsets = 0x60, kSiteTurn };
 template <int D_>
 struct Cfg {
   static constexpr int D = D_;
+  // Three buffers of scores between both tiles, one warp that fills and one that uses them
+  // (below); otherwise a buffer and a warp of its own for each tile.
+  static constexpr bool kThree = D == 64;
+  static constexpr int kAhead = kThree ? 2 : 1;      // blocks that the ring has keys ahead of values
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kChunkBytes = 128 * 128;    // 128 rows of 64 elements
-  static constexpr int kQBufs = D == 128 ? 1 : 2;  // of two tiles
+  static constexpr int kChunkBytes = 128 * 128;
+  static constexpr int kQBufs = D == 128 ? 1 : 2;  // of both tiles
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kOffKV = kQBufs * 2 * kTileBytes;
   static constexpr int kOffBar = kOffKV + kStages * kTileBytes;
   static constexpr int kQFull = 0, kQEmpty = 2;
   static constexpr int kFull = 4;
   static constexpr int kClean = kFull + kStages;
-  static constexpr int kSFull = kClean + kStages;  // [2]
-  static constexpr int kPFull = kSFull + 2;        // [2]
-  static constexpr int kOFull = kPFull + 2;        // [2]
-  static constexpr int kOFree = kOFull + 2;        // [2]
-  static constexpr int kTurn = kOFree + 2;         // [2]
   // Both tiles are done with block b (of the CTA's): its values and the next keys.
-  static constexpr int kBlocks = 8;                // more blocks than the ring's entries belong to
-  static constexpr int kDone = kTurn + 2;
-  static constexpr int kDrain = kDone + kBlocks;   // [2]
+  // kBlocks: more than the ring's entries belong to.
+  static constexpr int kBlocks = 16;
+  static constexpr int kDone = kClean + kBlocks;
+  static constexpr int kSFull = kDone + kBlocks;         // [2]; kThree: [2][3], of a tile and a buffer
+  static constexpr int kPFull = kSFull + (kThree ? 6 : 2); // [2]; kThree: [3], of a buffer
+  static constexpr int kFree = kPFull + 3;               // kThree: [3], P V is done with a buffer
+  static constexpr int kKeysIn = kFree + 3;              // kThree: [kBlocks], the keys of a block are there
+  static constexpr int kOFull = kKeysIn + (kThree ? kBlocks : 0);  // [2]
+  static constexpr int kOFree = kOFull + 2;              // [2]
+  static constexpr int kTurn = kOFree + 2;               // [2]
+  static constexpr int kDrain = kTurn + 2;               // [2]
   static constexpr int kSchedFull = kDrain + 2;
   static constexpr int kSchedEmpty = kSchedFull + kSlots;
   static constexpr int kNumBars = kSchedEmpty + kSlots;
@@ -97,13 +115,23 @@ struct Cfg {
   static constexpr int kOffDirty = kOffSched + 32 * kSlots; // int [2 kSlots]
   static constexpr int kOffPtr = kOffDirty + 8 * kSlots;    // int [2][kPromptFew + 1]: items ahead of each prompt, offsets
   static constexpr int kSmem = kOffPtr + 8 * (kPromptFew + 1);
-  // How often ring entry r's stage has held values before (entries alternate keys and
-  // values, so with an odd number of stages a stage does).
-  __device__ static __forceinline__ uint32_t uses(uint32_t r) {
-    return r / (uint32_t)(kStages % 2 ? 2 * kStages : kStages);
-  }
   static_assert(kSmem <= 232448, "shared memory");
-  static constexpr uint32_t kColS = 0, kColO = 256;  // tile x at + 128 x
+  // Tensor memory: S of tile x (kThree: buffer x) at 128 x, O of tile x at kColO + kStepO x.
+  static constexpr uint32_t kColO = kThree ? 384 : 256, kStepO = kThree ? 64 : 128;
+  // The ring holds an item's blocks (nb) in the order of their use: K_0 .. K_(kAhead - 1),
+  // then V_0, K_kAhead, V_1, K_(kAhead + 1), ...
+  __device__ static __forceinline__ int key_entry(int nb, int i) {
+    const int n0 = min(kAhead, nb);
+    return i < n0 ? i : 2 * i - n0 + 1;
+  }
+  __device__ static __forceinline__ int value_entry(int nb, int j) {
+    const int n0 = min(kAhead, nb);
+    return j < nb - n0 ? n0 + 2 * j : nb + j;
+  }
+  // Blocks of `keys` keys; matrix instructions of P V (16 keys each) for block j of them
+  // (values behind are not read).
+  __host__ __device__ static constexpr int blocks(int keys) { return (keys + 127) >> 7; }
+  __device__ static __forceinline__ int steps(int keys, int j) { return min(8, (keys - 128 * j + 15) >> 4); }
 };
 
 template <class C>
@@ -121,20 +149,19 @@ struct Item {
   int t0;        // first token of the item
   int unit;      // group of gp heads
 };
-// Keys that some row of tile x of an item attends (0: the tile has no token), and blocks
-// of them.
+// Keys that some row of tile x of an item attends (0: the tile has no token), and those
+// of the item.
 __device__ __forceinline__ int keys_of(const PromptParams& p, const Item& m, int x) {
   const int half = 128 >> p.gp_shift, first = m.t0 + x * half;
   if (first >= m.len) return 0;
   return p.causal ? min(m.len, first + half) : m.len;
 }
-__device__ __forceinline__ int blocks_of(const PromptParams& p, const Item& m, int x) { return (keys_of(p, m, x) + 127) >> 7; }
-// Matrix instructions of P V (16 keys each) for block j of `keys`: values behind them are
-// not read.
-__device__ __forceinline__ int steps_of(int keys, int j) { return min(8, (keys - 128 * j + 15) >> 4); }
-// The first key block that some row of the item does not attend as a whole.
+__device__ __forceinline__ int item_keys(const PromptParams& p, const Item& m) {
+  return p.causal ? min(m.len, m.t0 + (kPromptRows >> p.gp_shift)) : m.len;
+}
+// The first key that some row of the item does not attend.
 __device__ __forceinline__ int masked_from(const PromptParams& p, const Item& m) {
-  return p.causal ? min((m.t0 + 1) >> 7, m.len >> 7) : m.len >> 7;
+  return p.causal ? min(m.t0 + 1, m.len) : m.len;
 }
 
 template <class C>
@@ -227,9 +254,10 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
   const int work = tiles * units;
   const int* ptr = reinterpret_cast<const int*>(smem + C::kOffPtr);
   uint32_t q_it = 0, kv_it = 0, block = 0;
-  // Blocks that the entries of the ring belong to, a byte each, the oldest lowest: entry
-  // e holds keys or values until both tiles are done with that block.
+  // Blocks that the entries of the ring belong to, four bits each, the oldest lowest: an
+  // entry holds keys or values until both tiles are done with that block.
   uint64_t belongs = 0;
+  static_assert(4 * C::kStages <= 64 && C::kBlocks <= 16, "four bits");
   bool ok = true;
   for (uint32_t t = 0; ok; ++t) {
     const int slot = (int)(t % kSlots);
@@ -242,7 +270,7 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
       if (p.few) {
         const int x = tiles - 1 - it / units, i = prompt_of(ptr, p.n, x);
         const int* off = ptr + kPromptFew + 1;
-        m = Item{it, off[i], off[i + 1] - off[i], (x - ptr[i]) * (kPromptRows >> p.gp_shift), it % units};
+        m = Item{it, off[i], off[i + 1] - off[i], (x - ptr[i]) * (2 * half), it % units};
       } else {
         const int4 e = load_written(p.tiles + it / units);
         m = Item{it, e.x, e.y, e.z, it % units};
@@ -256,8 +284,8 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
     e[4] = m.unit;
     mbar_arrive(sm.bar(C::kSchedFull + slot));
     if (m.it < 0) break;
-    const int nb = max(blocks_of(p, m, 0), blocks_of(p, m, 1));
-    const bool two = blocks_of(p, m, 1) > 0;
+    const int nb = C::blocks(item_keys(p, m));
+    const bool two = m.t0 + half < m.len;
     const int h0 = m.unit << p.gp_shift, kvh = h0 / p.g;
     const int qb = (int)(q_it % C::kQBufs);
     if (!mbar_wait(sm.bar(C::kQEmpty + qb), ((q_it / C::kQBufs) & 1u) ^ 1u, wd, kSiteQEmpty)) break;
@@ -268,20 +296,23 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
     ++q_it;
     for (int j = 0; j < 2 * nb; ++j) {
       const uint32_t s = kv_it % C::kStages;
-      // Values j / 2 and the keys behind them belong to block j / 2, as do the first keys.
-      const uint32_t mine = block + (uint32_t)(j > 0 ? (j - 1) / 2 : 0);
+      // Entry j: the first keys, then values and keys in turn, then the last values.
+      const int n0 = min(C::kAhead, nb), e = j - n0, pairs = nb - n0;
+      const bool value = e >= 2 * pairs || (e >= 0 && !(e & 1));
+      const int of = e < 0 ? j : (e >= 2 * pairs ? e - pairs : (e & 1 ? n0 : 0) + (e >> 1));
+      const uint32_t mine = block + (uint32_t)(value ? of : max(0, of - 1));
       if (kv_it >= (uint32_t)C::kStages) {
-        // (blocks differ by less than 128: the low byte tells which of them it was)
-        const uint32_t was = mine - ((mine - (uint32_t)(belongs & 0xff)) & 0xffu);
+        // (blocks differ by less than 16: the low bits tell which of them it was)
+        const uint32_t was = mine - ((mine - (uint32_t)(belongs & 15)) & 15u);
         if (!mbar_wait(sm.bar(C::kDone + (int)(was % C::kBlocks)), (was / C::kBlocks) & 1u, wd, kSiteKvEmpty)) {
           ok = false;
           break;
         }
       }
-      belongs = belongs >> 8 & ~(0xffull << 8 * (C::kStages - 1)) | (uint64_t)(mine & 0xff) << 8 * (C::kStages - 1);
+      belongs = (belongs >> 4 & ~(15ull << 4 * (C::kStages - 1))) | (uint64_t)(mine & 15u) << 4 * (C::kStages - 1);
       const uint32_t full = sm.bar(C::kFull + (int)s);
       mbar_arrive_expect_tx(full, C::kTileBytes);
-      tma_load_4d(sm.kv(s), j & 1 ? &p.tmV : &p.tmK, 0, kvh, m.row0 + (j >> 1) * 128, 0, full, pol_kv);
+      tma_load_4d(sm.kv(s), value ? &p.tmV : &p.tmK, 0, kvh, m.row0 + of * 128, 0, full, pol_kv);
       ++kv_it;
     }
     block += (uint32_t)nb;
@@ -303,111 +334,238 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// The products of tile x, run by a whole warp, so that the descriptors are uniform
-// values; one lane issues.
+// What the issuing warps have in common.  A whole warp runs them, so that the descriptors
+// are uniform values; one lane issues.
 template <int D, bool FP16>
-__device__ __forceinline__ void issuer(const PromptParams& p, const uint8_t* smem, const Smem<Cfg<D>>& sm, uint32_t tmem_,
-                                       const Watchdog& wd, int x) {
+struct Products {
   using C = Cfg<D>;
-  constexpr uint32_t kIdescS = FP16 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false);
-  constexpr uint32_t kIdescO = FP16 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, true);
-  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_, 0);
-  const uint32_t scol = tmem + C::kColS + 128u * (uint32_t)x, ocol = tmem + C::kColO + 128u * (uint32_t)x;
-  const uint64_t qd0 = smem_desc_sw128(sm.q(0, x), 16, 1024);
-  const uint64_t kd0 = smem_desc_sw128(sm.kv(0), 16, 1024);
-  const uint64_t vd0 = smem_desc_sw128(sm.kv(0), C::kChunkBytes, 1024);
-  constexpr uint32_t kStep = (uint32_t)(C::kTileBytes >> 4);
-  // Items, ring entries and blocks so far; those of tile x; turns.
-  uint32_t q_it = 0, ring = 0, block = 0, pc = 0, oc = 0, turn = 0;
+  static constexpr uint32_t kIdescS = FP16 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false);
+  static constexpr uint32_t kIdescO = FP16 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, true);
+  const Smem<C>& sm;
+  const Watchdog& wd;
   bool ok = true;
-  auto stage = [](uint32_t r) { return r % (uint32_t)C::kStages; };
-  auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+
+  __device__ static __forceinline__ uint32_t stage(uint32_t r) { return r % (uint32_t)C::kStages; }
+  __device__ __forceinline__ uint64_t q(int qb, int x) const { return smem_desc_sw128(sm.q(qb, x), 16, 1024); }
+  __device__ __forceinline__ uint64_t k(uint32_t r) const { return smem_desc_sw128(sm.kv(stage(r)), 16, 1024); }
+  __device__ __forceinline__ uint64_t v(uint32_t r) const { return smem_desc_sw128(sm.kv(stage(r)), C::kChunkBytes, 1024); }
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int site) {
     ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, site));
     return ok;
-  };
-  // A wait that polls: a suspended try_wait is about 100 cycles later.
-  auto wait_spinning = [&](uint32_t bar, uint32_t parity, int site) {
+  }
+  // A wait that polls: a suspended try_wait is about 100 cycles later.  (64 polls are not
+  // always enough, 256 are: a prompt of 12007 tokens, 32 / 8 heads of 128, 701 and 692 us.)
+  __device__ __forceinline__ bool wait_spinning(uint32_t bar, uint32_t parity, int site) {
     bool there = false;
-    for (int i = 0; i < 64 && !there; ++i) there = mbar_test_wait(bar, parity);
+    for (int i = 0; i < 256 && !there; ++i) there = mbar_test_wait(bar, parity);
     if (__all_sync(0xffffffffu, there)) return true;
     return wait(bar, parity, site);
-  };
-  auto full = [&](uint32_t r) { return wait(sm.bar(C::kFull + (int)stage(r)), (r / C::kStages) & 1u, kSiteKvFull); };
-  auto issue_s = [&](int qb, uint32_t r) {
-    const uint64_t qd = qd0 + (uint64_t)((uint32_t)(qb * 2) * kStep), kd = kd0 + (uint64_t)(stage(r) * kStep);
+  }
+  __device__ __forceinline__ bool full(uint32_t r) {
+    return wait(sm.bar(C::kFull + (int)stage(r)), (r / C::kStages) & 1u, kSiteKvFull);
+  }
+  __device__ __forceinline__ bool clean(uint32_t block) {
+    return wait(sm.bar(C::kClean + (int)(block % C::kBlocks)), (block / C::kBlocks) & 1u, kSiteKvFull);
+  }
+  // By one lane:
+  __device__ static __forceinline__ void scores(uint32_t scol, uint64_t qd, uint64_t kd) {
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint64_t off = (uint64_t)(((kk / 4) * C::kChunkBytes + (kk % 4) * 32) >> 4);
       mma_ss(scol, qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
     }
-  };
-  for (uint32_t t = 0; ok; ++t) {
-    const Item got = take<C>(sm, smem, t, (threadIdx.x & 31) == 0, true, wd);
+  }
+  __device__ static __forceinline__ void values(uint32_t ocol, uint32_t pcol, uint64_t vd, int steps, bool more) {
+    if (steps == 8) {
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts(ocol, pcol + 8u * (uint32_t)kk, vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (more || kk > 0) ? 1u : 0u);
+    } else {
+#pragma unroll 1
+      for (int kk = 0; kk < steps; ++kk)
+        mma_ts(ocol, pcol + 8u * (uint32_t)kk, vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (more || kk > 0) ? 1u : 0u);
+    }
+  }
+  // Everything issued is done.
+  __device__ __forceinline__ void drain(int x) {
+    if (elect_one()) {
+      mma_commit(sm.bar(C::kDrain + x));
+      drain_wait(sm.bar(C::kDrain + x), 0, wd);
+    }
+    __syncwarp();
+  }
+};
+
+// d = 128: the products of tile x, in turns with the other's.
+template <int D, bool FP16>
+__device__ __forceinline__ void issuer(const PromptParams& p, const uint8_t* smem, const Smem<Cfg<D>>& sm, uint32_t tmem_,
+                                       const Watchdog& wd, int x) {
+  using C = Cfg<D>;
+  Products<D, FP16> w{sm, wd};
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_, 0);
+  const uint32_t scol = tmem + 128u * (uint32_t)x, ocol = tmem + C::kColO + C::kStepO * (uint32_t)x;
+  // Items, ring entries and blocks so far; blocks (P V) and items of tile x; turns.
+  uint32_t q_it = 0, ring = 0, block = 0, pc = 0, oc = 0, turn = 0;
+  while (w.ok) {
+    const Item got = take<C>(sm, smem, q_it, (threadIdx.x & 31) == 0, true, wd);
     if (__shfl_sync(0xffffffffu, got.it, 0) < 0) break;
-    const int keys = __shfl_sync(0xffffffffu, keys_of(p, got, x), 0), nx = (keys + 127) >> 7;
-    const int nb = max(nx, __shfl_sync(0xffffffffu, blocks_of(p, got, x ^ 1), 0));
+    const int nb = __shfl_sync(0xffffffffu, C::blocks(item_keys(p, got)), 0);
+    const int keys = __shfl_sync(0xffffffffu, keys_of(p, got, x), 0), nx = C::blocks(keys);
     const int qb = (int)(q_it % C::kQBufs);
+    const uint64_t qd = w.q(qb, x);
     // (Also where the tile has no token.  A wait by parity is one for this phase only if
     // the phase before it is known to be over: whoever waits on a barrier at all waits for
     // each of its phases, in order.)
-    if (!wait(sm.bar(C::kQFull + qb), (q_it / C::kQBufs) & 1u, kSiteQFull) || !full(ring)) break;
-    if (nx > 0) {
-      tc_fence_after();
-      if (elect_one()) {
-        issue_s(qb, ring);
+    if (!w.wait(sm.bar(C::kQFull + qb), (q_it / C::kQBufs) & 1u, kSiteQFull) || !w.full(ring)) break;
+    tc_fence_after();
+    if (elect_one()) {
+      if (nx > 0) {
+        w.scores(scol, qd, w.k(ring));
         mma_commit(sm.bar(C::kSFull + x));
         if (nx == 1) mma_commit(sm.bar(C::kQEmpty + qb));
+      } else {
+        mbar_arrive(sm.bar(C::kQEmpty + qb));
       }
-    } else if (elect_one()) {
-      mbar_arrive(sm.bar(C::kQEmpty + qb));
     }
     __syncwarp();
     for (int j = 0; j < nb; ++j, ++block, ++turn) {
-      const uint32_t rv = ring + 2 * (uint32_t)j + 1;
+      const uint32_t rv = ring + (uint32_t)C::value_entry(nb, j), rk = ring + (uint32_t)C::key_entry(nb, j + 1);
       const bool mine = j < nx, more = j + 1 < nx;
-      if (!full(rv) || (j + 1 < nb && !full(rv + 1))) break;
-      if (!wait(sm.bar(C::kClean + (int)stage(rv)), C::uses(rv) & 1u, kSiteKvFull)) break;
-      if (mine && j == 0 && oc > 0 && !wait(sm.bar(C::kOFree + x), (oc - 1) & 1u, kSiteODone)) break;
-      if (!wait(sm.bar(C::kTurn + x), (turn & 1u) ^ (x ? 0u : 1u), kSiteTurn)) break;
+      // (What the products take, ahead of the waits: behind the last one nothing but them.)
+      const uint64_t vd = w.v(rv), kd = w.k(rk);
+      const uint32_t done = sm.bar(C::kDone + (int)(block % C::kBlocks));
+      const int steps = C::steps(keys, j);
+      if (!w.full(rv) || (j + 1 < nb && !w.full(rk)) || !w.clean(block)) break;
+      if (mine && j == 0 && oc > 0 && !w.wait(sm.bar(C::kOFree + x), (oc - 1) & 1u, kSiteODone)) break;
+      if (!w.wait(sm.bar(C::kTurn + x), (turn & 1u) ^ (x ? 0u : 1u), kSiteTurn)) break;
       if (mine) {  // (last: what the softmax has written is awaited most)
-        if (!wait_spinning(sm.bar(C::kPFull + x), pc & 1u, kSitePFull)) break;
+        if (!w.wait_spinning(sm.bar(C::kPFull + x), pc & 1u, kSitePFull)) break;
         ++pc;
       }
       tc_fence_after();
-      const uint64_t vd = vd0 + (uint64_t)(stage(rv) * kStep);
-      const int steps = steps_of(keys, j);
       if (elect_one()) {
-        if (mine && steps == 8) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(ocol, scol + 8u * (uint32_t)kk, vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-        } else if (mine) {
-#pragma unroll 1
-          for (int kk = 0; kk < steps; ++kk)
-            mma_ts(ocol, scol + 8u * (uint32_t)kk, vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-        }
-        if (more) issue_s(qb, rv + 1);
+        if (mine) w.values(ocol, scol, vd, steps, j > 0);
+        if (more) w.scores(scol, qd, kd);
         mbar_arrive(sm.bar(C::kTurn + (x ^ 1)));
         if (mine) {
           mma_commit(sm.bar(more ? C::kSFull + x : C::kOFull + x));
-          mma_commit(sm.bar(C::kDone + (int)(block % C::kBlocks)));
+          mma_commit(done);
           if (j + 2 == nx) mma_commit(sm.bar(C::kQEmpty + qb));
         } else {
-          mbar_arrive(sm.bar(C::kDone + (int)(block % C::kBlocks)));
+          mbar_arrive(done);
         }
       }
       __syncwarp();
       if (mine && !more) ++oc;
     }
-    if (!ok) break;
     ring += 2 * (uint32_t)nb;
     ++q_it;
   }
-  if (elect_one()) {
-    mma_commit(sm.bar(C::kDrain + x));
-    drain_wait(sm.bar(C::kDrain + x), 0, wd);
+  w.drain(x);
+}
+
+// d = 64: steps go by blocks, of a block tile A's and then tile B's; step i's scores are in
+// buffer i % 3.  One warp issues S, up to three steps ahead, one P V.
+template <int D, bool FP16>
+__device__ __forceinline__ void issuer_of_scores(const PromptParams& p, const uint8_t* smem, const Smem<Cfg<D>>& sm,
+                                                 uint32_t tmem_, const Watchdog& wd) {
+  using C = Cfg<D>;
+  Products<D, FP16> w{sm, wd};
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_, 0);
+  // Items, ring entries and blocks so far; the buffer, its phase, and whether it was used before.
+  uint32_t q_it = 0, ring = 0, block = 0, s3 = 0, phase = 1;
+  bool used = false;
+  while (w.ok) {
+    const Item got = take<C>(sm, smem, q_it, (threadIdx.x & 31) == 0, true, wd);
+    if (__shfl_sync(0xffffffffu, got.it, 0) < 0) break;
+    const int nb = __shfl_sync(0xffffffffu, C::blocks(item_keys(p, got)), 0);
+    const int n0 = __shfl_sync(0xffffffffu, C::blocks(keys_of(p, got, 0)), 0);
+    const int n1 = __shfl_sync(0xffffffffu, C::blocks(keys_of(p, got, 1)), 0);
+    const int qb = (int)(q_it % C::kQBufs);
+    const uint64_t q0 = w.q(qb, 0), q1 = w.q(qb, 1);
+    if (!w.wait(sm.bar(C::kQFull + qb), (q_it / C::kQBufs) & 1u, kSiteQFull)) break;
+    for (int j = 0; j < nb && w.ok; ++j, ++block) {
+      const uint64_t kd = w.k(ring + (uint32_t)C::key_entry(nb, j));
+      if (!w.wait(sm.bar(C::kKeysIn + (int)(block % C::kBlocks)), (block / C::kBlocks) & 1u, kSiteKvFull)) break;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (j >= (x ? n1 : n0)) continue;
+        if (used && !w.wait_spinning(sm.bar(C::kFree + (int)s3), phase, kSitePFull)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          w.scores(tmem + 128u * s3, x ? q1 : q0, kd);
+          mma_commit(sm.bar(C::kSFull + 3 * x + (int)s3));
+        }
+        __syncwarp();
+        if (s3 == 2) {
+          s3 = 0;
+          phase ^= 1u;
+          used = true;
+        } else {
+          ++s3;
+        }
+      }
+      if (elect_one()) {
+        if (j > 0) mma_commit(sm.bar(C::kDone + (int)((block - 1) % C::kBlocks)));
+        if (j + 1 == nb) {
+          mma_commit(sm.bar(C::kDone + (int)(block % C::kBlocks)));
+          mma_commit(sm.bar(C::kQEmpty + qb));
+        }
+      }
+      __syncwarp();
+    }
+    ring += 2 * (uint32_t)nb;
+    ++q_it;
   }
-  __syncwarp();
+  w.drain(0);
+}
+
+template <int D, bool FP16>
+__device__ __forceinline__ void issuer_of_outputs(const PromptParams& p, const uint8_t* smem, const Smem<Cfg<D>>& sm,
+                                                  uint32_t tmem_, const Watchdog& wd) {
+  using C = Cfg<D>;
+  Products<D, FP16> w{sm, wd};
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_, 0);
+  // Items, ring entries and blocks so far; the buffer and its phase; the tiles' outputs.
+  uint32_t t = 0, ring = 0, block = 0, p3 = 0, phase = 0, oc[2] = {0, 0};
+  while (w.ok) {
+    const Item got = take<C>(sm, smem, t, (threadIdx.x & 31) == 0, true, wd);
+    if (__shfl_sync(0xffffffffu, got.it, 0) < 0) break;
+    const int nb = __shfl_sync(0xffffffffu, C::blocks(item_keys(p, got)), 0);
+    const int keys0 = __shfl_sync(0xffffffffu, keys_of(p, got, 0), 0);
+    const int keys1 = __shfl_sync(0xffffffffu, keys_of(p, got, 1), 0);
+    for (int j = 0; j < nb && w.ok; ++j, ++block) {
+      const uint64_t vd = w.v(ring + (uint32_t)C::value_entry(nb, j));
+      if (!w.clean(block)) break;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int keys = x ? keys1 : keys0, steps = C::steps(keys, j);
+        if (steps <= 0) continue;
+        const bool ends = 128 * (j + 1) >= keys;
+        if (j == 0 && oc[x] > 0 && !w.wait(sm.bar(C::kOFree + x), (oc[x] - 1) & 1u, kSiteODone)) break;
+        if (!w.wait_spinning(sm.bar(C::kPFull + (int)p3), phase, kSitePFull)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          w.values(tmem + C::kColO + C::kStepO * (uint32_t)x, tmem + 128u * p3, vd, steps, j > 0);
+          mma_commit(sm.bar(C::kFree + (int)p3));
+          if (ends) mma_commit(sm.bar(C::kOFull + x));
+        }
+        __syncwarp();
+        if (ends) ++oc[x];
+        if (p3 == 2) {
+          p3 = 0;
+          phase ^= 1u;
+        } else {
+          ++p3;
+        }
+      }
+      if (elect_one()) mma_commit(sm.bar(C::kDone + (int)(block % C::kBlocks)));
+      __syncwarp();
+    }
+    ring += 2 * (uint32_t)nb;
+    ++t;
+  }
+  w.drain(1);
 }
 
 // ------------------------------------------------------------------ values
@@ -423,11 +581,11 @@ __device__ __forceinline__ void scanner(const PromptParams& p, uint8_t* smem, co
                                         int lane) {
   using C = Cfg<D>;
   volatile int* dirty = reinterpret_cast<volatile int*>(smem + C::kOffDirty);
-  uint32_t ring = 0;
+  uint32_t ring = 0, block = 0;
   for (uint32_t t = 0;; ++t) {
     const Item m = take<C>(sm, smem, t, lane == 0, true, wd);
     if (m.it < 0) return;
-    const int nb = max(blocks_of(p, m, 0), blocks_of(p, m, 1)), first = masked_from(p, m);
+    const int keys = item_keys(p, m), nb = C::blocks(keys), from = masked_from(p, m);
     if (lane == 0) dirty[t % (2 * kSlots)] = 0;
     auto full = [&](uint32_t r) {
       return __all_sync(0xffffffffu,
@@ -436,37 +594,45 @@ __device__ __forceinline__ void scanner(const PromptParams& p, uint8_t* smem, co
     // (The keys, too: a stage may alternate between keys and values, and a wait that
     // skipped a phase would pass before the values are there.  Each wait comes ahead of the
     // arrival that the stage's next use goes by.)
-    if (!full(ring)) return;
-    for (int j = 0; j < nb; ++j) {
-      const uint32_t r = ring + 2 * (uint32_t)j + 1, s = r % C::kStages;
+    // kThree: the issuing warps go by this warp's waits, two arrivals a block.
+    const uint32_t block0 = block;
+    auto keys_in = [&](int j) {
+      if (!full(ring + (uint32_t)C::key_entry(nb, j))) return false;
+      if (C::kThree && lane == 0) mbar_arrive(sm.bar(C::kKeysIn + (int)((block0 + (uint32_t)j) % C::kBlocks)));
+      return true;
+    };
+    for (int j = 0; j < min(C::kAhead, nb); ++j)
+      if (!keys_in(j)) return;
+    for (int j = 0; j < nb; ++j, ++block) {
+      const uint32_t r = ring + (uint32_t)C::value_entry(nb, j), s = r % C::kStages;
       if (!full(r)) return;
-      if (j >= first) {
+      if ((j + 1) * 128 > from) {
         // Of the rows that are read, those that every row of the item attends can stay.
         bool here = false;
-        const int lo = p.causal ? max(0, m.t0 + 1 - 128 * j) : max(0, m.len - 128 * j);
-        const int end = 16 * steps_of(max(keys_of(p, m, 0), keys_of(p, m, 1)), j);
+        const int lo = max(0, from - 128 * j), end = 16 * C::steps(keys, j);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-        const uint32_t at = sm.kv(s) + (uint32_t)(c * C::kChunkBytes + lane * 16);
+          const uint32_t at = sm.kv(s) + (uint32_t)(c * C::kChunkBytes + lane * 16);
 #pragma unroll 4
-        for (int q = (lo & ~3) * 128; q < end * 128; q += 512) {
-          const uint4 w = ld_shared_v4(at + q);
-          const uint32_t a = no_numbers<FP16>(w.x), b = no_numbers<FP16>(w.y), c2 = no_numbers<FP16>(w.z),
-                         d = no_numbers<FP16>(w.w);
-          if (a | b | c2 | d) {
-            st_shared_v4(at + q, w.x & ~a, w.y & ~b, w.z & ~c2, w.w & ~d);
-            here = true;
+          for (int q = (lo & ~3) * 128; q < end * 128; q += 512) {
+            const uint4 x = ld_shared_v4(at + q);
+            const uint32_t a = no_numbers<FP16>(x.x), b = no_numbers<FP16>(x.y), e = no_numbers<FP16>(x.z),
+                           f = no_numbers<FP16>(x.w);
+            if (a | b | e | f) {
+              st_shared_v4(at + q, x.x & ~a, x.y & ~b, x.z & ~e, x.w & ~f);
+              here = true;
+            }
           }
-        }
         }
         if (__any_sync(0xffffffffu, here)) {
           fence_proxy_async_smem();  // the product reads what was written
           if (lane == 0) dirty[t % (2 * kSlots)] = 1;
         }
       }
-      if (j + 1 < nb && !full(r + 1)) return;
+      if (!C::kThree && j + C::kAhead < nb && !keys_in(j + C::kAhead)) return;
       __syncwarp();
-      if (lane == 0) mbar_arrive(sm.bar(C::kClean + (int)s));
+      if (lane == 0) mbar_arrive(sm.bar(C::kClean + (int)(block % C::kBlocks)));
+      if (C::kThree && j + C::kAhead < nb && !keys_in(j + C::kAhead)) return;
     }
     ring += 2 * (uint32_t)nb;
   }
@@ -482,7 +648,7 @@ __device__ __noinline__ void add_no_numbers(const PromptParams& p, const Item m,
   constexpr uint32_t kExp = FP16 ? 0x7c00u : 0x7f80u;
   const int c0 = (int)(threadIdx.x & 31) * kCols;
   const int h0 = m.unit << p.gp_shift, gp = 1 << p.gp_shift, rows = gp < 32 ? gp : 32;
-  const int end = min(m.len, tok0 + (32 >> p.gp_shift)), from = masked_from(p, m) << 7;
+  const int end = min(m.len, tok0 + (32 >> p.gp_shift)), from = masked_from(p, m) & ~127;
   const uint16_t* v = p.v + (long long)(h0 / p.g) * p.v_sh + c0;
   uint32_t seen[kCols];  // +inf 1, -inf 2, NaN 4
 #pragma unroll
@@ -529,16 +695,20 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
   const int x = (warp - 4) >> 2, quad = warp & 3;
   const int row = quad * 32 + lane;
   const uint32_t tl = (uint32_t)(quad * 32) << 16;
-  const uint32_t scol = tmem + tl + C::kColS + 128u * (uint32_t)x, ocol = tmem + tl + C::kColO + 128u * (uint32_t)x;
+  const uint32_t ocol = tmem + tl + C::kColO + C::kStepO * (uint32_t)x;
   const int half = 128 >> p.gp_shift, gp = 1 << p.gp_shift;
   const volatile int* dirty = reinterpret_cast<const volatile int*>(smem + C::kOffDirty);
   const float sl2 = p.scale_log2;
   const uint64_t sl2x2 = f2_make(sl2, sl2);
-  uint32_t sc = 0, oc = 0;
+  // Blocks and outputs of this tile; kThree: steps of both ahead of the item's, phases of the
+  // buffers' next scores.
+  uint32_t sc = 0, oc = 0, steps = 0, phases = 0;
   for (uint32_t t = 0;; ++t) {
     const Item m = take<C>(sm, smem, t, lane == 0, true, wd);
     if (m.it < 0) return;
-    const int n = blocks_of(p, m, x);
+    const int n0 = C::blocks(keys_of(p, m, 0)), n1 = C::blocks(keys_of(p, m, 1)), n = x ? n1 : n0;
+    const uint32_t base = steps;
+    steps += (uint32_t)(n0 + n1);
     if (n == 0) continue;
     const int first = m.t0 + x * half, tok = first + (row >> p.gp_shift);
     // Last key of this row, and the key below which all rows of the tile attend.
@@ -547,8 +717,17 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
     const int whole = p.causal ? min(first + 1, m.len) : m.len;
     float m_ref = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
-      if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(C::kSFull + x), sc & 1u, wd, kSiteSFull))) return;
-      ++sc;
+      // Where its scores are, and the phase that says so.
+      int buf = x, full = C::kSFull + x;
+      uint32_t parity = sc & 1u;
+      if constexpr (C::kThree) {
+        buf = (int)((base + (uint32_t)(min(n0, j + x) + min(n1, j))) % 3u);
+        full = C::kSFull + 3 * x + buf;
+        parity = phases >> buf & 1u;
+        phases ^= 1u << buf;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(full), parity, wd, kSiteSFull))) return;
+      const uint32_t scol = tmem + tl + 128u * (uint32_t)buf;
       tc_fence_after();
       uint32_t v[128], pk[64];
       float sum, factor = 1.f;
@@ -589,7 +768,13 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
               factor = ex2_approx(m_ref - m_new);
               m_ref = m_new;
             }
-            // (this block's scores have arrived, so the products before them are done with O)
+            // The products before this block's have to be done with O.  One buffer a tile: this
+            // block's scores have arrived, so they are.
+            if constexpr (C::kThree) {
+              const uint32_t i = base + (uint32_t)(min(n0, j - 1 + x) + min(n1, j - 1));
+              if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(C::kFree + (int)(i % 3u)), i / 3u & 1u, wd, kSiteODone))) return;
+            }
+            tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -623,7 +808,8 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sm.bar(C::kPFull + x));
+      if (lane == 0) mbar_arrive(sm.bar(C::kPFull + buf));
+      ++sc;
     }
     // ------------------------------------------------------------ epilogue
     if (!__all_sync(0xffffffffu, mbar_wait(sm.bar(C::kOFull + x), oc & 1u, wd, kSiteODone))) return;
@@ -682,21 +868,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     *abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(sm.bar(C::kQFull + i), 1);
-      mbar_init(sm.bar(C::kQEmpty + i), 2);
-      mbar_init(sm.bar(C::kSFull + i), 1);
-      mbar_init(sm.bar(C::kPFull + i), 4);
-      mbar_init(sm.bar(C::kOFull + i), 1);
-      mbar_init(sm.bar(C::kOFree + i), 4);
-    }
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(sm.bar(C::kFull + i), 1);
-      mbar_init(sm.bar(C::kClean + i), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
+      mbar_init(sm.bar(C::kQEmpty + i), C::kThree ? 1 : 2);
       mbar_init(sm.bar(C::kTurn + i), 1);
       mbar_init(sm.bar(C::kDrain + i), 1);
     }
-    for (int i = 0; i < C::kBlocks; ++i) mbar_init(sm.bar(C::kDone + i), 2);
+    for (int i = C::kSFull; i < C::kPFull; ++i) mbar_init(sm.bar(i), 1);
+    for (int i = C::kPFull; i < C::kFree; ++i) mbar_init(sm.bar(i), 4);
+    for (int i = C::kFree; i < C::kOFree; ++i) mbar_init(sm.bar(i), 1);
+    for (int i = C::kOFree; i < C::kTurn; ++i) mbar_init(sm.bar(i), 4);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(sm.bar(C::kFull + i), 1);
+    for (int i = 0; i < C::kBlocks; ++i) {
+      mbar_init(sm.bar(C::kClean + i), 1);
+      mbar_init(sm.bar(C::kDone + i), 2);
+    }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(sm.bar(C::kSchedFull + i), 1);
       mbar_init(sm.bar(C::kSchedEmpty + i), kConsumers);
@@ -722,8 +906,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     regs_dec<kRegsControl>();
     if (!*abort_flag) {
       if (warp == 3) scanner<D, FP16>(p, smem, sm, wd, lane);
-      else if (warp >= 1) issuer<D, FP16>(p, smem, sm, tmem, wd, warp - 1);
-      else {
+      else if (warp >= 1) {
+        if constexpr (!C::kThree) issuer<D, FP16>(p, smem, sm, tmem, wd, warp - 1);
+        else if (warp == 1) issuer_of_scores<D, FP16>(p, smem, sm, tmem, wd);
+        else issuer_of_outputs<D, FP16>(p, smem, sm, tmem, wd);
+      } else {
         const int few = p.few ? few_items(p, reinterpret_cast<int*>(smem + C::kOffPtr)) : 0;
         if (lane == 0) producer<D>(p, smem, sm, wd, few);
       }

@@ -824,9 +824,11 @@ bsa_status bsa_rope_apply(const bsa_rope* rope, const bsa_rows* q, const bsa_row
  * flags: 0 or BSA_PROMPT_CAUSAL.  scale <= 0 selects 1/sqrt(d).
  * workspace: device, 16-byte aligned, bsa_prompt_workspace_bytes bytes; scratch and
  *   status of this call (calls that overlap in time need their own).
- * Scores, sums and accumulators are fp32, weights are rounded to `dtype` relative to
- * (at most 2^8 times) their row's largest so far.  An infinity or NaN among the keys
- * or values reaches the rows that attend it and no other.  Two kernels.
+ * Scores, sums and accumulators are fp32.  Weights are rounded to `dtype`; they are taken
+ * relative to the largest score of the row's first 128 keys, or of the first later block of
+ * 128 whose weights of the row come to more than 2^15 of that.  An infinity or NaN among
+ * the keys or values reaches the rows that attend it and no other.  One kernel for up to 64
+ * prompts of up to 4096 tokens together, otherwise two.
  */
 size_t bsa_prompt_workspace_bytes(int n, int T, int Hq, int Hkv);
 bsa_status bsa_prompt_attention(const bsa_rows* q, const bsa_rows* k, const bsa_rows* v, const bsa_rows* o, float* LSE,
@@ -834,7 +836,8 @@ bsa_status bsa_prompt_attention(const bsa_rows* q, const bsa_rows* k, const bsa_
                                 float scale, void* workspace, size_t workspace_bytes, void* stream);
 /*
  * bsa_prompt_status -- synchronise `stream`, then report what the kernels of the last
- * bsa_prompt_attention with this workspace recorded: BSA_OK, BSA_ERR_INVALID_ARG (its
+ * bsa_prompt_attention with this workspace recorded (one at least has to have run with it):
+ * BSA_OK, BSA_ERR_INVALID_ARG (its
  * offsets) or BSA_ERR_TIMEOUT (a wait ran past the watchdog limit; the kernel stopped
  * cleanly).  *detail (may be NULL) receives (block << 8) | wait-site.
  */
