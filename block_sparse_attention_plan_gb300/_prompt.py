@@ -164,6 +164,8 @@ def rope(r: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None, positions: 
         where = (B, T)
     kr = ko = pptr = None
     Hk = 0
+    if k is None and out_k is not None:
+        raise ValueError("out_k without k")
     if k is not None:
         kr = _rows(k, index, "k", 1)
         ks = k.shape

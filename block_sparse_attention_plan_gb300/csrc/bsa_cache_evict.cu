@@ -23,6 +23,11 @@
 // read, writing them harms no source of a later place.  A round's places are read by
 // all CTAs of the cluster into registers, the cluster meets, then they are written;
 // no second meeting is needed, and nothing is copied twice or waits on a flag.
+//
+// What bounds them: the selection, short phases between barriers; the move, the bytes
+// of kept tokens there and back.  Measured, selection and move: 32 sequences of 2177 to
+// 2304 tokens to 2048, 8 heads of 128, E4M3: 14 + 45 us (the move 0.9 of a copy's rate); 48 of
+// 700 to 12000 to 1000, 8 heads of 64, INT8, pages of 16: 33 + 34; one of 64001 to 8000: 24 + 19.
 #include "bsa_cache.h"
 #include "bsa_cache_codes.cuh"
 #include "bsa_device.cuh"

@@ -21,6 +21,12 @@
 // costs less than turning halves about).  Pages, scales and weights are read a tile ahead.  The rows wait in shared memory, prepared once per
 // pair.  From 33 rows on the products are what costs (128 rows a pass, pieces are gone
 // over again for more): tiles of 16 keys, so that few tokens spread over all warps.
+//
+// Measured: 32 sequences of 500 to 32768 tokens, a query of 32 heads over 8 of 128, E4M3:
+// 103 us, 5.7 TB/s (operands read from global memory by their lanes 153, through the ring
+// 131, with up to 8 rows in registers 119, pieces cut with kHead 105: 12, 6, 20 or 32
+// places 105, 113, 104, 105).  4 of 3000 to 12001, 32 queries of 32 heads over 8 of 64, INT8:
+// 28 us (tiles of 64 keys 46).
 #include "bsa_cache.h"
 #include "bsa_cache_codes.cuh"
 #include "bsa_device.cuh"

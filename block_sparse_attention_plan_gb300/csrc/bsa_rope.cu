@@ -14,7 +14,8 @@
 // all heads of a token: a warp goes over the heads of q and then of k in rounds
 // of 32 / (d / 16) heads, kUnroll rounds of loads in flight.  With few tokens
 // (a decoding step) a token's rounds are spread over several warps, which then
-// compute the sines anew.
+// compute the sines anew.  (16001 tokens of 32 + 8 heads of 128: 55 us, 5.9 TB/s, 0.87 of a
+// copy's rate; a token of each of 64 sequences: 3 to 5 us.)
 #include "bsa_prompt.h"
 
 namespace bsa {

@@ -203,6 +203,24 @@ def test_scale_and_large_scores(bsa):
     check(bsa, q, k, v, ptr([260]), scale=1e-3, causal=False)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[1500, 130, 700], [100, 1300], [40] * 3 + [2100]])
+def test_references_that_move(bsa, dtype, d, lens):
+    """Scores that rise by 30 or more a block, fall, or jump: the reference moves in every block of some rows, in
+    none of others, in both tiles of an item and where an item has one."""
+    gen = torch.Generator().manual_seed(d + len(lens))
+    T = sum(lens)
+    u = torch.randint(0, 2, (d,), generator=gen).double() * 2 - 1
+    j = torch.arange(T).double()
+    f = torch.stack([j / T * 40, 40 - j / T * 40, (j // 200 % 2) * 30], 1)  # a K/V head each
+    k = (f[:, :, None] * u).to(dtype)
+    q = ((torch.rand(T, 6, 1, generator=gen).double() + 0.25) * u).to(dtype)
+    v = rows(gen, T, 3, d, dtype)
+    check(bsa, q, k, v, ptr(lens))
+    check(bsa, q, k, v, ptr(lens), causal=False)
+
+
 def test_equal_keys_give_the_mean(bsa):
     v = torch.randn(500, 1, 128, generator=torch.Generator().manual_seed(5)).to(torch.float16)
     k = torch.ones(500, 1, 128, dtype=torch.float16)

@@ -150,3 +150,9 @@ def test_refusals(bsa):
     assert bsa.rope(r, q[:0])[0].shape == (0, 2, 128)
     o, ok = bsa.rope(r, q, q[:, :0])  # no key heads
     assert ok.shape == (4, 0, 128) and torch.equal(o, q)
+
+
+def test_an_output_for_keys_that_are_not_given_is_refused(bsa):
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        bsa.rope(bsa.rope_create(64), q, out_k=q.clone())
