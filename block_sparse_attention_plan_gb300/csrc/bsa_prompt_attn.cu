@@ -353,8 +353,8 @@ struct Products {
     ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, site));
     return ok;
   }
-  // A wait that polls: a suspended try_wait is about 100 cycles later.  (64 polls are not
-  // always enough, 256 are: a prompt of 12007 tokens, 32 / 8 heads of 128, 701 and 692 us.)
+  // A wait that polls: a suspended try_wait is about 100 cycles later.  (64 or 256 polls
+  // are the same within 1 %.)
   __device__ __forceinline__ bool wait_spinning(uint32_t bar, uint32_t parity, int site) {
     bool there = false;
     for (int i = 0; i < 256 && !there; ++i) there = mbar_test_wait(bar, parity);
