@@ -34,7 +34,7 @@
 //             attend as a whole (below);
 //   warps 4-7, 8-11  the softmax of tile A and of tile B, a thread per row, against a
 //             reference that is the first block's maximum and moves (O is rescaled) only when
-//             a block's weights come to more than kMost: no maximum is taken of the others, a
+//             a block's weights come to more than 2^15: no maximum is taken of the others, a
 //             quarter of the time from S to P, which is what the two tiles wait for.  And the
 //             epilogue.
 //
@@ -73,9 +73,14 @@ constexpr int kRegsSoftmax = 208;
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split");
 constexpr int kSlots = 4;                   // work items published ahead
 constexpr int kConsumers = 2 + 1 + 8;       // issuing warps, scanning warp, eight softmax warps
-// A block's weights of a row that sum to more than this move the row's reference: in fp16
-// none of them is past its range of 2^16 then.
-constexpr float kMost = 32768.f;
+// A block's weights of a row that sum to more than 2^kMostLog move the row's reference.
+// fp16 weights are kept at 2^6 of their size, and none of them is past fp16's range of 2^16
+// then: 128 at the reference sum to 2^13, and what falls below the range is 2^-30 of the
+// reference.  bf16 weights have fp32's range: they are kept at 2^-kMostLog over the number of a
+// row's blocks, so that all of its weights sum to less than 1 and no finite value, however
+// large, takes O out of range.  (At the other end values below 2^-100 lose bits to fp32's
+// smallest numbers: weights at the reference are 2^-16 for one block, 2^-22 for 12007 tokens.)
+constexpr int kMostLog = 15;
 
 enum PromptSite : int { kSitePromptOffsets = 0x60, kSiteTurn };
 
@@ -688,9 +693,6 @@ template <int D, bool FP16>
 __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, const Smem<Cfg<D>>& sm, uint32_t tmem,
                                         const Watchdog& wd) {
   using C = Cfg<D>;
-  // fp16 weights are kept at 2^6 of their size: 128 at the reference sum to 2^13, and what
-  // falls below fp16's range is 2^-30 of the reference.
-  constexpr float kShift = FP16 ? 6.f : 0.f;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int x = (warp - 4) >> 2, quad = warp & 3;
   const int row = quad * 32 + lane;
@@ -715,6 +717,10 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
     const int lim = p.causal ? min(tok, m.len - 1) : m.len - 1;
     const int lim_warp = p.causal ? min(first + ((quad * 32) >> p.gp_shift), m.len - 1) : m.len - 1;  // its first row's
     const int whole = p.causal ? min(first + 1, m.len) : m.len;
+    // Weights are kept at 2^shift of their size and, in a block, summed to no more than `most`.
+    const int log_n = 32 - __clz(n);
+    const float shift = FP16 ? 6.f : (float)(-kMostLog - log_n);
+    const float most = FP16 ? (float)(1 << kMostLog) : __uint_as_float((uint32_t)(127 - log_n) << 23);
     float m_ref = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
       // Where its scores are, and the phase that says so.
@@ -732,7 +738,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
       uint32_t v[128], pk[64];
       float sum, factor = 1.f;
       // The first block sets the reference, m.  Later ones are weighed against it as it is:
-      // only where a row's weights come to more than kMost has a score passed it by so much
+      // only where a row's weights come to more than `most` has a score passed it by so much
       // that it has to move, and the scores (the weights are not stored yet) are read again.
       for (bool move = j == 0;; move = true) {
         tmem_ld32_at<0>(scol, v);
@@ -786,7 +792,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
             }
           }
         }
-        const float mb = kShift - (m_ref == -INFINITY ? 0.f : m_ref);
+        const float mb = shift - (m_ref == -INFINITY ? 0.f : m_ref);
         const uint64_t mbx2 = f2_make(mb, mb);
         uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -800,7 +806,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
         float s0, s1;
         f2_split(fadd2(fadd2(acc2[0], acc2[1]), fadd2(acc2[2], acc2[3])), s0, s1);
         sum = s0 + s1;
-        if (move || !__any_sync(0xffffffffu, sum > kMost || m_ref == -INFINITY)) break;
+        if (move || !__any_sync(0xffffffffu, sum > most || m_ref == -INFINITY)) break;
       }
       tmem_st32_at<0>(scol, pk);
       tmem_st32_at<32>(scol + 32u, pk);
@@ -849,7 +855,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
     if (lane == 0) mbar_arrive(sm.bar(C::kOFree + x));
     if (real && p.lse)
       p.lse[(long long)(m.row0 + tok) * p.Hq + head] =
-          l == 0.f ? -INFINITY : (m_ref - kShift + __log2f(l)) * 0.69314718055994531f;
+          l == 0.f ? -INFINITY : (m_ref - shift + __log2f(l)) * 0.69314718055994531f;
     if (dirty[t % (2 * kSlots)]) add_no_numbers<D, FP16>(p, m, first + ((quad * 32) >> p.gp_shift), quad * 32);
   }
 }

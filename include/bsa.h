@@ -827,8 +827,10 @@ bsa_status bsa_rope_apply(const bsa_rope* rope, const bsa_rows* q, const bsa_row
  * Scores, sums and accumulators are fp32.  Weights are rounded to `dtype`; they are taken
  * relative to the largest score of the row's first 128 keys, or of the first later block of
  * 128 whose weights of the row come to more than 2^15 of that.  An infinity or NaN among
- * the keys or values reaches the rows that attend it and no other.  One kernel for up to 64
- * prompts of up to 4096 tokens together, otherwise two.
+ * the keys or values reaches the rows that attend it and no other.  Finite values of any size
+ * give finite means (one within the weights' rounding of the type's largest may be rounded
+ * past it); values below 2^-100 lose bits.  One kernel for up to 64 prompts of up to 4096
+ * tokens together, otherwise two.
  */
 size_t bsa_prompt_workspace_bytes(int n, int T, int Hq, int Hkv);
 bsa_status bsa_prompt_attention(const bsa_rows* q, const bsa_rows* k, const bsa_rows* v, const bsa_rows* o, float* LSE,

@@ -283,3 +283,33 @@ def test_refusals(bsa):
             bad()
     o, lse = f(x[:0], x[:0], x[:0], ptr([0]).cuda())
     assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 6, 3), (128, 6, 3)])
+@pytest.mark.parametrize("lens", [[1500, 130, 7], [100], [2100]])
+def test_values_of_any_finite_size(bsa, d, Hq, Hkv, lens):
+    """bfloat16 values scaled by a power of two scale the outputs, bit for bit: sums of weights are below 1 in all, so
+    that no finite value leaves fp32's range, with scores that rise, fall or jump after the first 128 keys."""
+    gen = torch.Generator().manual_seed(d + len(lens))
+    T = sum(lens)
+    u = torch.randint(0, 2, (d,), generator=gen).double() * 2 - 1
+    j = torch.arange(T).double()
+    f = torch.stack([j / T * 5, 5 - j / T * 5, (j // 200 % 2) * 4], 1)
+    k = (f[:, :, None] * u).to(torch.bfloat16)
+    q = ((torch.rand(T, Hq, 1, generator=gen).double() + 0.25) * u * 8 / d ** 0.5).to(torch.bfloat16)
+    v = rows(gen, T, Hkv, d, torch.bfloat16).clamp(-3.9, 3.9)
+    for causal in (True, False):
+        o, lse = check(bsa, q, k, v, ptr(lens), causal)
+        for e in (115, 125, -90):
+            big = (v.double() * 2.0 ** e).to(torch.bfloat16)
+            assert big.isfinite().all()
+            got, gl = bsa.prompt_attention(q.cuda(), k.cuda(), big.cuda(), ptr(lens).cuda(), causal=causal)
+            assert torch.equal(gl, lse) and torch.equal(got.double(), o.double() * 2.0 ** e), e
+
+
+def test_the_largest_values(bsa):
+    """Every value the type's largest: the mean is that value (equal weights, their sums exact)."""
+    top = torch.finfo(torch.bfloat16).max
+    k = torch.zeros(1000, 1, 64, dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, top)
+    o, _ = bsa.prompt_attention(k, k, v, ptr([1000]).cuda())
+    assert (o == top).all()
