@@ -53,7 +53,7 @@ struct WeighCfg {
   static constexpr int kRowBytes = 2 * D + 16; // of a prepared query row (16: no bank conflicts)
   static constexpr int kOffRows = kWeighWarps * kStages * kTileBytes;
   static constexpr int kOffConst = kOffRows + ROWS * kRowBytes;  // {qs, lse} of each row
-  static constexpr int kOffLim = kOffConst + ROWS * 8;           // last key position of each row (causal)
+  static constexpr int kOffLim = kOffConst + ROWS * 8;           // last key position of each row (causal; -1: it has no sum)
   static constexpr int kOffHead = kOffLim + ROWS * 4;            // head in the group
   static constexpr int kOffBar = kOffHead + ROWS * 4;            // full [warps][stages]
   static constexpr int kOffTile = kOffBar + kWeighWarps * kStages * 8;  // [warps][stages][8]: tile, pool rows of its groups
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
       float* weights = p.weights + ((size_t)seq * c.Hkv + h) * p.stride;
       const uint8_t* mask = p.mask ? p.mask + ((size_t)b * p.Hq + (size_t)h * p.g) * p.NKB : nullptr;
       const int fresh0 = len > p.fresh ? len - p.fresh : 0;  // weights from here on begin at 0
-      const int free_end = p.causal ? len - p.nq + 1 : len;  // keys below it are seen by every query
+      const int free_end = p.causal ? len - p.nq + 1 : len;  // keys below it are seen by every query that has a sum
       for (int m0 = 0; m0 < p.M; m0 += ROWS) {
         const int rows = min(p.M - m0, ROWS);
         // ------------------------------------------------------------ requests
@@ -289,11 +289,12 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
         if (waiting) ahead();
         // ------------------------------------------------------------ the rows
         __syncthreads();  // (those before them are used up)
+        bool some_none = false;
         for (int m = warp * 8 + r8; m < ((rows + 7) & ~7); m += 8 * kWeighWarps) {
           // Four lanes a row: lane l4 has elements 64 v + 16 l4 .. + 15.
           uint32_t w[NV][8];
           const bool real = m < rows;
-          const int hd = real ? (m0 + m) / p.nq : 0, i = real ? (m0 + m) - hd * p.nq : 0;
+          const int hd = (m0 + min(m, rows - 1)) / p.nq, i = real ? (m0 + m) - hd * p.nq : 0;
           // A row of no sum, and one that is none, give nothing: zeros, and e^-inf.
           const float z = real ? load_written(p.lse + ((size_t)b * p.Hq + h * p.g + hd) * p.nq + i) : -INFINITY;
           const uint16_t* at = p.q.p + (long long)b * p.q.sb + (long long)(h * p.g + hd) * p.q.sh + (long long)i * p.q.st + 16 * l4;
@@ -335,11 +336,15 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
           if (l4 == 0) {
             s_const[2 * m] = real ? p.scale * __uint_as_float((uint32_t)(e + 127) << 23) : 0.f;
             s_const[2 * m + 1] = z == -INFINITY ? INFINITY : z;
-            s_lim[m] = p.causal ? len - p.nq + i : 0x7fffffff;
+            s_lim[m] = z == -INFINITY ? -1 : p.causal ? len - p.nq + i : 0x7fffffff;
             s_head[m] = hd;
           }
+          some_none |= real && z == -INFINITY;
         }
-        __syncthreads();
+        // Rows of no sum see no key: one that is no number would make NaN even of their zeros.
+        // (Those that only fill up an eight have the last row's head and see no other key than it:
+        // their NaN is one that the row gives itself.)
+        const int late_from = __syncthreads_or(some_none) ? 0 : free_end;
         // Up to 8 rows stay in registers: this lane's elements of row r8, and what rows
         // 2 l4 and 2 l4 + 1 are finished with.
         uint4 rb[ROWS == 8 ? 2 * NV : 1];
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_kernel(const __grid_co
           for (int gr = 0; gr < G; ++gr) {
             const float scale = sc[gr];
             const int j0 = key0 + gr * 16 + r8;  // this lane's keys: j0, j0 + 8
-            const bool late = key0 + gr * 16 + 15 >= free_end;
+            const bool late = key0 + gr * 16 + 15 >= late_from;
             float acc0 = 0.f, acc1 = 0.f;
             // This lane's word s4 of vector v as operand registers.
             auto operand = [&](int v, int s4, uint32_t (&a)[4]) {

@@ -491,3 +491,33 @@ def test_refusals(bsa):
     bsa.cache_weigh(c, q, lse, w)      # an empty cache
     bsa.cache_evict(c, w, i32(0, 5))
     assert bsa.cache_status(c) == (0, 0) and (w == 0).all()
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g,nq,causal,bk", [(1, 1, False, 0), (4, 1, False, 32), (3, 7, True, 0), (3, 7, True, 64), (8, 20, False, 0),
+                                            (8, 20, True, 32), (40, 1, False, 64)])
+def test_a_row_without_a_sum_gives_nothing_whatever_the_keys_are(bsa, kind, d, g, nq, causal, bk):
+    """Keys and scales that are no numbers, seen by rows whose LSE is -inf alone."""
+    gen = torch.Generator().manual_seed(g + d)
+    m = filled(kind, [150, 75], 2, 64, 32, d, seed=8)
+    q = (torch.randn(2, 2 * g, nq, d, generator=gen) * 0.2).to(torch.bfloat16).cuda()
+    lse = torch.randn(2, 2 * g, nq, generator=gen) + 3
+    lse[0, :g] = -math.inf       # the first head of sequence 0: no row has a sum
+    lse[1, g] = -math.inf        # one query head of several, and (masked) the only one that selects key block 0
+    mask = None
+    if bk:
+        mask = torch.ones(2, 2 * g, 150 // bk + 1, dtype=torch.uint8)
+        mask[1, g + 1:, 0] = 0
+    w0 = torch.rand(2, 2, 192, generator=gen)
+    plain, got = w0.cuda(), w0.cuda()
+    kw = dict(mask=None if mask is None else mask.cuda(), bk=bk, causal=causal, fresh=0)
+    bsa.cache_weigh(upload(bsa, m), q, lse.cuda(), plain, **kw)
+    if kind == "e4m3":
+        m.codes[0][m.table[0, 0], 0, 20] = 0x7F          # NaN
+    m.scales[0][m.table[0, 1], 0, 0] = math.inf
+    m.scales[0][m.table[0, 2], 0, 0] = math.nan
+    if bk:
+        m.scales[0][m.table[1, 0], 1, 0] = math.nan      # tokens 0 .. 31
+    bsa.cache_weigh(upload(bsa, m), q, lse.cuda(), got, **kw)
+    assert plain.isfinite().all() and torch.equal(plain, got)
+    assert torch.equal(got[0, 0].cpu(), w0[0, 0])
