@@ -36,6 +36,12 @@ constexpr int kPromptRows = 256;   // query rows of a work item: two tiles of 12
 // schedule kernel.
 constexpr int kPromptFew = 64, kPromptFewTokens = 4096;
 constexpr int kPromptCtlTiles = 3; // control word: work items of a group of heads (0-2: as a plan's)
+constexpr int kPromptCtlCtas = 4;  // control word: CTAs of the attention kernel
+// Behind the 16 control words, status and detail of each CTA: it clears its own when it
+// begins, which no other CTA's record can come before.
+constexpr int kPromptCtlOwn = 16;
+constexpr int kPromptMaxCtas = 512;
+constexpr int kPromptCtlWords = kPromptCtlOwn + 2 * kPromptMaxCtas;
 struct PromptParams {
   CUtensorMap tmQ;         // q as [halves][T][Hq][64], box {64, gp, 128 / gp, halves}: 128 rows, a token's heads together
   CUtensorMap tmK, tmV;    // k, v as [halves][T][Hkv][64], box {64, 1, 128, halves}
@@ -45,7 +51,7 @@ struct PromptParams {
   long long o_st, o_sh;
   float* lse;              // [T][Hq] or nullptr
   const int32_t* offsets;  // [n + 1]
-  int32_t* control;        // [16]
+  int32_t* control;        // [kPromptCtlWords]
   int32_t* tile_ptr;       // [n + 1]: work items ahead of each prompt
   int4* tiles;             // {first row, length, first token, 0}, longest first
   int n, T, Hq, Hkv, g;

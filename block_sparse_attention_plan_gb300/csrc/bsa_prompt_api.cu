@@ -50,7 +50,7 @@ bsa_status prompt_layout(int n, int T, int Hq, int Hkv, PromptLayout* out) {
   while (l.gp_shift < 4 && !(g >> l.gp_shift & 1)) ++l.gp_shift;
   const long long tiles = (long long)T / (kPromptRows >> l.gp_shift) + n;
   if (T > (1 << 30) || Hq > 65536 || tiles * (Hq >> l.gp_shift) >= (1ll << 31)) return BSA_ERR_UNSUPPORTED;
-  size_t off = align256(64);
+  size_t off = align256(4 * kPromptCtlWords);
   l.off_ptr = off;   off = align256(off + 4ull * ((uint64_t)n + 1));
   l.off_tiles = off; off = align256(off + 16ull * (uint64_t)tiles);
   l.bytes = off;
@@ -120,11 +120,14 @@ bsa_status bsa_prompt_attention(const bsa_rows* q, const bsa_rows* k, const bsa_
 bsa_status bsa_prompt_status(const void* workspace, void* stream, int32_t* detail) {
   if (!workspace || !aligned(workspace, 16)) return BSA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int32_t word[2] = {0, 0};
-  if (cudaMemcpyAsync(word, static_cast<const int32_t*>(workspace) + kCtlStatus, sizeof(word), cudaMemcpyDeviceToHost, s) !=
-          cudaSuccess ||
+  int32_t words[kPromptCtlWords];
+  if (cudaMemcpyAsync(words, workspace, sizeof(words), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess)
     return BSA_ERR_CUDA;
+  // What was found of the offsets, then what the CTAs' waits recorded, the first CTA's first.
+  const int32_t* word = words + kCtlStatus;
+  const int32_t ctas = words[kPromptCtlCtas];
+  for (int32_t i = 0; word[0] == BSA_OK && i < ctas && i < kPromptMaxCtas; ++i) word = words + kPromptCtlOwn + 2 * i;
   if (detail) *detail = word[1];
   return static_cast<bsa_status>(word[0]);
 }

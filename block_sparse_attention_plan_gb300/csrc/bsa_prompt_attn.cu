@@ -239,7 +239,7 @@ __device__ __forceinline__ int few_items(const PromptParams& p, int* ptr) {
   if (lane == 0) ptr[p.n] = base;
   __syncwarp();
   bad = __any_sync(0xffffffffu, bad);
-  if (blockIdx.x == 0 && lane == 0) {  // (a wait gives up a second later at the earliest)
+  if (blockIdx.x == 0 && lane == 0) {  // (what CTAs record of their waits has words of its own)
     p.control[kCtlStatus] = bad ? BSA_ERR_INVALID_ARG : BSA_OK;
     p.control[kCtlDetail] = bad ? kSitePromptOffsets : 0;
   }
@@ -868,7 +868,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const Smem<C> sm{smem_u32(smem)};
   volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  const Watchdog wd{abort_flag, p.control + kCtlStatus, p.control + kCtlDetail, p.watchdog_ns};
+  int32_t* own = p.control + kPromptCtlOwn + 2 * blockIdx.x;
+  const Watchdog wd{abort_flag, own, own + 1, p.watchdog_ns};
   next_may_launch();
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -899,6 +900,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tmem_relinquish();
   }
   wait_for_previous();
+  if (threadIdx.x == 0) {
+    own[0] = BSA_OK;
+    own[1] = 0;
+    if (blockIdx.x == 0) p.control[kPromptCtlCtas] = (int)gridDim.x;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1034,8 +1040,10 @@ cudaError_t launch(const PromptParams& p, int sms, cudaStream_t s) {
   constexpr int kSmem = Cfg<D>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const long long most = ((long long)p.T / (kPromptRows >> p.gp_shift) + p.n) * (p.Hq >> p.gp_shift);
-  return launch_after(prompt_kernel<D, FP16>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), kSmem, s, p);
+  long long ctas = ((long long)p.T / (kPromptRows >> p.gp_shift) + p.n) * (p.Hq >> p.gp_shift);
+  if (ctas > sms) ctas = sms;
+  if (ctas > kPromptMaxCtas) ctas = kPromptMaxCtas;
+  return launch_after(prompt_kernel<D, FP16>, dim3((unsigned)ctas), dim3(kThreads), kSmem, s, p);
 }
 
 }  // namespace

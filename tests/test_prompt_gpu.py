@@ -313,3 +313,20 @@ def test_the_largest_values(bsa):
     v = torch.full_like(k, top)
     o, _ = bsa.prompt_attention(k, k, v, ptr([1000]).cuda())
     assert (o == top).all()
+
+
+@pytest.mark.parametrize("n,T", [(3, 900), (70, 900)])
+def test_what_any_block_records_is_reported(bsa, n, T):
+    """Status words are each block's own: whatever the workspace held is gone after a call, and what one block recorded
+    is not lost to another's."""
+    gen = torch.Generator().manual_seed(n)
+    x = rows(gen, T, 8, 64, torch.bfloat16).cuda()
+    off = ptr([T // n] * (n - 1) + [T - T // n * (n - 1)]).cuda()
+    ws = torch.full((bsa.prompt_workspace_bytes(n, T, 8, 8),), 0xFA, dtype=torch.uint8, device="cuda")
+    bsa.prompt_attention(x, x, x, off, workspace=ws)
+    assert bsa.prompt_status(ws) == (0, 0)
+    words = ws.view(torch.int32)
+    words[16 + 2 * 5:16 + 2 * 5 + 2] = torch.tensor([-6, 5 << 8 | 0x52], dtype=torch.int32)  # as block 5's wait would
+    assert bsa.prompt_status(ws) == (-6, 5 << 8 | 0x52)
+    bsa.prompt_attention(x, x, x, off, workspace=ws)
+    assert bsa.prompt_status(ws) == (0, 0)
