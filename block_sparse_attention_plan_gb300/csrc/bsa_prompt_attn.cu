@@ -115,7 +115,7 @@ struct Cfg {
   static constexpr int kSchedFull = kDrain + 2;
   static constexpr int kSchedEmpty = kSchedFull + kSlots;
   static constexpr int kNumBars = kSchedEmpty + kSlots;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag, copies requested of K/V and of Q
   static constexpr int kOffSched = kOffMisc + 16;           // int [kSlots][8]
   static constexpr int kOffDirty = kOffSched + 32 * kSlots; // int [2 kSlots]
   static constexpr int kOffPtr = kOffDirty + 8 * kSlots;    // int [2][kPromptFew + 1]: items ahead of each prompt, offsets
@@ -322,14 +322,22 @@ __device__ __noinline__ void producer(const PromptParams& p, uint8_t* smem, cons
     }
     block += (uint32_t)nb;
   }
-  if (*wd.abort_flag) {  // copies already issued land before the shared memory goes away
-    const uint32_t nk = kv_it < (uint32_t)C::kStages ? kv_it : (uint32_t)C::kStages;
-    for (uint32_t t = kv_it - nk; t < kv_it; ++t)
-      drain_wait(sm.bar(C::kFull + (int)(t % C::kStages)), (t / C::kStages) & 1u, wd);
-    const uint32_t nq = q_it < (uint32_t)C::kQBufs ? q_it : (uint32_t)C::kQBufs;
-    for (uint32_t t = q_it - nq; t < q_it; ++t)
-      drain_wait(sm.bar(C::kQFull + (int)(t % C::kQBufs)), (t / C::kQBufs) & 1u, wd);
-  }
+  volatile uint32_t* asked = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc) + 2;
+  asked[0] = kv_it;
+  asked[1] = q_it;
+}
+// Copies that were requested land before the shared memory goes away.  For the CTA's end:
+// a wait may give up when the requests have long been made.
+template <class C>
+__device__ __noinline__ void drain_copies(const uint8_t* smem, const Smem<C> sm, const Watchdog wd) {
+  const volatile uint32_t* asked = reinterpret_cast<const volatile uint32_t*>(smem + C::kOffMisc) + 2;
+  const uint32_t kv_it = asked[0], q_it = asked[1];
+  const uint32_t nk = kv_it < (uint32_t)C::kStages ? kv_it : (uint32_t)C::kStages;
+  for (uint32_t t = kv_it - nk; t < kv_it; ++t)
+    drain_wait(sm.bar(C::kFull + (int)(t % C::kStages)), (t / C::kStages) & 1u, wd);
+  const uint32_t nq = q_it < (uint32_t)C::kQBufs ? q_it : (uint32_t)C::kQBufs;
+  for (uint32_t t = q_it - nq; t < q_it; ++t)
+    drain_wait(sm.bar(C::kQFull + (int)(t % C::kQBufs)), (t / C::kQBufs) & 1u, wd);
 }
 
 // ------------------------------------------------------------------ matrix products
@@ -873,6 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   next_may_launch();
   if (threadIdx.x == 0) {
     *abort_flag = 0;
+    tmem_holder[2] = tmem_holder[3] = 0u;
     for (int i = 0; i < 2; ++i) {
       mbar_init(sm.bar(C::kQFull + i), 1);
       mbar_init(sm.bar(C::kQEmpty + i), C::kThree ? 1 : 2);
@@ -931,6 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) drain_copies<C>(smem, sm, wd);
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -47,3 +47,13 @@ def test_shared_memory_limits_are_constants():
             names = [w for w in re.findall(r"[A-Za-z_]\w*", value) if w not in ("sizeof", "int")]
             assert any(w.startswith("k") for w in names) and "n" not in names, (name, value)
     assert found >= 5
+
+
+def test_copies_of_the_prompt_kernel_are_awaited_at_its_end():
+    """A wait may give up when the copies have long been requested and their requester is done: what waits for them
+    stands behind the CTA's last barrier, ahead of nothing but the release of tensor memory."""
+    text = dict(sources())["bsa_prompt_attn.cu"]
+    body = text[text.index("prompt_kernel("):text.index("prompt_schedule_kernel")]
+    end = body[body.rindex("__syncthreads();"):]
+    assert "abort_flag" in end and "drain_copies" in end and body.count("drain_copies") == 1
+    assert "return" not in body
