@@ -123,14 +123,16 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) evict_s
   const bool cuts = good && x.want < x.have;
   bool missing = false, shared = false;
   if (cuts) {
-    // Every page is one, and those that are written are the sequence's alone.
+    // Every page is one, and those that are written are the sequence's alone (the first ones, of
+    // sinks alone, are not).
     const int32_t* row = c.table + (size_t)x.seq * c.max_pages;
     const int lpage = 31 - __clz(c.page);
     const int hp = (x.have + c.page - 1) >> lpage, wp = (x.want + c.page - 1) >> lpage;
+    const int sp = min(p.sink, x.want - min(p.recent, x.want)) >> lpage;
     for (int j = tid; j < hp; j += kSelectThreads) {
       const int pg = load_written(row + j);
       if (pg < 0 || pg >= c.num_pages) missing = true;
-      else if (j < wp && load_written(c.refs + pg) > 1) shared = true;
+      else if (j >= sp && j < wp && load_written(c.refs + pg) > 1) shared = true;
     }
   }
   // This CTA's tokens: consecutive, the shares of warps' sizes.

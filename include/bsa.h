@@ -715,9 +715,10 @@ bsa_status bsa_cache_weigh(const bsa_cache* cache, const bsa_rows* q, const floa
  *   caller's own arrays: the first `length` entries of a row, up to keep_max of a sequence that is not cut.
  *   Must not be `keep` or `seqs`.
  * A sequence that is cut to more than keep_max, of a length or budget out of
- * range, or one of whose pages [0, ceil(k / page_size)) other sequences hold too, is
- * skipped and recorded (BSA_ERR_INVALID_ARG, detail = i), as is one with a
- * token in no page (BSA_ERR_PLAN_MISMATCH, detail = the sequence).
+ * range, or one of whose pages [floor(s / page_size), ceil(k / page_size)) other sequences
+ * hold too, is skipped and recorded (BSA_ERR_INVALID_ARG, detail = i), as is one with a
+ * token in no page (BSA_ERR_PLAN_MISMATCH, detail = the sequence).  (So sequences that
+ * began as forks of a common prompt are cut with that prompt as their sinks.)
  * n <= 4096.  workspace: device, 4-byte aligned, bsa_cache_evict_workspace_bytes(n)
  * bytes; calls that overlap in time need their own.  Two kernels.
  */

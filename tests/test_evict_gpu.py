@@ -521,3 +521,34 @@ def test_a_row_without_a_sum_gives_nothing_whatever_the_keys_are(bsa, kind, d, g
     bsa.cache_weigh(upload(bsa, m), q, lse.cuda(), got, **kw)
     assert plain.isfinite().all() and torch.equal(plain, got)
     assert torch.equal(got[0, 0].cpu(), w0[0, 0])
+
+
+@pytest.mark.parametrize("kind,page,sb,sink", [("e4m3", 16, 16, 32), ("int8", 32, 16, 70), ("e4m3", 64, 32, 64)])
+def test_shared_pages_of_sinks(bsa, kind, page, sb, sink):
+    """Pages that hold the first `sink` tokens alone are not written: other sequences may hold them too (a prompt that
+    all begin with), and their cuts agree with the model's."""
+    m = filled(kind, [300, 280, 290], 2, page, sb, 64, seed=4, spare=10)
+    whole = sink // page          # pages of sinks alone
+    for s in (1, 2):
+        for j in range(whole):
+            m.refs[m.table[s, j]] -= 1
+            m.table[s, j] = m.table[0, j]
+            m.refs[m.table[0, j]] += 1
+    c = upload(bsa, m)
+    gen = torch.Generator().manual_seed(5)
+    w = heavy(gen, 3, 2, m.table.shape[1] * page)
+    w = evict_both(bsa, m, c, w, [150, 140, 200], sink=sink, recent=20)
+    assert bsa.cache_status(c) == (0, 0) and m.refs.max() == 3
+    # a page of which one token is no sink is written: left as it is
+    t = w.clone()
+    bsa.cache_evict(c, t, i32(100), sink=whole * page - 1)
+    assert bsa.cache_status(c) == (-1, 0)
+    assert_state(c, m)
+    assert torch.equal(t, w)
+    # a budget below the sinks: what is kept are the first and the recent ones; pages behind are given back
+    k = whole * page
+    evict_both(bsa, m, c, w.cpu(), [k + 3] * 3, sink=1 << 30, recent=3)
+    assert bsa.cache_status(c) == (0, 0)
+    bsa.cache_evict(c, w, i32(k), sink=1 << 30, recent=3)
+    assert bsa.cache_status(c) == (-1, 0)  # (the last three move into the shared page)
+    assert_state(c, m)
