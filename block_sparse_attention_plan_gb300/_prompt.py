@@ -151,7 +151,13 @@ def rope(r: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None, positions: 
     """Rotary positions of q and (not None) k, bfloat16 or float16: [B, H, T, d], any strides between rows, with
     ``positions`` int32 [B, T]; or packed [T, H, d] with ``positions`` [T] (bsa_rope_apply).  Without positions
     they are 0 .. T-1.  ``inverse`` turns back, which also takes gradients of the outputs to those of the inputs.
-    ``out_q``, ``out_k``: where the results go, q and k themselves for a call in place.  Returns (q, k) turned."""
+    ``out_q``, ``out_k``: where the results go, q and k themselves for a call in place.  Returns (q, k) turned;
+    where gradients are recorded and q or k requires them, results that belong to the graph (and given outputs are
+    refused)."""
+    if (q.requires_grad or (k is not None and k.requires_grad)) and torch.is_grad_enabled():
+        if out_q is not None or out_k is not None:
+            raise ValueError("out_q and out_k are for calls that record no gradients")
+        return _Turn.apply(r, q, k, positions, inverse, stream)
     index = r._index
     qr = _rows(q, index, "q", 0)
     shape = q.shape
@@ -191,6 +197,28 @@ def rope(r: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None, positions: 
     _call(index, "bsa_rope_apply", r._ref, qr, _rows(out_q, index, "out_q", 3), Hq, kr, ko, Hk, _ELEMENTS[q.dtype],
           pptr, B, T, d, ROPE_INVERSE if inverse else 0, _raw_stream(index) if stream is None else stream.cuda_stream)
     return out_q, out_k
+
+
+class _Turn(torch.autograd.Function):
+    """``rope`` as a node of the graph: the gradients are turned the other way."""
+
+    @staticmethod
+    def forward(ctx, r, q, k, positions, inverse, stream):
+        ctx.rope, ctx.inverse = r, inverse
+        ctx.save_for_backward(positions)
+        return rope(r, q, k, positions, inverse, stream=stream)
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        positions, = ctx.saved_tensors
+        gq, gk = (g if g is None or _takes(g) else g.contiguous() for g in (gq, gk))
+        gq, gk = rope(ctx.rope, gq, gk, positions, not ctx.inverse)
+        return None, gq, gk, None, None, None
+
+
+def _takes(t: torch.Tensor) -> bool:
+    """Rows that the library reads as they lie."""
+    return t.stride(-1) == 1 and not t.data_ptr() & 15 and not any(s & 7 for n, s in zip(t.shape, t.stride()[:-1]) if n > 1)
 
 
 def prompt_workspace_bytes(n: int, T: int, Hq: int, Hkv: int) -> int:

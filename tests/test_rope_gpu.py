@@ -156,3 +156,48 @@ def test_an_output_for_keys_that_are_not_given_is_refused(bsa):
     q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
         bsa.rope(bsa.rope_create(64), q, out_k=q.clone())
+
+
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("inverse", [True, False])
+def test_gradients_reach_the_inputs(bsa, packed, inverse):
+    """The result belongs to the graph of its inputs: their gradients are the outputs' turned the other way."""
+    gen = torch.Generator().manual_seed(7)
+    shape = lambda h: (60, h, 64) if packed else (3, h, 20, 64)
+    q, k = (rows(gen, *shape(h), dtype=torch.bfloat16).cuda().requires_grad_() for h in (4, 2))
+    gq, gk = (rows(gen, *shape(h), dtype=torch.bfloat16).cuda() for h in (4, 2))
+    pos = torch.randint(0, 9999, (60,) if packed else (3, 20), generator=gen).int().cuda()
+    r = bsa.rope_create(32, pairs="neighbours", scaling="parts", factor=4.0, original=100)
+    oq, ok = bsa.rope(r, q, k, positions=pos, inverse=inverse)
+    with torch.no_grad():
+        wq, wk = bsa.rope(r, q, k, positions=pos, inverse=inverse)
+        tq, tk = bsa.rope(r, gq, gk, positions=pos, inverse=not inverse)
+    assert not wq.requires_grad and torch.equal(oq, wq) and torch.equal(ok, wk)
+    got = torch.autograd.grad((oq, ok), (q, k), (gq, gk))
+    assert torch.equal(got[0], tq) and torch.equal(got[1], tk)
+    # one of two; an expanded gradient; rows of another order; no keys
+    a, _ = bsa.rope(r, q, k.detach(), positions=pos, inverse=inverse)
+    assert torch.equal(torch.autograd.grad(a.sum(), q)[0], bsa.rope(r, torch.ones_like(gq), positions=pos, inverse=not inverse)[0])
+    _, b = bsa.rope(r, q.detach(), k, positions=pos, inverse=inverse)
+    assert torch.equal(torch.autograd.grad(b, k, gk.transpose(0, 1).contiguous().transpose(0, 1))[0], tk)
+    c, none = bsa.rope(r, q, positions=pos, inverse=inverse)
+    assert none is None and torch.equal(torch.autograd.grad(c, q, gq)[0], tq)
+    # and through a projection whose heads q and k are
+    x = rows(gen, *shape(6), dtype=torch.bfloat16).cuda().requires_grad_()
+    axis = 1
+    y = x * 1
+    oq, ok = bsa.rope(r, y.narrow(axis, 0, 4), y.narrow(axis, 4, 2), positions=pos, inverse=inverse)
+    torch.autograd.backward((oq, ok), (gq, gk))
+    assert torch.equal(x.grad, torch.cat([tq, tk], axis))
+
+
+def test_outputs_given_to_a_call_with_gradients_are_refused(bsa):
+    r = bsa.rope_create(64)
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    y = q * 1
+    for bad in (lambda: bsa.rope(r, y, out_q=y), lambda: bsa.rope(r, y.detach(), y, out_k=torch.empty_like(y)),
+                lambda: bsa.rope(r, y, out_q=torch.empty_like(y))):
+        with pytest.raises(ValueError):
+            bad()
+    with torch.no_grad():
+        assert bsa.rope(r, y, out_q=y)[0] is y
