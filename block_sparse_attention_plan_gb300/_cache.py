@@ -344,8 +344,10 @@ def cache_weigh(c: Cache, q: torch.Tensor, lse: torch.Tensor, weights: torch.Ten
     """Add the attention weight that each cached token gathers over q [B, Hq, nq, d] to ``weights`` float32
     [max_seqs, Hkv, tokens] (bsa_cache_weigh); q, ``seqs`` (each at most once), ``mask``, ``bk``, ``causal`` and
     ``scale`` as ``cache_attention`` was given them, ``lse`` what it returned.  The last ``fresh`` tokens of each
-    sequence begin at 0 (default nq: the queries' own tokens, new in a step of decoding; 1 << 30 for a prompt's
-    first call: all of them)."""
+    sequence begin at 0: all that were stored since the last call.  The default, nq, is right where those are the
+    queries' own (a step of decoding with a call in every step); after a chunk of which only the last queries are
+    given, or several steps, say how many (1 << 30 for a prompt's first call: all of the sequence), or the others
+    add to what lay there."""
     B, Hq, nq, d = q.shape
     if d != c.d:
         raise ValueError("q must be [B, Hq, nq, d] of the cache's d")
@@ -363,6 +365,7 @@ def cache_evict(c: Cache, weights: torch.Tensor, keep: torch.Tensor, seqs: Optio
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Cut sequences ``seqs`` (default 0 .. n-1) to ``keep`` int32 [n] tokens each (bsa_cache_evict): every K/V
     head keeps the first ``sink``, the last ``recent`` and those of largest ``weights`` between, in their order.
+    Pages that are written have to be the sequence's alone; those of sinks alone may be others' too.
     Returns ``kept`` int32 [n, Hkv, keep_max] (made here, as wide as sequences may be, when None): where the tokens
     of each row were; entries behind its length are not written."""
     n = keep.shape[0]

@@ -113,8 +113,8 @@ def _rows(t: torch.Tensor, index: int, name: str, slot: int):
 
 class Rope:
     """Rotary positions over a tensor of steps (see bsa_rope): ``steps`` int64 [rot / 2] on the device (the bits
-    of the unsigned words), ``amplitude``, ``pairs`` "half" or "neighbours".  ``rope_create`` makes one from
-    frequencies."""
+    of the unsigned words f_i / (2 pi) 2^64), ``amplitude``, ``pairs`` "half" or "neighbours".  ``rope_create`` makes
+    one from a base and a scaling; frequencies of another rule come in as steps."""
 
     def __init__(self, steps: torch.Tensor, amplitude: float = 1.0, pairs: str = "half"):
         if steps.dtype != torch.int64 or not steps.is_cuda or steps.dim() != 1 or not steps.is_contiguous():
@@ -235,7 +235,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets:
     [T, Hkv, d], bfloat16 or float16 with any strides between rows; ``offsets`` int32 [n + 1]: prompt i has rows
     offsets[i] .. offsets[i + 1] - 1.  ``workspace`` (uint8, prompt_workspace_bytes) is taken from the allocator when
     None; one that is given can be asked what the kernels recorded (``prompt_status``).  Returns (O [T, Hq, d],
-    LSE [T, Hq]); rows of no prompt are not written."""
+    LSE [T, Hq]); rows of no prompt are not written.  The results belong to no graph of gradients."""
     index = q.get_device()
     rows = [_rows(q, index, "q", 0), _rows(k, index, "k", 1), _rows(v, index, "v", 2)]
     shape, ks = q.shape, k.shape

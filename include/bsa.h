@@ -685,7 +685,9 @@ bsa_status bsa_cache_attention(const bsa_cache* cache, const bsa_rows* q, const 
  *   a sequence's row only its tokens' are written.
  * fresh: the last `fresh` tokens of each sequence begin at 0, whatever lies there
  *   (new tokens: nq after a step of decoding, any number from the length on for a
- *   prompt's first call); the others are added to.
+ *   prompt's first call); the others are added to.  Where more tokens were stored since
+ *   the last call than there are queries, all of them are fresh: what lies there otherwise
+ *   (an evicted token's weight) would be added to.
  * seqs: as for bsa_cache_attention, but each sequence at most once (a later row
  *   that names one with tokens again is skipped and recorded, BSA_ERR_INVALID_ARG).
  * LSE: device fp32 [B][Hq][nq] contiguous.  Other arguments as
@@ -760,8 +762,11 @@ bsa_status bsa_cache_forward(const bsa_plan* plan, const bsa_cache* cache, const
  *     y_b = amplitude (x_b cos(t f_i) + x_a sin(t f_i)),
  * for i < rot / 2; elements from rot on stay as they are.  Pairs are (i, i + rot/2)
  * with BSA_ROPE_HALF, (2i, 2i + 1) with BSA_ROPE_NEIGHBOURS.
- *   steps   device uint64 [rot / 2], 8-byte aligned: f_i / (2 pi) in 2^-64 turns,
- *           so that an angle is exact to 2^-31 turns at every position
+ *   steps   device uint64 [rot / 2], 8-byte aligned: f_i / (2 pi) in 2^-64 turns.
+ *           t times a step, less whole turns, is exact at every position t; its upper
+ *           32 bits, rounded to fp32, are what the sines are taken of (within 2^-26
+ *           turns).  Steps of bsa_rope_steps are doubles' (a relative 2^-52 or so, which t
+ *           multiplies: under 2^-23 turns for the fastest pair at t = 2^31)
  * rot: a multiple of 16, at most d.
  */
 #define BSA_ROPE_HALF 0
