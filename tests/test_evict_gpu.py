@@ -552,3 +552,39 @@ def test_shared_pages_of_sinks(bsa, kind, page, sb, sink):
     bsa.cache_evict(c, w, i32(k), sink=1 << 30, recent=3)
     assert bsa.cache_status(c) == (-1, 0)  # (the last three move into the shared page)
     assert_state(c, m)
+
+
+@pytest.mark.parametrize("kind,page,sb,d,lens,Hkv,g,nq,causal,bk,fresh", [
+    ("e4m3", 64, 32, 128, [150, 33], 2, 8, 1, False, 0, 1),          # 8 rows: the last in registers
+    ("e4m3", 64, 64, 128, [150, 40], 1, 9, 1, False, 0, 0),          # 9: the first from shared memory
+    ("int8", 32, 16, 128, [131, 64], 2, 4, 5, True, 0, 5),           # 20
+    ("e4m3", 16, 16, 128, [97, 300], 1, 16, 1, False, 0, 1),         # 16
+    ("int8", 64, 64, 128, [200, 31], 1, 8, 4, True, 0, 1 << 30),     # 32
+    ("e4m3", 64, 64, 128, [200, 31], 1, 11, 3, True, 0, 3),          # 33: tiles of 16 keys
+    ("int8", 64, 16, 64, [150, 33], 2, 8, 1, False, 0, 1),
+    ("e4m3", 32, 32, 64, [150, 70], 1, 9, 1, False, 0, 1),
+    ("int8", 16, 16, 64, [260, 64], 2, 4, 8, True, 0, 8),            # 32
+    ("e4m3", 64, 64, 64, [260, 65], 1, 3, 11, True, 0, 11),          # 33
+    ("e4m3", 64, 32, 64, [500, 131], 2, 3, 3, True, 32, 3),          # masked, rows in shared memory: two blocks a tile
+    ("int8", 64, 64, 64, [500, 131], 1, 4, 5, True, 64, 500),
+    ("e4m3", 32, 16, 128, [500, 131], 2, 3, 3, True, 32, 3),
+    ("int8", 64, 64, 128, [500, 131], 1, 16, 2, True, 64, 2),
+    ("e4m3", 64, 64, 128, [500, 131], 1, 33, 1, False, 32, 1),       # more heads of a group than lanes, 33 rows
+    ("int8", 64, 64, 64, [500, 131], 1, 32, 1, False, 32, 1)])
+def test_weights_at_the_borders_of_the_kernels(bsa, kind, page, sb, d, lens, Hkv, g, nq, causal, bk, fresh):
+    gen = torch.Generator().manual_seed(sum(lens) + d + g)
+    m = filled(kind, lens, Hkv, page, sb, d, seed=6)
+    for s in m.scales:
+        s *= np.float32(0.25)
+    c = upload(bsa, m)
+    B = len(lens)
+    q = (torch.randn(B, Hkv * g, nq, d, generator=gen) * 0.5).to(torch.float16 if page == 32 else torch.bfloat16)
+    lse = torch.randn(B, Hkv * g, nq, generator=gen) + 3
+    lse[0, -1, 0] = -math.inf
+    w0 = torch.rand(B, Hkv, m.table.shape[1] * page, generator=gen)
+    mask = None
+    if bk:
+        mask = (np.random.default_rng(2).random((B, Hkv * g, max(lens) // bk + 1)) < 0.2).astype(np.uint8) * 3
+        mask[:, :, 0::4], mask[:, :, 1::4] = 0, 1    # of four blocks the first for no head, the second for all
+    weigh_both(bsa, m, c, q, lse, w0, mask=mask, bk=bk, causal=causal, fresh=fresh)
+    assert bsa.cache_status(c) == (0, 0)

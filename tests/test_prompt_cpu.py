@@ -89,6 +89,39 @@ def test_rope_apply_refuses(lib, buf):
         assert got == want, i
 
 
+def test_prompt_attention_refuses(lib, buf):
+    good = lambda H: C.RowsC(buf.at, 0, 64, H * 64)
+    size = lib.bsa_prompt_workspace_bytes(2, 10, 4, 2)
+
+    def call(q=good(4), k=good(2), v=good(2), o=good(4), lse=VP(buf.at), dtype=0, off=VP(buf.at), n=2, T=10, Hq=4, Hkv=2, d=64, flags=0,
+             scale=0.0, ws=VP(buf.at), nbytes=size):
+        return lib.bsa_prompt_attention(q, k, v, o, lse, dtype, off, n, T, Hq, Hkv, d, flags, scale, ws, nbytes, None)
+
+    odd = VP(buf.at + 2)
+    cases = [(call(q=None), -1), (call(k=None), -1), (call(v=None), -1), (call(o=None), -1), (call(off=None), -1), (call(ws=None), -1),
+             (call(off=odd), -1), (call(lse=odd), -1), (call(ws=VP(buf.at + 8)), -1), (call(nbytes=size - 1), -5), (call(nbytes=0), -5),
+             (call(flags=2), -1), (call(scale=math.nan), -1), (call(scale=math.inf), -1), (call(dtype=2), -2), (call(d=96), -2),
+             (call(n=0), -1), (call(T=0), -1), (call(Hq=0), -1), (call(Hkv=0), -1), (call(Hq=5), -1),
+             (call(T=(1 << 30) + 1), -2), (call(Hq=65538), -2)]
+    for rows in ("q", "k", "v", "o"):
+        cases += [(call(**{rows: C.RowsC(buf.at + 8, 0, 64, 256)}), -1), (call(**{rows: C.RowsC(None, 0, 64, 256)}), -1),
+                  (call(**{rows: C.RowsC(buf.at, 0, 64, 257)}), -1), (call(**{rows: C.RowsC(buf.at, 0, 68, 256)}), -1),
+                  (call(**{rows: C.RowsC(buf.at, 0, 64, -256)}), -1), (call(**{rows: C.RowsC(buf.at, 0, 64, 0)}), -1),
+                  (call(**{rows: C.RowsC(buf.at, 0, 0, 256)}), -1), (call(**{rows: C.RowsC(buf.at, 0, 64, 1 << 38)}), -1)]
+    for i, (got, want) in enumerate(cases):
+        assert got == want, i
+
+
+def test_prompt_workspace_sizes(lib):
+    size = lib.bsa_prompt_workspace_bytes
+    assert 0 < size(1, 1, 1, 1) <= size(64, 4096, 32, 8) <= size(65, 4096, 32, 8) < size(65, 1 << 20, 32, 8)
+    # an item for every 256 rows of a group of heads (tokens x heads that go together) and one more for each prompt
+    for n, T, Hq, Hkv, gp in ((1, 100000, 8, 8, 1), (7, 100000, 32, 1, 16), (3, 50000, 28, 4, 1), (3, 50000, 24, 4, 2)):
+        assert size(n, T, Hq, Hkv) >= 16 * (T * gp // 256 + n) + 4 * (n + 1) + 64
+    for bad in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0), (1, 1, 3, 2), (1, (1 << 30) + 1, 1, 1), (1, 1, 65538, 1)):
+        assert size(*bad) == 0
+
+
 def test_rotation_oracle():
     x = np.random.default_rng(0).standard_normal((5, 3, 7, 32))
     f, _ = OP.frequencies(16)

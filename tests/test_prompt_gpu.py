@@ -1,5 +1,6 @@
 """GPU tests of the attention of packed prompts (bsa_prompt_attention) against fp64,
 with bounds from the arithmetic."""
+import ctypes
 import math
 
 import numpy as np
@@ -330,3 +331,64 @@ def test_what_any_block_records_is_reported(bsa, n, T):
     assert bsa.prompt_status(ws) == (-6, 5 << 8 | 0x52)
     bsa.prompt_attention(x, x, x, off, workspace=ws)
     assert bsa.prompt_status(ws) == (0, 0)
+
+
+def test_without_lse(bsa):
+    """LSE = NULL through the C ABI: the same outputs."""
+    from block_sparse_attention_plan_gb300 import _prompt as P
+    gen = torch.Generator().manual_seed(8)
+    for d, lens in ((64, [200, 3]), (128, [5000, 60])):
+        T = sum(lens)
+        q, k, v = (rows(gen, T, h, d, torch.bfloat16).cuda() for h in (4, 2, 2))
+        off = ptr(lens).cuda()
+        want, _ = bsa.prompt_attention(q, k, v, off)
+        out = torch.zeros_like(q)
+        ws = torch.empty(bsa.prompt_workspace_bytes(2, T, 4, 2), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        r = [ctypes.byref(P.RowsC(x.data_ptr(), 0, d, x.shape[1] * d)) for x in (q, k, v, out)]
+        assert P._library().bsa_prompt_attention(*r, None, 0, off.data_ptr(), 2, T, 4, 2, d, 1, 0.0, ws.data_ptr(), ws.numel(), None) == 0
+        assert bsa.prompt_status(ws) == (0, 0) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 7, 1), (128, 8, 2)])
+@pytest.mark.parametrize("lens", [[4096], [4000] + [1] * 60 + [0, 17, 19], [20] * 64, [0] * 30 + [4033] + [63] + [0] * 30])
+def test_with_and_without_the_schedule(bsa, d, Hq, Hkv, lens):
+    """Up to 64 prompts of 4096 tokens find their items without the schedule kernel: at the border, and one prompt or
+    token past it, with a long prompt ahead of short ones and behind, the same bits."""
+    gen = torch.Generator().manual_seed(len(lens))
+    T = sum(lens)
+    q, k, v = (rows(gen, 4097, h, d, torch.bfloat16).cuda() for h in (Hq, Hkv, Hkv))
+    for causal in (True, False):
+        few = bsa.prompt_attention(q[:T], k[:T], v[:T], ptr(lens).cuda(), causal=causal)
+        more = bsa.prompt_attention(q[:T], k[:T], v[:T], ptr(lens + [0] * (65 - len(lens))).cuda(), causal=causal)
+        longer = bsa.prompt_attention(q, k, v, ptr(lens).cuda(), causal=causal)      # (rows of no prompt behind)
+        for other in (more, longer):
+            assert torch.equal(few[0], other[0][:T]) and torch.equal(few[1], other[1][:T])
+    if T > 3000:
+        return
+    check(bsa, *(x[:T].cpu() for x in (q, k, v)), ptr(lens))
+
+
+def test_rows_past_32_bit_offsets(bsa):
+    """Rows whose offsets pass 2^31 elements and 2^32 bytes: by far tokens, by far heads, and outputs so."""
+    gen = torch.Generator().manual_seed(9)
+    T, H, d = 300, 4, 64
+    far = (1 << 31) // 100 // 8 * 8                        # elements between tokens: T of them pass 2^32
+    room = torch.zeros(T * far + H * d, dtype=torch.bfloat16, device="cuda")
+    x = rows(gen, T, H, d, torch.bfloat16).cuda()
+    for shape in ((far, d), (d, far * 64)):                # (by tokens, by heads)
+        view = room.as_strided((T, H, d), (*shape, 1))
+        view.copy_(x)
+        off = ptr([170, 130]).cuda()
+        want, wl = bsa.prompt_attention(x, x[:, :2], x[:, 2:], off)
+        got, gl = bsa.prompt_attention(view, view[:, :2], view[:, 2:], off)
+        assert torch.equal(want, got) and torch.equal(wl, gl)
+        r = bsa.rope_create(64)
+        tq, tk = bsa.rope(r, x, x[:, :2])
+        gq, gk = bsa.rope(r, view, view[:, :2], out_q=torch.empty_like(x), out_k=torch.empty_like(x[:, :2]))
+        assert torch.equal(tq, gq) and torch.equal(tk, gk)
+        bsa.rope(r, view, out_q=view)
+        assert torch.equal(view, tq)
+        bsa.prompt_attention(x, x[:, :2], x[:, 2:], off, out=view)
+        assert torch.equal(view, want)
+        view.zero_()
