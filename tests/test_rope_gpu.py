@@ -201,3 +201,28 @@ def test_outputs_given_to_a_call_with_gradients_are_refused(bsa):
             bad()
     with torch.no_grad():
         assert bsa.rope(r, y, out_q=y)[0] is y
+
+
+def test_gradients_in_a_captured_graph(bsa):
+    """Forward and gradients captured together.  (No eager graph of the same leaves may be alive then, whatever its
+    operations: a leaf's node belongs to the stream on which it was made, and capture refuses to wait for it.)"""
+    gen = torch.Generator().manual_seed(8)
+    r = bsa.rope_create(64)
+    q, gy = (rows(gen, 30, 4, 64, dtype=torch.bfloat16).cuda() for _ in range(2))
+    q.requires_grad_()
+    pos = torch.arange(30, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):  # (the first gradient sets up the engine)
+        torch.autograd.grad(bsa.rope(r, q, positions=pos)[0], q, gy)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, _ = bsa.rope(r, q, positions=pos)
+        gx, = torch.autograd.grad(o, q, gy)
+    with torch.no_grad():
+        q.mul_(2.0)
+        gy.add_(1.0)
+        pos.add_(5)
+        g.replay()
+        assert torch.equal(o, bsa.rope(r, q, positions=pos)[0]) and torch.equal(gx, bsa.rope(r, gy, positions=pos, inverse=True)[0])
