@@ -28,6 +28,11 @@
 // of kept tokens there and back.  Measured, selection and move: 32 sequences of 2177 to
 // 2304 tokens to 2048, 8 heads of 128, E4M3: 14 + 45 us (the move 0.9 of a copy's rate); 48 of
 // 700 to 12000 to 1000, 8 heads of 64, INT8, pages of 16: 33 + 34; one of 64001 to 8000: 24 + 19.
+//
+// Lengths are on the device; threads, shared memory and clusters of the selection go by the
+// table's width (or the weights', where that is less) and by the number of pairs.  The first of
+// these cases in tables of 2304, 8192, 12288, 16384, 32768 and 131072 tokens a sequence: 56, 58, 57,
+// 61, 59 and 72 us in all.  Two sequences of 192 tokens, 8 heads, in clusters of eight: 29 us.
 #include "bsa_cache.h"
 #include "bsa_cache_codes.cuh"
 #include "bsa_device.cuh"
@@ -89,8 +94,9 @@ __device__ __forceinline__ int2 ld_cluster2(uint32_t addr, int rank) {
 // Tokens of a CTA whose weights are held in shared memory, at most.
 constexpr int kHeld = 49152;
 constexpr int kList = 128;        // tokens of a bin that are ranked one against another
-// Tokens of a CTA on its own for which 512 threads do (fewer warps meet sooner; 32
-// sequences of 2304 tokens, 8 heads: 256, 512, 1024 threads 78, 67, 80 us in all).
+// Tokens of a CTA on its own, by its table, for which 512 threads do (fewer warps meet sooner; 32
+// sequences of 2304 tokens, 8 heads: 256, 512, 1024 threads 78, 67, 80 us in all; up to this
+// width two CTAs of 512 fit an SM with all weights held).
 constexpr int kFewTokens = 12288;
 
 template <int kSelectThreads>

@@ -26,7 +26,10 @@
 // 103 us, 5.7 TB/s (operands read from global memory by their lanes 153, through the ring
 // 131, with up to 8 rows in registers 119, pieces cut with kHead 105: 12, 6, 20 or 32
 // places 105, 113, 104, 105).  4 of 3000 to 12001, 32 queries of 32 heads over 8 of 64, INT8:
-// 28 us (tiles of 64 keys 46).
+// 28 us (tiles of 64 keys 46).  With masks the line is still cut by tokens, selected or not:
+// the first case with blocks of 64, of a head the first, the last 16 and 16 others: 101 us for a
+// quarter of the bytes (CTAs are busy 44 % of that time; those with a sequence's last blocks go on
+// the longest), with 64 others 110; 16 sequences, 8 queries: 109 (96 without the mask).
 #include "bsa_cache.h"
 #include "bsa_cache_codes.cuh"
 #include "bsa_device.cuh"

@@ -33,7 +33,15 @@ struct RopeParams {
 // Attention of packed prompts (bsa_prompt_attn.cu).
 constexpr int kPromptRows = 256;   // query rows of a work item: two tiles of 128
 // Up to so many prompts of so many tokens together find their items without the
-// schedule kernel.
+// schedule kernel.  The kernels with it and without it, us, at 32/8 heads of 128 and 8/2 of 64:
+//   24 of 1 to 59 tokens  21.8 / 18.5, 14.5 / 12.0    16 of 512  67.6 / 64.6, 24.4 / 20.5
+//   64 of 64              37.1 / 34.3, 16.4 / 12.3    64 of 512   221 / 211,  56.7 / 53.6
+//   one of 4096            105 / 101,  45.1 / 43.1    one of 8192 343 / 341,  78.0 / 76.0
+//   3500 behind 63 of 9   98.9 / 96.8, 41.5 / 39.0
+//   3500 ahead of 63 of 9 98.1 / 102,  41.5 / 59.6    8000 ahead of 63 of 20  341 / 361, 82.5 / 133
+// The schedule is 3 to 4 us, and past these limits less than what dealing the items out as
+// they lie may cost; below them a long prompt listed ahead of short ones is the one order
+// that it costs more (the lengths are on the device: no rule on them can choose).
 constexpr int kPromptFew = 64, kPromptFewTokens = 4096;
 constexpr int kPromptCtlTiles = 3; // control word: work items of a group of heads (0-2: as a plan's)
 constexpr int kPromptCtlCtas = 4;  // control word: CTAs of the attention kernel

@@ -6,9 +6,10 @@
 // in the group, at most 16).  A schedule kernel lists the items of all prompts,
 // those with the most key blocks first; the attention kernel's CTAs (one per SM) take
 // them, for one group of heads after the other, from a counter.  For few prompts of few
-// tokens the schedule kernel would be a quarter of the time: there each CTA finds its own
-// items in the line of all prompts', from its end on (a prompt's last items are its
-// longest).
+// tokens the schedule kernel would be up to a quarter of the time: there each CTA finds its
+// own items in the line of all prompts', from its end on.  That puts a prompt's longest
+// items first, but not those of a long prompt ahead of short ones (figures beside
+// kPromptFew).
 //
 // One CTA (384 threads):
 //   warp 0    takes work items, publishes them, loads both Q tiles and the K and
@@ -52,9 +53,17 @@
 // values are replaced by 0 in shared memory before the product, and an item that had
 // any adds them to the rows that do attend them at its end, from global memory.
 //
+// Weights are rounded to the inputs' type, which is what the tensor cores take beside such
+// values; their sum is of the unrounded ones.  O is 2e-3 (bf16) or 3e-4 (fp16) of its norm
+// off a result whose weights stay in 32 bits, and 1.2 to 1.3 times as far from the exact one
+// as that (rounding O is most of both).  Two products with P in two parts would take that away
+// for half as much work again.
+//
 // What bounds it: the tensor cores, 2 * 2 * 128 * 128 d flops a block and tile (d = 128:
-// 72 % busy, 1680 TFLOP/s for 12007 tokens, 700 us), and the exponentials, 128 * 128, with
-// what a step costs the issuing warps (d = 64: 1065 TFLOP/s for 8192 tokens).
+// 72 % busy; 12007 tokens, 32 / 8 heads: 694 to 713 us for the kernel alone, 1660 to 1700
+// TFLOP/s, 725 to 767 for a call among others, where the power limit comes in; not causal
+// 1421, 1661 TFLOP/s), and the exponentials, 128 * 128, with what a step costs the issuing
+// warps (d = 64, 8192 tokens: 258 to 270 us, 1020 to 1065 TFLOP/s, not causal 487, 1130).
 #include <cstdint>
 
 #include "bsa_device.cuh"
