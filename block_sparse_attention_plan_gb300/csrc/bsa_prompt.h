@@ -45,8 +45,7 @@ constexpr int kPromptRows = 256;   // query rows of a work item: two tiles of 12
 constexpr int kPromptFew = 64, kPromptFewTokens = 4096;
 constexpr int kPromptCtlTiles = 3; // control word: work items of a group of heads (0-2: as a plan's)
 constexpr int kPromptCtlCtas = 4;  // control word: CTAs of the attention kernel
-// Behind the 16 control words, status and detail of each CTA: it clears its own when it
-// begins, which no other CTA's record can come before.
+// Behind the 16 control words, status and detail of each CTA, which it writes as it ends.
 constexpr int kPromptCtlOwn = 16;
 constexpr int kPromptMaxCtas = 512;
 constexpr int kPromptCtlWords = kPromptCtlOwn + 2 * kPromptMaxCtas;

@@ -124,8 +124,8 @@ struct Cfg {
   static constexpr int kSchedFull = kDrain + 2;
   static constexpr int kSchedEmpty = kSchedFull + kSlots;
   static constexpr int kNumBars = kSchedEmpty + kSlots;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag, copies requested of K/V and of Q
-  static constexpr int kOffSched = kOffMisc + 16;           // int [kSlots][8]
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag, copies requested of K/V and of Q, status and detail
+  static constexpr int kOffSched = kOffMisc + 32;           // int [kSlots][8]
   static constexpr int kOffDirty = kOffSched + 32 * kSlots; // int [2 kSlots]
   static constexpr int kOffPtr = kOffDirty + 8 * kSlots;    // int [2][kPromptFew + 1]: items ahead of each prompt, offsets
   static constexpr int kSmem = kOffPtr + 8 * (kPromptFew + 1);
@@ -885,12 +885,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const Smem<C> sm{smem_u32(smem)};
   volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  int32_t* own = p.control + kPromptCtlOwn + 2 * blockIdx.x;
-  const Watchdog wd{abort_flag, own, own + 1, p.watchdog_ns};
+  // (Status words in shared memory until the end: pointers of the CTA's own into global memory
+  // are registers that every wait would hold, d = 64: 256 -> 264 us for the six documents.)
+  int32_t* found = reinterpret_cast<int32_t*>(smem + C::kOffMisc + 16);
+  const Watchdog wd{abort_flag, found, found + 1, p.watchdog_ns};
   next_may_launch();
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     tmem_holder[2] = tmem_holder[3] = 0u;
+    found[0] = BSA_OK;
+    found[1] = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(sm.bar(C::kQFull + i), 1);
       mbar_init(sm.bar(C::kQEmpty + i), C::kThree ? 1 : 2);
@@ -918,11 +922,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tmem_relinquish();
   }
   wait_for_previous();
-  if (threadIdx.x == 0) {
-    own[0] = BSA_OK;
-    own[1] = 0;
-    if (blockIdx.x == 0) p.control[kPromptCtlCtas] = (int)gridDim.x;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -949,7 +948,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag) drain_copies<C>(smem, sm, wd);
+  if (threadIdx.x == 0) {
+    if (*abort_flag) drain_copies<C>(smem, sm, wd);
+    int32_t* own = p.control + kPromptCtlOwn + 2 * blockIdx.x;
+    own[0] = *const_cast<volatile int32_t*>(found);
+    own[1] = *const_cast<volatile int32_t*>(found + 1);
+    if (blockIdx.x == 0) p.control[kPromptCtlCtas] = (int)gridDim.x;
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
