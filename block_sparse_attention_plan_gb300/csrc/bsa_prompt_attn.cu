@@ -734,6 +734,9 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
     const int lim = p.causal ? min(tok, m.len - 1) : m.len - 1;
     const int lim_warp = p.causal ? min(first + ((quad * 32) >> p.gp_shift), m.len - 1) : m.len - 1;  // its first row's
     const int whole = p.causal ? min(first + 1, m.len) : m.len;
+    // Rows of the warp that are the prompt's: those behind its end may hold anything, and move no
+    // reference.
+    const uint32_t own_rows = __ballot_sync(0xffffffffu, tok < m.len);
     // Weights are kept at 2^shift of their size and, in a block, summed to no more than `most`.
     const int log_n = 32 - __clz(n);
     const float shift = FP16 ? 6.f : (float)(-kMostLog - log_n);
@@ -823,7 +826,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, uint8_t* smem, co
         float s0, s1;
         f2_split(fadd2(fadd2(acc2[0], acc2[1]), fadd2(acc2[2], acc2[3])), s0, s1);
         sum = s0 + s1;
-        if (move || !__any_sync(0xffffffffu, sum > most || m_ref == -INFINITY)) break;
+        if (move || !(__ballot_sync(0xffffffffu, sum > most || m_ref == -INFINITY) & own_rows)) break;
       }
       tmem_st32_at<0>(scol, pk);
       tmem_st32_at<32>(scol + 32u, pk);

@@ -832,7 +832,8 @@ bsa_status bsa_rope_apply(const bsa_rope* rope, const bsa_rows* q, const bsa_row
  *   status of this call (calls that overlap in time need their own).
  * Scores, sums and accumulators are fp32.  Weights are rounded to `dtype`; they are taken
  * relative to the largest score of the row's first 128 keys, or of the first later block of
- * 128 whose weights of the row come to more than 2^15 of that.  An infinity or NaN among
+ * 128 whose weights of the row (or of one beside it, of the same prompt) come to more than
+ * 2^15 of that.  An infinity or NaN among
  * the keys or values reaches the rows that attend it and no other.  Finite values of any size
  * give finite means (one within the weights' rounding of the type's largest may be rounded
  * past it); values below 2^-100 lose bits.  One kernel for up to 64 prompts of up to 4096

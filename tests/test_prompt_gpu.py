@@ -392,3 +392,29 @@ def test_rows_past_32_bit_offsets(bsa):
         bsa.prompt_attention(x, x[:, :2], x[:, 2:], off, out=view)
         assert torch.equal(view, want)
         view.zero_()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d,g", [(64, 1), (64, 7), (128, 4), (128, 2)])
+@pytest.mark.parametrize("lens", [[300], [700, 45, 523]])
+def test_outputs_do_not_depend_on_rows_of_others(bsa, dtype, d, g, lens):
+    """The same bits whatever rows lie ahead of a prompt and behind it: none, other prompts', or anything."""
+    gen = torch.Generator("cuda").manual_seed(d + g)
+    T, pad = sum(lens), 300
+    q, k, v = (torch.randn(T + 2 * pad, h, d, device="cuda", generator=gen).to(dtype) for h in (2 * g, 2, 2))
+    off = ptr(lens, pad)
+    for causal in (True, False):
+        want = bsa.prompt_attention(q, k, v, off.cuda(), causal=causal)
+        for fill in (0.0, 100.0, math.inf, math.nan):
+            a, b, c = q.clone(), k.clone(), v.clone()
+            for x in (a, b, c):
+                x[:pad] = fill
+                x[pad + T:] = fill * torch.randn(x[pad + T:].shape, device="cuda", generator=gen).to(dtype)
+            got = bsa.prompt_attention(a, b, c, off.cuda(), causal=causal)
+            for w, o in zip(want, got):
+                assert torch.equal(w[pad:pad + T], o[pad:pad + T]), (causal, fill)
+        for i, n in enumerate(lens):  # each prompt on its own
+            lo = off[i].item()
+            alone = bsa.prompt_attention(q[lo:lo + n], k[lo:lo + n], v[lo:lo + n], ptr([n]).cuda(), causal=causal)
+            for w, o in zip(want, alone):
+                assert torch.equal(w[lo:lo + n], o), (causal, i)
