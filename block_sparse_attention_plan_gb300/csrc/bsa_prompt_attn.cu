@@ -28,7 +28,7 @@
 //             issue, S's arrival: half of a block's time) than for the products: tensor
 //             memory has room for three buffers of scores, so warp 1 issues S up to three
 //             steps (A, B, A ..) ahead, warp 2 P V.  (A prompt of 8192 tokens, 32 / 8 heads of
-//             64: 258 us, 288 in turns; one warp for both: 382, a step's waits, commits and
+//             64: 256 us, 288 in turns; one warp for both: 382, a step's waits, commits and
 //             descriptors are some 1700 cycles of its instructions; blocks of 64 keys with
 //             two buffers a tile: 360; four tiles of them: 607, spilled registers.)
 //   warp 3    looks over the values of every block that some row of the item does not
@@ -62,8 +62,8 @@
 // What bounds it: the tensor cores, 2 * 2 * 128 * 128 d flops a block and tile (d = 128:
 // 72 % busy; 12007 tokens, 32 / 8 heads: 694 to 713 us for the kernel alone, 1660 to 1700
 // TFLOP/s, 725 to 767 for a call among others, where the power limit comes in; not causal
-// 1421, 1661 TFLOP/s), and the exponentials, 128 * 128, with what a step costs the issuing
-// warps (d = 64, 8192 tokens: 258 to 270 us, 1020 to 1065 TFLOP/s, not causal 487, 1130).
+// 1399 to 1421, 1661 to 1689), and the exponentials, 128 * 128, with what a step costs the issuing
+// warps (d = 64, 8192 tokens: 255 to 260 us, 1057 to 1077 TFLOP/s, not causal 469, 1171).
 #include <cstdint>
 
 #include "bsa_device.cuh"
